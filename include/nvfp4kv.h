@@ -105,6 +105,7 @@ typedef enum {
 #define NVFP4KV_DEV_BAD_SLOT 0x2  /* slot outside [0, num_pages * page_size)      */
 #define NVFP4KV_DEV_BAD_LEN 0x4   /* length < 0 or > max_pages_per_seq*page_size  */
 #define NVFP4KV_DEV_TIMEOUT 0x8   /* a bounded wait for staged data gave up        */
+#define NVFP4KV_DEV_NO_PAGES 0x10 /* a step needs more pages than are free         */
 
 /* Element types of caller buffers.  NVFP4KV_E4M3 (OCP FP8 E4M3FN bytes at
  * scale 1.0) is accepted only where a call says so: the chunk K/V of the
@@ -375,6 +376,137 @@ nvfp4kv_status nvfp4kv_extend_attention_fp8_append(const nvfp4kv_cache *cache,
                                                    int32_t batch, int32_t num_q_heads, float sm_scale,
                                                    void *out, nvfp4kv_dtype out_dtype,
                                                    int32_t *dev_status, nvfp4kv_stream_t stream);
+
+/* ---- A step's tables, built on the device ------------------------------------
+ *
+ * A library utility: the pages name a paged cache ("SGLang stores KV cache in
+ * 4 bits", Interpretation) and leave its bookkeeping to the engine.  These two
+ * calls keep it on the device, so that a whole serving step, its page
+ * allocation included, can be captured into a graph.
+ *
+ * Free pages are a stack: free_pages[0 .. n - 1] are the ids of the free pages
+ * and *num_free = n (device int32).  plan_step takes from the top,
+ * release_pages puts back on top.
+ *
+ * nvfp4kv_plan_step: request b has context_lens[b] cached tokens, in the pages
+ * that its row of block_table lists, and adds new_lens[b] tokens (0 is
+ * allowed).  With had = ceil(context / 16) and has = ceil((context + new) / 16),
+ * it takes has - had fresh pages; fresh pages are numbered over the whole step
+ * in the order of (request, page), and the i-th is free_pages[n - 1 - i].
+ *   block_table  int32 [batch][max_pages_per_seq]: entries had .. has - 1 of
+ *                row b are written, the others left as they are
+ *   seq_lens     [batch]: context + new
+ *   q_indptr     [batch + 1]: running sum of new_lens, from 0
+ *   kv_indptr    [batch] or NULL: running sum of context_lens, from 0 (the row
+ *                offsets that nvfp4kv_dequant_prefix_fp8 takes)
+ *   slot_mapping [max_tokens]: row r of the step's tokens, the requests' new
+ *                tokens one after another, goes to page * 16 + position mod 16;
+ *                rows behind the last token get -1, which appending calls skip
+ *   positions    [max_tokens] or NULL: the row's position in its sequence; -1
+ *                behind the last token
+ *   num_free_out the pages left, n - fresh; may be num_free_in itself
+ * A request whose lengths are negative or pass max_pages_per_seq * 16 counts as
+ * empty (length 0, no tokens) and sets NVFP4KV_DEV_BAD_LEN.  A page id outside
+ * [0, num_pages) gives its tokens the slot -1 and sets NVFP4KV_DEV_BAD_PAGE.
+ * The step is taken as a whole or not at all: if it needs more than n pages
+ * (NVFP4KV_DEV_NO_PAGES), has more than max_tokens tokens, contexts that sum
+ * past 2^31 - 1, or n is outside [0, free_capacity] (NVFP4KV_DEV_BAD_LEN),
+ * then no page is taken, seq_lens are the context lengths, q_indptr is all 0,
+ * slots and positions are -1 (kv_indptr is all 0 where its sum does not fit)
+ * and num_free_out is n, clamped into that range.
+ * batch at most NVFP4KV_MAX_BATCH; num_pages * 16 below 2^31.  An output must
+ * not overlap another array, num_free_out on num_free_in excepted
+ * (NVFP4KV_ERR_INVALID_ARG).  The decode calls read seq_lens and block_table
+ * ahead of their wait for the kernel before them: this call's kernels let no
+ * other kernel start before they have written both. */
+nvfp4kv_status nvfp4kv_plan_step(const int32_t *context_lens, const int32_t *new_lens, int32_t batch,
+                                 int32_t *block_table, int32_t max_pages_per_seq, int32_t num_pages,
+                                 const int32_t *free_pages, int32_t free_capacity, const int32_t *num_free_in,
+                                 int32_t *num_free_out, int32_t *seq_lens, int32_t *q_indptr, int32_t *kv_indptr,
+                                 int32_t *slot_mapping, int32_t *positions, int32_t max_tokens,
+                                 int32_t *dev_status, nvfp4kv_stream_t stream);
+
+/* nvfp4kv_release_pages (a library utility): request b keeps its first
+ * keep_lens[b] of old_lens[b] tokens (0: the request has ended; fewer than
+ * before: drafted tokens were rejected).  Pages ceil(keep / 16) ..
+ * ceil(old / 16) - 1 of its row go back: over all requests, in the order of
+ * (request, page), they are written to free_pages[n], free_pages[n + 1], ...
+ * and *num_free_out = n + their number (may be num_free_in itself).  The block
+ * table is left as it is.  A request with keep > old, a negative length or one
+ * past max_pages_per_seq * 16 returns nothing and sets NVFP4KV_DEV_BAD_LEN; a
+ * page id outside [0, num_pages) goes back as it is and sets
+ * NVFP4KV_DEV_BAD_PAGE.  If the stack would pass free_capacity, or n is outside
+ * [0, free_capacity], nothing goes back (NVFP4KV_DEV_BAD_LEN; num_free_out is n
+ * clamped into that range).  A page must be
+ * held by one request only.  Limits as for nvfp4kv_plan_step. */
+nvfp4kv_status nvfp4kv_release_pages(const int32_t *old_lens, const int32_t *keep_lens, int32_t batch,
+                                     const int32_t *block_table, int32_t max_pages_per_seq, int32_t num_pages,
+                                     int32_t *free_pages, int32_t free_capacity, const int32_t *num_free_in,
+                                     int32_t *num_free_out, int32_t *dev_status, nvfp4kv_stream_t stream);
+
+/* ---- Head norm and position rotation of new queries and keys -------------------
+ *
+ * The pages start from finished queries and keys; this step before the cache
+ * write has no counterpart on the pages.
+ *
+ * For each row x of 128 channels (one token, one head) at position n:
+ *   y = x / sqrt(mean(x^2) + eps) * weight              (where a norm is given)
+ *   (y_a, y_b) -> scale * (y_a cos t - y_b sin t, y_b cos t + y_a sin t),
+ *   t = n * inv_freq[i], for the rotary_dim / 2 channel pairs (a, b) =
+ *   (i, i + rotary_dim / 2), or (2i, 2i + 1) when interleaved.
+ * Channels from rotary_dim on keep y.  Arithmetic in fp32, rounded once; the
+ * angles are exact to 2^-32 of a turn at every position. */
+typedef struct {
+    const double *inv_freq;      /* HOST array of rotary_dim / 2 finite values, radians a position */
+    int32_t rotary_dim;          /* 0 (no rotation), 32, 64, 96 or 128 */
+    int32_t interleaved;         /* 0 or 1 */
+    float scale;                 /* multiplies cos and sin; finite (1 for plain rotation) */
+} nvfp4kv_rope;
+
+/* Weights: device arrays [128] of weight_dtype (fp32 or bf16), 4-byte (fp32) or
+ * 2-byte (bf16) aligned; a null weight leaves that kind of row without a norm.
+ * eps: finite, >= 0. */
+typedef struct {
+    const void *q_weight;
+    const void *k_weight;
+    nvfp4kv_dtype weight_dtype;
+    float eps;
+} nvfp4kv_head_norm;
+
+/* q, k (no counterpart on the pages): num_tokens rows of [num_q_heads][128]
+ *   and [num_kv_heads][128], fp32 or bf16 (in_dtype), token t's at q + t *
+ *   q_stride (elements; at least the row, a multiple of 16 bytes, at most
+ *   2^28), so parts of a fused projection's rows can be given as they are;
+ *   16-byte aligned.
+ * positions: int32 [num_tokens] (device); a token with a negative position is
+ *   not there: its rows of the outputs are left as they are.
+ * rope, norm: host structs, either may be NULL; their host data is read
+ *   during the call.  Anything but the values above returns
+ *   NVFP4KV_ERR_UNSUPPORTED.
+ * q_out: bf16 [num_tokens][num_q_heads][128]; k_out: in_dtype
+ *   [num_tokens][num_kv_heads][128]; 16-byte aligned.  q_out may be q and
+ *   k_out may be k (same address, type and contiguous rows); any other overlap
+ *   with an input returns NVFP4KV_ERR_INVALID_ARG. */
+nvfp4kv_status nvfp4kv_qk_norm_rope(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                                    nvfp4kv_dtype in_dtype, int32_t num_tokens, int32_t num_q_heads,
+                                    int32_t num_kv_heads, const int32_t *positions, const nvfp4kv_rope *rope,
+                                    const nvfp4kv_head_norm *norm, void *q_out, void *k_out,
+                                    nvfp4kv_stream_t stream);
+
+/* The same fused with the cache write ("SGLang stores KV cache in 4 bits",
+ * Interpretation: new K/V are quantised into the NVFP4 cache): q_out as above;
+ * the finished keys, rounded to in_dtype, and the values v (rows as k's, at
+ * v_stride) go into the cache at slot_mapping[t] exactly as
+ * nvfp4kv_quantize_append would write them -- the keys are never stored
+ * elsewhere.  num_kv_heads is the cache's.  slot < 0 or position < 0 writes
+ * nothing of the token's K and V; slot >= num_pages * page_size likewise, and
+ * sets NVFP4KV_DEV_BAD_SLOT.  Slots must be distinct. */
+nvfp4kv_status nvfp4kv_qk_norm_rope_append(const nvfp4kv_cache *cache, const void *q, int64_t q_stride,
+                                           const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                                           nvfp4kv_dtype in_dtype, int32_t num_tokens, int32_t num_q_heads,
+                                           const int32_t *positions, const int32_t *slot_mapping,
+                                           const nvfp4kv_rope *rope, const nvfp4kv_head_norm *norm, void *q_out,
+                                           int32_t *dev_status, nvfp4kv_stream_t stream);
 
 /* FP8-E4M3 comparison cache, written and read the same way ("NVFP4-KV-Cache
  * auf der ...", "Unterstuetzung in den Engines": the FP8 baseline runs with

@@ -21,12 +21,18 @@ Functions carry the C names and take torch tensors:
     nvfp4kv_dequant_prefix_fp8(cache, block_table, prefix_lens, kv_indptr, k_out, v_out)
     nvfp4kv_extend_attention_fp8(q, q_indptr, k_prefix, v_prefix, kv_indptr, prefix_lens, k_chunk, v_chunk, ...)
     nvfp4kv_extend_attention_fp8_append(cache, slot_mapping, q, q_indptr, ...)
+  around a step
+    nvfp4kv_plan_step(context_lens, new_lens, block_table, num_pages, free_pages, num_free, ...)
+    nvfp4kv_release_pages(old_lens, keep_lens, block_table, num_pages, free_pages, num_free, ...)
+    nvfp4kv_qk_norm_rope(q, k, positions, q_out, k_out, rope=None, q_weight=None, k_weight=None, ...)
+    nvfp4kv_qk_norm_rope_append(cache, q, k, v, positions, slot_mapping, q_out, rope=None, ...)
   utilities
     nvfp4kv_read_device_status(dev_status, stream=None)
     nvfp4kv_set_wait_limit(polls) (failure detection: when bounded waits give up)
     nvfp4kv_cache_bytes / fp8kv_cache_bytes / nvfp4kv_status_string / nvfp4kv_version
 
-``NVFP4Cache`` and ``FP8Cache`` hold the pool tensors and build the C structs.
+``NVFP4Cache`` and ``FP8Cache`` hold the pool tensors and build the C structs;
+``Rope`` holds a position rotation.
 """
 from __future__ import annotations
 
@@ -41,7 +47,7 @@ PAGE_SIZE = 16
 HEAD_DIM = 128
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_CUDA, ERR_DEVICE_CHECK = 0, 1, 2, 3, 4, 5
-DEV_BAD_PAGE, DEV_BAD_SLOT, DEV_BAD_LEN, DEV_TIMEOUT = 0x1, 0x2, 0x4, 0x8
+DEV_BAD_PAGE, DEV_BAD_SLOT, DEV_BAD_LEN, DEV_TIMEOUT, DEV_NO_PAGES = 0x1, 0x2, 0x4, 0x8, 0x10
 F32, BF16, E4M3 = 0, 1, 2
 STATIC_SCRATCH_MAX_WORKERS = 3024   # NVFP4KV_STATIC_SCRATCH_MAX_WORKERS
 
@@ -72,8 +78,19 @@ class _Fp8Cache(ctypes.Structure):
                 ("page_size", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
 
 
+class _Rope(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+
+class _HeadNorm(ctypes.Structure):
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("weight_dtype", ctypes.c_int),
+                ("eps", ctypes.c_float)]
+
+
 _vp = ctypes.c_void_p
 _i32 = ctypes.c_int32
+_i64 = ctypes.c_int64
 _st = ctypes.c_int
 
 
@@ -125,6 +142,14 @@ def load(build_if_missing: bool = True):
             "nvfp4kv_extend_attention_fp8_append": (_st, [ctypes.POINTER(_Nvfp4Cache), _vp, _vp, _vp, _i32, _i32,
                                                           _vp, _vp, _vp, _vp, ctypes.c_int64, _vp, _vp, _st,
                                                           _i32, _i32, ctypes.c_float, _vp, _st, _vp, _vp]),
+            "nvfp4kv_plan_step": (_st, [_vp, _vp, _i32, _vp, _i32, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
+                                        _i32, _vp, _vp]),
+            "nvfp4kv_release_pages": (_st, [_vp, _vp, _i32, _vp, _i32, _i32, _vp, _i32, _vp, _vp, _vp, _vp]),
+            "nvfp4kv_qk_norm_rope": (_st, [_vp, _i64, _vp, _i64, _st, _i32, _i32, _i32, _vp, ctypes.POINTER(_Rope),
+                                           ctypes.POINTER(_HeadNorm), _vp, _vp, _vp]),
+            "nvfp4kv_qk_norm_rope_append": (_st, [ctypes.POINTER(_Nvfp4Cache), _vp, _i64, _vp, _i64, _vp, _i64, _st,
+                                                  _i32, _i32, _vp, _vp, ctypes.POINTER(_Rope),
+                                                  ctypes.POINTER(_HeadNorm), _vp, _vp, _vp]),
             "fp8kv_quantize_append": (_st, [ctypes.POINTER(_Fp8Cache), _vp, _vp, _st, _i32, _vp, _vp, _vp]),
             "fp8kv_paged_decode": (_st, [ctypes.POINTER(_Fp8Cache), _vp, _i32, _i32, _vp, _i32, _vp,
                                          ctypes.c_float, _vp, _st, _vp, ctypes.c_size_t, _i32, _vp, _vp]),
@@ -219,6 +244,39 @@ class FP8Cache(NVFP4Cache):
         assert rb == self.record_bytes
         self.page_size, self.head_dim = PAGE_SIZE, HEAD_DIM
         self._c = _Fp8Cache(pool.data_ptr(), self.num_pages, self.num_kv_heads, PAGE_SIZE, HEAD_DIM)
+
+
+class Rope:
+    """A position rotation: inv_freq (rotary_dim / 2 host floats, radians a
+    position; any scaling of long contexts is already in them), the pairing
+    (half-split, or interleaved) and a factor on cos and sin."""
+
+    def __init__(self, inv_freq, interleaved: bool = False, scale: float = 1.0):
+        vals = [float(v) for v in inv_freq]
+        self._f = (ctypes.c_double * max(1, len(vals)))(*vals)     # host array the library reads per call
+        self.rotary_dim, self.interleaved, self.scale = 2 * len(vals), bool(interleaved), float(scale)
+        self._c = _Rope(ctypes.addressof(self._f), self.rotary_dim, int(self.interleaved), self.scale)
+
+    @property
+    def c(self):
+        return ctypes.byref(self._c)
+
+
+def _tensor(t, name, dtype, shape, rows=False):
+    """Check a tensor argument: type, shape (None: any), on the current device,
+    contiguous (rows: the last two dimensions only)."""
+    import torch
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if len(t.shape) != len(shape) or any(w is not None and n != w for n, w in zip(t.shape, shape)):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name}: not on the current CUDA device")
+    if rows:
+        if t.shape[0] > 0 and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2])):
+            raise ValueError(f"{name}: heads and channels must be contiguous")
+    elif not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
 
 
 # --- entry points -------------------------------------------------------------
@@ -386,6 +444,113 @@ def nvfp4kv_extend_attention_fp8_append(cache: NVFP4Cache, slot_mapping, q, q_in
         _chunk_dtype_code(k_chunk), B, Hq, float(sm_scale), _ptr(out), _dtype_code(out), _ptr(dev_status),
         _stream(stream))
     _check(st, "nvfp4kv_extend_attention_fp8_append")
+
+
+def nvfp4kv_plan_step(context_lens, new_lens, block_table, num_pages, free_pages, num_free, num_free_out, seq_lens,
+                      q_indptr, slot_mapping, positions=None, kv_indptr=None, dev_status=None, stream=None) -> None:
+    """A step's tables from its requests' lengths (all int32 on the device):
+    takes fresh pages from the stack free_pages[: num_free], enters them into
+    block_table [B][max_pages], and writes seq_lens [B], q_indptr [B+1],
+    kv_indptr [B], slot_mapping and positions [max_tokens] (-1 behind the last
+    token) and num_free_out [1] (which may be num_free)."""
+    import torch
+    B, i32 = context_lens.shape[0], torch.int32
+    for t, name, shape in ((context_lens, "context_lens", (B,)), (new_lens, "new_lens", (B,)),
+                           (block_table, "block_table", (B, None)), (free_pages, "free_pages", (None,)),
+                           (num_free, "num_free", (1,)), (num_free_out, "num_free_out", (1,)),
+                           (seq_lens, "seq_lens", (B,)), (q_indptr, "q_indptr", (B + 1,)),
+                           (slot_mapping, "slot_mapping", (None,)),
+                           (positions, "positions", (slot_mapping.shape[0],)), (kv_indptr, "kv_indptr", (B,)),
+                           (dev_status, "dev_status", (1,))):
+        if t is not None:
+            _tensor(t, name, i32, shape)
+    st = load().nvfp4kv_plan_step(
+        _ptr(context_lens), _ptr(new_lens), B, _ptr(block_table), block_table.shape[1], int(num_pages),
+        _ptr(free_pages), free_pages.shape[0], _ptr(num_free), _ptr(num_free_out), _ptr(seq_lens), _ptr(q_indptr),
+        _ptr(kv_indptr), _ptr(slot_mapping), _ptr(positions), slot_mapping.shape[0], _ptr(dev_status),
+        _stream(stream))
+    _check(st, "nvfp4kv_plan_step")
+
+
+def nvfp4kv_release_pages(old_lens, keep_lens, block_table, num_pages, free_pages, num_free, num_free_out,
+                          dev_status=None, stream=None) -> None:
+    """Put the pages that requests no longer need (old_lens down to keep_lens
+    tokens, int32 [B]) back on the stack free_pages[: num_free]; num_free_out
+    [1] may be num_free."""
+    import torch
+    B, i32 = old_lens.shape[0], torch.int32
+    for t, name, shape in ((old_lens, "old_lens", (B,)), (keep_lens, "keep_lens", (B,)),
+                           (block_table, "block_table", (B, None)), (free_pages, "free_pages", (None,)),
+                           (num_free, "num_free", (1,)), (num_free_out, "num_free_out", (1,)),
+                           (dev_status, "dev_status", (1,))):
+        if t is not None:
+            _tensor(t, name, i32, shape)
+    st = load().nvfp4kv_release_pages(
+        _ptr(old_lens), _ptr(keep_lens), B, _ptr(block_table), block_table.shape[1], int(num_pages),
+        _ptr(free_pages), free_pages.shape[0], _ptr(num_free), _ptr(num_free_out), _ptr(dev_status),
+        _stream(stream))
+    _check(st, "nvfp4kv_release_pages")
+
+
+def _head_norm(q_weight, k_weight, eps):
+    if q_weight is None and k_weight is None:
+        return None
+    for t, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if t is not None:
+            _tensor(t, name, (q_weight if q_weight is not None else k_weight).dtype, (HEAD_DIM,))
+    return ctypes.byref(_HeadNorm(_ptr(q_weight), _ptr(k_weight),
+                                  _dtype_code(q_weight if q_weight is not None else k_weight), float(eps)))
+
+
+def _token_stride(t) -> int:
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def nvfp4kv_qk_norm_rope(q, k, positions, q_out, k_out, rope: Rope | None = None, q_weight=None, k_weight=None,
+                         eps=1e-6, stream=None) -> None:
+    """Norm (where a weight is given) and rotate each head of q [T][Hq][128] and
+    k [T][Hkv][128] (fp32 or bf16; tokens may be strided, as views of a fused
+    projection are) at positions int32 [T] (negative: token left out) into
+    q_out (bf16) and k_out (k's type)."""
+    import torch
+    T, Hq, _ = q.shape
+    Hkv = k.shape[1]
+    code = _dtype_code(q)
+    _tensor(q, "q", q.dtype, (T, Hq, HEAD_DIM), rows=True)
+    _tensor(k, "k", q.dtype, (T, Hkv, HEAD_DIM), rows=True)
+    _tensor(positions, "positions", torch.int32, (T,))
+    _tensor(q_out, "q_out", torch.bfloat16, (T, Hq, HEAD_DIM))
+    _tensor(k_out, "k_out", q.dtype, (T, Hkv, HEAD_DIM))
+    st = load().nvfp4kv_qk_norm_rope(
+        _ptr(q), _token_stride(q), _ptr(k), _token_stride(k), code, T, Hq, Hkv, _ptr(positions),
+        None if rope is None else rope.c, _head_norm(q_weight, k_weight, eps), _ptr(q_out), _ptr(k_out),
+        _stream(stream))
+    _check(st, "nvfp4kv_qk_norm_rope")
+
+
+def nvfp4kv_qk_norm_rope_append(cache: NVFP4Cache, q, k, v, positions, slot_mapping, q_out,
+                                rope: Rope | None = None, q_weight=None, k_weight=None, eps=1e-6, dev_status=None,
+                                stream=None) -> None:
+    """nvfp4kv_qk_norm_rope with the finished keys and the values v [T][Hkv][128]
+    written into the NVFP4 cache at slot_mapping int32 [T] instead of k_out."""
+    import torch
+    T, Hq, _ = q.shape
+    Hkv = cache.num_kv_heads
+    code = _dtype_code(q)
+    _tensor(q, "q", q.dtype, (T, Hq, HEAD_DIM), rows=True)
+    _tensor(k, "k", q.dtype, (T, Hkv, HEAD_DIM), rows=True)
+    _tensor(v, "v", q.dtype, (T, Hkv, HEAD_DIM), rows=True)
+    _tensor(positions, "positions", torch.int32, (T,))
+    _tensor(slot_mapping, "slot_mapping", torch.int32, (T,))
+    _tensor(cache.pool, "cache", torch.uint8, cache.pool.shape)
+    if dev_status is not None:
+        _tensor(dev_status, "dev_status", torch.int32, (1,))
+    _tensor(q_out, "q_out", torch.bfloat16, (T, Hq, HEAD_DIM))
+    st = load().nvfp4kv_qk_norm_rope_append(
+        cache.c, _ptr(q), _token_stride(q), _ptr(k), _token_stride(k), _ptr(v), _token_stride(v), code, T, Hq,
+        _ptr(positions), _ptr(slot_mapping), None if rope is None else rope.c, _head_norm(q_weight, k_weight, eps),
+        _ptr(q_out), _ptr(dev_status), _stream(stream))
+    _check(st, "nvfp4kv_qk_norm_rope_append")
 
 
 def nvfp4kv_cache_bytes(num_pages, num_kv_heads, page_size=PAGE_SIZE, head_dim=HEAD_DIM) -> int:

@@ -275,6 +275,147 @@ nvfp4kv_status check_extend(const void *q, const int32_t *q_indptr, int32_t q_ro
     return NVFP4KV_OK;
 }
 
+// A caller's array, as the overlap checks see it.
+struct Span {
+    const void *p;
+    size_t bytes;
+    bool written;
+};
+
+// Whether an array that the call writes shares memory with another one.
+template <size_t N>
+bool written_overlap(const Span (&a)[N])
+{
+    for (size_t i = 0; i < N; ++i)
+        for (size_t j = i + 1; j < N; ++j) {
+            if (!(a[i].written || a[j].written) || a[i].p == nullptr || a[j].p == nullptr || a[i].bytes == 0 ||
+                a[j].bytes == 0)
+                continue;
+            const uintptr_t x = reinterpret_cast<uintptr_t>(a[i].p), y = reinterpret_cast<uintptr_t>(a[j].p);
+            if (x < y ? y - x < a[i].bytes : x - y < a[j].bytes)
+                return true;
+        }
+    return false;
+}
+
+bool aligned4(const void *p)
+{
+    return (reinterpret_cast<uintptr_t>(p) & 3u) == 0;
+}
+
+// Checks that plan_step and release_pages share.
+nvfp4kv_status check_tables(const int32_t *a, const int32_t *b, int32_t batch, const int32_t *block_table,
+                            int32_t max_pages_per_seq, int32_t num_pages, const int32_t *free_pages,
+                            int32_t free_capacity, const int32_t *num_free_in, const int32_t *num_free_out)
+{
+    if (batch < 0 || max_pages_per_seq <= 0 || num_pages <= 0 || free_capacity < 0)
+        return NVFP4KV_ERR_INVALID_ARG;
+    if (batch > kMaxBatch || static_cast<int64_t>(batch) * max_pages_per_seq > (int64_t{1} << 31) - 1 ||
+        static_cast<int64_t>(max_pages_per_seq) * kPageSize > (int64_t{1} << 30) ||
+        static_cast<int64_t>(num_pages) * kPageSize > (int64_t{1} << 31) - 1)
+        return NVFP4KV_ERR_UNSUPPORTED;
+    if (batch > 0 && (a == nullptr || b == nullptr || block_table == nullptr))
+        return NVFP4KV_ERR_INVALID_ARG;
+    if (num_free_in == nullptr || num_free_out == nullptr || (free_capacity > 0 && free_pages == nullptr))
+        return NVFP4KV_ERR_INVALID_ARG;
+    for (const void *p : {static_cast<const void *>(a), static_cast<const void *>(b),
+                          static_cast<const void *>(block_table), static_cast<const void *>(free_pages),
+                          static_cast<const void *>(num_free_in), static_cast<const void *>(num_free_out)})
+        if (!aligned4(p))
+            return NVFP4KV_ERR_INVALID_ARG;
+    return NVFP4KV_OK;
+}
+
+// Rows of `heads` x 128 channels at a token stride: base and stride keep every
+// row on 16 bytes, and rows do not overlap.
+bool good_rows(const void *base, int64_t stride, int32_t heads, int elem_bytes)
+{
+    return base != nullptr && aligned16(base) && stride >= static_cast<int64_t>(heads) * kHeadDim &&
+           stride <= (int64_t{1} << 28) && (stride * elem_bytes) % 16 == 0;
+}
+
+size_t rows_bytes(int64_t stride, int32_t tokens, int32_t heads, int elem_bytes)
+{
+    return (static_cast<size_t>(stride) * (tokens - 1) + static_cast<size_t>(heads) * kHeadDim) * elem_bytes;
+}
+
+// f / 2 pi modulo 1 in units of 2^-64: |f| times 1 / 2 pi held as the sum of
+// two doubles (the product is good to about 2^-105 of itself before the whole
+// turns go), negated modulo 2^64 for a negative f.
+uint64_t turn_fraction(double f)
+{
+    constexpr double kHi = 0x1.45f306dc9c883p-3, kLo = -0x1.6b01ec5417056p-57;
+    const double a = std::fabs(f);
+    const double hi = a * kHi, lo = std::fma(a, kHi, -hi) + a * kLo;
+    const double rest = std::ldexp(lo, 64);           // below 2^62 while a is below 2^49; past that no fraction is left
+    uint64_t turn = static_cast<uint64_t>(std::ldexp(hi - std::floor(hi), 64));
+    if (std::fabs(rest) < 0x1p62)
+        turn += static_cast<uint64_t>(static_cast<int64_t>(rest));
+    return f < 0.0 ? uint64_t{0} - turn : turn;
+}
+
+// Arguments that the two norm-and-rotation calls share.  Fills p on success;
+// num_tokens == 0 is valid and launches nothing.
+nvfp4kv_status check_norm_rope(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                               nvfp4kv_dtype in_dtype, int32_t num_tokens, int32_t num_q_heads,
+                               int32_t num_kv_heads, const int32_t *positions, const nvfp4kv_rope *rope,
+                               const nvfp4kv_head_norm *norm, void *q_out, NormRopeParams &p)
+{
+    if (num_tokens < 0 || num_q_heads <= 0 || num_kv_heads <= 0)
+        return NVFP4KV_ERR_INVALID_ARG;
+    if (in_dtype != NVFP4KV_F32 && in_dtype != NVFP4KV_BF16)
+        return NVFP4KV_ERR_INVALID_ARG;
+    if (num_q_heads > 65535 || num_kv_heads > 65535)
+        return NVFP4KV_ERR_UNSUPPORTED;
+    p = NormRopeParams{};
+    p.rope_scale = 1.f;
+    if (rope != nullptr) {
+        if (rope->rotary_dim < 0 || rope->rotary_dim > kHeadDim || rope->rotary_dim % 32 != 0 ||
+            (rope->interleaved != 0 && rope->interleaved != 1) || !std::isfinite(rope->scale))
+            return NVFP4KV_ERR_UNSUPPORTED;
+        if (rope->rotary_dim > 0 && rope->inv_freq == nullptr)
+            return NVFP4KV_ERR_INVALID_ARG;
+        for (int i = 0; i < rope->rotary_dim / 2; ++i) {
+            if (!std::isfinite(rope->inv_freq[i]))
+                return NVFP4KV_ERR_UNSUPPORTED;
+            p.freq[i] = turn_fraction(rope->inv_freq[i]);
+        }
+        p.rot = rope->rotary_dim;
+        p.interleaved = rope->interleaved;
+        p.rope_scale = rope->scale;
+    }
+    if (norm != nullptr) {
+        if (norm->weight_dtype != NVFP4KV_F32 && norm->weight_dtype != NVFP4KV_BF16)
+            return NVFP4KV_ERR_INVALID_ARG;
+        if (!std::isfinite(norm->eps) || norm->eps < 0.f)
+            return NVFP4KV_ERR_UNSUPPORTED;
+        const uintptr_t mask = norm->weight_dtype == NVFP4KV_F32 ? 3u : 1u;
+        if ((reinterpret_cast<uintptr_t>(norm->q_weight) & mask) || (reinterpret_cast<uintptr_t>(norm->k_weight) & mask))
+            return NVFP4KV_ERR_INVALID_ARG;
+        p.q_weight = norm->q_weight;
+        p.k_weight = norm->k_weight;
+        p.weight_bf16 = norm->weight_dtype == NVFP4KV_BF16;
+        p.eps = norm->eps;
+    }
+    if (num_tokens == 0)
+        return NVFP4KV_OK;
+    const int size = in_dtype == NVFP4KV_BF16 ? 2 : 4;
+    if (!good_rows(q, q_stride, num_q_heads, size) || !good_rows(k, k_stride, num_kv_heads, size) ||
+        q_out == nullptr || !aligned16(q_out) || positions == nullptr || !aligned4(positions))
+        return NVFP4KV_ERR_INVALID_ARG;
+    p.q = q;
+    p.k = k;
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.positions = positions;
+    p.q_out = static_cast<uint16_t *>(q_out);
+    p.num_tokens = num_tokens;
+    p.hq = num_q_heads;
+    p.hkv = num_kv_heads;
+    p.in_bf16 = in_dtype == NVFP4KV_BF16;
+    return NVFP4KV_OK;
+}
+
 } // namespace
 
 extern "C" {
@@ -446,6 +587,171 @@ nvfp4kv_status nvfp4kv_extend_attention_fp8_append(const nvfp4kv_cache *cache, c
     p.gscale = cache->global_scale;
     p.hs = head_scales_of(cache);
     return from_cuda(launch_extend_attention(p, to_cuda(stream)));
+}
+
+nvfp4kv_status nvfp4kv_plan_step(const int32_t *context_lens, const int32_t *new_lens, int32_t batch,
+                                 int32_t *block_table, int32_t max_pages_per_seq, int32_t num_pages,
+                                 const int32_t *free_pages, int32_t free_capacity, const int32_t *num_free_in,
+                                 int32_t *num_free_out, int32_t *seq_lens, int32_t *q_indptr, int32_t *kv_indptr,
+                                 int32_t *slot_mapping, int32_t *positions, int32_t max_tokens,
+                                 int32_t *dev_status, nvfp4kv_stream_t stream)
+{
+    const nvfp4kv_status st = check_tables(context_lens, new_lens, batch, block_table, max_pages_per_seq, num_pages,
+                                           free_pages, free_capacity, num_free_in, num_free_out);
+    if (st != NVFP4KV_OK)
+        return st;
+    if (max_tokens < 0 || q_indptr == nullptr || (batch > 0 && seq_lens == nullptr) ||
+        (max_tokens > 0 && slot_mapping == nullptr))
+        return NVFP4KV_ERR_INVALID_ARG;
+    if (!aligned4(seq_lens) || !aligned4(q_indptr) || !aligned4(kv_indptr) || !aligned4(slot_mapping) ||
+        !aligned4(positions))
+        return NVFP4KV_ERR_INVALID_ARG;
+    const size_t n = 4 * static_cast<size_t>(batch), t = 4 * static_cast<size_t>(max_tokens);
+    const Span spans[] = {{context_lens, n, false},
+                          {new_lens, n, false},
+                          {free_pages, 4 * static_cast<size_t>(free_capacity), false},
+                          {num_free_in, 4, false},
+                          {num_free_out == num_free_in ? nullptr : num_free_out, 4, true},
+                          {block_table, n * static_cast<size_t>(max_pages_per_seq), true},
+                          {seq_lens, n, true},
+                          {q_indptr, n + 4, true},
+                          {kv_indptr, n, true},
+                          {slot_mapping, t, true},
+                          {positions, t, true},
+                          {dev_status, 4, true}};
+    if (written_overlap(spans))
+        return NVFP4KV_ERR_INVALID_ARG;
+    StepTablesParams p{};
+    p.lens_a = context_lens;
+    p.lens_b = new_lens;
+    p.block_table = block_table;
+    p.free_pages = free_pages;
+    p.num_free_in = num_free_in;
+    p.num_free_out = num_free_out;
+    p.seq_lens = seq_lens;
+    p.q_indptr = q_indptr;
+    p.kv_indptr = kv_indptr;
+    p.slot_mapping = slot_mapping;
+    p.positions = positions;
+    p.dev_status = dev_status;
+    p.batch = batch;
+    p.max_pages = max_pages_per_seq;
+    p.num_pages = num_pages;
+    p.free_capacity = free_capacity;
+    p.max_tokens = max_tokens;
+    return from_cuda(launch_plan_step(p, to_cuda(stream)));
+}
+
+nvfp4kv_status nvfp4kv_release_pages(const int32_t *old_lens, const int32_t *keep_lens, int32_t batch,
+                                     const int32_t *block_table, int32_t max_pages_per_seq, int32_t num_pages,
+                                     int32_t *free_pages, int32_t free_capacity, const int32_t *num_free_in,
+                                     int32_t *num_free_out, int32_t *dev_status, nvfp4kv_stream_t stream)
+{
+    const nvfp4kv_status st = check_tables(old_lens, keep_lens, batch, block_table, max_pages_per_seq, num_pages,
+                                           free_pages, free_capacity, num_free_in, num_free_out);
+    if (st != NVFP4KV_OK)
+        return st;
+    const size_t n = 4 * static_cast<size_t>(batch);
+    const Span spans[] = {{old_lens, n, false},
+                          {keep_lens, n, false},
+                          {block_table, n * static_cast<size_t>(max_pages_per_seq), false},
+                          {num_free_in, 4, false},
+                          {num_free_out == num_free_in ? nullptr : num_free_out, 4, true},
+                          {free_pages, 4 * static_cast<size_t>(free_capacity), true},
+                          {dev_status, 4, true}};
+    if (written_overlap(spans))
+        return NVFP4KV_ERR_INVALID_ARG;
+    StepTablesParams p{};
+    p.lens_a = old_lens;
+    p.lens_b = keep_lens;
+    p.block_table = const_cast<int32_t *>(block_table);
+    p.free_pages = free_pages;
+    p.free_pages_out = free_pages;
+    p.num_free_in = num_free_in;
+    p.num_free_out = num_free_out;
+    p.dev_status = dev_status;
+    p.batch = batch;
+    p.max_pages = max_pages_per_seq;
+    p.num_pages = num_pages;
+    p.free_capacity = free_capacity;
+    return from_cuda(launch_release_pages(p, to_cuda(stream)));
+}
+
+nvfp4kv_status nvfp4kv_qk_norm_rope(const void *q, int64_t q_stride, const void *k, int64_t k_stride,
+                                    nvfp4kv_dtype in_dtype, int32_t num_tokens, int32_t num_q_heads,
+                                    int32_t num_kv_heads, const int32_t *positions, const nvfp4kv_rope *rope,
+                                    const nvfp4kv_head_norm *norm, void *q_out, void *k_out,
+                                    nvfp4kv_stream_t stream)
+{
+    NormRopeParams p;
+    const nvfp4kv_status st = check_norm_rope(q, q_stride, k, k_stride, in_dtype, num_tokens, num_q_heads,
+                                              num_kv_heads, positions, rope, norm, q_out, p);
+    if (st != NVFP4KV_OK || num_tokens == 0)
+        return st;
+    if (k_out == nullptr || !aligned16(k_out))
+        return NVFP4KV_ERR_INVALID_ARG;
+    const int size = p.in_bf16 ? 2 : 4;
+    const int64_t q_row = static_cast<int64_t>(num_q_heads) * kHeadDim;
+    const int64_t k_row = static_cast<int64_t>(num_kv_heads) * kHeadDim;
+    const bool q_same = q_out == q && p.in_bf16 && q_stride == q_row;    // a row is read whole before it is written
+    const bool k_same = k_out == k && k_stride == k_row;
+    const size_t t = static_cast<size_t>(num_tokens), norm_bytes = kHeadDim * (p.weight_bf16 ? 2 : 4);
+    const Span spans[] = {{q_same ? nullptr : q, rows_bytes(q_stride, num_tokens, num_q_heads, size), false},
+                          {k_same ? nullptr : k, rows_bytes(k_stride, num_tokens, num_kv_heads, size), false},
+                          {positions, 4 * t, false},
+                          {p.q_weight, norm_bytes, false},
+                          {p.k_weight, norm_bytes, false},
+                          {q_out, t * q_row * 2, true},
+                          {k_out, t * k_row * size, true}};
+    if (written_overlap(spans))
+        return NVFP4KV_ERR_INVALID_ARG;
+    p.k_out = k_out;
+    return from_cuda(launch_norm_rope(p, to_cuda(stream)));
+}
+
+nvfp4kv_status nvfp4kv_qk_norm_rope_append(const nvfp4kv_cache *cache, const void *q, int64_t q_stride,
+                                           const void *k, int64_t k_stride, const void *v, int64_t v_stride,
+                                           nvfp4kv_dtype in_dtype, int32_t num_tokens, int32_t num_q_heads,
+                                           const int32_t *positions, const int32_t *slot_mapping,
+                                           const nvfp4kv_rope *rope, const nvfp4kv_head_norm *norm, void *q_out,
+                                           int32_t *dev_status, nvfp4kv_stream_t stream)
+{
+    nvfp4kv_status st = check_nvfp4(cache);
+    if (st != NVFP4KV_OK)
+        return st;
+    NormRopeParams p;
+    st = check_norm_rope(q, q_stride, k, k_stride, in_dtype, num_tokens, num_q_heads, cache->num_kv_heads, positions,
+                         rope, norm, q_out, p);
+    if (st != NVFP4KV_OK || num_tokens == 0)
+        return st;
+    if (static_cast<int64_t>(cache->num_pages) * kPageSize > (int64_t{1} << 31) - 1)
+        return NVFP4KV_ERR_UNSUPPORTED;      // slots are int32
+    const int size = p.in_bf16 ? 2 : 4;
+    if (!good_rows(v, v_stride, cache->num_kv_heads, size) || slot_mapping == nullptr || !aligned4(slot_mapping))
+        return NVFP4KV_ERR_INVALID_ARG;
+    const int64_t q_row = static_cast<int64_t>(num_q_heads) * kHeadDim;
+    const bool q_same = q_out == q && p.in_bf16 && q_stride == q_row;
+    const size_t t = static_cast<size_t>(num_tokens), norm_bytes = kHeadDim * (p.weight_bf16 ? 2 : 4);
+    const Span spans[] = {{q_same ? nullptr : q, rows_bytes(q_stride, num_tokens, num_q_heads, size), false},
+                          {k, rows_bytes(k_stride, num_tokens, p.hkv, size), false},
+                          {v, rows_bytes(v_stride, num_tokens, p.hkv, size), false},
+                          {positions, 4 * t, false},
+                          {slot_mapping, 4 * t, false},
+                          {p.q_weight, norm_bytes, false},
+                          {p.k_weight, norm_bytes, false},
+                          {q_out, t * q_row * 2, true},
+                          {cache->pool, static_cast<size_t>(cache->num_pages) * p.hkv * kNvfp4Record, true}};
+    if (written_overlap(spans))
+        return NVFP4KV_ERR_INVALID_ARG;
+    p.v = v;
+    p.v_stride = v_stride;
+    p.slot_mapping = slot_mapping;
+    p.pool = static_cast<uint8_t *>(cache->pool);
+    p.num_pages = cache->num_pages;
+    p.gscale = cache->global_scale;
+    p.hs = head_scales_of(cache);
+    p.dev_status = dev_status;
+    return from_cuda(launch_norm_rope(p, to_cuda(stream)));
 }
 
 nvfp4kv_status fp8kv_quantize_append(const fp8kv_cache *cache, const void *k_new, const void *v_new,

@@ -143,6 +143,65 @@ struct ExtendParams {
     CUtensorMap tm_v_chunk;
 };
 
+// Head norm and rotation of new queries and keys; with a pool the keys and
+// values go into the NVFP4 cache instead of k_out.
+struct NormRopeParams {
+    const void *q;               // rows [token][hq][128] at a token stride, in_dtype
+    const void *k;
+    const void *v;               // (append)
+    int64_t q_stride;            // elements from one token to the next
+    int64_t k_stride;
+    int64_t v_stride;
+    const int32_t *positions;    // [tokens], < 0: no such token
+    const void *q_weight;        // [128] or null: no norm
+    const void *k_weight;
+    uint16_t *q_out;             // bf16 [tokens][hq][128]
+    void *k_out;                 // [tokens][hkv][128], in_dtype
+    uint8_t *pool;               // append: page-head records
+    const int32_t *slot_mapping;
+    int32_t *dev_status;
+    int num_tokens;
+    int hq;
+    int hkv;
+    int num_pages;
+    int in_bf16;
+    int weight_bf16;
+    int rot;                     // rotated channels, a multiple of 32
+    int interleaved;
+    float eps;
+    float rope_scale;            // multiplies cos and sin
+    float gscale;
+    int heads_per_job;           // set by the launcher
+    int q_jobs;
+    int k_jobs;
+    HeadScales hs;
+    uint64_t freq[kHeadDim / 2]; // turns a position, in units of 2^-64
+};
+
+// A step's tables (plan: a = context lengths, b = new tokens) or the return of
+// pages (release: a = old lengths, b = lengths kept).
+struct StepTablesParams {
+    const int32_t *lens_a;       // [batch]
+    const int32_t *lens_b;       // [batch]
+    int32_t *block_table;        // [batch][max_pages]
+    const int32_t *free_pages;   // stack of free page ids, its top at num_free - 1 (plan)
+    int32_t *free_pages_out;     // the same (release)
+    const int32_t *num_free_in;
+    int32_t *num_free_out;       // may be num_free_in
+    int32_t *seq_lens;           // [batch]
+    int32_t *q_indptr;           // [batch + 1]
+    int32_t *kv_indptr;          // [batch], nullable
+    int32_t *slot_mapping;       // [max_tokens]
+    int32_t *positions;          // [max_tokens], nullable
+    int32_t *dev_status;
+    int batch;
+    int max_pages;
+    int num_pages;
+    int free_capacity;
+    int max_tokens;
+    int count_here;              // the kernel itself writes num_free_out (set by the launcher)
+};
+
 // Launch with programmatic stream serialisation allowed, so the kernel's
 // prologue may overlap the tail of the previous kernel in the stream; every
 // kernel launched this way calls pdl_wait() before touching data that the
@@ -175,6 +234,9 @@ cudaError_t launch_decode_nvfp4_multi(const DecodeParams &p, cudaStream_t s);
 cudaError_t launch_decode_fp8(const DecodeParams &p, cudaStream_t s);
 cudaError_t launch_merge(const DecodeParams &p, cudaStream_t s);
 cudaError_t launch_dequant_prefix_fp8(const PrefixParams &p, cudaStream_t s);
+cudaError_t launch_norm_rope(const NormRopeParams &p, cudaStream_t s);    // appends when p.pool != null
+cudaError_t launch_plan_step(const StepTablesParams &p, cudaStream_t s);
+cudaError_t launch_release_pages(const StepTablesParams &p, cudaStream_t s);
 cudaError_t launch_extend_attention(const ExtendParams &p, cudaStream_t s);   // appends when p.pool != null
 
 } // namespace nvfp4kv
