@@ -377,6 +377,53 @@ nvfp4kv_status nvfp4kv_extend_attention_fp8_append(const nvfp4kv_cache *cache,
                                                    void *out, nvfp4kv_dtype out_dtype,
                                                    int32_t *dev_status, nvfp4kv_stream_t stream);
 
+/* Chunk attention over the paged NVFP4 cache itself ("SGLang stores KV cache in
+ * 4 bits", Interpretation: attention dequantises the cached keys and values
+ * inside the kernel; there for decode, here for chunks of any length: prompt
+ * chunks, and drafted tokens to be checked, without the FP8 workspace, its
+ * pass over the prefix and its second rounding).  The chunk's tokens are in
+ * the cache already (nvfp4kv_quantize_append or nvfp4kv_qk_norm_rope_append):
+ * they are the last C = q_indptr[b+1] - q_indptr[b] of the seq_lens[b] tokens of
+ * sequence b, so chunk token t sits at position n = seq_lens[b] - C + t.  Query
+ * head i (kv head h = i / g) attends causally:
+ *   out[q_indptr[b] + t][i] = sum_j softmax_j(sm_scale * q . k_j) v_j over
+ *   j = max(0, n - window + 1) .. n   (window 0: j = 0 .. n)
+ * A row that sees no key (n < 0: a chunk longer than its sequence) gets zeros.
+ *   q            bf16 [q_rows][num_q_heads][128]
+ *   out          [q_rows][num_q_heads][128], out_dtype bf16 or fp32; rows
+ *                outside every [q_indptr[b], q_indptr[b+1]) are not written
+ *   q_indptr     int32 [batch + 1], seq_lens int32 [batch] (device)
+ *   block_table  int32 [batch][max_pages_per_seq] (device); only entries of pages
+ *                that some row sees are read, so entries that a window has left
+ *                behind may hold anything; one outside [0, num_pages) reads page
+ *                0 and sets NVFP4KV_DEV_BAD_PAGE
+ *   max_q_len    host bound on every C; it sizes the launch
+ *   window       0, or the number of keys a query sees at most, itself included
+ *   workspace    device scratch of at least the size below, 256-byte aligned,
+ *                not initialised (may be NULL when that is 0); two calls in
+ *                flight at once must not share it
+ * Pointers 16-byte aligned (index arrays 4-byte); out overlaps nothing else.
+ * Group g in 1..8, batch and kv heads at most 65535, max_q_len * g below 2^30.
+ * Arithmetic: every cached value is exact in fp16, q too (bf16 significands
+ * under a power of two a row; elements under 2^-28 of the row's largest lose
+ * bits), scores, softmax and outputs in fp32, softmax weights rounded to fp16
+ * for the value product.  A scale byte of 0x7F, which the quantiser never
+ * writes, reads as 480.  A sequence whose index range is outside [0, q_rows] or
+ * longer than max_q_len, or whose length is outside [0, max_pages_per_seq *
+ * 16], sets NVFP4KV_DEV_BAD_LEN and its rows are not written. */
+nvfp4kv_status nvfp4kv_paged_extend(const nvfp4kv_cache *cache, const void *q, const int32_t *q_indptr,
+                                    int32_t q_rows, int32_t max_q_len, int32_t batch, int32_t num_q_heads,
+                                    const int32_t *block_table, int32_t max_pages_per_seq,
+                                    const int32_t *seq_lens, int32_t window, float sm_scale, void *out,
+                                    nvfp4kv_dtype out_dtype, void *workspace, size_t workspace_bytes,
+                                    int32_t *dev_status, nvfp4kv_stream_t stream);
+
+/* Bytes of workspace that nvfp4kv_paged_extend needs with the same sizes on the
+ * current device (a library utility; 0 when the keys are not split, and for
+ * sizes that the call refuses).  Host only. */
+size_t nvfp4kv_paged_extend_workspace_size(int32_t q_rows, int32_t max_q_len, int32_t batch, int32_t num_q_heads,
+                                           int32_t num_kv_heads, int32_t max_pages_per_seq, int32_t window);
+
 /* ---- A step's tables, built on the device ------------------------------------
  *
  * A library utility: the pages name a paged cache ("SGLang stores KV cache in

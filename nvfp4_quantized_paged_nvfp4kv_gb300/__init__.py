@@ -21,6 +21,8 @@ Functions carry the C names and take torch tensors:
     nvfp4kv_dequant_prefix_fp8(cache, block_table, prefix_lens, kv_indptr, k_out, v_out)
     nvfp4kv_extend_attention_fp8(q, q_indptr, k_prefix, v_prefix, kv_indptr, prefix_lens, k_chunk, v_chunk, ...)
     nvfp4kv_extend_attention_fp8_append(cache, slot_mapping, q, q_indptr, ...)
+    nvfp4kv_paged_extend(cache, q, q_indptr, block_table, seq_lens, out, workspace, ...)
+    nvfp4kv_paged_extend_workspace_size(...), new_extend_workspace(...)
   around a step
     nvfp4kv_plan_step(context_lens, new_lens, block_table, num_pages, free_pages, num_free, ...)
     nvfp4kv_release_pages(old_lens, keep_lens, block_table, num_pages, free_pages, num_free, ...)
@@ -142,6 +144,9 @@ def load(build_if_missing: bool = True):
             "nvfp4kv_extend_attention_fp8_append": (_st, [ctypes.POINTER(_Nvfp4Cache), _vp, _vp, _vp, _i32, _i32,
                                                           _vp, _vp, _vp, _vp, ctypes.c_int64, _vp, _vp, _st,
                                                           _i32, _i32, ctypes.c_float, _vp, _st, _vp, _vp]),
+            "nvfp4kv_paged_extend": (_st, [ctypes.POINTER(_Nvfp4Cache), _vp, _vp, _i32, _i32, _i32, _i32, _vp, _i32, _vp,
+                                           _i32, ctypes.c_float, _vp, _st, _vp, ctypes.c_size_t, _vp, _vp]),
+            "nvfp4kv_paged_extend_workspace_size": (ctypes.c_size_t, [_i32] * 7),
             "nvfp4kv_plan_step": (_st, [_vp, _vp, _i32, _vp, _i32, _i32, _vp, _i32, _vp, _vp, _vp, _vp, _vp, _vp, _vp,
                                         _i32, _vp, _vp]),
             "nvfp4kv_release_pages": (_st, [_vp, _vp, _i32, _vp, _i32, _i32, _vp, _i32, _vp, _vp, _vp, _vp]),
@@ -446,6 +451,44 @@ def nvfp4kv_extend_attention_fp8_append(cache: NVFP4Cache, slot_mapping, q, q_in
     _check(st, "nvfp4kv_extend_attention_fp8_append")
 
 
+def nvfp4kv_paged_extend_workspace_size(q_rows, max_q_len, batch, num_q_heads, num_kv_heads, max_pages_per_seq,
+                                        window=0) -> int:
+    return int(load().nvfp4kv_paged_extend_workspace_size(q_rows, max_q_len, batch, num_q_heads, num_kv_heads,
+                                                          max_pages_per_seq, window))
+
+
+def nvfp4kv_paged_extend(cache: NVFP4Cache, q, q_indptr, block_table, seq_lens, out, workspace, max_q_len=None, window=0,
+                         sm_scale=None, dev_status=None, stream=None) -> None:
+    """Causal attention of a ragged chunk of tokens, already in the cache as the
+    last tokens of their sequences, over the paged NVFP4 cache.  q: bf16
+    [rows][Hq][128]; q_indptr int32 [B+1]; block_table int32 [B][pages];
+    seq_lens int32 [B]; out: bf16 or fp32 [rows][Hq][128]; workspace: see
+    new_extend_workspace (None where no bytes are needed).  max_q_len bounds
+    every chunk (read from q_indptr when None, which synchronises); window 0 or
+    the keys a query sees at most."""
+    import torch
+    if sm_scale is None:
+        sm_scale = 1.0 / math.sqrt(HEAD_DIM)
+    B, i32 = seq_lens.shape[0], torch.int32
+    rows, Hq, _ = q.shape
+    _tensor(q, "q", torch.bfloat16, (rows, Hq, HEAD_DIM))
+    _tensor(out, "out", out.dtype, (rows, Hq, HEAD_DIM))
+    _tensor(cache.pool, "cache", torch.uint8, cache.pool.shape)
+    for t, name, shape in ((q_indptr, "q_indptr", (B + 1,)), (block_table, "block_table", (B, None)),
+                           (seq_lens, "seq_lens", (B,)), (dev_status, "dev_status", (1,))):
+        if t is not None:
+            _tensor(t, name, i32, shape)
+    if workspace is not None:
+        _tensor(workspace, "workspace", torch.uint8, (None,))
+    if max_q_len is None:
+        max_q_len = int((q_indptr[1:] - q_indptr[:-1]).max().item()) if B > 0 else 0
+    st = load().nvfp4kv_paged_extend(
+        cache.c, _ptr(q), _ptr(q_indptr), rows, int(max_q_len), B, Hq, _ptr(block_table), block_table.shape[1],
+        _ptr(seq_lens), int(window), float(sm_scale), _ptr(out), _dtype_code(out), _ptr(workspace),
+        0 if workspace is None else workspace.numel(), _ptr(dev_status), _stream(stream))
+    _check(st, "nvfp4kv_paged_extend")
+
+
 def nvfp4kv_plan_step(context_lens, new_lens, block_table, num_pages, free_pages, num_free, num_free_out, seq_lens,
                       q_indptr, slot_mapping, positions=None, kv_indptr=None, dev_status=None, stream=None) -> None:
     """A step's tables from its requests' lengths (all int32 on the device):
@@ -598,4 +641,13 @@ def new_workspace(num_workers: int = 0, device="cuda"):
     """A decode workspace tensor of the size the library asks for."""
     import torch
     n = nvfp4kv_decode_workspace_size(num_workers)
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+
+
+def new_extend_workspace(q_rows, max_q_len, batch, num_q_heads, num_kv_heads, max_pages_per_seq, window=0,
+                         device="cuda"):
+    """A workspace tensor for nvfp4kv_paged_extend calls of these sizes."""
+    import torch
+    n = nvfp4kv_paged_extend_workspace_size(q_rows, max_q_len, batch, num_q_heads, num_kv_heads, max_pages_per_seq,
+                                            window)
     return torch.empty(max(n, 256), dtype=torch.uint8, device=device)

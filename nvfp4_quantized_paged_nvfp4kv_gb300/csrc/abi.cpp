@@ -326,6 +326,19 @@ nvfp4kv_status check_tables(const int32_t *a, const int32_t *b, int32_t batch, c
     return NVFP4KV_OK;
 }
 
+// Sizes of a paged extend call.
+nvfp4kv_status check_paged_extend_sizes(int32_t q_rows, int32_t max_q_len, int32_t batch, int32_t hq, int32_t hkv,
+                                        int32_t max_pages, int32_t window)
+{
+    if (q_rows < 0 || max_q_len < 0 || batch < 0 || hq <= 0 || hkv <= 0 || max_pages <= 0 || window < 0 || hq % hkv != 0)
+        return NVFP4KV_ERR_INVALID_ARG;
+    const int64_t group = hq / hkv;
+    if (group > kMaxGroup || hkv > 65535 || batch > 65535 || max_q_len * group >= (int64_t{1} << 30) ||
+        static_cast<int64_t>(max_pages) * kPageSize > (int64_t{1} << 30))
+        return NVFP4KV_ERR_UNSUPPORTED;
+    return NVFP4KV_OK;
+}
+
 // Rows of `heads` x 128 channels at a token stride: base and stride keep every
 // row on 16 bytes, and rows do not overlap.
 bool good_rows(const void *base, int64_t stride, int32_t heads, int elem_bytes)
@@ -587,6 +600,81 @@ nvfp4kv_status nvfp4kv_extend_attention_fp8_append(const nvfp4kv_cache *cache, c
     p.gscale = cache->global_scale;
     p.hs = head_scales_of(cache);
     return from_cuda(launch_extend_attention(p, to_cuda(stream)));
+}
+
+size_t nvfp4kv_paged_extend_workspace_size(int32_t q_rows, int32_t max_q_len, int32_t batch, int32_t num_q_heads,
+                                           int32_t num_kv_heads, int32_t max_pages_per_seq, int32_t window)
+{
+    if (check_paged_extend_sizes(q_rows, max_q_len, batch, num_q_heads, num_kv_heads, max_pages_per_seq, window) !=
+        NVFP4KV_OK)
+        return 0;
+    return paged_extend_shape(q_rows, max_q_len, batch, num_kv_heads, num_q_heads / num_kv_heads, max_pages_per_seq,
+                              window >= max_pages_per_seq * kPageSize ? 0 : window)
+        .workspace;
+}
+
+nvfp4kv_status nvfp4kv_paged_extend(const nvfp4kv_cache *cache, const void *q, const int32_t *q_indptr,
+                                    int32_t q_rows, int32_t max_q_len, int32_t batch, int32_t num_q_heads,
+                                    const int32_t *block_table, int32_t max_pages_per_seq,
+                                    const int32_t *seq_lens, int32_t window, float sm_scale, void *out,
+                                    nvfp4kv_dtype out_dtype, void *workspace, size_t workspace_bytes,
+                                    int32_t *dev_status, nvfp4kv_stream_t stream)
+{
+    nvfp4kv_status st = check_nvfp4(cache);
+    if (st != NVFP4KV_OK)
+        return st;
+    st = check_paged_extend_sizes(q_rows, max_q_len, batch, num_q_heads, cache->num_kv_heads, max_pages_per_seq, window);
+    if (st != NVFP4KV_OK)
+        return st;
+    if ((out_dtype != NVFP4KV_F32 && out_dtype != NVFP4KV_BF16) || !std::isfinite(sm_scale))
+        return NVFP4KV_ERR_INVALID_ARG;
+    if (batch == 0 || max_q_len == 0 || q_rows == 0)
+        return NVFP4KV_OK;
+    if (window >= max_pages_per_seq * kPageSize)
+        window = 0;                              // no sequence is longer
+    if (q == nullptr || out == nullptr || q_indptr == nullptr || block_table == nullptr || seq_lens == nullptr ||
+        !aligned16(q) || !aligned16(out) || !aligned4(q_indptr) || !aligned4(block_table) || !aligned4(seq_lens))
+        return NVFP4KV_ERR_INVALID_ARG;
+    const int32_t group = num_q_heads / cache->num_kv_heads;
+    const ExtendShape shape = paged_extend_shape(q_rows, max_q_len, batch, cache->num_kv_heads, group, max_pages_per_seq,
+                                                 window);
+    if (shape.workspace > 0 && (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
+                                workspace_bytes < shape.workspace))
+        return NVFP4KV_ERR_WORKSPACE;
+    const size_t elems = static_cast<size_t>(q_rows) * num_q_heads * kHeadDim;
+    const Span spans[] = {{q, 2 * elems, false},
+                          {q_indptr, 4 * (static_cast<size_t>(batch) + 1), false},
+                          {block_table, 4 * static_cast<size_t>(batch) * max_pages_per_seq, false},
+                          {seq_lens, 4 * static_cast<size_t>(batch), false},
+                          {cache->pool, static_cast<size_t>(cache->num_pages) * cache->num_kv_heads * kNvfp4Record, false},
+                          {out, elems * (out_dtype == NVFP4KV_F32 ? 4 : 2), true},
+                          {workspace, shape.workspace, true}};
+    if (written_overlap(spans))
+        return NVFP4KV_ERR_INVALID_ARG;
+    PagedExtendParams p{};
+    p.pool = static_cast<const uint8_t *>(cache->pool);
+    p.q = static_cast<const uint16_t *>(q);
+    p.q_indptr = q_indptr;
+    p.block_table = block_table;
+    p.seq_lens = seq_lens;
+    p.out = out;
+    p.partials = static_cast<float *>(workspace);
+    p.dev_status = dev_status;
+    p.batch = batch;
+    p.hq = num_q_heads;
+    p.hkv = cache->num_kv_heads;
+    p.group = group;
+    p.max_pages = max_pages_per_seq;
+    p.num_pages = cache->num_pages;
+    p.q_rows = q_rows;
+    p.max_q_len = max_q_len;
+    p.window = window;
+    p.out_f32 = out_dtype == NVFP4KV_F32;
+    p.qscale = static_cast<float>(static_cast<double>(sm_scale) * 1.4426950408889634);
+    p.gscale = cache->global_scale;
+    p.hs = head_scales_of(cache);
+    p.wait_limit = wait_limit();
+    return from_cuda(launch_paged_extend(p, shape, to_cuda(stream)));
 }
 
 nvfp4kv_status nvfp4kv_plan_step(const int32_t *context_lens, const int32_t *new_lens, int32_t batch,

@@ -143,6 +143,42 @@ struct ExtendParams {
     CUtensorMap tm_v_chunk;
 };
 
+// Chunk attention over the paged NVFP4 cache.
+struct PagedExtendParams {
+    const uint8_t *pool;         // page-head records
+    const uint16_t *q;           // bf16 [q_rows][hq][128]
+    const int32_t *q_indptr;     // [batch + 1]
+    const int32_t *block_table;  // [batch][max_pages]
+    const int32_t *seq_lens;     // [batch], the chunk's tokens included
+    void *out;                   // [q_rows][hq][128], bf16 or fp32
+    float *partials;             // splits > 1: [splits][q_rows][hq][128] O, then [..][2] maximum and sum
+    int32_t *dev_status;
+    int batch;
+    int hq;
+    int hkv;
+    int group;
+    int max_pages;
+    int num_pages;
+    int q_rows;
+    int max_q_len;
+    int window;                  // 0: none
+    int splits;                  // set by the launcher
+    int out_f32;
+    float qscale;                // sm_scale * log2(e)
+    float gscale;
+    HeadScales hs;
+    uint32_t wait_limit;
+};
+
+// How a paged extend call is cut: row blocks a CTA, row tiles a (sequence, kv
+// head), splits of the keys, and the bytes that the splits leave.
+struct ExtendShape {
+    int blocks;
+    int64_t row_tiles;
+    int splits;
+    size_t workspace;
+};
+
 // Head norm and rotation of new queries and keys; with a pool the keys and
 // values go into the NVFP4 cache instead of k_out.
 struct NormRopeParams {
@@ -234,6 +270,9 @@ cudaError_t launch_decode_nvfp4_multi(const DecodeParams &p, cudaStream_t s);
 cudaError_t launch_decode_fp8(const DecodeParams &p, cudaStream_t s);
 cudaError_t launch_merge(const DecodeParams &p, cudaStream_t s);
 cudaError_t launch_dequant_prefix_fp8(const PrefixParams &p, cudaStream_t s);
+ExtendShape paged_extend_shape(int64_t q_rows, int64_t max_q_len, int64_t batch, int64_t hkv, int64_t group,
+                               int64_t max_pages, int64_t window);
+cudaError_t launch_paged_extend(const PagedExtendParams &p, const ExtendShape &shape, cudaStream_t s);
 cudaError_t launch_norm_rope(const NormRopeParams &p, cudaStream_t s);    // appends when p.pool != null
 cudaError_t launch_plan_step(const StepTablesParams &p, cudaStream_t s);
 cudaError_t launch_release_pages(const StepTablesParams &p, cudaStream_t s);

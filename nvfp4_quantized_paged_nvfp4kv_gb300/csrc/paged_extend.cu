@@ -1,0 +1,681 @@
+// Attention of a ragged chunk of tokens over the paged NVFP4 cache itself, on
+// the fifth-generation tensor cores (tcgen05).
+//
+// Sequence b has seq_lens[b] = L cached tokens, the last C = q_indptr[b + 1] -
+// q_indptr[b] of them being the chunk; chunk token t sits at position
+// n = L - C + t and sees the keys max(0, n - window + 1) .. n (all up to n
+// without a window):
+//   o = sum_j softmax_j(sm_scale q . k_j) v_j,  k, v = G * E4M3 scale * E2M1 code.
+//
+// A row is a (chunk token, query head of the kv head's group) pair, taken
+// token-major.  A CTA owns kBlocks blocks of 128 rows of one sequence and kv
+// head, and a run of 64-key tiles.  Per tile:
+//   load      one warp copies the tile's four page records (2,304 bytes each,
+//             one bulk copy a page) into a ring, page ids looked up two windows
+//             of 32 pages ahead
+//   convert   four warps expand the codes to f16 in the operands' 128-byte
+//             swizzle, once for all row blocks: K as [64 keys][128 channels], V
+//             transposed as [128 channels][64 keys], so that the two tokens a V
+//             byte holds are neighbours in the operand
+//   S = Q K^T tcgen05.mma M128 N64 K16 x 8, Q resident in tensor memory (a Q
+//             operand in shared memory would take two thirds of this
+//             product's shared-memory bandwidth)
+//   softmax   one thread a row: mask, exp2 against a running maximum that is
+//             raised only when it grows by more than 2^8, P (f16) back into the
+//             columns of S
+//   O += P V  tcgen05.mma M128 N128 K16 x 4, P and O in tensor memory
+// With two row blocks the tensor core works on one block while the other is in
+// its softmax.
+//
+// Roundings.  Codes and scales: an E2M1 code (two significant bits) times an
+// E4M3 scale (four) is exact in f16.  The scale byte's seven bits moved to
+// f16's exponent and mantissa are the scale times 2^-8 without a conversion, so
+// K and V are held as value / (256 G) and the factors go to the scores and the
+// output in fp32.  Any byte gives a finite value this way (0x7F reads as 480
+// where E4M3 has NaN), so what masked places, unwritten slots and pages that
+// are not loaded hold cannot reach a row that does not see them.  Q: each row
+// times a power of two that puts its largest element in [2^14, 2^15), which
+// makes bf16 -> f16 exact but for elements under 2^-28 of the row's largest.
+// P is rounded to f16 (relative 2^-11, at most 2^8); scores, sums and O are
+// fp32.
+//
+// Few rows and many keys: the keys of each row block are split over
+// gridDim.x / tiles CTAs, each leaving its O, maximum and sum in the
+// workspace, which a second kernel joins.
+#include "tcgen05.cuh"
+
+namespace nvfp4kv {
+namespace {
+
+constexpr int kRowsBlock = 128;                // M of one MMA
+constexpr int kKeys = 64;                      // keys of a tile
+constexpr int kTilePages = kKeys / kPageSize;
+constexpr int kConvThreads = 128;
+constexpr float kRaise = 8.f;                  // log2 margin before the running maximum moves
+
+constexpr uint32_t kOpBytes = kKeys * kHeadDim * 2;            // 16 KB: a K or V operand tile
+constexpr uint32_t kRawBytes = kTilePages * kNvfp4Record;      // 9,216
+// tensor-memory columns of a row block: O (fp32), Q (f16 pairs), S (fp32; P
+// overwrites its first 32)
+constexpr uint32_t kTmO = 0, kTmQ = 128, kTmS = 192, kTmBlock = 256;
+
+template <int kBlocks>
+struct Shape {
+    static constexpr int kSoftmaxThreads = kBlocks * kRowsBlock;
+    static constexpr int kConvWarp = kSoftmaxThreads / 32;
+    static constexpr int kMmaWarp = kConvWarp + kConvThreads / 32;
+    static constexpr int kLoadWarp = kMmaWarp + 1;
+    static constexpr int kThreads = 32 * (kLoadWarp + 1);
+    static constexpr int kCtas = kBlocks == 1 ? 2 : 1;                 // on an SM
+    static constexpr int kStages = kBlocks == 1 ? 2 : 4;               // converted tiles
+    static constexpr int kRaw = kBlocks == 1 ? 4 : 8;                  // loaded tiles
+    static constexpr uint32_t kOffK = 0;
+    static constexpr uint32_t kOffV = kOffK + kStages * kOpBytes;
+    static constexpr uint32_t kOffRaw = kOffV + kStages * kOpBytes;
+    static constexpr uint32_t kOffBar = kOffRaw + kRaw * kRawBytes;
+    enum : int {
+        kRawFull = 0, kRawEmpty = kRawFull + kRaw, kKFull = kRawEmpty + kRaw, kVFull = kKFull + kStages,
+        kKEmpty = kVFull + kStages, kVEmpty = kKEmpty + kStages, kQFull = kVEmpty + kStages, kSFull = kQFull + kBlocks,
+        kPFull = kSFull + kBlocks, kDone = kPFull + kBlocks, kNumBars = kDone + 1
+    };
+    static constexpr uint32_t kOffSlot = kOffBar + 8 * kNumBars;
+    static constexpr uint32_t kSmem = kOffSlot + 8 + 1024;             // + slack to align the base
+    static constexpr uint32_t kTmemCols = kBlocks * kTmBlock;
+    static_assert(kCtas * (kSmem + 1024) <= 228 * 1024, "shared memory");
+    // (tensor memory is 512 columns: the CTAs that fit an SM never wait for it)
+    static_assert(kCtas * kTmemCols <= 512 && (kCtas + 1) * kSmem > 228 * 1024, "CTAs an SM");
+};
+
+__device__ __forceinline__ void st_shared128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+__device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int *fail, int32_t *dev_status,
+                                         uint32_t limit)
+{
+    if (*fail)
+        return false;
+    if (mbar_wait_bounded(bar, parity, limit))
+        return true;
+    *fail = 1;
+    report(dev_status, NVFP4KV_DEV_TIMEOUT);
+    return false;
+}
+
+// A sequence's chunk; false (nothing of it is written) when its index range,
+// or its length, is outside what the call was given.
+struct Chunk {
+    int c0, count, len;
+};
+
+__device__ __forceinline__ bool read_chunk(const PagedExtendParams &p, int b, Chunk &c)
+{
+    c.c0 = p.q_indptr[b];
+    const int c1 = p.q_indptr[b + 1];
+    c.len = p.seq_lens[b];
+    c.count = c1 - c.c0;
+    return c.c0 >= 0 && c1 >= c.c0 && c1 <= p.q_rows && c.count <= p.max_q_len && c.len >= 0 &&
+           c.len <= p.max_pages * kPageSize;
+}
+
+// K of a staged tile to f16 [key][channel], thread pt of 128: two quarter rows
+// of 32 channels.  Lanes of the upper channel half of a quarter pair store
+// their chunks in another order, so eight lanes meet eight bank groups.
+__device__ __forceinline__ void convert_k(uint32_t raw, uint32_t dst, int pt)
+{
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const uint32_t idx = pt + kConvThreads * u, key = idx >> 2, quarter = idx & 3u;
+        const uint32_t rec = raw + (key >> 4) * kNvfp4Record;
+        const uint4 d = lds128(rec + (key & 15u) * 64u + quarter * 16u);
+        const uint32_t two = lds_u16(rec + 2048u + (key & 15u) * 8u + 2u * quarter) & 0x7f7fu;
+        const bool swap = quarter & 2u;
+        const uint32_t w[4] = {swap ? d.z : d.x, swap ? d.w : d.y, swap ? d.x : d.z, swap ? d.y : d.w};
+        const uint32_t lo = two & 0xffu, hi = two >> 8;
+        const uint32_t sc[2] = {(swap ? hi : lo) * 0x00800080u, (swap ? lo : hi) * 0x00800080u};
+        const uint32_t row = dst + (quarter >> 1) * (kKeys * 128u) + key * 128u;
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i) {
+            uint32_t r0, r1, r2, r3;
+            e2m1x8_to_f16x2x4(w[i], r0, r1, r2, r3);
+            const uint32_t s = sc[i >> 1];
+            const uint32_t chunk = (4u * (quarter & 1u) + (i ^ (quarter & 2u))) ^ (key & 7u);
+            st_shared128(row + (chunk << 4), hmul2(r0, s), hmul2(r1, s), hmul2(r2, s), hmul2(r3, s));
+        }
+    }
+}
+
+// V of a staged tile to f16 [channel][key]: thread pt takes eight keys (half a
+// page, four token pairs), group g of the pairs' rows and half its blocks.
+__device__ __forceinline__ void convert_v(uint32_t raw, uint32_t dst, int pt)
+{
+    const uint32_t g = pt & 7, jh = (pt >> 3) & 1, eight = pt >> 4;
+    const uint32_t rec = raw + (eight >> 1) * kNvfp4Record, p0 = (eight & 1u) * 4u;
+    uint2 d[4], s[4];
+#pragma unroll
+    for (uint32_t r = 0; r < 4; ++r) {
+        const uint32_t p = p0 + r;
+        d[r] = lds64(rec + 1024u + p * 128u + ((g + 2u * p) & 7u) * 16u + 8u * jh);
+        s[r] = lds64(rec + 2176u + p * 16u + 8u * jh);
+    }
+#pragma unroll
+    for (uint32_t half = 0; half < 2; ++half) {
+        uint32_t f[4][4];                        // [pair row][(block, w)]: tokens 2p, 2p + 1
+#pragma unroll
+        for (uint32_t r = 0; r < 4; ++r) {
+            const uint32_t sw = (half ? s[r].y : s[r].x) & 0x7f7f7f7fu;
+            const uint32_t s0 = __byte_perm(sw, 0, 0x4140) << 7, s1 = __byte_perm(sw, 0, 0x4342) << 7;
+            e2m1x8_to_f16x2x4(half ? d[r].y : d[r].x, f[r][0], f[r][1], f[r][2], f[r][3]);
+            f[r][0] = hmul2(f[r][0], s0);
+            f[r][1] = hmul2(f[r][1], s0);
+            f[r][2] = hmul2(f[r][2], s1);
+            f[r][3] = hmul2(f[r][3], s1);
+        }
+#pragma unroll
+        for (uint32_t k = 0; k < 4; ++k) {
+            const uint32_t channel = 16u * (4u * jh + 2u * half + (k >> 1)) + 8u * (k & 1u) + g;
+            st_shared128(dst + channel * 128u + ((eight ^ g) << 4), f[0][k], f[1][k], f[2][k], f[3][k]);
+        }
+    }
+}
+
+template <int kBlocks>
+__global__ void __launch_bounds__(Shape<kBlocks>::kThreads, Shape<kBlocks>::kCtas)
+    paged_extend_kernel(const __grid_constant__ PagedExtendParams p)
+{
+    using S = Shape<kBlocks>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const uint32_t raw_addr = smem_addr(smem_raw);
+    const uint32_t base = (raw_addr + 1023u) & ~1023u;
+    uint8_t *gbase = smem_raw + (base - raw_addr);
+    volatile int *fail = reinterpret_cast<volatile int *>(gbase + S::kOffSlot + 4);
+    auto B = [&](int k) { return base + S::kOffBar + 8 * k; };
+
+    const int b = blockIdx.z, h = blockIdx.y;
+    const int row_tiles = static_cast<int>(gridDim.x) / p.splits;
+    const int split = static_cast<int>(blockIdx.x) % p.splits;
+    const int tile = row_tiles - 1 - static_cast<int>(blockIdx.x) / p.splits;   // later rows see more keys: first
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    Chunk c;
+    if (!read_chunk(p, b, c)) {
+        if (tid == 0 && tile == 0 && split == 0 && h == 0)
+            report(p.dev_status, NVFP4KV_DEV_BAD_LEN);
+        return;
+    }
+    const int g = p.group;
+    const int R = c.count * g;
+    const int row0 = tile * (kBlocks * kRowsBlock);
+    if (row0 >= R)
+        return;
+    const int first_pos = c.len - c.count;       // position of chunk token 0; negative when the chunk is longer
+    const int t_last = (min(row0 + kBlocks * kRowsBlock, R) - 1) / g;
+    const int key_end = max(0, first_pos + t_last + 1);
+    const int key_begin = p.window > 0 ? max(0, first_pos + row0 / g - p.window + 1) : 0;
+    int tile_lo = key_begin / kKeys, n_tiles = 0;
+    if (key_end > key_begin) {
+        const int all = (key_end + kKeys - 1) / kKeys - tile_lo;
+        const int from = static_cast<int>(static_cast<int64_t>(all) * split / p.splits);
+        n_tiles = static_cast<int>(static_cast<int64_t>(all) * (split + 1) / p.splits) - from;
+        tile_lo += from;
+    }
+
+    // this thread's row, when it is a softmax thread
+    const int row = row0 + tid;
+    const bool has_row = tid < S::kSoftmaxThreads && row < R;
+    const int t = min(row, R - 1) / g;
+    const int64_t out_row = static_cast<int64_t>(c.c0 + t) * p.hq + h * g + (min(row, R - 1) - t * g);
+    // where the partials go: [split][q_rows][hq][128], then [split][q_rows][hq][2]
+    const int64_t all_rows = static_cast<int64_t>(p.q_rows) * p.hq;
+    float *part_ml = p.partials + all_rows * p.splits * kHeadDim + 2 * (all_rows * split + out_row);
+
+    if (n_tiles <= 0) {
+        // no key of this range is visible to any row
+        if (has_row && p.splits > 1) {
+            part_ml[0] = -INFINITY;
+            part_ml[1] = 0.f;
+        } else if (has_row) {
+            const int words = p.out_f32 ? kHeadDim / 4 : kHeadDim / 8;
+            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.out) + out_row * kHeadDim * (p.out_f32 ? 4 : 2));
+            for (int k = 0; k < words; ++k)
+                dst[k] = make_uint4(0, 0, 0, 0);
+        }
+        return;
+    }
+
+    if (tid == 0) {
+        for (int k = 0; k < S::kRaw; ++k) {
+            mbar_init(B(S::kRawFull + k), 1);
+            mbar_init(B(S::kRawEmpty + k), kConvThreads);
+        }
+        for (int k = 0; k < S::kStages; ++k) {
+            mbar_init(B(S::kKFull + k), kConvThreads);
+            mbar_init(B(S::kVFull + k), kConvThreads);
+            mbar_init(B(S::kKEmpty + k), 1);
+            mbar_init(B(S::kVEmpty + k), 1);
+        }
+        for (int k = 0; k < kBlocks; ++k) {
+            mbar_init(B(S::kQFull + k), kRowsBlock);
+            mbar_init(B(S::kSFull + k), 1);
+            mbar_init(B(S::kPFull + k), kRowsBlock);
+        }
+        mbar_init(B(S::kDone), 1);
+        *fail = 0;
+        fence_mbar_init();
+    }
+    if (warp == S::kMmaWarp)
+        tmem_alloc(base + S::kOffSlot, S::kTmemCols);
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(gbase + S::kOffSlot);
+
+    if (warp == S::kLoadWarp) {
+        // lane l looks up page l % 4 of tile 8 w + l / 4, a window w ahead
+        const int page_lo = key_begin / kPageSize, page_hi = (key_end + kPageSize - 1) / kPageSize;
+        const int32_t *table = p.block_table + static_cast<size_t>(b) * p.max_pages;
+        auto lookup = [&](int i) {
+            const int pg = (tile_lo + i) * kTilePages + (lane & 3);
+            return i < n_tiles && pg >= page_lo && pg < page_hi ? __ldg(table + pg) : 0;
+        };
+        int cur = 0, nxt = lookup(lane >> 2);
+        int issued = 0;
+        for (int i = 0; i < n_tiles; ++i) {
+            if ((i & 7) == 0) {
+                cur = nxt;
+                nxt = lookup(i + 8 + (lane >> 2));
+                if (static_cast<unsigned>(cur) >= static_cast<unsigned>(p.num_pages)) {
+                    report(p.dev_status, NVFP4KV_DEV_BAD_PAGE);
+                    cur = 0;
+                }
+            }
+            const int st = i % S::kRaw;
+            // the stage was last read by the converters for tile i - kRaw
+            bool ok = true;
+            if (i >= S::kRaw)
+                ok = wait_bar(B(S::kRawEmpty + st), (i / S::kRaw - 1) & 1, fail, p.dev_status, p.wait_limit);
+            if (!__all_sync(kFullMask, ok))
+                break;
+            const int pg0 = (tile_lo + i) * kTilePages;
+            const int n = min(pg0 + kTilePages, page_hi) - max(pg0, page_lo);
+            if (lane == 0)
+                mbar_arrive_expect_tx(B(S::kRawFull + st), n * kNvfp4Record);
+            __syncwarp();
+            const int pg = pg0 + (lane & 3);
+            if ((lane >> 2) == (i & 7) && pg >= page_lo && pg < page_hi)
+                bulk_g2s(base + S::kOffRaw + st * kRawBytes + (lane & 3) * kNvfp4Record,
+                         p.pool + (static_cast<size_t>(cur) * p.hkv + h) * kNvfp4Record, kNvfp4Record,
+                         B(S::kRawFull + st));
+            ++issued;
+        }
+        // nothing issued may still be in flight when the CTA exits
+        for (int i = max(0, issued - S::kRaw); i < issued; ++i)
+            if (!mbar_wait_bounded(B(S::kRawFull + i % S::kRaw), (i / S::kRaw) & 1, kWaitLimit))
+                report(p.dev_status, NVFP4KV_DEV_TIMEOUT);
+        __syncwarp();
+    } else if (warp == S::kMmaWarp) {
+        if (lane == 0) {
+            constexpr uint32_t i_qk = idesc_f16(kRowsBlock, kKeys, false);
+            constexpr uint32_t i_pv = idesc_f16(kRowsBlock, kHeadDim, false);
+            auto wait = [&](int k, uint32_t parity) {
+                return wait_bar(B(k), parity, fail, p.dev_status, p.wait_limit);
+            };
+            auto qk = [&](int blk, int i) {
+                const uint32_t tb = tmem + blk * kTmBlock, kb = base + S::kOffK + (i % S::kStages) * kOpBytes;
+                tc_fence_after_sync();
+#pragma unroll
+                for (int s = 0; s < 8; ++s)
+                    umma_f16_ts(tb + kTmS, tb + kTmQ + 8 * s,
+                                smem_desc(kb + (s >> 2) * (kKeys * 128) + (s & 3) * 32, 16, 1024), i_qk, s > 0);
+                umma_commit(B(S::kSFull + blk));
+                if (blk == kBlocks - 1)
+                    umma_commit(B(S::kKEmpty + i % S::kStages));
+            };
+            auto pv = [&](int blk, int i) {
+                const uint32_t tb = tmem + blk * kTmBlock, vb = base + S::kOffV + (i % S::kStages) * kOpBytes;
+                tc_fence_after_sync();
+#pragma unroll
+                for (int s = 0; s < 4; ++s)
+                    umma_f16_ts(tb + kTmO, tb + kTmS + 8 * s, smem_desc(vb + 32 * s, 16, 1024), i_pv, i > 0 || s > 0);
+                if (blk == kBlocks - 1)
+                    umma_commit(B(S::kVEmpty + i % S::kStages));
+            };
+            // P V of tile i and Q K^T of tile i + 2 - 1 follow one another for
+            // each block in turn; S of a block is overwritten only after the
+            // product that reads its P, in issue order
+            bool ok = true;
+            for (int blk = 0; ok && blk < kBlocks; ++blk) {
+                ok = wait(S::kQFull + blk, 0) && (blk > 0 || wait(S::kKFull, 0));
+                if (ok)
+                    qk(blk, 0);
+            }
+            for (int i = 0; ok && i < n_tiles; ++i)
+                for (int blk = 0; ok && blk < kBlocks; ++blk) {
+                    ok = wait(S::kPFull + blk, i & 1) && (blk > 0 || wait(S::kVFull + i % S::kStages, (i / S::kStages) & 1));
+                    if (!ok)
+                        break;
+                    pv(blk, i);
+                    if (i + 1 < n_tiles) {
+                        ok = blk > 0 || wait(S::kKFull + (i + 1) % S::kStages, ((i + 1) / S::kStages) & 1);
+                        if (ok)
+                            qk(blk, i + 1);
+                    }
+                }
+            // nothing of this thread's may still run when tensor memory is freed
+            umma_commit(B(S::kDone));
+            if (!mbar_wait_bounded(B(S::kDone), 0, kWaitLimit))
+                report(p.dev_status, NVFP4KV_DEV_TIMEOUT);
+        }
+        __syncwarp();
+    } else if (warp >= S::kConvWarp) {
+        const int pt = tid - S::kSoftmaxThreads;
+        for (int i = 0; i < n_tiles; ++i) {
+            const int st = i % S::kStages, rs = i % S::kRaw;
+            const uint32_t raw = base + S::kOffRaw + rs * kRawBytes;
+            if (!wait_bar(B(S::kRawFull + rs), (i / S::kRaw) & 1, fail, p.dev_status, p.wait_limit))
+                break;
+            // the operand stages were last read by the products of tile i - kStages
+            if (i >= S::kStages &&
+                !wait_bar(B(S::kKEmpty + st), (i / S::kStages - 1) & 1, fail, p.dev_status, p.wait_limit))
+                break;
+            convert_k(raw, base + S::kOffK + st * kOpBytes, pt);
+            fence_async_shared();
+            mbar_arrive(B(S::kKFull + st));
+            if (i >= S::kStages &&
+                !wait_bar(B(S::kVEmpty + st), (i / S::kStages - 1) & 1, fail, p.dev_status, p.wait_limit))
+                break;
+            convert_v(raw, base + S::kOffV + st * kOpBytes, pt);
+            fence_async_shared();                // also orders the reads of the stage before its next copy
+            mbar_arrive(B(S::kVFull + st));
+            mbar_arrive(B(S::kRawEmpty + rs));
+        }
+    } else {
+        const int blk = warp >> 2;
+        const uint32_t tb = tmem + blk * kTmBlock + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        // the row of Q, scaled by a power of two; inv takes scores to log2 units
+        float inv;
+        {
+            uint32_t w[64];
+            const uint4 *src = reinterpret_cast<const uint4 *>(p.q + out_row * kHeadDim);
+            uint32_t m2 = 0;
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+                const uint4 v = has_row ? __ldg(src + k) : make_uint4(0, 0, 0, 0);
+                w[4 * k] = v.x;
+                w[4 * k + 1] = v.y;
+                w[4 * k + 2] = v.z;
+                w[4 * k + 3] = v.w;
+                m2 = __vmaxu2(m2, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                                           __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
+            }
+            const int expo = static_cast<int>(max(m2 & 0xffffu, m2 >> 16) >> 7);          // of the largest |q|
+            const int e = min(14 - (expo - 127), 112);
+            const float ks = p.hs.per_head ? p.hs.k[h] : p.gscale;
+            inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23) * 256.f * ks * fabsf(p.qscale);
+            float sc = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+            sc = p.qscale < 0.f ? -sc : sc;      // scores keep their order: the maximum is taken before inv
+            if (inv == 0.f) {                    // all scores are 0
+                inv = 1.f;
+                sc = 0.f;
+            }
+#pragma unroll
+            for (int k = 0; k < 64; ++k)
+                w[k] = pack_f16x2(__uint_as_float(w[k] << 16) * sc, __uint_as_float(w[k] & 0xffff0000u) * sc);
+            uint32_t half[32];
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+                half[k] = w[k];
+            tmem_st32(tb + kTmQ, half);
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+                half[k] = w[32 + k];
+            tmem_st32(tb + kTmQ + 32, half);
+            tmem_wait_st();
+            tc_fence_before_sync();
+            mbar_arrive(B(S::kQFull + blk));
+        }
+        const int pos = first_pos + t;           // keys lo .. pos are visible
+        const int lo = p.window > 0 ? pos - p.window + 1 : 0;
+        const uint64_t inv2 = f32x2_pack(inv, inv);
+        float m_used = -INFINITY, l = 0.f;
+        bool ok = true;
+        // the warp leaves together: its tensor-memory accesses are warp-wide
+        auto wait_warp = [&](int k, uint32_t parity) {
+            return __all_sync(kFullMask, wait_bar(B(k), parity, fail, p.dev_status, p.wait_limit));
+        };
+        for (int i = 0; i < n_tiles; ++i) {
+            if (!(ok = wait_warp(S::kSFull + blk, i & 1)))
+                break;
+            tc_fence_after_sync();
+            float s[64];
+            {
+                uint32_t s0[32], s1[32];
+                tmem_ld32(tb + kTmS, s0);
+                tmem_ld32(tb + kTmS + 32, s1);
+                tmem_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 32; ++j) {
+                    s[j] = __uint_as_float(s0[j]);
+                    s[j + 32] = __uint_as_float(s1[j]);
+                }
+            }
+            const int k0 = (tile_lo + i) * kKeys;
+            const int hi_j = pos + 1 - k0, lo_j = lo - k0;
+            if (hi_j < kKeys || lo_j > 0) {
+#pragma unroll
+                for (int j = 0; j < 64; ++j)
+                    if (j >= hi_j || j < lo_j)
+                        s[j] = -INFINITY;
+            }
+            float pm[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                pm[k] = fmax3(fmax3(s[8 * k], s[8 * k + 1], s[8 * k + 2]), fmax3(s[8 * k + 3], s[8 * k + 4], s[8 * k + 5]),
+                              fmaxf(s[8 * k + 6], s[8 * k + 7]));
+            const float mx = fmax3(fmax3(pm[0], pm[1], pm[2]), fmax3(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7])) * inv;
+            const bool need = mx > m_used + kRaise;
+            const float m_new = need ? mx : m_used;
+            const float mbase = m_new == -INFINITY ? 0.f : m_new;
+            const float alpha = need ? fast_exp2(m_used - mbase) : 1.f;
+            const uint64_t neg2 = f32x2_pack(-mbase, -mbase);
+            uint64_t acc[4] = {0, 0, 0, 0};
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+                const uint64_t d = fma_f32x2(f32x2_pack(s[2 * j], s[2 * j + 1]), inv2, neg2);
+                s[2 * j] = fast_exp2(f32x2_lo(d));
+                s[2 * j + 1] = fast_exp2(f32x2_hi(d));
+                acc[j & 3] = add_f32x2(acc[j & 3], f32x2_pack(s[2 * j], s[2 * j + 1]));
+            }
+            const uint64_t a = add_f32x2(add_f32x2(acc[0], acc[1]), add_f32x2(acc[2], acc[3]));
+            l = l * alpha + (f32x2_lo(a) + f32x2_hi(a));
+            m_used = m_new;
+            {
+                uint32_t pw[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    pw[j] = pack_f16x2(s[2 * j], s[2 * j + 1]);
+                tmem_st32(tb + kTmS, pw);
+            }
+            // a raised maximum: rescale the O rows of the warp (S of this tile
+            // was committed after P V of the one before, which has landed)
+            if (i >= 1 && __any_sync(kFullMask, need)) {
+#pragma unroll
+                for (int cb = 0; cb < 4; ++cb) {
+                    uint32_t o[32];
+                    tmem_ld32(tb + kTmO + 32 * cb, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+                    tmem_st32(tb + kTmO + 32 * cb, o);
+                }
+            }
+            tmem_wait_st();
+            tc_fence_before_sync();
+            mbar_arrive(B(S::kPFull + blk));
+        }
+        if (ok)
+            ok = wait_warp(S::kDone, 0);
+        if (ok) {
+            tc_fence_after_sync();
+            const float vs = (p.hs.per_head ? p.hs.v[h] : p.gscale) * 256.f;
+            const float f = p.splits > 1 ? vs : (l > 0.f ? vs / l : (l == 0.f ? 0.f : l));   // a NaN sum stays NaN
+            float *part_o = p.partials + (all_rows * split + out_row) * kHeadDim;
+            if (has_row && p.splits > 1) {
+                part_ml[0] = m_used;
+                part_ml[1] = l;
+            }
+#pragma unroll
+            for (int cb = 0; cb < 4; ++cb) {
+                uint32_t o[32];
+                tmem_ld32(tb + kTmO + 32 * cb, o);
+                tmem_wait_ld();
+                if (!has_row)
+                    continue;
+                if (p.splits > 1 || p.out_f32) {
+                    float *row_f = p.splits > 1 ? part_o : static_cast<float *>(p.out) + out_row * kHeadDim;
+                    float4 *dst = reinterpret_cast<float4 *>(row_f + 32 * cb);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        dst[k] = make_float4(__uint_as_float(o[4 * k]) * f, __uint_as_float(o[4 * k + 1]) * f,
+                                             __uint_as_float(o[4 * k + 2]) * f, __uint_as_float(o[4 * k + 3]) * f);
+                } else {
+                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + out_row * kHeadDim + 32 * cb);
+                    auto bf2 = [&](int j) {
+                        const __nv_bfloat162 two =
+                            __floats2bfloat162_rn(__uint_as_float(o[j]) * f, __uint_as_float(o[j + 1]) * f);
+                        return *reinterpret_cast<const uint32_t *>(&two);
+                    };
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        dst[k] = make_uint4(bf2(8 * k), bf2(8 * k + 2), bf2(8 * k + 4), bf2(8 * k + 6));
+                }
+            }
+        }
+    }
+
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == S::kMmaWarp) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, S::kTmemCols);
+    }
+}
+
+// Joins the splits of each row: with M = max_s m_s,
+//   o = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s.
+// One warp a (token, query head), four channels a lane.  Rows that no split saw
+// a key for get zeros; a split without keys left no O and is not read.
+__global__ void __launch_bounds__(256) paged_extend_join_kernel(const __grid_constant__ PagedExtendParams p)
+{
+    pdl_wait();
+    const int b = blockIdx.y, lane = threadIdx.x & 31;
+    Chunk c;
+    if (!read_chunk(p, b, c))
+        return;
+    const int64_t n = static_cast<int64_t>(c.count) * p.hq;
+    const int64_t i = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    if (i >= n)
+        return;
+    const int64_t all_rows = static_cast<int64_t>(p.q_rows) * p.hq, row = static_cast<int64_t>(c.c0) * p.hq + i;
+    const float *ml = p.partials + all_rows * p.splits * kHeadDim;
+    // lane s holds split s's maximum and sum (at most 32 splits)
+    float m = -INFINITY, l = 0.f;
+    if (lane < p.splits) {
+        const float2 v = __ldcg(reinterpret_cast<const float2 *>(ml) + all_rows * lane + row);
+        m = v.x;
+        l = v.y;
+    }
+    float M = m;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        M = fmaxf(M, __shfl_xor_sync(kFullMask, M, o));
+    const float w = m == -INFINITY ? 0.f : fast_exp2(m - M);
+    float den = w * l;
+    if (m == -INFINITY && l != l)
+        den = l;                                 // a row of NaN scores stays NaN
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        den += __shfl_xor_sync(kFullMask, den, o);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int s = 0; s < p.splits; ++s) {
+        const float ws = __shfl_sync(kFullMask, w, s);
+        if (ws == 0.f)
+            continue;
+        const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.partials + (all_rows * s + row) * kHeadDim) + lane);
+        acc.x += ws * v.x;
+        acc.y += ws * v.y;
+        acc.z += ws * v.z;
+        acc.w += ws * v.w;
+    }
+    const float f = den > 0.f ? 1.f / den : (den == 0.f ? 0.f : den);
+    acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+    if (den != den)
+        acc = make_float4(den, den, den, den);
+    if (p.out_f32) {
+        reinterpret_cast<float4 *>(static_cast<float *>(p.out) + row * kHeadDim)[lane] = acc;
+    } else {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(acc.x, acc.y), d = __floats2bfloat162_rn(acc.z, acc.w);
+        reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + row * kHeadDim)[lane] =
+            make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&d));
+    }
+}
+
+constexpr int kMaxSplits = 32;                 // a lane of the joining warp each
+constexpr int kMinSplitKeys = 512;             // keys that a split should have at least
+
+} // namespace
+
+// Row blocks a CTA takes and splits of the keys, from sizes the host knows.
+ExtendShape paged_extend_shape(int64_t q_rows, int64_t max_q_len, int64_t batch, int64_t hkv, int64_t group,
+                               int64_t max_pages, int64_t window)
+{
+    ExtendShape s;
+    if (max_q_len > q_rows)
+        max_q_len = q_rows;                      // no chunk is longer
+    s.blocks = max_q_len * group > kRowsBlock ? 2 : 1;
+    const int64_t rows = kRowsBlock * s.blocks;
+    s.row_tiles = (max_q_len * group + rows - 1) / rows;
+    const int64_t ctas = batch * s.row_tiles, filled = q_rows * group / rows + batch;
+    const int64_t units = hkv * (ctas < filled ? ctas : filled);
+    const int64_t slots = static_cast<int64_t>(sm_count()) * (s.blocks == 1 ? 2 : 1);
+    int64_t keys = max_pages * kPageSize;
+    if (window > 0 && window + max_q_len < keys)
+        keys = window + max_q_len;
+    int64_t n = units > 0 ? slots / units : 1;
+    if (n > keys / kMinSplitKeys)
+        n = keys / kMinSplitKeys;
+    s.splits = static_cast<int>(n < 1 ? 1 : (n > kMaxSplits ? kMaxSplits : n));
+    s.workspace = s.splits > 1 ? static_cast<size_t>(s.splits) * q_rows * hkv * group * (kHeadDim + 2) * sizeof(float) : 0;
+    return s;
+}
+
+template <int kBlocks>
+static cudaError_t launch_blocks(const PagedExtendParams &p, const ExtendShape &shape, cudaStream_t s)
+{
+    using S = Shape<kBlocks>;
+    const cudaError_t e = cudaFuncSetAttribute(paged_extend_kernel<kBlocks>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    if (e != cudaSuccess)
+        return e;
+    const dim3 grid(static_cast<unsigned>(shape.row_tiles * shape.splits), p.hkv, p.batch);
+    paged_extend_kernel<kBlocks><<<grid, S::kThreads, S::kSmem, s>>>(p);
+    return cudaGetLastError();
+}
+
+cudaError_t launch_paged_extend(const PagedExtendParams &in, const ExtendShape &shape, cudaStream_t s)
+{
+    PagedExtendParams p = in;
+    p.splits = shape.splits;
+    const cudaError_t e = shape.blocks == 1 ? launch_blocks<1>(p, shape, s) : launch_blocks<2>(p, shape, s);
+    if (e != cudaSuccess || shape.splits == 1)
+        return e;
+    const int64_t rows = static_cast<int64_t>(p.max_q_len < p.q_rows ? p.max_q_len : p.q_rows) * p.hq;
+    if ((rows + 7) / 8 > 0x7fffffffLL)
+        return cudaErrorInvalidValue;
+    return launch_pdl(paged_extend_join_kernel, dim3(static_cast<unsigned>((rows + 7) / 8), p.batch), dim3(256), 0, s, p);
+}
+
+} // namespace nvfp4kv

@@ -145,3 +145,37 @@ def test_rope_holds_its_frequencies():
     r = nv.Rope([1.0, 0.5] * 16, interleaved=True, scale=2.0)
     assert (r.rotary_dim, r._c.interleaved, r._c.scale) == (64, 1, 2.0)
     assert list(r._f) == [1.0, 0.5] * 16
+
+
+def extend(q=addr(0), qi=addr(1), rows=100, mql=50, batch=2, hq=4, bt=addr(2), mp=20, sl=addr(3), window=0, scale=0.088,
+           out=addr(4), dtype=nv.BF16, ws=addr(5), wsb=1 << 30, **cache):
+    kw = dict(pool=addr(7), num_pages=10, num_kv_heads=2, page_size=16, head_dim=128, global_scale=1.0)
+    kw.update(cache)
+    return nv.load().nvfp4kv_paged_extend(ctypes.byref(_Nvfp4Cache(**kw)), q, qi, rows, mql, batch, hq, bt, mp, sl,
+                                          window, scale, out, dtype, ws, wsb, None, None)
+
+
+@pytest.mark.parametrize("kw,want", [
+    (dict(rows=-1), nv.ERR_INVALID_ARG), (dict(mql=-1), nv.ERR_INVALID_ARG), (dict(batch=-1), nv.ERR_INVALID_ARG),
+    (dict(hq=0), nv.ERR_INVALID_ARG), (dict(hq=5), nv.ERR_INVALID_ARG), (dict(mp=0), nv.ERR_INVALID_ARG),
+    (dict(window=-1), nv.ERR_INVALID_ARG), (dict(hq=18), nv.ERR_UNSUPPORTED), (dict(batch=65536), nv.ERR_UNSUPPORTED),
+    (dict(mql=1 << 29), nv.ERR_UNSUPPORTED), (dict(mp=(1 << 26) + 1), nv.ERR_UNSUPPORTED),
+    (dict(dtype=nv.E4M3), nv.ERR_INVALID_ARG), (dict(scale=float("nan")), nv.ERR_INVALID_ARG),
+    (dict(q=None), nv.ERR_INVALID_ARG), (dict(out=None), nv.ERR_INVALID_ARG), (dict(sl=None), nv.ERR_INVALID_ARG),
+    (dict(q=addr(0) + 8), nv.ERR_INVALID_ARG), (dict(out=addr(4) + 8), nv.ERR_INVALID_ARG),
+    (dict(qi=addr(1) + 2), nv.ERR_INVALID_ARG), (dict(bt=addr(2) + 2), nv.ERR_INVALID_ARG),
+    (dict(out=addr(0)), nv.ERR_INVALID_ARG), (dict(out=addr(7) + 16), nv.ERR_INVALID_ARG),
+    (dict(out=addr(3) - 1024), nv.ERR_INVALID_ARG),
+    (dict(global_scale=-1.0), nv.ERR_UNSUPPORTED), (dict(pool=None), nv.ERR_INVALID_ARG),
+])
+def test_paged_extend_refusals(kw, want):
+    assert extend(**kw) == want
+
+
+def test_paged_extend_nothing_to_do_and_sizes():
+    none = dict(q=None, qi=None, bt=None, sl=None, out=None, ws=None)
+    assert extend(batch=0, **none) == nv.OK
+    assert extend(mql=0, **none) == nv.OK
+    assert extend(rows=0, **none) == nv.OK
+    size = nv.load().nvfp4kv_paged_extend_workspace_size
+    assert size(-1, 1, 1, 8, 2, 4, 0) == size(1, 1, 1, 7, 2, 4, 0) == 0     # sizes that the call refuses
