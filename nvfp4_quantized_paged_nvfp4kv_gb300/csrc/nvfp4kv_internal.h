@@ -170,10 +170,11 @@ struct PagedExtendParams {
     uint32_t wait_limit;
 };
 
-// How a paged extend call is cut: row blocks a CTA, row tiles a (sequence, kv
-// head), splits of the keys, and the bytes that the splits leave.
+// How a paged extend call is cut: whether a CTA's two MMA blocks share their
+// rows (and halve the keys), row tiles a (sequence, kv head), splits of the
+// keys, and the bytes that the splits leave.
 struct ExtendShape {
-    int blocks;
+    bool key_split;
     int64_t row_tiles;
     int splits;
     size_t workspace;

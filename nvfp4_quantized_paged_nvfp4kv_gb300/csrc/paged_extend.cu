@@ -8,24 +8,26 @@
 //   o = sum_j softmax_j(sm_scale q . k_j) v_j,  k, v = G * E4M3 scale * E2M1 code.
 //
 // A row is a (chunk token, query head of the kv head's group) pair, taken
-// token-major.  A CTA owns kBlocks blocks of 128 rows of one sequence and kv
-// head, and a run of 64-key tiles.  Per tile:
-//   load      one warp copies the tile's four page records (2,304 bytes each,
-//             one bulk copy a page) into a ring, page ids looked up two windows
-//             of 32 pages ahead
+// token-major.  A CTA owns rows of one sequence and kv head and a run of 128-key
+// tiles, and has two MMA blocks of 128 rows at work: two row blocks that share
+// every tile (kKeySplit false), or, where a sequence has no more than 128 rows
+// a kv head, the same row block twice, one copy on the even tiles and one on
+// the odd ones, joined in shared memory at the end (kKeySplit true).  The tensor
+// core works for one block while the other is in its softmax.  Per tile:
+//   load      one warp copies the page records (2,304 bytes each, one bulk copy
+//             a page) into a ring of 64-key granules, page ids looked up a
+//             window of 32 pages ahead
 //   convert   four warps expand the codes to f16 in the operands' 128-byte
-//             swizzle, once for all row blocks: K as [64 keys][128 channels], V
-//             transposed as [128 channels][64 keys], so that the two tokens a V
-//             byte holds are neighbours in the operand
-//   S = Q K^T tcgen05.mma M128 N64 K16 x 8, Q resident in tensor memory (a Q
-//             operand in shared memory would take two thirds of this
-//             product's shared-memory bandwidth)
+//             swizzle: K as [128 keys][128 channels], V transposed as
+//             [128 channels][128 keys], so that the two tokens that a V byte
+//             holds are neighbours in the operand
+//   S = Q K^T tcgen05.mma M128 N128 K16 x 8, Q in shared memory
 //   softmax   one thread a row: mask, exp2 against a running maximum that is
 //             raised only when it grows by more than 2^8, P (f16) back into the
 //             columns of S
-//   O += P V  tcgen05.mma M128 N128 K16 x 4, P and O in tensor memory
-// With two row blocks the tensor core works on one block while the other is in
-// its softmax.
+//   O += P V  tcgen05.mma M128 N128 K16 x 8, P and O in tensor memory
+// Tiles of 64 keys with Q in tensor memory, which spare the Q reads, ran at half
+// the rate: an M128 N64 MMA takes the tensor core the 64 cycles of an N128 one.
 //
 // Roundings.  Codes and scales: an E2M1 code (two significant bits) times an
 // E4M3 scale (four) is exact in f16.  The scale byte's seven bits moved to
@@ -39,68 +41,84 @@
 // P is rounded to f16 (relative 2^-11, at most 2^8); scores, sums and O are
 // fp32.
 //
-// Few rows and many keys: the keys of each row block are split over
-// gridDim.x / tiles CTAs, each leaving its O, maximum and sum in the
-// workspace, which a second kernel joins.
+// Few rows and many keys: the keys are split over gridDim.x / tiles CTAs, each
+// leaving its O, maximum and sum in the workspace, which a second kernel joins.
 #include "tcgen05.cuh"
 
 namespace nvfp4kv {
 namespace {
 
 constexpr int kRowsBlock = 128;                // M of one MMA
-constexpr int kKeys = 64;                      // keys of a tile
-constexpr int kTilePages = kKeys / kPageSize;
+constexpr int kKeys = 128;                     // keys of a tile
+constexpr int kGranKeys = 64;                  // keys of a granule: what is loaded and converted at a time
+constexpr int kGrans = kKeys / kGranKeys;
+constexpr int kGranPages = kGranKeys / kPageSize;
 constexpr int kConvThreads = 128;
 constexpr float kRaise = 8.f;                  // log2 margin before the running maximum moves
 
-constexpr uint32_t kOpBytes = kKeys * kHeadDim * 2;            // 16 KB: a K or V operand tile
-constexpr uint32_t kRawBytes = kTilePages * kNvfp4Record;      // 9,216
-// tensor-memory columns of a row block: O (fp32), Q (f16 pairs), S (fp32; P
-// overwrites its first 32)
-constexpr uint32_t kTmO = 0, kTmQ = 128, kTmS = 192, kTmBlock = 256;
+constexpr uint32_t kOpBytes = kKeys * kHeadDim * 2;            // 32 KB: a Q, K or V operand tile
+constexpr uint32_t kHalfBytes = kOpBytes / 2;                  // its 64-channel (V: 64-key) half: 128 rows of 128 bytes
+constexpr uint32_t kRawBytes = kGranPages * kNvfp4Record;      // 9,216
+// tensor-memory columns of a block: O (fp32), S (fp32; P overwrites its first 64)
+constexpr uint32_t kTmO = 0, kTmS = 128, kTmBlock = 256;
 
-template <int kBlocks>
+constexpr int kSoftmaxThreads = 2 * kRowsBlock;
+constexpr int kConvWarp = kSoftmaxThreads / 32;
+constexpr int kMmaWarp = kConvWarp + kConvThreads / 32;
+constexpr int kLoadWarp = kMmaWarp + 1;
+constexpr int kThreads = 32 * (kLoadWarp + 1);
+constexpr int kStages = 2;                     // converted tiles
+
+template <bool kKeySplit>
 struct Shape {
-    static constexpr int kSoftmaxThreads = kBlocks * kRowsBlock;
-    static constexpr int kConvWarp = kSoftmaxThreads / 32;
-    static constexpr int kMmaWarp = kConvWarp + kConvThreads / 32;
-    static constexpr int kLoadWarp = kMmaWarp + 1;
-    static constexpr int kThreads = 32 * (kLoadWarp + 1);
-    static constexpr int kCtas = kBlocks == 1 ? 2 : 1;                 // on an SM
-    static constexpr int kStages = kBlocks == 1 ? 2 : 4;               // converted tiles
-    static constexpr int kRaw = kBlocks == 1 ? 4 : 8;                  // loaded tiles
-    static constexpr uint32_t kOffK = 0;
+    static constexpr int kRows = kKeySplit ? kRowsBlock : 2 * kRowsBlock;    // of a CTA
+    static constexpr int kRaw = kKeySplit ? 6 : 3;                           // loaded granules
+    static constexpr uint32_t kOffQ = 0;
+    static constexpr uint32_t kOffK = kOffQ + kRows / kRowsBlock * kOpBytes;
     static constexpr uint32_t kOffV = kOffK + kStages * kOpBytes;
     static constexpr uint32_t kOffRaw = kOffV + kStages * kOpBytes;
     static constexpr uint32_t kOffBar = kOffRaw + kRaw * kRawBytes;
     enum : int {
         kRawFull = 0, kRawEmpty = kRawFull + kRaw, kKFull = kRawEmpty + kRaw, kVFull = kKFull + kStages,
-        kKEmpty = kVFull + kStages, kVEmpty = kKEmpty + kStages, kQFull = kVEmpty + kStages, kSFull = kQFull + kBlocks,
-        kPFull = kSFull + kBlocks, kDone = kPFull + kBlocks, kNumBars = kDone + 1
+        kTurn = kVFull + kStages, kQFull = kTurn + kStages, kSFull = kQFull + 1, kPFull = kSFull + 2, kDone = kPFull + 2,
+        kJoin = kDone + 1, kNumBars = kJoin + 1
     };
     static constexpr uint32_t kOffSlot = kOffBar + 8 * kNumBars;
-    static constexpr uint32_t kSmem = kOffSlot + 8 + 1024;             // + slack to align the base
-    static constexpr uint32_t kTmemCols = kBlocks * kTmBlock;
-    static_assert(kCtas * (kSmem + 1024) <= 228 * 1024, "shared memory");
-    // (tensor memory is 512 columns: the CTAs that fit an SM never wait for it)
-    static_assert(kCtas * kTmemCols <= 512 && (kCtas + 1) * kSmem > 228 * 1024, "CTAs an SM");
+    static constexpr uint32_t kSmem = kOffSlot + 8 + 1024;                   // + slack to align the base
+    // (one CTA an SM: all of tensor memory is its own)
+    static_assert(kSmem <= 227 * 1024 && 2 * kSmem > 228 * 1024, "shared memory");
 };
+// the second copy's O, maxima and sums of a key-split CTA take the K and V stages' place
+static_assert((kHeadDim + 2) * kRowsBlock * 4 <= 2 * kStages * kOpBytes, "join area");
 
 __device__ __forceinline__ void st_shared128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
 {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
+// Bounded wait for a phase.  Another role's failure is looked at only while the
+// phase is not there yet: a load of the flag in front of every wait cost a
+// quarter of the pipeline's turn-around.
 __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile int *fail, int32_t *dev_status,
                                          uint32_t limit)
 {
-    if (*fail)
-        return false;
-    if (mbar_wait_bounded(bar, parity, limit))
-        return true;
+    for (uint32_t i = 0; i < limit; ++i) {
+        if (mbar_try_wait(bar, parity))
+            return true;
+        if (*fail)
+            return false;
+    }
     *fail = 1;
     report(dev_status, NVFP4KV_DEV_TIMEOUT);
     return false;
+}
+
+// One arrival for the warp, after what all its lanes did before.
+__device__ __forceinline__ void warp_arrive(uint32_t bar, int lane)
+{
+    __syncwarp();
+    if (lane == 0)
+        mbar_arrive(bar);
 }
 
 // A sequence's chunk; false (nothing of it is written) when its index range,
@@ -119,9 +137,10 @@ __device__ __forceinline__ bool read_chunk(const PagedExtendParams &p, int b, Ch
            c.len <= p.max_pages * kPageSize;
 }
 
-// K of a staged tile to f16 [key][channel], thread pt of 128: two quarter rows
-// of 32 channels.  Lanes of the upper channel half of a quarter pair store
-// their chunks in another order, so eight lanes meet eight bank groups.
+// K of a staged granule to f16 [key][channel] at dst (its first key's row),
+// thread pt of 128: two quarter rows of 32 channels.  Lanes of the upper channel
+// half of a quarter pair store their chunks in another order, so eight lanes
+// meet eight bank groups.
 __device__ __forceinline__ void convert_k(uint32_t raw, uint32_t dst, int pt)
 {
 #pragma unroll
@@ -134,7 +153,7 @@ __device__ __forceinline__ void convert_k(uint32_t raw, uint32_t dst, int pt)
         const uint32_t w[4] = {swap ? d.z : d.x, swap ? d.w : d.y, swap ? d.x : d.z, swap ? d.y : d.w};
         const uint32_t lo = two & 0xffu, hi = two >> 8;
         const uint32_t sc[2] = {(swap ? hi : lo) * 0x00800080u, (swap ? lo : hi) * 0x00800080u};
-        const uint32_t row = dst + (quarter >> 1) * (kKeys * 128u) + key * 128u;
+        const uint32_t row = dst + (quarter >> 1) * kHalfBytes + key * 128u;
 #pragma unroll
         for (uint32_t i = 0; i < 4; ++i) {
             uint32_t r0, r1, r2, r3;
@@ -146,8 +165,9 @@ __device__ __forceinline__ void convert_k(uint32_t raw, uint32_t dst, int pt)
     }
 }
 
-// V of a staged tile to f16 [channel][key]: thread pt takes eight keys (half a
-// page, four token pairs), group g of the pairs' rows and half its blocks.
+// V of a staged granule to f16 [channel][key] (a 64-key half of the operand):
+// thread pt takes eight keys (half a page, four token pairs), group g of the
+// pairs' rows and half its blocks.
 __device__ __forceinline__ void convert_v(uint32_t raw, uint32_t dst, int pt)
 {
     const uint32_t g = pt & 7, jh = (pt >> 3) & 1, eight = pt >> 4;
@@ -180,11 +200,59 @@ __device__ __forceinline__ void convert_v(uint32_t raw, uint32_t dst, int pt)
     }
 }
 
-template <int kBlocks>
-__global__ void __launch_bounds__(Shape<kBlocks>::kThreads, Shape<kBlocks>::kCtas)
-    paged_extend_kernel(const __grid_constant__ PagedExtendParams p)
+// 64 scores of a row (tensor-memory columns at taddr), masked to the keys
+// lo_j .. hi_j - 1 of their 64.
+__device__ __forceinline__ void load_scores(uint32_t taddr, int lo_j, int hi_j, float (&s)[64])
 {
-    using S = Shape<kBlocks>;
+    uint32_t s0[32], s1[32];
+    tmem_ld32(taddr, s0);
+    tmem_ld32(taddr + 32, s1);
+    tmem_wait_ld();
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+        s[j] = __uint_as_float(s0[j]);
+        s[j + 32] = __uint_as_float(s1[j]);
+    }
+    if (hi_j < 64 || lo_j > 0) {
+#pragma unroll
+        for (int j = 0; j < 64; ++j)
+            if (j >= hi_j || j < lo_j)
+                s[j] = -INFINITY;
+    }
+}
+
+__device__ __forceinline__ float max_of(const float (&s)[64])
+{
+    float pm[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+        pm[k] = fmax3(fmax3(s[8 * k], s[8 * k + 1], s[8 * k + 2]), fmax3(s[8 * k + 3], s[8 * k + 4], s[8 * k + 5]),
+                      fmaxf(s[8 * k + 6], s[8 * k + 7]));
+    return fmax3(fmax3(pm[0], pm[1], pm[2]), fmax3(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7]));
+}
+
+// 2^(s inv - m) of 64 scores, as f16 pairs into 32 tensor-memory columns; their
+// sum (of the unrounded values) is returned.
+__device__ __forceinline__ float store_weights(uint32_t taddr, float (&s)[64], uint64_t inv2, uint64_t neg2)
+{
+    uint64_t acc[4] = {0, 0, 0, 0};
+    uint32_t pw[32];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+        const uint64_t d = fma_f32x2(f32x2_pack(s[2 * j], s[2 * j + 1]), inv2, neg2);
+        const float a = fast_exp2(f32x2_lo(d)), b = fast_exp2(f32x2_hi(d));
+        acc[j & 3] = add_f32x2(acc[j & 3], f32x2_pack(a, b));
+        pw[j] = pack_f16x2(a, b);
+    }
+    tmem_st32(taddr, pw);
+    const uint64_t a = add_f32x2(add_f32x2(acc[0], acc[1]), add_f32x2(acc[2], acc[3]));
+    return f32x2_lo(a) + f32x2_hi(a);
+}
+
+template <bool kKeySplit>
+__global__ void __launch_bounds__(kThreads, 1) paged_extend_kernel(const __grid_constant__ PagedExtendParams p)
+{
+    using S = Shape<kKeySplit>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw_addr = smem_addr(smem_raw);
     const uint32_t base = (raw_addr + 1023u) & ~1023u;
@@ -206,11 +274,11 @@ __global__ void __launch_bounds__(Shape<kBlocks>::kThreads, Shape<kBlocks>::kCta
     }
     const int g = p.group;
     const int R = c.count * g;
-    const int row0 = tile * (kBlocks * kRowsBlock);
+    const int row0 = tile * S::kRows;
     if (row0 >= R)
         return;
     const int first_pos = c.len - c.count;       // position of chunk token 0; negative when the chunk is longer
-    const int t_last = (min(row0 + kBlocks * kRowsBlock, R) - 1) / g;
+    const int t_last = (min(row0 + S::kRows, R) - 1) / g;
     const int key_end = max(0, first_pos + t_last + 1);
     const int key_begin = p.window > 0 ? max(0, first_pos + row0 / g - p.window + 1) : 0;
     int tile_lo = key_begin / kKeys, n_tiles = 0;
@@ -221,9 +289,10 @@ __global__ void __launch_bounds__(Shape<kBlocks>::kThreads, Shape<kBlocks>::kCta
         tile_lo += from;
     }
 
-    // this thread's row, when it is a softmax thread
-    const int row = row0 + tid;
-    const bool has_row = tid < S::kSoftmaxThreads && row < R;
+    // this thread's row and block, when it is a softmax thread
+    const int blk = warp >> 2;
+    const int row = row0 + (kKeySplit ? tid % kRowsBlock : tid);
+    const bool has_row = tid < kSoftmaxThreads && row < R;
     const int t = min(row, R - 1) / g;
     const int64_t out_row = static_cast<int64_t>(c.c0 + t) * p.hq + h * g + (min(row, R - 1) - t * g);
     // where the partials go: [split][q_rows][hq][128], then [split][q_rows][hq][2]
@@ -247,41 +316,43 @@ __global__ void __launch_bounds__(Shape<kBlocks>::kThreads, Shape<kBlocks>::kCta
     if (tid == 0) {
         for (int k = 0; k < S::kRaw; ++k) {
             mbar_init(B(S::kRawFull + k), 1);
-            mbar_init(B(S::kRawEmpty + k), kConvThreads);
+            mbar_init(B(S::kRawEmpty + k), kConvThreads / 32);
         }
-        for (int k = 0; k < S::kStages; ++k) {
-            mbar_init(B(S::kKFull + k), kConvThreads);
-            mbar_init(B(S::kVFull + k), kConvThreads);
-            mbar_init(B(S::kKEmpty + k), 1);
-            mbar_init(B(S::kVEmpty + k), 1);
+        for (int k = 0; k < kStages; ++k) {
+            mbar_init(B(S::kKFull + k), kConvThreads / 32);
+            mbar_init(B(S::kVFull + k), kConvThreads / 32);
+            mbar_init(B(S::kTurn + k), 1);
         }
-        for (int k = 0; k < kBlocks; ++k) {
-            mbar_init(B(S::kQFull + k), kRowsBlock);
+        mbar_init(B(S::kQFull), S::kRows / 32);
+        for (int k = 0; k < 2; ++k) {
             mbar_init(B(S::kSFull + k), 1);
-            mbar_init(B(S::kPFull + k), kRowsBlock);
+            mbar_init(B(S::kPFull + k), kRowsBlock / 32);
         }
         mbar_init(B(S::kDone), 1);
+        mbar_init(B(S::kJoin), kRowsBlock / 32);
         *fail = 0;
         fence_mbar_init();
     }
-    if (warp == S::kMmaWarp)
-        tmem_alloc(base + S::kOffSlot, S::kTmemCols);
+    if (warp == kMmaWarp)
+        tmem_alloc(base + S::kOffSlot, 2 * kTmBlock);
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(gbase + S::kOffSlot);
 
-    if (warp == S::kLoadWarp) {
-        // lane l looks up page l % 4 of tile 8 w + l / 4, a window w ahead
+    if (warp == kLoadWarp) {
+        // granules in order; lane l looks up page l % 4 of granule 8 w + l / 4, a
+        // window w ahead
         const int page_lo = key_begin / kPageSize, page_hi = (key_end + kPageSize - 1) / kPageSize;
+        const int n_grans = n_tiles * kGrans, first_page = tile_lo * (kKeys / kPageSize);
         const int32_t *table = p.block_table + static_cast<size_t>(b) * p.max_pages;
         auto lookup = [&](int i) {
-            const int pg = (tile_lo + i) * kTilePages + (lane & 3);
-            return i < n_tiles && pg >= page_lo && pg < page_hi ? __ldg(table + pg) : 0;
+            const int pg = first_page + i * kGranPages + (lane & 3);
+            return i < n_grans && pg >= page_lo && pg < page_hi ? __ldg(table + pg) : 0;
         };
         int cur = 0, nxt = lookup(lane >> 2);
         int issued = 0;
-        for (int i = 0; i < n_tiles; ++i) {
+        for (int i = 0; i < n_grans; ++i) {
             if ((i & 7) == 0) {
                 cur = nxt;
                 nxt = lookup(i + 8 + (lane >> 2));
@@ -291,14 +362,14 @@ __global__ void __launch_bounds__(Shape<kBlocks>::kThreads, Shape<kBlocks>::kCta
                 }
             }
             const int st = i % S::kRaw;
-            // the stage was last read by the converters for tile i - kRaw
+            // the stage was last read by the converters for granule i - kRaw
             bool ok = true;
             if (i >= S::kRaw)
                 ok = wait_bar(B(S::kRawEmpty + st), (i / S::kRaw - 1) & 1, fail, p.dev_status, p.wait_limit);
             if (!__all_sync(kFullMask, ok))
                 break;
-            const int pg0 = (tile_lo + i) * kTilePages;
-            const int n = min(pg0 + kTilePages, page_hi) - max(pg0, page_lo);
+            const int pg0 = first_page + i * kGranPages;
+            const int n = max(0, min(pg0 + kGranPages, page_hi) - max(pg0, page_lo));   // 0: no row sees the granule
             if (lane == 0)
                 mbar_arrive_expect_tx(B(S::kRawFull + st), n * kNvfp4Record);
             __syncwarp();
@@ -314,100 +385,134 @@ __global__ void __launch_bounds__(Shape<kBlocks>::kThreads, Shape<kBlocks>::kCta
             if (!mbar_wait_bounded(B(S::kRawFull + i % S::kRaw), (i / S::kRaw) & 1, kWaitLimit))
                 report(p.dev_status, NVFP4KV_DEV_TIMEOUT);
         __syncwarp();
-    } else if (warp == S::kMmaWarp) {
+    } else if (warp == kMmaWarp) {
         if (lane == 0) {
-            constexpr uint32_t i_qk = idesc_f16(kRowsBlock, kKeys, false);
-            constexpr uint32_t i_pv = idesc_f16(kRowsBlock, kHeadDim, false);
+            constexpr uint32_t idesc = idesc_f16(kRowsBlock, 128, false);     // both products: N = 128, K-major
             auto wait = [&](int k, uint32_t parity) {
                 return wait_bar(B(k), parity, fail, p.dev_status, p.wait_limit);
             };
-            auto qk = [&](int blk, int i) {
-                const uint32_t tb = tmem + blk * kTmBlock, kb = base + S::kOffK + (i % S::kStages) * kOpBytes;
+            // S of block `k` for tile x, then the commits: S itself and, after
+            // the last block that reads the tile, turn x: K of tile x is free,
+            // and V of the tile before it in the block's order.  (One commit
+            // for both: each takes the issuing thread as long as an MMA.)
+            auto qk = [&](int k, int x) {
+                const uint32_t qb = base + S::kOffQ + (kKeySplit ? 0 : k) * kOpBytes, kb = base + S::kOffK + (x & 1) * kOpBytes;
+                tc_fence_after_sync();
+#pragma unroll
+                for (int s = 0; s < 8; ++s) {
+                    const uint32_t off = (s >> 2) * kHalfBytes + (s & 3) * 32;
+                    umma_f16(tmem + k * kTmBlock + kTmS, smem_desc(qb + off, 16, 1024), smem_desc(kb + off, 16, 1024), idesc,
+                             s > 0);
+                }
+                umma_commit(B(S::kSFull + k));
+                if (kKeySplit || k == 1)
+                    umma_commit(B(S::kTurn + (x & 1)));
+            };
+            auto pv = [&](int k, int x, bool accumulate) {
+                const uint32_t tb = tmem + k * kTmBlock, vb = base + S::kOffV + (x & 1) * kOpBytes;
                 tc_fence_after_sync();
 #pragma unroll
                 for (int s = 0; s < 8; ++s)
-                    umma_f16_ts(tb + kTmS, tb + kTmQ + 8 * s,
-                                smem_desc(kb + (s >> 2) * (kKeys * 128) + (s & 3) * 32, 16, 1024), i_qk, s > 0);
-                umma_commit(B(S::kSFull + blk));
-                if (blk == kBlocks - 1)
-                    umma_commit(B(S::kKEmpty + i % S::kStages));
+                    umma_f16_ts(tb + kTmO, tb + kTmS + 8 * s, smem_desc(vb + (s >> 2) * kHalfBytes + (s & 3) * 32, 16, 1024),
+                                idesc, accumulate || s > 0);
             };
-            auto pv = [&](int blk, int i) {
-                const uint32_t tb = tmem + blk * kTmBlock, vb = base + S::kOffV + (i % S::kStages) * kOpBytes;
-                tc_fence_after_sync();
-#pragma unroll
-                for (int s = 0; s < 4; ++s)
-                    umma_f16_ts(tb + kTmO, tb + kTmS + 8 * s, smem_desc(vb + 32 * s, 16, 1024), i_pv, i > 0 || s > 0);
-                if (blk == kBlocks - 1)
-                    umma_commit(B(S::kVEmpty + i % S::kStages));
-            };
-            // P V of tile i and Q K^T of tile i + 2 - 1 follow one another for
-            // each block in turn; S of a block is overwritten only after the
-            // product that reads its P, in issue order
-            bool ok = true;
-            for (int blk = 0; ok && blk < kBlocks; ++blk) {
-                ok = wait(S::kQFull + blk, 0) && (blk > 0 || wait(S::kKFull, 0));
+            // For each block in turn: P V of its tile, then Q K^T of its next
+            // one, whose S overwrites that P in issue order.
+            bool ok = wait(S::kQFull, 0);
+            for (int k = 0; ok && k < 2; ++k) {
+                const int x = kKeySplit ? k : 0;
+                if (x >= n_tiles)
+                    break;
+                ok = (!kKeySplit && k > 0) || wait(S::kKFull + (x & 1), 0);
                 if (ok)
-                    qk(blk, 0);
+                    qk(k, x);
             }
-            for (int i = 0; ok && i < n_tiles; ++i)
-                for (int blk = 0; ok && blk < kBlocks; ++blk) {
-                    ok = wait(S::kPFull + blk, i & 1) && (blk > 0 || wait(S::kVFull + i % S::kStages, (i / S::kStages) & 1));
-                    if (!ok)
-                        break;
-                    pv(blk, i);
-                    if (i + 1 < n_tiles) {
-                        ok = blk > 0 || wait(S::kKFull + (i + 1) % S::kStages, ((i + 1) / S::kStages) & 1);
-                        if (ok)
-                            qk(blk, i + 1);
-                    }
+            const int items = kKeySplit ? n_tiles : 2 * n_tiles;
+            for (int it = 0; ok && it < items; ++it) {
+                const int k = it & 1, i = it >> 1;               // block, and its count of tiles
+                const int x = kKeySplit ? it : i, next = x + (kKeySplit ? 2 : 1);
+                const bool first_use = kKeySplit || k == 0;      // the other block has not waited for the tile
+                ok = wait(S::kPFull + k, i & 1) && (!first_use || wait(S::kVFull + (x & 1), (x >> 1) & 1));
+                if (!ok)
+                    break;
+                pv(k, x, i > 0);
+                if (next < n_tiles) {
+                    ok = !first_use || wait(S::kKFull + (next & 1), (next >> 1) & 1);
+                    if (ok)
+                        qk(k, next);
                 }
+            }
             // nothing of this thread's may still run when tensor memory is freed
             umma_commit(B(S::kDone));
             if (!mbar_wait_bounded(B(S::kDone), 0, kWaitLimit))
                 report(p.dev_status, NVFP4KV_DEV_TIMEOUT);
         }
         __syncwarp();
-    } else if (warp >= S::kConvWarp) {
-        const int pt = tid - S::kSoftmaxThreads;
-        for (int i = 0; i < n_tiles; ++i) {
-            const int st = i % S::kStages, rs = i % S::kRaw;
-            const uint32_t raw = base + S::kOffRaw + rs * kRawBytes;
-            if (!wait_bar(B(S::kRawFull + rs), (i / S::kRaw) & 1, fail, p.dev_status, p.wait_limit))
-                break;
-            // the operand stages were last read by the products of tile i - kStages
-            if (i >= S::kStages &&
-                !wait_bar(B(S::kKEmpty + st), (i / S::kStages - 1) & 1, fail, p.dev_status, p.wait_limit))
-                break;
-            convert_k(raw, base + S::kOffK + st * kOpBytes, pt);
-            fence_async_shared();
-            mbar_arrive(B(S::kKFull + st));
-            if (i >= S::kStages &&
-                !wait_bar(B(S::kVEmpty + st), (i / S::kStages - 1) & 1, fail, p.dev_status, p.wait_limit))
-                break;
-            convert_v(raw, base + S::kOffV + st * kOpBytes, pt);
-            fence_async_shared();                // also orders the reads of the stage before its next copy
-            mbar_arrive(B(S::kVFull + st));
-            mbar_arrive(B(S::kRawEmpty + rs));
+    } else if (warp >= kConvWarp) {
+        const int pt = tid - kSoftmaxThreads;
+        auto wait_warp = [&](int k, uint32_t parity) {
+            return __all_sync(kFullMask, wait_bar(B(k), parity, fail, p.dev_status, p.wait_limit));
+        };
+        // (the turn of tile x needs tile x's K, so a turn asked for here is at
+        // most kStages behind the last one done: its barrier has not come
+        // round again)
+        auto wait_turn = [&](int x) { return wait_warp(S::kTurn + (x & 1), (x >> 1) & 1); };
+        auto stage = [&](int gr) { return base + S::kOffRaw + gr % S::kRaw * kRawBytes; };
+        // K of tile x: its stage was last read in the turn of tile x - 2
+        auto make_k = [&](int x) {
+            bool ok = x < kStages || wait_turn(x - kStages);
+            for (int u = 0; ok && u < kGrans; ++u) {
+                const int gr = x * kGrans + u;
+                ok = wait_warp(S::kRawFull + gr % S::kRaw, (gr / S::kRaw) & 1);
+                if (ok)
+                    convert_k(stage(gr), base + S::kOffK + (x & 1) * kOpBytes + u * kGranKeys * 128, pt);
+            }
+            if (ok) {
+                fence_async_shared();
+                warp_arrive(B(S::kKFull + (x & 1)), lane);
+            }
+            return ok;
+        };
+        // V of tile x: its stage was last read by P V of tile x - 2, which the
+        // next turn follows (that of tile x where blocks alternate); then the
+        // granules are free
+        auto make_v = [&](int x) {
+            if (x >= kStages && !wait_turn(x - kStages + (kKeySplit ? 2 : 1)))
+                return false;
+#pragma unroll
+            for (int u = 0; u < kGrans; ++u) {
+                const int gr = x * kGrans + u;
+                convert_v(stage(gr), base + S::kOffV + (x & 1) * kOpBytes + u * kHalfBytes, pt);
+                fence_async_shared();            // also orders the reads of the granule before its next copy
+                warp_arrive(B(S::kRawEmpty + gr % S::kRaw), lane);
+            }
+            if (lane == 0)
+                mbar_arrive(B(S::kVFull + (x & 1)));
+            return true;
+        };
+        if (kKeySplit) {
+            // K of the next tile can be made a turn before V of this one
+            bool ok = make_k(0);
+            for (int x = 0; ok && x < n_tiles; ++x)
+                ok = (x + 1 >= n_tiles || make_k(x + 1)) && make_v(x);
+        } else {
+            for (int x = 0; x < n_tiles && make_k(x) && make_v(x); ++x) {
+            }
         }
     } else {
-        const int blk = warp >> 2;
+        const int r = tid % kRowsBlock;
         const uint32_t tb = tmem + blk * kTmBlock + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         // the row of Q, scaled by a power of two; inv takes scores to log2 units
         float inv;
         {
-            uint32_t w[64];
+            uint4 w[16];
             const uint4 *src = reinterpret_cast<const uint4 *>(p.q + out_row * kHeadDim);
             uint32_t m2 = 0;
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
-                const uint4 v = has_row ? __ldg(src + k) : make_uint4(0, 0, 0, 0);
-                w[4 * k] = v.x;
-                w[4 * k + 1] = v.y;
-                w[4 * k + 2] = v.z;
-                w[4 * k + 3] = v.w;
-                m2 = __vmaxu2(m2, __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
-                                           __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu)));
+                w[k] = has_row ? __ldg(src + k) : make_uint4(0, 0, 0, 0);
+                m2 = __vmaxu2(m2, __vmaxu2(__vmaxu2(w[k].x & 0x7fff7fffu, w[k].y & 0x7fff7fffu),
+                                           __vmaxu2(w[k].z & 0x7fff7fffu, w[k].w & 0x7fff7fffu)));
             }
             const int expo = static_cast<int>(max(m2 & 0xffffu, m2 >> 16) >> 7);          // of the largest |q|
             const int e = min(14 - (expo - 127), 112);
@@ -419,21 +524,18 @@ __global__ void __launch_bounds__(Shape<kBlocks>::kThreads, Shape<kBlocks>::kCta
                 inv = 1.f;
                 sc = 0.f;
             }
+            if (!kKeySplit || blk == 0) {
+                const uint32_t dst = base + S::kOffQ + (kKeySplit ? 0 : blk) * kOpBytes + r * 128u;
+                auto two = [&](uint32_t v) {
+                    return pack_f16x2(__uint_as_float(v << 16) * sc, __uint_as_float(v & 0xffff0000u) * sc);
+                };
 #pragma unroll
-            for (int k = 0; k < 64; ++k)
-                w[k] = pack_f16x2(__uint_as_float(w[k] << 16) * sc, __uint_as_float(w[k] & 0xffff0000u) * sc);
-            uint32_t half[32];
-#pragma unroll
-            for (int k = 0; k < 32; ++k)
-                half[k] = w[k];
-            tmem_st32(tb + kTmQ, half);
-#pragma unroll
-            for (int k = 0; k < 32; ++k)
-                half[k] = w[32 + k];
-            tmem_st32(tb + kTmQ + 32, half);
-            tmem_wait_st();
-            tc_fence_before_sync();
-            mbar_arrive(B(S::kQFull + blk));
+                for (uint32_t k = 0; k < 16; ++k)
+                    st_shared128(dst + (k >> 3) * kHalfBytes + (((k & 7u) ^ (r & 7u)) << 4), two(w[k].x), two(w[k].y),
+                                 two(w[k].z), two(w[k].w));
+                fence_async_shared();
+                warp_arrive(B(S::kQFull), lane);
+            }
         }
         const int pos = first_pos + t;           // keys lo .. pos are visible
         const int lo = p.window > 0 ? pos - p.window + 1 : 0;
@@ -444,59 +546,31 @@ __global__ void __launch_bounds__(Shape<kBlocks>::kThreads, Shape<kBlocks>::kCta
         auto wait_warp = [&](int k, uint32_t parity) {
             return __all_sync(kFullMask, wait_bar(B(k), parity, fail, p.dev_status, p.wait_limit));
         };
-        for (int i = 0; i < n_tiles; ++i) {
+        const int my_tiles = kKeySplit ? (n_tiles + 1 - blk) / 2 : n_tiles;
+        for (int i = 0; i < my_tiles; ++i) {
             if (!(ok = wait_warp(S::kSFull + blk, i & 1)))
                 break;
             tc_fence_after_sync();
-            float s[64];
-            {
-                uint32_t s0[32], s1[32];
-                tmem_ld32(tb + kTmS, s0);
-                tmem_ld32(tb + kTmS + 32, s1);
-                tmem_wait_ld();
-#pragma unroll
-                for (int j = 0; j < 32; ++j) {
-                    s[j] = __uint_as_float(s0[j]);
-                    s[j + 32] = __uint_as_float(s1[j]);
-                }
-            }
-            const int k0 = (tile_lo + i) * kKeys;
+            const int k0 = (tile_lo + (kKeySplit ? 2 * i + blk : i)) * kKeys;
             const int hi_j = pos + 1 - k0, lo_j = lo - k0;
-            if (hi_j < kKeys || lo_j > 0) {
-#pragma unroll
-                for (int j = 0; j < 64; ++j)
-                    if (j >= hi_j || j < lo_j)
-                        s[j] = -INFINITY;
-            }
-            float pm[8];
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                pm[k] = fmax3(fmax3(s[8 * k], s[8 * k + 1], s[8 * k + 2]), fmax3(s[8 * k + 3], s[8 * k + 4], s[8 * k + 5]),
-                              fmaxf(s[8 * k + 6], s[8 * k + 7]));
-            const float mx = fmax3(fmax3(pm[0], pm[1], pm[2]), fmax3(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7])) * inv;
+            // the maximum over all 128 scores; the first 64 stay in registers
+            float s[64];
+            load_scores(tb + kTmS + 64, lo_j - 64, hi_j - 64, s);
+            float mx = max_of(s);
+            load_scores(tb + kTmS, lo_j, hi_j, s);
+            mx = fmaxf(mx, max_of(s)) * inv;
             const bool need = mx > m_used + kRaise;
             const float m_new = need ? mx : m_used;
             const float mbase = m_new == -INFINITY ? 0.f : m_new;
             const float alpha = need ? fast_exp2(m_used - mbase) : 1.f;
             const uint64_t neg2 = f32x2_pack(-mbase, -mbase);
-            uint64_t acc[4] = {0, 0, 0, 0};
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
-                const uint64_t d = fma_f32x2(f32x2_pack(s[2 * j], s[2 * j + 1]), inv2, neg2);
-                s[2 * j] = fast_exp2(f32x2_lo(d));
-                s[2 * j + 1] = fast_exp2(f32x2_hi(d));
-                acc[j & 3] = add_f32x2(acc[j & 3], f32x2_pack(s[2 * j], s[2 * j + 1]));
-            }
-            const uint64_t a = add_f32x2(add_f32x2(acc[0], acc[1]), add_f32x2(acc[2], acc[3]));
-            l = l * alpha + (f32x2_lo(a) + f32x2_hi(a));
+            // weights of keys 0 .. 63 over the columns of scores 0 .. 31, of
+            // keys 64 .. 127 over those of scores 32 .. 63
+            float sum = store_weights(tb + kTmS, s, inv2, neg2);
+            load_scores(tb + kTmS + 64, lo_j - 64, hi_j - 64, s);
+            sum += store_weights(tb + kTmS + 32, s, inv2, neg2);
+            l = l * alpha + sum;
             m_used = m_new;
-            {
-                uint32_t pw[32];
-#pragma unroll
-                for (int j = 0; j < 32; ++j)
-                    pw[j] = pack_f16x2(s[2 * j], s[2 * j + 1]);
-                tmem_st32(tb + kTmS, pw);
-            }
             // a raised maximum: rescale the O rows of the warp (S of this tile
             // was committed after P V of the one before, which has landed)
             if (i >= 1 && __any_sync(kFullMask, need)) {
@@ -513,14 +587,44 @@ __global__ void __launch_bounds__(Shape<kBlocks>::kThreads, Shape<kBlocks>::kCta
             }
             tmem_wait_st();
             tc_fence_before_sync();
-            mbar_arrive(B(S::kPFull + blk));
+            warp_arrive(B(S::kPFull + blk), lane);
         }
         if (ok)
             ok = wait_warp(S::kDone, 0);
-        if (ok) {
-            tc_fence_after_sync();
+        tc_fence_after_sync();
+        float w0 = 1.f, w1 = 0.f;                // weights of this copy and of the other one
+        volatile float *other = reinterpret_cast<volatile float *>(gbase + S::kOffK);    // [130][128 rows]
+        if (kKeySplit) {
+            // (every MMA is done: the K and V stages are free)
+            if (ok && blk == 1) {
+                if (my_tiles > 0) {
+#pragma unroll
+                    for (int cb = 0; cb < 4; ++cb) {
+                        uint32_t o[32];
+                        tmem_ld32(tb + kTmO + 32 * cb, o);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            other[(32 * cb + j) * kRowsBlock + r] = __uint_as_float(o[j]);
+                    }
+                }
+                other[kHeadDim * kRowsBlock + r] = m_used;
+                other[(kHeadDim + 1) * kRowsBlock + r] = l;
+                warp_arrive(B(S::kJoin), lane);
+            }
+            if (ok && blk == 0 && (ok = wait_warp(S::kJoin, 0))) {
+                const float m1 = other[kHeadDim * kRowsBlock + r], l1 = other[(kHeadDim + 1) * kRowsBlock + r];
+                const float M = fmaxf(m_used, m1);
+                w0 = m_used == -INFINITY ? 0.f : fast_exp2(m_used - M);
+                w1 = m1 == -INFINITY ? 0.f : fast_exp2(m1 - M);
+                l = (l != l || l1 != l1) ? NAN : l * w0 + l1 * w1;
+                m_used = M;
+            }
+        }
+        if (ok && (!kKeySplit || blk == 0)) {
             const float vs = (p.hs.per_head ? p.hs.v[h] : p.gscale) * 256.f;
             const float f = p.splits > 1 ? vs : (l > 0.f ? vs / l : (l == 0.f ? 0.f : l));   // a NaN sum stays NaN
+            const float f0 = w0 * f, f1 = w1 * f;
             float *part_o = p.partials + (all_rows * split + out_row) * kHeadDim;
             if (has_row && p.splits > 1) {
                 part_ml[0] = m_used;
@@ -528,23 +632,30 @@ __global__ void __launch_bounds__(Shape<kBlocks>::kThreads, Shape<kBlocks>::kCta
             }
 #pragma unroll
             for (int cb = 0; cb < 4; ++cb) {
-                uint32_t o[32];
-                tmem_ld32(tb + kTmO + 32 * cb, o);
+                uint32_t w[32];
+                tmem_ld32(tb + kTmO + 32 * cb, w);
                 tmem_wait_ld();
                 if (!has_row)
                     continue;
+                float o[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j)
+                    o[j] = __uint_as_float(w[j]) * f0;
+                if (kKeySplit && f1 != 0.f) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        o[j] = fmaf(other[(32 * cb + j) * kRowsBlock + r], f1, o[j]);
+                }
                 if (p.splits > 1 || p.out_f32) {
                     float *row_f = p.splits > 1 ? part_o : static_cast<float *>(p.out) + out_row * kHeadDim;
                     float4 *dst = reinterpret_cast<float4 *>(row_f + 32 * cb);
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        dst[k] = make_float4(__uint_as_float(o[4 * k]) * f, __uint_as_float(o[4 * k + 1]) * f,
-                                             __uint_as_float(o[4 * k + 2]) * f, __uint_as_float(o[4 * k + 3]) * f);
+                        dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
                 } else {
                     uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + out_row * kHeadDim + 32 * cb);
                     auto bf2 = [&](int j) {
-                        const __nv_bfloat162 two =
-                            __floats2bfloat162_rn(__uint_as_float(o[j]) * f, __uint_as_float(o[j + 1]) * f);
+                        const __nv_bfloat162 two = __floats2bfloat162_rn(o[j], o[j + 1]);
                         return *reinterpret_cast<const uint32_t *>(&two);
                     };
 #pragma unroll
@@ -557,9 +668,9 @@ __global__ void __launch_bounds__(Shape<kBlocks>::kThreads, Shape<kBlocks>::kCta
 
     tc_fence_before_sync();
     __syncthreads();
-    if (warp == S::kMmaWarp) {
+    if (warp == kMmaWarp) {
         tc_fence_after_sync();
-        tmem_dealloc(tmem, S::kTmemCols);
+        tmem_dealloc(tmem, 2 * kTmBlock);
     }
 }
 
@@ -635,16 +746,15 @@ ExtendShape paged_extend_shape(int64_t q_rows, int64_t max_q_len, int64_t batch,
     ExtendShape s;
     if (max_q_len > q_rows)
         max_q_len = q_rows;                      // no chunk is longer
-    s.blocks = max_q_len * group > kRowsBlock ? 2 : 1;
-    const int64_t rows = kRowsBlock * s.blocks;
+    s.key_split = max_q_len * group <= kRowsBlock;
+    const int64_t rows = s.key_split ? kRowsBlock : 2 * kRowsBlock;
     s.row_tiles = (max_q_len * group + rows - 1) / rows;
     const int64_t ctas = batch * s.row_tiles, filled = q_rows * group / rows + batch;
     const int64_t units = hkv * (ctas < filled ? ctas : filled);
-    const int64_t slots = static_cast<int64_t>(sm_count()) * (s.blocks == 1 ? 2 : 1);
     int64_t keys = max_pages * kPageSize;
     if (window > 0 && window + max_q_len < keys)
         keys = window + max_q_len;
-    int64_t n = units > 0 ? slots / units : 1;
+    int64_t n = units > 0 ? sm_count() / units : 1;
     if (n > keys / kMinSplitKeys)
         n = keys / kMinSplitKeys;
     s.splits = static_cast<int>(n < 1 ? 1 : (n > kMaxSplits ? kMaxSplits : n));
@@ -652,16 +762,16 @@ ExtendShape paged_extend_shape(int64_t q_rows, int64_t max_q_len, int64_t batch,
     return s;
 }
 
-template <int kBlocks>
+template <bool kKeySplit>
 static cudaError_t launch_blocks(const PagedExtendParams &p, const ExtendShape &shape, cudaStream_t s)
 {
-    using S = Shape<kBlocks>;
-    const cudaError_t e = cudaFuncSetAttribute(paged_extend_kernel<kBlocks>,
+    using S = Shape<kKeySplit>;
+    const cudaError_t e = cudaFuncSetAttribute(paged_extend_kernel<kKeySplit>,
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     if (e != cudaSuccess)
         return e;
     const dim3 grid(static_cast<unsigned>(shape.row_tiles * shape.splits), p.hkv, p.batch);
-    paged_extend_kernel<kBlocks><<<grid, S::kThreads, S::kSmem, s>>>(p);
+    paged_extend_kernel<kKeySplit><<<grid, kThreads, S::kSmem, s>>>(p);
     return cudaGetLastError();
 }
 
@@ -669,7 +779,7 @@ cudaError_t launch_paged_extend(const PagedExtendParams &in, const ExtendShape &
 {
     PagedExtendParams p = in;
     p.splits = shape.splits;
-    const cudaError_t e = shape.blocks == 1 ? launch_blocks<1>(p, shape, s) : launch_blocks<2>(p, shape, s);
+    const cudaError_t e = shape.key_split ? launch_blocks<true>(p, shape, s) : launch_blocks<false>(p, shape, s);
     if (e != cudaSuccess || shape.splits == 1)
         return e;
     const int64_t rows = static_cast<int64_t>(p.max_q_len < p.q_rows ? p.max_q_len : p.q_rows) * p.hq;
