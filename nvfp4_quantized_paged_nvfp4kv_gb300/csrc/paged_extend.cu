@@ -65,7 +65,7 @@ constexpr uint32_t kTmO = 0, kTmS = 128, kTmBlock = 256;
 constexpr int kSoftmaxThreads = 2 * kRowsBlock;
 constexpr int kConvWarp = kSoftmaxThreads / 32;
 constexpr int kMmaWarp = kConvWarp + kConvThreads / 32;
-constexpr int kLoadWarp = kMmaWarp + 1;
+constexpr int kLoadWarp = kMmaWarp + 2;        // one MMA warp a block
 constexpr int kThreads = 32 * (kLoadWarp + 1);
 constexpr int kStages = 2;                     // converted tiles
 
@@ -80,8 +80,8 @@ struct Shape {
     static constexpr uint32_t kOffBar = kOffRaw + kRaw * kRawBytes;
     enum : int {
         kRawFull = 0, kRawEmpty = kRawFull + kRaw, kKFull = kRawEmpty + kRaw, kVFull = kKFull + kStages,
-        kTurn = kVFull + kStages, kQFull = kTurn + kStages, kSFull = kQFull + 1, kPFull = kSFull + 2, kDone = kPFull + 2,
-        kJoin = kDone + 1, kNumBars = kJoin + 1
+        kTurn = kVFull + kStages, kQFull = kTurn + kStages, kSFull = kQFull + 1, kPFull = kSFull + 2, kDone = kPFull + 4,
+        kGo = kDone + 2, kJoin = kGo + 2, kNumBars = kJoin + 1
     };
     static constexpr uint32_t kOffSlot = kOffBar + 8 * kNumBars;
     static constexpr uint32_t kSmem = kOffSlot + 8 + 1024;                   // + slack to align the base
@@ -321,14 +321,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_extend_kernel(const __grid_
         for (int k = 0; k < kStages; ++k) {
             mbar_init(B(S::kKFull + k), kConvThreads / 32);
             mbar_init(B(S::kVFull + k), kConvThreads / 32);
-            mbar_init(B(S::kTurn + k), 1);
+            mbar_init(B(S::kTurn + k), kKeySplit ? 1 : 2);
         }
         mbar_init(B(S::kQFull), S::kRows / 32);
         for (int k = 0; k < 2; ++k) {
             mbar_init(B(S::kSFull + k), 1);
             mbar_init(B(S::kPFull + k), kRowsBlock / 32);
+            mbar_init(B(S::kPFull + 2 + k), kRowsBlock / 32);
+            mbar_init(B(S::kDone + k), 1);
+            mbar_init(B(S::kGo + k), 1);
         }
-        mbar_init(B(S::kDone), 1);
         mbar_init(B(S::kJoin), kRowsBlock / 32);
         *fail = 0;
         fence_mbar_init();
@@ -385,66 +387,74 @@ __global__ void __launch_bounds__(kThreads, 1) paged_extend_kernel(const __grid_
             if (!mbar_wait_bounded(B(S::kRawFull + i % S::kRaw), (i / S::kRaw) & 1, kWaitLimit))
                 report(p.dev_status, NVFP4KV_DEV_TIMEOUT);
         __syncwarp();
-    } else if (warp == kMmaWarp) {
+    } else if (warp >= kMmaWarp) {
         if (lane == 0) {
             constexpr uint32_t idesc = idesc_f16(kRowsBlock, 128, false);     // both products: N = 128, K-major
-            auto wait = [&](int k, uint32_t parity) {
-                return wait_bar(B(k), parity, fail, p.dev_status, p.wait_limit);
+            const int k = warp - kMmaWarp;                       // the block
+            const uint32_t tb = tmem + k * kTmBlock, qb = base + S::kOffQ + (kKeySplit ? 0 : k) * kOpBytes;
+            auto wait = [&](int bar, uint32_t parity) {
+                return wait_bar(B(bar), parity, fail, p.dev_status, p.wait_limit);
             };
-            // S of block `k` for tile x, then the commits: S itself and, after
-            // the last block that reads the tile, turn x: K of tile x is free,
-            // and V of the tile before it in the block's order.  (One commit
-            // for both: each takes the issuing thread as long as an MMA.)
-            auto qk = [&](int k, int x) {
-                const uint32_t qb = base + S::kOffQ + (kKeySplit ? 0 : k) * kOpBytes, kb = base + S::kOffK + (x & 1) * kOpBytes;
+            // S of tile x; then turn x, which frees K of tile x and V of the
+            // block's tile before it.  (One commit for both.)
+            auto qk = [&](int x) {
+                const uint32_t kb = base + S::kOffK + (x & 1) * kOpBytes;
                 tc_fence_after_sync();
 #pragma unroll
                 for (int s = 0; s < 8; ++s) {
+                    if (s == 4)
+                        mbar_arrive(B(S::kGo + 1 - k));
                     const uint32_t off = (s >> 2) * kHalfBytes + (s & 3) * 32;
-                    umma_f16(tmem + k * kTmBlock + kTmS, smem_desc(qb + off, 16, 1024), smem_desc(kb + off, 16, 1024), idesc,
-                             s > 0);
+                    umma_f16(tb + kTmS, smem_desc(qb + off, 16, 1024), smem_desc(kb + off, 16, 1024), idesc, s > 0);
                 }
                 umma_commit(B(S::kSFull + k));
-                if (kKeySplit || k == 1)
-                    umma_commit(B(S::kTurn + (x & 1)));
+                umma_commit(B(S::kTurn + (x & 1)));
             };
-            auto pv = [&](int k, int x, bool accumulate) {
-                const uint32_t tb = tmem + k * kTmBlock, vb = base + S::kOffV + (x & 1) * kOpBytes;
+            // P V over the keys 64 half .. + 63 of tile x
+            auto pv = [&](int x, int half, bool accumulate) {
+                const uint32_t vb = base + S::kOffV + (x & 1) * kOpBytes + half * kHalfBytes;
                 tc_fence_after_sync();
 #pragma unroll
-                for (int s = 0; s < 8; ++s)
-                    umma_f16_ts(tb + kTmO, tb + kTmS + 8 * s, smem_desc(vb + (s >> 2) * kHalfBytes + (s & 3) * 32, 16, 1024),
-                                idesc, accumulate || s > 0);
+                for (int s = 0; s < 4; ++s)
+                    umma_f16_ts(tb + kTmO, tb + kTmS + 32 * half + 8 * s, smem_desc(vb + 32 * s, 16, 1024), idesc,
+                                accumulate || s > 0);
             };
-            // For each block in turn: P V of its tile, then Q K^T of its next
-            // one, whose S overwrites that P in issue order.
-            bool ok = wait(S::kQFull, 0);
-            for (int k = 0; ok && k < 2; ++k) {
-                const int x = kKeySplit ? k : 0;
-                if (x >= n_tiles)
-                    break;
-                ok = (!kKeySplit && k > 0) || wait(S::kKFull + (x & 1), 0);
-                if (ok)
-                    qk(k, x);
-            }
-            const int items = kKeySplit ? n_tiles : 2 * n_tiles;
-            for (int it = 0; ok && it < items; ++it) {
-                const int k = it & 1, i = it >> 1;               // block, and its count of tiles
-                const int x = kKeySplit ? it : i, next = x + (kKeySplit ? 2 : 1);
-                const bool first_use = kKeySplit || k == 0;      // the other block has not waited for the tile
-                ok = wait(S::kPFull + k, i & 1) && (!first_use || wait(S::kVFull + (x & 1), (x >> 1) & 1));
+            // P V of a tile, then Q K^T of the block's next one, whose S
+            // overwrites that P in issue order.  One thread for both blocks
+            // left the tensor core idle through the waits (a barrier takes 250
+            // cycles to read beside the MMAs' own shared-memory traffic); two
+            // threads without a rule fell into step, both blocks in their
+            // softmax at once.  So the blocks take turns: a block issues when
+            // the other one is half through the Q K^T of its own turn.
+            constexpr int step = kKeySplit ? 2 : 1;
+            const int x0 = kKeySplit ? k : 0;
+            const bool turns = !kKeySplit || n_tiles > 1;        // both blocks have tiles
+            int turn = 0;
+            auto go = [&]() {
+                const int n = turn++ - (k == 0 ? 1 : 0);
+                return !turns || n < 0 || wait(S::kGo + k, n & 1);
+            };
+            bool ok = x0 < n_tiles && wait(S::kQFull, 0) && wait(S::kKFull + (x0 & 1), 0) && go();
+            if (ok)
+                qk(x0);
+            for (int x = x0, i = 0; ok && x < n_tiles; x += step, ++i) {
+                const int next = x + step;
+                ok = wait(S::kVFull + (x & 1), (x >> 1) & 1) &&
+                     (next >= n_tiles || wait(S::kKFull + (next & 1), (next >> 1) & 1)) && wait(S::kPFull + k, i & 1) && go();
                 if (!ok)
                     break;
-                pv(k, x, i > 0);
-                if (next < n_tiles) {
-                    ok = !first_use || wait(S::kKFull + (next & 1), (next >> 1) & 1);
-                    if (ok)
-                        qk(k, next);
-                }
+                pv(x, 0, i > 0);
+                if (!(ok = wait(S::kPFull + 2 + k, i & 1)))
+                    break;
+                pv(x, 1, true);
+                if (next < n_tiles)
+                    qk(next);
+                else
+                    mbar_arrive(B(S::kGo + 1 - k));
             }
             // nothing of this thread's may still run when tensor memory is freed
-            umma_commit(B(S::kDone));
-            if (!mbar_wait_bounded(B(S::kDone), 0, kWaitLimit))
+            umma_commit(B(S::kDone + k));
+            if (!mbar_wait_bounded(B(S::kDone + k), 0, kWaitLimit))
                 report(p.dev_status, NVFP4KV_DEV_TIMEOUT);
         }
         __syncwarp();
@@ -567,10 +577,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_extend_kernel(const __grid_
             // weights of keys 0 .. 63 over the columns of scores 0 .. 31, of
             // keys 64 .. 127 over those of scores 32 .. 63
             float sum = store_weights(tb + kTmS, s, inv2, neg2);
-            load_scores(tb + kTmS + 64, lo_j - 64, hi_j - 64, s);
-            sum += store_weights(tb + kTmS + 32, s, inv2, neg2);
-            l = l * alpha + sum;
-            m_used = m_new;
             // a raised maximum: rescale the O rows of the warp (S of this tile
             // was committed after P V of the one before, which has landed)
             if (i >= 1 && __any_sync(kFullMask, need)) {
@@ -588,14 +594,21 @@ __global__ void __launch_bounds__(kThreads, 1) paged_extend_kernel(const __grid_
             tmem_wait_st();
             tc_fence_before_sync();
             warp_arrive(B(S::kPFull + blk), lane);
+            load_scores(tb + kTmS + 64, lo_j - 64, hi_j - 64, s);
+            sum += store_weights(tb + kTmS + 32, s, inv2, neg2);
+            l = l * alpha + sum;
+            m_used = m_new;
+            tmem_wait_st();
+            tc_fence_before_sync();
+            warp_arrive(B(S::kPFull + 2 + blk), lane);
         }
         if (ok)
-            ok = wait_warp(S::kDone, 0);
+            ok = wait_warp(S::kDone + blk, 0) && (!kKeySplit || wait_warp(S::kDone + 1 - blk, 0));
         tc_fence_after_sync();
         float w0 = 1.f, w1 = 0.f;                // weights of this copy and of the other one
         volatile float *other = reinterpret_cast<volatile float *>(gbase + S::kOffK);    // [130][128 rows]
         if (kKeySplit) {
-            // (every MMA is done: the K and V stages are free)
+            // (both blocks' MMAs are done: the K and V stages are free)
             if (ok && blk == 1) {
                 if (my_tiles > 0) {
 #pragma unroll
