@@ -538,7 +538,7 @@ nvfp4kv_status nvfp4kv_qk_norm_rope(const void *q, int64_t q_stride, const void 
                                     nvfp4kv_dtype in_dtype, int32_t num_tokens, int32_t num_q_heads,
                                     int32_t num_kv_heads, const int32_t *positions, const nvfp4kv_rope *rope,
                                     const nvfp4kv_head_norm *norm, void *q_out, void *k_out,
-                                    nvfp4kv_stream_t stream);
+                                    int32_t *dev_status, nvfp4kv_stream_t stream);
 
 /* The same fused with the cache write ("SGLang stores KV cache in 4 bits",
  * Interpretation: new K/V are quantised into the NVFP4 cache): q_out as above;

@@ -106,6 +106,8 @@ def library_path() -> str:
 def load(build_if_missing: bool = True):
     """Load libnvfp4kv.so (building it in-tree first if it is absent)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -151,7 +153,7 @@ def load(build_if_missing: bool = True):
                                         _i32, _vp, _vp]),
             "nvfp4kv_release_pages": (_st, [_vp, _vp, _i32, _vp, _i32, _i32, _vp, _i32, _vp, _vp, _vp, _vp]),
             "nvfp4kv_qk_norm_rope": (_st, [_vp, _i64, _vp, _i64, _st, _i32, _i32, _i32, _vp, ctypes.POINTER(_Rope),
-                                           ctypes.POINTER(_HeadNorm), _vp, _vp, _vp]),
+                                           ctypes.POINTER(_HeadNorm), _vp, _vp, _vp, _vp]),
             "nvfp4kv_qk_norm_rope_append": (_st, [ctypes.POINTER(_Nvfp4Cache), _vp, _i64, _vp, _i64, _vp, _i64, _st,
                                                   _i32, _i32, _vp, _vp, ctypes.POINTER(_Rope),
                                                   ctypes.POINTER(_HeadNorm), _vp, _vp, _vp]),
@@ -185,6 +187,10 @@ def _ptr(t) -> int | None:
 def _stream(stream) -> int | None:
     import torch
     if stream is None:
+        # the handle alone, without the Stream object around it (3 us a call)
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is not None:
+            return raw(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -267,21 +273,40 @@ class Rope:
         return ctypes.byref(self._c)
 
 
-def _tensor(t, name, dtype, shape, rows=False):
-    """Check a tensor argument: type, shape (None: any), on the current device,
-    contiguous (rows: the last two dimensions only)."""
+def _tensors(dtype, *args) -> None:
+    """Check (tensor, name, shape) arguments, None tensors passed over: type,
+    shape, on the current device, contiguous."""
     import torch
-    if t.dtype != dtype:
+    dev = None
+    for t, name, shape in args:
+        if t is None:
+            continue
+        if t.dtype is not dtype:
+            raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+        if t.shape != shape:
+            raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+        if dev is None:
+            dev = torch.cuda.current_device()
+        if t.get_device() != dev:
+            raise ValueError(f"{name}: not on the current CUDA device")
+        if not t.is_contiguous():
+            raise ValueError(f"{name}: must be contiguous")
+
+
+def _token_rows(t, name, dtype, shape) -> int:
+    """Check rows [tokens][heads][128] that may be strided by token (views of a
+    fused projection); returns the token stride in elements."""
+    import torch
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if len(t.shape) != len(shape) or any(w is not None and n != w for n, w in zip(t.shape, shape)):
+    if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.get_device() != torch.cuda.current_device():
         raise ValueError(f"{name}: not on the current CUDA device")
-    if rows:
-        if t.shape[0] > 0 and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != t.shape[2])):
-            raise ValueError(f"{name}: heads and channels must be contiguous")
-    elif not t.is_contiguous():
-        raise ValueError(f"{name}: must be contiguous")
+    step, head, one = t.stride()
+    if shape[0] > 0 and (one != 1 or (shape[1] > 1 and head != shape[2])):
+        raise ValueError(f"{name}: heads and channels must be contiguous")
+    return step if shape[0] > 1 else shape[1] * shape[2]
 
 
 # --- entry points -------------------------------------------------------------
@@ -469,22 +494,19 @@ def nvfp4kv_paged_extend(cache: NVFP4Cache, q, q_indptr, block_table, seq_lens, 
     import torch
     if sm_scale is None:
         sm_scale = 1.0 / math.sqrt(HEAD_DIM)
-    B, i32 = seq_lens.shape[0], torch.int32
+    B, pages = block_table.shape
     rows, Hq, _ = q.shape
-    _tensor(q, "q", torch.bfloat16, (rows, Hq, HEAD_DIM))
-    _tensor(out, "out", out.dtype, (rows, Hq, HEAD_DIM))
-    _tensor(cache.pool, "cache", torch.uint8, cache.pool.shape)
-    for t, name, shape in ((q_indptr, "q_indptr", (B + 1,)), (block_table, "block_table", (B, None)),
-                           (seq_lens, "seq_lens", (B,)), (dev_status, "dev_status", (1,))):
-        if t is not None:
-            _tensor(t, name, i32, shape)
-    if workspace is not None:
-        _tensor(workspace, "workspace", torch.uint8, (None,))
+    _tensors(torch.bfloat16, (q, "q", (rows, Hq, HEAD_DIM)))
+    _tensors(out.dtype, (out, "out", (rows, Hq, HEAD_DIM)))
+    _tensors(torch.uint8, (cache.pool, "cache", cache.pool.shape),
+             (workspace, "workspace", (0 if workspace is None else workspace.numel(),)))
+    _tensors(torch.int32, (q_indptr, "q_indptr", (B + 1,)), (block_table, "block_table", (B, pages)),
+             (seq_lens, "seq_lens", (B,)), (dev_status, "dev_status", (1,)))
     if max_q_len is None:
         max_q_len = int((q_indptr[1:] - q_indptr[:-1]).max().item()) if B > 0 else 0
     st = load().nvfp4kv_paged_extend(
-        cache.c, _ptr(q), _ptr(q_indptr), rows, int(max_q_len), B, Hq, _ptr(block_table), block_table.shape[1],
-        _ptr(seq_lens), int(window), float(sm_scale), _ptr(out), _dtype_code(out), _ptr(workspace),
+        cache.c, _ptr(q), _ptr(q_indptr), rows, int(max_q_len), B, Hq, _ptr(block_table), pages, _ptr(seq_lens),
+        int(window), float(sm_scale), _ptr(out), _dtype_code(out), _ptr(workspace),
         0 if workspace is None else workspace.numel(), _ptr(dev_status), _stream(stream))
     _check(st, "nvfp4kv_paged_extend")
 
@@ -497,21 +519,17 @@ def nvfp4kv_plan_step(context_lens, new_lens, block_table, num_pages, free_pages
     kv_indptr [B], slot_mapping and positions [max_tokens] (-1 behind the last
     token) and num_free_out [1] (which may be num_free)."""
     import torch
-    B, i32 = context_lens.shape[0], torch.int32
-    for t, name, shape in ((context_lens, "context_lens", (B,)), (new_lens, "new_lens", (B,)),
-                           (block_table, "block_table", (B, None)), (free_pages, "free_pages", (None,)),
-                           (num_free, "num_free", (1,)), (num_free_out, "num_free_out", (1,)),
-                           (seq_lens, "seq_lens", (B,)), (q_indptr, "q_indptr", (B + 1,)),
-                           (slot_mapping, "slot_mapping", (None,)),
-                           (positions, "positions", (slot_mapping.shape[0],)), (kv_indptr, "kv_indptr", (B,)),
-                           (dev_status, "dev_status", (1,))):
-        if t is not None:
-            _tensor(t, name, i32, shape)
+    B, pages = block_table.shape
+    T, F = slot_mapping.numel(), free_pages.numel()
+    _tensors(torch.int32, (context_lens, "context_lens", (B,)), (new_lens, "new_lens", (B,)),
+             (block_table, "block_table", (B, pages)), (free_pages, "free_pages", (F,)), (num_free, "num_free", (1,)),
+             (num_free_out, "num_free_out", (1,)), (seq_lens, "seq_lens", (B,)), (q_indptr, "q_indptr", (B + 1,)),
+             (slot_mapping, "slot_mapping", (T,)), (positions, "positions", (T,)), (kv_indptr, "kv_indptr", (B,)),
+             (dev_status, "dev_status", (1,)))
     st = load().nvfp4kv_plan_step(
-        _ptr(context_lens), _ptr(new_lens), B, _ptr(block_table), block_table.shape[1], int(num_pages),
-        _ptr(free_pages), free_pages.shape[0], _ptr(num_free), _ptr(num_free_out), _ptr(seq_lens), _ptr(q_indptr),
-        _ptr(kv_indptr), _ptr(slot_mapping), _ptr(positions), slot_mapping.shape[0], _ptr(dev_status),
-        _stream(stream))
+        _ptr(context_lens), _ptr(new_lens), B, _ptr(block_table), pages, int(num_pages), _ptr(free_pages), F,
+        _ptr(num_free), _ptr(num_free_out), _ptr(seq_lens), _ptr(q_indptr), _ptr(kv_indptr), _ptr(slot_mapping),
+        _ptr(positions), T, _ptr(dev_status), _stream(stream))
     _check(st, "nvfp4kv_plan_step")
 
 
@@ -521,52 +539,42 @@ def nvfp4kv_release_pages(old_lens, keep_lens, block_table, num_pages, free_page
     tokens, int32 [B]) back on the stack free_pages[: num_free]; num_free_out
     [1] may be num_free."""
     import torch
-    B, i32 = old_lens.shape[0], torch.int32
-    for t, name, shape in ((old_lens, "old_lens", (B,)), (keep_lens, "keep_lens", (B,)),
-                           (block_table, "block_table", (B, None)), (free_pages, "free_pages", (None,)),
-                           (num_free, "num_free", (1,)), (num_free_out, "num_free_out", (1,)),
-                           (dev_status, "dev_status", (1,))):
-        if t is not None:
-            _tensor(t, name, i32, shape)
+    B, pages = block_table.shape
+    F = free_pages.numel()
+    _tensors(torch.int32, (old_lens, "old_lens", (B,)), (keep_lens, "keep_lens", (B,)),
+             (block_table, "block_table", (B, pages)), (free_pages, "free_pages", (F,)), (num_free, "num_free", (1,)),
+             (num_free_out, "num_free_out", (1,)), (dev_status, "dev_status", (1,)))
     st = load().nvfp4kv_release_pages(
-        _ptr(old_lens), _ptr(keep_lens), B, _ptr(block_table), block_table.shape[1], int(num_pages),
-        _ptr(free_pages), free_pages.shape[0], _ptr(num_free), _ptr(num_free_out), _ptr(dev_status),
-        _stream(stream))
+        _ptr(old_lens), _ptr(keep_lens), B, _ptr(block_table), pages, int(num_pages), _ptr(free_pages), F,
+        _ptr(num_free), _ptr(num_free_out), _ptr(dev_status), _stream(stream))
     _check(st, "nvfp4kv_release_pages")
 
 
 def _head_norm(q_weight, k_weight, eps):
-    if q_weight is None and k_weight is None:
+    first = k_weight if q_weight is None else q_weight
+    if first is None:
         return None
-    for t, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if t is not None:
-            _tensor(t, name, (q_weight if q_weight is not None else k_weight).dtype, (HEAD_DIM,))
-    return ctypes.byref(_HeadNorm(_ptr(q_weight), _ptr(k_weight),
-                                  _dtype_code(q_weight if q_weight is not None else k_weight), float(eps)))
-
-
-def _token_stride(t) -> int:
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+    _tensors(first.dtype, (q_weight, "q_weight", (HEAD_DIM,)), (k_weight, "k_weight", (HEAD_DIM,)))
+    return ctypes.byref(_HeadNorm(_ptr(q_weight), _ptr(k_weight), _dtype_code(first), float(eps)))
 
 
 def nvfp4kv_qk_norm_rope(q, k, positions, q_out, k_out, rope: Rope | None = None, q_weight=None, k_weight=None,
-                         eps=1e-6, stream=None) -> None:
+                         eps=1e-6, dev_status=None, stream=None) -> None:
     """Norm (where a weight is given) and rotate each head of q [T][Hq][128] and
     k [T][Hkv][128] (fp32 or bf16; tokens may be strided, as views of a fused
     projection are) at positions int32 [T] (negative: token left out) into
     q_out (bf16) and k_out (k's type)."""
     import torch
     T, Hq, _ = q.shape
-    Hkv = k.shape[1]
-    code = _dtype_code(q)
-    _tensor(q, "q", q.dtype, (T, Hq, HEAD_DIM), rows=True)
-    _tensor(k, "k", q.dtype, (T, Hkv, HEAD_DIM), rows=True)
-    _tensor(positions, "positions", torch.int32, (T,))
-    _tensor(q_out, "q_out", torch.bfloat16, (T, Hq, HEAD_DIM))
-    _tensor(k_out, "k_out", q.dtype, (T, Hkv, HEAD_DIM))
+    Hkv, code = k.shape[1], _dtype_code(q)
+    q_step = _token_rows(q, "q", q.dtype, (T, Hq, HEAD_DIM))
+    k_step = _token_rows(k, "k", q.dtype, (T, Hkv, HEAD_DIM))
+    _tensors(torch.int32, (positions, "positions", (T,)), (dev_status, "dev_status", (1,)))
+    _tensors(torch.bfloat16, (q_out, "q_out", (T, Hq, HEAD_DIM)))
+    _tensors(q.dtype, (k_out, "k_out", (T, Hkv, HEAD_DIM)))
     st = load().nvfp4kv_qk_norm_rope(
-        _ptr(q), _token_stride(q), _ptr(k), _token_stride(k), code, T, Hq, Hkv, _ptr(positions),
-        None if rope is None else rope.c, _head_norm(q_weight, k_weight, eps), _ptr(q_out), _ptr(k_out),
+        _ptr(q), q_step, _ptr(k), k_step, code, T, Hq, Hkv, _ptr(positions), None if rope is None else rope.c,
+        _head_norm(q_weight, k_weight, eps), _ptr(q_out), _ptr(k_out), _ptr(dev_status),
         _stream(stream))
     _check(st, "nvfp4kv_qk_norm_rope")
 
@@ -578,21 +586,18 @@ def nvfp4kv_qk_norm_rope_append(cache: NVFP4Cache, q, k, v, positions, slot_mapp
     written into the NVFP4 cache at slot_mapping int32 [T] instead of k_out."""
     import torch
     T, Hq, _ = q.shape
-    Hkv = cache.num_kv_heads
-    code = _dtype_code(q)
-    _tensor(q, "q", q.dtype, (T, Hq, HEAD_DIM), rows=True)
-    _tensor(k, "k", q.dtype, (T, Hkv, HEAD_DIM), rows=True)
-    _tensor(v, "v", q.dtype, (T, Hkv, HEAD_DIM), rows=True)
-    _tensor(positions, "positions", torch.int32, (T,))
-    _tensor(slot_mapping, "slot_mapping", torch.int32, (T,))
-    _tensor(cache.pool, "cache", torch.uint8, cache.pool.shape)
-    if dev_status is not None:
-        _tensor(dev_status, "dev_status", torch.int32, (1,))
-    _tensor(q_out, "q_out", torch.bfloat16, (T, Hq, HEAD_DIM))
+    Hkv, code = cache.num_kv_heads, _dtype_code(q)
+    q_step = _token_rows(q, "q", q.dtype, (T, Hq, HEAD_DIM))
+    k_step = _token_rows(k, "k", q.dtype, (T, Hkv, HEAD_DIM))
+    v_step = _token_rows(v, "v", q.dtype, (T, Hkv, HEAD_DIM))
+    _tensors(torch.int32, (positions, "positions", (T,)), (slot_mapping, "slot_mapping", (T,)),
+             (dev_status, "dev_status", (1,)))
+    _tensors(torch.bfloat16, (q_out, "q_out", (T, Hq, HEAD_DIM)))
+    _tensors(torch.uint8, (cache.pool, "cache", cache.pool.shape))
     st = load().nvfp4kv_qk_norm_rope_append(
-        cache.c, _ptr(q), _token_stride(q), _ptr(k), _token_stride(k), _ptr(v), _token_stride(v), code, T, Hq,
-        _ptr(positions), _ptr(slot_mapping), None if rope is None else rope.c, _head_norm(q_weight, k_weight, eps),
-        _ptr(q_out), _ptr(dev_status), _stream(stream))
+        cache.c, _ptr(q), q_step, _ptr(k), k_step, _ptr(v), v_step, code, T, Hq, _ptr(positions), _ptr(slot_mapping),
+        None if rope is None else rope.c, _head_norm(q_weight, k_weight, eps), _ptr(q_out), _ptr(dev_status),
+        _stream(stream))
     _check(st, "nvfp4kv_qk_norm_rope_append")
 
 

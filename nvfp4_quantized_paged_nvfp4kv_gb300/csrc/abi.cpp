@@ -426,6 +426,7 @@ nvfp4kv_status check_norm_rope(const void *q, int64_t q_stride, const void *k, i
     p.hq = num_q_heads;
     p.hkv = num_kv_heads;
     p.in_bf16 = in_dtype == NVFP4KV_BF16;
+    p.wait_limit = wait_limit();
     return NVFP4KV_OK;
 }
 
@@ -769,7 +770,7 @@ nvfp4kv_status nvfp4kv_qk_norm_rope(const void *q, int64_t q_stride, const void 
                                     nvfp4kv_dtype in_dtype, int32_t num_tokens, int32_t num_q_heads,
                                     int32_t num_kv_heads, const int32_t *positions, const nvfp4kv_rope *rope,
                                     const nvfp4kv_head_norm *norm, void *q_out, void *k_out,
-                                    nvfp4kv_stream_t stream)
+                                    int32_t *dev_status, nvfp4kv_stream_t stream)
 {
     NormRopeParams p;
     const nvfp4kv_status st = check_norm_rope(q, q_stride, k, k_stride, in_dtype, num_tokens, num_q_heads,
@@ -794,6 +795,7 @@ nvfp4kv_status nvfp4kv_qk_norm_rope(const void *q, int64_t q_stride, const void 
     if (written_overlap(spans))
         return NVFP4KV_ERR_INVALID_ARG;
     p.k_out = k_out;
+    p.dev_status = dev_status;
     return from_cuda(launch_norm_rope(p, to_cuda(stream)));
 }
 

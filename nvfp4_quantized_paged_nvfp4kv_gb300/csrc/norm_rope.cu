@@ -14,13 +14,22 @@
 // of a turn exactly (up to n 2^-65); cos and sin are taken of its signed top
 // 32 bits.
 //
-// Work split.  A row is eight lanes with 16 channels each (one cache block),
-// so a warp instruction covers four heads of one token: the sum of squares is
-// three shuffles, a half-split pair's partner is the same place in another
-// lane of the row, and a lane holds a whole block for the quantiser.  A warp
-// job is one token and a run of its heads: the job's cos and sin, multiplied
-// by the weights of their channels, stay in 32 registers of the lane for all
-// its heads.  Q jobs, K jobs and (fused) V blocks share one launch.
+// Work split.  A row is eight lanes, lane l with channels 8l .. 8l + 7 and 64 +
+// 8l .. 64 + 8l + 7, so that eight lanes load or store 128 bytes on end (16
+// channels on end a lane touched every 32-byte sector twice: 63 us for 8,192
+// tokens of 48 + 8 heads), a warp instruction covers four heads of one token,
+// and the half-split partner of a full rotation is in the lane itself.  A warp
+// job is one token and a run of its heads, four at a time, queries then keys.
+// The job's cos and sin, multiplied by the weights of their channels, are worked
+// out once by the warp (each lane doing so for its own 16 channels cost 15 of
+// 62 us) and stay in 32 registers of the lane for all heads of a kind; products
+// run on packed fp32 pairs.  For the cache two
+// neighbouring lanes swap halves and hold a whole 16-value block each.  The row
+// jobs and (fused) the V blocks share one launch of resident CTAs.
+//
+// Loads.  Four heads are 1 KB on end (2 KB in fp32); each warp keeps a ring of
+// them in shared memory, filled by bulk copies that run ahead of the work and
+// across its jobs.
 #include "nvfp4kv.h"
 #include "record_write.cuh"
 
@@ -36,25 +45,41 @@ __device__ __forceinline__ uint32_t bf16x2_bits(float lo, float hi)
     return *reinterpret_cast<const uint32_t *>(&two);
 }
 
-// Sixteen channels of an input row to fp32.
+// A lane's two pieces of an output row.
 template <bool kBf16>
-__device__ __forceinline__ void store16(void *dst, size_t elem_off, const float (&y)[16])
+__device__ __forceinline__ void store_pieces(void *dst, size_t elem_off, const float (&y)[16])
 {
-    if constexpr (kBf16) {
-        uint4 *d = reinterpret_cast<uint4 *>(static_cast<uint16_t *>(dst) + elem_off);
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-            d[k] = make_uint4(bf16x2_bits(y[8 * k], y[8 * k + 1]), bf16x2_bits(y[8 * k + 2], y[8 * k + 3]),
-                              bf16x2_bits(y[8 * k + 4], y[8 * k + 5]), bf16x2_bits(y[8 * k + 6], y[8 * k + 7]));
-    } else {
-        float4 *d = reinterpret_cast<float4 *>(static_cast<float *>(dst) + elem_off);
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            d[k] = make_float4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+    for (int k = 0; k < 2; ++k) {
+        const float *v = y + 8 * k;
+        if constexpr (kBf16)
+            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(dst) + elem_off + 64 * k) =
+                make_uint4(bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3]), bf16x2_bits(v[4], v[5]),
+                           bf16x2_bits(v[6], v[7]));
+        else {
+            float4 *d = reinterpret_cast<float4 *>(static_cast<float *>(dst) + elem_off + 64 * k);
+            d[0] = make_float4(v[0], v[1], v[2], v[3]);
+            d[1] = make_float4(v[4], v[5], v[6], v[7]);
+        }
     }
 }
 
-// Plain (coherent) loads: an output row may be the input row.
+// A lane's two pieces of a row staged at `row`.
+template <bool kBf16>
+__device__ __forceinline__ void read_pieces(uint32_t row, int part, RawBlock<kBf16> &r)
+{
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        if constexpr (kBf16) {
+            r.v[k] = lds128(row + 16 * part + 128 * k);
+        } else {
+            r.v[2 * k] = lds128(row + 32 * part + 256 * k);
+            r.v[2 * k + 1] = lds128(row + 32 * part + 256 * k + 16);
+        }
+    }
+}
+
+// Sixteen values on end.
 template <bool kBf16>
 __device__ __forceinline__ void load_row(const void *src, size_t elem_off, RawBlock<kBf16> &r)
 {
@@ -63,6 +88,12 @@ __device__ __forceinline__ void load_row(const void *src, size_t elem_off, RawBl
 #pragma unroll
     for (int i = 0; i < (kBf16 ? 2 : 4); ++i)
         r.v[i] = p[i];
+}
+
+__device__ __forceinline__ uint4 shuffled(const uint4 &v, int from)
+{
+    return make_uint4(__shfl_sync(kFullMask, v.x, from), __shfl_sync(kFullMask, v.y, from),
+                      __shfl_sync(kFullMask, v.z, from), __shfl_sync(kFullMask, v.w, from));
 }
 
 __device__ __forceinline__ bool slot_site(const NormRopeParams &p, int slot, int h, size_t &record, int &tok,
@@ -81,123 +112,290 @@ __device__ __forceinline__ bool slot_site(const NormRopeParams &p, int slot, int
     return true;
 }
 
-// Token t's rows head0 .. head0 + n - 1 of Q or K, by one warp.
-template <bool kBf16, bool kAppend>
-__device__ __forceinline__ void rows_job(const NormRopeParams &p, int t, int head0, int n, bool is_k, float2 *cs)
-{
-    const int lane = threadIdx.x & 31, part = lane & 7, sub = lane >> 3;
-    const int pos = p.positions[t];
-    if (pos < 0)
-        return;                                  // a token that is not there: nothing is written
-    const int half = p.rot >> 1;
-    // the first rows' loads go out before the angles are worked out
-    const void *src = is_k ? p.k : p.q;
-    const size_t row = static_cast<size_t>(t) * (is_k ? p.k_stride : p.q_stride) + static_cast<size_t>(16 * part);
-    RawBlock<kBf16> nxt;
-    if (sub < n)
-        load_row<kBf16>(src, row + static_cast<size_t>(head0 + sub) * kHeadDim, nxt);
+template <bool kBf16>
+struct Ring {
+    static constexpr int kStages = kBf16 ? 6 : 4;            // quads in flight a warp
+    static constexpr uint32_t kRow = kHeadDim * (kBf16 ? 2 : 4);
+    static constexpr uint32_t kStage = 4 * kRow;
+    static constexpr int kCtas = kBf16 ? 5 : 4;              // on an SM (registers)
+    static constexpr uint32_t kSmem = kNrWarps * kStages * kStage;
+    static_assert(kCtas * (kSmem + 4608) <= 227 * 1024, "shared memory");
+};
 
+// What a CTA keeps in shared memory beside the rings: the weights of both kinds
+// as fp32, the frequencies, each warp's angles, its rotation tables (of two
+// channels 2u, 2u + 1 at a place: cos times weight, and the signed sin times the
+// partner's weight) and its ring's barriers.
+struct NrShared {
+    float weight[2][kHeadDim];
+    uint64_t freq[kHeadDim / 2];
+    float2 cs[kNrWarps][kHeadDim / 2];
+    float4 table[kNrWarps][kHeadDim / 2];
+    uint64_t bar[kNrWarps][6];
+};
+
+// A place in a warp's sequence of quads: quads quad .. end - 1 of token t's run
+// `run` are left; quads 0 .. p.q_quads - 1 are queries, the others keys.
+struct Cursor {
+    int t, run, quad, end;
+
+    // the run at (t, run), if there is one
+    __device__ __forceinline__ bool open(const NormRopeParams &p)
+    {
+        const int quads = p.q_quads + (p.hkv + 3) / 4;
+        quad = quads * run / p.token_jobs;
+        end = quads * (run + 1) / p.token_jobs;
+        return t < p.num_tokens;
+    }
+    __device__ __forceinline__ bool first(const NormRopeParams &p, long long job)
+    {
+        const long long at = job / p.token_jobs;
+        t = at < p.num_tokens ? static_cast<int>(at) : p.num_tokens;
+        run = static_cast<int>(job - at * p.token_jobs);
+        return open(p);
+    }
+    // dt, dr: the warp's stride in tokens and runs
+    __device__ __forceinline__ bool next(const NormRopeParams &p, int dt, int dr)
+    {
+        run += dr;
+        const int carry = run >= p.token_jobs ? 1 : 0;
+        run -= carry ? p.token_jobs : 0;
+        t = t > p.num_tokens - dt - carry ? p.num_tokens : t + dt + carry;
+        return open(p);
+    }
+};
+
+// The row jobs of one warp: `first`, first + stride, ...  False when a wait for
+// staged rows gave up.
+template <bool kBf16, bool kAppend>
+__device__ __forceinline__ bool rows_of_warp(const NormRopeParams &p, NrShared &sh, uint32_t ring, long long first,
+                                             long long stride)
+{
+    using G = Ring<kBf16>;
+    const int lane = threadIdx.x & 31, part = lane & 7, sub = lane >> 3, warp = threadIdx.x >> 5;
+    float2 *cs = sh.cs[warp];
+    const uint32_t bar = smem_addr(sh.bar[warp]);
+    const int half = p.rot >> 1;
+    const int c0 = 8 * part;                     // channel of value j: c0 + (j & 7) + 64 (j / 8)
+
+    // stage st gets the quad at f, which moves on (whole warp; lane 0 copies)
+    const int dt = static_cast<int>(stride / p.token_jobs), dr = static_cast<int>(stride % p.token_jobs);
+    Cursor f, w;
+    bool more = f.first(p, first);
+    auto fetch = [&](int st) {
+        const bool is_k = f.quad >= p.q_quads;
+        const int head = 4 * (is_k ? f.quad - p.q_quads : f.quad);
+        const int rows = min(4, (is_k ? p.hkv : p.hq) - head);
+        if (lane == 0) {
+            constexpr int size = kBf16 ? 2 : 4;
+            const size_t at = static_cast<size_t>(f.t) * (is_k ? p.k_stride : p.q_stride) + head * kHeadDim;
+            mbar_arrive_expect_tx(bar + 8 * st, rows * G::kRow);
+            bulk_g2s(ring + st * G::kStage, static_cast<const uint8_t *>(is_k ? p.k : p.q) + at * size, rows * G::kRow,
+                     bar + 8 * st);
+        }
+        if (++f.quad == f.end)
+            more = f.next(p, dt, dr);
+    };
+    int issued = 0;
+    for (; issued < G::kStages && more; ++issued)
+        fetch(issued);
+
+    int st = 0, done = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (bool has = w.first(p, first); ok && has; has = w.next(p, dt, dr)) {
+    const int t = w.t;
+    const int pos = p.positions[t];              // < 0: a token that is not there, nothing of it is written
+    __syncwarp();                                // (the last job's angles have been read)
     for (int i = lane; i < half; i += 32) {
-        const uint64_t turn = p.freq[i] * static_cast<uint64_t>(pos);
+        const uint64_t turn = sh.freq[i] * static_cast<uint64_t>(static_cast<uint32_t>(max(pos, 0)));
         float sn, c;
         sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f, &sn, &c);
         cs[i] = make_float2(c * p.rope_scale, sn * p.rope_scale);
     }
     __syncwarp();
-    // y_c = rstd (x_c wc + x_partner ws)
-    const void *w = is_k ? p.k_weight : p.q_weight;
-    auto weight = [&](int c) {
-        if (w == nullptr)
-            return 1.f;
-        return p.weight_bf16 ? __uint_as_float(static_cast<uint32_t>(__ldg(static_cast<const uint16_t *>(w) + c)) << 16)
-                             : __ldg(static_cast<const float *>(w) + c);
-    };
-    float wc[16], ws[16];
-    const int c0 = 16 * part;
-    const bool turns = c0 < p.rot;
-    int partner = part;
-    if (turns && !p.interleaved)
-        partner = c0 < half ? part + half / 16 : part - half / 16;
+    // y_c = rstd (x_c wc + x_partner ws), two channels in a register
+    uint64_t wc[8], ws[8];
+    auto tables = [&](const float *wt) {
+        float4 *tab = sh.table[warp];
+        __syncwarp();                            // the last table has been read
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-        const int c = c0 + j;
-        const float wt = weight(c);
-        wc[j] = wt;
-        ws[j] = 0.f;
-        if (turns) {
-            if (p.interleaved) {
-                const float2 a = cs[c >> 1];
-                wc[j] = wt * a.x;
-                ws[j] = (j & 1 ? a.y : -a.y) * weight(c ^ 1);
-            } else {
-                const bool low = c < half;
-                const float2 a = cs[low ? c : c - half];
-                wc[j] = wt * a.x;
-                ws[j] = (low ? -a.y : a.y) * weight(low ? c + half : c - half);
+        for (int u = lane; u < kHeadDim / 2; u += 32) {
+            // place u: piece u / 32, channels 64 piece + 8 (u mod 8) + 2 (u / 8 mod 4) and the next
+            const int c = 64 * (u >> 5) + 8 * (u & 7) + 2 * ((u >> 3) & 3);
+            const float2 own = *reinterpret_cast<const float2 *>(wt + c);
+            float4 v = make_float4(own.x, own.y, 0.f, 0.f);
+            if (c < p.rot) {
+                if (p.interleaved) {
+                    const float2 a = cs[c >> 1];
+                    v = make_float4(own.x * a.x, own.y * a.x, -a.y * own.y, a.y * own.x);
+                } else {
+                    const bool low = c < half;
+                    const int mate = low ? c + half : c - half;
+                    const float4 a = *reinterpret_cast<const float4 *>(cs + (low ? c : mate));
+                    const float2 m = *reinterpret_cast<const float2 *>(wt + mate);
+                    v = make_float4(own.x * a.x, own.y * a.z, (low ? -a.y : a.y) * m.x, (low ? -a.w : a.w) * m.y);
+                }
             }
+            tab[u] = v;
         }
-    }
-    const int from = (lane & 24) | partner;
-    for (int r0 = 0; r0 < n; r0 += 4) {
-        const bool live = r0 + sub < n;
-        const RawBlock<kBf16> cur = nxt;
-        if (r0 + 4 + sub < n)
-            load_row<kBf16>(src, row + static_cast<size_t>(head0 + r0 + 4 + sub) * kHeadDim, nxt);
+        __syncwarp();
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float4 v = tab[32 * (j >> 2) + 8 * (j & 3) + part];
+            wc[j] = f32x2_pack(v.x, v.y);
+            ws[j] = f32x2_pack(v.z, v.w);
+        }
+    };
+    // where a half-split partner piece is, when not in the lane itself: chunk
+    // (of eight channels) 8 k + part of the row, plus or minus half / 8
+    const bool swaps = !p.interleaved && p.rot > 0 && p.rot < kHeadDim;
+    auto mate_chunk = [&](int k) {
+        const int chunk = 8 * k + part;
+        return 8 * chunk < half ? chunk + half / 8 : (8 * chunk < p.rot ? chunk - half / 8 : chunk);
+    };
+    for (int quad = w.quad; quad < w.end; ++quad) {
+        const bool is_k = quad >= p.q_quads;
+        if (quad == w.quad || quad == p.q_quads)
+            tables(sh.weight[is_k]);
+        const int head = 4 * (is_k ? quad - p.q_quads : quad) + sub;
+        const bool live = pos >= 0 && head < (is_k ? p.hkv : p.hq);
+        ok = __all_sync(kFullMask, mbar_wait_bounded(bar + 8 * st, phase, p.wait_limit));
+        if (!ok)
+            break;
+        RawBlock<kBf16> cur;                     // (rows behind the last head: what the stage held, not written)
+        read_pieces<kBf16>(ring + st * G::kStage + sub * G::kRow, part, cur);
+        ++done;
+        if (more) {
+            fence_async_shared();                // the stage's reads before its next copy
+            __syncwarp();
+            fetch(st);
+            ++issued;
+        }
+        if (++st == G::kStages) {
+            st = 0;
+            phase ^= 1u;
+        }
         float x[16], y[16];
         unpack<kBf16>(cur, x);
-        float rstd = 1.f;
-        if (w != nullptr) {
-            float sum = 0.f;
+        uint64_t x2[8];
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-                sum = fmaf(x[j], x[j], sum);
+        for (int j = 0; j < 8; ++j)
+            x2[j] = f32x2_pack(x[2 * j], x[2 * j + 1]);
+        uint64_t rstd2 = f32x2_pack(1.f, 1.f);
+        if ((is_k ? p.k_weight : p.q_weight) != nullptr) {
+            uint64_t a = mul_f32x2(x2[0], x2[0]), b = mul_f32x2(x2[1], x2[1]);
+#pragma unroll
+            for (int j = 2; j < 8; j += 2) {
+                a = fma_f32x2(x2[j], x2[j], a);
+                b = fma_f32x2(x2[j + 1], x2[j + 1], b);
+            }
+            a = add_f32x2(a, b);
+            float sum = f32x2_lo(a) + f32x2_hi(a);
 #pragma unroll
             for (int o = 1; o < 8; o <<= 1)
                 sum += __shfl_xor_sync(kFullMask, sum, o);
-            rstd = rsqrtf(fmaf(sum, 1.f / kHeadDim, p.eps));
+            const float rstd = rsqrtf(fmaf(sum, 1.f / kHeadDim, p.eps));
+            rstd2 = f32x2_pack(rstd, rstd);
         }
+        auto turn = [&](int j, uint64_t mate) {
+            const uint64_t v = mul_f32x2(rstd2, fma_f32x2(x2[j], wc[j], mul_f32x2(mate, ws[j])));
+            y[2 * j] = f32x2_lo(v);
+            y[2 * j + 1] = f32x2_hi(v);
+        };
         if (p.interleaved) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-                y[j] = rstd * fmaf(x[j], wc[j], x[j ^ 1] * ws[j]);
-        } else {
-            RawBlock<kBf16> other;
+            for (int j = 0; j < 8; ++j)
+                turn(j, f32x2_pack(x[2 * j + 1], x[2 * j]));
+        } else if (!swaps) {
 #pragma unroll
-            for (int i = 0; i < (kBf16 ? 2 : 4); ++i) {
-                other.v[i].x = __shfl_sync(kFullMask, cur.v[i].x, from);
-                other.v[i].y = __shfl_sync(kFullMask, cur.v[i].y, from);
-                other.v[i].z = __shfl_sync(kFullMask, cur.v[i].z, from);
-                other.v[i].w = __shfl_sync(kFullMask, cur.v[i].w, from);
+            for (int j = 0; j < 8; ++j)
+                turn(j, x2[j ^ 4]);
+        } else {
+            RawBlock<kBf16> other = cur;
+            constexpr int n = kBf16 ? 1 : 2;     // 16-byte words of a piece
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                if (k == 1 && p.rot <= 64)
+                    break;                       // nothing turns in the second pieces
+                const int mate = mate_chunk(k), from = (lane & 24) | (mate & 7);
+#pragma unroll
+                for (int i = 0; i < n; ++i) {
+                    const uint4 a = shuffled(cur.v[i], from);
+                    other.v[n * k + i] = a;
+                    if (p.rot > 64) {
+                        const uint4 b = shuffled(cur.v[n + i], from);
+                        if (mate >= 8)
+                            other.v[n * k + i] = b;
+                    }
+                }
             }
             float z[16];
             unpack<kBf16>(other, z);
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-                y[j] = rstd * fmaf(x[j], wc[j], z[j] * ws[j]);
+            for (int j = 0; j < 8; ++j)
+                turn(j, f32x2_pack(z[2 * j], z[2 * j + 1]));
+        }
+        if constexpr (kAppend) {
+            if (is_k) {
+                // the cache holds what the key would be in the input type: the
+                // same bytes as storing it and quantising the stored row.  Even
+                // lanes give their second piece for the neighbour's first: block
+                // part / 2, or 4 + part / 2 in odd lanes.
+                const bool odd = part & 1;
+                float v[16];
+                if constexpr (kBf16) {
+                    uint32_t w[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        w[j] = bf16x2_bits(y[2 * j], y[2 * j + 1]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t got = __shfl_xor_sync(kFullMask, odd ? w[j] : w[4 + j], 1);
+                        const uint32_t first = odd ? got : w[j], second = odd ? w[4 + j] : got;
+                        v[2 * j] = __uint_as_float(first << 16);
+                        v[2 * j + 1] = __uint_as_float(first & 0xffff0000u);
+                        v[8 + 2 * j] = __uint_as_float(second << 16);
+                        v[8 + 2 * j + 1] = __uint_as_float(second & 0xffff0000u);
+                    }
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float got = __shfl_xor_sync(kFullMask, odd ? y[j] : y[8 + j], 1);
+                        v[j] = odd ? got : y[j];
+                        v[8 + j] = odd ? y[8 + j] : got;
+                    }
+                }
+                size_t rec;
+                int tok;
+                if (live && slot_site(p, p.slot_mapping[t], head, rec, tok, head == 0 && part == 0)) {
+                    const uint32_t flip = divide_by_tensor_scale(v, head_tensor_scale(p.hs, false, head, p.gscale));
+                    write_nvfp4_block(p.pool + rec, false, tok, (part >> 1) + (odd ? 4 : 0), v, ScaleOfByte(), flip);
+                }
+                continue;
+            }
         }
         if (!live)
             continue;
-        const int head = head0 + r0 + sub;
-        if (!is_k) {
-            store16<true>(p.q_out, (static_cast<size_t>(t) * p.hq + head) * kHeadDim + c0, y);
-        } else if constexpr (!kAppend) {
-            store16<kBf16>(p.k_out, (static_cast<size_t>(t) * p.hkv + head) * kHeadDim + c0, y);
-        } else {
-            size_t rec;
-            int tok;
-            if (!slot_site(p, p.slot_mapping[t], head, rec, tok, head == 0 && part == 0))
-                continue;
-            // the cache holds what the key would be in the input type: the
-            // same bytes as storing it and quantising the stored row
-            if constexpr (kBf16) {
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-                    y[j] = __bfloat162float(__float2bfloat16_rn(y[j]));
+        if (!is_k)
+            store_pieces<true>(p.q_out, (static_cast<size_t>(t) * p.hq + head) * kHeadDim + c0, y);
+        else
+            store_pieces<kBf16>(p.k_out, (static_cast<size_t>(t) * p.hkv + head) * kHeadDim + c0, y);
+    }
+    }
+    if (!ok) {
+        // let the copies in flight land before the CTA exits
+        if (lane == 0)
+            report(p.dev_status, NVFP4KV_DEV_TIMEOUT);
+        for (; done < issued; ++done) {
+            mbar_wait_bounded(bar + 8 * st, phase, kWaitLimit);
+            if (++st == G::kStages) {
+                st = 0;
+                phase ^= 1u;
             }
-            const uint32_t flip = divide_by_tensor_scale(y, head_tensor_scale(p.hs, false, head, p.gscale));
-            write_nvfp4_block(p.pool + rec, false, tok, part, y, ScaleOfByte(), flip);
         }
     }
+    return ok;
 }
 
 // V block `blk` of head h for the pr-th token pair of the call (pairs begin
@@ -247,37 +445,67 @@ __device__ __forceinline__ void v_pair_job(const NormRopeParams &p, int pr, int 
     }
 }
 
-// Warp jobs, token-major: per token q_jobs runs of Q heads and k_jobs runs of
-// K heads; then the V blocks, one a thread.
+// Warp jobs, token-major: a token's quads in p.token_jobs runs; then the V
+// blocks, one a thread.
 template <bool kBf16, bool kAppend>
-__global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const __grid_constant__ NormRopeParams p)
+__global__ void __launch_bounds__(kNrThreads, Ring<kBf16>::kCtas)
+    norm_rope_kernel(const __grid_constant__ NormRopeParams p)
 {
-    __shared__ float2 cs[kNrWarps][kHeadDim / 2];
+    extern __shared__ __align__(128) uint8_t nr_ring[];
+    __shared__ NrShared sh;
+    const int warp = threadIdx.x >> 5;
+    if ((threadIdx.x & 31) == 0) {
+        for (int k = 0; k < Ring<kBf16>::kStages; ++k)
+            mbar_init(smem_addr(&sh.bar[warp][k]), 1);
+        fence_mbar_init();
+    }
     // (the wait comes before the trigger: a kernel that starts early behind
     // this one finds everything before it complete)
     pdl_wait();
     pdl_launch_dependents();
-    const int warp = threadIdx.x >> 5;
-    const long long job = static_cast<long long>(blockIdx.x) * kNrWarps + warp;
-    const int per = p.q_jobs + p.k_jobs;
-    const long long row_jobs = static_cast<long long>(p.num_tokens) * per;
-    if (job < row_jobs) {
-        const int t = static_cast<int>(job / per);
-        int j = static_cast<int>(job - static_cast<long long>(t) * per);
-        const bool is_k = j >= p.q_jobs;
-        if (is_k)
-            j -= p.q_jobs;
-        const int heads = is_k ? p.hkv : p.hq;
-        const int head0 = j * p.heads_per_job;
-        rows_job<kBf16, kAppend>(p, t, head0, min(p.heads_per_job, heads - head0), is_k, cs[warp]);
-    } else if constexpr (kAppend) {
-        const long long item = (job - row_jobs) * 32 + (threadIdx.x & 31);
-        const long long unit = item >> 3;        // pair * hkv + h
-        const long long pr = unit / p.hkv;
-        if (2 * pr <= p.num_tokens)              // (the early start adds half a pair)
-            v_pair_job<kBf16>(p, static_cast<int>(pr), static_cast<int>(unit - pr * p.hkv),
-                              static_cast<int>(item & 7));
+    for (int i = threadIdx.x; i < 2 * kHeadDim; i += kNrThreads) {
+        const void *w = i < kHeadDim ? p.q_weight : p.k_weight;
+        const int c = i % kHeadDim;
+        float v = 1.f;
+        if (w != nullptr)
+            v = p.weight_bf16 ? __uint_as_float(static_cast<uint32_t>(static_cast<const uint16_t *>(w)[c]) << 16)
+                              : static_cast<const float *>(w)[c];
+        sh.weight[i / kHeadDim][c] = v;
     }
+    if (threadIdx.x < kHeadDim / 2)
+        sh.freq[threadIdx.x] = p.freq[threadIdx.x];
+    __syncthreads();
+    const long long row_jobs = static_cast<long long>(p.num_tokens) * p.token_jobs;
+    const long long first = static_cast<long long>(blockIdx.x) * kNrWarps + warp;
+    const long long stride = static_cast<long long>(gridDim.x) * kNrWarps;
+    if (!rows_of_warp<kBf16, kAppend>(p, sh, smem_addr(nr_ring) + warp * Ring<kBf16>::kStages * Ring<kBf16>::kStage,
+                                      first, stride))
+        return;
+    if constexpr (kAppend) {
+        long long job = first < row_jobs ? first + (row_jobs - first + stride - 1) / stride * stride : first;
+        for (; job < row_jobs + p.v_jobs; job += stride) {
+            const long long item = (job - row_jobs) * 32 + (threadIdx.x & 31);
+            const long long unit = item >> 3;    // pair * hkv + h
+            const long long pr = unit / p.hkv;
+            if (2 * pr <= p.num_tokens)          // (the early start adds half a pair)
+                v_pair_job<kBf16>(p, static_cast<int>(pr), static_cast<int>(unit - pr * p.hkv),
+                                  static_cast<int>(item & 7));
+        }
+    }
+}
+
+template <bool kBf16, bool kAppend>
+cudaError_t launch_rows(const NormRopeParams &p, long long jobs, int sms, cudaStream_t s)
+{
+    using G = Ring<kBf16>;
+    const auto kernel = norm_rope_kernel<kBf16, kAppend>;
+    if (G::kSmem > 48 * 1024) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, G::kSmem);
+        if (e != cudaSuccess)
+            return e;
+    }
+    const long long want = (jobs + kNrWarps - 1) / kNrWarps, most = static_cast<long long>(sms) * G::kCtas;
+    return launch_pdl(kernel, dim3(static_cast<unsigned>(want < most ? want : most)), dim3(kNrThreads), G::kSmem, s, p);
 }
 
 } // namespace
@@ -285,22 +513,19 @@ __global__ void __launch_bounds__(kNrThreads) norm_rope_kernel(const __grid_cons
 cudaError_t launch_norm_rope(const NormRopeParams &in, cudaStream_t s)
 {
     NormRopeParams p = in;
-    // four heads a job while that leaves fewer jobs than fill the SMs twice
-    // over, else sixteen, so a job's angles serve more rows
-    const long long quads = static_cast<long long>(p.num_tokens) * ((p.hq + 3) / 4 + (p.hkv + 3) / 4);
-    p.heads_per_job = quads < 32LL * sm_count() ? 4 : 16;
-    p.q_jobs = (p.hq + p.heads_per_job - 1) / p.heads_per_job;
-    p.k_jobs = (p.hkv + p.heads_per_job - 1) / p.heads_per_job;
-    long long warps = static_cast<long long>(p.num_tokens) * (p.q_jobs + p.k_jobs);
+    const int sms = sm_count() > 0 ? sm_count() : 1;
+    p.q_quads = (p.hq + 3) / 4;
+    const int quads = p.q_quads + (p.hkv + 3) / 4;
+    // one quad a job while the jobs do not fill the SMs, else about eight, so
+    // that a job's angles and tables serve more rows
+    const long long all = static_cast<long long>(p.num_tokens) * quads;
+    p.token_jobs = all <= 20LL * sms ? quads : (quads + 7) / 8;
     const bool append = p.pool != nullptr;
+    p.v_jobs = append ? ((static_cast<long long>(p.num_tokens) + 2) / 2 * p.hkv * 8 + 31) / 32 : 0;
+    const long long jobs = static_cast<long long>(p.num_tokens) * p.token_jobs + p.v_jobs;
     if (append)
-        warps += ((static_cast<long long>(p.num_tokens) + 2) / 2 * p.hkv * 8 + 31) / 32;
-    const long long grid = (warps + kNrWarps - 1) / kNrWarps;
-    if (grid > 0x7fffffffLL)
-        return cudaErrorInvalidValue;
-    const auto kernel = append ? (p.in_bf16 ? norm_rope_kernel<true, true> : norm_rope_kernel<false, true>)
-                               : (p.in_bf16 ? norm_rope_kernel<true, false> : norm_rope_kernel<false, false>);
-    return launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), dim3(kNrThreads), 0, s, p);
+        return p.in_bf16 ? launch_rows<true, true>(p, jobs, sms, s) : launch_rows<false, true>(p, jobs, sms, s);
+    return p.in_bf16 ? launch_rows<true, false>(p, jobs, sms, s) : launch_rows<false, false>(p, jobs, sms, s);
 }
 
 } // namespace nvfp4kv

@@ -208,11 +208,12 @@ struct NormRopeParams {
     float eps;
     float rope_scale;            // multiplies cos and sin
     float gscale;
-    int heads_per_job;           // set by the launcher
-    int q_jobs;
-    int k_jobs;
+    int q_quads;                 // set by the launcher: runs of four query heads,
+    int token_jobs;              // warp jobs that a token's quads are split over,
+    long long v_jobs;            // and warps of V blocks
     HeadScales hs;
     uint64_t freq[kHeadDim / 2]; // turns a position, in units of 2^-64
+    uint32_t wait_limit;
 };
 
 // A step's tables (plan: a = context lengths, b = new tokens) or the return of

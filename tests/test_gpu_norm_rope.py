@@ -239,3 +239,22 @@ def test_two_streams_and_a_replayed_graph():
     torch.cuda.synchronize()
     for a, b in outs + [(qo, ko)]:
         assert torch.equal(a, want_q) and torch.equal(b, want_k)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_wait_runs_out_then_recovers(dtype):
+    T, hq, hkv = 300, 12, 4
+    q, k = rows(T, hq, dtype, 22), rows(T, hkv, dtype, 23)
+    pos = torch.arange(T, dtype=torch.int32, device=DEV)
+    qo, ko = torch.zeros((T, hq, 128), dtype=torch.bfloat16, device=DEV), torch.zeros_like(k)
+    status = torch.zeros(1, dtype=torch.int32, device=DEV)
+    prev = nv.nvfp4kv_set_wait_limit(0)
+    try:
+        nv.nvfp4kv_qk_norm_rope(q, k, pos, qo, ko, dev_status=status)
+        assert nv.read_device_status(status) == nv.DEV_TIMEOUT
+    finally:
+        nv.nvfp4kv_set_wait_limit(prev)
+    status.zero_()
+    nv.nvfp4kv_qk_norm_rope(q, k, pos, qo, ko, dev_status=status)
+    assert nv.read_device_status(status) == 0
+    assert torch.equal(qo, q.to(torch.bfloat16)) and torch.equal(ko, k)      # no norm, no rotation

@@ -71,7 +71,7 @@ def norm_rope(q=addr(0), qs=1024, k=addr(1), ks=256, dtype=nv.BF16, T=4, hq=8, h
               qo=addr(3), ko=addr(4)):
     return nv.load().nvfp4kv_qk_norm_rope(q, qs, k, ks, dtype, T, hq, hkv, pos,
                                           None if rp is None else ctypes.byref(rp),
-                                          None if nm is None else ctypes.byref(nm), qo, ko, None)
+                                          None if nm is None else ctypes.byref(nm), qo, ko, None, None)
 
 
 def append(q=addr(0), qs=1024, k=addr(1), ks=256, v=addr(5), vs=256, dtype=nv.BF16, T=4, hq=8, pos=addr(2),
