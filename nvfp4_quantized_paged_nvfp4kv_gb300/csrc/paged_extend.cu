@@ -22,9 +22,10 @@
 //             [128 channels][128 keys], so that the two tokens that a V byte
 //             holds are neighbours in the operand
 //   S = Q K^T tcgen05.mma M128 N128 K16 x 8, Q in shared memory
-//   softmax   one thread a row: mask, exp2 against a running maximum that is
-//             raised only when it grows by more than 2^8, P (f16) back into the
-//             columns of S
+//   softmax   one thread a row, 64 keys at a time: exp2 against a reference
+//             that is the largest score of the first keys seen and is raised
+//             only when the sum of 64 weights passes 2^15 (so that no maximum is
+//             taken as a rule), P (f16) back into the columns of S
 //   O += P V  tcgen05.mma M128 N128 K16 x 8, P and O in tensor memory
 // Tiles of 64 keys with Q in tensor memory, which spare the Q reads, ran at half
 // the rate: an M128 N64 MMA takes the tensor core the 64 cycles of an N128 one.
@@ -38,8 +39,8 @@
 // are not loaded hold cannot reach a row that does not see them.  Q: each row
 // times a power of two that puts its largest element in [2^14, 2^15), which
 // makes bf16 -> f16 exact but for elements under 2^-28 of the row's largest.
-// P is rounded to f16 (relative 2^-11, at most 2^8); scores, sums and O are
-// fp32.
+// P is rounded to f16 (relative 2^-11, at most 2^15, its largest at least 1);
+// scores, sums and O are fp32.
 //
 // Few rows and many keys: the keys are split over gridDim.x / tiles CTAs, each
 // leaving its O, maximum and sum in the workspace, which a second kernel joins.
@@ -54,7 +55,7 @@ constexpr int kGranKeys = 64;                  // keys of a granule: what is loa
 constexpr int kGrans = kKeys / kGranKeys;
 constexpr int kGranPages = kGranKeys / kPageSize;
 constexpr int kConvThreads = 128;
-constexpr float kRaise = 8.f;                  // log2 margin before the running maximum moves
+constexpr float kMaxSum = 32768.f;             // of 64 weights, before the reference of the softmax moves
 
 constexpr uint32_t kOpBytes = kKeys * kHeadDim * 2;            // 32 KB: a Q, K or V operand tile
 constexpr uint32_t kHalfBytes = kOpBytes / 2;                  // its 64-channel (V: 64-key) half: 128 rows of 128 bytes
@@ -80,7 +81,7 @@ struct Shape {
     static constexpr uint32_t kOffBar = kOffRaw + kRaw * kRawBytes;
     enum : int {
         kRawFull = 0, kRawEmpty = kRawFull + kRaw, kKFull = kRawEmpty + kRaw, kVFull = kKFull + kStages,
-        kTurn = kVFull + kStages, kQFull = kTurn + kStages, kSFull = kQFull + 1, kPFull = kSFull + 2, kDone = kPFull + 4,
+        kTurn = kVFull + kStages, kQFull = kTurn + kStages, kSFull = kQFull + 1, kPFull = kSFull + 2, kHalf = kPFull + 4, kDone = kHalf + 2,
         kGo = kDone + 2, kJoin = kGo + 2, kNumBars = kJoin + 1
     };
     static constexpr uint32_t kOffSlot = kOffBar + 8 * kNumBars;
@@ -106,6 +107,23 @@ __device__ __forceinline__ bool wait_bar(uint32_t bar, uint32_t parity, volatile
         if (mbar_try_wait(bar, parity))
             return true;
         if (*fail)
+            return false;
+    }
+    *fail = 1;
+    report(dev_status, NVFP4KV_DEV_TIMEOUT);
+    return false;
+}
+
+// The same for three phases at once: one after the other each read of a barrier
+// would cost its whole latency.
+__device__ __forceinline__ bool wait_bars(uint32_t a, uint32_t pa, uint32_t b, uint32_t pb, uint32_t c, uint32_t pc,
+                                          volatile int *fail, int32_t *dev_status, uint32_t limit)
+{
+    for (uint64_t i = 0; i < 64ull * limit; ++i) {       // (test_wait does not wait: more polls to the limit)
+        const bool ra = mbar_test_wait(a, pa), rb = mbar_test_wait(b, pb), rc = mbar_test_wait(c, pc);
+        if (ra && rb && rc)
+            return true;
+        if ((i & 63) == 63 && *fail)
             return false;
     }
     *fail = 1;
@@ -231,12 +249,13 @@ __device__ __forceinline__ float max_of(const float (&s)[64])
     return fmax3(fmax3(pm[0], pm[1], pm[2]), fmax3(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7]));
 }
 
-// 2^(s inv - m) of 64 scores, as f16 pairs into 32 tensor-memory columns; their
-// sum (of the unrounded values) is returned.
-__device__ __forceinline__ float store_weights(uint32_t taddr, float (&s)[64], uint64_t inv2, uint64_t neg2)
+// 2^(s inv - m) of 64 scores, as f16 pairs; their sum (of the unrounded values)
+// is returned.
+__device__ __forceinline__ float weights_of(const float (&s)[64], uint64_t inv2, float m, uint32_t (&pw)[32])
 {
+    const float mbase = m == -INFINITY ? 0.f : m;
+    const uint64_t neg2 = f32x2_pack(-mbase, -mbase);
     uint64_t acc[4] = {0, 0, 0, 0};
-    uint32_t pw[32];
 #pragma unroll
     for (int j = 0; j < 32; ++j) {
         const uint64_t d = fma_f32x2(f32x2_pack(s[2 * j], s[2 * j + 1]), inv2, neg2);
@@ -244,7 +263,6 @@ __device__ __forceinline__ float store_weights(uint32_t taddr, float (&s)[64], u
         acc[j & 3] = add_f32x2(acc[j & 3], f32x2_pack(a, b));
         pw[j] = pack_f16x2(a, b);
     }
-    tmem_st32(taddr, pw);
     const uint64_t a = add_f32x2(add_f32x2(acc[0], acc[1]), add_f32x2(acc[2], acc[3]));
     return f32x2_lo(a) + f32x2_hi(a);
 }
@@ -328,6 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_extend_kernel(const __grid_
             mbar_init(B(S::kSFull + k), 1);
             mbar_init(B(S::kPFull + k), kRowsBlock / 32);
             mbar_init(B(S::kPFull + 2 + k), kRowsBlock / 32);
+            mbar_init(B(S::kHalf + k), 1);
             mbar_init(B(S::kDone + k), 1);
             mbar_init(B(S::kGo + k), 1);
         }
@@ -429,21 +448,24 @@ __global__ void __launch_bounds__(kThreads, 1) paged_extend_kernel(const __grid_
             constexpr int step = kKeySplit ? 2 : 1;
             const int x0 = kKeySplit ? k : 0;
             const bool turns = !kKeySplit || n_tiles > 1;        // both blocks have tiles
-            int turn = 0;
-            auto go = [&]() {
-                const int n = turn++ - (k == 0 ? 1 : 0);
-                return !turns || n < 0 || wait(S::kGo + k, n & 1);
-            };
-            bool ok = x0 < n_tiles && wait(S::kQFull, 0) && wait(S::kKFull + (x0 & 1), 0) && go();
+            // Turn n of a block follows turn n - 1 (block 0) or n (block 1) of the
+            // other.  K of the next tile comes after V of this one from the same
+            // converter warps, so one wait covers both.
+            bool ok = x0 < n_tiles && wait(S::kQFull, 0) && wait(S::kKFull + (x0 & 1), 0) &&
+                      (k == 0 || wait(S::kGo + 1, 0));
             if (ok)
                 qk(x0);
             for (int x = x0, i = 0; ok && x < n_tiles; x += step, ++i) {
                 const int next = x + step;
-                ok = wait(S::kVFull + (x & 1), (x >> 1) & 1) &&
-                     (next >= n_tiles || wait(S::kKFull + (next & 1), (next >> 1) & 1)) && wait(S::kPFull + k, i & 1) && go();
+                const uint32_t p_bar = B(S::kPFull + k), p_par = i & 1;
+                const uint32_t go_bar = turns ? B(S::kGo + k) : p_bar, go_par = turns ? (k == 0 ? i : i + 1) & 1 : p_par;
+                const uint32_t kv_bar = next < n_tiles ? B(S::kKFull + (next & 1)) : B(S::kVFull + (x & 1));
+                const uint32_t kv_par = next < n_tiles ? (next >> 1) & 1 : (x >> 1) & 1;
+                ok = wait_bars(p_bar, p_par, go_bar, go_par, kv_bar, kv_par, fail, p.dev_status, p.wait_limit);
                 if (!ok)
                     break;
                 pv(x, 0, i > 0);
+                umma_commit(B(S::kHalf + k));
                 if (!(ok = wait(S::kPFull + 2 + k, i & 1)))
                     break;
                 pv(x, 1, true);
@@ -563,44 +585,63 @@ __global__ void __launch_bounds__(kThreads, 1) paged_extend_kernel(const __grid_
             tc_fence_after_sync();
             const int k0 = (tile_lo + (kKeySplit ? 2 * i + blk : i)) * kKeys;
             const int hi_j = pos + 1 - k0, lo_j = lo - k0;
-            // the maximum over all 128 scores; the first 64 stay in registers
-            float s[64];
-            load_scores(tb + kTmS + 64, lo_j - 64, hi_j - 64, s);
-            float mx = max_of(s);
-            load_scores(tb + kTmS, lo_j, hi_j, s);
-            mx = fmaxf(mx, max_of(s)) * inv;
-            const bool need = mx > m_used + kRaise;
-            const float m_new = need ? mx : m_used;
-            const float mbase = m_new == -INFINITY ? 0.f : m_new;
-            const float alpha = need ? fast_exp2(m_used - mbase) : 1.f;
-            const uint64_t neg2 = f32x2_pack(-mbase, -mbase);
-            // weights of keys 0 .. 63 over the columns of scores 0 .. 31, of
+            // weights of keys 0 .. 63 go over the columns of scores 0 .. 31, of
             // keys 64 .. 127 over those of scores 32 .. 63
-            float sum = store_weights(tb + kTmS, s, inv2, neg2);
-            // a raised maximum: rescale the O rows of the warp (S of this tile
-            // was committed after P V of the one before, which has landed)
-            if (i >= 1 && __any_sync(kFullMask, need)) {
+#pragma unroll 1
+            for (int hf = 0; ok && hf < 2; ++hf) {
+                const uint32_t at = tb + kTmS + 64 * hf;
+                const int lo_h = lo_j - 64 * hf, hi_h = hi_j - 64 * hf;
+                // the rows for which `need` holds take their largest score as
+                // reference; O and l, which were relative to the old one, follow
+                auto raise = [&](bool need, float mx) {
+                    const float m_new = need ? mx : m_used;
+                    const float alpha = need ? fast_exp2(m_used - (m_new == -INFINITY ? 0.f : m_new)) : 1.f;
+                    m_used = m_new;
+                    l *= alpha;
+                    if (i == 0 && hf == 0)
+                        return true;             // no O yet
+                    // the products before this one have landed: S of this tile
+                    // was committed after those of the last tile
+                    if (hf == 1 && !wait_warp(S::kHalf + blk, i & 1))
+                        return false;
+                    tc_fence_after_sync();
+#pragma unroll 1
+                    for (int cb = 0; cb < 4; ++cb) {
+                        uint32_t o[32];
+                        tmem_ld32(tb + kTmO + 32 * cb, o);
+                        tmem_wait_ld();
 #pragma unroll
-                for (int cb = 0; cb < 4; ++cb) {
-                    uint32_t o[32];
-                    tmem_ld32(tb + kTmO + 32 * cb, o);
-                    tmem_wait_ld();
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
-                    tmem_st32(tb + kTmO + 32 * cb, o);
+                        for (int j = 0; j < 32; ++j)
+                            o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+                        tmem_st32(tb + kTmO + 32 * cb, o);
+                    }
+                    return true;
+                };
+                float s[64];
+                load_scores(at, lo_h, hi_h, s);
+                const bool first = m_used == -INFINITY;
+                if (__any_sync(kFullMask, first)) {
+                    const float mx = max_of(s) * inv;
+                    if (__any_sync(kFullMask, first && mx > -INFINITY) && !(ok = raise(first && mx > -INFINITY, mx)))
+                        break;
+                    load_scores(at, lo_h, hi_h, s);      // (64 registers fewer to keep meanwhile)
                 }
+                uint32_t pw[32];
+                float sum = weights_of(s, inv2, m_used, pw);
+                if (__any_sync(kFullMask, sum > kMaxSum)) {
+                    load_scores(at, lo_h, hi_h, s);
+                    if (!(ok = raise(sum > kMaxSum, max_of(s) * inv)))
+                        break;
+                    sum = weights_of(s, inv2, m_used, pw);
+                }
+                l += sum;
+                tmem_st32(tb + kTmS + 32 * hf, pw);
+                tmem_wait_st();
+                tc_fence_before_sync();
+                warp_arrive(B(S::kPFull + 2 * hf + blk), lane);
             }
-            tmem_wait_st();
-            tc_fence_before_sync();
-            warp_arrive(B(S::kPFull + blk), lane);
-            load_scores(tb + kTmS + 64, lo_j - 64, hi_j - 64, s);
-            sum += store_weights(tb + kTmS + 32, s, inv2, neg2);
-            l = l * alpha + sum;
-            m_used = m_new;
-            tmem_wait_st();
-            tc_fence_before_sync();
-            warp_arrive(B(S::kPFull + 2 + blk), lane);
+            if (!ok)
+                break;
         }
         if (ok)
             ok = wait_warp(S::kDone + blk, 0) && (!kKeySplit || wait_warp(S::kDone + 1 - blk, 0));
