@@ -155,18 +155,35 @@ __device__ __forceinline__ bool read_chunk(const PagedExtendParams &p, int b, Ch
            c.len <= p.max_pages * kPageSize;
 }
 
-// K of a staged granule to f16 [key][channel] at dst (its first key's row),
-// thread pt of 128: two quarter rows of 32 channels.  Lanes of the upper channel
-// half of a quarter pair store their chunks in another order, so eight lanes
-// meet eight bank groups.
-__device__ __forceinline__ void convert_k(uint32_t raw, uint32_t dst, int pt)
+// K of a staged granule, thread pt of 128: two quarter rows of 32 channels.
+// Loads and conversions are apart so that all loads of a tile are out before the
+// first conversion (one warp a scheduler has no other to hide them behind).
+struct RawK {
+    uint4 d[2];
+    uint32_t s[2];
+};
+
+__device__ __forceinline__ void load_k(uint32_t raw, int pt, RawK &k)
 {
 #pragma unroll
     for (int u = 0; u < 2; ++u) {
         const uint32_t idx = pt + kConvThreads * u, key = idx >> 2, quarter = idx & 3u;
         const uint32_t rec = raw + (key >> 4) * kNvfp4Record;
-        const uint4 d = lds128(rec + (key & 15u) * 64u + quarter * 16u);
-        const uint32_t two = lds_u16(rec + 2048u + (key & 15u) * 8u + 2u * quarter) & 0x7f7fu;
+        k.d[u] = lds128(rec + (key & 15u) * 64u + quarter * 16u);
+        k.s[u] = lds_u16(rec + 2048u + (key & 15u) * 8u + 2u * quarter);
+    }
+}
+
+// ... to f16 [key][channel] at dst (the granule's first key's row).  Lanes of
+// the upper channel half of a quarter pair store their chunks in another order,
+// so eight lanes meet eight bank groups.
+__device__ __forceinline__ void convert_k(const RawK &k, uint32_t dst, int pt)
+{
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const uint32_t idx = pt + kConvThreads * u, key = idx >> 2, quarter = idx & 3u;
+        const uint4 d = k.d[u];
+        const uint32_t two = k.s[u] & 0x7f7fu;
         const bool swap = quarter & 2u;
         const uint32_t w[4] = {swap ? d.z : d.x, swap ? d.w : d.y, swap ? d.x : d.z, swap ? d.y : d.w};
         const uint32_t lo = two & 0xffu, hi = two >> 8;
@@ -183,28 +200,36 @@ __device__ __forceinline__ void convert_k(uint32_t raw, uint32_t dst, int pt)
     }
 }
 
-// V of a staged granule to f16 [channel][key] (a 64-key half of the operand):
-// thread pt takes eight keys (half a page, four token pairs), group g of the
-// pairs' rows and half its blocks.
-__device__ __forceinline__ void convert_v(uint32_t raw, uint32_t dst, int pt)
+// V of a staged granule: thread pt takes eight keys (half a page, four token
+// pairs), group g of the pairs' rows and half its blocks.
+struct RawV {
+    uint2 d[4], s[4];
+};
+
+__device__ __forceinline__ void load_v(uint32_t raw, int pt, RawV &v)
 {
     const uint32_t g = pt & 7, jh = (pt >> 3) & 1, eight = pt >> 4;
     const uint32_t rec = raw + (eight >> 1) * kNvfp4Record, p0 = (eight & 1u) * 4u;
-    uint2 d[4], s[4];
 #pragma unroll
     for (uint32_t r = 0; r < 4; ++r) {
         const uint32_t p = p0 + r;
-        d[r] = lds64(rec + 1024u + p * 128u + ((g + 2u * p) & 7u) * 16u + 8u * jh);
-        s[r] = lds64(rec + 2176u + p * 16u + 8u * jh);
+        v.d[r] = lds64(rec + 1024u + p * 128u + ((g + 2u * p) & 7u) * 16u + 8u * jh);
+        v.s[r] = lds64(rec + 2176u + p * 16u + 8u * jh);
     }
+}
+
+// ... to f16 [channel][key] (a 64-key half of the operand).
+__device__ __forceinline__ void convert_v(const RawV &v, uint32_t dst, int pt)
+{
+    const uint32_t g = pt & 7, jh = (pt >> 3) & 1, eight = pt >> 4;
 #pragma unroll
     for (uint32_t half = 0; half < 2; ++half) {
         uint32_t f[4][4];                        // [pair row][(block, w)]: tokens 2p, 2p + 1
 #pragma unroll
         for (uint32_t r = 0; r < 4; ++r) {
-            const uint32_t sw = (half ? s[r].y : s[r].x) & 0x7f7f7f7fu;
+            const uint32_t sw = (half ? v.s[r].y : v.s[r].x) & 0x7f7f7f7fu;
             const uint32_t s0 = __byte_perm(sw, 0, 0x4140) << 7, s1 = __byte_perm(sw, 0, 0x4342) << 7;
-            e2m1x8_to_f16x2x4(half ? d[r].y : d[r].x, f[r][0], f[r][1], f[r][2], f[r][3]);
+            e2m1x8_to_f16x2x4(half ? v.d[r].y : v.d[r].x, f[r][0], f[r][1], f[r][2], f[r][3]);
             f[r][0] = hmul2(f[r][0], s0);
             f[r][1] = hmul2(f[r][1], s0);
             f[r][2] = hmul2(f[r][2], s1);
@@ -492,34 +517,43 @@ __global__ void __launch_bounds__(kThreads, 1) paged_extend_kernel(const __grid_
         auto stage = [&](int gr) { return base + S::kOffRaw + gr % S::kRaw * kRawBytes; };
         // K of tile x: its stage was last read in the turn of tile x - 2
         auto make_k = [&](int x) {
-            bool ok = x < kStages || wait_turn(x - kStages);
-            for (int u = 0; ok && u < kGrans; ++u) {
+            RawK k[kGrans];
+            bool ok = true;
+#pragma unroll
+            for (int u = 0; u < kGrans; ++u) {
                 const int gr = x * kGrans + u;
-                ok = wait_warp(S::kRawFull + gr % S::kRaw, (gr / S::kRaw) & 1);
+                ok = ok && wait_warp(S::kRawFull + gr % S::kRaw, (gr / S::kRaw) & 1);
                 if (ok)
-                    convert_k(stage(gr), base + S::kOffK + (x & 1) * kOpBytes + u * kGranKeys * 128, pt);
+                    load_k(stage(gr), pt, k[u]);
             }
-            if (ok) {
-                fence_async_shared();
-                warp_arrive(B(S::kKFull + (x & 1)), lane);
-            }
-            return ok;
+            if (!ok || (x >= kStages && !wait_turn(x - kStages)))
+                return false;
+#pragma unroll
+            for (int u = 0; u < kGrans; ++u)
+                convert_k(k[u], base + S::kOffK + (x & 1) * kOpBytes + u * kGranKeys * 128, pt);
+            fence_async_shared();
+            warp_arrive(B(S::kKFull + (x & 1)), lane);
+            return true;
         };
         // V of tile x: its stage was last read by P V of tile x - 2, which the
         // next turn follows (that of tile x where blocks alternate); then the
         // granules are free
         auto make_v = [&](int x) {
+            RawV v[kGrans];
+#pragma unroll
+            for (int u = 0; u < kGrans; ++u)
+                load_v(stage(x * kGrans + u), pt, v[u]);
+            fence_async_shared();                // the granules' reads before their next copies
+#pragma unroll
+            for (int u = 0; u < kGrans; ++u)
+                warp_arrive(B(S::kRawEmpty + (x * kGrans + u) % S::kRaw), lane);
             if (x >= kStages && !wait_turn(x - kStages + (kKeySplit ? 2 : 1)))
                 return false;
 #pragma unroll
-            for (int u = 0; u < kGrans; ++u) {
-                const int gr = x * kGrans + u;
-                convert_v(stage(gr), base + S::kOffV + (x & 1) * kOpBytes + u * kHalfBytes, pt);
-                fence_async_shared();            // also orders the reads of the granule before its next copy
-                warp_arrive(B(S::kRawEmpty + gr % S::kRaw), lane);
-            }
-            if (lane == 0)
-                mbar_arrive(B(S::kVFull + (x & 1)));
+            for (int u = 0; u < kGrans; ++u)
+                convert_v(v[u], base + S::kOffV + (x & 1) * kOpBytes + u * kHalfBytes, pt);
+            fence_async_shared();
+            warp_arrive(B(S::kVFull + (x & 1)), lane);
             return true;
         };
         if (kKeySplit) {
