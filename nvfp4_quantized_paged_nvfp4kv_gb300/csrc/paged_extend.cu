@@ -65,15 +65,16 @@ constexpr uint32_t kTmO = 0, kTmS = 128, kTmBlock = 256;
 
 constexpr int kSoftmaxThreads = 2 * kRowsBlock;
 constexpr int kConvWarp = kSoftmaxThreads / 32;
-constexpr int kMmaWarp = kConvWarp + kConvThreads / 32;
-constexpr int kLoadWarp = kMmaWarp + 2;        // one MMA warp a block
-constexpr int kThreads = 32 * (kLoadWarp + 1);
 constexpr int kStages = 2;                     // converted tiles
 
 template <bool kKeySplit>
 struct Shape {
     static constexpr int kRows = kKeySplit ? kRowsBlock : 2 * kRowsBlock;    // of a CTA
     static constexpr int kRaw = kKeySplit ? 6 : 3;                           // loaded granules
+    static constexpr int kConvGroups = kKeySplit ? 2 : 1;                    // of 128 threads; two: one a block
+    static constexpr int kMmaWarp = kConvWarp + kConvGroups * kConvThreads / 32;
+    static constexpr int kLoadWarp = kMmaWarp + 2;                           // one MMA warp a block
+    static constexpr int kThreads = 32 * (kLoadWarp + 1);
     static constexpr uint32_t kOffQ = 0;
     static constexpr uint32_t kOffK = kOffQ + kRows / kRowsBlock * kOpBytes;
     static constexpr uint32_t kOffV = kOffK + kStages * kOpBytes;
@@ -293,7 +294,8 @@ __device__ __forceinline__ float weights_of(const float (&s)[64], uint64_t inv2,
 }
 
 template <bool kKeySplit>
-__global__ void __launch_bounds__(kThreads, 1) paged_extend_kernel(const __grid_constant__ PagedExtendParams p)
+__global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
+    paged_extend_kernel(const __grid_constant__ PagedExtendParams p)
 {
     using S = Shape<kKeySplit>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -379,14 +381,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_extend_kernel(const __grid_
         *fail = 0;
         fence_mbar_init();
     }
-    if (warp == kMmaWarp)
+    if (warp == S::kMmaWarp)
         tmem_alloc(base + S::kOffSlot, 2 * kTmBlock);
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(gbase + S::kOffSlot);
 
-    if (warp == kLoadWarp) {
+    if (warp == S::kLoadWarp) {
         // granules in order; lane l looks up page l % 4 of granule 8 w + l / 4, a
         // window w ahead
         const int page_lo = key_begin / kPageSize, page_hi = (key_end + kPageSize - 1) / kPageSize;
@@ -431,10 +433,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_extend_kernel(const __grid_
             if (!mbar_wait_bounded(B(S::kRawFull + i % S::kRaw), (i / S::kRaw) & 1, kWaitLimit))
                 report(p.dev_status, NVFP4KV_DEV_TIMEOUT);
         __syncwarp();
-    } else if (warp >= kMmaWarp) {
+    } else if (warp >= S::kMmaWarp) {
         if (lane == 0) {
             constexpr uint32_t idesc = idesc_f16(kRowsBlock, 128, false);     // both products: N = 128, K-major
-            const int k = warp - kMmaWarp;                       // the block
+            const int k = warp - S::kMmaWarp;                       // the block
             const uint32_t tb = tmem + k * kTmBlock, qb = base + S::kOffQ + (kKeySplit ? 0 : k) * kOpBytes;
             auto wait = [&](int bar, uint32_t parity) {
                 return wait_bar(B(bar), parity, fail, p.dev_status, p.wait_limit);
@@ -506,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_extend_kernel(const __grid_
         }
         __syncwarp();
     } else if (warp >= kConvWarp) {
-        const int pt = tid - kSoftmaxThreads;
+        const int pt = (tid - kSoftmaxThreads) % kConvThreads;
         auto wait_warp = [&](int k, uint32_t parity) {
             return __all_sync(kFullMask, wait_bar(B(k), parity, fail, p.dev_status, p.wait_limit));
         };
@@ -515,54 +517,76 @@ __global__ void __launch_bounds__(kThreads, 1) paged_extend_kernel(const __grid_
         // round again)
         auto wait_turn = [&](int x) { return wait_warp(S::kTurn + (x & 1), (x >> 1) & 1); };
         auto stage = [&](int gr) { return base + S::kOffRaw + gr % S::kRaw * kRawBytes; };
-        // K of tile x: its stage was last read in the turn of tile x - 2
-        auto make_k = [&](int x) {
-            RawK k[kGrans];
-            bool ok = true;
+        // A tile's bytes go to registers as soon as they are there, so that the
+        // ring's stages are free for the copies to come while conversions wait
+        // for their operand stages.
+        RawK kx[kGrans];
+        RawV vx[kGrans];
+        auto take_k = [&](int x) {
 #pragma unroll
             for (int u = 0; u < kGrans; ++u) {
                 const int gr = x * kGrans + u;
-                ok = ok && wait_warp(S::kRawFull + gr % S::kRaw, (gr / S::kRaw) & 1);
-                if (ok)
-                    load_k(stage(gr), pt, k[u]);
+                if (!wait_warp(S::kRawFull + gr % S::kRaw, (gr / S::kRaw) & 1))
+                    return false;
+                load_k(stage(gr), pt, kx[u]);
             }
-            if (!ok || (x >= kStages && !wait_turn(x - kStages)))
+            return true;
+        };
+        auto take_v = [&](int x) {
+#pragma unroll
+            for (int u = 0; u < kGrans; ++u)
+                load_v(stage(x * kGrans + u), pt, vx[u]);
+            fence_async_shared();                // the reads before the stages' next copies
+#pragma unroll
+            for (int u = 0; u < kGrans; ++u)
+                warp_arrive(B(S::kRawEmpty + (x * kGrans + u) % S::kRaw), lane);
+        };
+        // K of tile x: its stage was last read in the turn of tile x - 2
+        auto make_k = [&](int x) {
+            if (x >= kStages && !wait_turn(x - kStages))
                 return false;
 #pragma unroll
             for (int u = 0; u < kGrans; ++u)
-                convert_k(k[u], base + S::kOffK + (x & 1) * kOpBytes + u * kGranKeys * 128, pt);
+                convert_k(kx[u], base + S::kOffK + (x & 1) * kOpBytes + u * kGranKeys * 128, pt);
             fence_async_shared();
             warp_arrive(B(S::kKFull + (x & 1)), lane);
             return true;
         };
         // V of tile x: its stage was last read by P V of tile x - 2, which the
-        // next turn follows (that of tile x where blocks alternate); then the
-        // granules are free
+        // next turn follows (that of tile x where blocks alternate)
         auto make_v = [&](int x) {
-            RawV v[kGrans];
-#pragma unroll
-            for (int u = 0; u < kGrans; ++u)
-                load_v(stage(x * kGrans + u), pt, v[u]);
-            fence_async_shared();                // the granules' reads before their next copies
-#pragma unroll
-            for (int u = 0; u < kGrans; ++u)
-                warp_arrive(B(S::kRawEmpty + (x * kGrans + u) % S::kRaw), lane);
             if (x >= kStages && !wait_turn(x - kStages + (kKeySplit ? 2 : 1)))
                 return false;
 #pragma unroll
             for (int u = 0; u < kGrans; ++u)
-                convert_v(v[u], base + S::kOffV + (x & 1) * kOpBytes + u * kHalfBytes, pt);
+                convert_v(vx[u], base + S::kOffV + (x & 1) * kOpBytes + u * kHalfBytes, pt);
             fence_async_shared();
             warp_arrive(B(S::kVFull + (x & 1)), lane);
             return true;
         };
-        if (kKeySplit) {
-            // K of the next tile can be made a turn before V of this one
-            bool ok = make_k(0);
-            for (int x = 0; ok && x < n_tiles; ++x)
-                ok = (x + 1 >= n_tiles || make_k(x + 1)) && make_v(x);
+        if constexpr (kKeySplit) {
+            // each group makes its block's tiles: V of one and K of the next
+            // between the block's turns (one group for both blocks was what they
+            // waited for: 1.5 us a tile against 1.2)
+            int x = (tid - kSoftmaxThreads) / kConvThreads;
+            bool ok = x < n_tiles && take_k(x);
+            if (ok) {
+                take_v(x);
+                ok = make_k(x);
+            }
+            for (; ok && x < n_tiles; x += 2) {
+                const bool next = x + 2 < n_tiles;
+                ok = (!next || take_k(x + 2)) && make_v(x);
+                if (ok && next) {
+                    take_v(x + 2);
+                    ok = make_k(x + 2);
+                }
+            }
         } else {
-            for (int x = 0; x < n_tiles && make_k(x) && make_v(x); ++x) {
+            for (int x = 0; x < n_tiles && take_k(x); ++x) {
+                take_v(x);
+                if (!make_k(x) || !make_v(x))
+                    break;
             }
         }
     } else {
@@ -756,7 +780,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_extend_kernel(const __grid_
 
     tc_fence_before_sync();
     __syncthreads();
-    if (warp == kMmaWarp) {
+    if (warp == S::kMmaWarp) {
         tc_fence_after_sync();
         tmem_dealloc(tmem, 2 * kTmBlock);
     }
@@ -859,7 +883,7 @@ static cudaError_t launch_blocks(const PagedExtendParams &p, const ExtendShape &
     if (e != cudaSuccess)
         return e;
     const dim3 grid(static_cast<unsigned>(shape.row_tiles * shape.splits), p.hkv, p.batch);
-    paged_extend_kernel<kKeySplit><<<grid, kThreads, S::kSmem, s>>>(p);
+    paged_extend_kernel<kKeySplit><<<grid, S::kThreads, S::kSmem, s>>>(p);
     return cudaGetLastError();
 }
 
