@@ -639,6 +639,8 @@ nvfp4kv_status nvfp4kv_paged_extend(const nvfp4kv_cache *cache, const void *q, c
     const int32_t group = num_q_heads / cache->num_kv_heads;
     const ExtendShape shape = paged_extend_shape(q_rows, max_q_len, batch, cache->num_kv_heads, group, max_pages_per_seq,
                                                  window);
+    if (shape.units > (int64_t{1} << 31) - 1)
+        return NVFP4KV_ERR_UNSUPPORTED;
     if (shape.workspace > 0 && (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
                                 workspace_bytes < shape.workspace))
         return NVFP4KV_ERR_WORKSPACE;

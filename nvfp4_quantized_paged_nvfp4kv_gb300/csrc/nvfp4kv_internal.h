@@ -162,7 +162,9 @@ struct PagedExtendParams {
     int q_rows;
     int max_q_len;
     int window;                  // 0: none
-    int splits;                  // set by the launcher
+    int splits;                  // set by the launcher, as are
+    int row_tiles;               // row tiles a (sequence, kv head) and
+    int64_t units;               // row tiles x splits x kv heads x sequences
     int out_f32;
     float qscale;                // sm_scale * log2(e)
     float gscale;
@@ -177,6 +179,7 @@ struct ExtendShape {
     bool key_split;
     int64_t row_tiles;
     int splits;
+    int64_t units;
     size_t workspace;
 };
 

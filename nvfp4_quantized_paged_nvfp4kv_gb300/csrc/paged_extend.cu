@@ -82,8 +82,9 @@ struct Shape {
     static constexpr uint32_t kOffBar = kOffRaw + kRaw * kRawBytes;
     enum : int {
         kRawFull = 0, kRawEmpty = kRawFull + kRaw, kKFull = kRawEmpty + kRaw, kVFull = kKFull + kStages,
-        kTurn = kVFull + kStages, kQFull = kTurn + kStages, kSFull = kQFull + 1, kPFull = kSFull + 2, kHalf = kPFull + 4, kDone = kHalf + 2,
-        kGo = kDone + 2, kJoin = kGo + 2, kNumBars = kJoin + 1
+        kTurn = kVFull + kStages, kQFull = kTurn + kStages, kSFull = kQFull + 2, kPFull = kSFull + 2, kHalf = kPFull + 4,
+        kDone = kHalf + 2,
+kGo = kDone + 2, kExit = kGo + 2, kJoin = kExit + 2, kNumBars = kJoin + 1
     };
     static constexpr uint32_t kOffSlot = kOffBar + 8 * kNumBars;
     static constexpr uint32_t kSmem = kOffSlot + 8 + 1024;                   // + slack to align the base
@@ -293,6 +294,100 @@ __device__ __forceinline__ float weights_of(const float (&s)[64], uint64_t inv2,
     return f32x2_lo(a) + f32x2_hi(a);
 }
 
+// A unit of work: some rows of one sequence and kv head, and a run of its key
+// tiles.
+enum { kNoRows, kNoKeys, kWork };
+
+struct UnitPlace {
+    int b, h, split;
+    int row0, rows;                      // first row, and rows of the sequence and kv head
+    int c0, first_pos;                   // row and position of chunk token 0 (negative position: the chunk is longer)
+    int key_begin, key_end;              // keys that some row sees
+    int tile_lo, n_tiles;                // its tiles
+};
+
+// A softmax thread's row.
+struct Row {
+    bool live;
+    int t;                               // chunk token
+    int64_t at;                          // row of q and out, in heads
+
+    // the row's maximum and sum in the workspace: [split][q_rows][hq][2] behind
+    // [split][q_rows][hq][128]
+    __device__ __forceinline__ float *ml(const PagedExtendParams &p, const UnitPlace &u) const
+    {
+        const int64_t all = static_cast<int64_t>(p.q_rows) * p.hq;
+        return p.partials + all * p.splits * kHeadDim + 2 * (all * u.split + at);
+    }
+
+    // what a row leaves that sees no key of the unit
+    __device__ __forceinline__ void nothing(const PagedExtendParams &p, const UnitPlace &u) const
+    {
+        if (!live)
+            return;
+        if (p.splits > 1) {
+            float *d = ml(p, u);
+            d[0] = -INFINITY;
+            d[1] = 0.f;
+            return;
+        }
+        const int words = p.out_f32 ? kHeadDim / 4 : kHeadDim / 8;
+        uint4 *d = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.out) + at * kHeadDim * (p.out_f32 ? 4 : 2));
+        for (int k = 0; k < words; ++k)
+            d[k] = make_uint4(0, 0, 0, 0);
+    }
+};
+
+template <bool kKeySplit>
+struct Unit : UnitPlace {
+    static constexpr int kRows = Shape<kKeySplit>::kRows;
+
+    // Unit idx of p.units: splits innermost, then kv heads, sequences, row tiles
+    // from the last; `rep`: this thread reports a sequence out of bounds.
+    __device__ __forceinline__ int open(const PagedExtendParams &p, int idx, bool rep)
+    {
+        split = idx % p.splits;
+        idx /= p.splits;
+        h = idx % p.hkv;
+        idx /= p.hkv;
+        b = idx % p.batch;
+        const int tile = p.row_tiles - 1 - idx / p.batch;
+        Chunk c;
+        if (!read_chunk(p, b, c)) {
+            if (rep && tile == 0 && split == 0 && h == 0)
+                report(p.dev_status, NVFP4KV_DEV_BAD_LEN);
+            return kNoRows;
+        }
+        rows = c.count * p.group;
+        row0 = tile * kRows;
+        if (row0 >= rows)
+            return kNoRows;
+        c0 = c.c0;
+        first_pos = c.len - c.count;
+        const int t_last = (min(row0 + kRows, rows) - 1) / p.group;
+        key_end = max(0, first_pos + t_last + 1);
+        key_begin = p.window > 0 ? max(0, first_pos + row0 / p.group - p.window + 1) : 0;
+        if (key_end <= key_begin)
+            return kNoKeys;
+        tile_lo = key_begin / kKeys;
+        const int all = (key_end + kKeys - 1) / kKeys - tile_lo;
+        const int from = static_cast<int>(static_cast<int64_t>(all) * split / p.splits);
+        n_tiles = static_cast<int>(static_cast<int64_t>(all) * (split + 1) / p.splits) - from;
+        tile_lo += from;
+        return n_tiles > 0 ? kWork : kNoKeys;
+    }
+
+    __device__ __forceinline__ Row row(const PagedExtendParams &p, int tid) const
+    {
+        const int r = row0 + tid % kRows, in = min(r, rows - 1);
+        Row w;
+        w.live = r < rows;
+        w.t = in / p.group;
+        w.at = static_cast<int64_t>(c0 + w.t) * p.hq + h * p.group + (in - w.t * p.group);
+        return w;
+    }
+};
+
 template <bool kKeySplit>
 __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
     paged_extend_kernel(const __grid_constant__ PagedExtendParams p)
@@ -305,58 +400,35 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
     volatile int *fail = reinterpret_cast<volatile int *>(gbase + S::kOffSlot + 4);
     auto B = [&](int k) { return base + S::kOffBar + 8 * k; };
 
-    const int b = blockIdx.z, h = blockIdx.y;
-    const int row_tiles = static_cast<int>(gridDim.x) / p.splits;
-    const int split = static_cast<int>(blockIdx.x) % p.splits;
-    const int tile = row_tiles - 1 - static_cast<int>(blockIdx.x) / p.splits;   // later rows see more keys: first
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-
-    Chunk c;
-    if (!read_chunk(p, b, c)) {
-        if (tid == 0 && tile == 0 && split == 0 && h == 0)
-            report(p.dev_status, NVFP4KV_DEV_BAD_LEN);
-        return;
-    }
-    const int g = p.group;
-    const int R = c.count * g;
-    const int row0 = tile * S::kRows;
-    if (row0 >= R)
-        return;
-    const int first_pos = c.len - c.count;       // position of chunk token 0; negative when the chunk is longer
-    const int t_last = (min(row0 + S::kRows, R) - 1) / g;
-    const int key_end = max(0, first_pos + t_last + 1);
-    const int key_begin = p.window > 0 ? max(0, first_pos + row0 / g - p.window + 1) : 0;
-    int tile_lo = key_begin / kKeys, n_tiles = 0;
-    if (key_end > key_begin) {
-        const int all = (key_end + kKeys - 1) / kKeys - tile_lo;
-        const int from = static_cast<int>(static_cast<int64_t>(all) * split / p.splits);
-        n_tiles = static_cast<int>(static_cast<int64_t>(all) * (split + 1) / p.splits) - from;
-        tile_lo += from;
-    }
-
-    // this thread's row and block, when it is a softmax thread
-    const int blk = warp >> 2;
-    const int row = row0 + (kKeySplit ? tid % kRowsBlock : tid);
-    const bool has_row = tid < kSoftmaxThreads && row < R;
-    const int t = min(row, R - 1) / g;
-    const int64_t out_row = static_cast<int64_t>(c.c0 + t) * p.hq + h * g + (min(row, R - 1) - t * g);
-    // where the partials go: [split][q_rows][hq][128], then [split][q_rows][hq][2]
-    const int64_t all_rows = static_cast<int64_t>(p.q_rows) * p.hq;
-    float *part_ml = p.partials + all_rows * p.splits * kHeadDim + 2 * (all_rows * split + out_row);
-
-    if (n_tiles <= 0) {
-        // no key of this range is visible to any row
-        if (has_row && p.splits > 1) {
-            part_ml[0] = -INFINITY;
-            part_ml[1] = 0.f;
-        } else if (has_row) {
-            const int words = p.out_f32 ? kHeadDim / 4 : kHeadDim / 8;
-            uint4 *dst = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.out) + out_row * kHeadDim * (p.out_f32 ? 4 : 2));
-            for (int k = 0; k < words; ++k)
-                dst[k] = make_uint4(0, 0, 0, 0);
+    Unit<kKeySplit> only;
+    if constexpr (kKeySplit) {                   // one unit a CTA: what has no keys ends here
+        const int kind = only.open(p, blockIdx.x, tid == 0);
+        if (kind != kWork) {
+            if (kind == kNoKeys && tid < kRowsBlock)
+                only.row(p, tid).nothing(p, only);
+            return;
         }
-        return;
     }
+    // The units of this CTA, one after the other, in turns that reverse (later
+    // rows, which see more keys, have the lower numbers): fn(unit) for each with
+    // keys, until it returns false.
+    auto for_units = [&](auto fn) {
+        if constexpr (kKeySplit)
+            return fn(only);
+        Unit<kKeySplit> u;
+        for (int r = 0; r * static_cast<int64_t>(gridDim.x) < p.units; ++r) {
+            const int64_t idx = static_cast<int64_t>(r) * gridDim.x + ((r & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+            if (idx < p.units) {
+                const int kind = u.open(p, static_cast<int>(idx), warp == S::kLoadWarp && lane == 0);
+                if (kind == kNoKeys && tid < kSoftmaxThreads)
+                    u.row(p, tid).nothing(p, u);
+                if (kind == kWork && !fn(u))
+                    return false;
+            }
+        }
+        return true;
+    };
 
     if (tid == 0) {
         for (int k = 0; k < S::kRaw; ++k) {
@@ -368,14 +440,15 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
             mbar_init(B(S::kVFull + k), kConvThreads / 32);
             mbar_init(B(S::kTurn + k), kKeySplit ? 1 : 2);
         }
-        mbar_init(B(S::kQFull), S::kRows / 32);
         for (int k = 0; k < 2; ++k) {
+            mbar_init(B(S::kQFull + k), kRowsBlock / 32);
             mbar_init(B(S::kSFull + k), 1);
             mbar_init(B(S::kPFull + k), kRowsBlock / 32);
             mbar_init(B(S::kPFull + 2 + k), kRowsBlock / 32);
             mbar_init(B(S::kHalf + k), 1);
             mbar_init(B(S::kDone + k), 1);
             mbar_init(B(S::kGo + k), 1);
+            mbar_init(B(S::kExit + k), 1);
         }
         mbar_init(B(S::kJoin), kRowsBlock / 32);
         *fail = 0;
@@ -389,45 +462,47 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
     const uint32_t tmem = *reinterpret_cast<volatile uint32_t *>(gbase + S::kOffSlot);
 
     if (warp == S::kLoadWarp) {
-        // granules in order; lane l looks up page l % 4 of granule 8 w + l / 4, a
-        // window w ahead
-        const int page_lo = key_begin / kPageSize, page_hi = (key_end + kPageSize - 1) / kPageSize;
-        const int n_grans = n_tiles * kGrans, first_page = tile_lo * (kKeys / kPageSize);
-        const int32_t *table = p.block_table + static_cast<size_t>(b) * p.max_pages;
-        auto lookup = [&](int i) {
-            const int pg = first_page + i * kGranPages + (lane & 3);
-            return i < n_grans && pg >= page_lo && pg < page_hi ? __ldg(table + pg) : 0;
-        };
-        int cur = 0, nxt = lookup(lane >> 2);
+        // granules in order; lane l looks up page l % 4 of a unit's granule 8 w +
+        // l / 4, a window w ahead
         int issued = 0;
-        for (int i = 0; i < n_grans; ++i) {
-            if ((i & 7) == 0) {
-                cur = nxt;
-                nxt = lookup(i + 8 + (lane >> 2));
-                if (static_cast<unsigned>(cur) >= static_cast<unsigned>(p.num_pages)) {
-                    report(p.dev_status, NVFP4KV_DEV_BAD_PAGE);
-                    cur = 0;
+        for_units([&](const Unit<kKeySplit> &u) {
+            const int page_lo = u.key_begin / kPageSize, page_hi = (u.key_end + kPageSize - 1) / kPageSize;
+            const int n_grans = u.n_tiles * kGrans, first_page = u.tile_lo * (kKeys / kPageSize);
+            const int32_t *table = p.block_table + static_cast<size_t>(u.b) * p.max_pages;
+            auto lookup = [&](int i) {
+                const int pg = first_page + i * kGranPages + (lane & 3);
+                return i < n_grans && pg >= page_lo && pg < page_hi ? __ldg(table + pg) : 0;
+            };
+            int cur = 0, nxt = lookup(lane >> 2);
+            for (int i = 0; i < n_grans; ++i, ++issued) {
+                if ((i & 7) == 0) {
+                    cur = nxt;
+                    nxt = lookup(i + 8 + (lane >> 2));
+                    if (static_cast<unsigned>(cur) >= static_cast<unsigned>(p.num_pages)) {
+                        report(p.dev_status, NVFP4KV_DEV_BAD_PAGE);
+                        cur = 0;
+                    }
                 }
+                const int st = issued % S::kRaw;
+                // the stage was last read by the converters kRaw granules ago
+                bool ok = true;
+                if (issued >= S::kRaw)
+                    ok = wait_bar(B(S::kRawEmpty + st), (issued / S::kRaw - 1) & 1, fail, p.dev_status, p.wait_limit);
+                if (!__all_sync(kFullMask, ok))
+                    return false;
+                const int pg0 = first_page + i * kGranPages;
+                const int n = max(0, min(pg0 + kGranPages, page_hi) - max(pg0, page_lo));   // 0: no row sees the granule
+                if (lane == 0)
+                    mbar_arrive_expect_tx(B(S::kRawFull + st), n * kNvfp4Record);
+                __syncwarp();
+                const int pg = pg0 + (lane & 3);
+                if ((lane >> 2) == (i & 7) && pg >= page_lo && pg < page_hi)
+                    bulk_g2s(base + S::kOffRaw + st * kRawBytes + (lane & 3) * kNvfp4Record,
+                             p.pool + (static_cast<size_t>(cur) * p.hkv + u.h) * kNvfp4Record, kNvfp4Record,
+                             B(S::kRawFull + st));
             }
-            const int st = i % S::kRaw;
-            // the stage was last read by the converters for granule i - kRaw
-            bool ok = true;
-            if (i >= S::kRaw)
-                ok = wait_bar(B(S::kRawEmpty + st), (i / S::kRaw - 1) & 1, fail, p.dev_status, p.wait_limit);
-            if (!__all_sync(kFullMask, ok))
-                break;
-            const int pg0 = first_page + i * kGranPages;
-            const int n = max(0, min(pg0 + kGranPages, page_hi) - max(pg0, page_lo));   // 0: no row sees the granule
-            if (lane == 0)
-                mbar_arrive_expect_tx(B(S::kRawFull + st), n * kNvfp4Record);
-            __syncwarp();
-            const int pg = pg0 + (lane & 3);
-            if ((lane >> 2) == (i & 7) && pg >= page_lo && pg < page_hi)
-                bulk_g2s(base + S::kOffRaw + st * kRawBytes + (lane & 3) * kNvfp4Record,
-                         p.pool + (static_cast<size_t>(cur) * p.hkv + h) * kNvfp4Record, kNvfp4Record,
-                         B(S::kRawFull + st));
-            ++issued;
-        }
+            return true;
+        });
         // nothing issued may still be in flight when the CTA exits
         for (int i = max(0, issued - S::kRaw); i < issued; ++i)
             if (!mbar_wait_bounded(B(S::kRawFull + i % S::kRaw), (i / S::kRaw) & 1, kWaitLimit))
@@ -472,38 +547,53 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
             // threads without a rule fell into step, both blocks in their
             // softmax at once.  So the blocks take turns: a block issues when
             // the other one is half through the Q K^T of its own turn.
+            // Batch n of a block (its P V and Q K^T of one tile step) follows batch
+            // n - 1 (block 0) or n (block 1) of the other.  K of the next tile
+            // comes after V of this one from the same converter warps, so one
+            // wait covers both.
             constexpr int step = kKeySplit ? 2 : 1;
-            const int x0 = kKeySplit ? k : 0;
-            const bool turns = !kKeySplit || n_tiles > 1;        // both blocks have tiles
-            // Turn n of a block follows turn n - 1 (block 0) or n (block 1) of the
-            // other.  K of the next tile comes after V of this one from the same
-            // converter warps, so one wait covers both.
-            bool ok = x0 < n_tiles && wait(S::kQFull, 0) && wait(S::kKFull + (x0 & 1), 0) &&
-                      (k == 0 || wait(S::kGo + 1, 0));
-            if (ok)
-                qk(x0);
-            for (int x = x0, i = 0; ok && x < n_tiles; x += step, ++i) {
-                const int next = x + step;
-                const uint32_t p_bar = B(S::kPFull + k), p_par = i & 1;
-                const uint32_t go_bar = turns ? B(S::kGo + k) : p_bar, go_par = turns ? (k == 0 ? i : i + 1) & 1 : p_par;
-                const uint32_t kv_bar = next < n_tiles ? B(S::kKFull + (next & 1)) : B(S::kVFull + (x & 1));
-                const uint32_t kv_par = next < n_tiles ? (next >> 1) & 1 : (x >> 1) & 1;
-                ok = wait_bars(p_bar, p_par, go_bar, go_par, kv_bar, kv_par, fail, p.dev_status, p.wait_limit);
+            int xb = 0, ib = 0, un = 0, batch = 0;       // tiles, the block's tiles, units and batches before
+            for_units([&](const Unit<kKeySplit> &u) {
+                const int n = u.n_tiles, x0 = kKeySplit ? k : 0;
+                if (x0 >= n)
+                    return true;                         // (one tile only: the other block has it)
+                const bool turns = !kKeySplit || n > 1;  // both blocks have tiles
+                const int go_lag = k == 0 ? 1 : 0;
+                bool ok = wait(S::kQFull + (kKeySplit ? 0 : k), un & 1) &&
+                          wait(S::kKFull + ((xb + x0) & 1), ((xb + x0) >> 1) & 1) &&
+                          (!turns || batch < go_lag || wait(S::kGo + k, (batch - go_lag) & 1));
                 if (!ok)
-                    break;
-                pv(x, 0, i > 0);
-                umma_commit(B(S::kHalf + k));
-                if (!(ok = wait(S::kPFull + 2 + k, i & 1)))
-                    break;
-                pv(x, 1, true);
-                if (next < n_tiles)
-                    qk(next);
-                else
-                    mbar_arrive(B(S::kGo + 1 - k));
-            }
+                    return false;
+                qk(xb + x0);
+                ++batch;
+                for (int j = x0, i = ib; j < n; j += step, ++i, ++batch) {
+                    const int x = xb + j, next = x + step;
+                    const bool more = j + step < n;
+                    const uint32_t p_bar = B(S::kPFull + k), p_par = i & 1;
+                    const uint32_t go_bar = turns ? B(S::kGo + k) : p_bar, go_par = turns ? (batch - go_lag) & 1 : p_par;
+                    const uint32_t kv_bar = more ? B(S::kKFull + (next & 1)) : B(S::kVFull + (x & 1));
+                    const uint32_t kv_par = more ? (next >> 1) & 1 : (x >> 1) & 1;
+                    if (!wait_bars(p_bar, p_par, go_bar, go_par, kv_bar, kv_par, fail, p.dev_status, p.wait_limit))
+                        return false;
+                    pv(x, 0, j > x0);
+                    umma_commit(B(S::kHalf + k));
+                    if (!wait(S::kPFull + 2 + k, i & 1))
+                        return false;
+                    pv(x, 1, true);
+                    if (more)
+                        qk(next);
+                    else
+                        mbar_arrive(B(S::kGo + 1 - k));
+                }
+                umma_commit(B(S::kDone + k));
+                xb += n;
+                ib += n;
+                ++un;
+                return true;
+            });
             // nothing of this thread's may still run when tensor memory is freed
-            umma_commit(B(S::kDone + k));
-            if (!mbar_wait_bounded(B(S::kDone + k), 0, kWaitLimit))
+            umma_commit(B(S::kExit + k));
+            if (!mbar_wait_bounded(B(S::kExit + k), 0, kWaitLimit))
                 report(p.dev_status, NVFP4KV_DEV_TIMEOUT);
         }
         __syncwarp();
@@ -564,34 +654,51 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
             warp_arrive(B(S::kVFull + (x & 1)), lane);
             return true;
         };
-        if constexpr (kKeySplit) {
-            // each group makes its block's tiles: V of one and K of the next
-            // between the block's turns (one group for both blocks was what they
-            // waited for: 1.5 us a tile against 1.2)
-            int x = (tid - kSoftmaxThreads) / kConvThreads;
-            bool ok = x < n_tiles && take_k(x);
-            if (ok) {
-                take_v(x);
-                ok = make_k(x);
-            }
-            for (; ok && x < n_tiles; x += 2) {
-                const bool next = x + 2 < n_tiles;
-                ok = (!next || take_k(x + 2)) && make_v(x);
-                if (ok && next) {
-                    take_v(x + 2);
-                    ok = make_k(x + 2);
+        int xb = 0;                              // tiles of the units before
+        for_units([&](const Unit<kKeySplit> &un) {
+            const int n_tiles = un.n_tiles;
+            if constexpr (kKeySplit) {
+                // each group makes its block's tiles: V of one and K of the next
+                // between the block's turns (one group for both blocks was what
+                // they waited for: 1.5 us a tile against 1.2)
+                int x = (tid - kSoftmaxThreads) / kConvThreads;
+                bool ok = x < n_tiles && take_k(x);
+                if (ok) {
+                    take_v(x);
+                    ok = make_k(x);
                 }
+                for (; ok && x < n_tiles; x += 2) {
+                    const bool next = x + 2 < n_tiles;
+                    ok = (!next || take_k(x + 2)) && make_v(x);
+                    if (ok && next) {
+                        take_v(x + 2);
+                        ok = make_k(x + 2);
+                    }
+                }
+            } else {
+                for (int x = xb; x < xb + n_tiles; ++x) {
+                    if (!take_k(x))
+                        return false;
+                    take_v(x);
+                    if (!make_k(x) || !make_v(x))
+                        return false;
+                }
+                xb += n_tiles;
             }
-        } else {
-            for (int x = 0; x < n_tiles && take_k(x); ++x) {
-                take_v(x);
-                if (!make_k(x) || !make_v(x))
-                    break;
-            }
-        }
+            return true;
+        });
     } else {
-        const int r = tid % kRowsBlock;
+        const int blk = warp >> 2, r = tid % kRowsBlock;
         const uint32_t tb = tmem + blk * kTmBlock + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        // the warp leaves together: its tensor-memory accesses are warp-wide
+        auto wait_warp = [&](int k, uint32_t parity) {
+            return __all_sync(kFullMask, wait_bar(B(k), parity, fail, p.dev_status, p.wait_limit));
+        };
+        int ib = 0, un = 0;                      // the block's tiles, and the units, before
+        for_units([&](const Unit<kKeySplit> &u) {
+        const Row row = u.row(p, tid);
+        const bool has_row = row.live;
+        const int64_t out_row = row.at;
         // the row of Q, scaled by a power of two; inv takes scores to log2 units
         float inv;
         {
@@ -606,7 +713,7 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
             }
             const int expo = static_cast<int>(max(m2 & 0xffffu, m2 >> 16) >> 7);          // of the largest |q|
             const int e = min(14 - (expo - 127), 112);
-            const float ks = p.hs.per_head ? p.hs.k[h] : p.gscale;
+            const float ks = p.hs.per_head ? p.hs.k[u.h] : p.gscale;
             inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23) * 256.f * ks * fabsf(p.qscale);
             float sc = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
             sc = p.qscale < 0.f ? -sc : sc;      // scores keep their order: the maximum is taken before inv
@@ -624,24 +731,21 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
                     st_shared128(dst + (k >> 3) * kHalfBytes + (((k & 7u) ^ (r & 7u)) << 4), two(w[k].x), two(w[k].y),
                                  two(w[k].z), two(w[k].w));
                 fence_async_shared();
-                warp_arrive(B(S::kQFull), lane);
+                warp_arrive(B(S::kQFull + blk), lane);
             }
         }
-        const int pos = first_pos + t;           // keys lo .. pos are visible
+        const int pos = u.first_pos + row.t;     // keys lo .. pos are visible
         const int lo = p.window > 0 ? pos - p.window + 1 : 0;
         const uint64_t inv2 = f32x2_pack(inv, inv);
         float m_used = -INFINITY, l = 0.f;
         bool ok = true;
-        // the warp leaves together: its tensor-memory accesses are warp-wide
-        auto wait_warp = [&](int k, uint32_t parity) {
-            return __all_sync(kFullMask, wait_bar(B(k), parity, fail, p.dev_status, p.wait_limit));
-        };
-        const int my_tiles = kKeySplit ? (n_tiles + 1 - blk) / 2 : n_tiles;
-        for (int i = 0; i < my_tiles; ++i) {
+        const int my_tiles = kKeySplit ? (u.n_tiles + 1 - blk) / 2 : u.n_tiles;
+        for (int j = 0; j < my_tiles; ++j) {
+            const int i = ib + j;
             if (!(ok = wait_warp(S::kSFull + blk, i & 1)))
                 break;
             tc_fence_after_sync();
-            const int k0 = (tile_lo + (kKeySplit ? 2 * i + blk : i)) * kKeys;
+            const int k0 = (u.tile_lo + (kKeySplit ? 2 * j + blk : j)) * kKeys;
             const int hi_j = pos + 1 - k0, lo_j = lo - k0;
             // weights of keys 0 .. 63 go over the columns of scores 0 .. 31, of
             // keys 64 .. 127 over those of scores 32 .. 63
@@ -656,7 +760,7 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
                     const float alpha = need ? fast_exp2(m_used - (m_new == -INFINITY ? 0.f : m_new)) : 1.f;
                     m_used = m_new;
                     l *= alpha;
-                    if (i == 0 && hf == 0)
+                    if (j == 0 && hf == 0)
                         return true;             // no O yet
                     // the products before this one have landed: S of this tile
                     // was committed after those of the last tile
@@ -669,8 +773,8 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
                         tmem_ld32(tb + kTmO + 32 * cb, o);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+                        for (int e = 0; e < 32; ++e)
+                            o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
                         tmem_st32(tb + kTmO + 32 * cb, o);
                     }
                     return true;
@@ -701,8 +805,12 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
             if (!ok)
                 break;
         }
+        // (a key-split CTA's second block has no tile, and no end, where there is one tile only)
         if (ok)
-            ok = wait_warp(S::kDone + blk, 0) && (!kKeySplit || wait_warp(S::kDone + 1 - blk, 0));
+            ok = (my_tiles == 0 || wait_warp(S::kDone + blk, un & 1)) &&
+                 (!kKeySplit || u.n_tiles < 2 || wait_warp(S::kDone + 1 - blk, 0));
+        if (kKeySplit && ok && my_tiles == 0)
+            ok = wait_warp(S::kDone, 0);
         tc_fence_after_sync();
         float w0 = 1.f, w1 = 0.f;                // weights of this copy and of the other one
         volatile float *other = reinterpret_cast<volatile float *>(gbase + S::kOffK);    // [130][128 rows]
@@ -734,10 +842,12 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
             }
         }
         if (ok && (!kKeySplit || blk == 0)) {
-            const float vs = (p.hs.per_head ? p.hs.v[h] : p.gscale) * 256.f;
+            const float vs = (p.hs.per_head ? p.hs.v[u.h] : p.gscale) * 256.f;
             const float f = p.splits > 1 ? vs : (l > 0.f ? vs / l : (l == 0.f ? 0.f : l));   // a NaN sum stays NaN
             const float f0 = w0 * f, f1 = w1 * f;
-            float *part_o = p.partials + (all_rows * split + out_row) * kHeadDim;
+            const int64_t all_rows = static_cast<int64_t>(p.q_rows) * p.hq;
+            float *part_o = p.partials + (all_rows * u.split + out_row) * kHeadDim;
+            float *part_ml = row.ml(p, u);
             if (has_row && p.splits > 1) {
                 part_ml[0] = m_used;
                 part_ml[1] = l;
@@ -776,6 +886,10 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
                 }
             }
         }
+        ib += my_tiles;
+        ++un;
+        return ok;
+        });
     }
 
     tc_fence_before_sync();
@@ -870,6 +984,7 @@ ExtendShape paged_extend_shape(int64_t q_rows, int64_t max_q_len, int64_t batch,
     if (n > keys / kMinSplitKeys)
         n = keys / kMinSplitKeys;
     s.splits = static_cast<int>(n < 1 ? 1 : (n > kMaxSplits ? kMaxSplits : n));
+    s.units = s.row_tiles * s.splits * hkv * batch;
     s.workspace = s.splits > 1 ? static_cast<size_t>(s.splits) * q_rows * hkv * group * (kHeadDim + 2) * sizeof(float) : 0;
     return s;
 }
@@ -882,7 +997,10 @@ static cudaError_t launch_blocks(const PagedExtendParams &p, const ExtendShape &
                                                cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
     if (e != cudaSuccess)
         return e;
-    const dim3 grid(static_cast<unsigned>(shape.row_tiles * shape.splits), p.hkv, p.batch);
+    // row blocks: resident CTAs that take unit after unit, so that loads and
+    // conversions for the next run behind the end of the last
+    const int64_t sms = sm_count() > 0 ? sm_count() : 1;
+    const unsigned grid = static_cast<unsigned>(kKeySplit || shape.units < sms ? shape.units : sms);
     paged_extend_kernel<kKeySplit><<<grid, S::kThreads, S::kSmem, s>>>(p);
     return cudaGetLastError();
 }
@@ -891,6 +1009,8 @@ cudaError_t launch_paged_extend(const PagedExtendParams &in, const ExtendShape &
 {
     PagedExtendParams p = in;
     p.splits = shape.splits;
+    p.row_tiles = static_cast<int>(shape.row_tiles);
+    p.units = shape.units;
     const cudaError_t e = shape.key_split ? launch_blocks<true>(p, shape, s) : launch_blocks<false>(p, shape, s);
     if (e != cudaSuccess || shape.splits == 1)
         return e;
