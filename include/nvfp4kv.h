@@ -403,7 +403,8 @@ nvfp4kv_status nvfp4kv_extend_attention_fp8_append(const nvfp4kv_cache *cache,
  *                not initialised (may be NULL when that is 0); two calls in
  *                flight at once must not share it
  * Pointers 16-byte aligned (index arrays 4-byte); out overlaps nothing else.
- * Group g in 1..8, batch and kv heads at most 65535, max_q_len * g below 2^30.
+ * Group g in 1..8, batch at most NVFP4KV_MAX_BATCH, kv heads at most 65535,
+ * max_q_len * g below 2^30.
  * Arithmetic: every cached value is exact in fp16, q too (bf16 significands
  * under a power of two a row; elements under 2^-28 of the row's largest lose
  * bits), scores, softmax and outputs in fp32, softmax weights rounded to fp16
@@ -419,8 +420,8 @@ nvfp4kv_status nvfp4kv_paged_extend(const nvfp4kv_cache *cache, const void *q, c
                                     int32_t *dev_status, nvfp4kv_stream_t stream);
 
 /* Bytes of workspace that nvfp4kv_paged_extend needs with the same sizes on the
- * current device (a library utility; 0 when the keys are not split, and for
- * sizes that the call refuses).  Host only. */
+ * current device (a library utility; 0 for sizes that the call refuses).  Host
+ * only; the result depends on the current device's SM count. */
 size_t nvfp4kv_paged_extend_workspace_size(int32_t q_rows, int32_t max_q_len, int32_t batch, int32_t num_q_heads,
                                            int32_t num_kv_heads, int32_t max_pages_per_seq, int32_t window);
 

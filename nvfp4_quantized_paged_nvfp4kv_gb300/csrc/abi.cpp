@@ -333,7 +333,7 @@ nvfp4kv_status check_paged_extend_sizes(int32_t q_rows, int32_t max_q_len, int32
     if (q_rows < 0 || max_q_len < 0 || batch < 0 || hq <= 0 || hkv <= 0 || max_pages <= 0 || window < 0 || hq % hkv != 0)
         return NVFP4KV_ERR_INVALID_ARG;
     const int64_t group = hq / hkv;
-    if (group > kMaxGroup || hkv > 65535 || batch > 65535 || max_q_len * group >= (int64_t{1} << 30) ||
+    if (group > kMaxGroup || hkv > 65535 || batch > kMaxBatch || max_q_len * group >= (int64_t{1} << 30) ||
         static_cast<int64_t>(max_pages) * kPageSize > (int64_t{1} << 30))
         return NVFP4KV_ERR_UNSUPPORTED;
     return NVFP4KV_OK;
@@ -639,8 +639,6 @@ nvfp4kv_status nvfp4kv_paged_extend(const nvfp4kv_cache *cache, const void *q, c
     const int32_t group = num_q_heads / cache->num_kv_heads;
     const ExtendShape shape = paged_extend_shape(q_rows, max_q_len, batch, cache->num_kv_heads, group, max_pages_per_seq,
                                                  window);
-    if (shape.units > (int64_t{1} << 31) - 1)
-        return NVFP4KV_ERR_UNSUPPORTED;
     if (shape.workspace > 0 && (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
                                 workspace_bytes < shape.workspace))
         return NVFP4KV_ERR_WORKSPACE;

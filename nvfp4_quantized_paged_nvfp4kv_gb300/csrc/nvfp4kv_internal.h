@@ -151,7 +151,7 @@ struct PagedExtendParams {
     const int32_t *block_table;  // [batch][max_pages]
     const int32_t *seq_lens;     // [batch], the chunk's tokens included
     void *out;                   // [q_rows][hq][128], bf16 or fp32
-    float *partials;             // splits > 1: [splits][q_rows][hq][128] O, then [..][2] maximum and sum
+    float *partials;             // workers > 1: two pieces and a note of each CTA (paged_extend.cu)
     int32_t *dev_status;
     int batch;
     int hq;
@@ -162,9 +162,7 @@ struct PagedExtendParams {
     int q_rows;
     int max_q_len;
     int window;                  // 0: none
-    int splits;                  // set by the launcher, as are
-    int row_tiles;               // row tiles a (sequence, kv head) and
-    int64_t units;               // row tiles x splits x kv heads x sequences
+    int workers;                 // CTAs (set by the launcher)
     int out_f32;
     float qscale;                // sm_scale * log2(e)
     float gscale;
@@ -173,13 +171,11 @@ struct PagedExtendParams {
 };
 
 // How a paged extend call is cut: whether a CTA's two MMA blocks share their
-// rows (and halve the keys), row tiles a (sequence, kv head), splits of the
-// keys, and the bytes that the splits leave.
+// rows (and halve the keys), how many CTAs take part, and the bytes of
+// workspace.
 struct ExtendShape {
     bool key_split;
-    int64_t row_tiles;
-    int splits;
-    int64_t units;
+    int workers;
     size_t workspace;
 };
 

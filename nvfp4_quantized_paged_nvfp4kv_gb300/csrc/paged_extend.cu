@@ -42,8 +42,15 @@
 // P is rounded to f16 (relative 2^-11, at most 2^15, its largest at least 1);
 // scores, sums and O are fp32.
 //
-// Few rows and many keys: the keys are split over gridDim.x / tiles CTAs, each
-// leaving its O, maximum and sum in the workspace, which a second kernel joins.
+// Work split.  A unit is a row tile of one sequence and kv head with all its key
+// tiles.  The units' tiles, heads outermost, form one sequence, a unit counting
+// one more for its own cost, which is cut into equal runs, one a resident CTA:
+// no wave is left half empty (2.5 waves of equal units took 3) and few rows
+// with many keys still occupy every SM.  A CTA's run begins and ends inside a
+// unit as a rule: of those it leaves O, reference and sum in the workspace (at
+// most two pieces), which a second kernel joins; the units inside are written
+// directly.  Loads and conversions for the next unit run behind the end of the
+// last.
 #include "tcgen05.cuh"
 
 namespace nvfp4kv {
@@ -84,15 +91,17 @@ struct Shape {
         kRawFull = 0, kRawEmpty = kRawFull + kRaw, kKFull = kRawEmpty + kRaw, kVFull = kKFull + kStages,
         kTurn = kVFull + kStages, kQFull = kTurn + kStages, kSFull = kQFull + 2, kPFull = kSFull + 2, kHalf = kPFull + 4,
         kDone = kHalf + 2,
-kGo = kDone + 2, kExit = kGo + 2, kJoin = kExit + 2, kNumBars = kJoin + 1
+kGo = kDone + 2, kExit = kGo + 2, kJoin = kExit + 2, kFree = kJoin + 1, kNumBars = kFree + 1
     };
-    static constexpr uint32_t kOffSlot = kOffBar + 8 * kNumBars;
-    static constexpr uint32_t kSmem = kOffSlot + 8 + 1024;                   // + slack to align the base
+    static constexpr uint32_t kOffSlot = kOffBar + 8 * kNumBars;             // tensor-memory address, failure flag
+    static constexpr uint32_t kOffRun = (kOffSlot + 8 + 15) / 16 * 16;
+    static constexpr uint32_t kOffMl = kOffRun + 64;                         // key split: the second block's (reference, sum) rows
+    static constexpr uint32_t kSmem = kOffMl + (kKeySplit ? 8 * kRowsBlock : 0) + 1024;                   // + slack to align the base
     // (one CTA an SM: all of tensor memory is its own)
     static_assert(kSmem <= 227 * 1024 && 2 * kSmem > 228 * 1024, "shared memory");
 };
-// the second copy's O, maxima and sums of a key-split CTA take the K and V stages' place
-static_assert((kHeadDim + 2) * kRowsBlock * 4 <= 2 * kStages * kOpBytes, "join area");
+// the sequences' weights, summed up, take the operand stages' place while a CTA looks for its run
+static_assert((kMaxBatch + 1) * 8 <= 2 * kStages * kOpBytes, "weight table");
 
 __device__ __forceinline__ void st_shared128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
 {
@@ -294,99 +303,197 @@ __device__ __forceinline__ float weights_of(const float (&s)[64], uint64_t inv2,
     return f32x2_lo(a) + f32x2_hi(a);
 }
 
-// A unit of work: some rows of one sequence and kv head, and a run of its key
-// tiles.
-enum { kNoRows, kNoKeys, kWork };
-
-struct UnitPlace {
-    int b, h, split;
+// A row tile of one sequence and kv head, and the piece of its key tiles that
+// falls into a CTA's run.
+struct Unit {
+    int b, h, tile;
     int row0, rows;                      // first row, and rows of the sequence and kv head
     int c0, first_pos;                   // row and position of chunk token 0 (negative position: the chunk is longer)
     int key_begin, key_end;              // keys that some row sees
-    int tile_lo, n_tiles;                // its tiles
+    int tile_lo, all;                    // first key tile, and how many
+    int from, n_tiles;                   // the piece: tiles from .. from + n_tiles - 1 of them
+
+    __device__ __forceinline__ bool whole() const { return n_tiles == all; }
+
+    // Row tile `at` of a sequence with rows.
+    template <int kRows>
+    __device__ __forceinline__ void set(const PagedExtendParams &p, const Chunk &c, int at)
+    {
+        tile = at;
+        rows = c.count * p.group;
+        row0 = at * kRows;
+        c0 = c.c0;
+        first_pos = c.len - c.count;
+        const int t_last = (min(row0 + kRows, rows) - 1) / p.group;
+        key_end = max(0, first_pos + t_last + 1);
+        key_begin = p.window > 0 ? max(0, first_pos + row0 / p.group - p.window + 1) : 0;
+        tile_lo = key_begin / kKeys;
+        all = key_end > key_begin ? (key_end + kKeys - 1) / kKeys - tile_lo : 0;
+    }
 };
+
+// Row tiles of a sequence; 0 for one out of bounds.
+template <int kRows>
+__device__ __forceinline__ int row_tiles_of(const PagedExtendParams &p, int b, Chunk &c)
+{
+    return read_chunk(p, b, c) ? (c.count * p.group + kRows - 1) / kRows : 0;
+}
+
+// Where a CTA's run begins, and how much it holds (in tiles and units).
+struct Run {
+    int h, b, tile, off;
+    long long left;
+};
+
+constexpr int kMinRun = 3;               // a run is at least this long, else fewer CTAs take part
+
+// Finds the run of worker `worker` of `workers`; whole CTA.  `table`: batch + 1
+// sums in shared memory.
+template <int kRows>
+__device__ __forceinline__ void find_run(const PagedExtendParams &p, int worker, int workers, long long *table, Run *run)
+{
+    __shared__ long long part[32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    // weights: a group of lanes a sequence, the more lanes the fewer sequences
+    int width = 32;
+    while (width > 1 && blockDim.x / width < p.batch)
+        width >>= 1;
+    const int sub = lane & (width - 1), groups = blockDim.x / width;
+    for (int b0 = 0; b0 < p.batch; b0 += groups) {
+        const int b = b0 + static_cast<int>(threadIdx.x) / width;
+        long long w = 0;
+        if (b < p.batch) {
+            Chunk c;
+            const int n = row_tiles_of<kRows>(p, b, c);
+            if (n == 0 && sub == 0 && worker == 0 && !read_chunk(p, b, c))
+                report(p.dev_status, NVFP4KV_DEV_BAD_LEN);
+            Unit u;
+            for (int i = sub; i < n; i += width) {
+                u.set<kRows>(p, c, i);
+                w += u.all + 1;
+            }
+        }
+        for (int o = 1; o < width; o <<= 1)
+            w += __shfl_xor_sync(kFullMask, w, o);
+        if (b < p.batch && sub == 0)
+            table[b + 1] = w;
+    }
+    if (threadIdx.x == 0)
+        table[0] = 0;
+    __syncthreads();
+    // their running sum
+    long long carry = 0;
+    for (int b0 = 0; b0 < p.batch; b0 += blockDim.x) {
+        const int b = b0 + threadIdx.x;
+        long long x = b < p.batch ? table[b + 1] : 0;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(kFullMask, x, o);
+            if (lane >= o)
+                x += y;
+        }
+        if (lane == 31)
+            part[warp] = x;
+        __syncthreads();
+        long long total = 0, before = carry;
+        for (int k = 0; k < warps; ++k) {
+            before += k < warp ? part[k] : 0;
+            total += part[k];
+        }
+        if (b < p.batch)
+            table[b + 1] = before + x;
+        carry += total;
+        __syncthreads();
+    }
+    if (warp == 0) {
+        const long long head = table[p.batch], all = head * p.hkv;
+        const long long use = min(static_cast<long long>(workers), max(1LL, all / kMinRun));
+        Run r{};
+        if (worker < use) {
+            const long long lo = all * worker / use, hi = all * (worker + 1) / use;
+            r.left = hi - lo;
+            if (r.left > 0) {
+                r.h = static_cast<int>(lo / head);
+                long long at = lo - r.h * head;
+                int x = 0, y = p.batch;              // the last sequence that begins at or before `at`
+                while (y - x > 1) {
+                    const int mid = (x + y) >> 1;
+                    if (table[mid] <= at)
+                        x = mid;
+                    else
+                        y = mid;
+                }
+                r.b = x;
+                at -= table[x];
+                Chunk c;
+                const int n = row_tiles_of<kRows>(p, x, c);
+                for (int i0 = 0; i0 < n; i0 += 32) {
+                    Unit u;
+                    int w = 0;
+                    if (i0 + lane < n) {
+                        u.set<kRows>(p, c, i0 + lane);
+                        w = u.all + 1;
+                    }
+                    long long incl = w;
+#pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const long long v = __shfl_up_sync(kFullMask, incl, o);
+                        if (lane >= o)
+                            incl += v;
+                    }
+                    const unsigned past = __ballot_sync(kFullMask, i0 + lane < n && incl > at);
+                    if (past) {
+                        const int hit = __ffs(past) - 1;
+                        r.tile = i0 + hit;
+                        r.off = static_cast<int>(at - __shfl_sync(kFullMask, incl - w, hit));
+                        break;
+                    }
+                    at -= __shfl_sync(kFullMask, incl, 31);
+                }
+            }
+        }
+        if (lane == 0)
+            *run = r;
+    }
+    __syncthreads();
+}
 
 // A softmax thread's row.
 struct Row {
     bool live;
     int t;                               // chunk token
     int64_t at;                          // row of q and out, in heads
-
-    // the row's maximum and sum in the workspace: [split][q_rows][hq][2] behind
-    // [split][q_rows][hq][128]
-    __device__ __forceinline__ float *ml(const PagedExtendParams &p, const UnitPlace &u) const
-    {
-        const int64_t all = static_cast<int64_t>(p.q_rows) * p.hq;
-        return p.partials + all * p.splits * kHeadDim + 2 * (all * u.split + at);
-    }
-
-    // what a row leaves that sees no key of the unit
-    __device__ __forceinline__ void nothing(const PagedExtendParams &p, const UnitPlace &u) const
-    {
-        if (!live)
-            return;
-        if (p.splits > 1) {
-            float *d = ml(p, u);
-            d[0] = -INFINITY;
-            d[1] = 0.f;
-            return;
-        }
-        const int words = p.out_f32 ? kHeadDim / 4 : kHeadDim / 8;
-        uint4 *d = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.out) + at * kHeadDim * (p.out_f32 ? 4 : 2));
-        for (int k = 0; k < words; ++k)
-            d[k] = make_uint4(0, 0, 0, 0);
-    }
 };
 
-template <bool kKeySplit>
-struct Unit : UnitPlace {
-    static constexpr int kRows = Shape<kKeySplit>::kRows;
+template <int kRows>
+__device__ __forceinline__ Row row_of(const PagedExtendParams &p, const Unit &u, int tid)
+{
+    const int r = u.row0 + tid % kRows, in = min(r, u.rows - 1);
+    Row w;
+    w.live = r < u.rows;
+    w.t = in / p.group;
+    w.at = static_cast<int64_t>(u.c0 + w.t) * p.hq + u.h * p.group + (in - w.t * p.group);
+    return w;
+}
 
-    // Unit idx of p.units: splits innermost, then kv heads, sequences, row tiles
-    // from the last; `rep`: this thread reports a sequence out of bounds.
-    __device__ __forceinline__ int open(const PagedExtendParams &p, int idx, bool rep)
-    {
-        split = idx % p.splits;
-        idx /= p.splits;
-        h = idx % p.hkv;
-        idx /= p.hkv;
-        b = idx % p.batch;
-        const int tile = p.row_tiles - 1 - idx / p.batch;
-        Chunk c;
-        if (!read_chunk(p, b, c)) {
-            if (rep && tile == 0 && split == 0 && h == 0)
-                report(p.dev_status, NVFP4KV_DEV_BAD_LEN);
-            return kNoRows;
-        }
-        rows = c.count * p.group;
-        row0 = tile * kRows;
-        if (row0 >= rows)
-            return kNoRows;
-        c0 = c.c0;
-        first_pos = c.len - c.count;
-        const int t_last = (min(row0 + kRows, rows) - 1) / p.group;
-        key_end = max(0, first_pos + t_last + 1);
-        key_begin = p.window > 0 ? max(0, first_pos + row0 / p.group - p.window + 1) : 0;
-        if (key_end <= key_begin)
-            return kNoKeys;
-        tile_lo = key_begin / kKeys;
-        const int all = (key_end + kKeys - 1) / kKeys - tile_lo;
-        const int from = static_cast<int>(static_cast<int64_t>(all) * split / p.splits);
-        n_tiles = static_cast<int>(static_cast<int64_t>(all) * (split + 1) / p.splits) - from;
-        tile_lo += from;
-        return n_tiles > 0 ? kWork : kNoKeys;
-    }
+// The workspace: for each CTA two pieces of (O [rows][128], then (reference,
+// sum) [rows]) -- the one that begins inside its unit and the one that begins
+// with it but does not end it -- and then a note of each CTA.
+template <int kRows>
+constexpr size_t kPieceFloats = static_cast<size_t>(kRows) * (kHeadDim + 2);
 
-    __device__ __forceinline__ Row row(const PagedExtendParams &p, int tid) const
-    {
-        const int r = row0 + tid % kRows, in = min(r, rows - 1);
-        Row w;
-        w.live = r < rows;
-        w.t = in / p.group;
-        w.at = static_cast<int64_t>(c0 + w.t) * p.hq + h * p.group + (in - w.t * p.group);
-        return w;
-    }
+struct Note {
+    int tail;                            // 1: the second piece is there, of the rows below
+    int h, row0, rows, c0;
+    int head;                            // 1: the first piece is there, 2: and it ends its unit
+    int pad[2];
 };
+
+template <int kRows>
+__device__ __forceinline__ Note *notes_of(const PagedExtendParams &p)
+{
+    return reinterpret_cast<Note *>(p.partials + 2 * kPieceFloats<kRows> * p.workers);
+}
 
 template <bool kKeySplit>
 __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
@@ -401,30 +508,42 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
     auto B = [&](int k) { return base + S::kOffBar + 8 * k; };
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    Unit<kKeySplit> only;
-    if constexpr (kKeySplit) {                   // one unit a CTA: what has no keys ends here
-        const int kind = only.open(p, blockIdx.x, tid == 0);
-        if (kind != kWork) {
-            if (kind == kNoKeys && tid < kRowsBlock)
-                only.row(p, tid).nothing(p, only);
-            return;
-        }
-    }
-    // The units of this CTA, one after the other, in turns that reverse (later
-    // rows, which see more keys, have the lower numbers): fn(unit) for each with
+    constexpr int kRows = S::kRows;
+    Run *run = reinterpret_cast<Run *>(gbase + S::kOffRun);
+    find_run<kRows>(p, blockIdx.x, gridDim.x, reinterpret_cast<long long *>(gbase + S::kOffK), run);
+    const Run start = *run;
+    // The units of this CTA's run, one after the other: fn(unit) for each with
     // keys, until it returns false.
     auto for_units = [&](auto fn) {
-        if constexpr (kKeySplit)
-            return fn(only);
-        Unit<kKeySplit> u;
-        for (int r = 0; r * static_cast<int64_t>(gridDim.x) < p.units; ++r) {
-            const int64_t idx = static_cast<int64_t>(r) * gridDim.x + ((r & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-            if (idx < p.units) {
-                const int kind = u.open(p, static_cast<int>(idx), warp == S::kLoadWarp && lane == 0);
-                if (kind == kNoKeys && tid < kSoftmaxThreads)
-                    u.row(p, tid).nothing(p, u);
-                if (kind == kWork && !fn(u))
+        Unit u{};
+        u.h = start.h;
+        u.b = start.b;
+        int at = start.tile, off = start.off;
+        for (long long left = start.left; left > 0 && u.h < p.hkv;) {
+            Chunk c;
+            const int n = row_tiles_of<kRows>(p, u.b, c);
+            for (; at < n && left > 0; ++at, off = 0) {
+                u.set<kRows>(p, c, at);
+                // place 0 of a unit is its own cost, place 1 + i key tile i
+                const int take = static_cast<int>(min(left, static_cast<long long>(u.all + 1 - off)));
+                u.from = max(0, off - 1);
+                u.n_tiles = max(0, off + take - 1) - u.from;
+                left -= take;
+                if (u.all == 0 && tid < kRows) {
+                    // rows that see no key
+                    const Row row = row_of<kRows>(p, u, tid);
+                    const int words = p.out_f32 ? kHeadDim / 4 : kHeadDim / 8;
+                    uint4 *d = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.out) + row.at * kHeadDim * (p.out_f32 ? 4 : 2));
+                    for (int k = 0; row.live && k < words; ++k)
+                        d[k] = make_uint4(0, 0, 0, 0);
+                }
+                if (u.n_tiles > 0 && !fn(u))
                     return false;
+            }
+            at = off = 0;
+            if (++u.b == p.batch) {
+                u.b = 0;
+                ++u.h;
             }
         }
         return true;
@@ -451,7 +570,12 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
             mbar_init(B(S::kExit + k), 1);
         }
         mbar_init(B(S::kJoin), kRowsBlock / 32);
+        mbar_init(B(S::kFree), kRowsBlock / 32);
         *fail = 0;
+        if (p.workers > 1) {
+            Note *note = notes_of<kRows>(p) + blockIdx.x;
+            note->tail = note->head = 0;
+        }
         fence_mbar_init();
     }
     if (warp == S::kMmaWarp)
@@ -465,9 +589,9 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
         // granules in order; lane l looks up page l % 4 of a unit's granule 8 w +
         // l / 4, a window w ahead
         int issued = 0;
-        for_units([&](const Unit<kKeySplit> &u) {
+        for_units([&](const Unit &u) {
             const int page_lo = u.key_begin / kPageSize, page_hi = (u.key_end + kPageSize - 1) / kPageSize;
-            const int n_grans = u.n_tiles * kGrans, first_page = u.tile_lo * (kKeys / kPageSize);
+            const int n_grans = u.n_tiles * kGrans, first_page = (u.tile_lo + u.from) * (kKeys / kPageSize);
             const int32_t *table = p.block_table + static_cast<size_t>(u.b) * p.max_pages;
             auto lookup = [&](int i) {
                 const int pg = first_page + i * kGranPages + (lane & 3);
@@ -518,12 +642,12 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
             };
             // S of tile x; then turn x, which frees K of tile x and V of the
             // block's tile before it.  (One commit for both.)
-            auto qk = [&](int x) {
+            auto qk = [&](int x, bool turns) {
                 const uint32_t kb = base + S::kOffK + (x & 1) * kOpBytes;
                 tc_fence_after_sync();
 #pragma unroll
                 for (int s = 0; s < 8; ++s) {
-                    if (s == 4)
+                    if (s == 4 && turns)
                         mbar_arrive(B(S::kGo + 1 - k));
                     const uint32_t off = (s >> 2) * kHalfBytes + (s & 3) * 32;
                     umma_f16(tb + kTmS, smem_desc(qb + off, 16, 1024), smem_desc(kb + off, 16, 1024), idesc, s > 0);
@@ -551,44 +675,55 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
             // n - 1 (block 0) or n (block 1) of the other.  K of the next tile
             // comes after V of this one from the same converter warps, so one
             // wait covers both.
+            // A tile's number x counts the CTA's tiles (row blocks), or twice the
+            // block's own, plus the block (key split): its stage is x mod 2.
             constexpr int step = kKeySplit ? 2 : 1;
-            int xb = 0, ib = 0, un = 0, batch = 0;       // tiles, the block's tiles, units and batches before
-            for_units([&](const Unit<kKeySplit> &u) {
-                const int n = u.n_tiles, x0 = kKeySplit ? k : 0;
-                if (x0 >= n)
-                    return true;                         // (one tile only: the other block has it)
-                const bool turns = !kKeySplit || n > 1;  // both blocks have tiles
-                const int go_lag = k == 0 ? 1 : 0;
-                bool ok = wait(S::kQFull + (kKeySplit ? 0 : k), un & 1) &&
-                          wait(S::kKFull + ((xb + x0) & 1), ((xb + x0) >> 1) & 1) &&
-                          (!turns || batch < go_lag || wait(S::kGo + k, (batch - go_lag) & 1));
-                if (!ok)
+            int ib = 0, un = 0, batch = 0;               // the block's tiles, units and batches so far
+            const int go_lag = k == 0 ? 1 : 0;
+            for_units([&](const Unit &u) {
+                const int mine = kKeySplit ? (u.n_tiles + 1 - k) / 2 : u.n_tiles;
+                const bool turns = !kKeySplit || u.n_tiles > 1;          // both blocks have tiles
+                auto number = [&](int i) { return kKeySplit ? 2 * i + k : i; };
+                auto go = [&]() { return !turns || batch < go_lag || wait(S::kGo + k, (batch - go_lag) & 1); };
+                // (every phase is waited for, also by a block without tiles)
+                if (!wait(S::kQFull + (kKeySplit ? 0 : k), un++ & 1))
                     return false;
-                qk(xb + x0);
-                ++batch;
-                for (int j = x0, i = ib; j < n; j += step, ++i, ++batch) {
-                    const int x = xb + j, next = x + step;
-                    const bool more = j + step < n;
+                if (mine == 0)
+                    return true;
+                const int x0 = number(ib);
+                if (!wait(S::kKFull + (x0 & 1), (x0 >> 1) & 1) || !go())
+                    return false;
+                qk(x0, turns);
+                batch += turns;
+                for (int j = 0; j < mine; ++j, batch += turns) {
+                    const int i = ib + j, x = number(i), next = x + step;
+                    const bool more = j + 1 < mine;
                     const uint32_t p_bar = B(S::kPFull + k), p_par = i & 1;
-                    const uint32_t go_bar = turns ? B(S::kGo + k) : p_bar, go_par = turns ? (batch - go_lag) & 1 : p_par;
+                    const bool waits = turns && batch >= go_lag;
+                    const uint32_t go_bar = waits ? B(S::kGo + k) : p_bar, go_par = waits ? (batch - go_lag) & 1 : p_par;
                     const uint32_t kv_bar = more ? B(S::kKFull + (next & 1)) : B(S::kVFull + (x & 1));
                     const uint32_t kv_par = more ? (next >> 1) & 1 : (x >> 1) & 1;
                     if (!wait_bars(p_bar, p_par, go_bar, go_par, kv_bar, kv_par, fail, p.dev_status, p.wait_limit))
                         return false;
-                    pv(x, 0, j > x0);
+                    pv(x, 0, j > 0);
                     umma_commit(B(S::kHalf + k));
                     if (!wait(S::kPFull + 2 + k, i & 1))
                         return false;
                     pv(x, 1, true);
                     if (more)
-                        qk(next);
-                    else
+                        qk(next, turns);
+                    else if (turns)
                         mbar_arrive(B(S::kGo + 1 - k));
                 }
                 umma_commit(B(S::kDone + k));
-                xb += n;
-                ib += n;
-                ++un;
+                ib += mine;
+                if (kKeySplit && turns && k == 1 && (u.n_tiles & 1)) {
+                    // the other block had a tile more: a batch without work keeps the turns even
+                    if (!go())
+                        return false;
+                    mbar_arrive(B(S::kGo + 1 - k));
+                    ++batch;
+                }
                 return true;
             });
             // nothing of this thread's may still run when tensor memory is freed
@@ -606,30 +741,32 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
         // most kStages behind the last one done: its barrier has not come
         // round again)
         auto wait_turn = [&](int x) { return wait_warp(S::kTurn + (x & 1), (x >> 1) & 1); };
+        // tiles by their number x (see the MMA warps), granules by the place y of
+        // their tile in the CTA's run
         auto stage = [&](int gr) { return base + S::kOffRaw + gr % S::kRaw * kRawBytes; };
         // A tile's bytes go to registers as soon as they are there, so that the
         // ring's stages are free for the copies to come while conversions wait
         // for their operand stages.
         RawK kx[kGrans];
         RawV vx[kGrans];
-        auto take_k = [&](int x) {
+        auto take_k = [&](int y) {
 #pragma unroll
             for (int u = 0; u < kGrans; ++u) {
-                const int gr = x * kGrans + u;
+                const int gr = y * kGrans + u;
                 if (!wait_warp(S::kRawFull + gr % S::kRaw, (gr / S::kRaw) & 1))
                     return false;
                 load_k(stage(gr), pt, kx[u]);
             }
             return true;
         };
-        auto take_v = [&](int x) {
+        auto take_v = [&](int y) {
 #pragma unroll
             for (int u = 0; u < kGrans; ++u)
-                load_v(stage(x * kGrans + u), pt, vx[u]);
+                load_v(stage(y * kGrans + u), pt, vx[u]);
             fence_async_shared();                // the reads before the stages' next copies
 #pragma unroll
             for (int u = 0; u < kGrans; ++u)
-                warp_arrive(B(S::kRawEmpty + (x * kGrans + u) % S::kRaw), lane);
+                warp_arrive(B(S::kRawEmpty + (y * kGrans + u) % S::kRaw), lane);
         };
         // K of tile x: its stage was last read in the turn of tile x - 2
         auto make_k = [&](int x) {
@@ -654,38 +791,41 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
             warp_arrive(B(S::kVFull + (x & 1)), lane);
             return true;
         };
-        int xb = 0;                              // tiles of the units before
-        for_units([&](const Unit<kKeySplit> &un) {
-            const int n_tiles = un.n_tiles;
+        int yb = 0, ib = 0;                      // the CTA's tiles, and the group's, so far
+        for_units([&](const Unit &u) {
             if constexpr (kKeySplit) {
                 // each group makes its block's tiles: V of one and K of the next
                 // between the block's turns (one group for both blocks was what
                 // they waited for: 1.5 us a tile against 1.2)
-                int x = (tid - kSoftmaxThreads) / kConvThreads;
-                bool ok = x < n_tiles && take_k(x);
-                if (ok) {
-                    take_v(x);
+                const int k = (tid - kSoftmaxThreads) / kConvThreads;
+                int y = yb + k, x = 2 * ib + k;
+                const int end = yb + u.n_tiles;
+                bool ok = y >= end || take_k(y);
+                if (ok && y < end) {
+                    take_v(y);
                     ok = make_k(x);
                 }
-                for (; ok && x < n_tiles; x += 2) {
-                    const bool next = x + 2 < n_tiles;
-                    ok = (!next || take_k(x + 2)) && make_v(x);
+                for (; ok && y < end; y += 2, x += 2, ++ib) {
+                    const bool next = y + 2 < end;
+                    ok = (!next || take_k(y + 2)) && make_v(x);
                     if (ok && next) {
-                        take_v(x + 2);
+                        take_v(y + 2);
                         ok = make_k(x + 2);
                     }
                 }
+                yb = end;
+                return ok;
             } else {
-                for (int x = xb; x < xb + n_tiles; ++x) {
-                    if (!take_k(x))
+                const int end = yb + u.n_tiles;
+                for (; yb < end; ++yb) {
+                    if (!take_k(yb))
                         return false;
-                    take_v(x);
-                    if (!make_k(x) || !make_v(x))
+                    take_v(yb);
+                    if (!make_k(yb) || !make_v(yb))
                         return false;
                 }
-                xb += n_tiles;
+                return true;
             }
-            return true;
         });
     } else {
         const int blk = warp >> 2, r = tid % kRowsBlock;
@@ -694,9 +834,10 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
         auto wait_warp = [&](int k, uint32_t parity) {
             return __all_sync(kFullMask, wait_bar(B(k), parity, fail, p.dev_status, p.wait_limit));
         };
-        int ib = 0, un = 0;                      // the block's tiles, and the units, before
-        for_units([&](const Unit<kKeySplit> &u) {
-        const Row row = u.row(p, tid);
+        int ib = 0, un = 0, dn = 0;              // the block's tiles, units, and units with tiles, so far
+        float2 *second = reinterpret_cast<float2 *>(gbase + S::kOffMl);
+        for_units([&](const Unit &u) {
+        const Row row = row_of<kRows>(p, u, tid);
         const bool has_row = row.live;
         const int64_t out_row = row.at;
         // the row of Q, scaled by a power of two; inv takes scores to log2 units
@@ -740,12 +881,16 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
         float m_used = -INFINITY, l = 0.f;
         bool ok = true;
         const int my_tiles = kKeySplit ? (u.n_tiles + 1 - blk) / 2 : u.n_tiles;
-        for (int j = 0; j < my_tiles; ++j) {
+        // the first block reads the second one's O at the end of a unit: that
+        // must be over before the next weights bring the next O
+        if (kKeySplit && blk == 1 && un > 0)
+            ok = wait_warp(S::kFree, (un - 1) & 1);
+        for (int j = 0; ok && j < my_tiles; ++j) {
             const int i = ib + j;
             if (!(ok = wait_warp(S::kSFull + blk, i & 1)))
                 break;
             tc_fence_after_sync();
-            const int k0 = (u.tile_lo + (kKeySplit ? 2 * j + blk : j)) * kKeys;
+            const int k0 = (u.tile_lo + u.from + (kKeySplit ? 2 * j + blk : j)) * kKeys;
             const int hi_j = pos + 1 - k0, lo_j = lo - k0;
             // weights of keys 0 .. 63 go over the columns of scores 0 .. 31, of
             // keys 64 .. 127 over those of scores 32 .. 63
@@ -805,71 +950,70 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
             if (!ok)
                 break;
         }
-        // (a key-split CTA's second block has no tile, and no end, where there is one tile only)
-        if (ok)
-            ok = (my_tiles == 0 || wait_warp(S::kDone + blk, un & 1)) &&
-                 (!kKeySplit || u.n_tiles < 2 || wait_warp(S::kDone + 1 - blk, 0));
-        if (kKeySplit && ok && my_tiles == 0)
-            ok = wait_warp(S::kDone, 0);
-        tc_fence_after_sync();
-        float w0 = 1.f, w1 = 0.f;                // weights of this copy and of the other one
-        volatile float *other = reinterpret_cast<volatile float *>(gbase + S::kOffK);    // [130][128 rows]
-        if (kKeySplit) {
-            // (both blocks' MMAs are done: the K and V stages are free)
-            if (ok && blk == 1) {
-                if (my_tiles > 0) {
-#pragma unroll
-                    for (int cb = 0; cb < 4; ++cb) {
-                        uint32_t o[32];
-                        tmem_ld32(tb + kTmO + 32 * cb, o);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            other[(32 * cb + j) * kRowsBlock + r] = __uint_as_float(o[j]);
-                    }
+        // The block's products have landed; with split keys the first block, which
+        // puts both together, also waits for the second one's.
+        if (ok && my_tiles > 0)
+            ok = wait_warp(S::kDone + blk, dn++ & 1);
+        float w0 = 1.f, w1 = 0.f;                // weights of this block's O and of the other's
+        if constexpr (kKeySplit) {
+            if (blk == 1) {
+                if (ok) {
+                    second[r] = make_float2(m_used, l);
+                    tc_fence_before_sync();
+                    warp_arrive(B(S::kJoin), lane);      // (after the wait for its products)
                 }
-                other[kHeadDim * kRowsBlock + r] = m_used;
-                other[(kHeadDim + 1) * kRowsBlock + r] = l;
-                warp_arrive(B(S::kJoin), lane);
-            }
-            if (ok && blk == 0 && (ok = wait_warp(S::kJoin, 0))) {
-                const float m1 = other[kHeadDim * kRowsBlock + r], l1 = other[(kHeadDim + 1) * kRowsBlock + r];
-                const float M = fmaxf(m_used, m1);
+            } else if (ok && (ok = wait_warp(S::kJoin, un & 1))) {
+                const float2 o = second[r];
+                const float M = fmaxf(m_used, o.x);
                 w0 = m_used == -INFINITY ? 0.f : fast_exp2(m_used - M);
-                w1 = m1 == -INFINITY ? 0.f : fast_exp2(m1 - M);
-                l = (l != l || l1 != l1) ? NAN : l * w0 + l1 * w1;
+                w1 = o.x == -INFINITY ? 0.f : fast_exp2(o.x - M);
+                l = (l != l || o.y != o.y) ? NAN : l * w0 + o.y * w1;
                 m_used = M;
             }
         }
+        tc_fence_after_sync();
         if (ok && (!kKeySplit || blk == 0)) {
             const float vs = (p.hs.per_head ? p.hs.v[u.h] : p.gscale) * 256.f;
-            const float f = p.splits > 1 ? vs : (l > 0.f ? vs / l : (l == 0.f ? 0.f : l));   // a NaN sum stays NaN
+            const bool whole = u.whole();
+            const float f = !whole ? vs : (l > 0.f ? vs / l : (l == 0.f ? 0.f : l));   // a NaN sum stays NaN
             const float f0 = w0 * f, f1 = w1 * f;
-            const int64_t all_rows = static_cast<int64_t>(p.q_rows) * p.hq;
-            float *part_o = p.partials + (all_rows * u.split + out_row) * kHeadDim;
-            float *part_ml = row.ml(p, u);
-            if (has_row && p.splits > 1) {
-                part_ml[0] = m_used;
-                part_ml[1] = l;
+            const int piece = 2 * blockIdx.x + (u.from > 0 ? 0 : 1), rr = tid % kRows;
+            float *part = p.partials + kPieceFloats<kRows> * piece;
+            if (has_row && !whole)
+                reinterpret_cast<float2 *>(part + kRows * kHeadDim)[rr] = make_float2(m_used, l);
+            if (!whole && tid == 0) {
+                Note *note = notes_of<kRows>(p) + blockIdx.x;
+                if (u.from > 0) {
+                    note->head = u.from + u.n_tiles == u.all ? 2 : 1;
+                } else {
+                    note->h = u.h;
+                    note->row0 = u.row0;
+                    note->rows = u.rows;
+                    note->c0 = u.c0;
+                    note->tail = 1;
+                }
             }
-#pragma unroll
+#pragma unroll 1
             for (int cb = 0; cb < 4; ++cb) {
                 uint32_t w[32];
+                float o[32];
                 tmem_ld32(tb + kTmO + 32 * cb, w);
                 tmem_wait_ld();
-                if (!has_row)
-                    continue;
-                float o[32];
 #pragma unroll
                 for (int j = 0; j < 32; ++j)
                     o[j] = __uint_as_float(w[j]) * f0;
-                if (kKeySplit && f1 != 0.f) {
+                if constexpr (kKeySplit) {
+                    // (the second block's columns of the same lanes; nothing there without its tiles)
+                    tmem_ld32(tb + kTmBlock + kTmO + 32 * cb, w);
+                    tmem_wait_ld();
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
-                        o[j] = fmaf(other[(32 * cb + j) * kRowsBlock + r], f1, o[j]);
+                        o[j] = w1 != 0.f ? fmaf(__uint_as_float(w[j]), f1, o[j]) : o[j];
                 }
-                if (p.splits > 1 || p.out_f32) {
-                    float *row_f = p.splits > 1 ? part_o : static_cast<float *>(p.out) + out_row * kHeadDim;
+                if (!has_row)
+                    continue;
+                if (!whole || p.out_f32) {
+                    float *row_f = !whole ? part + rr * kHeadDim : static_cast<float *>(p.out) + out_row * kHeadDim;
                     float4 *dst = reinterpret_cast<float4 *>(row_f + 32 * cb);
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
@@ -884,6 +1028,10 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
                     for (int k = 0; k < 4; ++k)
                         dst[k] = make_uint4(bf2(8 * k), bf2(8 * k + 2), bf2(8 * k + 4), bf2(8 * k + 6));
                 }
+            }
+            if (kKeySplit) {
+                tc_fence_before_sync();
+                warp_arrive(B(S::kFree), lane);
             }
         }
         ib += my_tiles;
@@ -900,72 +1048,85 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
     }
 }
 
-// Joins the splits of each row: with M = max_s m_s,
-//   o = sum_s 2^(m_s - M) O_s / sum_s 2^(m_s - M) l_s.
-// One warp a (token, query head), four channels a lane.  Rows that no split saw
-// a key for get zeros; a split without keys left no O and is not read.
+// Joins the pieces of the units that CTA blockIdx.x began and did not end: with
+// reference m_j and sum l_j of piece j, M = max_j m_j,
+//   o = sum_j 2^(m_j - M) O_j / sum_j 2^(m_j - M) l_j.
+// The pieces are the CTA's own second one and the first ones of the CTAs after
+// it, up to the one that ends the unit.  One warp a row, four channels a lane.
+template <int kRows>
 __global__ void __launch_bounds__(256) paged_extend_join_kernel(const __grid_constant__ PagedExtendParams p)
 {
     pdl_wait();
-    const int b = blockIdx.y, lane = threadIdx.x & 31;
-    Chunk c;
-    if (!read_chunk(p, b, c))
+    const int lane = threadIdx.x & 31, first = blockIdx.x;
+    const Note *notes = notes_of<kRows>(p);
+    if (!__ldcg(&notes[first].tail))
         return;
-    const int64_t n = static_cast<int64_t>(c.count) * p.hq;
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
-    if (i >= n)
+    const int rr = blockIdx.y * 8 + (threadIdx.x >> 5), row = __ldcg(&notes[first].row0) + rr;
+    if (row >= __ldcg(&notes[first].rows))
         return;
-    const int64_t all_rows = static_cast<int64_t>(p.q_rows) * p.hq, row = static_cast<int64_t>(c.c0) * p.hq + i;
-    const float *ml = p.partials + all_rows * p.splits * kHeadDim;
-    // lane s holds split s's maximum and sum (at most 32 splits)
-    float m = -INFINITY, l = 0.f;
-    if (lane < p.splits) {
-        const float2 v = __ldcg(reinterpret_cast<const float2 *>(ml) + all_rows * lane + row);
-        m = v.x;
-        l = v.y;
-    }
-    float M = m;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        M = fmaxf(M, __shfl_xor_sync(kFullMask, M, o));
-    const float w = m == -INFINITY ? 0.f : fast_exp2(m - M);
-    float den = w * l;
-    if (m == -INFINITY && l != l)
-        den = l;                                 // a row of NaN scores stays NaN
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        den += __shfl_xor_sync(kFullMask, den, o);
+    float M = -INFINITY, den = 0.f;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    bool last = false;
+    for (int j0 = first; !last && j0 < p.workers; j0 += 32) {
+        // lane i: piece j0 + i, if the unit reaches that far
+        const int j = j0 + lane;
+        const int head = j > first && j < p.workers ? __ldcg(&notes[j].head) : (j == first ? 1 : 0);
+        const unsigned stop = __ballot_sync(kFullMask, head != 1);       // 2 ends it; 0 does not occur before that
+        const int n = stop ? __ffs(stop) - 1 + (__shfl_sync(kFullMask, head, __ffs(stop) - 1) == 2) : 32;
+        last = stop != 0;
+        float m = -INFINITY, l = 0.f;
+        const size_t piece = kPieceFloats<kRows> * (2 * static_cast<size_t>(j) + (j == first));
+        if (lane < n) {
+            const float2 v = __ldcg(reinterpret_cast<const float2 *>(p.partials + piece + kRows * kHeadDim) + rr);
+            m = v.x;
+            l = v.y;
+        }
+        float top = m;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            top = fmaxf(top, __shfl_xor_sync(kFullMask, top, o));
+        top = fmaxf(top, M);
+        const float old = M == -INFINITY ? 0.f : fast_exp2(M - top);
+        const float w = m == -INFINITY ? 0.f : fast_exp2(m - top);
+        float add = (m == -INFINITY && l != l) ? l : w * l;              // a row of NaN scores stays NaN
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+            add += __shfl_xor_sync(kFullMask, add, o);
+        den = den * old + add;
+        acc = make_float4(acc.x * old, acc.y * old, acc.z * old, acc.w * old);
+        M = top;
 #pragma unroll 4
-    for (int s = 0; s < p.splits; ++s) {
-        const float ws = __shfl_sync(kFullMask, w, s);
-        if (ws == 0.f)
-            continue;
-        const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.partials + (all_rows * s + row) * kHeadDim) + lane);
-        acc.x += ws * v.x;
-        acc.y += ws * v.y;
-        acc.z += ws * v.z;
-        acc.w += ws * v.w;
+        for (int i = 0; i < n; ++i) {
+            const float wi = __shfl_sync(kFullMask, w, i);
+            const size_t at = kPieceFloats<kRows> * (2 * static_cast<size_t>(j0 + i) + (j0 + i == first)) +
+                              static_cast<size_t>(rr) * kHeadDim;
+            const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.partials + at) + lane);
+            acc.x += wi != 0.f ? wi * v.x : 0.f;
+            acc.y += wi != 0.f ? wi * v.y : 0.f;
+            acc.z += wi != 0.f ? wi * v.z : 0.f;
+            acc.w += wi != 0.f ? wi * v.w : 0.f;
+        }
     }
-    const float f = den > 0.f ? 1.f / den : (den == 0.f ? 0.f : den);
+    const float f = den > 0.f ? 1.f / den : 0.f;
     acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
     if (den != den)
         acc = make_float4(den, den, den, den);
+    const int t = row / p.group;
+    const int64_t at = (static_cast<int64_t>(__ldcg(&notes[first].c0) + t) * p.hq +
+                        __ldcg(&notes[first].h) * p.group + (row - t * p.group)) * kHeadDim;
     if (p.out_f32) {
-        reinterpret_cast<float4 *>(static_cast<float *>(p.out) + row * kHeadDim)[lane] = acc;
+        reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at)[lane] = acc;
     } else {
         const __nv_bfloat162 a = __floats2bfloat162_rn(acc.x, acc.y), d = __floats2bfloat162_rn(acc.z, acc.w);
-        reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + row * kHeadDim)[lane] =
+        reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + at)[lane] =
             make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&d));
     }
 }
 
-constexpr int kMaxSplits = 32;                 // a lane of the joining warp each
-constexpr int kMinSplitKeys = 512;             // keys that a split should have at least
-
 } // namespace
 
-// Row blocks a CTA takes and splits of the keys, from sizes the host knows.
+// Whether a CTA's two blocks share their rows, how many CTAs take part and the
+// bytes that their pieces take, from sizes the host knows.
 ExtendShape paged_extend_shape(int64_t q_rows, int64_t max_q_len, int64_t batch, int64_t hkv, int64_t group,
                                int64_t max_pages, int64_t window)
 {
@@ -974,50 +1135,41 @@ ExtendShape paged_extend_shape(int64_t q_rows, int64_t max_q_len, int64_t batch,
         max_q_len = q_rows;                      // no chunk is longer
     s.key_split = max_q_len * group <= kRowsBlock;
     const int64_t rows = s.key_split ? kRowsBlock : 2 * kRowsBlock;
-    s.row_tiles = (max_q_len * group + rows - 1) / rows;
-    const int64_t ctas = batch * s.row_tiles, filled = q_rows * group / rows + batch;
-    const int64_t units = hkv * (ctas < filled ? ctas : filled);
+    const int64_t row_tiles = (max_q_len * group + rows - 1) / rows;
+    const int64_t most = batch * row_tiles, filled = q_rows * group / rows + batch;
     int64_t keys = max_pages * kPageSize;
     if (window > 0 && window + max_q_len < keys)
         keys = window + max_q_len;
-    int64_t n = units > 0 ? sm_count() / units : 1;
-    if (n > keys / kMinSplitKeys)
-        n = keys / kMinSplitKeys;
-    s.splits = static_cast<int>(n < 1 ? 1 : (n > kMaxSplits ? kMaxSplits : n));
-    s.units = s.row_tiles * s.splits * hkv * batch;
-    s.workspace = s.splits > 1 ? static_cast<size_t>(s.splits) * q_rows * hkv * group * (kHeadDim + 2) * sizeof(float) : 0;
+    // (the CTAs see the true lengths and leave out those that would have less
+    // than kMinRun tiles)
+    const int64_t sms = sm_count() > 0 ? sm_count() : 1;
+    const int64_t runs = hkv * (most < filled ? most : filled) * ((keys + kKeys - 1) / kKeys + 2) / kMinRun;
+    s.workers = static_cast<int>(runs < 1 ? 1 : (runs < sms ? runs : sms));
+    const size_t piece = (s.key_split ? kPieceFloats<kRowsBlock> : kPieceFloats<2 * kRowsBlock>)*sizeof(float);
+    s.workspace = s.workers > 1 ? s.workers * (2 * piece + sizeof(Note)) : 0;
     return s;
 }
 
 template <bool kKeySplit>
-static cudaError_t launch_blocks(const PagedExtendParams &p, const ExtendShape &shape, cudaStream_t s)
+static cudaError_t launch_extend(const PagedExtendParams &p, cudaStream_t s)
 {
     using S = Shape<kKeySplit>;
-    const cudaError_t e = cudaFuncSetAttribute(paged_extend_kernel<kKeySplit>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+    cudaError_t e = cudaFuncSetAttribute(paged_extend_kernel<kKeySplit>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         S::kSmem);
     if (e != cudaSuccess)
         return e;
-    // row blocks: resident CTAs that take unit after unit, so that loads and
-    // conversions for the next run behind the end of the last
-    const int64_t sms = sm_count() > 0 ? sm_count() : 1;
-    const unsigned grid = static_cast<unsigned>(kKeySplit || shape.units < sms ? shape.units : sms);
-    paged_extend_kernel<kKeySplit><<<grid, S::kThreads, S::kSmem, s>>>(p);
-    return cudaGetLastError();
+    paged_extend_kernel<kKeySplit><<<p.workers, S::kThreads, S::kSmem, s>>>(p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess || p.workers == 1)
+        return e;
+    return launch_pdl(paged_extend_join_kernel<S::kRows>, dim3(p.workers - 1, S::kRows / 8), dim3(256), 0, s, p);
 }
 
 cudaError_t launch_paged_extend(const PagedExtendParams &in, const ExtendShape &shape, cudaStream_t s)
 {
     PagedExtendParams p = in;
-    p.splits = shape.splits;
-    p.row_tiles = static_cast<int>(shape.row_tiles);
-    p.units = shape.units;
-    const cudaError_t e = shape.key_split ? launch_blocks<true>(p, shape, s) : launch_blocks<false>(p, shape, s);
-    if (e != cudaSuccess || shape.splits == 1)
-        return e;
-    const int64_t rows = static_cast<int64_t>(p.max_q_len < p.q_rows ? p.max_q_len : p.q_rows) * p.hq;
-    if ((rows + 7) / 8 > 0x7fffffffLL)
-        return cudaErrorInvalidValue;
-    return launch_pdl(paged_extend_join_kernel, dim3(static_cast<unsigned>((rows + 7) / 8), p.batch), dim3(256), 0, s, p);
+    p.workers = shape.workers;
+    return shape.key_split ? launch_extend<true>(p, s) : launch_extend<false>(p, s);
 }
 
 } // namespace nvfp4kv

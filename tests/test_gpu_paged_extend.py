@@ -165,6 +165,42 @@ def test_window(lens, chunks, hq, hkv, window):
     check(c.run(window=window), c, c.want(window=window), torch.float32)
 
 
+@pytest.mark.parametrize("hq,hkv,most", [(8, 2, 3), (6, 1, 21), (16, 4, 40), (3, 3, 300)])
+@pytest.mark.parametrize("seed", [0, 1])
+def test_many_ragged_sequences(hq, hkv, most, seed):
+    """Many units, none like the next: runs of work begin and end anywhere in
+    them; among them empty chunks, empty sequences and chunks without prefix."""
+    rng = np.random.default_rng(100 + seed)
+    n = int(rng.integers(20, 60))
+    lens = [int(x) for x in rng.integers(0, 700, n)]
+    chunks = [min(x, int(c)) for x, c in zip(lens, rng.integers(0, most + 1, n))]
+    chunks[3], chunks[7] = 0, lens[7] if lens[7] <= most else chunks[7]
+    c = Case(lens, chunks, hq, hkv, seed=seed)
+    check(c.run(max_q_len=most), c, c.want(), torch.float32)
+    check(c.run(max_q_len=most, window=100, dtype=torch.bfloat16), c, c.want(window=100), torch.bfloat16)
+
+
+def test_largest_batch():
+    """8,192 sequences, one beyond is refused."""
+    B = 8192
+    lens = [1 + i % 40 for i in range(B)]
+    chunks = [min(n, 1 + i % 3) for i, n in enumerate(lens)]
+    c = Case(lens[:64], chunks[:64], 2, 1, seed=21, spare_rows=0)
+    # the same 64 sequences over and over
+    reps = B // 64
+    q = c.q.repeat(reps, 1, 1)
+    ptr = torch.tensor(indptr(chunks[:64] * reps), device=DEV)
+    out = torch.full(q.shape, 77.0, device=DEV)
+    ws = nv.new_extend_workspace(q.shape[0], 3, B, 2, 1, c.table.shape[1])
+    nv.nvfp4kv_paged_extend(c.cache, q, ptr, c.table_d.repeat(reps, 1), c.seq_lens.repeat(reps), out, ws, max_q_len=3,
+                            dev_status=c.status)
+    want = c.want()
+    for r in (0, 1, reps // 2, reps - 1):
+        check(out.view(reps, -1, 2, 128)[r], c, want, torch.float32)
+    # every copy alike, up to rounding: a run of work may cut a unit
+    assert_close(out.view(reps, -1).cpu(), out.view(reps, -1)[:1].expand(reps, -1).cpu(), "copies")
+
+
 @pytest.mark.parametrize("hs", [False, True])
 def test_tensor_scales(hs):
     scales = ([0.5, 3.0, 1.0], [2.0, 0.125, 7.0]) if hs else None
@@ -251,7 +287,8 @@ def test_bad_pages_and_lengths():
         assert (out[r[b]:r[b + 1]] == 77).all()
         for o in range(3):
             if o != b:
-                assert torch.equal(out[r[o]:r[o + 1]], good[r[o]:r[o + 1]])
+                # (other work, other cuts: the same up to rounding)
+                assert_close(out[r[o]:r[o + 1]].cpu(), good[r[o]:r[o + 1]].cpu(), "the other sequences")
         t[at] = keep
     c.status.zero_()
     out = c.run(max_q_len=99)                                    # the third chunk is longer than promised

@@ -158,7 +158,7 @@ def extend(q=addr(0), qi=addr(1), rows=100, mql=50, batch=2, hq=4, bt=addr(2), m
 @pytest.mark.parametrize("kw,want", [
     (dict(rows=-1), nv.ERR_INVALID_ARG), (dict(mql=-1), nv.ERR_INVALID_ARG), (dict(batch=-1), nv.ERR_INVALID_ARG),
     (dict(hq=0), nv.ERR_INVALID_ARG), (dict(hq=5), nv.ERR_INVALID_ARG), (dict(mp=0), nv.ERR_INVALID_ARG),
-    (dict(window=-1), nv.ERR_INVALID_ARG), (dict(hq=18), nv.ERR_UNSUPPORTED), (dict(batch=65536), nv.ERR_UNSUPPORTED),
+    (dict(window=-1), nv.ERR_INVALID_ARG), (dict(hq=18), nv.ERR_UNSUPPORTED), (dict(batch=8193), nv.ERR_UNSUPPORTED),
     (dict(mql=1 << 29), nv.ERR_UNSUPPORTED), (dict(mp=(1 << 26) + 1), nv.ERR_UNSUPPORTED),
     (dict(dtype=nv.E4M3), nv.ERR_INVALID_ARG), (dict(scale=float("nan")), nv.ERR_INVALID_ARG),
     (dict(q=None), nv.ERR_INVALID_ARG), (dict(out=None), nv.ERR_INVALID_ARG), (dict(sl=None), nv.ERR_INVALID_ARG),
