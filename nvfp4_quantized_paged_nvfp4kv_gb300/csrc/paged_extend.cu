@@ -1052,74 +1052,103 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
 // reference m_j and sum l_j of piece j, M = max_j m_j,
 //   o = sum_j 2^(m_j - M) O_j / sum_j 2^(m_j - M) l_j.
 // The pieces are the CTA's own second one and the first ones of the CTAs after
-// it, up to the one that ends the unit.  One warp a row, four channels a lane.
+// it, up to the one that ends the unit.  A warp takes four rows, four channels a
+// lane: what bounds it is the chain of loads (note, sums, O), which the four
+// rows share.
+constexpr int kJoinRows = 4;
+
 template <int kRows>
 __global__ void __launch_bounds__(256) paged_extend_join_kernel(const __grid_constant__ PagedExtendParams p)
 {
     pdl_wait();
     const int lane = threadIdx.x & 31, first = blockIdx.x;
     const Note *notes = notes_of<kRows>(p);
-    if (!__ldcg(&notes[first].tail))
+    const int4 n0 = __ldcg(reinterpret_cast<const int4 *>(notes + first));       // tail, h, row0, rows
+    const int c0 = __ldcg(&notes[first].c0);
+    int head = first + lane < p.workers ? __ldcg(&notes[first + lane].head) : 0;
+    const int rr = (blockIdx.y * 8 + (threadIdx.x >> 5)) * kJoinRows, left = n0.w - n0.z - rr;     // rows from here on
+    if (!n0.x || left <= 0)
         return;
-    const int rr = blockIdx.y * 8 + (threadIdx.x >> 5), row = __ldcg(&notes[first].row0) + rr;
-    if (row >= __ldcg(&notes[first].rows))
-        return;
-    float M = -INFINITY, den = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float M[kJoinRows], den[kJoinRows];
+    float4 acc[kJoinRows];
+#pragma unroll
+    for (int k = 0; k < kJoinRows; ++k) {
+        M[k] = -INFINITY;
+        den[k] = 0.f;
+        acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
     bool last = false;
     for (int j0 = first; !last && j0 < p.workers; j0 += 32) {
         // lane i: piece j0 + i, if the unit reaches that far
         const int j = j0 + lane;
-        const int head = j > first && j < p.workers ? __ldcg(&notes[j].head) : (j == first ? 1 : 0);
+        if (j0 > first)
+            head = j < p.workers ? __ldcg(&notes[j].head) : 0;
+        else if (lane == 0)
+            head = 1;                            // the piece that begins the unit
         const unsigned stop = __ballot_sync(kFullMask, head != 1);       // 2 ends it; 0 does not occur before that
         const int n = stop ? __ffs(stop) - 1 + (__shfl_sync(kFullMask, head, __ffs(stop) - 1) == 2) : 32;
         last = stop != 0;
-        float m = -INFINITY, l = 0.f;
         const size_t piece = kPieceFloats<kRows> * (2 * static_cast<size_t>(j) + (j == first));
-        if (lane < n) {
-            const float2 v = __ldcg(reinterpret_cast<const float2 *>(p.partials + piece + kRows * kHeadDim) + rr);
-            m = v.x;
-            l = v.y;
+        float2 ml[kJoinRows];
+#pragma unroll
+        for (int k = 0; k < kJoinRows; ++k)
+            ml[k] = lane < n ? __ldcg(reinterpret_cast<const float2 *>(p.partials + piece + kRows * kHeadDim) + rr + k)
+                             : make_float2(-INFINITY, 0.f);
+        float w[kJoinRows];
+#pragma unroll
+        for (int k = 0; k < kJoinRows; ++k) {
+            const float m = ml[k].x, l = ml[k].y;
+            float top = m;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+                top = fmaxf(top, __shfl_xor_sync(kFullMask, top, o));
+            top = fmaxf(top, M[k]);
+            const float old = M[k] == -INFINITY ? 0.f : fast_exp2(M[k] - top);
+            w[k] = m == -INFINITY ? 0.f : fast_exp2(m - top);
+            float add = (m == -INFINITY && l != l) ? l : w[k] * l;       // a row of NaN scores stays NaN
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1)
+                add += __shfl_xor_sync(kFullMask, add, o);
+            den[k] = den[k] * old + add;
+            acc[k] = make_float4(acc[k].x * old, acc[k].y * old, acc[k].z * old, acc[k].w * old);
+            M[k] = top;
         }
-        float top = m;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            top = fmaxf(top, __shfl_xor_sync(kFullMask, top, o));
-        top = fmaxf(top, M);
-        const float old = M == -INFINITY ? 0.f : fast_exp2(M - top);
-        const float w = m == -INFINITY ? 0.f : fast_exp2(m - top);
-        float add = (m == -INFINITY && l != l) ? l : w * l;              // a row of NaN scores stays NaN
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            add += __shfl_xor_sync(kFullMask, add, o);
-        den = den * old + add;
-        acc = make_float4(acc.x * old, acc.y * old, acc.z * old, acc.w * old);
-        M = top;
-#pragma unroll 4
+#pragma unroll 2
         for (int i = 0; i < n; ++i) {
-            const float wi = __shfl_sync(kFullMask, w, i);
-            const size_t at = kPieceFloats<kRows> * (2 * static_cast<size_t>(j0 + i) + (j0 + i == first)) +
-                              static_cast<size_t>(rr) * kHeadDim;
-            const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.partials + at) + lane);
-            acc.x += wi != 0.f ? wi * v.x : 0.f;
-            acc.y += wi != 0.f ? wi * v.y : 0.f;
-            acc.z += wi != 0.f ? wi * v.z : 0.f;
-            acc.w += wi != 0.f ? wi * v.w : 0.f;
+            const float4 *o = reinterpret_cast<const float4 *>(
+                                  p.partials + kPieceFloats<kRows> * (2 * static_cast<size_t>(j0 + i) + (j0 + i == first)) +
+                                  static_cast<size_t>(rr) * kHeadDim) + lane;
+            float4 v[kJoinRows];
+#pragma unroll
+            for (int k = 0; k < kJoinRows; ++k)  // (rows behind the last: memory of the piece, not used)
+                v[k] = __ldcg(o + k * (kHeadDim / 4));
+#pragma unroll
+            for (int k = 0; k < kJoinRows; ++k) {
+                const float wi = __shfl_sync(kFullMask, w[k], i);
+                acc[k].x += wi != 0.f ? wi * v[k].x : 0.f;
+                acc[k].y += wi != 0.f ? wi * v[k].y : 0.f;
+                acc[k].z += wi != 0.f ? wi * v[k].z : 0.f;
+                acc[k].w += wi != 0.f ? wi * v[k].w : 0.f;
+            }
         }
     }
-    const float f = den > 0.f ? 1.f / den : 0.f;
-    acc = make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
-    if (den != den)
-        acc = make_float4(den, den, den, den);
-    const int t = row / p.group;
-    const int64_t at = (static_cast<int64_t>(__ldcg(&notes[first].c0) + t) * p.hq +
-                        __ldcg(&notes[first].h) * p.group + (row - t * p.group)) * kHeadDim;
-    if (p.out_f32) {
-        reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at)[lane] = acc;
-    } else {
-        const __nv_bfloat162 a = __floats2bfloat162_rn(acc.x, acc.y), d = __floats2bfloat162_rn(acc.z, acc.w);
-        reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + at)[lane] =
-            make_uint2(*reinterpret_cast<const uint32_t *>(&a), *reinterpret_cast<const uint32_t *>(&d));
+#pragma unroll
+    for (int k = 0; k < kJoinRows; ++k) {
+        if (k >= left)
+            break;
+        const float f = den[k] > 0.f ? 1.f / den[k] : 0.f;
+        float4 a = make_float4(acc[k].x * f, acc[k].y * f, acc[k].z * f, acc[k].w * f);
+        if (den[k] != den[k])
+            a = make_float4(den[k], den[k], den[k], den[k]);
+        const int row = n0.z + rr + k, t = row / p.group;
+        const int64_t at = (static_cast<int64_t>(c0 + t) * p.hq + n0.y * p.group + (row - t * p.group)) * kHeadDim;
+        if (p.out_f32) {
+            reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at)[lane] = a;
+        } else {
+            const __nv_bfloat162 lo = __floats2bfloat162_rn(a.x, a.y), hi = __floats2bfloat162_rn(a.z, a.w);
+            reinterpret_cast<uint2 *>(static_cast<__nv_bfloat16 *>(p.out) + at)[lane] =
+                make_uint2(*reinterpret_cast<const uint32_t *>(&lo), *reinterpret_cast<const uint32_t *>(&hi));
+        }
     }
 }
 
@@ -1162,7 +1191,7 @@ static cudaError_t launch_extend(const PagedExtendParams &p, cudaStream_t s)
     e = cudaGetLastError();
     if (e != cudaSuccess || p.workers == 1)
         return e;
-    return launch_pdl(paged_extend_join_kernel<S::kRows>, dim3(p.workers - 1, S::kRows / 8), dim3(256), 0, s, p);
+    return launch_pdl(paged_extend_join_kernel<S::kRows>, dim3(p.workers - 1, S::kRows / (8 * kJoinRows)), dim3(256), 0, s, p);
 }
 
 cudaError_t launch_paged_extend(const PagedExtendParams &in, const ExtendShape &shape, cudaStream_t s)
