@@ -840,37 +840,55 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
         const Row row = row_of<kRows>(p, u, tid);
         const bool has_row = row.live;
         const int64_t out_row = row.at;
-        // the row of Q, scaled by a power of two; inv takes scores to log2 units
+        // The rows of Q, each scaled by a power of two; inv takes this thread's
+        // scores to log2 units.  A warp loads its 32 rows two at a time, half a
+        // warp a row (a row a thread, 16 bytes at a time, took 5 us).
+        const unsigned live = __ballot_sync(kFullMask, has_row);
+        const uint32_t stage = base + S::kOffQ + (kKeySplit ? 0 : blk) * kOpBytes;
         float inv;
         {
+            const int piece = lane & 15;
             uint4 w[16];
-            const uint4 *src = reinterpret_cast<const uint4 *>(p.q + out_row * kHeadDim);
-            uint32_t m2 = 0;
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-                w[k] = has_row ? __ldg(src + k) : make_uint4(0, 0, 0, 0);
-                m2 = __vmaxu2(m2, __vmaxu2(__vmaxu2(w[k].x & 0x7fff7fffu, w[k].y & 0x7fff7fffu),
-                                           __vmaxu2(w[k].z & 0x7fff7fffu, w[k].w & 0x7fff7fffu)));
+            for (int i = 0; i < 16; ++i) {
+                const int of = 2 * i + (lane >> 4);
+                const int64_t at = __shfl_sync(kFullMask, out_row, of);
+                w[i] = (live >> of) & 1u ? __ldg(reinterpret_cast<const uint4 *>(p.q + at * kHeadDim) + piece)
+                                         : make_uint4(0, 0, 0, 0);
             }
-            const int expo = static_cast<int>(max(m2 & 0xffffu, m2 >> 16) >> 7);          // of the largest |q|
-            const int e = min(14 - (expo - 127), 112);
             const float ks = p.hs.per_head ? p.hs.k[u.h] : p.gscale;
-            inv = __uint_as_float(static_cast<uint32_t>(127 - e) << 23) * 256.f * ks * fabsf(p.qscale);
-            float sc = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-            sc = p.qscale < 0.f ? -sc : sc;      // scores keep their order: the maximum is taken before inv
-            if (inv == 0.f) {                    // all scores are 0
-                inv = 1.f;
-                sc = 0.f;
-            }
-            if (!kKeySplit || blk == 0) {
-                const uint32_t dst = base + S::kOffQ + (kKeySplit ? 0 : blk) * kOpBytes + r * 128u;
-                auto two = [&](uint32_t v) {
-                    return pack_f16x2(__uint_as_float(v << 16) * sc, __uint_as_float(v & 0xffff0000u) * sc);
-                };
+            const float to_log2 = 256.f * ks * fabsf(p.qscale);
+            int own = 0;
 #pragma unroll
-                for (uint32_t k = 0; k < 16; ++k)
-                    st_shared128(dst + (k >> 3) * kHalfBytes + (((k & 7u) ^ (r & 7u)) << 4), two(w[k].x), two(w[k].y),
-                                 two(w[k].z), two(w[k].w));
+            for (int i = 0; i < 16; ++i) {
+                const uint4 v = w[i];
+                const uint32_t m2 = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
+                                             __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
+                int top = max(m2 & 0xffffu, m2 >> 16);
+#pragma unroll
+                for (int o = 1; o < 16; o <<= 1)
+                    top = max(top, __shfl_xor_sync(kFullMask, top, o));
+                // 2^e puts the largest |q| into [2^14, 2^15)
+                const int e = min(14 - ((top >> 7) - 127), 112);
+                const int e0 = __shfl_sync(kFullMask, e, 0), e1 = __shfl_sync(kFullMask, e, 16);
+                own = lane == 2 * i ? e0 : (lane == 2 * i + 1 ? e1 : own);
+                if (!kKeySplit || blk == 0) {
+                    float sc = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+                    sc = p.qscale < 0.f ? -sc : sc;      // scores keep their order: references are taken before inv
+                    if (__uint_as_float(static_cast<uint32_t>(127 - e) << 23) * to_log2 == 0.f)
+                        sc = 0.f;                        // all scores are 0
+                    auto two = [&](uint32_t q2) {
+                        return pack_f16x2(__uint_as_float(q2 << 16) * sc, __uint_as_float(q2 & 0xffff0000u) * sc);
+                    };
+                    const uint32_t at = 32u * (warp & 3) + 2u * i + (lane >> 4);
+                    st_shared128(stage + (piece >> 3) * kHalfBytes + at * 128u + (((piece & 7u) ^ (at & 7u)) << 4),
+                                 two(v.x), two(v.y), two(v.z), two(v.w));
+                }
+            }
+            inv = __uint_as_float(static_cast<uint32_t>(127 - own) << 23) * to_log2;
+            if (inv == 0.f)
+                inv = 1.f;
+            if (!kKeySplit || blk == 0) {
                 fence_async_shared();
                 warp_arrive(B(S::kQFull + blk), lane);
             }
@@ -993,10 +1011,13 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
                     note->tail = 1;
                 }
             }
-#pragma unroll 1
-            for (int cb = 0; cb < 4; ++cb) {
+            // Rows go out by way of the Q tile, which no product reads any more: the
+            // warp's 8 KB hold 256 bytes of each of its rows (all channels in
+            // bf16, half of them in fp32), which half a warp then stores on end.
+            const bool f32 = !whole || p.out_f32;
+            const uint32_t mine = stage + 8192u * (warp & 3);
+            auto load_o = [&](int cb, float (&o)[32]) {
                 uint32_t w[32];
-                float o[32];
                 tmem_ld32(tb + kTmO + 32 * cb, w);
                 tmem_wait_ld();
 #pragma unroll
@@ -1010,25 +1031,48 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
                     for (int j = 0; j < 32; ++j)
                         o[j] = w1 != 0.f ? fmaf(__uint_as_float(w[j]), f1, o[j]) : o[j];
                 }
-                if (!has_row)
-                    continue;
-                if (!whole || p.out_f32) {
-                    float *row_f = !whole ? part + rr * kHeadDim : static_cast<float *>(p.out) + out_row * kHeadDim;
-                    float4 *dst = reinterpret_cast<float4 *>(row_f + 32 * cb);
+            };
+            auto place = [&](int of, uint32_t chunk) { return mine + 256u * of + ((chunk ^ (of & 7u)) << 4); };
+#pragma unroll 1
+            for (int pass = 0; pass < (f32 ? 2 : 1); ++pass) {
+                __syncwarp();
+#pragma unroll 1
+                for (int half = 0; half < (f32 ? 2 : 4); ++half) {
+                    float o[32];
+                    load_o(f32 ? 2 * pass + half : half, o);
+                    if (f32) {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-                } else {
-                    uint4 *dst = reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + out_row * kHeadDim + 32 * cb);
-                    auto bf2 = [&](int j) {
-                        const __nv_bfloat162 two = __floats2bfloat162_rn(o[j], o[j + 1]);
-                        return *reinterpret_cast<const uint32_t *>(&two);
-                    };
+                        for (int k = 0; k < 8; ++k)
+                            st_shared128(place(lane, 8 * half + k), __float_as_uint(o[4 * k]), __float_as_uint(o[4 * k + 1]),
+                                         __float_as_uint(o[4 * k + 2]), __float_as_uint(o[4 * k + 3]));
+                    } else {
+                        auto bf2 = [&](int j) {
+                            const __nv_bfloat162 two = __floats2bfloat162_rn(o[j], o[j + 1]);
+                            return *reinterpret_cast<const uint32_t *>(&two);
+                        };
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        dst[k] = make_uint4(bf2(8 * k), bf2(8 * k + 2), bf2(8 * k + 4), bf2(8 * k + 6));
+                        for (int k = 0; k < 4; ++k)
+                            st_shared128(place(lane, 4 * half + k), bf2(8 * k), bf2(8 * k + 2), bf2(8 * k + 4), bf2(8 * k + 6));
+                    }
+                }
+                __syncwarp();
+#pragma unroll 4
+                for (int i = 0; i < 16; ++i) {
+                    const int of = 2 * i + (lane >> 4);
+                    const uint32_t chunk = lane & 15;
+                    const int64_t at = __shfl_sync(kFullMask, out_row, of);
+                    if (!((live >> of) & 1u))
+                        continue;
+                    const uint4 v = lds128(place(of, chunk));
+                    if (!whole)
+                        *(reinterpret_cast<uint4 *>(part + (rr - lane + of) * kHeadDim + 64 * pass) + chunk) = v;
+                    else if (p.out_f32)
+                        *(reinterpret_cast<uint4 *>(static_cast<float *>(p.out) + at * kHeadDim + 64 * pass) + chunk) = v;
+                    else
+                        *(reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + at * kHeadDim) + chunk) = v;
                 }
             }
+            __syncwarp();
             if (kKeySplit) {
                 tc_fence_before_sync();
                 warp_arrive(B(S::kFree), lane);
