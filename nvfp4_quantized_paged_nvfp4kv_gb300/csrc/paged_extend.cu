@@ -549,6 +549,26 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
         return true;
     };
 
+    // the rows of Q to come, into L2: the first unit's now, later the next row
+    // tile's while the last one is worked on
+    auto ask_for_q = [&](Unit u, int at) {
+        Chunk c;
+        if (tid >= kRows || at >= row_tiles_of<kRows>(p, u.b, c))
+            return;
+        u.set<kRows>(p, c, at);
+        const Row row = row_of<kRows>(p, u, tid);
+        if (row.live) {
+            const uint16_t *q = p.q + row.at * kHeadDim;
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(q));
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(q + kHeadDim / 2));
+        }
+    };
+    if (start.left > 0) {
+        Unit u{};
+        u.h = start.h;
+        u.b = start.b;
+        ask_for_q(u, start.tile);
+    }
     if (tid == 0) {
         for (int k = 0; k < S::kRaw; ++k) {
             mbar_init(B(S::kRawFull + k), 1);
@@ -858,34 +878,45 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
             }
             const float ks = p.hs.per_head ? p.hs.k[u.h] : p.gscale;
             const float to_log2 = 256.f * ks * fabsf(p.qscale);
-            int own = 0;
+            // each row's largest |q| (bf16 bits): 16 reductions over half a warp at
+            // once, halving the rows a lane holds at every exchange; lane l ends
+            // with row 2 (l mod 16) + l / 16
+            uint32_t top[16];
 #pragma unroll
             for (int i = 0; i < 16; ++i) {
-                const uint4 v = w[i];
-                const uint32_t m2 = __vmaxu2(__vmaxu2(v.x & 0x7fff7fffu, v.y & 0x7fff7fffu),
-                                             __vmaxu2(v.z & 0x7fff7fffu, v.w & 0x7fff7fffu));
-                int top = max(m2 & 0xffffu, m2 >> 16);
+                const uint32_t m2 = __vmaxu2(__vmaxu2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu),
+                                             __vmaxu2(w[i].z & 0x7fff7fffu, w[i].w & 0x7fff7fffu));
+                top[i] = max(m2 & 0xffffu, m2 >> 16);
+            }
 #pragma unroll
-                for (int o = 1; o < 16; o <<= 1)
-                    top = max(top, __shfl_xor_sync(kFullMask, top, o));
-                // 2^e puts the largest |q| into [2^14, 2^15)
-                const int e = min(14 - ((top >> 7) - 127), 112);
-                const int e0 = __shfl_sync(kFullMask, e, 0), e1 = __shfl_sync(kFullMask, e, 16);
-                own = lane == 2 * i ? e0 : (lane == 2 * i + 1 ? e1 : own);
-                if (!kKeySplit || blk == 0) {
-                    float sc = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-                    sc = p.qscale < 0.f ? -sc : sc;      // scores keep their order: references are taken before inv
-                    if (__uint_as_float(static_cast<uint32_t>(127 - e) << 23) * to_log2 == 0.f)
-                        sc = 0.f;                        // all scores are 0
+            for (int o = 8; o > 0; o >>= 1) {
+                const bool upper = lane & o;
+#pragma unroll
+                for (int i = 0; i < o; ++i) {
+                    const uint32_t got = __shfl_xor_sync(kFullMask, upper ? top[i] : top[i + o], o);
+                    top[i] = max(upper ? top[i + o] : top[i], got);
+                }
+            }
+            // 2^e puts it into [2^14, 2^15)
+            const int e = min(14 - (static_cast<int>(top[0] >> 7) - 127), 112);
+            auto unscaled = [&](int ee) { return __uint_as_float(static_cast<uint32_t>(127 - ee) << 23) * to_log2; };
+            if (!kKeySplit || blk == 0) {
+                float sc = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+                sc = p.qscale < 0.f ? -sc : sc;          // scores keep their order: references are taken before inv
+                if (unscaled(e) == 0.f)
+                    sc = 0.f;                            // all scores are 0
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float f = __shfl_sync(kFullMask, sc, (lane & 16) | i);
                     auto two = [&](uint32_t q2) {
-                        return pack_f16x2(__uint_as_float(q2 << 16) * sc, __uint_as_float(q2 & 0xffff0000u) * sc);
+                        return pack_f16x2(__uint_as_float(q2 << 16) * f, __uint_as_float(q2 & 0xffff0000u) * f);
                     };
                     const uint32_t at = 32u * (warp & 3) + 2u * i + (lane >> 4);
                     st_shared128(stage + (piece >> 3) * kHalfBytes + at * 128u + (((piece & 7u) ^ (at & 7u)) << 4),
-                                 two(v.x), two(v.y), two(v.z), two(v.w));
+                                 two(w[i].x), two(w[i].y), two(w[i].z), two(w[i].w));
                 }
             }
-            inv = __uint_as_float(static_cast<uint32_t>(127 - own) << 23) * to_log2;
+            inv = unscaled(__shfl_sync(kFullMask, e, ((lane & 1) << 4) | (lane >> 1)));
             if (inv == 0.f)
                 inv = 1.f;
             if (!kKeySplit || blk == 0) {
@@ -893,6 +924,7 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
                 warp_arrive(B(S::kQFull + blk), lane);
             }
         }
+        ask_for_q(u, u.tile + 1);
         const int pos = u.first_pos + row.t;     // keys lo .. pos are visible
         const int lo = p.window > 0 ? pos - p.window + 1 : 0;
         const uint64_t inv2 = f32x2_pack(inv, inv);
@@ -1056,20 +1088,23 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
                     }
                 }
                 __syncwarp();
-#pragma unroll 4
-                for (int i = 0; i < 16; ++i) {
-                    const int of = 2 * i + (lane >> 4);
-                    const uint32_t chunk = lane & 15;
-                    const int64_t at = __shfl_sync(kFullMask, out_row, of);
-                    if (!((live >> of) & 1u))
-                        continue;
-                    const uint4 v = lds128(place(of, chunk));
-                    if (!whole)
-                        *(reinterpret_cast<uint4 *>(part + (rr - lane + of) * kHeadDim + 64 * pass) + chunk) = v;
-                    else if (p.out_f32)
-                        *(reinterpret_cast<uint4 *>(static_cast<float *>(p.out) + at * kHeadDim + 64 * pass) + chunk) = v;
-                    else
-                        *(reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p.out) + at * kHeadDim) + chunk) = v;
+                const uint32_t chunk = lane & 15;
+                if (!whole) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(part + (rr - lane + (lane >> 4)) * kHeadDim + 64 * pass) + chunk;
+#pragma unroll 8
+                    for (int i = 0; i < 16; ++i)     // (rows that are none: their place in the piece)
+                        dst[i * (2 * kHeadDim / 4)] = lds128(place(2 * i + (lane >> 4), chunk));
+                } else {
+                    const int size = p.out_f32 ? 4 : 2;
+                    uint8_t *dst = static_cast<uint8_t *>(p.out) + 64 * 4 * pass + 16 * chunk;
+#pragma unroll 8
+                    for (int i = 0; i < 16; ++i) {
+                        const int of = 2 * i + (lane >> 4);
+                        const int64_t at = __shfl_sync(kFullMask, out_row, of);
+                        const uint4 v = lds128(place(of, chunk));
+                        if ((live >> of) & 1u)
+                            *reinterpret_cast<uint4 *>(dst + at * kHeadDim * size) = v;
+                    }
                 }
             }
             __syncwarp();
@@ -1096,14 +1131,16 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
 // reference m_j and sum l_j of piece j, M = max_j m_j,
 //   o = sum_j 2^(m_j - M) O_j / sum_j 2^(m_j - M) l_j.
 // The pieces are the CTA's own second one and the first ones of the CTAs after
-// it, up to the one that ends the unit.  A warp takes four rows, four channels a
-// lane: what bounds it is the chain of loads (note, sums, O), which the four
-// rows share.
-constexpr int kJoinRows = 4;
+// it, up to the one that ends the unit.  Four channels a lane.  What bounds it is
+// the chain of loads (note, sums, O): a warp takes four rows where units are in
+// few pieces, one row and eight pieces at a time where few rows are in many.
+template <int kRows>
+constexpr int kJoinRowsOf = kRows == kRowsBlock ? 1 : 4;
 
 template <int kRows>
 __global__ void __launch_bounds__(256) paged_extend_join_kernel(const __grid_constant__ PagedExtendParams p)
 {
+    constexpr int kJoinRows = kJoinRowsOf<kRows>, kAhead = 8 / kJoinRows;
     pdl_wait();
     const int lane = threadIdx.x & 31, first = blockIdx.x;
     const Note *notes = notes_of<kRows>(p);
@@ -1157,7 +1194,7 @@ __global__ void __launch_bounds__(256) paged_extend_join_kernel(const __grid_con
             acc[k] = make_float4(acc[k].x * old, acc[k].y * old, acc[k].z * old, acc[k].w * old);
             M[k] = top;
         }
-#pragma unroll 2
+#pragma unroll kAhead
         for (int i = 0; i < n; ++i) {
             const float4 *o = reinterpret_cast<const float4 *>(
                                   p.partials + kPieceFloats<kRows> * (2 * static_cast<size_t>(j0 + i) + (j0 + i == first)) +
@@ -1235,7 +1272,7 @@ static cudaError_t launch_extend(const PagedExtendParams &p, cudaStream_t s)
     e = cudaGetLastError();
     if (e != cudaSuccess || p.workers == 1)
         return e;
-    return launch_pdl(paged_extend_join_kernel<S::kRows>, dim3(p.workers - 1, S::kRows / (8 * kJoinRows)), dim3(256), 0, s, p);
+    return launch_pdl(paged_extend_join_kernel<S::kRows>, dim3(p.workers - 1, S::kRows / (8 * kJoinRowsOf<S::kRows>)), dim3(256), 0, s, p);
 }
 
 cudaError_t launch_paged_extend(const PagedExtendParams &in, const ExtendShape &shape, cudaStream_t s)
