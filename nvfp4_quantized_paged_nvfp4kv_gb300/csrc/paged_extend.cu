@@ -254,9 +254,8 @@ __device__ __forceinline__ void convert_v(const RawV &v, uint32_t dst, int pt)
     }
 }
 
-// 64 scores of a row (tensor-memory columns at taddr), masked to the keys
-// lo_j .. hi_j - 1 of their 64.
-__device__ __forceinline__ void load_scores(uint32_t taddr, int lo_j, int hi_j, float (&s)[64])
+// 64 scores of a row (tensor-memory columns at taddr).
+__device__ __forceinline__ void load_scores(uint32_t taddr, float (&s)[64])
 {
     uint32_t s0[32], s1[32];
     tmem_ld32(taddr, s0);
@@ -267,33 +266,18 @@ __device__ __forceinline__ void load_scores(uint32_t taddr, int lo_j, int hi_j, 
         s[j] = __uint_as_float(s0[j]);
         s[j + 32] = __uint_as_float(s1[j]);
     }
-    if (hi_j < 64 || lo_j > 0) {
-#pragma unroll
-        for (int j = 0; j < 64; ++j)
-            if (j >= hi_j || j < lo_j)
-                s[j] = -INFINITY;
-    }
 }
 
-__device__ __forceinline__ float max_of(const float (&s)[64])
-{
-    float pm[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k)
-        pm[k] = fmax3(fmax3(s[8 * k], s[8 * k + 1], s[8 * k + 2]), fmax3(s[8 * k + 3], s[8 * k + 4], s[8 * k + 5]),
-                      fmaxf(s[8 * k + 6], s[8 * k + 7]));
-    return fmax3(fmax3(pm[0], pm[1], pm[2]), fmax3(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7]));
-}
-
-// 2^(s inv - m) of 64 scores, as f16 pairs; their sum (of the unrounded values)
-// is returned.
-__device__ __forceinline__ float weights_of(const float (&s)[64], uint64_t inv2, float m, uint32_t (&pw)[32])
+// 2^(s inv - m) of scores, as f16 pairs; their sum (of the unrounded values) is
+// returned.
+template <int kN>
+__device__ __forceinline__ float weights_of(const float (&s)[kN], uint64_t inv2, float m, uint32_t (&pw)[kN / 2])
 {
     const float mbase = m == -INFINITY ? 0.f : m;
     const uint64_t neg2 = f32x2_pack(-mbase, -mbase);
     uint64_t acc[4] = {0, 0, 0, 0};
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
+    for (int j = 0; j < kN / 2; ++j) {
         const uint64_t d = fma_f32x2(f32x2_pack(s[2 * j], s[2 * j + 1]), inv2, neg2);
         const float a = fast_exp2(f32x2_lo(d)), b = fast_exp2(f32x2_hi(d));
         acc[j & 3] = add_f32x2(acc[j & 3], f32x2_pack(a, b));
@@ -301,6 +285,82 @@ __device__ __forceinline__ float weights_of(const float (&s)[64], uint64_t inv2,
     }
     const uint64_t a = add_f32x2(add_f32x2(acc[0], acc[1]), add_f32x2(acc[2], acc[3]));
     return f32x2_lo(a) + f32x2_hi(a);
+}
+
+// What a row's softmax keeps: the reference and the sum of weights relative to it.
+struct RowSum {
+    float m, l;
+};
+
+// Bits lo .. hi - 1 (any integers) of 32.
+__device__ __forceinline__ uint32_t bit_range(int lo, int hi)
+{
+    const uint32_t below_hi = hi >= 32 ? ~0u : (hi <= 0 ? 0u : (1u << hi) - 1u);
+    const uint32_t below_lo = lo >= 32 ? ~0u : (lo <= 0 ? 0u : (1u << lo) - 1u);
+    return below_hi & ~below_lo;
+}
+
+// The weights of 64 scores the long way: masked to the keys lo .. hi - 1 of them,
+// and, where a row has no reference yet or its weights sum to more than kMaxSum,
+// with the reference raised to the largest score; O (where has_o), once landed()
+// says that the products so far are in it, and l, which are relative to the old
+// one, follow.  A warp together; false when landed() gave up.
+template <class Landed>
+__device__ __forceinline__ bool weights_with_care(uint32_t scores, uint32_t weights, uint32_t o_cols, bool has_o, int lo, int hi,
+                                                  float inv, RowSum &row, Landed landed)
+{
+    const uint64_t inv2 = f32x2_pack(inv, inv);
+    const uint32_t seen[2] = {bit_range(lo, hi), bit_range(lo - 32, hi - 32)};
+    auto load = [&](float (&s)[64]) {
+        load_scores(scores, s);
+#pragma unroll
+        for (int j = 0; j < 64; ++j)
+            s[j] = (seen[j >> 5] >> (j & 31)) & 1u ? s[j] : -INFINITY;
+    };
+    bool raise = row.m == -INFINITY;
+    for (bool again = false;; again = true) {
+        if (__any_sync(kFullMask, raise)) {
+            float s[64];
+            load(s);
+            float pm[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                pm[k] = fmax3(fmax3(s[8 * k], s[8 * k + 1], s[8 * k + 2]), fmax3(s[8 * k + 3], s[8 * k + 4], s[8 * k + 5]),
+                              fmaxf(s[8 * k + 6], s[8 * k + 7]));
+            const float top =
+                fmax3(fmax3(pm[0], pm[1], pm[2]), fmax3(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7])) * inv;
+            raise = raise && top > -INFINITY;
+            const float m_new = raise ? top : row.m;
+            const float alpha = raise ? fast_exp2(row.m - m_new) : 1.f;
+            row.m = m_new;
+            row.l *= alpha;
+            if (has_o && __any_sync(kFullMask, raise)) {
+                if (!landed())
+                    return false;
+                tc_fence_after_sync();
+#pragma unroll 1
+                for (int cb = 0; cb < 4; ++cb) {
+                    uint32_t o[32];
+                    tmem_ld32(o_cols + 32 * cb, o);
+                    tmem_wait_ld();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                    tmem_st32(o_cols + 32 * cb, o);
+                }
+            }
+        }
+        float s[64];
+        uint32_t pw[32];
+        load(s);
+        const float sum = weights_of(s, inv2, row.m, pw);
+        raise = sum > kMaxSum;
+        if (again || !__any_sync(kFullMask, raise)) {
+            row.l += sum;
+            tmem_st32(weights, pw);              // (over scores that have been read)
+            return true;
+        }
+    }
 }
 
 // A row tile of one sequence and kv head, and the piece of its key tiles that
@@ -476,6 +536,60 @@ __device__ __forceinline__ Row row_of(const PagedExtendParams &p, const Unit &u,
     return w;
 }
 
+// A CTA's way through its run.
+struct Walk {
+    Unit u;
+    Chunk c;
+    int n, at, off;                      // row tiles of the sequence, the next one, and its place to begin at
+    long long left;
+
+    __device__ __forceinline__ explicit Walk(const Run &r) : u{}, c{}, n(-1), at(r.tile), off(r.off), left(r.left)
+    {
+        u.h = r.h;
+        u.b = r.b;
+    }
+};
+
+// The next unit with keys (its piece in w.u), or false at the end of the run.
+// Rows that see no key are written on the way, by threads 0 .. kRows - 1.  (One
+// copy for all roles.)
+template <int kRows>
+__device__ __forceinline__ bool next_unit(const PagedExtendParams &p, Walk &w, int tid)
+{
+    Unit &u = w.u;
+    while (w.left > 0 && u.h < p.hkv) {
+        if (w.n < 0)
+            w.n = row_tiles_of<kRows>(p, u.b, w.c);
+        if (w.at >= w.n) {
+            w.n = -1;
+            w.at = w.off = 0;
+            if (++u.b == p.batch) {
+                u.b = 0;
+                ++u.h;
+            }
+            continue;
+        }
+        u.set<kRows>(p, w.c, w.at);
+        // place 0 of a unit is its own cost, place 1 + i key tile i
+        const int take = static_cast<int>(min(w.left, static_cast<long long>(u.all + 1 - w.off)));
+        u.from = max(0, w.off - 1);
+        u.n_tiles = max(0, w.off + take - 1) - u.from;
+        w.left -= take;
+        ++w.at;
+        w.off = 0;
+        if (u.all == 0 && tid < kRows) {
+            const Row row = row_of<kRows>(p, u, tid);
+            const int words = p.out_f32 ? kHeadDim / 4 : kHeadDim / 8;
+            uint4 *d = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.out) + row.at * kHeadDim * (p.out_f32 ? 4 : 2));
+            for (int k = 0; row.live && k < words; ++k)
+                d[k] = make_uint4(0, 0, 0, 0);
+        }
+        if (u.n_tiles > 0)
+            return true;
+    }
+    return false;
+}
+
 // The workspace: for each CTA two pieces of (O [rows][128], then (reference,
 // sum) [rows]) -- the one that begins inside its unit and the one that begins
 // with it but does not end it -- and then a note of each CTA.
@@ -515,36 +629,11 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
     // The units of this CTA's run, one after the other: fn(unit) for each with
     // keys, until it returns false.
     auto for_units = [&](auto fn) {
-        Unit u{};
-        u.h = start.h;
-        u.b = start.b;
-        int at = start.tile, off = start.off;
-        for (long long left = start.left; left > 0 && u.h < p.hkv;) {
-            Chunk c;
-            const int n = row_tiles_of<kRows>(p, u.b, c);
-            for (; at < n && left > 0; ++at, off = 0) {
-                u.set<kRows>(p, c, at);
-                // place 0 of a unit is its own cost, place 1 + i key tile i
-                const int take = static_cast<int>(min(left, static_cast<long long>(u.all + 1 - off)));
-                u.from = max(0, off - 1);
-                u.n_tiles = max(0, off + take - 1) - u.from;
-                left -= take;
-                if (u.all == 0 && tid < kRows) {
-                    // rows that see no key
-                    const Row row = row_of<kRows>(p, u, tid);
-                    const int words = p.out_f32 ? kHeadDim / 4 : kHeadDim / 8;
-                    uint4 *d = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.out) + row.at * kHeadDim * (p.out_f32 ? 4 : 2));
-                    for (int k = 0; row.live && k < words; ++k)
-                        d[k] = make_uint4(0, 0, 0, 0);
-                }
-                if (u.n_tiles > 0 && !fn(u))
-                    return false;
-            }
-            at = off = 0;
-            if (++u.b == p.batch) {
-                u.b = 0;
-                ++u.h;
-            }
+        Walk w(start);
+        while (next_unit<kRows>(p, w, tid)) {
+            const Unit u = w.u;                  // (a copy in registers: the walk's own is in memory)
+            if (!fn(u))
+                return false;
         }
         return true;
     };
@@ -945,54 +1034,35 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
             // weights of keys 0 .. 63 go over the columns of scores 0 .. 31, of
             // keys 64 .. 127 over those of scores 32 .. 63
 #pragma unroll 1
-            for (int hf = 0; ok && hf < 2; ++hf) {
-                const uint32_t at = tb + kTmS + 64 * hf;
+            for (int hf = 0; hf < 2; ++hf) {
+                const uint32_t at = tb + kTmS + 64 * hf, to = tb + kTmS + 32 * hf;
                 const int lo_h = lo_j - 64 * hf, hi_h = hi_j - 64 * hf;
-                // the rows for which `need` holds take their largest score as
-                // reference; O and l, which were relative to the old one, follow
-                auto raise = [&](bool need, float mx) {
-                    const float m_new = need ? mx : m_used;
-                    const float alpha = need ? fast_exp2(m_used - (m_new == -INFINITY ? 0.f : m_new)) : 1.f;
-                    m_used = m_new;
-                    l *= alpha;
-                    if (j == 0 && hf == 0)
-                        return true;             // no O yet
-                    // the products before this one have landed: S of this tile
-                    // was committed after those of the last tile
-                    if (hf == 1 && !wait_warp(S::kHalf + blk, i & 1))
-                        return false;
-                    tc_fence_after_sync();
-#pragma unroll 1
-                    for (int cb = 0; cb < 4; ++cb) {
-                        uint32_t o[32];
-                        tmem_ld32(tb + kTmO + 32 * cb, o);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                        tmem_st32(tb + kTmO + 32 * cb, o);
+                bool care = m_used == -INFINITY || lo_h > 0 || hi_h < 64;
+                if (!__any_sync(kFullMask, care)) {
+                    float s[64];
+                    uint32_t pw[32];
+                    load_scores(at, s);
+                    const float sum = weights_of(s, inv2, m_used, pw);
+                    care = __any_sync(kFullMask, sum > kMaxSum);
+                    if (!care) {
+                        l += sum;
+                        tmem_st32(to, pw);
                     }
-                    return true;
-                };
-                float s[64];
-                load_scores(at, lo_h, hi_h, s);
-                const bool first = m_used == -INFINITY;
-                if (__any_sync(kFullMask, first)) {
-                    const float mx = max_of(s) * inv;
-                    if (__any_sync(kFullMask, first && mx > -INFINITY) && !(ok = raise(first && mx > -INFINITY, mx)))
-                        break;
-                    load_scores(at, lo_h, hi_h, s);      // (64 registers fewer to keep meanwhile)
+                } else {
+                    care = true;
                 }
-                uint32_t pw[32];
-                float sum = weights_of(s, inv2, m_used, pw);
-                if (__any_sync(kFullMask, sum > kMaxSum)) {
-                    load_scores(at, lo_h, hi_h, s);
-                    if (!(ok = raise(sum > kMaxSum, max_of(s) * inv)))
+                if (care) {
+                    // O is there after the unit's first products: of the last tile
+                    // (S of this one was committed after them), and of this tile's
+                    // first half, which may still be under way
+                    RowSum sum{m_used, l};
+                    ok = weights_with_care(at, to, tb + kTmO, j > 0 || hf == 1, lo_h, hi_h, inv, sum,
+                                           [&] { return hf == 0 || wait_warp(S::kHalf + blk, i & 1); });
+                    if (!ok)
                         break;
-                    sum = weights_of(s, inv2, m_used, pw);
+                    m_used = sum.m;
+                    l = sum.l;
                 }
-                l += sum;
-                tmem_st32(tb + kTmS + 32 * hf, pw);
                 tmem_wait_st();
                 tc_fence_before_sync();
                 warp_arrive(B(S::kPFull + 2 * hf + blk), lane);
