@@ -406,6 +406,74 @@ struct Run {
 };
 
 constexpr int kMinRun = 3;               // a run is at least this long, else fewer CTAs take part
+// A cut that leaves no more than this of a unit on one side moves to the unit's
+// border: a piece more costs a CTA some 8 us, as much as four to five tiles,
+// and the join.
+constexpr int kSnap = 4;
+
+// A place in the sequence of units: `off` into row tile `tile` of sequence b, kv
+// head h; `at` counts from the beginning.
+struct Place {
+    int h, b, tile, off;
+    long long at;
+};
+
+// Where the cut at `at` of `head` x hkv places falls (whole warp); table: batch +
+// 1 running sums.
+template <int kRows>
+__device__ __forceinline__ Place find_cut(const PagedExtendParams &p, long long at, long long head, const long long *table,
+                                          int lane)
+{
+    Place r{p.hkv, 0, 0, 0, at};
+    if (at >= head * p.hkv)
+        return r;
+    r.h = static_cast<int>(at / head);
+    long long rest = at - r.h * head;
+    int x = 0, y = p.batch;              // the last sequence that begins at or before `rest`
+    while (y - x > 1) {
+        const int mid = (x + y) >> 1;
+        if (table[mid] <= rest)
+            x = mid;
+        else
+            y = mid;
+    }
+    r.b = x;
+    rest -= table[x];
+    Chunk c;
+    const int n = row_tiles_of<kRows>(p, x, c);
+    for (int i0 = 0; i0 < n; i0 += 32) {
+        Unit u;
+        int w = 0;
+        if (i0 + lane < n) {
+            u.set<kRows>(p, c, i0 + lane);
+            w = u.all + 1;
+        }
+        long long incl = w;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long v = __shfl_up_sync(kFullMask, incl, o);
+            if (lane >= o)
+                incl += v;
+        }
+        const unsigned past = __ballot_sync(kFullMask, i0 + lane < n && incl > rest);
+        if (past) {
+            const int hit = __ffs(past) - 1, size = __shfl_sync(kFullMask, w, hit);
+            r.tile = i0 + hit;
+            r.off = static_cast<int>(rest - __shfl_sync(kFullMask, incl - w, hit));
+            if (r.off <= kSnap && r.off <= size - r.off) {
+                r.at -= r.off;
+                r.off = 0;
+            } else if (size - r.off <= kSnap) {  // to the unit's end: the next one's beginning
+                r.at += size - r.off;
+                ++r.tile;
+                r.off = 0;
+            }
+            break;
+        }
+        rest -= __shfl_sync(kFullMask, incl, 31);
+    }
+    return r;
+}
 
 // Finds the run of worker `worker` of `workers`; whole CTA.  `table`: batch + 1
 // sums in shared memory.
@@ -465,56 +533,24 @@ __device__ __forceinline__ void find_run(const PagedExtendParams &p, int worker,
         carry += total;
         __syncthreads();
     }
-    if (warp == 0) {
+    // the run's two ends, by a warp each
+    if (warp < 2) {
         const long long head = table[p.batch], all = head * p.hkv;
         const long long use = min(static_cast<long long>(workers), max(1LL, all / kMinRun));
-        Run r{};
-        if (worker < use) {
-            const long long lo = all * worker / use, hi = all * (worker + 1) / use;
-            r.left = hi - lo;
-            if (r.left > 0) {
-                r.h = static_cast<int>(lo / head);
-                long long at = lo - r.h * head;
-                int x = 0, y = p.batch;              // the last sequence that begins at or before `at`
-                while (y - x > 1) {
-                    const int mid = (x + y) >> 1;
-                    if (table[mid] <= at)
-                        x = mid;
-                    else
-                        y = mid;
-                }
-                r.b = x;
-                at -= table[x];
-                Chunk c;
-                const int n = row_tiles_of<kRows>(p, x, c);
-                for (int i0 = 0; i0 < n; i0 += 32) {
-                    Unit u;
-                    int w = 0;
-                    if (i0 + lane < n) {
-                        u.set<kRows>(p, c, i0 + lane);
-                        w = u.all + 1;
-                    }
-                    long long incl = w;
-#pragma unroll
-                    for (int o = 1; o < 32; o <<= 1) {
-                        const long long v = __shfl_up_sync(kFullMask, incl, o);
-                        if (lane >= o)
-                            incl += v;
-                    }
-                    const unsigned past = __ballot_sync(kFullMask, i0 + lane < n && incl > at);
-                    if (past) {
-                        const int hit = __ffs(past) - 1;
-                        r.tile = i0 + hit;
-                        r.off = static_cast<int>(at - __shfl_sync(kFullMask, incl - w, hit));
-                        break;
-                    }
-                    at -= __shfl_sync(kFullMask, incl, 31);
-                }
+        const Place r = find_cut<kRows>(p, all * min(worker + warp, static_cast<int>(use)) / use, head, table, lane);
+        if (lane == 0) {
+            if (warp == 0) {
+                run->h = r.h;
+                run->b = r.b;
+                run->tile = r.tile;
+                run->off = r.off;
             }
+            part[warp] = r.at;
         }
-        if (lane == 0)
-            *run = r;
     }
+    __syncthreads();
+    if (threadIdx.x == 0)
+        run->left = part[1] - part[0];
     __syncthreads();
 }
 
