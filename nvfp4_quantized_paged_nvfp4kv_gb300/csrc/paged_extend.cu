@@ -91,7 +91,8 @@ struct Shape {
         kRawFull = 0, kRawEmpty = kRawFull + kRaw, kKFull = kRawEmpty + kRaw, kVFull = kKFull + kStages,
         kTurn = kVFull + kStages, kQFull = kTurn + kStages, kSFull = kQFull + 2, kPFull = kSFull + 2, kHalf = kPFull + 4,
         kDone = kHalf + 2,
-kGo = kDone + 2, kExit = kGo + 2, kJoin = kExit + 2, kFree = kJoin + 1, kNumBars = kFree + 1
+kGo = kDone + 2, kExit = kGo + 2, kJoin = kExit + 2, kFree = kJoin + 1, kVDone = kFree + 1,
+        kNumBars = kVDone + 2
     };
     static constexpr uint32_t kOffSlot = kOffBar + 8 * kNumBars;             // tensor-memory address, failure flag
     static constexpr uint32_t kOffRun = (kOffSlot + 8 + 15) / 16 * 16;
@@ -713,6 +714,7 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
             mbar_init(B(S::kDone + k), 1);
             mbar_init(B(S::kGo + k), 1);
             mbar_init(B(S::kExit + k), 1);
+            mbar_init(B(S::kVDone + k), 1);
         }
         mbar_init(B(S::kJoin), kRowsBlock / 32);
         mbar_init(B(S::kFree), kRowsBlock / 32);
@@ -817,9 +819,9 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
             // softmax at once.  So the blocks take turns: a block issues when
             // the other one is half through the Q K^T of its own turn.
             // Batch n of a block (its P V and Q K^T of one tile step) follows batch
-            // n - 1 (block 0) or n (block 1) of the other.  K of the next tile
-            // comes after V of this one from the same converter warps, so one
-            // wait covers both.
+            // n - 1 (block 0) or n (block 1) of the other.  With row blocks K of
+            // the next tile is there as a rule, and comes after V of this one from
+            // the same converter warps: one wait covers both.
             // A tile's number x counts the CTA's tiles (row blocks), or twice the
             // block's own, plus the block (key split): its stage is x mod 2.
             constexpr int step = kKeySplit ? 2 : 1;
@@ -846,8 +848,9 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
                     const uint32_t p_bar = B(S::kPFull + k), p_par = i & 1;
                     const bool waits = turns && batch >= go_lag;
                     const uint32_t go_bar = waits ? B(S::kGo + k) : p_bar, go_par = waits ? (batch - go_lag) & 1 : p_par;
-                    const uint32_t kv_bar = more ? B(S::kKFull + (next & 1)) : B(S::kVFull + (x & 1));
-                    const uint32_t kv_par = more ? (next >> 1) & 1 : (x >> 1) & 1;
+                    const bool k_first = !kKeySplit && more;
+                    const uint32_t kv_bar = k_first ? B(S::kKFull + (next & 1)) : B(S::kVFull + (x & 1));
+                    const uint32_t kv_par = k_first ? (next >> 1) & 1 : (x >> 1) & 1;
                     if (!wait_bars(p_bar, p_par, go_bar, go_par, kv_bar, kv_par, fail, p.dev_status, p.wait_limit))
                         return false;
                     pv(x, 0, j > 0);
@@ -855,6 +858,11 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
                     if (!wait(S::kPFull + 2 + k, i & 1))
                         return false;
                     pv(x, 1, true);
+                    if (kKeySplit) {
+                        umma_commit(B(S::kVDone + k));
+                        if (more && !wait(S::kKFull + (next & 1), (next >> 1) & 1))
+                            return false;
+                    }
                     if (more)
                         qk(next, turns);
                     else if (turns)
@@ -924,10 +932,10 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
             warp_arrive(B(S::kKFull + (x & 1)), lane);
             return true;
         };
-        // V of tile x: its stage was last read by P V of tile x - 2, which the
-        // next turn follows (that of tile x where blocks alternate)
+        // V of tile x: its stage was last read by P V of tile x - 2, which turn
+        // x - 1 follows; a block with stages of its own has its word for it
         auto make_v = [&](int x) {
-            if (x >= kStages && !wait_turn(x - kStages + (kKeySplit ? 2 : 1)))
+            if (x >= kStages && !(kKeySplit ? wait_warp(S::kVDone + (x & 1), ((x >> 1) - 1) & 1) : wait_turn(x - 1)))
                 return false;
 #pragma unroll
             for (int u = 0; u < kGrans; ++u)
@@ -939,24 +947,25 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
         int yb = 0, ib = 0;                      // the CTA's tiles, and the group's, so far
         for_units([&](const Unit &u) {
             if constexpr (kKeySplit) {
-                // each group makes its block's tiles: V of one and K of the next
-                // between the block's turns (one group for both blocks was what
-                // they waited for: 1.5 us a tile against 1.2)
-                const int k = (tid - kSoftmaxThreads) / kConvThreads;
+                // each group makes its block's tiles: V of one as soon as P V of
+                // the one before is done, K of the next after Q K^T of this one
+                // (one group for both blocks was what they waited for)
+                const int k = (tid - kSoftmaxThreads) / kConvThreads, end = yb + u.n_tiles;
                 int y = yb + k, x = 2 * ib + k;
-                const int end = yb + u.n_tiles;
-                bool ok = y >= end || take_k(y);
-                if (ok && y < end) {
+                auto next_k = [&]() {
+                    if (!take_k(y))
+                        return false;
                     take_v(y);
-                    ok = make_k(x);
-                }
-                for (; ok && y < end; y += 2, x += 2, ++ib) {
-                    const bool next = y + 2 < end;
-                    ok = (!next || take_k(y + 2)) && make_v(x);
-                    if (ok && next) {
-                        take_v(y + 2);
-                        ok = make_k(x + 2);
-                    }
+                    return make_k(x);
+                };
+                bool ok = y >= end || next_k();
+                while (ok && y < end) {
+                    ok = make_v(x);
+                    y += 2;
+                    x += 2;
+                    ++ib;
+                    if (ok && y < end)
+                        ok = next_k();
                 }
                 yb = end;
                 return ok;
