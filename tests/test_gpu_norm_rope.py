@@ -197,6 +197,27 @@ def test_fused_append_equals_the_two_calls(T, hq, hkv, G, heads, dtype):
         np.testing.assert_array_equal(got, want)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rot,inter", [(0, False), (32, False), (64, True), (96, False), (96, True)])
+def test_fused_append_of_strided_rows_and_partial_rotations(dtype, rot, inter):
+    """Parts of a fused projection, every rotation: the bytes of the two calls."""
+    T, hq, hkv = 45, 5, 3
+    qkv = rows(T, hq + 2 * hkv, dtype, 30)
+    q, k, v = qkv[:, :hq], qkv[:, hq:hq + hkv], qkv[:, hq + hkv:]
+    w = (1 + 0.5 * rows(1, 1, torch.float32, 31)).reshape(128)
+    pos = torch.arange(T, dtype=torch.int32, device=DEV) + 70000
+    slots = torch.randperm(64, device=DEV)[:T].to(torch.int32)
+    rope = nv.Rope(inv_freqs(rot), interleaved=inter)
+    one, two = (nv.NVFP4Cache.allocate(4, hkv, device=DEV) for _ in range(2))
+    q1, q2 = (torch.empty((T, hq, 128), dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    ko = torch.empty((T, hkv, 128), dtype=dtype, device=DEV)
+    nv.nvfp4kv_qk_norm_rope_append(one, q, k, v, pos, slots, q1, rope, k_weight=w)
+    nv.nvfp4kv_qk_norm_rope(q, k, pos, q2, ko, rope, k_weight=w)
+    nv.nvfp4kv_quantize_append(two, ko, v.contiguous(), slots)
+    assert torch.equal(q1, q2) and torch.equal(one.pool, two.pool)
+    check(ko, *reference(k, w, range(70000, 70000 + T), inv_freqs(rot), inter, 1.0, 1e-6), dtype, "k")
+
+
 def test_neighbours_in_a_page_are_kept():
     """A token written alone leaves the other tokens of its page as they were."""
     hkv = 2
