@@ -855,14 +855,15 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
                         return false;
                     pv(x, 0, j > 0);
                     umma_commit(B(S::kHalf + k));
-                    if (!wait(S::kPFull + 2 + k, i & 1))
+                    // (with split keys K of the next tile is there by now as a rule)
+                    if (!(kKeySplit && more ? wait_bars(B(S::kPFull + 2 + k), i & 1, B(S::kPFull + 2 + k), i & 1,
+                                                        B(S::kKFull + (next & 1)), (next >> 1) & 1, fail, p.dev_status,
+                                                        p.wait_limit)
+                                            : wait(S::kPFull + 2 + k, i & 1)))
                         return false;
                     pv(x, 1, true);
-                    if (kKeySplit) {
+                    if (kKeySplit)
                         umma_commit(B(S::kVDone + k));
-                        if (more && !wait(S::kKFull + (next & 1), (next >> 1) & 1))
-                            return false;
-                    }
                     if (more)
                         qk(next, turns);
                     else if (turns)
