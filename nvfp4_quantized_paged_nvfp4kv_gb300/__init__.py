@@ -184,13 +184,13 @@ def _ptr(t) -> int | None:
     return None if t is None else t.data_ptr()
 
 
-def _stream(stream) -> int | None:
+def _stream(stream, dev=None) -> int | None:
     import torch
     if stream is None:
         # the handle alone, without the Stream object around it (3 us a call)
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
         if raw is not None:
-            return raw(torch.cuda.current_device())
+            return raw(torch.cuda.current_device() if dev is None else dev)
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -267,42 +267,46 @@ class Rope:
         self._f = (ctypes.c_double * max(1, len(vals)))(*vals)     # host array the library reads per call
         self.rotary_dim, self.interleaved, self.scale = 2 * len(vals), bool(interleaved), float(scale)
         self._c = _Rope(ctypes.addressof(self._f), self.rotary_dim, int(self.interleaved), self.scale)
-
-    @property
-    def c(self):
-        return ctypes.byref(self._c)
+        self.c = ctypes.byref(self._c)
 
 
-def _tensors(dtype, *args) -> None:
-    """Check (tensor, name, shape) arguments, None tensors passed over: type,
-    shape, on the current device, contiguous."""
+def _current_device() -> int:
+    """The current CUDA device; -1, which the checks refuse, where there is none."""
     import torch
-    dev = None
-    for t, name, shape in args:
-        if t is None:
-            continue
-        if t.dtype is not dtype:
-            raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-        if t.shape != shape:
-            raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-        if dev is None:
-            dev = torch.cuda.current_device()
-        if t.get_device() != dev:
-            raise ValueError(f"{name}: not on the current CUDA device")
-        if not t.is_contiguous():
-            raise ValueError(f"{name}: must be contiguous")
+    try:
+        get = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+        return get()
+    except (AssertionError, RuntimeError):
+        return -1
 
 
-def _token_rows(t, name, dtype, shape) -> int:
-    """Check rows [tokens][heads][128] that may be strided by token (views of a
-    fused projection); returns the token stride in elements."""
-    import torch
+def _bad(t, name, dtype, shape, dev):
+    """Raise for a tensor argument that is not what the call needs."""
     if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.get_device() != torch.cuda.current_device():
+    if t.get_device() != dev or dev < 0:
         raise ValueError(f"{name}: not on the current CUDA device")
+    raise ValueError(f"{name}: must be contiguous")
+
+
+def _tensors(dev, dtype, *args) -> None:
+    """Check (tensor, name, shape) arguments, None tensors passed over: type,
+    shape, on device dev, contiguous."""
+    for t, name, shape in args:
+        if t is not None and not (t.dtype is dtype and t.shape == shape and t.get_device() == dev and
+                                  t.is_contiguous()):
+            _bad(t, name, dtype, shape, dev)
+    if dev < 0:
+        raise ValueError("no CUDA device")
+
+
+def _token_rows(dev, t, name, dtype, shape) -> int:
+    """Check rows [tokens][heads][128] that may be strided by token (views of a
+    fused projection); returns the token stride in elements."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or dev < 0:
+        _bad(t, name, dtype, shape, dev)
     step, head, one = t.stride()
     if shape[0] > 0 and (one != 1 or (shape[1] > 1 and head != shape[2])):
         raise ValueError(f"{name}: heads and channels must be contiguous")
@@ -494,20 +498,21 @@ def nvfp4kv_paged_extend(cache: NVFP4Cache, q, q_indptr, block_table, seq_lens, 
     import torch
     if sm_scale is None:
         sm_scale = 1.0 / math.sqrt(HEAD_DIM)
+    dev = _current_device()
     B, pages = block_table.shape
     rows, Hq, _ = q.shape
-    _tensors(torch.bfloat16, (q, "q", (rows, Hq, HEAD_DIM)))
-    _tensors(out.dtype, (out, "out", (rows, Hq, HEAD_DIM)))
-    _tensors(torch.uint8, (cache.pool, "cache", cache.pool.shape),
+    _tensors(dev, torch.bfloat16, (q, "q", (rows, Hq, HEAD_DIM)))
+    _tensors(dev, out.dtype, (out, "out", (rows, Hq, HEAD_DIM)))
+    _tensors(dev, torch.uint8, (cache.pool, "cache", cache.pool.shape),
              (workspace, "workspace", (0 if workspace is None else workspace.numel(),)))
-    _tensors(torch.int32, (q_indptr, "q_indptr", (B + 1,)), (block_table, "block_table", (B, pages)),
+    _tensors(dev, torch.int32, (q_indptr, "q_indptr", (B + 1,)), (block_table, "block_table", (B, pages)),
              (seq_lens, "seq_lens", (B,)), (dev_status, "dev_status", (1,)))
     if max_q_len is None:
         max_q_len = int((q_indptr[1:] - q_indptr[:-1]).max().item()) if B > 0 else 0
     st = load().nvfp4kv_paged_extend(
         cache.c, _ptr(q), _ptr(q_indptr), rows, int(max_q_len), B, Hq, _ptr(block_table), pages, _ptr(seq_lens),
         int(window), float(sm_scale), _ptr(out), _dtype_code(out), _ptr(workspace),
-        0 if workspace is None else workspace.numel(), _ptr(dev_status), _stream(stream))
+        0 if workspace is None else workspace.numel(), _ptr(dev_status), _stream(stream, dev))
     _check(st, "nvfp4kv_paged_extend")
 
 
@@ -519,9 +524,10 @@ def nvfp4kv_plan_step(context_lens, new_lens, block_table, num_pages, free_pages
     kv_indptr [B], slot_mapping and positions [max_tokens] (-1 behind the last
     token) and num_free_out [1] (which may be num_free)."""
     import torch
+    dev = _current_device()
     B, pages = block_table.shape
     T, F = slot_mapping.numel(), free_pages.numel()
-    _tensors(torch.int32, (context_lens, "context_lens", (B,)), (new_lens, "new_lens", (B,)),
+    _tensors(dev, torch.int32, (context_lens, "context_lens", (B,)), (new_lens, "new_lens", (B,)),
              (block_table, "block_table", (B, pages)), (free_pages, "free_pages", (F,)), (num_free, "num_free", (1,)),
              (num_free_out, "num_free_out", (1,)), (seq_lens, "seq_lens", (B,)), (q_indptr, "q_indptr", (B + 1,)),
              (slot_mapping, "slot_mapping", (T,)), (positions, "positions", (T,)), (kv_indptr, "kv_indptr", (B,)),
@@ -529,7 +535,7 @@ def nvfp4kv_plan_step(context_lens, new_lens, block_table, num_pages, free_pages
     st = load().nvfp4kv_plan_step(
         _ptr(context_lens), _ptr(new_lens), B, _ptr(block_table), pages, int(num_pages), _ptr(free_pages), F,
         _ptr(num_free), _ptr(num_free_out), _ptr(seq_lens), _ptr(q_indptr), _ptr(kv_indptr), _ptr(slot_mapping),
-        _ptr(positions), T, _ptr(dev_status), _stream(stream))
+        _ptr(positions), T, _ptr(dev_status), _stream(stream, dev))
     _check(st, "nvfp4kv_plan_step")
 
 
@@ -539,22 +545,23 @@ def nvfp4kv_release_pages(old_lens, keep_lens, block_table, num_pages, free_page
     tokens, int32 [B]) back on the stack free_pages[: num_free]; num_free_out
     [1] may be num_free."""
     import torch
+    dev = _current_device()
     B, pages = block_table.shape
     F = free_pages.numel()
-    _tensors(torch.int32, (old_lens, "old_lens", (B,)), (keep_lens, "keep_lens", (B,)),
+    _tensors(dev, torch.int32, (old_lens, "old_lens", (B,)), (keep_lens, "keep_lens", (B,)),
              (block_table, "block_table", (B, pages)), (free_pages, "free_pages", (F,)), (num_free, "num_free", (1,)),
              (num_free_out, "num_free_out", (1,)), (dev_status, "dev_status", (1,)))
     st = load().nvfp4kv_release_pages(
         _ptr(old_lens), _ptr(keep_lens), B, _ptr(block_table), pages, int(num_pages), _ptr(free_pages), F,
-        _ptr(num_free), _ptr(num_free_out), _ptr(dev_status), _stream(stream))
+        _ptr(num_free), _ptr(num_free_out), _ptr(dev_status), _stream(stream, dev))
     _check(st, "nvfp4kv_release_pages")
 
 
-def _head_norm(q_weight, k_weight, eps):
+def _head_norm(dev, q_weight, k_weight, eps):
     first = k_weight if q_weight is None else q_weight
     if first is None:
         return None
-    _tensors(first.dtype, (q_weight, "q_weight", (HEAD_DIM,)), (k_weight, "k_weight", (HEAD_DIM,)))
+    _tensors(dev, first.dtype, (q_weight, "q_weight", (HEAD_DIM,)), (k_weight, "k_weight", (HEAD_DIM,)))
     return ctypes.byref(_HeadNorm(_ptr(q_weight), _ptr(k_weight), _dtype_code(first), float(eps)))
 
 
@@ -565,17 +572,18 @@ def nvfp4kv_qk_norm_rope(q, k, positions, q_out, k_out, rope: Rope | None = None
     projection are) at positions int32 [T] (negative: token left out) into
     q_out (bf16) and k_out (k's type)."""
     import torch
+    dev = _current_device()
     T, Hq, _ = q.shape
     Hkv, code = k.shape[1], _dtype_code(q)
-    q_step = _token_rows(q, "q", q.dtype, (T, Hq, HEAD_DIM))
-    k_step = _token_rows(k, "k", q.dtype, (T, Hkv, HEAD_DIM))
-    _tensors(torch.int32, (positions, "positions", (T,)), (dev_status, "dev_status", (1,)))
-    _tensors(torch.bfloat16, (q_out, "q_out", (T, Hq, HEAD_DIM)))
-    _tensors(q.dtype, (k_out, "k_out", (T, Hkv, HEAD_DIM)))
+    q_step = _token_rows(dev, q, "q", q.dtype, (T, Hq, HEAD_DIM))
+    k_step = _token_rows(dev, k, "k", q.dtype, (T, Hkv, HEAD_DIM))
+    _tensors(dev, torch.int32, (positions, "positions", (T,)), (dev_status, "dev_status", (1,)))
+    _tensors(dev, torch.bfloat16, (q_out, "q_out", (T, Hq, HEAD_DIM)))
+    _tensors(dev, q.dtype, (k_out, "k_out", (T, Hkv, HEAD_DIM)))
     st = load().nvfp4kv_qk_norm_rope(
         _ptr(q), q_step, _ptr(k), k_step, code, T, Hq, Hkv, _ptr(positions), None if rope is None else rope.c,
-        _head_norm(q_weight, k_weight, eps), _ptr(q_out), _ptr(k_out), _ptr(dev_status),
-        _stream(stream))
+        _head_norm(dev, q_weight, k_weight, eps), _ptr(q_out), _ptr(k_out), _ptr(dev_status),
+        _stream(stream, dev))
     _check(st, "nvfp4kv_qk_norm_rope")
 
 
@@ -585,19 +593,20 @@ def nvfp4kv_qk_norm_rope_append(cache: NVFP4Cache, q, k, v, positions, slot_mapp
     """nvfp4kv_qk_norm_rope with the finished keys and the values v [T][Hkv][128]
     written into the NVFP4 cache at slot_mapping int32 [T] instead of k_out."""
     import torch
+    dev = _current_device()
     T, Hq, _ = q.shape
     Hkv, code = cache.num_kv_heads, _dtype_code(q)
-    q_step = _token_rows(q, "q", q.dtype, (T, Hq, HEAD_DIM))
-    k_step = _token_rows(k, "k", q.dtype, (T, Hkv, HEAD_DIM))
-    v_step = _token_rows(v, "v", q.dtype, (T, Hkv, HEAD_DIM))
-    _tensors(torch.int32, (positions, "positions", (T,)), (slot_mapping, "slot_mapping", (T,)),
+    q_step = _token_rows(dev, q, "q", q.dtype, (T, Hq, HEAD_DIM))
+    k_step = _token_rows(dev, k, "k", q.dtype, (T, Hkv, HEAD_DIM))
+    v_step = _token_rows(dev, v, "v", q.dtype, (T, Hkv, HEAD_DIM))
+    _tensors(dev, torch.int32, (positions, "positions", (T,)), (slot_mapping, "slot_mapping", (T,)),
              (dev_status, "dev_status", (1,)))
-    _tensors(torch.bfloat16, (q_out, "q_out", (T, Hq, HEAD_DIM)))
-    _tensors(torch.uint8, (cache.pool, "cache", cache.pool.shape))
+    _tensors(dev, torch.bfloat16, (q_out, "q_out", (T, Hq, HEAD_DIM)))
+    _tensors(dev, torch.uint8, (cache.pool, "cache", cache.pool.shape))
     st = load().nvfp4kv_qk_norm_rope_append(
         cache.c, _ptr(q), q_step, _ptr(k), k_step, _ptr(v), v_step, code, T, Hq, _ptr(positions), _ptr(slot_mapping),
-        None if rope is None else rope.c, _head_norm(q_weight, k_weight, eps), _ptr(q_out), _ptr(dev_status),
-        _stream(stream))
+        None if rope is None else rope.c, _head_norm(dev, q_weight, k_weight, eps), _ptr(q_out), _ptr(dev_status),
+        _stream(stream, dev))
     _check(st, "nvfp4kv_qk_norm_rope_append")
 
 
