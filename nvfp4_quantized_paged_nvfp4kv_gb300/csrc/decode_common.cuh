@@ -381,7 +381,8 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, kDecodeCtasPerSm) decode_ke
     // The merge kernel that follows may start its own prologue meanwhile.
     pdl_launch_dependents();
     // The work split and the block-table lookups read only the lengths and the
-    // block table, which no kernel of this library writes; they run before the
+    // block table, which only the step-table kernels of this library write, and
+    // those are over before anything behind them starts; so they run before the
     // wait for the previous kernel in the stream, overlapping its tail.  The
     // cache records, q, the new K/V, the output and the workspace are touched
     // only after the wait.
@@ -398,8 +399,13 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, kDecodeCtasPerSm) decode_ke
 
     // The worker: this warp's page-heads [lo, hi).
     auto run_worker = [&]() {
-    if (lo >= hi)
+    if (lo >= hi) {
+        // (a grid without any work still ends behind the kernel before it: what
+        // comes next waits for this grid only)
+        if (T == 0)
+            pdl_wait();
         return;
+    }
 
     // ---- producer: page-head lookahead window, lane l holds index win + l ----
     // Lane l looks up page-head win + l of the current window and of the next
