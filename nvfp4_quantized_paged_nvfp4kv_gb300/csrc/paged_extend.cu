@@ -90,8 +90,7 @@ struct Shape {
     enum : int {
         kRawFull = 0, kRawEmpty = kRawFull + kRaw, kKFull = kRawEmpty + kRaw, kVFull = kKFull + kStages,
         kTurn = kVFull + kStages, kQFull = kTurn + kStages, kSFull = kQFull + 2, kPFull = kSFull + 2, kHalf = kPFull + 4,
-        kDone = kHalf + 2,
-kGo = kDone + 2, kExit = kGo + 2, kJoin = kExit + 2, kFree = kJoin + 1, kVDone = kFree + 1,
+        kDone = kHalf + 2, kGo = kDone + 2, kExit = kGo + 2, kJoin = kExit + 2, kFree = kJoin + 1, kVDone = kFree + 1,
         kNumBars = kVDone + 2
     };
     static constexpr uint32_t kOffSlot = kOffBar + 8 * kNumBars;             // tensor-memory address, failure flag
@@ -443,7 +442,7 @@ __device__ __forceinline__ Place find_cut(const PagedExtendParams &p, long long 
     Chunk c;
     const int n = row_tiles_of<kRows>(p, x, c);
     for (int i0 = 0; i0 < n; i0 += 32) {
-        Unit u;
+        Unit u{};
         int w = 0;
         if (i0 + lane < n) {
             u.set<kRows>(p, c, i0 + lane);
@@ -496,7 +495,7 @@ __device__ __forceinline__ void find_run(const PagedExtendParams &p, int worker,
             const int n = row_tiles_of<kRows>(p, b, c);
             if (n == 0 && sub == 0 && worker == 0 && !read_chunk(p, b, c))
                 report(p.dev_status, NVFP4KV_DEV_BAD_LEN);
-            Unit u;
+            Unit u{};
             for (int i = sub; i < n; i += width) {
                 u.set<kRows>(p, c, i);
                 w += u.all + 1;
@@ -661,6 +660,38 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     constexpr int kRows = S::kRows;
     Run *run = reinterpret_cast<Run *>(gbase + S::kOffRun);
+    if (tid == 0) {
+        for (int k = 0; k < S::kRaw; ++k) {
+            mbar_init(B(S::kRawFull + k), 1);
+            mbar_init(B(S::kRawEmpty + k), kConvThreads / 32);
+        }
+        for (int k = 0; k < kStages; ++k) {
+            mbar_init(B(S::kKFull + k), kConvThreads / 32);
+            mbar_init(B(S::kVFull + k), kConvThreads / 32);
+            mbar_init(B(S::kTurn + k), kKeySplit ? 1 : 2);
+        }
+        for (int k = 0; k < 2; ++k) {
+            mbar_init(B(S::kQFull + k), kRowsBlock / 32);
+            mbar_init(B(S::kSFull + k), 1);
+            mbar_init(B(S::kPFull + k), kRowsBlock / 32);
+            mbar_init(B(S::kPFull + 2 + k), kRowsBlock / 32);
+            mbar_init(B(S::kHalf + k), 1);
+            mbar_init(B(S::kDone + k), 1);
+            mbar_init(B(S::kGo + k), 1);
+            mbar_init(B(S::kExit + k), 1);
+            mbar_init(B(S::kVDone + k), 1);
+        }
+        mbar_init(B(S::kJoin), kRowsBlock / 32);
+        mbar_init(B(S::kFree), kRowsBlock / 32);
+        *fail = 0;
+        fence_mbar_init();
+    }
+    // nothing before this reads or writes what other kernels do
+    pdl_wait();
+    if (tid == 0 && p.partials != nullptr) {
+        Note *note = notes_of<kRows>(p) + blockIdx.x;
+        note->tail = note->head = 0;
+    }
     find_run<kRows>(p, blockIdx.x, gridDim.x, reinterpret_cast<long long *>(gbase + S::kOffK), run);
     const Run start = *run;
     // The units of this CTA's run, one after the other: fn(unit) for each with
@@ -694,36 +725,6 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
         u.h = start.h;
         u.b = start.b;
         ask_for_q(u, start.tile);
-    }
-    if (tid == 0) {
-        for (int k = 0; k < S::kRaw; ++k) {
-            mbar_init(B(S::kRawFull + k), 1);
-            mbar_init(B(S::kRawEmpty + k), kConvThreads / 32);
-        }
-        for (int k = 0; k < kStages; ++k) {
-            mbar_init(B(S::kKFull + k), kConvThreads / 32);
-            mbar_init(B(S::kVFull + k), kConvThreads / 32);
-            mbar_init(B(S::kTurn + k), kKeySplit ? 1 : 2);
-        }
-        for (int k = 0; k < 2; ++k) {
-            mbar_init(B(S::kQFull + k), kRowsBlock / 32);
-            mbar_init(B(S::kSFull + k), 1);
-            mbar_init(B(S::kPFull + k), kRowsBlock / 32);
-            mbar_init(B(S::kPFull + 2 + k), kRowsBlock / 32);
-            mbar_init(B(S::kHalf + k), 1);
-            mbar_init(B(S::kDone + k), 1);
-            mbar_init(B(S::kGo + k), 1);
-            mbar_init(B(S::kExit + k), 1);
-            mbar_init(B(S::kVDone + k), 1);
-        }
-        mbar_init(B(S::kJoin), kRowsBlock / 32);
-        mbar_init(B(S::kFree), kRowsBlock / 32);
-        *fail = 0;
-        if (p.workers > 1) {
-            Note *note = notes_of<kRows>(p) + blockIdx.x;
-            note->tail = note->head = 0;
-        }
-        fence_mbar_init();
     }
     if (warp == S::kMmaWarp)
         tmem_alloc(base + S::kOffSlot, 2 * kTmBlock);
@@ -774,6 +775,9 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
             }
             return true;
         });
+        // the next kernel's launch overlaps the last tiles (it waits for this
+        // one's end before it reads anything)
+        pdl_launch_dependents();
         // nothing issued may still be in flight when the CTA exits
         for (int i = max(0, issued - S::kRaw); i < issued; ++i)
             if (!mbar_wait_bounded(B(S::kRawFull + i % S::kRaw), (i / S::kRaw) & 1, kWaitLimit))
@@ -1258,6 +1262,7 @@ __global__ void __launch_bounds__(256) paged_extend_join_kernel(const __grid_con
 {
     constexpr int kJoinRows = kJoinRowsOf<kRows>, kAhead = 8 / kJoinRows;
     pdl_wait();
+    pdl_launch_dependents();
     const int lane = threadIdx.x & 31, first = blockIdx.x;
     const Note *notes = notes_of<kRows>(p);
     const int4 n0 = __ldcg(reinterpret_cast<const int4 *>(notes + first));       // tail, h, row0, rows
@@ -1372,7 +1377,17 @@ ExtendShape paged_extend_shape(int64_t q_rows, int64_t max_q_len, int64_t batch,
     const int64_t runs = hkv * (most < filled ? most : filled) * ((keys + kKeys - 1) / kKeys + 2) / kMinRun;
     s.workers = static_cast<int>(runs < 1 ? 1 : (runs < sms ? runs : sms));
     const size_t piece = (s.key_split ? kPieceFloats<kRowsBlock> : kPieceFloats<2 * kRowsBlock>)*sizeof(float);
-    s.workspace = s.workers > 1 ? s.workers * (2 * piece + sizeof(Note)) : 0;
+    // No unit is cut, and nothing left to join, where none has more than 2 kSnap
+    // tiles (find_cut moves every cut to a border).
+    int64_t tiles = (max_pages * kPageSize + kKeys - 1) / kKeys;
+    if (window > 0) {
+        // the keys of a row tile's tokens begin anywhere in a key tile
+        const int64_t span = window + (max_q_len < rows / group + 2 ? max_q_len : rows / group + 2);
+        const int64_t most_tiles = (span + kKeys - 1) / kKeys + 1;
+        tiles = most_tiles < tiles ? most_tiles : tiles;
+    }
+    const bool cuts = s.workers > 1 && tiles > 2 * kSnap;
+    s.workspace = cuts ? s.workers * (2 * piece + sizeof(Note)) : 0;
     return s;
 }
 
@@ -1384,9 +1399,8 @@ static cudaError_t launch_extend(const PagedExtendParams &p, cudaStream_t s)
                                          S::kSmem);
     if (e != cudaSuccess)
         return e;
-    paged_extend_kernel<kKeySplit><<<p.workers, S::kThreads, S::kSmem, s>>>(p);
-    e = cudaGetLastError();
-    if (e != cudaSuccess || p.workers == 1)
+    e = launch_pdl(paged_extend_kernel<kKeySplit>, dim3(p.workers), dim3(S::kThreads), S::kSmem, s, p);
+    if (e != cudaSuccess || p.partials == nullptr)
         return e;
     return launch_pdl(paged_extend_join_kernel<S::kRows>, dim3(p.workers - 1, S::kRows / (8 * kJoinRowsOf<S::kRows>)), dim3(256), 0, s, p);
 }
@@ -1395,6 +1409,8 @@ cudaError_t launch_paged_extend(const PagedExtendParams &in, const ExtendShape &
 {
     PagedExtendParams p = in;
     p.workers = shape.workers;
+    if (shape.workspace == 0)
+        p.partials = nullptr;                    // no pieces
     return shape.key_split ? launch_extend<true>(p, s) : launch_extend<false>(p, s);
 }
 

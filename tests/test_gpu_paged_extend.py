@@ -355,3 +355,43 @@ def test_wait_runs_out_then_recovers():
         nv.nvfp4kv_set_wait_limit(prev)
     c.status.zero_()
     check(c.run(), c, c.want(), torch.float32)
+
+
+@pytest.mark.parametrize("lens,chunks,hq,hkv,window", [
+    ((1024, 1000, 3, 513, 0, 896) * 5, (16, 1, 3, 7, 0, 16) * 5, 8, 2, 0),       # key split, tables of 64 pages
+    ((1024, 700, 1024), (400, 129, 1), 8, 2, 0),                                 # row blocks
+    ((5000, 4097, 130, 2500) * 4, (8, 1, 8, 3) * 4, 16, 4, 888),                 # windows that begin anywhere in a tile
+    ((4000, 2049), (900, 333), 8, 4, 766),
+])
+def test_short_key_ranges_need_no_workspace(lens, chunks, hq, hkv, window):
+    """Where no row tile sees more than eight 128-key tiles' worth of keys, no
+    run is cut inside one and there is nothing to join."""
+    c = Case(lens, chunks, hq, hkv, seed=21, spare_entries=0)
+    size = nv.nvfp4kv_paged_extend_workspace_size
+    args = (c.rows, max(chunks), len(lens), hq, hkv)
+    assert size(*args, c.table.shape[1], window) == 0
+    assert (size(*args, c.table.shape[1], window + 1) if window else size(*args, c.table.shape[1] + 1, 0)) > 0
+    out = torch.full((c.rows, hq, 128), 77.0, device=DEV)
+    nv.nvfp4kv_paged_extend(c.cache, c.q, c.q_indptr, c.table_d, c.seq_lens, out, None, max_q_len=max(chunks),
+                            window=window, dev_status=c.status)
+    check(out, c, c.want(window=window), torch.float32)
+
+
+def test_calls_in_a_row_share_a_workspace():
+    """Each call's kernels may be launched before the last call's have ended;
+    a decode without any work between them does not let them pass."""
+    a, b = Case((5000, 900), (5, 16), 8, 2, seed=22), Case((3000,), (300,), 8, 2, seed=23)
+    ws = torch.empty(max(a.workspace().numel(), b.workspace().numel()), dtype=torch.uint8, device=DEV)
+    want_a, want_b = a.run(ws=ws).clone(), b.run(ws=ws).clone()
+    torch.cuda.synchronize()
+    none = torch.zeros(2, dtype=torch.int32, device=DEV)
+    q, o, dws = torch.zeros((2, 8, 128), dtype=torch.bfloat16, device=DEV), torch.empty((2, 8, 128), device=DEV), nv.new_workspace()
+    outs = []
+    for _ in range(8):
+        outs.append((a.run(ws=ws), want_a))
+        nv.nvfp4kv_paged_decode(a.cache, q, a.table_d, none, o, dws)
+        outs.append((b.run(ws=ws), want_b))
+        outs.append((a.run(ws=ws), want_a))
+    for got, want in outs:
+        assert torch.equal(got, want)
+    assert not o.any()
