@@ -44,9 +44,11 @@
 //
 // Work split.  A unit is a row tile of one sequence and kv head with all its key
 // tiles.  The units' tiles, heads outermost, form one sequence, a unit counting
-// one more for its own cost, which is cut into equal runs, one a resident CTA:
-// no wave is left half empty (2.5 waves of equal units took 3) and few rows
-// with many keys still occupy every SM.  A CTA's run begins and ends inside a
+// four more for its own cost (with one a prompt of 4,096 tokens took 176 us, not
+// 154), which is cut into equal runs, one a resident CTA: no wave is left half
+// empty and few rows with many keys still occupy every SM (whole units, cut by a
+// fixed number where there were few: 2,048 tokens at 32K 1.37 ms, 1.14 in runs).
+// A CTA's run begins and ends inside a
 // unit as a rule: of those it leaves O, reference and sum in the workspace (at
 // most two pieces), which a second kernel joins; the units inside are written
 // directly.  Loads and conversions for the next unit run behind the end of the
@@ -406,10 +408,13 @@ struct Run {
 };
 
 constexpr int kMinRun = 3;               // a run is at least this long, else fewer CTAs take part
-// A cut that leaves no more than this of a unit on one side moves to the unit's
-// border: a piece more costs a CTA some 8 us, as much as four to five tiles,
-// and the join.
-constexpr int kSnap = 4;
+// What a unit costs beside its tiles, in tiles (Q in, O out, the pipeline filled
+// anew: some 8 us), and so also what a cut inside a unit costs.
+constexpr int kUnitCost = 4;
+// A cut moves to its unit's nearer border where it would leave no more than
+// kSnap tiles of the unit on one side, or where the unit has no more than kWhole
+// (a call without cuts needs no join: 700 tokens of 32 + 8 heads 23 us, 28 with).
+constexpr int kSnap = 2, kWhole = 8;
 
 // A place in the sequence of units: `off` into row tile `tile` of sequence b, kv
 // head h; `at` counts from the beginning.
@@ -446,7 +451,7 @@ __device__ __forceinline__ Place find_cut(const PagedExtendParams &p, long long 
         int w = 0;
         if (i0 + lane < n) {
             u.set<kRows>(p, c, i0 + lane);
-            w = u.all + 1;
+            w = u.all + kUnitCost;
         }
         long long incl = w;
 #pragma unroll
@@ -460,12 +465,11 @@ __device__ __forceinline__ Place find_cut(const PagedExtendParams &p, long long 
             const int hit = __ffs(past) - 1, size = __shfl_sync(kFullMask, w, hit);
             r.tile = i0 + hit;
             r.off = static_cast<int>(rest - __shfl_sync(kFullMask, incl - w, hit));
-            if (r.off <= kSnap && r.off <= size - r.off) {
-                r.at -= r.off;
-                r.off = 0;
-            } else if (size - r.off <= kSnap) {  // to the unit's end: the next one's beginning
-                r.at += size - r.off;
-                ++r.tile;
+            const int before = r.off - kUnitCost, behind = size - r.off;     // tiles
+            if (before <= kSnap || behind <= kSnap || before + behind <= kWhole) {
+                const bool down = before <= behind;
+                r.at += down ? -r.off : behind;
+                r.tile += !down;                 // (up: the next one's beginning)
                 r.off = 0;
             }
             break;
@@ -498,7 +502,7 @@ __device__ __forceinline__ void find_run(const PagedExtendParams &p, int worker,
             Unit u{};
             for (int i = sub; i < n; i += width) {
                 u.set<kRows>(p, c, i);
-                w += u.all + 1;
+                w += u.all + kUnitCost;
             }
         }
         for (int o = 1; o < width; o <<= 1)
@@ -606,10 +610,10 @@ __device__ __forceinline__ bool next_unit(const PagedExtendParams &p, Walk &w, i
             continue;
         }
         u.set<kRows>(p, w.c, w.at);
-        // place 0 of a unit is its own cost, place 1 + i key tile i
-        const int take = static_cast<int>(min(w.left, static_cast<long long>(u.all + 1 - w.off)));
-        u.from = max(0, w.off - 1);
-        u.n_tiles = max(0, w.off + take - 1) - u.from;
+        // the first places of a unit are its own cost, then come its tiles
+        const int take = static_cast<int>(min(w.left, static_cast<long long>(u.all + kUnitCost - w.off)));
+        u.from = max(0, w.off - kUnitCost);
+        u.n_tiles = max(0, w.off + take - kUnitCost) - u.from;
         w.left -= take;
         ++w.at;
         w.off = 0;
@@ -1374,11 +1378,11 @@ ExtendShape paged_extend_shape(int64_t q_rows, int64_t max_q_len, int64_t batch,
     // (the CTAs see the true lengths and leave out those that would have less
     // than kMinRun tiles)
     const int64_t sms = sm_count() > 0 ? sm_count() : 1;
-    const int64_t runs = hkv * (most < filled ? most : filled) * ((keys + kKeys - 1) / kKeys + 2) / kMinRun;
+    const int64_t runs = hkv * (most < filled ? most : filled) * ((keys + kKeys - 1) / kKeys + 1 + kUnitCost) / kMinRun;
     s.workers = static_cast<int>(runs < 1 ? 1 : (runs < sms ? runs : sms));
     const size_t piece = (s.key_split ? kPieceFloats<kRowsBlock> : kPieceFloats<2 * kRowsBlock>)*sizeof(float);
-    // No unit is cut, and nothing left to join, where none has more than 2 kSnap
-    // tiles (find_cut moves every cut to a border).
+    // No unit is cut, and there is nothing to join, where none has more than
+    // kWhole tiles.
     int64_t tiles = (max_pages * kPageSize + kKeys - 1) / kKeys;
     if (window > 0) {
         // the keys of a row tile's tokens begin anywhere in a key tile
@@ -1386,7 +1390,7 @@ ExtendShape paged_extend_shape(int64_t q_rows, int64_t max_q_len, int64_t batch,
         const int64_t most_tiles = (span + kKeys - 1) / kKeys + 1;
         tiles = most_tiles < tiles ? most_tiles : tiles;
     }
-    const bool cuts = s.workers > 1 && tiles > 2 * kSnap;
+    const bool cuts = s.workers > 1 && tiles > kWhole;
     s.workspace = cuts ? s.workers * (2 * piece + sizeof(Note)) : 0;
     return s;
 }
