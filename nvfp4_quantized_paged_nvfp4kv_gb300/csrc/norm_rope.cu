@@ -134,42 +134,25 @@ struct NrShared {
     uint64_t bar[kNrWarps][Ring<true>::kStages];
 };
 
-// A place in a warp's sequence of quads: quads quad .. end - 1 of token t's run
-// `run` are left; quads 0 .. p.q_quads - 1 are queries, the others keys.
+// A place in a warp's quads, which are `left` from quad `quad` of token t on;
+// quads 0 .. p.q_quads - 1 of a token are queries, the others keys.
 struct Cursor {
-    int t, run, quad, end;
+    int t, quad;
+    long long left;
 
-    // the run at (t, run), if there is one
-    __device__ __forceinline__ bool open(const NormRopeParams &p)
+    // quads from .. to - 1 of the call
+    __device__ __forceinline__ Cursor(const NormRopeParams &p, long long from, long long to)
+        : t(static_cast<int>(from / p.quads)), quad(static_cast<int>(from - static_cast<long long>(t) * p.quads)),
+          left(to - from)
     {
-        const int quads = p.q_quads + (p.hkv + 3) / 4;
-        quad = quads * run / p.token_jobs;
-        end = quads * (run + 1) / p.token_jobs;
-        return t < p.num_tokens;
-    }
-    __device__ __forceinline__ bool first(const NormRopeParams &p, long long job)
-    {
-        const long long at = job / p.token_jobs;
-        t = at < p.num_tokens ? static_cast<int>(at) : p.num_tokens;
-        run = static_cast<int>(job - at * p.token_jobs);
-        return open(p);
-    }
-    // dt, dr: the warp's stride in tokens and runs
-    __device__ __forceinline__ bool next(const NormRopeParams &p, int dt, int dr)
-    {
-        run += dr;
-        const int carry = run >= p.token_jobs ? 1 : 0;
-        run -= carry ? p.token_jobs : 0;
-        t = t > p.num_tokens - dt - carry ? p.num_tokens : t + dt + carry;
-        return open(p);
     }
 };
 
-// The row jobs of one warp: `first`, first + stride, ...  False when a wait for
-// staged rows gave up.
+// One warp's rows, quads from .. to - 1 of the call.  False when a wait for staged
+// rows gave up.
 template <bool kBf16, bool kAppend>
-__device__ __forceinline__ bool rows_of_warp(const NormRopeParams &p, NrShared &sh, uint32_t ring, long long first,
-                                             long long stride)
+__device__ __forceinline__ bool rows_of_warp(const NormRopeParams &p, NrShared &sh, uint32_t ring, long long from,
+                                             long long to)
 {
     using G = Ring<kBf16>;
     const int lane = threadIdx.x & 31, part = lane & 7, sub = lane >> 3, warp = threadIdx.x >> 5;
@@ -179,9 +162,7 @@ __device__ __forceinline__ bool rows_of_warp(const NormRopeParams &p, NrShared &
     const int c0 = 8 * part;                     // channel of value j: c0 + (j & 7) + 64 (j / 8)
 
     // stage st gets the quad at f, which moves on (whole warp; lane 0 copies)
-    const int dt = static_cast<int>(stride / p.token_jobs), dr = static_cast<int>(stride % p.token_jobs);
-    Cursor f, w;
-    bool more = f.first(p, first);
+    Cursor f(p, from, to), w = f;
     auto fetch = [&](int st) {
         const bool is_k = f.quad >= p.q_quads;
         const int head = 4 * (is_k ? f.quad - p.q_quads : f.quad);
@@ -193,20 +174,25 @@ __device__ __forceinline__ bool rows_of_warp(const NormRopeParams &p, NrShared &
             bulk_g2s(ring + st * G::kStage, static_cast<const uint8_t *>(is_k ? p.k : p.q) + at * size, rows * G::kRow,
                      bar + 8 * st);
         }
-        if (++f.quad == f.end)
-            more = f.next(p, dt, dr);
+        --f.left;
+        if (++f.quad == p.quads) {
+            f.quad = 0;
+            ++f.t;
+        }
     };
     int issued = 0;
-    for (; issued < G::kStages && more; ++issued)
+    for (; issued < G::kStages && f.left > 0; ++issued)
         fetch(issued);
 
     int st = 0, done = 0;
     uint32_t phase = 0;
     bool ok = true;
-    for (bool has = w.first(p, first); ok && has; has = w.next(p, dt, dr)) {
+    for (; ok && w.left > 0; ++w.t, w.quad = 0) {
     const int t = w.t;
+    const int end = static_cast<int>(min(w.left + w.quad, static_cast<long long>(p.quads)));
+    w.left -= end - w.quad;
     const int pos = p.positions[t];              // < 0: a token that is not there, nothing of it is written
-    __syncwarp();                                // (the last job's angles have been read)
+    __syncwarp();                                // (the last token's angles have been read)
     for (int i = lane; i < half; i += 32) {
         const uint64_t turn = sh.freq[i] * static_cast<uint64_t>(static_cast<uint32_t>(max(pos, 0)));
         float sn, c;
@@ -254,7 +240,7 @@ __device__ __forceinline__ bool rows_of_warp(const NormRopeParams &p, NrShared &
         const int chunk = 8 * k + part;
         return 8 * chunk < half ? chunk + half / 8 : (8 * chunk < p.rot ? chunk - half / 8 : chunk);
     };
-    for (int quad = w.quad; quad < w.end; ++quad) {
+    for (int quad = w.quad; quad < end; ++quad) {
         const bool is_k = quad >= p.q_quads;
         if (quad == w.quad || quad == p.q_quads)
             tables(sh.weight[is_k]);
@@ -266,7 +252,7 @@ __device__ __forceinline__ bool rows_of_warp(const NormRopeParams &p, NrShared &
         RawBlock<kBf16> cur;                     // (rows behind the last head: what the stage held, not written)
         read_pieces<kBf16>(ring + st * G::kStage + sub * G::kRow, part, cur);
         ++done;
-        if (more) {
+        if (f.left > 0) {
             fence_async_shared();                // the stage's reads before its next copy
             __syncwarp();
             fetch(st);
@@ -445,8 +431,8 @@ __device__ __forceinline__ void v_pair_job(const NormRopeParams &p, int pr, int 
     }
 }
 
-// Warp jobs, token-major: a token's quads in p.token_jobs runs; then the V
-// blocks, one a thread.
+// Each warp takes an equal run of the call's quads, token-major, and then of the
+// V blocks, one a thread.
 template <bool kBf16, bool kAppend>
 __global__ void __launch_bounds__(kNrThreads, Ring<kBf16>::kCtas)
     norm_rope_kernel(const __grid_constant__ NormRopeParams p)
@@ -475,16 +461,16 @@ __global__ void __launch_bounds__(kNrThreads, Ring<kBf16>::kCtas)
     if (threadIdx.x < kHeadDim / 2)
         sh.freq[threadIdx.x] = p.freq[threadIdx.x];
     __syncthreads();
-    const long long row_jobs = static_cast<long long>(p.num_tokens) * p.token_jobs;
-    const long long first = static_cast<long long>(blockIdx.x) * kNrWarps + warp;
-    const long long stride = static_cast<long long>(gridDim.x) * kNrWarps;
+    const long long quads = static_cast<long long>(p.num_tokens) * p.quads;
+    const long long warps = static_cast<long long>(gridDim.x) * kNrWarps, rows = min(warps, quads);
+    const long long me = static_cast<long long>(blockIdx.x) * kNrWarps + warp, run = min(me, rows);
     if (!rows_of_warp<kBf16, kAppend>(p, sh, smem_addr(nr_ring) + warp * Ring<kBf16>::kStages * Ring<kBf16>::kStage,
-                                      first, stride))
+                                      quads * run / rows, quads * min(run + 1, rows) / rows))
         return;
     if constexpr (kAppend) {
-        long long job = first < row_jobs ? first + (row_jobs - first + stride - 1) / stride * stride : first;
-        for (; job < row_jobs + p.v_jobs; job += stride) {
-            const long long item = (job - row_jobs) * 32 + (threadIdx.x & 31);
+        // (warps without rows come first)
+        for (long long job = me >= rows ? me - rows : me + warps - rows; job < p.v_jobs; job += warps) {
+            const long long item = job * 32 + (threadIdx.x & 31);
             const long long unit = item >> 3;    // pair * hkv + h
             const long long pr = unit / p.hkv;
             if (2 * pr <= p.num_tokens)          // (the early start adds half a pair)
@@ -515,14 +501,10 @@ cudaError_t launch_norm_rope(const NormRopeParams &in, cudaStream_t s)
     NormRopeParams p = in;
     const int sms = sm_count() > 0 ? sm_count() : 1;
     p.q_quads = (p.hq + 3) / 4;
-    const int quads = p.q_quads + (p.hkv + 3) / 4;
-    // one quad a job while the jobs do not fill the SMs, else up to sixteen, so
-    // that a job's angles and tables serve more rows (eight: 3% slower, four: 20%)
-    const long long all = static_cast<long long>(p.num_tokens) * quads;
-    p.token_jobs = all <= 20LL * sms ? quads : (quads + 15) / 16;
+    p.quads = p.q_quads + (p.hkv + 3) / 4;
     const bool append = p.pool != nullptr;
     p.v_jobs = append ? ((static_cast<long long>(p.num_tokens) + 2) / 2 * p.hkv * 8 + 31) / 32 : 0;
-    const long long jobs = static_cast<long long>(p.num_tokens) * p.token_jobs + p.v_jobs;
+    const long long jobs = static_cast<long long>(p.num_tokens) * p.quads + p.v_jobs;
     if (append)
         return p.in_bf16 ? launch_rows<true, true>(p, jobs, sms, s) : launch_rows<false, true>(p, jobs, sms, s);
     return p.in_bf16 ? launch_rows<true, false>(p, jobs, sms, s) : launch_rows<false, false>(p, jobs, sms, s);

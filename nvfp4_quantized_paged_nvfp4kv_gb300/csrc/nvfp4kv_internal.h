@@ -207,8 +207,7 @@ struct NormRopeParams {
     float eps;
     float rope_scale;            // multiplies cos and sin
     float gscale;
-    int q_quads;                 // set by the launcher: runs of four query heads,
-    int token_jobs;              // warp jobs that a token's quads are split over,
+    int q_quads, quads;          // set by the launcher: fours of a token's query heads, and of all heads,
     long long v_jobs;            // and warps of V blocks
     HeadScales hs;
     uint64_t freq[kHeadDim / 2]; // turns a position, in units of 2^-64
