@@ -17,21 +17,27 @@
 // Work split.  A row is eight lanes, lane l with channels 8l .. 8l + 7 and 64 +
 // 8l .. 64 + 8l + 7, so that eight lanes load or store 128 bytes on end (16
 // channels on end a lane touched every 32-byte sector twice: 63 us for 8,192
-// tokens of 48 + 8 heads), a warp instruction covers four heads of one token,
-// and the half-split partner of a full rotation is in the lane itself.  A warp
-// job is one token and a run of its heads, four at a time, queries then keys.
-// The job's cos and sin, multiplied by the weights of their channels, are worked
-// out once by the warp (each lane doing so for its own 16 channels cost 15 of
-// 62 us) and stay in 32 registers of the lane for all heads of a kind; products
-// run on packed fp32 pairs.  For the cache two
-// neighbouring lanes swap halves and hold a whole 16-value block each.  The row
-// jobs and (fused) the V blocks share one launch of resident CTAs.
+// tokens of 48 + 8 heads, 43 now), a warp instruction covers four heads of one
+// token (a quad), and the half-split partner of a full rotation is in the lane
+// itself.  A token's quads are its queries', then its keys'; each warp takes an
+// equal run of the call's quads (whole tokens, 2.7 a warp, left a tenth of the
+// warps' time idle).  A token's cos and sin, multiplied by the weights of their
+// channels, are worked out once by the warp (each lane doing so for its own 16
+// channels cost 15 us) and stay in 32 registers of the lane for all its heads of
+// a kind; products run on packed fp32 pairs.  For the cache two neighbouring
+// lanes swap halves and hold a whole 16-value block each.  The rows and (fused)
+// the V blocks share one launch of resident CTAs.
 //
 // Loads.  Four heads are 1 KB on end (2 KB in fp32); each warp keeps a ring of
 // them in shared memory, filled by bulk copies that run ahead of the work and
-// across its jobs.
+// across its tokens.
+//
+// Bound.  8,192 bf16 tokens of 48 + 8 heads out of a fused projection's rows:
+// 235 MB in 43 us, 5.5 TB/s, 82% of a copy's rate, with 63% of the issue slots
+// taken.  With the cache write, 244 MB in 45 us.
 #include "nvfp4kv.h"
 #include "record_write.cuh"
+#include <type_traits>
 
 namespace nvfp4kv {
 namespace {
@@ -45,19 +51,19 @@ __device__ __forceinline__ uint32_t bf16x2_bits(float lo, float hi)
     return *reinterpret_cast<const uint32_t *>(&two);
 }
 
-// A lane's two pieces of an output row.
+// A lane's two pieces of an output row, the first at dst.
 template <bool kBf16>
-__device__ __forceinline__ void store_pieces(void *dst, size_t elem_off, const float (&y)[16])
+__device__ __forceinline__ void store_pieces(uint8_t *dst, const float (&y)[16])
 {
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
         const float *v = y + 8 * k;
         if constexpr (kBf16)
-            *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(dst) + elem_off + 64 * k) =
+            *reinterpret_cast<uint4 *>(dst + 128 * k) =
                 make_uint4(bf16x2_bits(v[0], v[1]), bf16x2_bits(v[2], v[3]), bf16x2_bits(v[4], v[5]),
                            bf16x2_bits(v[6], v[7]));
         else {
-            float4 *d = reinterpret_cast<float4 *>(static_cast<float *>(dst) + elem_off + 64 * k);
+            float4 *d = reinterpret_cast<float4 *>(dst + 256 * k);
             d[0] = make_float4(v[0], v[1], v[2], v[3]);
             d[1] = make_float4(v[4], v[5], v[6], v[7]);
         }
@@ -134,23 +140,48 @@ struct NrShared {
     uint64_t bar[kNrWarps][Ring<true>::kStages];
 };
 
-// A place in a warp's quads, which are `left` from quad `quad` of token t on;
-// quads 0 .. p.q_quads - 1 of a token are queries, the others keys.
-struct Cursor {
-    int t, quad;
-    long long left;
+// The copies of a warp's quads, one after the other: `left` to go, the next one's
+// rows at src, `heads` of its kind and token from there on.
+template <bool kBf16>
+struct Feed {
+    const uint8_t *src;
+    int t, left, heads;
+    bool is_k;
 
-    // quads from .. to - 1 of the call
-    __device__ __forceinline__ Cursor(const NormRopeParams &p, long long from, long long to)
-        : t(static_cast<int>(from / p.quads)), quad(static_cast<int>(from - static_cast<long long>(t) * p.quads)),
-          left(to - from)
+    // head `head` of token t
+    __device__ __forceinline__ void at(const NormRopeParams &p, int head)
     {
+        const size_t elem = static_cast<size_t>(t) * (is_k ? p.k_stride : p.q_stride) + head * kHeadDim;
+        src = static_cast<const uint8_t *>(is_k ? p.k : p.q) + elem * (kBf16 ? 2 : 4);
+        heads = (is_k ? p.hkv : p.hq) - head;
+    }
+    __device__ __forceinline__ Feed(const NormRopeParams &p, int token, int quad, int n)
+        : t(token), left(n), is_k(quad >= p.q_quads)
+    {
+        at(p, 4 * (is_k ? quad - p.q_quads : quad));
+    }
+    // the next quad to `stage` (whole warp; lane 0 copies)
+    __device__ __forceinline__ void fetch(const NormRopeParams &p, uint32_t stage, uint32_t bar)
+    {
+        using G = Ring<kBf16>;
+        if ((threadIdx.x & 31) == 0) {
+            const uint32_t bytes = min(4, heads) * G::kRow;
+            mbar_arrive_expect_tx(bar, bytes);
+            bulk_g2s(stage, src, bytes, bar);
+        }
+        src += G::kStage;
+        heads -= 4;
+        if (--left > 0 && heads <= 0) {
+            t += is_k;
+            is_k = !is_k;
+            at(p, 0);
+        }
     }
 };
 
 // One warp's rows, quads from .. to - 1 of the call.  False when a wait for staged
 // rows gave up.
-template <bool kBf16, bool kAppend>
+template <bool kBf16, bool kAppend, bool kSwaps>
 __device__ __forceinline__ bool rows_of_warp(const NormRopeParams &p, NrShared &sh, uint32_t ring, long long from,
                                              long long to)
 {
@@ -161,36 +192,20 @@ __device__ __forceinline__ bool rows_of_warp(const NormRopeParams &p, NrShared &
     const int half = p.rot >> 1;
     const int c0 = 8 * part;                     // channel of value j: c0 + (j & 7) + 64 (j / 8)
 
-    // stage st gets the quad at f, which moves on (whole warp; lane 0 copies)
-    Cursor f(p, from, to), w = f;
-    auto fetch = [&](int st) {
-        const bool is_k = f.quad >= p.q_quads;
-        const int head = 4 * (is_k ? f.quad - p.q_quads : f.quad);
-        const int rows = min(4, (is_k ? p.hkv : p.hq) - head);
-        if (lane == 0) {
-            constexpr int size = kBf16 ? 2 : 4;
-            const size_t at = static_cast<size_t>(f.t) * (is_k ? p.k_stride : p.q_stride) + head * kHeadDim;
-            mbar_arrive_expect_tx(bar + 8 * st, rows * G::kRow);
-            bulk_g2s(ring + st * G::kStage, static_cast<const uint8_t *>(is_k ? p.k : p.q) + at * size, rows * G::kRow,
-                     bar + 8 * st);
-        }
-        --f.left;
-        if (++f.quad == p.quads) {
-            f.quad = 0;
-            ++f.t;
-        }
-    };
-    int issued = 0;
-    for (; issued < G::kStages && f.left > 0; ++issued)
-        fetch(issued);
+    int t = static_cast<int>(from / p.quads), quad = static_cast<int>(from - static_cast<long long>(t) * p.quads);
+    int left = static_cast<int>(to - from);
+    if (left <= 0)
+        return true;
+    Feed<kBf16> feed(p, t, quad, left);
+    for (int st = 0; st < G::kStages && feed.left > 0; ++st)
+        feed.fetch(p, ring + st * G::kStage, bar + 8 * st);
 
-    int st = 0, done = 0;
-    uint32_t phase = 0;
+    uint32_t st = 0, phase = 0;
+    int end = quad;
     bool ok = true;
-    for (; ok && w.left > 0; ++w.t, w.quad = 0) {
-    const int t = w.t;
-    const int end = static_cast<int>(min(w.left + w.quad, static_cast<long long>(p.quads)));
-    w.left -= end - w.quad;
+    for (; ok && left > 0; ++t, quad = 0) {
+    end = min(p.quads, quad + left);
+    left -= end - quad;
     const int pos = p.positions[t];              // < 0: a token that is not there, nothing of it is written
     __syncwarp();                                // (the last token's angles have been read)
     for (int i = lane; i < half; i += 32) {
@@ -235,28 +250,30 @@ __device__ __forceinline__ bool rows_of_warp(const NormRopeParams &p, NrShared &
     };
     // where a half-split partner piece is, when not in the lane itself: chunk
     // (of eight channels) 8 k + part of the row, plus or minus half / 8
-    const bool swaps = !p.interleaved && p.rot > 0 && p.rot < kHeadDim;
     auto mate_chunk = [&](int k) {
         const int chunk = 8 * k + part;
         return 8 * chunk < half ? chunk + half / 8 : (8 * chunk < p.rot ? chunk - half / 8 : chunk);
     };
-    for (int quad = w.quad; quad < end; ++quad) {
-        const bool is_k = quad >= p.q_quads;
-        if (quad == w.quad || quad == p.q_quads)
-            tables(sh.weight[is_k]);
-        const int head = 4 * (is_k ? quad - p.q_quads : quad) + sub;
-        const bool live = pos >= 0 && head < (is_k ? p.hkv : p.hq);
+    while (ok && quad < end) {                   // the queries, then the keys
+    const bool is_k = quad >= p.q_quads;
+    const int stop = is_k ? end : min(end, p.q_quads);
+    tables(sh.weight[is_k]);
+    const bool normed = (is_k ? p.k_weight : p.q_weight) != nullptr;
+    const int heads = is_k ? p.hkv : p.hq, head = 4 * (is_k ? quad - p.q_quads : quad) + sub;
+    int ahead = pos >= 0 ? heads - head : 0;     // (positive: the lane's head is there)
+    const size_t out_row = (static_cast<size_t>(t) * heads + head) * kHeadDim + c0;
+    uint8_t *out = static_cast<uint8_t *>(is_k ? p.k_out : p.q_out) + out_row * (is_k && !kBf16 ? 4 : 2);
+    for (; quad < stop; ++quad, ahead -= 4, out += 4 * kHeadDim * (is_k && !kBf16 ? 4 : 2)) {
+        const bool live = ahead > 0;
         ok = __all_sync(kFullMask, mbar_wait_bounded(bar + 8 * st, phase, p.wait_limit));
         if (!ok)
             break;
         RawBlock<kBf16> cur;                     // (rows behind the last head: what the stage held, not written)
         read_pieces<kBf16>(ring + st * G::kStage + sub * G::kRow, part, cur);
-        ++done;
-        if (f.left > 0) {
+        if (feed.left > 0) {
             fence_async_shared();                // the stage's reads before its next copy
             __syncwarp();
-            fetch(st);
-            ++issued;
+            feed.fetch(p, ring + st * G::kStage, bar + 8 * st);
         }
         if (++st == G::kStages) {
             st = 0;
@@ -269,7 +286,7 @@ __device__ __forceinline__ bool rows_of_warp(const NormRopeParams &p, NrShared &
         for (int j = 0; j < 8; ++j)
             x2[j] = f32x2_pack(x[2 * j], x[2 * j + 1]);
         uint64_t rstd2 = f32x2_pack(1.f, 1.f);
-        if ((is_k ? p.k_weight : p.q_weight) != nullptr) {
+        if (normed) {
             uint64_t a = mul_f32x2(x2[0], x2[0]), b = mul_f32x2(x2[1], x2[1]);
 #pragma unroll
             for (int j = 2; j < 8; j += 2) {
@@ -289,14 +306,16 @@ __device__ __forceinline__ bool rows_of_warp(const NormRopeParams &p, NrShared &
             y[2 * j] = f32x2_lo(v);
             y[2 * j + 1] = f32x2_hi(v);
         };
-        if (p.interleaved) {
+        if constexpr (!kSwaps) {
+            if (p.interleaved) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                turn(j, f32x2_pack(x[2 * j + 1], x[2 * j]));
-        } else if (!swaps) {
+                for (int j = 0; j < 8; ++j)
+                    turn(j, f32x2_pack(x[2 * j + 1], x[2 * j]));
+            } else {
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                turn(j, x2[j ^ 4]);
+                for (int j = 0; j < 8; ++j)
+                    turn(j, x2[j ^ 4]);
+            }
         } else {
             RawBlock<kBf16> other = cur;
             constexpr int n = kBf16 ? 1 : 2;     // 16-byte words of a piece
@@ -354,8 +373,9 @@ __device__ __forceinline__ bool rows_of_warp(const NormRopeParams &p, NrShared &
                 }
                 size_t rec;
                 int tok;
-                if (live && slot_site(p, p.slot_mapping[t], head, rec, tok, head == 0 && part == 0)) {
-                    const uint32_t flip = divide_by_tensor_scale(v, head_tensor_scale(p.hs, false, head, p.gscale));
+                const int h = heads - ahead;
+                if (live && slot_site(p, p.slot_mapping[t], h, rec, tok, h == 0 && part == 0)) {
+                    const uint32_t flip = divide_by_tensor_scale(v, head_tensor_scale(p.hs, false, h, p.gscale));
                     write_nvfp4_block(p.pool + rec, false, tok, (part >> 1) + (odd ? 4 : 0), v, ScaleOfByte(), flip);
                 }
                 continue;
@@ -363,17 +383,18 @@ __device__ __forceinline__ bool rows_of_warp(const NormRopeParams &p, NrShared &
         }
         if (!live)
             continue;
-        if (!is_k)
-            store_pieces<true>(p.q_out, (static_cast<size_t>(t) * p.hq + head) * kHeadDim + c0, y);
+        if (kBf16 || !is_k)
+            store_pieces<true>(out, y);
         else
-            store_pieces<kBf16>(p.k_out, (static_cast<size_t>(t) * p.hkv + head) * kHeadDim + c0, y);
+            store_pieces<false>(out, y);
+    }
     }
     }
     if (!ok) {
         // let the copies in flight land before the CTA exits
         if (lane == 0)
             report(p.dev_status, NVFP4KV_DEV_TIMEOUT);
-        for (; done < issued; ++done) {
+        for (int n = left + end - quad - feed.left; n > 0; --n) {
             mbar_wait_bounded(bar + 8 * st, phase, kWaitLimit);
             if (++st == G::kStages) {
                 st = 0;
@@ -433,7 +454,7 @@ __device__ __forceinline__ void v_pair_job(const NormRopeParams &p, int pr, int 
 
 // Each warp takes an equal run of the call's quads, token-major, and then of the
 // V blocks, one a thread.
-template <bool kBf16, bool kAppend>
+template <bool kBf16, bool kAppend, bool kSwaps>
 __global__ void __launch_bounds__(kNrThreads, Ring<kBf16>::kCtas)
     norm_rope_kernel(const __grid_constant__ NormRopeParams p)
 {
@@ -464,7 +485,7 @@ __global__ void __launch_bounds__(kNrThreads, Ring<kBf16>::kCtas)
     const long long quads = static_cast<long long>(p.num_tokens) * p.quads;
     const long long warps = static_cast<long long>(gridDim.x) * kNrWarps, rows = min(warps, quads);
     const long long me = static_cast<long long>(blockIdx.x) * kNrWarps + warp, run = min(me, rows);
-    if (!rows_of_warp<kBf16, kAppend>(p, sh, smem_addr(nr_ring) + warp * Ring<kBf16>::kStages * Ring<kBf16>::kStage,
+    if (!rows_of_warp<kBf16, kAppend, kSwaps>(p, sh, smem_addr(nr_ring) + warp * Ring<kBf16>::kStages * Ring<kBf16>::kStage,
                                       quads * run / rows, quads * min(run + 1, rows) / rows))
         return;
     if constexpr (kAppend) {
@@ -480,11 +501,11 @@ __global__ void __launch_bounds__(kNrThreads, Ring<kBf16>::kCtas)
     }
 }
 
-template <bool kBf16, bool kAppend>
+template <bool kBf16, bool kAppend, bool kSwaps>
 cudaError_t launch_rows(const NormRopeParams &p, long long jobs, int sms, cudaStream_t s)
 {
     using G = Ring<kBf16>;
-    const auto kernel = norm_rope_kernel<kBf16, kAppend>;
+    const auto kernel = norm_rope_kernel<kBf16, kAppend, kSwaps>;
     if (G::kSmem > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, G::kSmem);
         if (e != cudaSuccess)
@@ -505,9 +526,15 @@ cudaError_t launch_norm_rope(const NormRopeParams &in, cudaStream_t s)
     const bool append = p.pool != nullptr;
     p.v_jobs = append ? ((static_cast<long long>(p.num_tokens) + 2) / 2 * p.hkv * 8 + 31) / 32 : 0;
     const long long jobs = static_cast<long long>(p.num_tokens) * p.quads + p.v_jobs;
+    // rotations whose pairs are in two lanes have a kernel of their own (their
+    // registers cost the others 1 us of 44)
+    auto launch = [&](auto bf16, auto app) {
+        return !p.interleaved && p.rot > 0 && p.rot < kHeadDim ? launch_rows<bf16.value, app.value, true>(p, jobs, sms, s)
+                                                              : launch_rows<bf16.value, app.value, false>(p, jobs, sms, s);
+    };
     if (append)
-        return p.in_bf16 ? launch_rows<true, true>(p, jobs, sms, s) : launch_rows<false, true>(p, jobs, sms, s);
-    return p.in_bf16 ? launch_rows<true, false>(p, jobs, sms, s) : launch_rows<false, false>(p, jobs, sms, s);
+        return p.in_bf16 ? launch(std::true_type(), std::true_type()) : launch(std::false_type(), std::true_type());
+    return p.in_bf16 ? launch(std::true_type(), std::false_type()) : launch(std::false_type(), std::false_type());
 }
 
 } // namespace nvfp4kv
