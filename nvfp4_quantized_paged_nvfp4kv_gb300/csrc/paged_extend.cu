@@ -110,6 +110,20 @@ __device__ __forceinline__ void st_shared128(uint32_t addr, uint32_t a, uint32_t
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
+// 32 bytes to global memory, at 32 (wide) or 16.
+__device__ __forceinline__ void store_sector(uint8_t *dst, bool wide, uint32_t a, uint32_t b, uint32_t c, uint32_t d,
+                                             uint32_t e, uint32_t f, uint32_t g, uint32_t h)
+{
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(a), "r"(b), "r"(c), "r"(d),
+                     "r"(e), "r"(f), "r"(g), "r"(h)
+                     : "memory");
+    } else {
+        reinterpret_cast<uint4 *>(dst)[0] = make_uint4(a, b, c, d);
+        reinterpret_cast<uint4 *>(dst)[1] = make_uint4(e, f, g, h);
+    }
+}
+
 // Bounded wait for a phase.  Another role's failure is looked at only while the
 // phase is not there yet: a load of the flag in front of every wait cost a
 // quarter of the pipeline's turn-around.
@@ -1167,68 +1181,46 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
                     note->tail = 1;
                 }
             }
-            // Rows go out by way of the Q tile, which no product reads any more: the
-            // warp's 8 KB hold 256 bytes of each of its rows (all channels in
-            // bf16, half of them in fp32), which half a warp then stores on end.
-            const bool f32 = !whole || p.out_f32;
-            const uint32_t mine = stage + 8192u * (warp & 3);
-            auto load_o = [&](int cb, float (&o)[32]) {
-                uint32_t w[32];
-                tmem_ld32(tb + kTmO + 32 * cb, w);
+            // A row a thread, 32 bytes (a whole sector) a store.
+            const bool f32 = !whole || p.out_f32, wide = !whole || (reinterpret_cast<uintptr_t>(p.out) & 31u) == 0;
+            uint8_t *dst = whole ? static_cast<uint8_t *>(p.out) + out_row * kHeadDim * (p.out_f32 ? 4 : 2)
+                                 : reinterpret_cast<uint8_t *>(part + rr * kHeadDim);
+#pragma unroll 1
+            for (int cb = 0; cb < 4; ++cb) {
+                uint32_t o[32];
+                tmem_ld32(tb + kTmO + 32 * cb, o);
                 tmem_wait_ld();
 #pragma unroll
                 for (int j = 0; j < 32; ++j)
-                    o[j] = __uint_as_float(w[j]) * f0;
+                    o[j] = __float_as_uint(__uint_as_float(o[j]) * f0);
                 if constexpr (kKeySplit) {
                     // (the second block's columns of the same lanes; nothing there without its tiles)
+                    uint32_t w[32];
                     tmem_ld32(tb + kTmBlock + kTmO + 32 * cb, w);
                     tmem_wait_ld();
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
-                        o[j] = w1 != 0.f ? fmaf(__uint_as_float(w[j]), f1, o[j]) : o[j];
+                        o[j] = w1 != 0.f ? __float_as_uint(fmaf(__uint_as_float(w[j]), f1, __uint_as_float(o[j]))) : o[j];
                 }
-            };
-            auto place = [&](int of, uint32_t chunk) { return mine + 256u * of + ((chunk ^ (of & 7u)) << 4); };
-#pragma unroll 1
-            for (int pass = 0; pass < (f32 ? 2 : 1); ++pass) {
-                __syncwarp();
-#pragma unroll 1
-                for (int half = 0; half < (f32 ? 2 : 4); ++half) {
-                    float o[32];
-                    load_o(f32 ? 2 * pass + half : half, o);
-                    if (f32) {
+                if (!has_row)
+                    continue;
+                if (f32) {
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            st_shared128(place(lane, 8 * half + k), __float_as_uint(o[4 * k]), __float_as_uint(o[4 * k + 1]),
-                                         __float_as_uint(o[4 * k + 2]), __float_as_uint(o[4 * k + 3]));
-                    } else {
-                        auto bf2 = [&](int j) {
-                            const __nv_bfloat162 two = __floats2bfloat162_rn(o[j], o[j + 1]);
-                            return *reinterpret_cast<const uint32_t *>(&two);
-                        };
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            st_shared128(place(lane, 4 * half + k), bf2(8 * k), bf2(8 * k + 2), bf2(8 * k + 4), bf2(8 * k + 6));
-                    }
-                }
-                __syncwarp();
-                const uint32_t chunk = lane & 15;
-                if (!whole) {
-                    uint4 *dst = reinterpret_cast<uint4 *>(part + (rr - lane + (lane >> 4)) * kHeadDim + 64 * pass) + chunk;
-#pragma unroll 8
-                    for (int i = 0; i < 16; ++i)     // (rows that are none: their place in the piece)
-                        dst[i * (2 * kHeadDim / 4)] = lds128(place(2 * i + (lane >> 4), chunk));
+                    for (int k = 0; k < 4; ++k)
+                        store_sector(dst + 128 * cb + 32 * k, wide, o[8 * k], o[8 * k + 1], o[8 * k + 2], o[8 * k + 3],
+                                     o[8 * k + 4], o[8 * k + 5], o[8 * k + 6], o[8 * k + 7]);
                 } else {
-                    const int size = p.out_f32 ? 4 : 2;
-                    uint8_t *dst = static_cast<uint8_t *>(p.out) + 64 * 4 * pass + 16 * chunk;
-#pragma unroll 8
-                    for (int i = 0; i < 16; ++i) {
-                        const int of = 2 * i + (lane >> 4);
-                        const int64_t at = __shfl_sync(kFullMask, out_row, of);
-                        const uint4 v = lds128(place(of, chunk));
-                        if ((live >> of) & 1u)
-                            *reinterpret_cast<uint4 *>(dst + at * kHeadDim * size) = v;
+                    uint32_t h[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) {
+                        const __nv_bfloat162 two =
+                            __floats2bfloat162_rn(__uint_as_float(o[2 * j]), __uint_as_float(o[2 * j + 1]));
+                        h[j] = *reinterpret_cast<const uint32_t *>(&two);
                     }
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+                        store_sector(dst + 64 * cb + 32 * k, wide, h[8 * k], h[8 * k + 1], h[8 * k + 2], h[8 * k + 3],
+                                     h[8 * k + 4], h[8 * k + 5], h[8 * k + 6], h[8 * k + 7]);
                 }
             }
             __syncwarp();
