@@ -485,8 +485,9 @@ __global__ void __launch_bounds__(kNrThreads, Ring<kBf16>::kCtas)
     const long long quads = static_cast<long long>(p.num_tokens) * p.quads;
     const long long warps = static_cast<long long>(gridDim.x) * kNrWarps, rows = min(warps, quads);
     const long long me = static_cast<long long>(blockIdx.x) * kNrWarps + warp, run = min(me, rows);
-    if (!rows_of_warp<kBf16, kAppend, kSwaps>(p, sh, smem_addr(nr_ring) + warp * Ring<kBf16>::kStages * Ring<kBf16>::kStage,
-                                      quads * run / rows, quads * min(run + 1, rows) / rows))
+    if (!rows_of_warp<kBf16, kAppend, kSwaps>(p, sh,
+                                              smem_addr(nr_ring) + warp * Ring<kBf16>::kStages * Ring<kBf16>::kStage,
+                                              quads * run / rows, quads * min(run + 1, rows) / rows))
         return;
     if constexpr (kAppend) {
         // (warps without rows come first)
@@ -529,8 +530,9 @@ cudaError_t launch_norm_rope(const NormRopeParams &in, cudaStream_t s)
     // rotations whose pairs are in two lanes have a kernel of their own (their
     // registers cost the others 1 us of 44)
     auto launch = [&](auto bf16, auto app) {
-        return !p.interleaved && p.rot > 0 && p.rot < kHeadDim ? launch_rows<bf16.value, app.value, true>(p, jobs, sms, s)
-                                                              : launch_rows<bf16.value, app.value, false>(p, jobs, sms, s);
+        const bool swaps = !p.interleaved && p.rot > 0 && p.rot < kHeadDim;
+        return swaps ? launch_rows<bf16.value, app.value, true>(p, jobs, sms, s)
+                     : launch_rows<bf16.value, app.value, false>(p, jobs, sms, s);
     };
     if (append)
         return p.in_bf16 ? launch(std::true_type(), std::true_type()) : launch(std::false_type(), std::true_type());

@@ -48,11 +48,17 @@
 // 154), which is cut into equal runs, one a resident CTA: no wave is left half
 // empty and few rows with many keys still occupy every SM (whole units, cut by a
 // fixed number where there were few: 2,048 tokens at 32K 1.37 ms, 1.14 in runs).
-// A CTA's run begins and ends inside a
-// unit as a rule: of those it leaves O, reference and sum in the workspace (at
-// most two pieces), which a second kernel joins; the units inside are written
-// directly.  Loads and conversions for the next unit run behind the end of the
-// last.
+// A CTA's run begins and ends inside a unit as a rule: of those it leaves O,
+// reference and sum in the workspace (at most two pieces), which a second kernel
+// joins; the units inside are written directly.  Loads and conversions for the
+// next unit run behind the end of the last.  (Its Q by the converter warps, or by
+// the softmax warps ahead of the last unit's output, also overlaps, but the state
+// it keeps in registers cost every tile 3 to 4%.)
+//
+// Bound.  2,048 tokens of 48 + 8 heads at 32K: 1,400 TFLOP/s, 73% of a library
+// GEMM's rate; a tile's softmax, P V and Q K^T follow one another, and two blocks
+// fill most of each other's gaps.  16 tokens each of 12 sequences at 8K: 75 us,
+// the conversion of a tile for one block's rows only.
 #include "tcgen05.cuh"
 
 namespace nvfp4kv {
@@ -91,14 +97,14 @@ struct Shape {
     static constexpr uint32_t kOffBar = kOffRaw + kRaw * kRawBytes;
     enum : int {
         kRawFull = 0, kRawEmpty = kRawFull + kRaw, kKFull = kRawEmpty + kRaw, kVFull = kKFull + kStages,
-        kTurn = kVFull + kStages, kQFull = kTurn + kStages, kSFull = kQFull + 2, kPFull = kSFull + 2, kHalf = kPFull + 4,
-        kDone = kHalf + 2, kGo = kDone + 2, kExit = kGo + 2, kJoin = kExit + 2, kFree = kJoin + 1, kVDone = kFree + 1,
+        kTurn = kVFull + kStages, kQFull = kTurn + kStages, kSFull = kQFull + 2, kPFull = kSFull + 2,
+        kHalf = kPFull + 4, kDone = kHalf + 2, kGo = kDone + 2, kExit = kGo + 2, kJoin = kExit + 2, kFree = kJoin + 1, kVDone = kFree + 1,
         kNumBars = kVDone + 2
     };
     static constexpr uint32_t kOffSlot = kOffBar + 8 * kNumBars;             // tensor-memory address, failure flag
     static constexpr uint32_t kOffRun = (kOffSlot + 8 + 15) / 16 * 16;
-    static constexpr uint32_t kOffMl = kOffRun + 64;                         // key split: the second block's (reference, sum) rows
-    static constexpr uint32_t kSmem = kOffMl + (kKeySplit ? 8 * kRowsBlock : 0) + 1024;                   // + slack to align the base
+    static constexpr uint32_t kOffMl = kOffRun + 64;         // key split: the second block's (reference, sum) rows
+    static constexpr uint32_t kSmem = kOffMl + (kKeySplit ? 8 * kRowsBlock : 0) + 1024;      // + slack to align the base
     // (one CTA an SM: all of tensor memory is its own)
     static_assert(kSmem <= 227 * 1024 && 2 * kSmem > 228 * 1024, "shared memory");
 };
@@ -322,8 +328,8 @@ __device__ __forceinline__ uint32_t bit_range(int lo, int hi)
 // says that the products so far are in it, and l, which are relative to the old
 // one, follow.  A warp together; false when landed() gave up.
 template <class Landed>
-__device__ __forceinline__ bool weights_with_care(uint32_t scores, uint32_t weights, uint32_t o_cols, bool has_o, int lo, int hi,
-                                                  float inv, RowSum &row, Landed landed)
+__device__ __forceinline__ bool weights_with_care(uint32_t scores, uint32_t weights, uint32_t o_cols, bool has_o,
+                                                  int lo, int hi, float inv, RowSum &row, Landed landed)
 {
     const uint64_t inv2 = f32x2_pack(inv, inv);
     const uint32_t seen[2] = {bit_range(lo, hi), bit_range(lo - 32, hi - 32)};
@@ -341,8 +347,8 @@ __device__ __forceinline__ bool weights_with_care(uint32_t scores, uint32_t weig
             float pm[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-                pm[k] = fmax3(fmax3(s[8 * k], s[8 * k + 1], s[8 * k + 2]), fmax3(s[8 * k + 3], s[8 * k + 4], s[8 * k + 5]),
-                              fmaxf(s[8 * k + 6], s[8 * k + 7]));
+                pm[k] = fmax3(fmax3(s[8 * k], s[8 * k + 1], s[8 * k + 2]),
+                              fmax3(s[8 * k + 3], s[8 * k + 4], s[8 * k + 5]), fmaxf(s[8 * k + 6], s[8 * k + 7]));
             const float top =
                 fmax3(fmax3(pm[0], pm[1], pm[2]), fmax3(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7])) * inv;
             raise = raise && top > -INFINITY;
@@ -440,8 +446,8 @@ struct Place {
 // Where the cut at `at` of `head` x hkv places falls (whole warp); table: batch +
 // 1 running sums.
 template <int kRows>
-__device__ __forceinline__ Place find_cut(const PagedExtendParams &p, long long at, long long head, const long long *table,
-                                          int lane)
+__device__ __forceinline__ Place find_cut(const PagedExtendParams &p, long long at, long long head,
+                                          const long long *table, int lane)
 {
     Place r{p.hkv, 0, 0, 0, at};
     if (at >= head * p.hkv)
@@ -496,7 +502,8 @@ __device__ __forceinline__ Place find_cut(const PagedExtendParams &p, long long 
 // Finds the run of worker `worker` of `workers`; whole CTA.  `table`: batch + 1
 // sums in shared memory.
 template <int kRows>
-__device__ __forceinline__ void find_run(const PagedExtendParams &p, int worker, int workers, long long *table, Run *run)
+__device__ __forceinline__ void find_run(const PagedExtendParams &p, int worker, int workers, long long *table,
+                                         Run *run)
 {
     __shared__ long long part[32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
@@ -634,7 +641,8 @@ __device__ __forceinline__ bool next_unit(const PagedExtendParams &p, Walk &w, i
         if (u.all == 0 && tid < kRows) {
             const Row row = row_of<kRows>(p, u, tid);
             const int words = p.out_f32 ? kHeadDim / 4 : kHeadDim / 8;
-            uint4 *d = reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.out) + row.at * kHeadDim * (p.out_f32 ? 4 : 2));
+            uint4 *d =
+                reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.out) + row.at * kHeadDim * (p.out_f32 ? 4 : 2));
             for (int k = 0; row.live && k < words; ++k)
                 d[k] = make_uint4(0, 0, 0, 0);
         }
@@ -781,7 +789,8 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
                 if (!__all_sync(kFullMask, ok))
                     return false;
                 const int pg0 = first_page + i * kGranPages;
-                const int n = max(0, min(pg0 + kGranPages, page_hi) - max(pg0, page_lo));   // 0: no row sees the granule
+                // (0 where no row sees the granule)
+                const int n = max(0, min(pg0 + kGranPages, page_hi) - max(pg0, page_lo));
                 if (lane == 0)
                     mbar_arrive_expect_tx(B(S::kRawFull + st), n * kNvfp4Record);
                 __syncwarp();
@@ -869,7 +878,8 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
                     const bool more = j + 1 < mine;
                     const uint32_t p_bar = B(S::kPFull + k), p_par = i & 1;
                     const bool waits = turns && batch >= go_lag;
-                    const uint32_t go_bar = waits ? B(S::kGo + k) : p_bar, go_par = waits ? (batch - go_lag) & 1 : p_par;
+                    const uint32_t go_bar = waits ? B(S::kGo + k) : p_bar;
+                    const uint32_t go_par = waits ? (batch - go_lag) & 1 : p_par;
                     const bool k_first = !kKeySplit && more;
                     const uint32_t kv_bar = k_first ? B(S::kKFull + (next & 1)) : B(S::kVFull + (x & 1));
                     const uint32_t kv_par = k_first ? (next >> 1) & 1 : (x >> 1) & 1;
@@ -1188,6 +1198,7 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
 #pragma unroll 1
             for (int cb = 0; cb < 4; ++cb) {
                 uint32_t o[32];
+                __syncwarp();                    // (lanes without a row skip the stores)
                 tmem_ld32(tb + kTmO + 32 * cb, o);
                 tmem_wait_ld();
 #pragma unroll
@@ -1200,7 +1211,8 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
                     tmem_wait_ld();
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
-                        o[j] = w1 != 0.f ? __float_as_uint(fmaf(__uint_as_float(w[j]), f1, __uint_as_float(o[j]))) : o[j];
+                        if (w1 != 0.f)
+                            o[j] = __float_as_uint(fmaf(__uint_as_float(w[j]), f1, __uint_as_float(o[j])));
                 }
                 if (!has_row)
                     continue;
@@ -1314,7 +1326,8 @@ __global__ void __launch_bounds__(256) paged_extend_join_kernel(const __grid_con
 #pragma unroll kAhead
         for (int i = 0; i < n; ++i) {
             const float4 *o = reinterpret_cast<const float4 *>(
-                                  p.partials + kPieceFloats<kRows> * (2 * static_cast<size_t>(j0 + i) + (j0 + i == first)) +
+                                  p.partials +
+                                  kPieceFloats<kRows> * (2 * static_cast<size_t>(j0 + i) + (j0 + i == first)) +
                                   static_cast<size_t>(rr) * kHeadDim) + lane;
             float4 v[kJoinRows];
 #pragma unroll
@@ -1398,7 +1411,8 @@ static cudaError_t launch_extend(const PagedExtendParams &p, cudaStream_t s)
     e = launch_pdl(paged_extend_kernel<kKeySplit>, dim3(p.workers), dim3(S::kThreads), S::kSmem, s, p);
     if (e != cudaSuccess || p.partials == nullptr)
         return e;
-    return launch_pdl(paged_extend_join_kernel<S::kRows>, dim3(p.workers - 1, S::kRows / (8 * kJoinRowsOf<S::kRows>)), dim3(256), 0, s, p);
+    return launch_pdl(paged_extend_join_kernel<S::kRows>,
+                      dim3(p.workers - 1, S::kRows / (8 * kJoinRowsOf<S::kRows>)), dim3(256), 0, s, p);
 }
 
 cudaError_t launch_paged_extend(const PagedExtendParams &in, const ExtendShape &shape, cudaStream_t s)
