@@ -1383,8 +1383,9 @@ ExtendShape paged_extend_shape(int64_t q_rows, int64_t max_q_len, int64_t batch,
     // (the CTAs see the true lengths and leave out those that would have less
     // than kMinRun tiles)
     const int64_t sms = sm_count() > 0 ? sm_count() : 1;
-    const int64_t runs = hkv * (most < filled ? most : filled) * ((keys + kKeys - 1) / kKeys + 1 + kUnitCost) / kMinRun;
-    s.workers = static_cast<int>(runs < 1 ? 1 : (runs < sms ? runs : sms));
+    const int64_t unit = (keys + kKeys - 1) / kKeys + 1 + kUnitCost;
+    const double runs = static_cast<double>(hkv) * (most < filled ? most : filled) * unit / kMinRun;   // (may pass 64 bits)
+    s.workers = runs < 1 ? 1 : (runs < sms ? static_cast<int>(runs) : static_cast<int>(sms));
     const size_t piece = (s.key_split ? kPieceFloats<kRowsBlock> : kPieceFloats<2 * kRowsBlock>)*sizeof(float);
     // No unit is cut, and there is nothing to join, where none has more than
     // kWhole tiles.

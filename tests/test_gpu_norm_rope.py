@@ -279,3 +279,35 @@ def test_wait_runs_out_then_recovers(dtype):
     nv.nvfp4kv_qk_norm_rope(q, k, pos, qo, ko, dev_status=status)
     assert nv.read_device_status(status) == 0
     assert torch.equal(qo, q.to(torch.bfloat16)) and torch.equal(ko, k)      # no norm, no rotation
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T,hq,hkv,rot,inter", [(3701, 10, 3, 128, False), (2999, 20, 6, 64, False), (8200, 1, 1, 128, True)])
+def test_rows_do_not_depend_on_the_split(T, hq, hkv, rot, inter, dtype):
+    """More rows than resident warps, runs that begin and end inside a token and
+    between queries and keys: the bits of short calls, alone and with the cache."""
+    q, k, v = rows(T, hq, dtype, 40), rows(T, hkv, dtype, 41), rows(T, hkv, dtype, 42)
+    w = (1 + 0.5 * rows(1, 1, torch.float32, 43)).reshape(128)
+    pos = torch.arange(T, dtype=torch.int32, device=DEV) + 99999
+    pos[::7] = -1                                                # tokens that are not there
+    slots = torch.arange(3, T + 3, dtype=torch.int32, device=DEV)
+    rope = nv.Rope(inv_freqs(rot), interleaved=inter)
+
+    def outs():
+        return (torch.full((T, hq, 128), 7.0, dtype=torch.bfloat16, device=DEV), torch.full((T, hkv, 128), 7.0, dtype=dtype, device=DEV),
+                torch.full((T, hq, 128), 7.0, dtype=torch.bfloat16, device=DEV), nv.NVFP4Cache.allocate(T // 16 + 2, hkv, device=DEV))
+
+    def run(at, qo, ko, qa, cache):
+        nv.nvfp4kv_qk_norm_rope(q[at], k[at], pos[at], qo[at], ko[at], rope, q_weight=w, k_weight=w)
+        nv.nvfp4kv_qk_norm_rope_append(cache, q[at], k[at], v[at], pos[at], slots[at], qa[at], rope, q_weight=w, k_weight=w)
+
+    whole, parts = outs(), outs()
+    whole[3].pool.zero_()
+    parts[3].pool.zero_()
+    run(slice(0, T), *whole)
+    for a in range(0, T, 97):
+        run(slice(a, min(a + 97, T)), *parts)
+    for a, b in zip(whole[:3] + (whole[3].pool,), parts[:3] + (parts[3].pool,)):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    assert torch.equal(whole[0], whole[2])
+    assert (whole[0][::7] == 7).all() and (whole[1][::7] == 7).all()

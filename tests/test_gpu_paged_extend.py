@@ -395,3 +395,23 @@ def test_calls_in_a_row_share_a_workspace():
     for got, want in outs:
         assert torch.equal(got, want)
     assert not o.any()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_output_at_16_bytes(dtype):
+    """An output that begins 16 bytes behind a 32-byte boundary: the bits of one
+    on the boundary, and nothing around it."""
+    c = Case((900, 3000), (70, 5), 8, 2, seed=24)
+    want = c.run(dtype=dtype)
+    n, pad = want.numel(), 16 // want.element_size()
+    buf = torch.full((n + 2 * pad,), 77.0, dtype=dtype, device=DEV)
+    out = buf[pad:pad + n].view(want.shape)
+    assert out.data_ptr() % 32 == 16
+    c.run(dtype=dtype, out=out)
+    assert torch.equal(out, want) and (buf[:pad] == 77).all() and (buf[pad + n:] == 77).all()
+
+
+def test_workspace_size_of_the_largest_sizes():
+    """Work counted past 64 bits still means every SM."""
+    size, big = nv.nvfp4kv_paged_extend_workspace_size, 2 ** 31 - 1
+    assert size(big, 2 ** 30 - 1, 8192, 65535, 65535, 2 ** 26, 0) == size(4096, 4096, 4, 8, 8, 4096, 0) > 0
