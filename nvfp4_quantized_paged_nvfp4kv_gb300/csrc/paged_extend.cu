@@ -103,13 +103,13 @@ struct Shape {
     };
     static constexpr uint32_t kOffSlot = kOffBar + 8 * kNumBars;             // tensor-memory address, failure flag
     static constexpr uint32_t kOffRun = (kOffSlot + 8 + 15) / 16 * 16;
-    static constexpr uint32_t kOffMl = kOffRun + 64;         // key split: the second block's (reference, sum) rows
+    static constexpr uint32_t kOffMl = kOffRun + 80;         // key split: the second block's (reference, sum) rows
     static constexpr uint32_t kSmem = kOffMl + (kKeySplit ? 8 * kRowsBlock : 0) + 1024;      // + slack to align the base
     // (one CTA an SM: all of tensor memory is its own)
     static_assert(kSmem <= 227 * 1024 && 2 * kSmem > 228 * 1024, "shared memory");
 };
-// the sequences' weights, summed up, take the operand stages' place while a CTA looks for its run
-static_assert((kMaxBatch + 1) * 8 <= 2 * kStages * kOpBytes, "weight table");
+// the sequences' weights, summed up, and chunks take the operand stages' place while a CTA looks for its run
+constexpr uint32_t kTableBytes = (kMaxBatch + 2) * 8;
 
 __device__ __forceinline__ void st_shared128(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
 {
@@ -421,10 +421,13 @@ __device__ __forceinline__ int row_tiles_of(const PagedExtendParams &p, int b, C
     return read_chunk(p, b, c) ? (c.count * p.group + kRows - 1) / kRows : 0;
 }
 
-// Where a CTA's run begins, and how much it holds (in tiles and units).
+// Where a CTA's run begins (c, n: that sequence's chunk and row tiles), and how
+// much it holds (in tiles and units).
 struct Run {
     int h, b, tile, off;
     long long left;
+    Chunk c;
+    int n;
 };
 
 constexpr int kMinRun = 3;               // a run is at least this long, else fewer CTAs take part
@@ -441,15 +444,22 @@ constexpr int kSnap = 2, kWhole = 8;
 struct Place {
     int h, b, tile, off;
     long long at;
+    Chunk c;
+    int n;                               // row tiles of the sequence
 };
 
+// Chunks that find_run keeps in shared memory for find_cut: with nearly all of it
+// taken there is no first-level cache, and a second read costs as much as the
+// first.
+constexpr int kKeptChunks = 1024;
+
 // Where the cut at `at` of `head` x hkv places falls (whole warp); table: batch +
-// 1 running sums.
+// 1 running sums; kept: the first kKeptChunks sequences' chunks.
 template <int kRows>
 __device__ __forceinline__ Place find_cut(const PagedExtendParams &p, long long at, long long head,
-                                          const long long *table, int lane)
+                                          const long long *table, const Chunk *kept, int lane)
 {
-    Place r{p.hkv, 0, 0, 0, at};
+    Place r{p.hkv, 0, 0, 0, at, {0, 0, 0}, -1};
     if (at >= head * p.hkv)
         return r;
     r.h = static_cast<int>(at / head);
@@ -464,8 +474,10 @@ __device__ __forceinline__ Place find_cut(const PagedExtendParams &p, long long 
     }
     r.b = x;
     rest -= table[x];
-    Chunk c;
-    const int n = row_tiles_of<kRows>(p, x, c);
+    Chunk c = kept[min(x, kKeptChunks - 1)];
+    const int n = x < kKeptChunks ? (c.count * p.group + kRows - 1) / kRows : row_tiles_of<kRows>(p, x, c);
+    r.c = c;
+    r.n = n;
     for (int i0 = 0; i0 < n; i0 += 32) {
         Unit u{};
         int w = 0;
@@ -499,11 +511,11 @@ __device__ __forceinline__ Place find_cut(const PagedExtendParams &p, long long 
     return r;
 }
 
-// Finds the run of worker `worker` of `workers`; whole CTA.  `table`: batch + 1
-// sums in shared memory.
+// Finds the run of worker `worker` of `workers`; whole CTA.  In shared memory:
+// `table`, batch + 1 sums, and `kept`, kKeptChunks chunks.
 template <int kRows>
 __device__ __forceinline__ void find_run(const PagedExtendParams &p, int worker, int workers, long long *table,
-                                         Run *run)
+                                         Chunk *kept, Run *run)
 {
     __shared__ long long part[32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
@@ -520,6 +532,8 @@ __device__ __forceinline__ void find_run(const PagedExtendParams &p, int worker,
             const int n = row_tiles_of<kRows>(p, b, c);
             if (n == 0 && sub == 0 && worker == 0 && !read_chunk(p, b, c))
                 report(p.dev_status, NVFP4KV_DEV_BAD_LEN);
+            if (sub == 0 && b < kKeptChunks)
+                kept[b] = {c.c0, n > 0 ? c.count : 0, c.len};
             Unit u{};
             for (int i = sub; i < n; i += width) {
                 u.set<kRows>(p, c, i);
@@ -562,13 +576,16 @@ __device__ __forceinline__ void find_run(const PagedExtendParams &p, int worker,
     if (warp < 2) {
         const long long head = table[p.batch], all = head * p.hkv;
         const long long use = min(static_cast<long long>(workers), max(1LL, all / kMinRun));
-        const Place r = find_cut<kRows>(p, all * min(worker + warp, static_cast<int>(use)) / use, head, table, lane);
+        const Place r = find_cut<kRows>(p, all * min(worker + warp, static_cast<int>(use)) / use, head, table, kept,
+                                        lane);
         if (lane == 0) {
             if (warp == 0) {
                 run->h = r.h;
                 run->b = r.b;
                 run->tile = r.tile;
                 run->off = r.off;
+                run->c = r.c;
+                run->n = r.n;
             }
             part[warp] = r.at;
         }
@@ -604,7 +621,7 @@ struct Walk {
     int n, at, off;                      // row tiles of the sequence, the next one, and its place to begin at
     long long left;
 
-    __device__ __forceinline__ explicit Walk(const Run &r) : u{}, c{}, n(-1), at(r.tile), off(r.off), left(r.left)
+    __device__ __forceinline__ explicit Walk(const Run &r) : u{}, c(r.c), n(r.n), at(r.tile), off(r.off), left(r.left)
     {
         u.h = r.h;
         u.b = r.b;
@@ -718,7 +735,9 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
         Note *note = notes_of<kRows>(p) + blockIdx.x;
         note->tail = note->head = 0;
     }
-    find_run<kRows>(p, blockIdx.x, gridDim.x, reinterpret_cast<long long *>(gbase + S::kOffK), run);
+    find_run<kRows>(p, blockIdx.x, gridDim.x, reinterpret_cast<long long *>(gbase + S::kOffK),
+                    reinterpret_cast<Chunk *>(gbase + S::kOffK + kTableBytes), run);
+    static_assert(kTableBytes + kKeptChunks * sizeof(Chunk) <= 2 * kStages * kOpBytes && sizeof(Run) <= 80, "tables");
     const Run start = *run;
     // The units of this CTA's run, one after the other: fn(unit) for each with
     // keys, until it returns false.
@@ -734,11 +753,9 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
 
     // the rows of Q to come, into L2: the first unit's now, later the next row
     // tile's while the last one is worked on
-    auto ask_for_q = [&](Unit u, int at) {
-        Chunk c;
-        if (tid >= kRows || at >= row_tiles_of<kRows>(p, u.b, c))
+    auto ask_for_q = [&](const Unit &u) {
+        if (tid >= kRows)
             return;
-        u.set<kRows>(p, c, at);
         const Row row = row_of<kRows>(p, u, tid);
         if (row.live) {
             const uint16_t *q = p.q + row.at * kHeadDim;
@@ -746,11 +763,11 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
             asm volatile("prefetch.global.L2 [%0];" ::"l"(q + kHeadDim / 2));
         }
     };
-    if (start.left > 0) {
+    if (start.left > 0 && start.tile < start.n) {
         Unit u{};
         u.h = start.h;
-        u.b = start.b;
-        ask_for_q(u, start.tile);
+        u.set<kRows>(p, start.c, start.tile);
+        ask_for_q(u);
     }
     if (warp == S::kMmaWarp)
         tmem_alloc(base + S::kOffSlot, 2 * kTmBlock);
@@ -1091,7 +1108,11 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
                 warp_arrive(B(S::kQFull + blk), lane);
             }
         }
-        ask_for_q(u, u.tile + 1);
+        if (u.row0 + kRows < u.rows) {
+            Unit after = u;
+            after.row0 += kRows;
+            ask_for_q(after);
+        }
         const int pos = u.first_pos + row.t;     // keys lo .. pos are visible
         const int lo = p.window > 0 ? pos - p.window + 1 : 0;
         const uint64_t inv2 = f32x2_pack(inv, inv);
