@@ -502,8 +502,9 @@ nvfp4kv_status nvfp4kv_release_pages(const int32_t *old_lens, const int32_t *kee
  *   (y_a, y_b) -> scale * (y_a cos t - y_b sin t, y_b cos t + y_a sin t),
  *   t = n * inv_freq[i], for the rotary_dim / 2 channel pairs (a, b) =
  *   (i, i + rotary_dim / 2), or (2i, 2i + 1) when interleaved.
- * Channels from rotary_dim on keep y.  Arithmetic in fp32, rounded once; the
- * angles are exact to 2^-32 of a turn at every position. */
+ * Channels from rotary_dim on keep y.  Arithmetic in fp32, rounded once; whole
+ * turns are taken off the angles in 64-bit integers, so they are as good at
+ * every position as near 0. */
 typedef struct {
     const double *inv_freq;      /* HOST array of rotary_dim / 2 finite values, radians a position */
     int32_t rotary_dim;          /* 0 (no rotation), 32, 64, 96 or 128 */
