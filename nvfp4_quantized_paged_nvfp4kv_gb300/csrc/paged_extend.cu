@@ -103,8 +103,9 @@ struct Shape {
     };
     static constexpr uint32_t kOffSlot = kOffBar + 8 * kNumBars;             // tensor-memory address, failure flag
     static constexpr uint32_t kOffRun = (kOffSlot + 8 + 15) / 16 * 16;
-    static constexpr uint32_t kOffMl = kOffRun + 80;         // key split: the second block's (reference, sum) rows
-    static constexpr uint32_t kSmem = kOffMl + (kKeySplit ? 8 * kRowsBlock : 0) + 1024;      // + slack to align the base
+    // key split: (reference, sum) of both blocks' rows, and the rows' score factors
+    static constexpr uint32_t kOffMl = kOffRun + 80, kOffInv = kOffMl + (kKeySplit ? 2 * 8 * kRowsBlock : 0);
+    static constexpr uint32_t kSmem = kOffInv + (kKeySplit ? 4 * kRowsBlock : 0) + 1024;     // + slack to align the base
     // (one CTA an SM: all of tensor memory is its own)
     static_assert(kSmem <= 227 * 1024 && 2 * kSmem > 228 * 1024, "shared memory");
 };
@@ -714,7 +715,7 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
             mbar_init(B(S::kTurn + k), kKeySplit ? 1 : 2);
         }
         for (int k = 0; k < 2; ++k) {
-            mbar_init(B(S::kQFull + k), kRowsBlock / 32);
+            mbar_init(B(S::kQFull + k), (kKeySplit ? 2 : 1) * kRowsBlock / 32);
             mbar_init(B(S::kSFull + k), 1);
             mbar_init(B(S::kPFull + k), kRowsBlock / 32);
             mbar_init(B(S::kPFull + 2 + k), kRowsBlock / 32);
@@ -724,8 +725,8 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
             mbar_init(B(S::kExit + k), 1);
             mbar_init(B(S::kVDone + k), 1);
         }
-        mbar_init(B(S::kJoin), kRowsBlock / 32);
-        mbar_init(B(S::kFree), kRowsBlock / 32);
+        mbar_init(B(S::kJoin), kSoftmaxThreads / 32);
+        mbar_init(B(S::kFree), kSoftmaxThreads / 32);
         *fail = 0;
         fence_mbar_init();
     }
@@ -1039,41 +1040,48 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
             return __all_sync(kFullMask, wait_bar(B(k), parity, fail, p.dev_status, p.wait_limit));
         };
         int ib = 0, un = 0, dn = 0;              // the block's tiles, units, and units with tiles, so far
-        float2 *second = reinterpret_cast<float2 *>(gbase + S::kOffMl);
+        float2 *ml = reinterpret_cast<float2 *>(gbase + S::kOffMl);
+        volatile float *invs = reinterpret_cast<volatile float *>(gbase + S::kOffInv);
         for_units([&](const Unit &u) {
         const Row row = row_of<kRows>(p, u, tid);
         const bool has_row = row.live;
         const int64_t out_row = row.at;
+        // With split keys both blocks read both blocks' O at the end of a unit, and
+        // share Q: the last unit must be over for both.
+        if (kKeySplit && un > 0 && !wait_warp(S::kFree, (un - 1) & 1))
+            return false;
         // The rows of Q, each scaled by a power of two; inv takes this thread's
         // scores to log2 units.  A warp loads its 32 rows two at a time, half a
-        // warp a row (a row a thread, 16 bytes at a time, took 5 us).
+        // warp a row (a row a thread, 16 bytes at a time, took 5 us); with split
+        // keys the blocks take half of the rows each.
         const unsigned live = __ballot_sync(kFullMask, has_row);
         const uint32_t stage = base + S::kOffQ + (kKeySplit ? 0 : blk) * kOpBytes;
         float inv;
         {
-            const int piece = lane & 15;
-            uint4 w[16];
+            constexpr int kN = kKeySplit ? 8 : 16;
+            const int piece = lane & 15, first = kKeySplit ? 16 * blk : 0;
+            uint4 w[kN];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                const int of = 2 * i + (lane >> 4);
+            for (int i = 0; i < kN; ++i) {
+                const int of = first + 2 * i + (lane >> 4);
                 const int64_t at = __shfl_sync(kFullMask, out_row, of);
                 w[i] = (live >> of) & 1u ? __ldg(reinterpret_cast<const uint4 *>(p.q + at * kHeadDim) + piece)
                                          : make_uint4(0, 0, 0, 0);
             }
             const float ks = p.hs.per_head ? p.hs.k[u.h] : p.gscale;
             const float to_log2 = 256.f * ks * fabsf(p.qscale);
-            // each row's largest |q| (bf16 bits): 16 reductions over half a warp at
+            // each row's largest |q| (bf16 bits): kN reductions over half a warp at
             // once, halving the rows a lane holds at every exchange; lane l ends
-            // with row 2 (l mod 16) + l / 16
-            uint32_t top[16];
+            // with row first + 2 (l mod kN) + l / 16
+            uint32_t top[kN];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
+            for (int i = 0; i < kN; ++i) {
                 const uint32_t m2 = __vmaxu2(__vmaxu2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu),
                                              __vmaxu2(w[i].z & 0x7fff7fffu, w[i].w & 0x7fff7fffu));
                 top[i] = max(m2 & 0xffffu, m2 >> 16);
             }
 #pragma unroll
-            for (int o = 8; o > 0; o >>= 1) {
+            for (int o = kN / 2; o > 0; o >>= 1) {
                 const bool upper = lane & o;
 #pragma unroll
                 for (int i = 0; i < o; ++i) {
@@ -1081,32 +1089,34 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
                     top[i] = max(upper ? top[i + o] : top[i], got);
                 }
             }
+            if (kN == 8)
+                top[0] = max(top[0], __shfl_xor_sync(kFullMask, top[0], 8));
             // 2^e puts it into [2^14, 2^15)
             const int e = min(14 - (static_cast<int>(top[0] >> 7) - 127), 112);
-            auto unscaled = [&](int ee) { return __uint_as_float(static_cast<uint32_t>(127 - ee) << 23) * to_log2; };
-            if (!kKeySplit || blk == 0) {
-                float sc = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
-                sc = p.qscale < 0.f ? -sc : sc;          // scores keep their order: references are taken before inv
-                if (unscaled(e) == 0.f)
-                    sc = 0.f;                            // all scores are 0
+            const float unscaled = __uint_as_float(static_cast<uint32_t>(127 - e) << 23) * to_log2;
+            float sc = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+            sc = p.qscale < 0.f ? -sc : sc;      // scores keep their order: references are taken before inv
+            if (unscaled == 0.f)
+                sc = 0.f;                        // all scores are 0
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float f = __shfl_sync(kFullMask, sc, (lane & 16) | i);
-                    auto two = [&](uint32_t q2) {
-                        return pack_f16x2(__uint_as_float(q2 << 16) * f, __uint_as_float(q2 & 0xffff0000u) * f);
-                    };
-                    const uint32_t at = 32u * (warp & 3) + 2u * i + (lane >> 4);
-                    st_shared128(stage + (piece >> 3) * kHalfBytes + at * 128u + (((piece & 7u) ^ (at & 7u)) << 4),
-                                 two(w[i].x), two(w[i].y), two(w[i].z), two(w[i].w));
-                }
+            for (int i = 0; i < kN; ++i) {
+                const float f = __shfl_sync(kFullMask, sc, (lane & 16) | i);
+                auto two = [&](uint32_t q2) {
+                    return pack_f16x2(__uint_as_float(q2 << 16) * f, __uint_as_float(q2 & 0xffff0000u) * f);
+                };
+                const uint32_t at = 32u * (warp & 3) + first + 2u * i + (lane >> 4);
+                st_shared128(stage + (piece >> 3) * kHalfBytes + at * 128u + (((piece & 7u) ^ (at & 7u)) << 4),
+                             two(w[i].x), two(w[i].y), two(w[i].z), two(w[i].w));
             }
-            inv = unscaled(__shfl_sync(kFullMask, e, ((lane & 1) << 4) | (lane >> 1)));
-            if (inv == 0.f)
-                inv = 1.f;
-            if (!kKeySplit || blk == 0) {
-                fence_async_shared();
-                warp_arrive(B(S::kQFull + blk), lane);
+            inv = unscaled == 0.f ? 1.f : unscaled;
+            if constexpr (kKeySplit) {
+                if (!(lane & 8))                 // (read once the first scores are there)
+                    invs[32 * (warp & 3) + first + 2 * (lane & 7) + (lane >> 4)] = inv;
+            } else {
+                inv = __shfl_sync(kFullMask, inv, ((lane & 1) << 4) | (lane >> 1));
             }
+            fence_async_shared();
+            warp_arrive(B(S::kQFull + (kKeySplit ? 0 : blk)), lane);
         }
         if (u.row0 + kRows < u.rows) {
             Unit after = u;
@@ -1115,19 +1125,17 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
         }
         const int pos = u.first_pos + row.t;     // keys lo .. pos are visible
         const int lo = p.window > 0 ? pos - p.window + 1 : 0;
-        const uint64_t inv2 = f32x2_pack(inv, inv);
         float m_used = -INFINITY, l = 0.f;
         bool ok = true;
         const int my_tiles = kKeySplit ? (u.n_tiles + 1 - blk) / 2 : u.n_tiles;
-        // the first block reads the second one's O at the end of a unit: that
-        // must be over before the next weights bring the next O
-        if (kKeySplit && blk == 1 && un > 0)
-            ok = wait_warp(S::kFree, (un - 1) & 1);
         for (int j = 0; ok && j < my_tiles; ++j) {
             const int i = ib + j;
             if (!(ok = wait_warp(S::kSFull + blk, i & 1)))
                 break;
             tc_fence_after_sync();
+            if (kKeySplit && j == 0)
+                inv = invs[r];
+            const uint64_t inv2 = f32x2_pack(inv, inv);
             const int k0 = (u.tile_lo + u.from + (kKeySplit ? 2 * j + blk : j)) * kKeys;
             const int hi_j = pos + 1 - k0, lo_j = lo - k0;
             // weights of keys 0 .. 63 go over the columns of scores 0 .. 31, of
@@ -1169,36 +1177,36 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
             if (!ok)
                 break;
         }
-        // The block's products have landed; with split keys the first block, which
-        // puts both together, also waits for the second one's.
+        // The block's products have landed; with split keys the other block's too,
+        // and each block puts half of the channels together.
         if (ok && my_tiles > 0)
             ok = wait_warp(S::kDone + blk, dn++ & 1);
-        float w0 = 1.f, w1 = 0.f;                // weights of this block's O and of the other's
+        float w0 = 1.f, w1 = 0.f;                // weights of the blocks' O (row blocks: of its own)
         if constexpr (kKeySplit) {
-            if (blk == 1) {
-                if (ok) {
-                    second[r] = make_float2(m_used, l);
-                    tc_fence_before_sync();
-                    warp_arrive(B(S::kJoin), lane);      // (after the wait for its products)
-                }
-            } else if (ok && (ok = wait_warp(S::kJoin, un & 1))) {
-                const float2 o = second[r];
-                const float M = fmaxf(m_used, o.x);
-                w0 = m_used == -INFINITY ? 0.f : fast_exp2(m_used - M);
-                w1 = o.x == -INFINITY ? 0.f : fast_exp2(o.x - M);
-                l = (l != l || o.y != o.y) ? NAN : l * w0 + o.y * w1;
-                m_used = M;
+            if (ok) {
+                ml[kRowsBlock * blk + r] = make_float2(m_used, l);
+                tc_fence_before_sync();
+                warp_arrive(B(S::kJoin), lane);
+                ok = wait_warp(S::kJoin, un & 1);
+            }
+            if (ok) {
+                const float2 a = ml[r], b = ml[kRowsBlock + r];
+                m_used = fmaxf(a.x, b.x);
+                w0 = a.x == -INFINITY ? 0.f : fast_exp2(a.x - m_used);
+                w1 = b.x == -INFINITY ? 0.f : fast_exp2(b.x - m_used);
+                l = (a.y != a.y || b.y != b.y) ? NAN : a.y * w0 + b.y * w1;
             }
         }
         tc_fence_after_sync();
-        if (ok && (!kKeySplit || blk == 0)) {
+        if (ok) {
             const float vs = (p.hs.per_head ? p.hs.v[u.h] : p.gscale) * 256.f;
             const bool whole = u.whole();
             const float f = !whole ? vs : (l > 0.f ? vs / l : (l == 0.f ? 0.f : l));   // a NaN sum stays NaN
             const float f0 = w0 * f, f1 = w1 * f;
+            const uint32_t to = kKeySplit ? tb - blk * kTmBlock : tb;    // (the first block's)
             const int piece = 2 * blockIdx.x + (u.from > 0 ? 0 : 1), rr = tid % kRows;
             float *part = p.partials + kPieceFloats<kRows> * piece;
-            if (has_row && !whole)
+            if (has_row && !whole && (!kKeySplit || blk == 0))
                 reinterpret_cast<float2 *>(part + kRows * kHeadDim)[rr] = make_float2(m_used, l);
             if (!whole && tid == 0) {
                 Note *note = notes_of<kRows>(p) + blockIdx.x;
@@ -1217,10 +1225,10 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
             uint8_t *dst = whole ? static_cast<uint8_t *>(p.out) + out_row * kHeadDim * (p.out_f32 ? 4 : 2)
                                  : reinterpret_cast<uint8_t *>(part + rr * kHeadDim);
 #pragma unroll 1
-            for (int cb = 0; cb < 4; ++cb) {
+            for (int cb = kKeySplit ? 2 * blk : 0; cb < (kKeySplit ? 2 * blk + 2 : 4); ++cb) {
                 uint32_t o[32];
                 __syncwarp();                    // (lanes without a row skip the stores)
-                tmem_ld32(tb + kTmO + 32 * cb, o);
+                tmem_ld32(to + kTmO + 32 * cb, o);
                 tmem_wait_ld();
 #pragma unroll
                 for (int j = 0; j < 32; ++j)
@@ -1228,7 +1236,7 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
                 if constexpr (kKeySplit) {
                     // (the second block's columns of the same lanes; nothing there without its tiles)
                     uint32_t w[32];
-                    tmem_ld32(tb + kTmBlock + kTmO + 32 * cb, w);
+                    tmem_ld32(to + kTmBlock + kTmO + 32 * cb, w);
                     tmem_wait_ld();
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
