@@ -57,7 +57,7 @@
 //
 // Bound.  2,048 tokens of 48 + 8 heads at 32K: 1,400 TFLOP/s, 73% of a library
 // GEMM's rate; a tile's softmax, P V and Q K^T follow one another, and two blocks
-// fill most of each other's gaps.  16 tokens each of 12 sequences at 8K: 75 us,
+// fill most of each other's gaps.  16 tokens each of 12 sequences at 8K: 73 us,
 // the conversion of a tile for one block's rows only.
 #include "tcgen05.cuh"
 
@@ -1061,12 +1061,15 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
             constexpr int kN = kKeySplit ? 8 : 16;
             const int piece = lane & 15, first = kKeySplit ? 16 * blk : 0;
             uint4 w[kN];
+            // (places of the tile's rows from its first token's on pass no 32 bits)
+            const int64_t start = static_cast<int64_t>(u.c0 + u.row0 / p.group) * p.hq + u.h * p.group;
+            const uint4 *from = reinterpret_cast<const uint4 *>(p.q + start * kHeadDim) + piece;
+            const int rel = static_cast<int>(out_row - start);
 #pragma unroll
             for (int i = 0; i < kN; ++i) {
                 const int of = first + 2 * i + (lane >> 4);
-                const int64_t at = __shfl_sync(kFullMask, out_row, of);
-                w[i] = (live >> of) & 1u ? __ldg(reinterpret_cast<const uint4 *>(p.q + at * kHeadDim) + piece)
-                                         : make_uint4(0, 0, 0, 0);
+                const int at = __shfl_sync(kFullMask, rel, of);
+                w[i] = (live >> of) & 1u ? __ldg(from + static_cast<int64_t>(at) * (kHeadDim / 8)) : make_uint4(0, 0, 0, 0);
             }
             const float ks = p.hs.per_head ? p.hs.k[u.h] : p.gscale;
             const float to_log2 = 256.f * ks * fabsf(p.qscale);
