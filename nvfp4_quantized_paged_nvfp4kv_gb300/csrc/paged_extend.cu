@@ -98,14 +98,14 @@ struct Shape {
     enum : int {
         kRawFull = 0, kRawEmpty = kRawFull + kRaw, kKFull = kRawEmpty + kRaw, kVFull = kKFull + kStages,
         kTurn = kVFull + kStages, kQFull = kTurn + kStages, kSFull = kQFull + 2, kPFull = kSFull + 2,
-        kHalf = kPFull + 4, kDone = kHalf + 2, kGo = kDone + 2, kExit = kGo + 2, kJoin = kExit + 2, kFree = kJoin + 1, kVDone = kFree + 1,
-        kNumBars = kVDone + 2
+        kHalf = kPFull + 4, kDone = kHalf + 2, kGo = kDone + 2, kExit = kGo + 2, kJoin = kExit + 2, kFree = kJoin + 1,
+        kVDone = kFree + 1, kNumBars = kVDone + 2
     };
     static constexpr uint32_t kOffSlot = kOffBar + 8 * kNumBars;             // tensor-memory address, failure flag
     static constexpr uint32_t kOffRun = (kOffSlot + 8 + 15) / 16 * 16;
     // key split: (reference, sum) of both blocks' rows, and the rows' score factors
     static constexpr uint32_t kOffMl = kOffRun + 80, kOffInv = kOffMl + (kKeySplit ? 2 * 8 * kRowsBlock : 0);
-    static constexpr uint32_t kSmem = kOffInv + (kKeySplit ? 4 * kRowsBlock : 0) + 1024;     // + slack to align the base
+    static constexpr uint32_t kSmem = kOffInv + (kKeySplit ? 4 * kRowsBlock : 0) + 1024;   // + slack to align the base
     // (one CTA an SM: all of tensor memory is its own)
     static_assert(kSmem <= 227 * 1024 && 2 * kSmem > 228 * 1024, "shared memory");
 };
@@ -122,8 +122,8 @@ __device__ __forceinline__ void store_sector(uint8_t *dst, bool wide, uint32_t a
                                              uint32_t e, uint32_t f, uint32_t g, uint32_t h)
 {
     if (wide) {
-        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(a), "r"(b), "r"(c), "r"(d),
-                     "r"(e), "r"(f), "r"(g), "r"(h)
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst), "r"(a), "r"(b), "r"(c),
+                     "r"(d), "r"(e), "r"(f), "r"(g), "r"(h)
                      : "memory");
     } else {
         reinterpret_cast<uint4 *>(dst)[0] = make_uint4(a, b, c, d);
@@ -1076,7 +1076,9 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
             for (int i = 0; i < kN; ++i) {
                 const int of = first + 2 * i + (lane >> 4);
                 const int at = __shfl_sync(kFullMask, rel, of);
-                w[i] = (live >> of) & 1u ? __ldg(from + static_cast<int64_t>(at) * (kHeadDim / 8)) : make_uint4(0, 0, 0, 0);
+                w[i] = make_uint4(0, 0, 0, 0);
+                if ((live >> of) & 1u)
+                    w[i] = __ldg(from + static_cast<int64_t>(at) * (kHeadDim / 8));
             }
             const float ks = p.hs.per_head ? p.hs.k[u.h] : p.gscale;
             const float to_log2 = 256.f * ks * fabsf(p.qscale);
@@ -1423,7 +1425,8 @@ ExtendShape paged_extend_shape(int64_t q_rows, int64_t max_q_len, int64_t batch,
     // than kMinRun tiles)
     const int64_t sms = sm_count() > 0 ? sm_count() : 1;
     const int64_t unit = (keys + kKeys - 1) / kKeys + 1 + kUnitCost;
-    const double runs = static_cast<double>(hkv) * (most < filled ? most : filled) * unit / kMinRun;   // (may pass 64 bits)
+    // (may pass 64 bits)
+    const double runs = static_cast<double>(hkv) * (most < filled ? most : filled) * unit / kMinRun;
     s.workers = runs < 1 ? 1 : (runs < sms ? static_cast<int>(runs) : static_cast<int>(sms));
     const size_t piece = (s.key_split ? kPieceFloats<kRowsBlock> : kPieceFloats<2 * kRowsBlock>)*sizeof(float);
     // No unit is cut, and there is nothing to join, where none has more than
