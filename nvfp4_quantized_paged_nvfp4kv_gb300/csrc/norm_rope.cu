@@ -34,7 +34,7 @@
 //
 // Bound.  8,192 bf16 tokens of 48 + 8 heads out of a fused projection's rows:
 // 235 MB in 43 us, 5.5 TB/s, 82% of a copy's rate, with 58% of the issue slots
-// taken.  With the cache write, 244 MB in 45 us.
+// taken.  With the cache write, 244 MB in 43 us.
 #include "nvfp4kv.h"
 #include "record_write.cuh"
 #include <type_traits>
@@ -179,9 +179,16 @@ struct Feed {
     }
 };
 
+// Where a channel's partner is: in the lane's other piece (half-split rotations of
+// all channels), in the neighbouring channel (interleaved ones, and no rotation),
+// or in another lane (half-split ones of some channels).  A kernel each: what the
+// others need costs registers and instruction fetches (half-split, with the cache
+// write: 43.1 us alone, 44.5 beside one other form, 46.0 beside two).
+enum Pairs : int { kOpposite, kNeighbours, kTwoLanes };
+
 // One warp's rows, quads from .. to - 1 of the call.  False when a wait for staged
 // rows gave up.
-template <bool kBf16, bool kAppend, bool kSwaps>
+template <bool kBf16, bool kAppend, int kPairs>
 __device__ __forceinline__ bool rows_of_warp(const NormRopeParams &p, NrShared &sh, uint32_t ring, long long from,
                                              long long to)
 {
@@ -215,7 +222,14 @@ __device__ __forceinline__ bool rows_of_warp(const NormRopeParams &p, NrShared &
         cs[i] = make_float2(c * p.rope_scale, sn * p.rope_scale);
     }
     __syncwarp();
-    // y_c = rstd (x_c wc + x_partner ws), two channels in a register
+    // y_c = rstd (x_c wc + x_partner ws), two channels in a register.  A channel
+    // that is not turned must not see any other one, whose infinity or NaN would
+    // reach it through a zero factor.  It has -0 for ws and 0 for its partner (and
+    // so keeps the sign of a zero), or, in bf16 rows whose pieces come by shuffles,
+    // itself for its partner and half the weight for both: x w / 2, rounded, plus
+    // x w / 2 rounds to what x w rounds to (2 us less than zeroing the pieces;
+    // fp32 rows may hold values whose half is not a number of fp32).
+    constexpr bool kHalves = kPairs == kTwoLanes && kBf16;
     uint64_t wc[8], ws[8];
     auto tables = [&](const float *wt) {
         float4 *tab = sh.table[warp];
@@ -225,7 +239,8 @@ __device__ __forceinline__ bool rows_of_warp(const NormRopeParams &p, NrShared &
             // place u: piece u / 32, channels 64 piece + 8 (u mod 8) + 2 (u / 8 mod 4) and the next
             const int c = 64 * (u >> 5) + 8 * (u & 7) + 2 * ((u >> 3) & 3);
             const float2 own = *reinterpret_cast<const float2 *>(wt + c);
-            float4 v = make_float4(own.x, own.y, 0.f, 0.f);
+            float4 v = kHalves ? make_float4(0.5f * own.x, 0.5f * own.y, 0.5f * own.x, 0.5f * own.y)
+                               : make_float4(own.x, own.y, -0.f, -0.f);
             if (c < p.rot) {
                 if (p.interleaved) {
                     const float2 a = cs[c >> 1];
@@ -306,33 +321,42 @@ __device__ __forceinline__ bool rows_of_warp(const NormRopeParams &p, NrShared &
             y[2 * j] = f32x2_lo(v);
             y[2 * j + 1] = f32x2_hi(v);
         };
-        if constexpr (!kSwaps) {
-            if (p.interleaved) {
+        if constexpr (kPairs == kOpposite) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                turn(j, x2[j ^ 4]);
+        } else if constexpr (kPairs == kNeighbours) {
+            if (p.rot == kHeadDim) {
 #pragma unroll
                 for (int j = 0; j < 8; ++j)
                     turn(j, f32x2_pack(x[2 * j + 1], x[2 * j]));
             } else {
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    turn(j, x2[j ^ 4]);
+                for (int j = 0; j < 8; ++j) {
+                    const bool turned = c0 + 64 * (j >> 2) < p.rot;      // (a piece as a whole)
+                    turn(j, turned ? f32x2_pack(x[2 * j + 1], x[2 * j]) : 0);
+                }
             }
         } else {
-            RawBlock<kBf16> other = cur;
+            // (a piece that is not turned: the lane's own, or zeros)
+            RawBlock<kBf16> other = kHalves ? cur : RawBlock<kBf16>{};
             constexpr int n = kBf16 ? 1 : 2;     // 16-byte words of a piece
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
                 if (k == 1 && p.rot <= 64)
                     break;                       // nothing turns in the second pieces
                 const int mate = mate_chunk(k), from = (lane & 24) | (mate & 7);
+                const bool turned = c0 + 64 * k < p.rot;
 #pragma unroll
                 for (int i = 0; i < n; ++i) {
-                    const uint4 a = shuffled(cur.v[i], from);
-                    other.v[n * k + i] = a;
+                    uint4 a = shuffled(cur.v[i], from);
                     if (p.rot > 64) {
                         const uint4 b = shuffled(cur.v[n + i], from);
                         if (mate >= 8)
-                            other.v[n * k + i] = b;
+                            a = b;
                     }
+                    if (kHalves || turned)
+                        other.v[n * k + i] = a;
                 }
             }
             float z[16];
@@ -454,7 +478,7 @@ __device__ __forceinline__ void v_pair_job(const NormRopeParams &p, int pr, int 
 
 // Each warp takes an equal run of the call's quads, token-major, and then of the
 // V blocks, one a thread.
-template <bool kBf16, bool kAppend, bool kSwaps>
+template <bool kBf16, bool kAppend, int kPairs>
 __global__ void __launch_bounds__(kNrThreads, Ring<kBf16>::kCtas)
     norm_rope_kernel(const __grid_constant__ NormRopeParams p)
 {
@@ -485,7 +509,7 @@ __global__ void __launch_bounds__(kNrThreads, Ring<kBf16>::kCtas)
     const long long quads = static_cast<long long>(p.num_tokens) * p.quads;
     const long long warps = static_cast<long long>(gridDim.x) * kNrWarps, rows = min(warps, quads);
     const long long me = static_cast<long long>(blockIdx.x) * kNrWarps + warp, run = min(me, rows);
-    if (!rows_of_warp<kBf16, kAppend, kSwaps>(p, sh,
+    if (!rows_of_warp<kBf16, kAppend, kPairs>(p, sh,
                                               smem_addr(nr_ring) + warp * Ring<kBf16>::kStages * Ring<kBf16>::kStage,
                                               quads * run / rows, quads * min(run + 1, rows) / rows))
         return;
@@ -502,11 +526,11 @@ __global__ void __launch_bounds__(kNrThreads, Ring<kBf16>::kCtas)
     }
 }
 
-template <bool kBf16, bool kAppend, bool kSwaps>
+template <bool kBf16, bool kAppend, int kPairs>
 cudaError_t launch_rows(const NormRopeParams &p, long long jobs, int sms, cudaStream_t s)
 {
     using G = Ring<kBf16>;
-    const auto kernel = norm_rope_kernel<kBf16, kAppend, kSwaps>;
+    const auto kernel = norm_rope_kernel<kBf16, kAppend, kPairs>;
     if (G::kSmem > 48 * 1024) {
         const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, G::kSmem);
         if (e != cudaSuccess)
@@ -527,12 +551,11 @@ cudaError_t launch_norm_rope(const NormRopeParams &in, cudaStream_t s)
     const bool append = p.pool != nullptr;
     p.v_jobs = append ? ((static_cast<long long>(p.num_tokens) + 2) / 2 * p.hkv * 8 + 31) / 32 : 0;
     const long long jobs = static_cast<long long>(p.num_tokens) * p.quads + p.v_jobs;
-    // rotations whose pairs are in two lanes have a kernel of their own (their
-    // registers cost the others 1 us of 44)
     auto launch = [&](auto bf16, auto app) {
-        const bool swaps = !p.interleaved && p.rot > 0 && p.rot < kHeadDim;
-        return swaps ? launch_rows<bf16.value, app.value, true>(p, jobs, sms, s)
-                     : launch_rows<bf16.value, app.value, false>(p, jobs, sms, s);
+        if (p.interleaved || p.rot == 0)
+            return launch_rows<bf16.value, app.value, kNeighbours>(p, jobs, sms, s);
+        return p.rot == kHeadDim ? launch_rows<bf16.value, app.value, kOpposite>(p, jobs, sms, s)
+                                 : launch_rows<bf16.value, app.value, kTwoLanes>(p, jobs, sms, s);
     };
     if (append)
         return p.in_bf16 ? launch(std::true_type(), std::true_type()) : launch(std::false_type(), std::true_type());
