@@ -71,6 +71,11 @@ constexpr int kGrans = kKeys / kGranKeys;
 constexpr int kGranPages = kGranKeys / kPageSize;
 constexpr int kConvThreads = 128;
 constexpr float kMaxSum = 32768.f;             // of 64 weights, before the reference of the softmax moves
+// From here on a reference's last place is two log2 units and more, and what the
+// fused s inv - m leaves of the rounding of m would be a weight of its own (past
+// f16 from 2^28 on): rows that have such a reference take scores rounded to fp32
+// first, of which m is one.
+constexpr float kFar = 16777216.f;
 
 constexpr uint32_t kOpBytes = kKeys * kHeadDim * 2;            // 32 KB: a Q, K or V operand tile
 constexpr uint32_t kHalfBytes = kOpBytes / 2;                  // its 64-channel (V: 64-key) half: 128 rows of 128 bytes
@@ -292,16 +297,21 @@ __device__ __forceinline__ void load_scores(uint32_t taddr, float (&s)[64])
 }
 
 // 2^(s inv - m) of scores, as f16 pairs; their sum (of the unrounded values) is
-// returned.
-template <int kN>
-__device__ __forceinline__ float weights_of(const float (&s)[kN], uint64_t inv2, float m, uint32_t (&pw)[kN / 2])
+// returned.  kCare: m may be far from 0.
+template <bool kCare, int kN>
+__device__ __forceinline__ float weights_of(const float (&s)[kN], float inv, float m, uint32_t (&pw)[kN / 2])
 {
     const float mbase = m == -INFINITY ? 0.f : m;
-    const uint64_t neg2 = f32x2_pack(-mbase, -mbase);
+    const bool far = kCare && fabsf(mbase) >= kFar;
+    const float pre = far ? inv : 1.f, by = far ? 1.f : inv;     // (a branch for far rows spilled, a product does not)
+    const uint64_t pre2 = f32x2_pack(pre, pre), by2 = f32x2_pack(by, by), neg2 = f32x2_pack(-mbase, -mbase);
     uint64_t acc[4] = {0, 0, 0, 0};
 #pragma unroll
     for (int j = 0; j < kN / 2; ++j) {
-        const uint64_t d = fma_f32x2(f32x2_pack(s[2 * j], s[2 * j + 1]), inv2, neg2);
+        uint64_t x = f32x2_pack(s[2 * j], s[2 * j + 1]);
+        if (kCare)
+            x = mul_f32x2(x, pre2);
+        const uint64_t d = fma_f32x2(x, by2, neg2);
         const float a = fast_exp2(f32x2_lo(d)), b = fast_exp2(f32x2_hi(d));
         acc[j & 3] = add_f32x2(acc[j & 3], f32x2_pack(a, b));
         pw[j] = pack_f16x2(a, b);
@@ -324,7 +334,7 @@ __device__ __forceinline__ uint32_t bit_range(int lo, int hi)
 }
 
 // The weights of 64 scores the long way: masked to the keys lo .. hi - 1 of them,
-// and, where a row has no reference yet or its weights sum to more than kMaxSum,
+// far from 0 too, and, where a row has no reference yet or its weights sum to more than kMaxSum,
 // with the reference raised to the largest score; O (where has_o), once landed()
 // says that the products so far are in it, and l, which are relative to the old
 // one, follow.  A warp together; false when landed() gave up.  kKeep: the scores
@@ -334,7 +344,6 @@ template <bool kKeep, class Landed>
 __device__ __forceinline__ bool weights_with_care(uint32_t scores, uint32_t weights, uint32_t o_cols, bool has_o,
                                                   int lo, int hi, float inv, RowSum &row, Landed landed)
 {
-    const uint64_t inv2 = f32x2_pack(inv, inv);
     const uint32_t seen[2] = {bit_range(lo, hi), bit_range(lo - 32, hi - 32)};
     auto load = [&](float (&s)[64]) {
         load_scores(scores, s);
@@ -355,8 +364,8 @@ __device__ __forceinline__ bool weights_with_care(uint32_t scores, uint32_t weig
             for (int k = 0; k < 8; ++k)
                 pm[k] = fmax3(fmax3(s[8 * k], s[8 * k + 1], s[8 * k + 2]),
                               fmax3(s[8 * k + 3], s[8 * k + 4], s[8 * k + 5]), fmaxf(s[8 * k + 6], s[8 * k + 7]));
-            const float top =
-                fmax3(fmax3(pm[0], pm[1], pm[2]), fmax3(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7])) * inv;
+            const float top = __fmul_rn(
+                fmax3(fmax3(pm[0], pm[1], pm[2]), fmax3(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7])), inv);
             raise = raise && top > -INFINITY;
             const float m_new = raise ? top : row.m;
             const float alpha = raise ? fast_exp2(row.m - m_new) : 1.f;
@@ -383,7 +392,7 @@ __device__ __forceinline__ bool weights_with_care(uint32_t scores, uint32_t weig
         if (!kKeep)
             load(s);
         uint32_t pw[32];
-        const float sum = weights_of(s, inv2, row.m, pw);
+        const float sum = weights_of<true>(s, inv, row.m, pw);
         raise = sum > kMaxSum;
         if (again || !__any_sync(kFullMask, raise)) {
             row.l += sum;
@@ -1147,7 +1156,6 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
             tc_fence_after_sync();
             if (kKeySplit && j == 0)
                 inv = invs[r];
-            const uint64_t inv2 = f32x2_pack(inv, inv);
             const int k0 = (u.tile_lo + u.from + (kKeySplit ? 2 * j + blk : j)) * kKeys;
             const int hi_j = pos + 1 - k0, lo_j = lo - k0;
             // weights of keys 0 .. 63 go over the columns of scores 0 .. 31, of
@@ -1156,12 +1164,12 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
             for (int hf = 0; hf < 2; ++hf) {
                 const uint32_t at = tb + kTmS + 64 * hf, to = tb + kTmS + 32 * hf;
                 const int lo_h = lo_j - 64 * hf, hi_h = hi_j - 64 * hf;
-                bool care = m_used == -INFINITY || lo_h > 0 || hi_h < 64;
+                bool care = !(fabsf(m_used) < kFar) || lo_h > 0 || hi_h < 64;     // (no reference yet: -inf)
                 if (!__any_sync(kFullMask, care)) {
                     float s[64];
                     uint32_t pw[32];
                     load_scores(at, s);
-                    const float sum = weights_of(s, inv2, m_used, pw);
+                    const float sum = weights_of<false>(s, inv, m_used, pw);
                     care = __any_sync(kFullMask, sum > kMaxSum);
                     if (!care) {
                         l += sum;
