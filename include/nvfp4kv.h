@@ -408,8 +408,11 @@ nvfp4kv_status nvfp4kv_extend_attention_fp8_append(const nvfp4kv_cache *cache,
  * Arithmetic: every cached value is exact in fp16, q too (bf16 significands
  * under a power of two a row; elements under 2^-28 of the row's largest lose
  * bits), scores, softmax and outputs in fp32, softmax weights rounded to fp16
- * for the value product.  A scale byte of 0x7F, which the quantiser never
- * writes, reads as 480.  A sequence whose index range is outside [0, q_rows] or
+ * for the value product (each off by 2^-11 of itself, and those more than 14 log2
+ * units behind the row's largest by no more than 2^-10 of the row's sum of weights
+ * altogether, up to 2^23 keys and scores of 2^24 log2 units).
+ * A scale byte of 0x7F, which the quantiser never writes, reads as 480.  A
+ * sequence whose index range is outside [0, q_rows] or
  * longer than max_q_len, or whose length is outside [0, max_pages_per_seq *
  * 16], sets NVFP4KV_DEV_BAD_LEN and its rows are not written. */
 nvfp4kv_status nvfp4kv_paged_extend(const nvfp4kv_cache *cache, const void *q, const int32_t *q_indptr,

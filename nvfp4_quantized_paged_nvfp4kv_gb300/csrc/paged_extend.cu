@@ -23,8 +23,8 @@
 //             holds are neighbours in the operand
 //   S = Q K^T tcgen05.mma M128 N128 K16 x 8, Q in shared memory
 //   softmax   one thread a row, 64 keys at a time: exp2 against a reference
-//             that is the largest score of the first keys seen and is raised
-//             only when the sum of 64 weights passes 2^15 (so that no maximum is
+//             0 to 8 log2 units under the largest score of the first keys seen,
+//             raised only when the sum of 64 weights passes 2^15 (so that no maximum is
 //             taken as a rule), P (f16) back into the columns of S
 //   O += P V  tcgen05.mma M128 N128 K16 x 8, P and O in tensor memory
 // Tiles of 64 keys with Q in tensor memory, which spare the Q reads, ran at half
@@ -39,8 +39,9 @@
 // are not loaded hold cannot reach a row that does not see them.  Q: each row
 // times a power of two that puts its largest element in [2^14, 2^15), which
 // makes bf16 -> f16 exact but for elements under 2^-28 of the row's largest.
-// P is rounded to f16 (relative 2^-11, at most 2^15, its largest at least 1);
-// scores, sums and O are fp32.
+// P is rounded to f16 (at most 2^15, its largest at least 1): relative 2^-11 down to
+// 2^-14, and below by up to 2^-25, which the reference keeps at 2^-10 of the sum of
+// weights over all keys (reference_lift).  Scores, sums and O are fp32.
 //
 // Work split.  A unit is a row tile of one sequence and kv head with all its key
 // tiles.  The units' tiles, heads outermost, form one sequence, a unit counting
@@ -320,6 +321,19 @@ __device__ __forceinline__ float weights_of(const float (&s)[kN], float inv, flo
     return f32x2_lo(a) + f32x2_hi(a);
 }
 
+// How far under the largest score a new reference is, in log2 units, for a piece of
+// so many tiles.  A weight is off by up to 2^-25 as an f16 number, and gone below
+// that: over 2^15 keys as much as 2^-10 of the sum of weights, over 2^20 3%.  One
+// unit a doubling keeps it at 2^-10, up to 2^23 keys (at nine 64 equal weights would
+// be at kMaxSum).  Fewer units leave more room before the reference moves: with eight
+// for every piece a 4,096-token prompt of scores 6 log2 units apart took 307 us, not
+// 165, with one for 2,048 tokens at 32K 1.31 ms, not 1.23.
+__device__ __forceinline__ float reference_lift(int tiles)
+{
+    constexpr int kFree = (1 << 15) / kKeys;
+    return tiles <= kFree ? 0.f : static_cast<float>(min(8, 32 - __clz((tiles - 1) / kFree)));
+}
+
 // What a row's softmax keeps: the reference and the sum of weights relative to it.
 struct RowSum {
     float m, l;
@@ -334,15 +348,16 @@ __device__ __forceinline__ uint32_t bit_range(int lo, int hi)
 }
 
 // The weights of 64 scores the long way: masked to the keys lo .. hi - 1 of them,
-// far from 0 too, and, where a row has no reference yet or its weights sum to more than kMaxSum,
-// with the reference raised to the largest score; O (where has_o), once landed()
-// says that the products so far are in it, and l, which are relative to the old
-// one, follow.  A warp together; false when landed() gave up.  kKeep: the scores
-// stay in registers between the maximum and the weights (row blocks: 0.5% faster;
-// with split keys and their 96 registers they spill, 9% slower).
+// with references far from 0, and, where a row has no reference yet or its weights
+// sum to more than kMaxSum, with the reference raised to `lift` under the
+// largest score; O (where has_o), once landed() says that the products so far are in it,
+// and l, which are relative to the old one, follow.  A warp together; false when
+// landed() gave up.  kKeep: the scores stay in registers between the maximum and
+// the weights (row blocks: 0.5% faster; with split keys and their 96 registers they
+// spill, 9% slower).
 template <bool kKeep, class Landed>
 __device__ __forceinline__ bool weights_with_care(uint32_t scores, uint32_t weights, uint32_t o_cols, bool has_o,
-                                                  int lo, int hi, float inv, RowSum &row, Landed landed)
+                                                  int lo, int hi, float inv, int tiles, RowSum &row, Landed landed)
 {
     const uint32_t seen[2] = {bit_range(lo, hi), bit_range(lo - 32, hi - 32)};
     auto load = [&](float (&s)[64]) {
@@ -367,7 +382,7 @@ __device__ __forceinline__ bool weights_with_care(uint32_t scores, uint32_t weig
             const float top = __fmul_rn(
                 fmax3(fmax3(pm[0], pm[1], pm[2]), fmax3(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7])), inv);
             raise = raise && top > -INFINITY;
-            const float m_new = raise ? top : row.m;
+            const float m_new = raise ? (fabsf(top) < kFar ? top - reference_lift(tiles) : top) : row.m;
             const float alpha = raise ? fast_exp2(row.m - m_new) : 1.f;
             row.m = m_new;
             row.l *= alpha;
@@ -1183,8 +1198,8 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
                     // (S of this one was committed after them), and of this tile's
                     // first half, which may still be under way
                     RowSum sum{m_used, l};
-                    ok = weights_with_care<!kKeySplit>(at, to, tb + kTmO, j > 0 || hf == 1, lo_h, hi_h, inv, sum,
-                                                       [&] { return hf == 0 || wait_warp(S::kHalf + blk, i & 1); });
+                    ok = weights_with_care<!kKeySplit>(at, to, tb + kTmO, j > 0 || hf == 1, lo_h, hi_h, inv, u.n_tiles,
+                                                       sum, [&] { return hf == 0 || wait_warp(S::kHalf + blk, i & 1); });
                     if (!ok)
                         break;
                     m_used = sum.m;

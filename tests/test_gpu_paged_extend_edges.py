@@ -1,5 +1,5 @@
 """Chunk attention over the paged NVFP4 cache at the edges of its range: scores
-far past those of ordinary models.
+far past those of ordinary models, long tails of small weights.
 
 A score is a sum of 128 exact products in fp32 (off by at most 2^-17 of
 sum |q k|) times one factor (2^-24).  Where the largest score of a row is ahead
@@ -12,6 +12,7 @@ import numpy as np
 import pytest
 import torch
 
+import nvfp4_quantized_paged_nvfp4kv_gb300 as nv
 from gpu_util import DEV
 from test_gpu_paged_extend import Case
 
@@ -77,3 +78,62 @@ def test_huge_scores(lens, chunks, hq, hkv, window, power, sm_scale):
     n = sum(check_sharp(out[rows, heads], s, v, 64 + 2.0 ** -15 * 1.4426950408889634 * size)
             for rows, heads, s, v, size in heads_of(c, window, sm_scale))
     assert n > 0 and int(c.status.item()) == 0
+
+
+def run_repeated(c, times, sm_scale=None):
+    """One sequence's call as `times` sequences alike, on the same pages; outputs by
+    sequence.  (Equal units, as many as there are SMs: none is cut.)"""
+    m = c.chunks[0]
+    ptr = torch.arange(times + 1, dtype=torch.int32, device=DEV) * m
+    out = torch.full((times * m, c.hq, 128), 77.0, device=DEV)
+    ws = nv.new_extend_workspace(times * m, m, times, c.hq, c.hkv, c.table.shape[1])
+    nv.nvfp4kv_paged_extend(c.cache, c.q[:m].repeat(times, 1, 1), ptr, c.table_d.repeat(times, 1), c.seq_lens.repeat(times),
+                            out, ws, max_q_len=m, sm_scale=sm_scale, dev_status=c.status)
+    assert int(c.status.item()) == 0
+    return out.view(times, m, c.hq, 128)
+
+
+@pytest.mark.parametrize("chunk", [1, 20])
+@pytest.mark.parametrize("gap", [20.0, 25.3, 27.0])
+@pytest.mark.parametrize("where", ["first", "middle", "last", "none"])
+def test_one_key_ahead_of_a_long_flat_tail(chunk, gap, where):
+    """A key whose value is 0, `gap` log2 units ahead of 131,071 others, all in one
+    run of work: what comes out is the others' share alone.
+
+    Tolerance: weights in f16's subnormal range are off by no more than 2^-10 of
+    the row's sum of weights together, and so the output by 2^-10 of the mean |v|;
+    2^-10 of the sum for the others (2^-11 each, and in the divisor), 2^-15 for the
+    scores (one exact product times a factor), 2^-20 for the sums of O."""
+    n, hq = 131072, 8
+    c = Case((n,), (chunk,), hq, 1, seed=41)
+    g = torch.Generator(device=DEV).manual_seed(42)
+    ahead = {"first": 0, "middle": n // 2, "last": n - chunk, "none": None}[where]
+    k, v = torch.zeros((n, 1, 128), device=DEV), 1 + torch.rand((n, 1, 128), generator=g, device=DEV)
+    if ahead is not None:
+        k[ahead, 0, 0], v[ahead] = 6.0, 0.0
+    s = torch.tensor((c.table[0, np.arange(n) // 16] * 16 + np.arange(n) % 16).astype(np.int32), device=DEV)
+    nv.nvfp4kv_quantize_append(c.cache, k, v, s)
+    c.q[..., 0] = 1.0
+    sm_scale = gap / 6.0 / 1.4426950408889634
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    out = run_repeated(c, sms, sm_scale).double()
+    for _, heads, s, v, _ in heads_of(c, 0, sm_scale):
+        p = torch.softmax(s, -1)
+        want, size = p @ v, p @ v.abs()
+        seen = s > -np.inf
+        mean = seen.double() @ v.abs() / seen.sum(-1, keepdim=True)
+        tol = (2.0 ** -10 + 2.0 ** -15 + 2.0 ** -20) * size + 2.0 ** -10 * mean
+        for b in (0, sms // 2, sms - 1):
+            assert ((out[b, :, heads] - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("times", [1, 152])
+@pytest.mark.parametrize("chunk", [3, 40])
+def test_flat_scores_over_a_long_context(chunk, times):
+    """Queries of zeros: every weight alike, the mean of all values."""
+    c = Case((50000,), (chunk,), 4, 1, seed=43)
+    c.q.zero_()
+    out = run_repeated(c, times).double()
+    for _, heads, s, v, _ in heads_of(c):
+        p = torch.softmax(s, -1)
+        assert ((out[:, :, heads] - p @ v).abs() <= 2.0 ** -10 * (p @ v.abs())).all()
