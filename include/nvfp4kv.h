@@ -410,7 +410,8 @@ nvfp4kv_status nvfp4kv_extend_attention_fp8_append(const nvfp4kv_cache *cache,
  * bits), scores, softmax and outputs in fp32, softmax weights rounded to fp16
  * for the value product (each off by 2^-11 of itself, and those more than 14 log2
  * units behind the row's largest by no more than 2^-10 of the row's sum of weights
- * altogether, up to 2^23 keys and scores of 2^24 log2 units).
+ * altogether, up to 2^23 keys and scores of 2^24 log2 units).  A query with a NaN
+ * or an infinity makes its row NaN if it sees a key; so may scores past fp32's range.
  * A scale byte of 0x7F, which the quantiser never writes, reads as 480.  A
  * sequence whose index range is outside [0, q_rows] or
  * longer than max_q_len, or whose length is outside [0, max_pages_per_seq *

@@ -381,6 +381,10 @@ __device__ __forceinline__ bool weights_with_care(uint32_t scores, uint32_t weig
                               fmax3(s[8 * k + 3], s[8 * k + 4], s[8 * k + 5]), fmaxf(s[8 * k + 6], s[8 * k + 7]));
             const float top = __fmul_rn(
                 fmax3(fmax3(pm[0], pm[1], pm[2]), fmax3(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7])), inv);
+            // (keys, but every score -inf: an infinite query, say; no weights, but not
+            // a row that sees nothing)
+            if (raise && top == -INFINITY && (seen[0] | seen[1]))
+                row.l = NAN;
             raise = raise && top > -INFINITY;
             const float m_new = raise ? (fabsf(top) < kFar ? top - reference_lift(tiles) : top) : row.m;
             const float alpha = raise ? fast_exp2(row.m - m_new) : 1.f;

@@ -1,5 +1,6 @@
 """Chunk attention over the paged NVFP4 cache at the edges of its range: scores
-far past those of ordinary models, long tails of small weights.
+far past those of ordinary models, long tails of small weights, queries that are
+not finite.
 
 A score is a sum of 128 exact products in fp32 (off by at most 2^-17 of
 sum |q k|) times one factor (2^-24).  Where the largest score of a row is ahead
@@ -137,3 +138,68 @@ def test_flat_scores_over_a_long_context(chunk, times):
     for _, heads, s, v, _ in heads_of(c):
         p = torch.softmax(s, -1)
         assert ((out[:, :, heads] - p @ v).abs() <= 2.0 ** -10 * (p @ v.abs())).all()
+
+
+ODD = [float("nan"), float("inf"), -float("inf")]
+
+
+@pytest.mark.parametrize("lens,chunks,hq,hkv,window", [
+    ((1,), (1,), 1, 1, 0),
+    ((40, 9), (40, 9), 8, 2, 0),                 # rows that see one key
+    ((300, 80), (5, 16), 8, 2, 1),               # one key a row, split keys
+    ((300,), (300,), 4, 2, 1),                   # one key a row, row blocks
+    ((5000,), (16,), 8, 2, 0),                   # split keys, cut
+    ((6000,), (200,), 2, 1, 0),                  # row blocks, cut
+    ((4000, 3000), (200, 260), 2, 1, 900),       # row blocks, cut, a window that leaves pieces without keys
+])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_queries_that_are_not_finite(lens, chunks, hq, hkv, window, dtype):
+    """A NaN or an infinity anywhere in a query makes its row NaN, also where all
+    its scores are minus infinity; every other row keeps its bits."""
+    c = Case(lens, chunks, hq, hkv, seed=31)
+    clean = c.run(window=window, dtype=dtype).clone()
+    n, hit = sum(c.chunks), torch.zeros((c.rows, hq), dtype=torch.bool, device=DEV)
+    kp, _ = c.planes()
+    at = 0
+    for b, (length, m) in enumerate(zip(lens, chunks)):
+        for t in range(0, m, 1 if m <= 16 else 7):
+            i = (5 * t + 3 * b) % hq
+            pos = length - m + t
+            k = kp[c.table[b, pos // 16], i // (hq // hkv), pos % 16]            # the row's last key
+            ch = int(np.abs(k).argmax())
+            odd = ODD[t % 3]
+            if t % 2 and odd != odd:
+                odd = ODD[2]
+            # (an infinity: of the sign that sends the score of that key to minus infinity)
+            c.q[at + t, i, ch] = -float("inf") * float(np.sign(k[ch])) if odd == -float("inf") else odd
+            hit[at + t, i] = True
+        at += m
+    assert hit.any()
+    out = c.run(window=window, dtype=dtype)
+    assert out[hit].isnan().all()
+    assert torch.equal(out[~hit], clean[~hit])
+    assert (out[n:] == 77).all() and int(c.status.item()) == 0
+
+
+def test_query_that_is_not_finite_and_sees_no_key():
+    """Rows before position 0 stay zeros whatever they hold."""
+    c = Case((5, 0, 70), (9, 3, 10), 4, 2, seed=32)
+    c.q[0, 1, 5], c.q[3, 0, 7], c.q[10, 2, 0], c.q[8, 3, 1] = float("nan"), float("inf"), -float("inf"), float("nan")
+    out = c.run()
+    assert (out[:4] == 0).all() and (out[9:12] == 0).all()
+    assert out[8, 3].isnan().all() and not out[8, :3].isnan().any() and not out[12:].isnan().any()
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("lens,chunks", [((1,), (1,)), ((6000,), (3,)), ((6000,), (140,))])
+def test_scores_past_the_range_of_fp32(sign, lens, chunks):
+    """All scores of a row past fp32's largest, on either side: NaN, never the
+    zeros of a row that sees nothing."""
+    c = Case(lens, chunks, 2, 1, seed=33)
+    n = lens[0]
+    k = torch.ones((n, 1, 128), device=DEV)
+    s = torch.tensor((c.table[0, np.arange(n) // 16] * 16 + np.arange(n) % 16).astype(np.int32), device=DEV)
+    nv.nvfp4kv_quantize_append(c.cache, k, k, s)
+    c.q.fill_(sign * 2.0 ** 127)
+    out = c.run(sm_scale=1.0)
+    assert out[:sum(chunks)].isnan().all()
