@@ -44,7 +44,9 @@ constexpr int kSoftmaxThreads = 128;          // warps 0-3
 constexpr int kProducerThreads = 128;         // warps 4-7
 constexpr int kMmaWarp = 8;
 constexpr int kTcThreads = kSoftmaxThreads + kProducerThreads + 32;
-constexpr float kRescaleLog2 = 8.f;           // raise the running maximum only past this margin
+// Raise the running maximum only past this margin (of the difference: where eight is
+// half of fp32's last place, maximum + 8 may round to the score itself, sixteen up).
+constexpr float kRescaleLog2 = 8.f;
 
 constexpr uint32_t kQBytes = kTcRows * kHeadDim * 2;   // 32 KB
 constexpr uint32_t kKVBytes = kTcKeys * kHeadDim * 2;  // 16 KB per K or V tile
@@ -599,7 +601,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) extend_tc_kernel(const __grid_c
                 pm[k] = fmax3(fmax3(s[8 * k], s[8 * k + 1], s[8 * k + 2]), fmax3(s[8 * k + 3], s[8 * k + 4], s[8 * k + 5]),
                               fmaxf(s[8 * k + 6], s[8 * k + 7]));
             const float mx = fmax3(fmax3(pm[0], pm[1], pm[2]), fmax3(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7]));
-            const bool need = mx > m_used + kRescaleLog2;
+            const bool need = mx - m_used > kRescaleLog2;     // (none of -inf - -inf)
             const float m_new = need ? mx : m_used;
             const float mbase = m_new == -INFINITY ? 0.f : m_new;
             const float alpha = need ? fast_exp2(m_used - mbase) : 1.f;
@@ -730,6 +732,13 @@ constexpr uint32_t kF8Smem = kF8OffFail + 4 + 1024;
 static_assert(kF8OffRowInv % 16 == 0, "row scale table alignment");
 static_assert(kF8OffK % 1024 == 0 && kF8OffV % 1024 == 0 && kF8OffVraw % 1024 == 0, "swizzle atoms");
 static_assert(2 * (kF8Smem + 1024) <= 228 * 1024, "two CTAs per SM");
+
+// A row whose S is multiplied by this or more may have scores past 2^24 log2 units
+// (S is at most 128 x 256 x 448): the product left unrounded beside a rounded maximum
+// is off by half of its last place, past f16 from 2^28 on, so such rows round it
+// first.  (2,048 bf16 tokens behind 162K: 7.61 ms, 7.48 without it; found from each
+// tile's maximum instead 7.68, in a loop or a function of their own 7.58 and 7.75.)
+constexpr float kBigInv = 1.f;
 
 // Two fp32 -> E4M3 bytes and back to fp32, exactly (the decode is exact).
 __device__ __forceinline__ float2 e4m3x2_value(uint32_t two)
@@ -1165,6 +1174,7 @@ __global__ void __launch_bounds__(kF8Threads, 2) extend_f8_kernel(const __grid_c
         const int t = min(row, R - 1) / g;
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp * 32) << 16);
         const float inv_row = rowinv[r];
+        const bool any_big_row = __any_sync(kFullMask, inv_row >= kBigInv);
         float m_used = -INFINITY, l = 0.f;
         bool ok = true;
         auto wait_warp = [&](uint32_t bar_addr, uint32_t parity) {
@@ -1175,14 +1185,15 @@ __global__ void __launch_bounds__(kF8Threads, 2) extend_f8_kernel(const __grid_c
             if (!(ok = wait_warp(B(kF8SFull + b), (i >> 1) & 1)))
                 break;
             float inv = inv_row;
+            bool any_big = any_big_row;
             if (kChunkBf16 && i >= c.n_pre) {
                 // the chunk tile's key scale 2^-f, published with its terms
                 const int cc = i - c.n_pre;
                 if (!(ok = wait_warp(B(kF8KScale + cc % kF8KScaleRing), (cc / kF8KScaleRing) & 1)))
                     break;
                 inv *= reinterpret_cast<const volatile float *>(gbase + kF8OffKScale)[cc % kF8KScaleRing];
+                any_big = __any_sync(kFullMask, inv >= kBigInv);
             }
-            const uint64_t inv2 = f32x2_pack(inv, inv);
             tc_fence_after_sync();
             uint32_t sr0[32], sr1[32];
             tmem_ld32(lane_base + kColS + b * kTcKeys, sr0);
@@ -1195,23 +1206,26 @@ __global__ void __launch_bounds__(kF8Threads, 2) extend_f8_kernel(const __grid_c
                 s[j + 32] = __uint_as_float(sr1[j]);
             }
             const int lim = i < c.n_pre ? c.P - i * kTcKeys : t + 1 - (i - c.n_pre) * kTcKeys;
-            if (lim < kTcKeys) {
+            if (lim < kTcKeys || any_big) {
+                const float pre = inv >= kBigInv ? inv : 1.f;
 #pragma unroll
                 for (int j = 0; j < 64; ++j)
-                    if (j >= lim)
-                        s[j] = -INFINITY;
+                    s[j] = j >= lim ? -INFINITY : __fmul_rn(s[j], pre);
+                inv = inv >= kBigInv ? 1.f : inv;
             }
             float pm[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k)
                 pm[k] = fmax3(fmax3(s[8 * k], s[8 * k + 1], s[8 * k + 2]), fmax3(s[8 * k + 3], s[8 * k + 4], s[8 * k + 5]),
                               fmaxf(s[8 * k + 6], s[8 * k + 7]));
-            const float mx = fmax3(fmax3(pm[0], pm[1], pm[2]), fmax3(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7])) * inv;
-            const bool need = mx > m_used + kRescaleLog2;
+            const float mx = __fmul_rn(
+                fmax3(fmax3(pm[0], pm[1], pm[2]), fmax3(pm[3], pm[4], pm[5]), fmaxf(pm[6], pm[7])), inv);
+            const bool need = mx - m_used > kRescaleLog2;     // (none of -inf - -inf)
             const float m_new = need ? mx : m_used;
             const float mbase = m_new == -INFINITY ? 0.f : m_new;
             const float alpha = need ? fast_exp2(m_used - mbase) : 1.f;
             const uint64_t neg2 = f32x2_pack(-mbase, -mbase);
+            const uint64_t inv2 = f32x2_pack(inv, inv);
             uint64_t acc[4] = {0, 0, 0, 0};
 #pragma unroll
             for (int j = 0; j < 32; ++j) {

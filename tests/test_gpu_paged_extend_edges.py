@@ -41,15 +41,15 @@ def heads_of(c, window=0, sm_scale=None):
         r += m
 
 
-def check_sharp(out, s, v, ahead_by):
-    """Rows out [rows][heads][128] against scores s and values v; ahead_by
-    [rows][heads]: log2 units that make the first key the only one.  Returns how
-    many rows had one key that far ahead."""
+def check_sharp(out, s, v, ahead_by, v_step=0.0):
+    """Rows out [rows][heads][128] against scores s and values v (v_step: what a
+    value may be off by); ahead_by [rows][heads]: log2 units that make the first key
+    the only one.  Returns how many rows had one key that far ahead."""
     out = out.double()
     two = torch.cat([s, torch.full_like(s[..., :1], -np.inf)], -1).topk(2, -1)
     sure = (two.values[..., 0] - two.values[..., 1]) * 1.4426950408889634 > ahead_by
     want = v[two.indices[..., 0]]
-    assert ((out - want).abs() <= 2.0 ** -10 * want.abs())[sure].all()
+    assert ((out - want).abs() <= 2.0 ** -10 * want.abs() + v_step)[sure].all()
     hi, lo = torch.empty_like(out), torch.empty_like(out)
     for i, j in np.ndindex(*s.shape[:2]):
         seen = v[s[i, j] > -np.inf]
