@@ -1,6 +1,6 @@
 """Chunk attention over the paged NVFP4 cache at the edges of its range: scores
 far past those of ordinary models, long tails of small weights, queries that are
-not finite.
+not finite, row tiles in more pieces than the join takes at once.
 
 A score is a sum of 128 exact products in fp32 (off by at most 2^-17 of
 sum |q k|) times one factor (2^-24).  Where the largest score of a row is ahead
@@ -15,7 +15,7 @@ import torch
 
 import nvfp4_quantized_paged_nvfp4kv_gb300 as nv
 from gpu_util import DEV
-from test_gpu_paged_extend import Case
+from test_gpu_paged_extend import Case, check
 
 pytestmark = pytest.mark.gpu
 
@@ -203,3 +203,22 @@ def test_scores_past_the_range_of_fp32(sign, lens, chunks):
     c.q.fill_(sign * 2.0 ** 127)
     out = c.run(sm_scale=1.0)
     assert out[:sum(chunks)].isnan().all()
+
+
+@pytest.mark.parametrize("ramp", [12.0, -12.0, 40.0, -40.0, 0.0])
+@pytest.mark.parametrize("chunk,hq", [(3, 1), (200, 1), (90, 3)])
+def test_a_unit_in_many_pieces(ramp, chunk, hq):
+    """One row tile over 40,000 keys is cut into some hundred pieces, so the join
+    takes several rounds of 32.  Scores rise or fall by `ramp` log2 units along the
+    context: the largest score moves from round to round, or stays behind."""
+    n = 40000
+    c = Case((n,), (chunk,), hq, 1, seed=51)
+    g = torch.Generator(device=DEV).manual_seed(52)
+    k, v = (torch.randn((n, 1, 128), generator=g, device=DEV) for _ in range(2))
+    k[:, 0, :16] = torch.linspace(0, 1, n, device=DEV)[:, None]
+    s = torch.tensor((c.table[0, np.arange(n) // 16] * 16 + np.arange(n) % 16).astype(np.int32), device=DEV)
+    nv.nvfp4kv_quantize_append(c.cache, k, v, s)
+    c.q[..., :16] = ramp / 16 / 1.4426950408889634 * 128 ** 0.5
+    ws = c.workspace()
+    assert ws.numel() > 64 * 2 * 128 * 130 * 4                   # pieces of more than 64 CTAs
+    check(c.run(ws=ws), c, c.want(), torch.float32)
