@@ -313,6 +313,20 @@ def _token_rows(dev, t, name, dtype, shape) -> int:
     return step if shape[0] > 1 else shape[1] * shape[2]
 
 
+def _int32(x, name) -> int:
+    """An integer argument of the library's 32-bit parameters (ctypes would cut
+    a larger one to its low bits)."""
+    x = int(x)
+    if not -2 ** 31 <= x < 2 ** 31:
+        raise ValueError(f"{name}: {x} does not fit 32 bits")
+    return x
+
+
+def _window(x) -> int:
+    """A sliding window; one past 32 bits is longer than any sequence."""
+    return _int32(min(int(x), 2 ** 31 - 1), "window")
+
+
 # --- entry points -------------------------------------------------------------
 
 def nvfp4kv_quantize_append(cache: NVFP4Cache, k_new, v_new, slot_mapping, dev_status=None,
@@ -482,8 +496,10 @@ def nvfp4kv_extend_attention_fp8_append(cache: NVFP4Cache, slot_mapping, q, q_in
 
 def nvfp4kv_paged_extend_workspace_size(q_rows, max_q_len, batch, num_q_heads, num_kv_heads, max_pages_per_seq,
                                         window=0) -> int:
-    return int(load().nvfp4kv_paged_extend_workspace_size(q_rows, max_q_len, batch, num_q_heads, num_kv_heads,
-                                                          max_pages_per_seq, window))
+    return int(load().nvfp4kv_paged_extend_workspace_size(
+        _int32(q_rows, "q_rows"), _int32(max_q_len, "max_q_len"), _int32(batch, "batch"),
+        _int32(num_q_heads, "num_q_heads"), _int32(num_kv_heads, "num_kv_heads"),
+        _int32(max_pages_per_seq, "max_pages_per_seq"), _window(window)))
 
 
 def nvfp4kv_paged_extend(cache: NVFP4Cache, q, q_indptr, block_table, seq_lens, out, workspace, max_q_len=None, window=0,
@@ -510,8 +526,8 @@ def nvfp4kv_paged_extend(cache: NVFP4Cache, q, q_indptr, block_table, seq_lens, 
     if max_q_len is None:
         max_q_len = int((q_indptr[1:] - q_indptr[:-1]).max().item()) if B > 0 else 0
     st = load().nvfp4kv_paged_extend(
-        cache.c, _ptr(q), _ptr(q_indptr), rows, int(max_q_len), B, Hq, _ptr(block_table), pages, _ptr(seq_lens),
-        int(window), float(sm_scale), _ptr(out), _dtype_code(out), _ptr(workspace),
+        cache.c, _ptr(q), _ptr(q_indptr), rows, _int32(max_q_len, "max_q_len"), B, Hq, _ptr(block_table), pages,
+        _ptr(seq_lens), _window(window), float(sm_scale), _ptr(out), _dtype_code(out), _ptr(workspace),
         0 if workspace is None else workspace.numel(), _ptr(dev_status), _stream(stream, dev))
     _check(st, "nvfp4kv_paged_extend")
 
@@ -533,7 +549,8 @@ def nvfp4kv_plan_step(context_lens, new_lens, block_table, num_pages, free_pages
              (slot_mapping, "slot_mapping", (T,)), (positions, "positions", (T,)), (kv_indptr, "kv_indptr", (B,)),
              (dev_status, "dev_status", (1,)))
     st = load().nvfp4kv_plan_step(
-        _ptr(context_lens), _ptr(new_lens), B, _ptr(block_table), pages, int(num_pages), _ptr(free_pages), F,
+        _ptr(context_lens), _ptr(new_lens), B, _ptr(block_table), pages, _int32(num_pages, "num_pages"),
+        _ptr(free_pages), F,
         _ptr(num_free), _ptr(num_free_out), _ptr(seq_lens), _ptr(q_indptr), _ptr(kv_indptr), _ptr(slot_mapping),
         _ptr(positions), T, _ptr(dev_status), _stream(stream, dev))
     _check(st, "nvfp4kv_plan_step")
@@ -552,7 +569,8 @@ def nvfp4kv_release_pages(old_lens, keep_lens, block_table, num_pages, free_page
              (block_table, "block_table", (B, pages)), (free_pages, "free_pages", (F,)), (num_free, "num_free", (1,)),
              (num_free_out, "num_free_out", (1,)), (dev_status, "dev_status", (1,)))
     st = load().nvfp4kv_release_pages(
-        _ptr(old_lens), _ptr(keep_lens), B, _ptr(block_table), pages, int(num_pages), _ptr(free_pages), F,
+        _ptr(old_lens), _ptr(keep_lens), B, _ptr(block_table), pages, _int32(num_pages, "num_pages"),
+        _ptr(free_pages), F,
         _ptr(num_free), _ptr(num_free_out), _ptr(dev_status), _stream(stream, dev))
     _check(st, "nvfp4kv_release_pages")
 

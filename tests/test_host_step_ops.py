@@ -179,3 +179,17 @@ def test_paged_extend_nothing_to_do_and_sizes():
     assert extend(rows=0, **none) == nv.OK
     size = nv.load().nvfp4kv_paged_extend_workspace_size
     assert size(-1, 1, 1, 8, 2, 4, 0) == size(1, 1, 1, 7, 2, 4, 0) == 0     # sizes that the call refuses
+
+
+def test_sizes_past_32_bits():
+    """A window that no sequence reaches is no window; other sizes are refused, not
+    cut to their low 32 bits."""
+    size = nv.nvfp4kv_paged_extend_workspace_size
+    args = (4096, 4096, 4, 8, 8, 4096)
+    for window in (2 ** 31, 2 ** 32 + 1, 2 ** 63 - 1):
+        assert size(*args, window) == size(*args, 0)
+    for i in range(6):
+        with pytest.raises(ValueError, match="32 bits"):
+            size(*(2 ** 32 + x if k == i else x for k, x in enumerate(args)))
+    with pytest.raises(ValueError, match="32 bits"):
+        size(*args, -2 ** 32 + 1)
