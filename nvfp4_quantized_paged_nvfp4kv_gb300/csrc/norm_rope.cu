@@ -11,8 +11,8 @@
 // Angles.  n * f_i in fp32 is off by |angle| 2^-24: 0.06 radians at a position
 // of a million.  f_i / 2 pi is kept as a 64-bit binary fraction of a turn
 // instead, and n times it, modulo 2^64 as integers multiply, is the fraction
-// of a turn exactly (up to n 2^-65); cos and sin are taken of its signed top
-// 32 bits.
+// of a turn to n 2^-63 (f_i / 2 pi is cut to 64 bits in two parts); cos and sin
+// are taken of its signed top 32 bits.
 //
 // Work split.  A row is eight lanes, lane l with channels 8l .. 8l + 7 and 64 +
 // 8l .. 64 + 8l + 7, so that eight lanes load or store 128 bytes on end (16
