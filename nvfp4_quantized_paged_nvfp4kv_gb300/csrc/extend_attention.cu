@@ -822,9 +822,10 @@ __global__ void __launch_bounds__(kF8Threads, 2) extend_f8_kernel(const __grid_c
         int e = 0;
         if (am >= 1e-30f)
             e = 7 - (static_cast<int>((__float_as_uint(am) >> 23) & 0xffu) - 127);
-        const float sc = __uint_as_float(static_cast<uint32_t>(127 + e) << 23);
+        // (a negative scale's sign goes to Q, so that the largest S is the largest score)
+        const float sc = copysignf(__uint_as_float(static_cast<uint32_t>(127 + e) << 23), p.qscale);
         if (piece == 0)
-            rowinv[r] = __uint_as_float(static_cast<uint32_t>(127 - e) << 23) * p.qscale;
+            rowinv[r] = __uint_as_float(static_cast<uint32_t>(127 - e) << 23) * fabsf(p.qscale);
         uint32_t term[kF8QTerms][2];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {

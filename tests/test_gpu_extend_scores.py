@@ -81,3 +81,22 @@ def test_a_step_of_sixteen_at_2_to_27():
     room = {150: (2.0 ** -16 + 256 * 2.0 ** -32) * top + 2.0 ** -25, 5: 149 * 2.0 ** -16 * top + 2.0 ** -25}
     for rows, key in ((slice(150, 256), 150), (slice(5, 150), 5)):
         assert ((out[rows].double() - v[key]).abs() <= 2.0 ** -10 * v[key].abs() + room[key]).all()
+
+
+@pytest.mark.parametrize("prefix,chunks,chunk", [
+    ((3000, 0), (60, 70), "bf16"),
+    ((300, 0, 65), (130, 1, 64), "e4m3"),
+    ((70, 0), (200, 300), "bf16"),               # the f16 kernel
+])
+def test_negative_scale(prefix, chunks, chunk):
+    """Scores fall as q k rises: the same as queries of the other sign."""
+    e = workloads.extend_custom(prefix, chunks, 8, 2, seed=17)
+    x = to_dev(workloads.extend_inputs(e, chunk=chunk))
+    x["q"] = (x["q"].float() * 8).to(torch.bfloat16)
+    outs = []
+    for sign in (1, -1):
+        outs.append(torch.empty((e.q_rows, 8, 128), device=DEV))
+        nv.nvfp4kv_extend_attention_fp8(x["q"] * sign, x["q_indptr"], x["k_prefix"], x["v_prefix"], x["kv_indptr"],
+                                        x["prefix_lens"], x["k_chunk"], x["v_chunk"], outs[-1], max_q_len=max(chunks),
+                                        sm_scale=0.088 * sign)
+    assert torch.equal(*outs)
