@@ -736,7 +736,7 @@ static_assert(2 * (kF8Smem + 1024) <= 228 * 1024, "two CTAs per SM");
 // A row whose S is multiplied by this or more may have scores past 2^24 log2 units
 // (S is at most 128 x 256 x 448): the product left unrounded beside a rounded maximum
 // is off by half of its last place, past f16 from 2^28 on, so such rows round it
-// first.  (2,048 bf16 tokens behind 162K: 7.61 ms, 7.48 without it; found from each
+// first.  (2,048 bf16 tokens behind 162K: 7.57 ms, 7.48 without it; found from each
 // tile's maximum instead 7.68, in a loop or a function of their own 7.58 and 7.75.)
 constexpr float kBigInv = 1.f;
 
@@ -1175,7 +1175,7 @@ __global__ void __launch_bounds__(kF8Threads, 2) extend_f8_kernel(const __grid_c
         const int t = min(row, R - 1) / g;
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(warp * 32) << 16);
         const float inv_row = rowinv[r];
-        const bool any_big_row = __any_sync(kFullMask, inv_row >= kBigInv);
+        const float inv_most = __uint_as_float(__reduce_max_sync(kFullMask, __float_as_uint(inv_row)));    // of the warp
         float m_used = -INFINITY, l = 0.f;
         bool ok = true;
         auto wait_warp = [&](uint32_t bar_addr, uint32_t parity) {
@@ -1186,14 +1186,15 @@ __global__ void __launch_bounds__(kF8Threads, 2) extend_f8_kernel(const __grid_c
             if (!(ok = wait_warp(B(kF8SFull + b), (i >> 1) & 1)))
                 break;
             float inv = inv_row;
-            bool any_big = any_big_row;
+            float most = inv_most;
             if (kChunkBf16 && i >= c.n_pre) {
                 // the chunk tile's key scale 2^-f, published with its terms
                 const int cc = i - c.n_pre;
                 if (!(ok = wait_warp(B(kF8KScale + cc % kF8KScaleRing), (cc / kF8KScaleRing) & 1)))
                     break;
-                inv *= reinterpret_cast<const volatile float *>(gbase + kF8OffKScale)[cc % kF8KScaleRing];
-                any_big = __any_sync(kFullMask, inv >= kBigInv);
+                const float k_scale = reinterpret_cast<const volatile float *>(gbase + kF8OffKScale)[cc % kF8KScaleRing];
+                inv *= k_scale;
+                most *= k_scale;
             }
             tc_fence_after_sync();
             uint32_t sr0[32], sr1[32];
@@ -1207,11 +1208,14 @@ __global__ void __launch_bounds__(kF8Threads, 2) extend_f8_kernel(const __grid_c
                 s[j + 32] = __uint_as_float(sr1[j]);
             }
             const int lim = i < c.n_pre ? c.P - i * kTcKeys : t + 1 - (i - c.n_pre) * kTcKeys;
-            if (lim < kTcKeys || any_big) {
+            if (lim < kTcKeys || most >= kBigInv) {
                 const float pre = inv >= kBigInv ? inv : 1.f;
 #pragma unroll
-                for (int j = 0; j < 64; ++j)
-                    s[j] = j >= lim ? -INFINITY : __fmul_rn(s[j], pre);
+                for (int j = 0; j < 64; j += 2) {
+                    const uint64_t x = mul_f32x2(f32x2_pack(s[j], s[j + 1]), f32x2_pack(pre, pre));
+                    s[j] = j >= lim ? -INFINITY : f32x2_lo(x);
+                    s[j + 1] = j + 1 >= lim ? -INFINITY : f32x2_hi(x);
+                }
                 inv = inv >= kBigInv ? 1.f : inv;
             }
             float pm[8];
