@@ -33,7 +33,7 @@
 // across its tokens.
 //
 // Bound.  8,192 bf16 tokens of 48 + 8 heads out of a fused projection's rows:
-// 235 MB in 43 us, 5.5 TB/s, 82% of a copy's rate, with 58% of the issue slots
+// 235 MB in 43 us, 5.5 TB/s, 82% of a copy's rate, with 56% of the issue slots
 // taken.  With the cache write, 244 MB in 43 us.
 #include "nvfp4kv.h"
 #include "record_write.cuh"

@@ -39,9 +39,10 @@
 // are not loaded hold cannot reach a row that does not see them.  Q: each row
 // times a power of two that puts its largest element in [2^14, 2^15), which
 // makes bf16 -> f16 exact but for elements under 2^-28 of the row's largest.
-// P is rounded to f16 (at most 2^15, its largest at least 1): relative 2^-11 down to
-// 2^-14, and below by up to 2^-25, which the reference keeps at 2^-10 of the sum of
-// weights over all keys (reference_lift).  Scores, sums and O are fp32.
+// P is rounded to f16, the type of V beside it (bf16 would hold V too, with P three
+// bits coarser); at most 2^15, its largest at least 1: relative 2^-11 down to 2^-14,
+// and below by up to 2^-25, which the reference keeps at 2^-10 of the sum of weights
+// over all keys (reference_lift).  Scores, sums and O are fp32.
 //
 // Work split.  A unit is a row tile of one sequence and kv head with all its key
 // tiles.  The units' tiles, heads outermost, form one sequence, a unit counting
