@@ -68,6 +68,11 @@
  *                 f(p) = (p mod 2) + 4 * (floor(p / 2) mod 2), holds channels
  *                 8c .. 8c + 7, byte 2i + w being channel 8c + i of token 2p + w.
  *
+ * Block-scaled FP8 record, R = FP8BKV_RECORD_BYTES = 4128: the FP8 record, with
+ *   codes relative to a scale, and behind it the scales of its page-head, fp32
+ *   powers of two:
+ *   [4096, 4100)  K scale; [4100, 4104) V scale; [4104, 4128) not used.
+ *
  * Supported geometry: head_dim 128, page_size 16, num_q_heads a multiple of
  * num_kv_heads with group g = num_q_heads / num_kv_heads in 1..8,
  * global_scale a positive normal finite fp32.  Anything else returns
@@ -114,6 +119,7 @@ typedef enum { NVFP4KV_F32 = 0, NVFP4KV_BF16 = 1, NVFP4KV_E4M3 = 2 } nvfp4kv_dty
 
 #define NVFP4KV_RECORD_BYTES 2304
 #define FP8KV_RECORD_BYTES 4096
+#define FP8BKV_RECORD_BYTES 4128
 
 /* NVFP4 cache: pool of num_pages * num_kv_heads records laid out as above,
  * 16-byte aligned; global_scale is the tensor scale G described above.
@@ -146,6 +152,26 @@ typedef struct {
     int32_t page_size;
     int32_t head_dim;
 } fp8kv_cache;
+
+/* FP8-E4M3 cache with a scale for each page and kv head: pool of records as
+ * above, 16-byte aligned. */
+typedef struct {
+    void *pool;
+    int32_t num_pages;
+    int32_t num_kv_heads;
+    int32_t page_size;
+    int32_t head_dim;
+} fp8bkv_cache;
+
+/* Bounds of the keys of each page and kv head (see nvfp4kv_page_bounds):
+ * bounds int8 [num_pages][num_kv_heads][2][128], 16-byte aligned, and steps fp32
+ * [num_pages][num_kv_heads].  They belong to one cache: its page ids, its heads. */
+typedef struct {
+    int8_t *bounds;
+    float *steps;
+    int32_t num_pages;
+    int32_t num_kv_heads;
+} nvfp4kv_bounds;
 
 /* Write side ("SGLang stores KV cache in 4 bits", Interpretation ¶2: prefill
  * quantises the new K/V into the NVFP4 cache).
@@ -588,6 +614,164 @@ nvfp4kv_status fp8kv_append_paged_decode(const fp8kv_cache *cache, const void *k
                                          void *out, nvfp4kv_dtype out_dtype, void *workspace,
                                          size_t workspace_bytes, int32_t num_workers, int32_t *dev_status,
                                          nvfp4kv_stream_t stream);
+
+/* ---- An FP8 cache with a scale for each page and kv head -----------------------
+ *
+ * The pages compare with an FP8 cache at scale 1.0 ("NVFP4-KV-Cache auf der
+ * ...", "Bytes pro Token": uncalibrated), which saturates at 448 and loses small
+ * values.  Here each page of a kv head has its own scale for K and for V (this
+ * library's choice; the pages name calibration as the next step), found as
+ * the tokens are written: with amax the largest magnitude of the block's new
+ * values,
+ *   s = 2^e, e the least integer with amax <= 448 * 2^e, from -100 to 100,
+ *   code = E4M3_rn_satfinite(x / s)   (x / s is exact).
+ * A page that holds tokens already keeps its scale unless new tokens need a
+ * larger one; then the codes that are there are rounded anew,
+ * E4M3_rn(code * s_old / s), which is exact but for codes that become subnormal.
+ * A page whose first token comes with the call starts from that call's tokens.
+ */
+
+/* Write the last C = q_indptr[b+1] - q_indptr[b] tokens of sequence b's
+ * seq_lens[b] tokens (a library utility: the write side of this cache; the
+ * arguments are those of nvfp4kv_paged_extend, so that nvfp4kv_plan_step's
+ * outputs fit).  Sequence b's rows are q_indptr[b] .. q_indptr[b+1] - 1 of
+ *   k_new, v_new  [num_tokens][num_kv_heads][128], fp32 or bf16, 16-byte aligned
+ * and go to positions seq_lens[b] - C .. seq_lens[b] - 1, in the pages that the
+ * block table (int32 [batch][max_pages_per_seq]) lists.  Rows outside every
+ * range are not read.  Positions of the last page behind the sequence hold
+ * unspecified codes afterwards.  A page that receives tokens must not be in
+ * another sequence's table.
+ * A sequence whose range is outside [0, num_tokens], or whose length is less
+ * than C or more than max_pages_per_seq * 16, is not written and sets
+ * NVFP4KV_DEV_BAD_LEN; a page id outside [0, num_pages) is skipped and sets
+ * NVFP4KV_DEV_BAD_PAGE.  q_indptr must not fall from one sequence to the next.
+ * batch at most NVFP4KV_MAX_BATCH.  Non-finite inputs give unspecified codes. */
+nvfp4kv_status fp8bkv_append(const fp8bkv_cache *cache, const void *k_new, const void *v_new, nvfp4kv_dtype in_dtype,
+                             int32_t num_tokens, const int32_t *q_indptr, int32_t batch, const int32_t *block_table,
+                             int32_t max_pages_per_seq, const int32_t *seq_lens, int32_t *dev_status,
+                             nvfp4kv_stream_t stream);
+
+/* Read cached rows back (a library utility): for j < lens[b]
+ *   k_out[kv_indptr[b] + j][h][c] = code * scale, rounded to out_dtype
+ * (fp32 and bf16 hold it exactly, but for values past their range; NVFP4KV_E4M3
+ * rounds and saturates: the FP8 workspace that the extend calls take), v_out the
+ * same; each [rows][num_kv_heads][128], 16-byte aligned, sized by the caller.
+ * Lengths and page ids are checked as in nvfp4kv_paged_decode.  batch at most
+ * NVFP4KV_MAX_BATCH. */
+nvfp4kv_status fp8bkv_dequant(const fp8bkv_cache *cache, const int32_t *block_table, int32_t max_pages_per_seq,
+                              const int32_t *lens, const int32_t *kv_indptr, int32_t batch, void *k_out, void *v_out,
+                              nvfp4kv_dtype out_dtype, int32_t *dev_status, nvfp4kv_stream_t stream);
+
+/* Decode attention over the block-scaled cache (a library utility with no
+ * counterpart on the pages): q_len query tokens per sequence (1 ..
+ * NVFP4KV_MAX_QUERY_TOKENS), causal among themselves, as in
+ * nvfp4kv_paged_decode_multi.  Arguments, checks and results as there.
+ * Arithmetic: codes are exact in fp16, q too (bf16 significands under a power of
+ * two a row; elements under 2^-28 of the row's largest lose bits); sm_scale and
+ * a page's scales are applied in fp32, where scores, softmax and outputs are held;
+ * softmax weights are rounded to fp16 for the value product. */
+nvfp4kv_status fp8bkv_paged_decode(const fp8bkv_cache *cache, const void *q, int32_t batch, int32_t q_len,
+                                   int32_t num_q_heads, const int32_t *block_table, int32_t max_pages_per_seq,
+                                   const int32_t *seq_lens, float sm_scale, void *out, nvfp4kv_dtype out_dtype,
+                                   void *workspace, size_t workspace_bytes, int32_t num_workers, int32_t *dev_status,
+                                   nvfp4kv_stream_t stream);
+
+/* Bytes of a block-scaled FP8 pool; -1 for invalid arguments (a library utility;
+ * host only).  Only the supported geometry has one. */
+int64_t fp8bkv_cache_bytes(int32_t num_pages, int32_t num_kv_heads, int32_t page_size, int32_t head_dim);
+
+/* ---- Attention over the pages that a query selects ------------------------------
+ *
+ * The pages read the whole cache at every step; these calls (with no counterpart
+ * there) read, for each query token and kv head, the pages that a cheap score
+ * puts first.  Three steps: bounds of the pages' keys, kept up as tokens are
+ * written; the selection; decode over the selected pages.
+ *
+ * Bounds of a page and kv head over the page's cached tokens (values as cached,
+ * without the tensor scale G): u = max |k|, r = fl32(127 / u),
+ *   bounds[..][1][c] = min(127, ceil(fl32(max_t k[t][c] * r)))
+ *   bounds[..][0][c] = max(-127, floor(fl32(min_t k[t][c] * r)))
+ *   steps[..] = fl32(u / 127);   u = 0: all of them 0.
+ */
+
+/* Brings the bounds of sequence b's pages floor(from_lens[b] / 16) ..
+ * ceil(seq_lens[b] / 16) - 1 up to date (a library utility): those that tokens
+ * from_lens[b] .. seq_lens[b] - 1 were written into.  from_lens NULL: all pages.
+ * After tokens were rejected the bounds of the last page are wider than need be
+ * until it is written into again, never narrower.
+ * A length outside [0, max_pages_per_seq * 16] is clamped and sets
+ * NVFP4KV_DEV_BAD_LEN, as does a negative from_lens; a page id outside
+ * [0, num_pages) is skipped and sets NVFP4KV_DEV_BAD_PAGE.  batch at most
+ * NVFP4KV_MAX_BATCH.  bounds must have the cache's num_pages and
+ * num_kv_heads (NVFP4KV_ERR_INVALID_ARG). */
+nvfp4kv_status nvfp4kv_page_bounds(const nvfp4kv_cache *cache, const nvfp4kv_bounds *bounds,
+                                   const int32_t *block_table, int32_t max_pages_per_seq, const int32_t *from_lens,
+                                   const int32_t *seq_lens, int32_t batch, int32_t *dev_status,
+                                   nvfp4kv_stream_t stream);
+
+/* The same of the block-scaled FP8 cache (a library utility). */
+nvfp4kv_status fp8bkv_page_bounds(const fp8bkv_cache *cache, const nvfp4kv_bounds *bounds, const int32_t *block_table,
+                                  int32_t max_pages_per_seq, const int32_t *from_lens, const int32_t *seq_lens,
+                                  int32_t batch, int32_t *dev_status, nvfp4kv_stream_t stream);
+
+/* Selects pages for each query token and kv head (a library utility, for either
+ * cache).  Query token t of sequence b (q bf16 [batch][q_len][num_q_heads][128],
+ * q_len 1 .. NVFP4KV_MAX_QUERY_TOKENS, the sequence's last positions) sees the
+ * first n = seq_lens[b] - q_len + t + 1 tokens, so P = ceil(n / 16) pages (none
+ * where n <= 0).  With the group's queries in whole steps, w = rint(fl32(q *
+ * fl32(127 / max |q|))), the maximum over the group's heads and channels:
+ *   score(page) = fl32(step * max_h sum_c max(w_hc * hi_c, w_hc * lo_c)),
+ * the most that a key within the bounds can reach with one of the heads; the
+ * sum is a whole number below 2^24, so the score depends on no order of sums.
+ * Selected are the first `first_pages` and the last `last_pages` of the P and the
+ * others of the largest scores, the lower page where two are equal, `budget` in
+ * all, or all P where they are no more than that.
+ *   pages      int32 [batch][q_len][num_kv_heads][budget]: the selected pages'
+ *              places in the sequence (indices into its row of the block table),
+ *              ascending, -1 behind the last one
+ *   workspace  device scratch of at least the size below, 256-byte aligned, not
+ *              initialised; two calls in flight at once must not share it
+ * first_pages + last_pages at most budget; max_pages_per_seq at most 2^20;
+ * batch * q_len at most NVFP4KV_MAX_BATCH.  A length outside [0,
+ * max_pages_per_seq * 16] is clamped and sets NVFP4KV_DEV_BAD_LEN; the score of a
+ * page id outside [0, num_pages) is that of page 0 and sets
+ * NVFP4KV_DEV_BAD_PAGE.  Non-finite queries give an unspecified selection (of
+ * pages there are).  pages and the workspace overlap nothing else
+ * (NVFP4KV_ERR_INVALID_ARG). */
+nvfp4kv_status nvfp4kv_select_pages(const nvfp4kv_bounds *bounds, const void *q, int32_t batch, int32_t q_len,
+                                    int32_t num_q_heads, const int32_t *block_table, int32_t max_pages_per_seq,
+                                    const int32_t *seq_lens, int32_t budget, int32_t first_pages, int32_t last_pages,
+                                    int32_t *pages, void *workspace, size_t workspace_bytes, int32_t *dev_status,
+                                    nvfp4kv_stream_t stream);
+
+/* Bytes of workspace that nvfp4kv_select_pages needs (a library utility; host
+ * only; 0 for sizes that the call refuses). */
+size_t nvfp4kv_select_pages_workspace_size(int32_t batch, int32_t q_len, int32_t num_kv_heads,
+                                           int32_t max_pages_per_seq);
+
+/* Decode attention over listed pages (a library utility): query token t of
+ * sequence b, kv head h attends over those of its first n = seq_lens[b] - q_len +
+ * t + 1 tokens that lie in the first min(budget, ceil(n / 16)) entries of
+ * pages[b][t][h] (as nvfp4kv_select_pages writes them; any order).  An entry
+ * outside [0, ceil(n / 16)) has no tokens and sets NVFP4KV_DEV_BAD_PAGE; an entry
+ * that is there twice counts twice.  A token that sees no key gets zeros.
+ *   q    bf16 [batch][q_len][num_q_heads][128], out the same in out_dtype
+ *   workspace, num_workers  as for nvfp4kv_paged_decode
+ * batch * q_len at most NVFP4KV_MAX_BATCH; other arguments, checks and arithmetic
+ * as for nvfp4kv_paged_decode. */
+nvfp4kv_status nvfp4kv_selected_decode(const nvfp4kv_cache *cache, const void *q, int32_t batch, int32_t q_len,
+                                       int32_t num_q_heads, const int32_t *block_table, int32_t max_pages_per_seq,
+                                       const int32_t *seq_lens, const int32_t *pages, int32_t budget, float sm_scale,
+                                       void *out, nvfp4kv_dtype out_dtype, void *workspace, size_t workspace_bytes,
+                                       int32_t num_workers, int32_t *dev_status, nvfp4kv_stream_t stream);
+
+/* The same over the block-scaled FP8 cache (a library utility), with
+ * fp8bkv_paged_decode's arithmetic. */
+nvfp4kv_status fp8bkv_selected_decode(const fp8bkv_cache *cache, const void *q, int32_t batch, int32_t q_len,
+                                      int32_t num_q_heads, const int32_t *block_table, int32_t max_pages_per_seq,
+                                      const int32_t *seq_lens, const int32_t *pages, int32_t budget, float sm_scale,
+                                      void *out, nvfp4kv_dtype out_dtype, void *workspace, size_t workspace_bytes,
+                                      int32_t num_workers, int32_t *dev_status, nvfp4kv_stream_t stream);
 
 /* Bytes of an NVFP4 pool (K and V data and scales) for a geometry:
  * num_pages * num_kv_heads * page_size * 2 * (head_dim/2 + head_dim/16),

@@ -28,6 +28,15 @@ Functions carry the C names and take torch tensors:
     nvfp4kv_release_pages(old_lens, keep_lens, block_table, num_pages, free_pages, num_free, ...)
     nvfp4kv_qk_norm_rope(q, k, positions, q_out, k_out, rope=None, q_weight=None, k_weight=None, ...)
     nvfp4kv_qk_norm_rope_append(cache, q, k, v, positions, slot_mapping, q_out, rope=None, ...)
+  block-scaled FP8 cache (FP8BlockCache)
+    fp8bkv_append(cache, k_new, v_new, q_indptr, block_table, seq_lens, dev_status=None)
+    fp8bkv_dequant(cache, block_table, lens, kv_indptr, k_out, v_out, dev_status=None)
+    fp8bkv_paged_decode(cache, q, block_table, seq_lens, out, workspace, ...)
+  attention over selected pages (either cache)
+    nvfp4kv_page_bounds / fp8bkv_page_bounds(cache, bounds, block_table, seq_lens, from_lens=None, ...)
+    nvfp4kv_select_pages(bounds, q, block_table, seq_lens, pages, workspace, first_pages=1, last_pages=1, ...)
+    nvfp4kv_select_pages_workspace_size(batch, q_len, num_kv_heads, max_pages), new_select_workspace(...)
+    nvfp4kv_selected_decode / fp8bkv_selected_decode(cache, q, block_table, seq_lens, pages, out, workspace, ...)
   utilities
     nvfp4kv_read_device_status(dev_status, stream=None)
     nvfp4kv_set_wait_limit(polls) (failure detection: when bounded waits give up)
@@ -65,6 +74,7 @@ class Nvfp4kvError(RuntimeError):
 
 NVFP4_RECORD_BYTES = 2304      # one page-head record: K, V data and scales
 FP8_RECORD_BYTES = 4096
+FP8_BLOCK_RECORD_BYTES = 4128
 
 
 class _Nvfp4Cache(ctypes.Structure):
@@ -78,6 +88,15 @@ class _Fp8Cache(ctypes.Structure):
     _fields_ = [("pool", ctypes.c_void_p),
                 ("num_pages", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
                 ("page_size", ctypes.c_int32), ("head_dim", ctypes.c_int32)]
+
+
+class _Fp8BlockCache(ctypes.Structure):
+    _fields_ = _Fp8Cache._fields_
+
+
+class _Bounds(ctypes.Structure):
+    _fields_ = [("bounds", ctypes.c_void_p), ("steps", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32)]
 
 
 class _Rope(ctypes.Structure):
@@ -160,6 +179,23 @@ def load(build_if_missing: bool = True):
             "fp8kv_quantize_append": (_st, [ctypes.POINTER(_Fp8Cache), _vp, _vp, _st, _i32, _vp, _vp, _vp]),
             "fp8kv_paged_decode": (_st, [ctypes.POINTER(_Fp8Cache), _vp, _i32, _i32, _vp, _i32, _vp,
                                          ctypes.c_float, _vp, _st, _vp, ctypes.c_size_t, _i32, _vp, _vp]),
+            "fp8bkv_append": (_st, [ctypes.POINTER(_Fp8BlockCache), _vp, _vp, _st, _i32, _vp, _i32, _vp, _i32, _vp, _vp,
+                                    _vp]),
+            "fp8bkv_dequant": (_st, [ctypes.POINTER(_Fp8BlockCache), _vp, _i32, _vp, _vp, _i32, _vp, _vp, _st, _vp, _vp]),
+            "fp8bkv_paged_decode": (_st, [ctypes.POINTER(_Fp8BlockCache), _vp, _i32, _i32, _i32, _vp, _i32, _vp,
+                                          ctypes.c_float, _vp, _st, _vp, ctypes.c_size_t, _i32, _vp, _vp]),
+            "nvfp4kv_page_bounds": (_st, [ctypes.POINTER(_Nvfp4Cache), ctypes.POINTER(_Bounds), _vp, _i32, _vp, _vp,
+                                          _i32, _vp, _vp]),
+            "fp8bkv_page_bounds": (_st, [ctypes.POINTER(_Fp8BlockCache), ctypes.POINTER(_Bounds), _vp, _i32, _vp, _vp,
+                                         _i32, _vp, _vp]),
+            "nvfp4kv_select_pages": (_st, [ctypes.POINTER(_Bounds), _vp, _i32, _i32, _i32, _vp, _i32, _vp, _i32, _i32,
+                                           _i32, _vp, _vp, ctypes.c_size_t, _vp, _vp]),
+            "nvfp4kv_select_pages_workspace_size": (ctypes.c_size_t, [_i32] * 4),
+            "nvfp4kv_selected_decode": (_st, [ctypes.POINTER(_Nvfp4Cache), _vp, _i32, _i32, _i32, _vp, _i32, _vp, _vp,
+                                              _i32, ctypes.c_float, _vp, _st, _vp, ctypes.c_size_t, _i32, _vp, _vp]),
+            "fp8bkv_selected_decode": (_st, [ctypes.POINTER(_Fp8BlockCache), _vp, _i32, _i32, _i32, _vp, _i32, _vp, _vp,
+                                             _i32, ctypes.c_float, _vp, _st, _vp, ctypes.c_size_t, _i32, _vp, _vp]),
+            "fp8bkv_cache_bytes": (ctypes.c_int64, [_i32, _i32, _i32, _i32]),
             "nvfp4kv_cache_bytes": (ctypes.c_int64, [_i32, _i32, _i32, _i32]),
             "fp8kv_cache_bytes": (ctypes.c_int64, [_i32, _i32, _i32, _i32]),
             "nvfp4kv_status_string": (ctypes.c_char_p, [_st]),
@@ -248,13 +284,40 @@ class FP8Cache(NVFP4Cache):
     """An FP8-E4M3 pool: uint8 [num_pages][num_kv_heads][FP8_RECORD_BYTES] records."""
 
     record_bytes = FP8_RECORD_BYTES
+    _struct = _Fp8Cache
 
     def __init__(self, pool):
         self.pool = pool
         self.num_pages, self.num_kv_heads, rb = pool.shape
         assert rb == self.record_bytes
         self.page_size, self.head_dim = PAGE_SIZE, HEAD_DIM
-        self._c = _Fp8Cache(pool.data_ptr(), self.num_pages, self.num_kv_heads, PAGE_SIZE, HEAD_DIM)
+        self._c = self._struct(pool.data_ptr(), self.num_pages, self.num_kv_heads, PAGE_SIZE, HEAD_DIM)
+
+
+class FP8BlockCache(FP8Cache):
+    """An FP8-E4M3 pool with a scale for each page and kv head: uint8
+    [num_pages][num_kv_heads][FP8_BLOCK_RECORD_BYTES] records."""
+
+    record_bytes = FP8_BLOCK_RECORD_BYTES
+    _struct = _Fp8BlockCache
+
+
+class PageBounds:
+    """Bounds of the keys of a cache's pages: bounds int8
+    [num_pages][num_kv_heads][2][128] (least, largest), steps fp32
+    [num_pages][num_kv_heads]."""
+
+    def __init__(self, bounds, steps):
+        self.bounds, self.steps = bounds, steps
+        self.num_pages, self.num_kv_heads = steps.shape
+        self._c = _Bounds(bounds.data_ptr(), steps.data_ptr(), self.num_pages, self.num_kv_heads)
+        self.c = ctypes.byref(self._c)
+
+    @classmethod
+    def allocate(cls, num_pages, num_kv_heads, device="cuda"):
+        import torch
+        return cls(torch.zeros((num_pages, num_kv_heads, 2, HEAD_DIM), dtype=torch.int8, device=device),
+                   torch.zeros((num_pages, num_kv_heads), dtype=torch.float32, device=device))
 
 
 class Rope:
@@ -628,6 +691,201 @@ def nvfp4kv_qk_norm_rope_append(cache: NVFP4Cache, q, k, v, positions, slot_mapp
     _check(st, "nvfp4kv_qk_norm_rope_append")
 
 
+def _pool(cache, kind):
+    """(cache, name, shape) of a cache argument's pool for _tensors."""
+    if type(cache).record_bytes != kind.record_bytes:
+        raise TypeError(f"cache: expected {kind.__name__}, got {type(cache).__name__}")
+    return cache.pool, "cache", (cache.num_pages, cache.num_kv_heads, kind.record_bytes)
+
+
+def fp8bkv_append(cache: FP8BlockCache, k_new, v_new, q_indptr, block_table, seq_lens, dev_status=None,
+                  stream=None) -> None:
+    """Write the rows k_new, v_new [T][Hkv][128] (fp32 or bf16), sequence b's being
+    q_indptr[b] .. q_indptr[b+1] - 1 (int32 [B+1]), as the last tokens of its
+    seq_lens[b] (int32 [B], they included) into the pages of block_table int32
+    [B][pages]; a page's scale rises where they need it."""
+    import torch
+    pool = _pool(cache, FP8BlockCache)
+    dev = _current_device()
+    B, pages = block_table.shape
+    T, code = k_new.shape[0], _dtype_code(k_new)
+    rows = (T, cache.num_kv_heads, HEAD_DIM)
+    _tensors(dev, torch.uint8, pool)
+    _tensors(dev, k_new.dtype, (k_new, "k_new", rows), (v_new, "v_new", rows))
+    _tensors(dev, torch.int32, (q_indptr, "q_indptr", (B + 1,)), (block_table, "block_table", (B, pages)),
+             (seq_lens, "seq_lens", (B,)), (dev_status, "dev_status", (1,)))
+    st = load().fp8bkv_append(cache.c, _ptr(k_new), _ptr(v_new), code, T, _ptr(q_indptr), B, _ptr(block_table), pages,
+                              _ptr(seq_lens), _ptr(dev_status), _stream(stream, dev))
+    _check(st, "fp8bkv_append")
+
+
+def fp8bkv_dequant(cache: FP8BlockCache, block_table, lens, kv_indptr, k_out, v_out, dev_status=None,
+                   stream=None) -> None:
+    """Read the first lens[b] cached rows of each sequence back into rows
+    kv_indptr[b] .. of k_out and v_out [rows][Hkv][128]: fp32, bf16, or E4M3
+    (uint8 or float8_e4m3fn: the workspace of the extend calls)."""
+    import torch
+    pool = _pool(cache, FP8BlockCache)
+    dev = _current_device()
+    B, pages = block_table.shape
+    code = _dtype_code(k_out) if k_out.dtype is torch.float32 else _chunk_dtype_code(k_out)
+    rows = (k_out.shape[0], cache.num_kv_heads, HEAD_DIM)
+    _tensors(dev, torch.uint8, pool)
+    _tensors(dev, k_out.dtype, (k_out, "k_out", rows), (v_out, "v_out", rows))
+    _tensors(dev, torch.int32, (block_table, "block_table", (B, pages)), (lens, "lens", (B,)),
+             (kv_indptr, "kv_indptr", (B,)), (dev_status, "dev_status", (1,)))
+    st = load().fp8bkv_dequant(cache.c, _ptr(block_table), pages, _ptr(lens), _ptr(kv_indptr), B, _ptr(k_out),
+                               _ptr(v_out), code, _ptr(dev_status), _stream(stream, dev))
+    _check(st, "fp8bkv_dequant")
+
+
+def _query_rows(dev, q, out, batch):
+    """Check q bf16 [B][Hq][128] or [B][q_len][Hq][128] and out of its shape;
+    returns (q_len, Hq)."""
+    import torch
+    if q.dim() not in (3, 4):
+        raise ValueError(f"q: expected [B][Hq][128] or [B][q_len][Hq][128], got shape {tuple(q.shape)}")
+    q_len, heads = (1, q.shape[1]) if q.dim() == 3 else (q.shape[1], q.shape[2])
+    shape = (batch, heads, HEAD_DIM) if q.dim() == 3 else (batch, q_len, heads, HEAD_DIM)
+    _tensors(dev, torch.bfloat16, (q, "q", shape))
+    if out is not None:
+        _tensors(dev, out.dtype, (out, "out", shape))
+    return q_len, heads
+
+
+def fp8bkv_paged_decode(cache: FP8BlockCache, q, block_table, seq_lens, out, workspace, sm_scale=None, num_workers=0,
+                        dev_status=None, stream=None) -> None:
+    """Decode attention over the block-scaled FP8 cache.  q: bf16 [B][Hq][128], or
+    [B][q_len][Hq][128] for the last q_len positions of each sequence, causal
+    among themselves; out: bf16 or fp32 of q's shape; workspace: new_workspace."""
+    import torch
+    if sm_scale is None:
+        sm_scale = 1.0 / math.sqrt(HEAD_DIM)
+    pool = _pool(cache, FP8BlockCache)
+    dev = _current_device()
+    B, pages = block_table.shape
+    q_len, heads = _query_rows(dev, q, out, B)
+    _tensors(dev, torch.uint8, pool,
+             (workspace, "workspace", (0 if workspace is None else workspace.numel(),)))
+    _tensors(dev, torch.int32, (block_table, "block_table", (B, pages)), (seq_lens, "seq_lens", (B,)),
+             (dev_status, "dev_status", (1,)))
+    st = load().fp8bkv_paged_decode(
+        cache.c, _ptr(q), B, q_len, heads, _ptr(block_table), pages, _ptr(seq_lens), float(sm_scale), _ptr(out),
+        _dtype_code(out), _ptr(workspace), 0 if workspace is None else workspace.numel(),
+        _int32(num_workers, "num_workers"), _ptr(dev_status), _stream(stream, dev))
+    _check(st, "fp8bkv_paged_decode")
+
+
+def _bounds_tensors(dev, bounds: PageBounds) -> None:
+    import torch
+    n, h = bounds.num_pages, bounds.num_kv_heads
+    _tensors(dev, torch.int8, (bounds.bounds, "bounds.bounds", (n, h, 2, HEAD_DIM)))
+    _tensors(dev, torch.float32, (bounds.steps, "bounds.steps", (n, h)))
+
+
+def _page_bounds(name, kind, cache, bounds, block_table, seq_lens, from_lens, dev_status, stream):
+    import torch
+    pool = _pool(cache, kind)
+    dev = _current_device()
+    B, pages = block_table.shape
+    _tensors(dev, torch.uint8, pool)
+    _bounds_tensors(dev, bounds)
+    _tensors(dev, torch.int32, (block_table, "block_table", (B, pages)), (seq_lens, "seq_lens", (B,)),
+             (from_lens, "from_lens", (B,)), (dev_status, "dev_status", (1,)))
+    st = getattr(load(), name)(cache.c, bounds.c, _ptr(block_table), pages, _ptr(from_lens), _ptr(seq_lens), B,
+                               _ptr(dev_status), _stream(stream, dev))
+    _check(st, name)
+
+
+def nvfp4kv_page_bounds(cache: NVFP4Cache, bounds: PageBounds, block_table, seq_lens, from_lens=None, dev_status=None,
+                        stream=None) -> None:
+    """Bring the bounds of the pages that tokens from_lens[b] .. seq_lens[b] - 1
+    (int32 [B]; None: from 0) were written into up to date."""
+    _page_bounds("nvfp4kv_page_bounds", NVFP4Cache, cache, bounds, block_table, seq_lens, from_lens, dev_status, stream)
+
+
+def fp8bkv_page_bounds(cache: FP8BlockCache, bounds: PageBounds, block_table, seq_lens, from_lens=None,
+                       dev_status=None, stream=None) -> None:
+    """nvfp4kv_page_bounds of a block-scaled FP8 cache."""
+    _page_bounds("fp8bkv_page_bounds", FP8BlockCache, cache, bounds, block_table, seq_lens, from_lens, dev_status, stream)
+
+
+def nvfp4kv_select_pages_workspace_size(batch, q_len, num_kv_heads, max_pages_per_seq) -> int:
+    return int(load().nvfp4kv_select_pages_workspace_size(
+        _int32(batch, "batch"), _int32(q_len, "q_len"), _int32(num_kv_heads, "num_kv_heads"),
+        _int32(max_pages_per_seq, "max_pages_per_seq")))
+
+
+def nvfp4kv_select_pages(bounds: PageBounds, q, block_table, seq_lens, pages, workspace, first_pages=1, last_pages=1,
+                         dev_status=None, stream=None) -> None:
+    """Select pages for each query token and kv head: the first first_pages and
+    the last last_pages that the token sees and the best of the others by the
+    score of their bounds, into pages int32 [B][q_len][Hkv][budget] (ascending
+    places in the sequence, -1 behind the last; [B][Hkv][budget] where q is
+    [B][Hq][128]).  workspace: new_select_workspace."""
+    import torch
+    dev = _current_device()
+    B, max_pages = block_table.shape
+    q_len, heads = _query_rows(dev, q, None, B)
+    _bounds_tensors(dev, bounds)
+    budget = pages.shape[-1]
+    shape = (B, q_len, bounds.num_kv_heads, budget)
+    _tensors(dev, torch.int32,
+             (pages, "pages", shape if pages.dim() == 4 or q.dim() == 4 else (B, bounds.num_kv_heads, budget)),
+             (block_table, "block_table", (B, max_pages)), (seq_lens, "seq_lens", (B,)),
+             (dev_status, "dev_status", (1,)))
+    _tensors(dev, torch.uint8, (workspace, "workspace", (0 if workspace is None else workspace.numel(),)))
+    st = load().nvfp4kv_select_pages(
+        bounds.c, _ptr(q), B, q_len, heads, _ptr(block_table), max_pages, _ptr(seq_lens), budget,
+        _int32(first_pages, "first_pages"), _int32(last_pages, "last_pages"), _ptr(pages), _ptr(workspace),
+        0 if workspace is None else workspace.numel(), _ptr(dev_status), _stream(stream, dev))
+    _check(st, "nvfp4kv_select_pages")
+
+
+def _selected_decode(name, kind, cache, q, block_table, seq_lens, pages, out, workspace, sm_scale, num_workers,
+                     dev_status, stream):
+    import torch
+    if sm_scale is None:
+        sm_scale = 1.0 / math.sqrt(HEAD_DIM)
+    pool = _pool(cache, kind)
+    dev = _current_device()
+    B, max_pages = block_table.shape
+    q_len, heads = _query_rows(dev, q, out, B)
+    budget = pages.shape[-1]
+    shape = (B, q_len, cache.num_kv_heads, budget)
+    _tensors(dev, torch.uint8, pool,
+             (workspace, "workspace", (0 if workspace is None else workspace.numel(),)))
+    _tensors(dev, torch.int32,
+             (pages, "pages", shape if pages.dim() == 4 or q.dim() == 4 else (B, cache.num_kv_heads, budget)),
+             (block_table, "block_table", (B, max_pages)), (seq_lens, "seq_lens", (B,)),
+             (dev_status, "dev_status", (1,)))
+    st = getattr(load(), name)(
+        cache.c, _ptr(q), B, q_len, heads, _ptr(block_table), max_pages, _ptr(seq_lens), _ptr(pages), budget,
+        float(sm_scale), _ptr(out), _dtype_code(out), _ptr(workspace), 0 if workspace is None else workspace.numel(),
+        _int32(num_workers, "num_workers"), _ptr(dev_status), _stream(stream, dev))
+    _check(st, name)
+
+
+def nvfp4kv_selected_decode(cache: NVFP4Cache, q, block_table, seq_lens, pages, out, workspace, sm_scale=None,
+                            num_workers=0, dev_status=None, stream=None) -> None:
+    """Decode attention of each query token and kv head over the pages listed for
+    it (as nvfp4kv_select_pages writes them).  q, out and workspace as for
+    fp8bkv_paged_decode."""
+    _selected_decode("nvfp4kv_selected_decode", NVFP4Cache, cache, q, block_table, seq_lens, pages, out, workspace,
+                     sm_scale, num_workers, dev_status, stream)
+
+
+def fp8bkv_selected_decode(cache: FP8BlockCache, q, block_table, seq_lens, pages, out, workspace, sm_scale=None,
+                           num_workers=0, dev_status=None, stream=None) -> None:
+    """nvfp4kv_selected_decode over a block-scaled FP8 cache."""
+    _selected_decode("fp8bkv_selected_decode", FP8BlockCache, cache, q, block_table, seq_lens, pages, out, workspace,
+                     sm_scale, num_workers, dev_status, stream)
+
+
+def fp8bkv_cache_bytes(num_pages, num_kv_heads, page_size=PAGE_SIZE, head_dim=HEAD_DIM) -> int:
+    return int(load().fp8bkv_cache_bytes(num_pages, num_kv_heads, page_size, head_dim))
+
+
 def nvfp4kv_cache_bytes(num_pages, num_kv_heads, page_size=PAGE_SIZE, head_dim=HEAD_DIM) -> int:
     return int(load().nvfp4kv_cache_bytes(num_pages, num_kv_heads, page_size, head_dim))
 
@@ -682,4 +940,11 @@ def new_extend_workspace(q_rows, max_q_len, batch, num_q_heads, num_kv_heads, ma
     import torch
     n = nvfp4kv_paged_extend_workspace_size(q_rows, max_q_len, batch, num_q_heads, num_kv_heads, max_pages_per_seq,
                                             window)
+    return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
+
+
+def new_select_workspace(batch, q_len, num_kv_heads, max_pages_per_seq, device="cuda"):
+    """A workspace tensor for nvfp4kv_select_pages calls of these sizes."""
+    import torch
+    n = nvfp4kv_select_pages_workspace_size(batch, q_len, num_kv_heads, max_pages_per_seq)
     return torch.empty(max(n, 256), dtype=torch.uint8, device=device)

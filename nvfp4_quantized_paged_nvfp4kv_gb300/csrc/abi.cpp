@@ -92,7 +92,8 @@ nvfp4kv_status check_nvfp4(const nvfp4kv_cache *c)
     return NVFP4KV_OK;
 }
 
-nvfp4kv_status check_fp8(const fp8kv_cache *c)
+template <class Cache>                           // fp8kv_cache, fp8bkv_cache
+nvfp4kv_status check_fp8(const Cache *c)
 {
     if (c == nullptr)
         return NVFP4KV_ERR_INVALID_ARG;
@@ -336,6 +337,143 @@ nvfp4kv_status check_paged_extend_sizes(int32_t q_rows, int32_t max_q_len, int32
     if (group > kMaxGroup || hkv > 65535 || batch > kMaxBatch || max_q_len * group >= (int64_t{1} << 30) ||
         static_cast<int64_t>(max_pages) * kPageSize > (int64_t{1} << 30))
         return NVFP4KV_ERR_UNSUPPORTED;
+    return NVFP4KV_OK;
+}
+
+// A block table, the lengths of its rows, and an optional array as long.
+nvfp4kv_status check_rows(int32_t batch, const int32_t *block_table, int32_t max_pages_per_seq, const int32_t *lens,
+                          const int32_t *more)
+{
+    if (batch < 0 || max_pages_per_seq <= 0)
+        return NVFP4KV_ERR_INVALID_ARG;
+    if (batch > kMaxBatch || static_cast<int64_t>(batch) * max_pages_per_seq > (int64_t{1} << 31) - 1 ||
+        static_cast<int64_t>(max_pages_per_seq) * kPageSize > (int64_t{1} << 30))
+        return NVFP4KV_ERR_UNSUPPORTED;
+    if (batch > 0 && (block_table == nullptr || lens == nullptr || !aligned4(block_table) || !aligned4(lens) ||
+                      !aligned4(more)))
+        return NVFP4KV_ERR_INVALID_ARG;
+    return NVFP4KV_OK;
+}
+
+nvfp4kv_status check_bounds(const nvfp4kv_bounds *b)
+{
+    if (b == nullptr || b->num_pages <= 0 || b->num_kv_heads <= 0 || b->bounds == nullptr || !aligned16(b->bounds) ||
+        b->steps == nullptr || !aligned4(b->steps))
+        return NVFP4KV_ERR_INVALID_ARG;
+    if (static_cast<int64_t>(b->num_pages) * b->num_kv_heads > (int64_t{1} << 31) - 1)
+        return NVFP4KV_ERR_UNSUPPORTED;
+    return NVFP4KV_OK;
+}
+
+size_t heads_of(const nvfp4kv_bounds *b)
+{
+    return static_cast<size_t>(b->num_pages) * b->num_kv_heads;
+}
+
+// Bounds of either cache's pages; the cache is checked.
+template <class Cache, class Launch>
+nvfp4kv_status page_bounds(const Cache *cache, size_t record, const nvfp4kv_bounds *bounds, const int32_t *block_table,
+                           int32_t max_pages_per_seq, const int32_t *from_lens, const int32_t *seq_lens, int32_t batch,
+                           int32_t *dev_status, nvfp4kv_stream_t stream, Launch launch)
+{
+    nvfp4kv_status st = check_bounds(bounds);
+    if (st != NVFP4KV_OK)
+        return st;
+    if (bounds->num_pages != cache->num_pages || bounds->num_kv_heads != cache->num_kv_heads)
+        return NVFP4KV_ERR_INVALID_ARG;
+    st = check_rows(batch, block_table, max_pages_per_seq, seq_lens, from_lens);
+    if (st != NVFP4KV_OK || batch == 0)
+        return st;
+    const size_t n = 4 * static_cast<size_t>(batch), heads = heads_of(bounds);
+    const Span spans[] = {{cache->pool, heads * record, false},
+                          {block_table, n * static_cast<size_t>(max_pages_per_seq), false},
+                          {from_lens, n, false},
+                          {seq_lens, n, false},
+                          {bounds->bounds, heads * 2 * kHeadDim, true},
+                          {bounds->steps, 4 * heads, true}};
+    if (written_overlap(spans))
+        return NVFP4KV_ERR_INVALID_ARG;
+    BoundsParams p{};
+    p.pool = static_cast<const uint8_t *>(cache->pool);
+    p.block_table = block_table;
+    p.from_lens = from_lens;
+    p.seq_lens = seq_lens;
+    p.bounds = bounds->bounds;
+    p.steps = bounds->steps;
+    p.dev_status = dev_status;
+    p.batch = batch;
+    p.hkv = cache->num_kv_heads;
+    p.max_pages = max_pages_per_seq;
+    p.num_pages = cache->num_pages;
+    return from_cuda(launch(p, to_cuda(stream)));
+}
+
+constexpr int32_t kMaxSelectPages = 1 << 20;
+
+nvfp4kv_status check_query_tokens(int32_t batch, int32_t q_len)
+{
+    if (batch < 0 || q_len < 1)
+        return NVFP4KV_ERR_INVALID_ARG;
+    if (q_len > NVFP4KV_MAX_QUERY_TOKENS || static_cast<int64_t>(batch) * q_len > kMaxBatch)
+        return NVFP4KV_ERR_UNSUPPORTED;
+    return NVFP4KV_OK;
+}
+
+nvfp4kv_status check_select_sizes(int32_t batch, int32_t q_len, int32_t hkv, int32_t max_pages)
+{
+    const nvfp4kv_status st = check_query_tokens(batch, q_len);
+    if (st != NVFP4KV_OK)
+        return st;
+    if (hkv <= 0 || max_pages <= 0)
+        return NVFP4KV_ERR_INVALID_ARG;
+    if (max_pages > kMaxSelectPages || static_cast<int64_t>(batch) * q_len * hkv > (int64_t{1} << 31) - 1 ||
+        static_cast<int64_t>(batch) * hkv * ((max_pages + 15) / 16) > (int64_t{1} << 31) - 1)
+        return NVFP4KV_ERR_UNSUPPORTED;
+    return NVFP4KV_OK;
+}
+
+size_t select_workspace(int32_t batch, int32_t q_len, int32_t hkv, int32_t max_pages)
+{
+    return 4 * static_cast<size_t>(batch) * q_len * hkv * score_row_stride(max_pages);
+}
+
+// Decode over listed pages: fills p (except the cache's pool and scales).
+nvfp4kv_status check_selected(int32_t hkv, int32_t num_pages, size_t pool_bytes, const void *pool, const void *q,
+                              int32_t batch, int32_t q_len, int32_t num_q_heads, const int32_t *block_table,
+                              int32_t max_pages_per_seq, const int32_t *seq_lens, const int32_t *pages, int32_t budget,
+                              float sm_scale, void *out, nvfp4kv_dtype out_dtype, void *workspace,
+                              size_t workspace_bytes, int32_t num_workers, int32_t *dev_status, DecodeParams &p)
+{
+    nvfp4kv_status st = check_query_tokens(batch, q_len);
+    if (st != NVFP4KV_OK)
+        return st;
+    st = check_rows(batch, block_table, max_pages_per_seq, seq_lens, pages);
+    if (st != NVFP4KV_OK)
+        return st;
+    if (budget <= 0)
+        return NVFP4KV_ERR_INVALID_ARG;
+    // (a row's pages are at most the budget: what the work split is made for)
+    const int32_t most = budget < max_pages_per_seq ? budget : max_pages_per_seq;
+    st = check_decode(hkv, num_pages, q, batch * q_len, num_q_heads, block_table, most, seq_lens, sm_scale, out,
+                      out_dtype, workspace, workspace_bytes, num_workers, dev_status, p);
+    if (st != NVFP4KV_OK || batch == 0)
+        return st;
+    if (pages == nullptr)
+        return NVFP4KV_ERR_INVALID_ARG;
+    const size_t rows = static_cast<size_t>(batch) * q_len, elems = rows * num_q_heads * kHeadDim;
+    const Span spans[] = {{q, 2 * elems, false},
+                          {block_table, 4 * static_cast<size_t>(batch) * max_pages_per_seq, false},
+                          {seq_lens, 4 * static_cast<size_t>(batch), false},
+                          {pages, 4 * rows * hkv * static_cast<size_t>(budget), false},
+                          {pool, pool_bytes, false},
+                          {out, elems * (out_dtype == NVFP4KV_F32 ? 4 : 2), true},
+                          {workspace, decode_workspace_bytes(p.num_workers), true}};
+    if (written_overlap(spans))
+        return NVFP4KV_ERR_INVALID_ARG;
+    p.max_pages = max_pages_per_seq;
+    p.sel_pages = pages;
+    p.budget = budget;
+    p.sel_q_len = q_len;
     return NVFP4KV_OK;
 }
 
@@ -950,6 +1088,250 @@ nvfp4kv_status fp8kv_append_paged_decode(const fp8kv_cache *cache, const void *k
     if (e == cudaSuccess)
         e = launch_merge(p, to_cuda(stream));
     return from_cuda(e);
+}
+
+nvfp4kv_status fp8bkv_append(const fp8bkv_cache *cache, const void *k_new, const void *v_new, nvfp4kv_dtype in_dtype,
+                             int32_t num_tokens, const int32_t *q_indptr, int32_t batch, const int32_t *block_table,
+                             int32_t max_pages_per_seq, const int32_t *seq_lens, int32_t *dev_status,
+                             nvfp4kv_stream_t stream)
+{
+    nvfp4kv_status st = check_fp8(cache);
+    if (st != NVFP4KV_OK)
+        return st;
+    st = check_append(k_new, v_new, in_dtype, num_tokens, q_indptr);
+    if (st != NVFP4KV_OK)
+        return st;
+    st = check_rows(batch, block_table, max_pages_per_seq, seq_lens, nullptr);
+    if (st != NVFP4KV_OK || num_tokens == 0 || batch == 0)
+        return st;
+    const size_t n = 4 * static_cast<size_t>(batch), size = in_dtype == NVFP4KV_BF16 ? 2 : 4;
+    const size_t row = static_cast<size_t>(cache->num_kv_heads) * kHeadDim * size;
+    const Span spans[] = {{k_new, num_tokens * row, false},
+                          {v_new, num_tokens * row, false},
+                          {q_indptr, n + 4, false},
+                          {block_table, n * static_cast<size_t>(max_pages_per_seq), false},
+                          {seq_lens, n, false},
+                          {cache->pool, static_cast<size_t>(cache->num_pages) * cache->num_kv_heads * kFp8BlockRecord, true}};
+    if (written_overlap(spans))
+        return NVFP4KV_ERR_INVALID_ARG;
+    BlockAppendParams p{};
+    p.k_new = k_new;
+    p.v_new = v_new;
+    p.q_indptr = q_indptr;
+    p.block_table = block_table;
+    p.seq_lens = seq_lens;
+    p.pool = static_cast<uint8_t *>(cache->pool);
+    p.dev_status = dev_status;
+    p.num_tokens = num_tokens;
+    p.batch = batch;
+    p.hkv = cache->num_kv_heads;
+    p.max_pages = max_pages_per_seq;
+    p.num_pages = cache->num_pages;
+    p.in_bf16 = in_dtype == NVFP4KV_BF16;
+    return from_cuda(launch_block_append(p, to_cuda(stream)));
+}
+
+nvfp4kv_status fp8bkv_dequant(const fp8bkv_cache *cache, const int32_t *block_table, int32_t max_pages_per_seq,
+                              const int32_t *lens, const int32_t *kv_indptr, int32_t batch, void *k_out, void *v_out,
+                              nvfp4kv_dtype out_dtype, int32_t *dev_status, nvfp4kv_stream_t stream)
+{
+    nvfp4kv_status st = check_fp8(cache);
+    if (st != NVFP4KV_OK)
+        return st;
+    if (out_dtype != NVFP4KV_F32 && out_dtype != NVFP4KV_BF16 && out_dtype != NVFP4KV_E4M3)
+        return NVFP4KV_ERR_INVALID_ARG;
+    st = check_rows(batch, block_table, max_pages_per_seq, lens, kv_indptr);
+    if (st != NVFP4KV_OK || batch == 0)
+        return st;
+    if (kv_indptr == nullptr || k_out == nullptr || v_out == nullptr || !aligned16(k_out) || !aligned16(v_out))
+        return NVFP4KV_ERR_INVALID_ARG;
+    BlockReadParams p{};
+    p.pool = static_cast<const uint8_t *>(cache->pool);
+    p.block_table = block_table;
+    p.lens = lens;
+    p.kv_indptr = kv_indptr;
+    p.k_out = k_out;
+    p.v_out = v_out;
+    p.dev_status = dev_status;
+    p.batch = batch;
+    p.hkv = cache->num_kv_heads;
+    p.max_pages = max_pages_per_seq;
+    p.num_pages = cache->num_pages;
+    p.out_dtype = out_dtype;
+    return from_cuda(launch_block_read(p, to_cuda(stream)));
+}
+
+nvfp4kv_status fp8bkv_paged_decode(const fp8bkv_cache *cache, const void *q, int32_t batch, int32_t q_len,
+                                   int32_t num_q_heads, const int32_t *block_table, int32_t max_pages_per_seq,
+                                   const int32_t *seq_lens, float sm_scale, void *out, nvfp4kv_dtype out_dtype,
+                                   void *workspace, size_t workspace_bytes, int32_t num_workers, int32_t *dev_status,
+                                   nvfp4kv_stream_t stream)
+{
+    nvfp4kv_status st = check_fp8(cache);
+    if (st != NVFP4KV_OK)
+        return st;
+    if (q_len < 1 || q_len > NVFP4KV_MAX_QUERY_TOKENS)
+        return q_len < 1 ? NVFP4KV_ERR_INVALID_ARG : NVFP4KV_ERR_UNSUPPORTED;
+    DecodeParams p;
+    st = check_decode(cache->num_kv_heads, cache->num_pages, q, batch, num_q_heads, block_table, max_pages_per_seq,
+                      seq_lens, sm_scale, out, out_dtype, workspace, workspace_bytes, num_workers, dev_status, p);
+    if (st != NVFP4KV_OK || batch == 0)
+        return st;
+    p.q_len = q_len;
+    p.rows = p.group * q_len;
+    p.row_groups = (p.rows + kMaxGroup - 1) / kMaxGroup;
+    if (static_cast<int64_t>(batch) * cache->num_kv_heads * p.row_groups * max_pages_per_seq > (int64_t{1} << 31) - 1)
+        return NVFP4KV_ERR_UNSUPPORTED;
+    p.pool = static_cast<const uint8_t *>(cache->pool);
+    cudaError_t e = launch_decode_fp8_block(p, to_cuda(stream));
+    if (e == cudaSuccess)
+        e = launch_merge(p, to_cuda(stream));
+    return from_cuda(e);
+}
+
+nvfp4kv_status nvfp4kv_page_bounds(const nvfp4kv_cache *cache, const nvfp4kv_bounds *bounds,
+                                   const int32_t *block_table, int32_t max_pages_per_seq, const int32_t *from_lens,
+                                   const int32_t *seq_lens, int32_t batch, int32_t *dev_status,
+                                   nvfp4kv_stream_t stream)
+{
+    const nvfp4kv_status st = check_nvfp4(cache);
+    if (st != NVFP4KV_OK)
+        return st;
+    return page_bounds(cache, kNvfp4Record, bounds, block_table, max_pages_per_seq, from_lens, seq_lens, batch,
+                       dev_status, stream, launch_page_bounds_nvfp4);
+}
+
+nvfp4kv_status fp8bkv_page_bounds(const fp8bkv_cache *cache, const nvfp4kv_bounds *bounds, const int32_t *block_table,
+                                  int32_t max_pages_per_seq, const int32_t *from_lens, const int32_t *seq_lens,
+                                  int32_t batch, int32_t *dev_status, nvfp4kv_stream_t stream)
+{
+    const nvfp4kv_status st = check_fp8(cache);
+    if (st != NVFP4KV_OK)
+        return st;
+    return page_bounds(cache, kFp8BlockRecord, bounds, block_table, max_pages_per_seq, from_lens, seq_lens, batch,
+                       dev_status, stream, launch_page_bounds_fp8_block);
+}
+
+size_t nvfp4kv_select_pages_workspace_size(int32_t batch, int32_t q_len, int32_t num_kv_heads,
+                                           int32_t max_pages_per_seq)
+{
+    if (check_select_sizes(batch, q_len, num_kv_heads, max_pages_per_seq) != NVFP4KV_OK)
+        return 0;
+    return select_workspace(batch, q_len, num_kv_heads, max_pages_per_seq);
+}
+
+nvfp4kv_status nvfp4kv_select_pages(const nvfp4kv_bounds *bounds, const void *q, int32_t batch, int32_t q_len,
+                                    int32_t num_q_heads, const int32_t *block_table, int32_t max_pages_per_seq,
+                                    const int32_t *seq_lens, int32_t budget, int32_t first_pages, int32_t last_pages,
+                                    int32_t *pages, void *workspace, size_t workspace_bytes, int32_t *dev_status,
+                                    nvfp4kv_stream_t stream)
+{
+    nvfp4kv_status st = check_bounds(bounds);
+    if (st != NVFP4KV_OK)
+        return st;
+    const int32_t hkv = bounds->num_kv_heads;
+    st = check_select_sizes(batch, q_len, hkv, max_pages_per_seq);
+    if (st == NVFP4KV_OK)
+        st = check_rows(batch, block_table, max_pages_per_seq, seq_lens, pages);
+    if (st != NVFP4KV_OK)
+        return st;
+    if (num_q_heads <= 0 || num_q_heads % hkv != 0 || budget <= 0 || first_pages < 0 || last_pages < 0 ||
+        first_pages > budget - last_pages)
+        return NVFP4KV_ERR_INVALID_ARG;
+    if (num_q_heads / hkv > kMaxGroup)
+        return NVFP4KV_ERR_UNSUPPORTED;
+    if (batch == 0)
+        return NVFP4KV_OK;
+    if (q == nullptr || !aligned16(q) || pages == nullptr)
+        return NVFP4KV_ERR_INVALID_ARG;
+    const size_t need = select_workspace(batch, q_len, hkv, max_pages_per_seq);
+    if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) || workspace_bytes < need)
+        return NVFP4KV_ERR_WORKSPACE;
+    const size_t rows = static_cast<size_t>(batch) * q_len, heads = heads_of(bounds);
+    const Span spans[] = {{bounds->bounds, heads * 2 * kHeadDim, false},
+                          {bounds->steps, 4 * heads, false},
+                          {q, 2 * rows * num_q_heads * kHeadDim, false},
+                          {block_table, 4 * static_cast<size_t>(batch) * max_pages_per_seq, false},
+                          {seq_lens, 4 * static_cast<size_t>(batch), false},
+                          {pages, 4 * rows * hkv * static_cast<size_t>(budget), true},
+                          {workspace, need, true}};
+    if (written_overlap(spans))
+        return NVFP4KV_ERR_INVALID_ARG;
+    SelectParams p{};
+    p.bounds = bounds->bounds;
+    p.steps = bounds->steps;
+    p.q = static_cast<const uint16_t *>(q);
+    p.block_table = block_table;
+    p.seq_lens = seq_lens;
+    p.pages = pages;
+    p.scores = static_cast<float *>(workspace);
+    p.dev_status = dev_status;
+    p.batch = batch;
+    p.q_len = q_len;
+    p.hq = num_q_heads;
+    p.hkv = hkv;
+    p.group = num_q_heads / hkv;
+    p.max_pages = max_pages_per_seq;
+    p.num_pages = bounds->num_pages;
+    p.budget = budget;
+    p.first = first_pages;
+    p.last = last_pages;
+    p.score_stride = score_row_stride(max_pages_per_seq);
+    return from_cuda(launch_select_pages(p, to_cuda(stream)));
+}
+
+nvfp4kv_status nvfp4kv_selected_decode(const nvfp4kv_cache *cache, const void *q, int32_t batch, int32_t q_len,
+                                       int32_t num_q_heads, const int32_t *block_table, int32_t max_pages_per_seq,
+                                       const int32_t *seq_lens, const int32_t *pages, int32_t budget, float sm_scale,
+                                       void *out, nvfp4kv_dtype out_dtype, void *workspace, size_t workspace_bytes,
+                                       int32_t num_workers, int32_t *dev_status, nvfp4kv_stream_t stream)
+{
+    nvfp4kv_status st = check_nvfp4(cache);
+    if (st != NVFP4KV_OK)
+        return st;
+    DecodeParams p;
+    st = check_selected(cache->num_kv_heads, cache->num_pages,
+                        static_cast<size_t>(cache->num_pages) * cache->num_kv_heads * kNvfp4Record, cache->pool, q, batch,
+                        q_len, num_q_heads, block_table, max_pages_per_seq, seq_lens, pages, budget, sm_scale, out,
+                        out_dtype, workspace, workspace_bytes, num_workers, dev_status, p);
+    if (st != NVFP4KV_OK || batch == 0)
+        return st;
+    p.pool = static_cast<const uint8_t *>(cache->pool);
+    apply_tensor_scale(p, sm_scale, cache);
+    cudaError_t e = launch_decode_selected_nvfp4(p, to_cuda(stream));
+    if (e == cudaSuccess)
+        e = launch_merge(p, to_cuda(stream));
+    return from_cuda(e);
+}
+
+nvfp4kv_status fp8bkv_selected_decode(const fp8bkv_cache *cache, const void *q, int32_t batch, int32_t q_len,
+                                      int32_t num_q_heads, const int32_t *block_table, int32_t max_pages_per_seq,
+                                      const int32_t *seq_lens, const int32_t *pages, int32_t budget, float sm_scale,
+                                      void *out, nvfp4kv_dtype out_dtype, void *workspace, size_t workspace_bytes,
+                                      int32_t num_workers, int32_t *dev_status, nvfp4kv_stream_t stream)
+{
+    nvfp4kv_status st = check_fp8(cache);
+    if (st != NVFP4KV_OK)
+        return st;
+    DecodeParams p;
+    st = check_selected(cache->num_kv_heads, cache->num_pages,
+                        static_cast<size_t>(cache->num_pages) * cache->num_kv_heads * kFp8BlockRecord, cache->pool, q,
+                        batch, q_len, num_q_heads, block_table, max_pages_per_seq, seq_lens, pages, budget, sm_scale, out,
+                        out_dtype, workspace, workspace_bytes, num_workers, dev_status, p);
+    if (st != NVFP4KV_OK || batch == 0)
+        return st;
+    p.pool = static_cast<const uint8_t *>(cache->pool);
+    cudaError_t e = launch_decode_selected_fp8_block(p, to_cuda(stream));
+    if (e == cudaSuccess)
+        e = launch_merge(p, to_cuda(stream));
+    return from_cuda(e);
+}
+
+int64_t fp8bkv_cache_bytes(int32_t num_pages, int32_t num_kv_heads, int32_t page_size, int32_t head_dim)
+{
+    if (num_pages < 0 || num_kv_heads < 0 || page_size != kPageSize || head_dim != kHeadDim)
+        return -1;
+    return static_cast<int64_t>(num_pages) * num_kv_heads * kFp8BlockRecord;
 }
 
 int64_t nvfp4kv_cache_bytes(int32_t num_pages, int32_t num_kv_heads, int32_t page_size, int32_t head_dim)

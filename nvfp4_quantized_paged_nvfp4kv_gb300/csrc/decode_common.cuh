@@ -44,11 +44,11 @@ __device__ __forceinline__ int clamp_len(int L, int max_len)
 constexpr int kPrefixScratch = 32;
 static_assert(kDecodeWarps <= kPrefixScratch, "build_prefix takes one scratch slot per warp");
 
-// prefix[b] = sum over b' < b of hkv * ceil(len_b' / 16), for b in [0, batch].
-// Whole CTA; blockDim.x a multiple of 32, at most 32 warps; scratch holds
-// kPrefixScratch slots and must not overlap prefix.
-__device__ __forceinline__ void build_prefix(const int32_t *seq_lens, int batch, int hkv, int max_len,
-                                             int32_t *prefix, int32_t *scratch, int32_t *dev_status)
+// prefix[b] = sum over b' < b of count(b'), for b in [0, batch].  Whole CTA;
+// blockDim.x a multiple of 32, at most 32 warps; scratch holds kPrefixScratch
+// slots and must not overlap prefix.
+template <class Count>
+__device__ __forceinline__ void build_prefix_of(Count count, int batch, int32_t *prefix, int32_t *scratch)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int nwarps = blockDim.x >> 5;
@@ -56,14 +56,8 @@ __device__ __forceinline__ void build_prefix(const int32_t *seq_lens, int batch,
     for (int base = 0; base < batch; base += blockDim.x) {
         const int b = base + threadIdx.x;
         int v = 0;
-        if (b < batch) {
-            int L = seq_lens[b];
-            if (L < 0 || L > max_len) {
-                report(dev_status, NVFP4KV_DEV_BAD_LEN);
-                L = clamp_len(L, max_len);
-            }
-            v = hkv * ((L + kPageSize - 1) / kPageSize);
-        }
+        if (b < batch)
+            v = count(b);
         int x = v;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -89,6 +83,38 @@ __device__ __forceinline__ void build_prefix(const int32_t *seq_lens, int batch,
     if (threadIdx.x == 0)
         prefix[batch] = carry;
     __syncthreads();
+}
+
+// The same of hkv * ceil(len_b / 16).
+__device__ __forceinline__ void build_prefix(const int32_t *seq_lens, int batch, int hkv, int max_len,
+                                             int32_t *prefix, int32_t *scratch, int32_t *dev_status)
+{
+    build_prefix_of(
+        [=](int b) {
+            int L = seq_lens[b];
+            if (L < 0 || L > max_len) {
+                report(dev_status, NVFP4KV_DEV_BAD_LEN);
+                L = clamp_len(L, max_len);
+            }
+            return hkv * ((L + kPageSize - 1) / kPageSize);
+        },
+        batch, prefix, scratch);
+}
+
+// Attention over listed pages: the "sequences" of the work split are the
+// batch * q_len query tokens, row = sequence * q_len + token.  Tokens that row
+// sees (its sequence's last q_len positions are the query tokens) ...
+__device__ __forceinline__ int selected_row_len(const DecodeParams &p, int row)
+{
+    const int b = row / p.sel_q_len, t = row - b * p.sel_q_len;
+    const int n = clamp_len(__ldg(p.seq_lens + b), p.max_pages * kPageSize) - p.sel_q_len + t + 1;
+    return n > 0 ? n : 0;
+}
+
+// ... and the pages listed for each of its kv heads: all of them, or the budget.
+__device__ __forceinline__ int selected_row_pages(const DecodeParams &p, int row)
+{
+    return min(p.budget, (selected_row_len(p, row) + kPageSize - 1) / kPageSize);
 }
 
 // Largest b with prefix[b] <= j, for 0 <= j < prefix[batch].
@@ -150,6 +176,7 @@ struct LaneOffsets {
 struct Nvfp4Format {
     static constexpr int kStages = 5;
     static constexpr int kRecord = 2304;
+    static constexpr bool kPageScales = false;   // (scales beside the values, not one for the whole record)
 
     // x as left by divide_by_tensor_scale, whose code flip comes with it
     __device__ static __forceinline__ void write_block(uint8_t *rec, bool is_v, int tok, int blk,
@@ -251,6 +278,7 @@ struct Nvfp4Format {
 struct Fp8Format {
     static constexpr int kStages = 3;
     static constexpr int kRecord = 4096;
+    static constexpr bool kPageScales = false;
 
     // (the FP8 cache has no tensor scale: x is the row itself, flip kCodeFlip)
     __device__ static __forceinline__ void write_block(uint8_t *rec, bool is_v, int tok, int blk,
@@ -322,6 +350,14 @@ struct Fp8Format {
     }
 };
 
+// FP8 with a scale for each page-head of K and of V: the FP8 record and behind
+// it the two scales.  A code is exact in fp16 whatever its page's scale; the
+// scales go to the fp32 scores and to the fp32 sum of a page's products.
+struct Fp8BlockFormat : Fp8Format {
+    static constexpr int kRecord = kFp8BlockRecord;
+    static constexpr bool kPageScales = true;
+};
+
 template <class Fmt>
 __host__ __device__ constexpr size_t decode_smem_fixed()
 {
@@ -329,10 +365,12 @@ __host__ __device__ constexpr size_t decode_smem_fixed()
            kPrefixScratch * sizeof(int32_t);
 }
 
-template <class Fmt>
+// (page lists: beside each ring stage the number of tokens of its page that count)
+template <class Fmt, bool kSelected = false>
 size_t decode_smem_bytes(int batch)
 {
-    return decode_smem_fixed<Fmt>() + static_cast<size_t>(batch + 1) * sizeof(int32_t);
+    return decode_smem_fixed<Fmt>() + (kSelected ? kDecodeWarps * Fmt::kStages * sizeof(int32_t) : 0) +
+           static_cast<size_t>(batch + 1) * sizeof(int32_t);
 }
 
 // one CTA per SM: the staging rings of all its warps plus the largest prefix table
@@ -340,6 +378,9 @@ static_assert(decode_smem_fixed<Nvfp4Format>() + (kMaxBatch + 1) * sizeof(int32_
               "NVFP4 decode shared memory");
 static_assert(decode_smem_fixed<Fp8Format>() + (kMaxBatch + 1) * sizeof(int32_t) <= 227 * 1024,
               "FP8 decode shared memory");
+static_assert(decode_smem_fixed<Fp8BlockFormat>() + kDecodeWarps * Fp8BlockFormat::kStages * sizeof(int32_t) +
+                      (kMaxBatch + 1) * sizeof(int32_t) <= 227 * 1024,
+              "block-scaled FP8 decode shared memory");
 
 // ---- the decode kernel -------------------------------------------------------
 
@@ -355,9 +396,13 @@ __device__ __forceinline__ size_t out_row(const DecodeParams &p, int b, int hp, 
 // of one kv head ("virtual heads" hkv * row_groups per sequence), numbered
 // with the row group innermost so that the row groups of a kv head read the
 // same pages close together in time.
-template <class Fmt, bool kMulti = false>
+// kSelected: attention over listed pages.  A "sequence" is one query token, a
+// segment's pages are the entries of its list; they come from the kernel
+// before, so nothing of them is read ahead of the wait.
+template <class Fmt, bool kMulti = false, bool kSelected = false>
 __global__ void __launch_bounds__(kDecodeWarps * 32, kDecodeCtasPerSm) decode_kernel(const __grid_constant__ DecodeParams p)
 {
+    static_assert(!(kMulti && kSelected), "rows with page lists are taken one token a segment");
     extern __shared__ __align__(16) uint8_t smem_raw[];
     const uint32_t raw_addr = smem_addr(smem_raw);
     uint8_t *smem = smem_raw + ((128u - (raw_addr & 127u)) & 127u);
@@ -366,7 +411,9 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, kDecodeCtasPerSm) decode_ke
     uint8_t *data_base = smem;
     uint64_t *bars = reinterpret_cast<uint64_t *>(data_base + kDecodeWarps * S * R);
     int32_t *scratch = reinterpret_cast<int32_t *>(bars + kDecodeWarps * S);
-    int32_t *prefix = scratch + kPrefixScratch;
+    int32_t *prefix = scratch + kPrefixScratch + (kSelected ? kDecodeWarps * S : 0);
+    // tokens of the page in each stage of this warp's ring that count
+    volatile int32_t *counted = scratch + kPrefixScratch + (threadIdx.x >> 5) * S;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int gid = lane >> 2, tig = lane & 3;
@@ -388,8 +435,27 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, kDecodeCtasPerSm) decode_ke
     // only after the wait.
     const int max_len = p.max_pages * kPageSize;
     const int nseg = kMulti ? p.hkv * p.row_groups : p.hkv;   // segments per sequence
-    build_prefix(p.seq_lens, p.batch, nseg, max_len, prefix, scratch,
-                 blockIdx.x == 0 ? p.dev_status : nullptr);
+    if constexpr (kSelected) {
+        build_prefix_of(
+            [&](int row) {
+                if (blockIdx.x == 0 && row % p.sel_q_len == 0) {
+                    const int L = __ldg(p.seq_lens + row / p.sel_q_len);
+                    if (L < 0 || L > max_len)
+                        report(p.dev_status, NVFP4KV_DEV_BAD_LEN);
+                }
+                return nseg * selected_row_pages(p, row);
+            },
+            p.batch, prefix, scratch);
+    } else {
+        build_prefix(p.seq_lens, p.batch, nseg, max_len, prefix, scratch,
+                     blockIdx.x == 0 ? p.dev_status : nullptr);
+    }
+    auto len_of = [&](int b) {
+        if constexpr (kSelected)
+            return selected_row_len(p, b);
+        else
+            return clamp_len(p.seq_lens[b], max_len);
+    };
 
     const int w = blockIdx.x * kDecodeWarps + warp;
     const long long T = prefix[p.batch];
@@ -415,9 +481,28 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, kDecodeCtasPerSm) decode_ke
     int win = lo;
     int nxt_phys = 0, nxt_h = 0;
     uint32_t cur_rec = 0;
+    int cur_counted = 0, nxt_counted = 0;        // (page lists: tokens of the entry that count)
     auto lookup = [&](int j, int &phys, int &hh) {
         phys = 0;
         hh = 0;
+        if constexpr (kSelected) {
+            nxt_counted = 0;
+            if (j < hi) {
+                const int row = find_seq(prefix, p.batch, j);
+                const int r = j - prefix[row];
+                const int n = (prefix[row + 1] - prefix[row]) / nseg;
+                hh = r / n;
+                const int page = __ldcg(p.sel_pages + (static_cast<size_t>(row) * p.hkv + hh) * p.budget + (r - hh * n));
+                const int L = selected_row_len(p, row);
+                if (page >= 0 && page < (L + kPageSize - 1) / kPageSize) {
+                    nxt_counted = min(L - page * kPageSize, kPageSize);
+                    phys = __ldg(p.block_table + static_cast<size_t>(row / p.sel_q_len) * p.max_pages + page);
+                } else {
+                    report(p.dev_status, NVFP4KV_DEV_BAD_PAGE);      // (no token of it counts)
+                }
+            }
+            return;
+        }
         if (j < hi) {
             const int b = find_seq(prefix, p.batch, j);
             const int r = j - prefix[b];
@@ -436,9 +521,12 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, kDecodeCtasPerSm) decode_ke
         }
         return static_cast<uint32_t>(phys) * static_cast<uint32_t>(p.hkv) + static_cast<uint32_t>(hh);
     };
+    if constexpr (kSelected)
+        pdl_wait();                              // the lists come from the kernel before
     {
         int phys, hh;
         lookup(win + lane, phys, hh);
+        cur_counted = nxt_counted;
         lookup(win + 32 + lane, nxt_phys, nxt_h);
         cur_rec = record_of(phys, hh, win + lane);
     }
@@ -450,9 +538,14 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, kDecodeCtasPerSm) decode_ke
             win += 32;
             rel -= 32;
             cur_rec = record_of(nxt_phys, nxt_h, win + lane);
+            cur_counted = nxt_counted;
             lookup(win + 32 + lane, nxt_phys, nxt_h);
         }
         const uint32_t z = __shfl_sync(kFullMask, cur_rec, rel);
+        if constexpr (kSelected) {
+            if (lane == rel)
+                counted[st] = cur_counted;       // (read a __syncwarp and more later)
+        }
         if (lane == 0) {
             const uint32_t bar = wbar + 8 * st;
             mbar_arrive_expect_tx(bar, R);
@@ -465,10 +558,11 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, kDecodeCtasPerSm) decode_ke
     int n = (prefix[b + 1] - prefix[b]) / nseg;
     int h = (lo - prefix[b]) / n;                 // segment (kv head, or row group) in the sequence
     int pg = lo - prefix[b] - h * n;
-    int L = clamp_len(p.seq_lens[b], max_len);
+    int L = len_of(b);
     int seg_begin = prefix[b] + h * n;
 
-    pdl_wait();
+    if constexpr (!kSelected)
+        pdl_wait();
     // The first two records go out at once, the rest of the ring once the
     // first has landed: when every warp asks for its whole ring together,
     // each warp's first record would arrive late in that burst.  With the
@@ -519,6 +613,7 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, kDecodeCtasPerSm) decode_ke
         issue(x, x - lo);
 
     uint32_t qf[16];
+    float inv0 = 1.f, inv1 = 1.f;                // (page scales) factors of the scores of rows 2tig, 2tig + 1
     float m0, m1, l0, l1;
     float oacc[8][4];
     const int g = p.group;
@@ -541,7 +636,36 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, kDecodeCtasPerSm) decode_ke
             limA = rA < p.rows ? L - p.q_len + rA / g + 1 : 0;
             limB = rB < p.rows ? L - p.q_len + rB / g + 1 : 0;
         }
-        if (has_row) {
+        if constexpr (Fmt::kPageScales) {
+            // A page's scale may be anything, and with it the queries that go with
+            // it: each row times the power of two that puts its largest element in
+            // [2^14, 2^15), which makes bf16 -> f16 exact but for elements under
+            // 2^-28 of that; its inverse and sm_scale go to the fp32 scores.
+            uint32_t w[16];
+            float top = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint4 r = has_row ? __ldg(reinterpret_cast<const uint4 *>(qsrc + 32 * tig) + i) : make_uint4(0, 0, 0, 0);
+                w[4 * i] = r.x;
+                w[4 * i + 1] = r.y;
+                w[4 * i + 2] = r.z;
+                w[4 * i + 3] = r.w;
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                top = fmaxf(top, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xffff0000u))));
+            top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 2));
+            // (the exponents of 2^up and 2^-up both stay within fp32's)
+            const int up = top > 0.f ? max(-112, min(126, 127 + 14 - static_cast<int>(__float_as_uint(top) >> 23))) : 0;
+            const float by = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                qf[i] = pack_f16x2(__uint_as_float(w[i] << 16) * by, __uint_as_float(w[i] & 0xffff0000u) * by);
+            const float inv = p.qscale * __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+            inv0 = __shfl_sync(kFullMask, inv, 8 * tig);
+            inv1 = __shfl_sync(kFullMask, inv, 8 * tig + 4);
+        } else if (has_row) {
             const float qsc = p.hs.per_head ? p.qs[kMulti ? hp : h] : p.qscale;
             const uint4 *qrow = reinterpret_cast<const uint4 *>(qsrc + 32 * tig);
 #pragma unroll
@@ -642,7 +766,9 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, kDecodeCtasPerSm) decode_ke
     }
 
     // One step handles one page-head, or two of the same segment.
-    auto step = [&](auto npc, uint32_t rec0, uint32_t rec1, int last_valid, int pos0) {
+    // Tokens that count: all of a first of two, last_valid of the last one; with
+    // page lists each has its own number.
+    auto step = [&](auto npc, uint32_t rec0, uint32_t rec1, int first_valid, int last_valid, int pos0) {
         constexpr int NP = decltype(npc)::value;
         // S^T = K . Q^T
         // (two accumulators per page-head halve the dependent MMA chain)
@@ -660,8 +786,27 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, kDecodeCtasPerSm) decode_ke
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 sc[q][e] += sd[e];
+            if constexpr (Fmt::kPageScales) {
+                const float ks = __uint_as_float(lds32((q == 0 ? rec0 : rec1) + kFp8Record));
+                const float f0 = ks * inv0, f1 = ks * inv1;
+                sc[q][0] *= f0;
+                sc[q][1] *= f1;
+                sc[q][2] *= f0;
+                sc[q][3] *= f1;
+            }
         }
-        if constexpr (kMulti) {
+        if constexpr (kSelected) {
+#pragma unroll
+            for (int q = 0; q < NP; ++q) {
+                const int valid = q == NP - 1 ? last_valid : first_valid;
+                if (valid < kPageSize) {
+                    if (gid >= valid)
+                        sc[q][0] = sc[q][1] = -INFINITY;
+                    if (gid + 8 >= valid)
+                        sc[q][2] = sc[q][3] = -INFINITY;
+                }
+            }
+        } else if constexpr (kMulti) {
             // key pos0 + 16q + token against each column's visible count
             if (pos0 + NP * kPageSize > min(limA, limB)) {
 #pragma unroll
@@ -719,7 +864,7 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, kDecodeCtasPerSm) decode_ke
         for (int q = 0; q < NP; ++q) {
             float p0 = fast_exp2(sc[q][0] - m0), p1 = fast_exp2(sc[q][1] - m1);
             float p2 = fast_exp2(sc[q][2] - m0), p3 = fast_exp2(sc[q][3] - m1);
-            if constexpr (kMulti) {
+            if constexpr (kMulti || kSelected) {
                 // a masked score against a maximum that is still -inf
                 p0 = sc[q][0] == -INFINITY ? 0.f : p0;
                 p1 = sc[q][1] == -INFINITY ? 0.f : p1;
@@ -737,10 +882,24 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, kDecodeCtasPerSm) decode_ke
 #pragma unroll
         for (int q = 0; q < NP; ++q) {
             uint32_t va[8][4];
-            Fmt::load_v(q == 0 ? rec0 : rec1, off, tig, q == NP - 1 ? last_valid : kPageSize, va);
+            const int valid = q == NP - 1 ? last_valid : (kSelected ? first_valid : kPageSize);
+            Fmt::load_v(q == 0 ? rec0 : rec1, off, tig, valid, va);
+            if constexpr (Fmt::kPageScales) {
+                // (a page of which nothing counts: its scale may be anything)
+                const float vs = valid > 0 ? __uint_as_float(lds32((q == 0 ? rec0 : rec1) + kFp8Record + 4)) : 0.f;
 #pragma unroll
-            for (int jj = 0; jj < 8; ++jj)
-                mma_f16_16816(oacc[jj], va[jj][0], va[jj][1], va[jj][2], va[jj][3], pb[q][0], pb[q][1]);
+                for (int jj = 0; jj < 8; ++jj) {
+                    float o[4] = {0.f, 0.f, 0.f, 0.f};
+                    mma_f16_16816(o, va[jj][0], va[jj][1], va[jj][2], va[jj][3], pb[q][0], pb[q][1]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        oacc[jj][e] = fmaf(o[e], vs, oacc[jj][e]);
+                }
+            } else {
+#pragma unroll
+                for (int jj = 0; jj < 8; ++jj)
+                    mma_f16_16816(oacc[jj], va[jj][0], va[jj][1], va[jj][2], va[jj][3], pb[q][0], pb[q][1]);
+            }
         }
     };
 
@@ -778,11 +937,16 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, kDecodeCtasPerSm) decode_ke
             return;
         }
         const int plast = pg + np - 1;
-        const int last_valid = (plast == n - 1) ? (L - plast * kPageSize) : kPageSize;
+        int first_valid = kPageSize, last_valid = (plast == n - 1) ? (L - plast * kPageSize) : kPageSize;
+        if constexpr (kSelected) {
+            __syncwarp();
+            first_valid = counted[st];
+            last_valid = np == 2 ? counted[st1] : first_valid;
+        }
         if (np == 2)
-            step(std::integral_constant<int, 2>(), wdata + st * R, wdata + st1 * R, last_valid, pg * kPageSize);
+            step(std::integral_constant<int, 2>(), wdata + st * R, wdata + st1 * R, first_valid, last_valid, pg * kPageSize);
         else
-            step(std::integral_constant<int, 1>(), wdata + st * R, wdata + st * R, last_valid, pg * kPageSize);
+            step(std::integral_constant<int, 1>(), wdata + st * R, wdata + st * R, first_valid, last_valid, pg * kPageSize);
 
         __syncwarp();
         if (j + S < hi)
@@ -808,7 +972,7 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, kDecodeCtasPerSm) decode_ke
                         ++b;
                     } while (prefix[b + 1] == prefix[b]);
                     n = (prefix[b + 1] - prefix[b]) / nseg;
-                    L = clamp_len(p.seq_lens[b], max_len);
+                    L = len_of(b);
                 }
                 seg_begin = prefix[b] + h * n;
                 start_segment();

@@ -1,0 +1,23 @@
+// Paged decode over the block-scaled FP8 cache: instantiations and launcher.
+#include "decode_common.cuh"
+
+namespace nvfp4kv {
+
+template <bool kMulti>
+static cudaError_t launch_decode(const DecodeParams &p, cudaStream_t s)
+{
+    const size_t smem = decode_smem_bytes<Fp8BlockFormat>(p.batch);
+    cudaError_t e = cudaFuncSetAttribute(decode_kernel<Fp8BlockFormat, kMulti>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess)
+        return e;
+    const int grid = (p.num_workers + kDecodeWarps - 1) / kDecodeWarps;
+    return launch_pdl(decode_kernel<Fp8BlockFormat, kMulti>, dim3(grid), dim3(kDecodeWarps * 32), smem, s, p);
+}
+
+cudaError_t launch_decode_fp8_block(const DecodeParams &p, cudaStream_t s)
+{
+    return p.q_len > 1 ? launch_decode<true>(p, s) : launch_decode<false>(p, s);
+}
+
+} // namespace nvfp4kv

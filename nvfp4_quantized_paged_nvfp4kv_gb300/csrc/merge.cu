@@ -24,7 +24,10 @@ __device__ __forceinline__ void merge_segment_row(const DecodeParams &p, int32_t
     int32_t *scratch = msmem;
     int32_t *prefix = msmem + kPrefixScratch;
     const int nseg = p.hkv * p.row_groups;       // segments per sequence (row groups of kv heads)
-    build_prefix(p.seq_lens, p.batch, nseg, p.max_pages * kPageSize, prefix, scratch, nullptr);
+    if (p.sel_pages != nullptr)
+        build_prefix_of([&](int row) { return nseg * selected_row_pages(p, row); }, p.batch, prefix, scratch);
+    else
+        build_prefix(p.seq_lens, p.batch, nseg, p.max_pages * kPageSize, prefix, scratch, nullptr);
 
     const int b = blockIdx.x / nseg;
     const int h = blockIdx.x - b * nseg;

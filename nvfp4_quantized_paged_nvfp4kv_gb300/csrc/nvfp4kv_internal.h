@@ -18,6 +18,7 @@ constexpr int kDecodeCtasPerSm = 1;          // occupancy the default worker cou
 constexpr int kPartialFloats = kMaxGroup * kHeadDim + 2 * kMaxGroup;  // O[8][128], m[8], l[8]
 constexpr int kNvfp4Record = 2304;           // bytes of an NVFP4 page-head record
 constexpr int kFp8Record = 4096;             // bytes of an FP8 page-head record
+constexpr int kFp8BlockRecord = FP8BKV_RECORD_BYTES;  // ... of one with its scales of K and V behind it
 constexpr int kMaxBatch = NVFP4KV_MAX_BATCH; // prefix table lives in shared memory
 constexpr int kMaxScaledHeads = NVFP4KV_MAX_SCALED_KV_HEADS;
 // Polls before a wait for staged data (or for another role of the CTA) gives
@@ -73,6 +74,11 @@ struct DecodeParams {
     HeadScales hs;
     float qs[kMaxScaledHeads];
     uint32_t wait_limit;         // polls before a wait gives up (kWaitLimit by default)
+    // attention over listed pages: `batch` counts query tokens, sel_q_len of a
+    // sequence; sel_pages [batch][hkv][budget] pages of the sequence
+    const int32_t *sel_pages;
+    int budget;
+    int sel_q_len;
 };
 
 struct QuantParams {
@@ -141,6 +147,77 @@ struct ExtendParams {
     CUtensorMap tm_v_prefix;
     CUtensorMap tm_k_chunk;
     CUtensorMap tm_v_chunk;
+};
+
+// New rows into the block-scaled FP8 cache.
+struct BlockAppendParams {
+    const void *k_new;           // [num_tokens][hkv][128]
+    const void *v_new;
+    const int32_t *q_indptr;     // [batch + 1]: rows of each sequence
+    const int32_t *block_table;  // [batch][max_pages]
+    const int32_t *seq_lens;     // [batch], the new tokens included
+    uint8_t *pool;               // page-head records [num_pages][hkv][kFp8BlockRecord]
+    int32_t *dev_status;
+    int num_tokens;
+    int batch;
+    int hkv;
+    int max_pages;
+    int num_pages;
+    int in_bf16;
+};
+
+// Cached rows of the block-scaled FP8 cache, read back.
+struct BlockReadParams {
+    const uint8_t *pool;
+    const int32_t *block_table;
+    const int32_t *lens;         // [batch]
+    const int32_t *kv_indptr;    // [batch] first output row of each sequence
+    void *k_out;                 // [rows][hkv][128] of out_dtype
+    void *v_out;
+    int32_t *dev_status;
+    int batch;
+    int hkv;
+    int max_pages;
+    int num_pages;
+    int out_dtype;               // nvfp4kv_dtype
+};
+
+// Bounds of the pages' keys.
+struct BoundsParams {
+    const uint8_t *pool;
+    const int32_t *block_table;
+    const int32_t *from_lens;    // [batch] or null: 0
+    const int32_t *seq_lens;     // [batch]
+    int8_t *bounds;              // [num_pages][hkv][2][128]: least, largest
+    float *steps;                // [num_pages][hkv]
+    int32_t *dev_status;
+    int batch;
+    int hkv;
+    int max_pages;
+    int num_pages;
+};
+
+// The pages that each query token looks at.
+struct SelectParams {
+    const int8_t *bounds;
+    const float *steps;
+    const uint16_t *q;           // bf16 [batch][q_len][hq][128]
+    const int32_t *block_table;
+    const int32_t *seq_lens;
+    int32_t *pages;              // [batch][q_len][hkv][budget]
+    float *scores;               // [batch][q_len][hkv][score_stride]
+    int32_t *dev_status;
+    int batch;
+    int q_len;
+    int hq;
+    int hkv;
+    int group;
+    int max_pages;
+    int num_pages;
+    int budget;
+    int first;                   // pages always taken, at the beginning
+    int last;                    // ... and at the end
+    int score_stride;            // max_pages rounded up to tiles
 };
 
 // Chunk attention over the paged NVFP4 cache.
@@ -268,7 +345,16 @@ cudaError_t launch_quantize_append_fp8(const QuantParams &p, cudaStream_t s);
 cudaError_t launch_decode_nvfp4(const DecodeParams &p, cudaStream_t s);
 cudaError_t launch_decode_nvfp4_multi(const DecodeParams &p, cudaStream_t s);
 cudaError_t launch_decode_fp8(const DecodeParams &p, cudaStream_t s);
+cudaError_t launch_decode_fp8_block(const DecodeParams &p, cudaStream_t s);         // (p.q_len > 1: several tokens)
+cudaError_t launch_decode_selected_nvfp4(const DecodeParams &p, cudaStream_t s);
+cudaError_t launch_decode_selected_fp8_block(const DecodeParams &p, cudaStream_t s);
 cudaError_t launch_merge(const DecodeParams &p, cudaStream_t s);
+cudaError_t launch_block_append(const BlockAppendParams &p, cudaStream_t s);
+cudaError_t launch_block_read(const BlockReadParams &p, cudaStream_t s);
+cudaError_t launch_page_bounds_nvfp4(const BoundsParams &p, cudaStream_t s);
+cudaError_t launch_page_bounds_fp8_block(const BoundsParams &p, cudaStream_t s);
+int score_row_stride(int max_pages);                                               // floats of a row of scores
+cudaError_t launch_select_pages(const SelectParams &p, cudaStream_t s);
 cudaError_t launch_dequant_prefix_fp8(const PrefixParams &p, cudaStream_t s);
 ExtendShape paged_extend_shape(int64_t q_rows, int64_t max_q_len, int64_t batch, int64_t hkv, int64_t group,
                                int64_t max_pages, int64_t window);
