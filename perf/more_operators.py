@@ -371,8 +371,6 @@ def prepare(c, seed):
             s["page_bounds"] = nv.PageBounds(s["bounds"], s["steps"])
         if op in ("decode8", "sparse"):
             s["workspace"] = nv.new_workspace()
-        if op == "sparse":
-            s["scores"] = nv.new_select_workspace(b, c["q_len"], hkv, s["table"].shape[1])
     return s
 
 
@@ -396,7 +394,7 @@ def _own(s):
         call = nv.nvfp4kv_page_bounds if s["cache"] == 4 else nv.fp8bkv_page_bounds
         call(s["kv"], s["page_bounds"], s["table"], s["lens"], from_lens=s["begin"], dev_status=s["status"])
         return dict(bounds=s["bounds"], steps=s["steps"])
-    nv.nvfp4kv_select_pages(s["page_bounds"], s["q"], s["table"], s["lens"], s["pages"], s["scores"], first_pages=s["first"],
+    nv.nvfp4kv_select_pages(s["page_bounds"], s["q"], s["table"], s["lens"], s["pages"], first_pages=s["first"],
                             last_pages=s["last"], dev_status=s["status"])
     call = nv.nvfp4kv_selected_decode if s["cache"] == 4 else nv.fp8bkv_selected_decode
     call(s["kv"], s["q"], s["table"], s["lens"], s["pages"], s["out"], s["workspace"], dev_status=s["status"])
