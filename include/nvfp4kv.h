@@ -729,25 +729,18 @@ nvfp4kv_status fp8bkv_page_bounds(const fp8bkv_cache *cache, const nvfp4kv_bound
  *   pages      int32 [batch][q_len][num_kv_heads][budget]: the selected pages'
  *              places in the sequence (indices into its row of the block table),
  *              ascending, -1 behind the last one
- *   workspace  device scratch of at least the size below, 256-byte aligned, not
- *              initialised; two calls in flight at once must not share it
- * first_pages + last_pages at most budget; max_pages_per_seq at most 2^20;
- * batch * q_len at most NVFP4KV_MAX_BATCH.  A length outside [0,
+ * first_pages + last_pages at most budget; max_pages_per_seq at most
+ * NVFP4KV_MAX_SELECT_PAGES (the scores stay in shared memory); batch * q_len at
+ * most NVFP4KV_MAX_BATCH.  A length outside [0,
  * max_pages_per_seq * 16] is clamped and sets NVFP4KV_DEV_BAD_LEN; the score of a
  * page id outside [0, num_pages) is that of page 0 and sets
  * NVFP4KV_DEV_BAD_PAGE.  Non-finite queries give an unspecified selection (of
- * pages there are).  pages and the workspace overlap nothing else
- * (NVFP4KV_ERR_INVALID_ARG). */
+ * pages there are).  pages overlaps nothing else (NVFP4KV_ERR_INVALID_ARG). */
+#define NVFP4KV_MAX_SELECT_PAGES 65536
 nvfp4kv_status nvfp4kv_select_pages(const nvfp4kv_bounds *bounds, const void *q, int32_t batch, int32_t q_len,
                                     int32_t num_q_heads, const int32_t *block_table, int32_t max_pages_per_seq,
                                     const int32_t *seq_lens, int32_t budget, int32_t first_pages, int32_t last_pages,
-                                    int32_t *pages, void *workspace, size_t workspace_bytes, int32_t *dev_status,
-                                    nvfp4kv_stream_t stream);
-
-/* Bytes of workspace that nvfp4kv_select_pages needs (a library utility; host
- * only; 0 for sizes that the call refuses). */
-size_t nvfp4kv_select_pages_workspace_size(int32_t batch, int32_t q_len, int32_t num_kv_heads,
-                                           int32_t max_pages_per_seq);
+                                    int32_t *pages, int32_t *dev_status, nvfp4kv_stream_t stream);
 
 /* Decode attention over listed pages (a library utility): query token t of
  * sequence b, kv head h attends over those of its first n = seq_lens[b] - q_len +

@@ -34,8 +34,7 @@ Functions carry the C names and take torch tensors:
     fp8bkv_paged_decode(cache, q, block_table, seq_lens, out, workspace, ...)
   attention over selected pages (either cache)
     nvfp4kv_page_bounds / fp8bkv_page_bounds(cache, bounds, block_table, seq_lens, from_lens=None, ...)
-    nvfp4kv_select_pages(bounds, q, block_table, seq_lens, pages, workspace, first_pages=1, last_pages=1, ...)
-    nvfp4kv_select_pages_workspace_size(batch, q_len, num_kv_heads, max_pages), new_select_workspace(...)
+    nvfp4kv_select_pages(bounds, q, block_table, seq_lens, pages, first_pages=1, last_pages=1, ...)
     nvfp4kv_selected_decode / fp8bkv_selected_decode(cache, q, block_table, seq_lens, pages, out, workspace, ...)
   utilities
     nvfp4kv_read_device_status(dev_status, stream=None)
@@ -189,8 +188,7 @@ def load(build_if_missing: bool = True):
             "fp8bkv_page_bounds": (_st, [ctypes.POINTER(_Fp8BlockCache), ctypes.POINTER(_Bounds), _vp, _i32, _vp, _vp,
                                          _i32, _vp, _vp]),
             "nvfp4kv_select_pages": (_st, [ctypes.POINTER(_Bounds), _vp, _i32, _i32, _i32, _vp, _i32, _vp, _i32, _i32,
-                                           _i32, _vp, _vp, ctypes.c_size_t, _vp, _vp]),
-            "nvfp4kv_select_pages_workspace_size": (ctypes.c_size_t, [_i32] * 4),
+                                           _i32, _vp, _vp, _vp]),
             "nvfp4kv_selected_decode": (_st, [ctypes.POINTER(_Nvfp4Cache), _vp, _i32, _i32, _i32, _vp, _i32, _vp, _vp,
                                               _i32, ctypes.c_float, _vp, _st, _vp, ctypes.c_size_t, _i32, _vp, _vp]),
             "fp8bkv_selected_decode": (_st, [ctypes.POINTER(_Fp8BlockCache), _vp, _i32, _i32, _i32, _vp, _i32, _vp, _vp,
@@ -810,19 +808,13 @@ def fp8bkv_page_bounds(cache: FP8BlockCache, bounds: PageBounds, block_table, se
     _page_bounds("fp8bkv_page_bounds", FP8BlockCache, cache, bounds, block_table, seq_lens, from_lens, dev_status, stream)
 
 
-def nvfp4kv_select_pages_workspace_size(batch, q_len, num_kv_heads, max_pages_per_seq) -> int:
-    return int(load().nvfp4kv_select_pages_workspace_size(
-        _int32(batch, "batch"), _int32(q_len, "q_len"), _int32(num_kv_heads, "num_kv_heads"),
-        _int32(max_pages_per_seq, "max_pages_per_seq")))
-
-
-def nvfp4kv_select_pages(bounds: PageBounds, q, block_table, seq_lens, pages, workspace, first_pages=1, last_pages=1,
+def nvfp4kv_select_pages(bounds: PageBounds, q, block_table, seq_lens, pages, first_pages=1, last_pages=1,
                          dev_status=None, stream=None) -> None:
     """Select pages for each query token and kv head: the first first_pages and
     the last last_pages that the token sees and the best of the others by the
     score of their bounds, into pages int32 [B][q_len][Hkv][budget] (ascending
     places in the sequence, -1 behind the last; [B][Hkv][budget] where q is
-    [B][Hq][128]).  workspace: new_select_workspace."""
+    [B][Hq][128])."""
     import torch
     dev = _current_device()
     B, max_pages = block_table.shape
@@ -834,11 +826,10 @@ def nvfp4kv_select_pages(bounds: PageBounds, q, block_table, seq_lens, pages, wo
              (pages, "pages", shape if pages.dim() == 4 or q.dim() == 4 else (B, bounds.num_kv_heads, budget)),
              (block_table, "block_table", (B, max_pages)), (seq_lens, "seq_lens", (B,)),
              (dev_status, "dev_status", (1,)))
-    _tensors(dev, torch.uint8, (workspace, "workspace", (0 if workspace is None else workspace.numel(),)))
     st = load().nvfp4kv_select_pages(
         bounds.c, _ptr(q), B, q_len, heads, _ptr(block_table), max_pages, _ptr(seq_lens), budget,
-        _int32(first_pages, "first_pages"), _int32(last_pages, "last_pages"), _ptr(pages), _ptr(workspace),
-        0 if workspace is None else workspace.numel(), _ptr(dev_status), _stream(stream, dev))
+        _int32(first_pages, "first_pages"), _int32(last_pages, "last_pages"), _ptr(pages), _ptr(dev_status),
+        _stream(stream, dev))
     _check(st, "nvfp4kv_select_pages")
 
 
@@ -942,9 +933,3 @@ def new_extend_workspace(q_rows, max_q_len, batch, num_q_heads, num_kv_heads, ma
                                             window)
     return torch.empty(max(n, 256), dtype=torch.uint8, device=device)
 
-
-def new_select_workspace(batch, q_len, num_kv_heads, max_pages_per_seq, device="cuda"):
-    """A workspace tensor for nvfp4kv_select_pages calls of these sizes."""
-    import torch
-    n = nvfp4kv_select_pages_workspace_size(batch, q_len, num_kv_heads, max_pages_per_seq)
-    return torch.empty(max(n, 256), dtype=torch.uint8, device=device)

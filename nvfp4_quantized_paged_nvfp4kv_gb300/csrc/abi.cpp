@@ -408,7 +408,7 @@ nvfp4kv_status page_bounds(const Cache *cache, size_t record, const nvfp4kv_boun
     return from_cuda(launch(p, to_cuda(stream)));
 }
 
-constexpr int32_t kMaxSelectPages = 1 << 20;
+constexpr int32_t kMaxSelectPages = NVFP4KV_MAX_SELECT_PAGES;
 
 nvfp4kv_status check_query_tokens(int32_t batch, int32_t q_len)
 {
@@ -426,15 +426,16 @@ nvfp4kv_status check_select_sizes(int32_t batch, int32_t q_len, int32_t hkv, int
         return st;
     if (hkv <= 0 || max_pages <= 0)
         return NVFP4KV_ERR_INVALID_ARG;
-    if (max_pages > kMaxSelectPages || static_cast<int64_t>(batch) * q_len * hkv > (int64_t{1} << 31) - 1 ||
-        static_cast<int64_t>(batch) * hkv * ((max_pages + 15) / 16) > (int64_t{1} << 31) - 1)
+    if (max_pages > kMaxSelectPages || static_cast<int64_t>(batch) * q_len * hkv > (int64_t{1} << 27))
         return NVFP4KV_ERR_UNSUPPORTED;
     return NVFP4KV_OK;
 }
 
-size_t select_workspace(int32_t batch, int32_t q_len, int32_t hkv, int32_t max_pages)
+// CTAs a cluster for a decode over listed pages (0: the worker split).
+int cluster_ranks(const DecodeParams &p, bool eight_bits)
 {
-    return 4 * static_cast<size_t>(batch) * q_len * hkv * score_row_stride(max_pages);
+    return cluster_decode_ranks(static_cast<int64_t>(p.batch) * p.hkv, p.budget < p.max_pages ? p.budget : p.max_pages,
+                                eight_bits);
 }
 
 // Decode over listed pages: fills p (except the cache's pool and scales).
@@ -1177,12 +1178,20 @@ nvfp4kv_status fp8bkv_paged_decode(const fp8bkv_cache *cache, const void *q, int
                       seq_lens, sm_scale, out, out_dtype, workspace, workspace_bytes, num_workers, dev_status, p);
     if (st != NVFP4KV_OK || batch == 0)
         return st;
+    p.pool = static_cast<const uint8_t *>(cache->pool);
+    // short sequences: each query token by a cluster of its own
+    const int ranks =
+        num_workers == 0 ? cluster_decode_ranks(static_cast<int64_t>(batch) * q_len * p.hkv, max_pages_per_seq, true) : 0;
+    if (ranks > 0) {
+        p.batch = batch * q_len;
+        p.sel_q_len = q_len;
+        return from_cuda(launch_cluster_decode_fp8_block(p, ranks, to_cuda(stream)));
+    }
     p.q_len = q_len;
     p.rows = p.group * q_len;
     p.row_groups = (p.rows + kMaxGroup - 1) / kMaxGroup;
     if (static_cast<int64_t>(batch) * cache->num_kv_heads * p.row_groups * max_pages_per_seq > (int64_t{1} << 31) - 1)
         return NVFP4KV_ERR_UNSUPPORTED;
-    p.pool = static_cast<const uint8_t *>(cache->pool);
     cudaError_t e = launch_decode_fp8_block(p, to_cuda(stream));
     if (e == cudaSuccess)
         e = launch_merge(p, to_cuda(stream));
@@ -1212,19 +1221,10 @@ nvfp4kv_status fp8bkv_page_bounds(const fp8bkv_cache *cache, const nvfp4kv_bound
                        dev_status, stream, launch_page_bounds_fp8_block);
 }
 
-size_t nvfp4kv_select_pages_workspace_size(int32_t batch, int32_t q_len, int32_t num_kv_heads,
-                                           int32_t max_pages_per_seq)
-{
-    if (check_select_sizes(batch, q_len, num_kv_heads, max_pages_per_seq) != NVFP4KV_OK)
-        return 0;
-    return select_workspace(batch, q_len, num_kv_heads, max_pages_per_seq);
-}
-
 nvfp4kv_status nvfp4kv_select_pages(const nvfp4kv_bounds *bounds, const void *q, int32_t batch, int32_t q_len,
                                     int32_t num_q_heads, const int32_t *block_table, int32_t max_pages_per_seq,
                                     const int32_t *seq_lens, int32_t budget, int32_t first_pages, int32_t last_pages,
-                                    int32_t *pages, void *workspace, size_t workspace_bytes, int32_t *dev_status,
-                                    nvfp4kv_stream_t stream)
+                                    int32_t *pages, int32_t *dev_status, nvfp4kv_stream_t stream)
 {
     nvfp4kv_status st = check_bounds(bounds);
     if (st != NVFP4KV_OK)
@@ -1244,17 +1244,13 @@ nvfp4kv_status nvfp4kv_select_pages(const nvfp4kv_bounds *bounds, const void *q,
         return NVFP4KV_OK;
     if (q == nullptr || !aligned16(q) || pages == nullptr)
         return NVFP4KV_ERR_INVALID_ARG;
-    const size_t need = select_workspace(batch, q_len, hkv, max_pages_per_seq);
-    if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255u) || workspace_bytes < need)
-        return NVFP4KV_ERR_WORKSPACE;
     const size_t rows = static_cast<size_t>(batch) * q_len, heads = heads_of(bounds);
     const Span spans[] = {{bounds->bounds, heads * 2 * kHeadDim, false},
                           {bounds->steps, 4 * heads, false},
                           {q, 2 * rows * num_q_heads * kHeadDim, false},
                           {block_table, 4 * static_cast<size_t>(batch) * max_pages_per_seq, false},
                           {seq_lens, 4 * static_cast<size_t>(batch), false},
-                          {pages, 4 * rows * hkv * static_cast<size_t>(budget), true},
-                          {workspace, need, true}};
+                          {pages, 4 * rows * hkv * static_cast<size_t>(budget), true}};
     if (written_overlap(spans))
         return NVFP4KV_ERR_INVALID_ARG;
     SelectParams p{};
@@ -1264,7 +1260,6 @@ nvfp4kv_status nvfp4kv_select_pages(const nvfp4kv_bounds *bounds, const void *q,
     p.block_table = block_table;
     p.seq_lens = seq_lens;
     p.pages = pages;
-    p.scores = static_cast<float *>(workspace);
     p.dev_status = dev_status;
     p.batch = batch;
     p.q_len = q_len;
@@ -1276,7 +1271,6 @@ nvfp4kv_status nvfp4kv_select_pages(const nvfp4kv_bounds *bounds, const void *q,
     p.budget = budget;
     p.first = first_pages;
     p.last = last_pages;
-    p.score_stride = score_row_stride(max_pages_per_seq);
     return from_cuda(launch_select_pages(p, to_cuda(stream)));
 }
 
@@ -1298,6 +1292,8 @@ nvfp4kv_status nvfp4kv_selected_decode(const nvfp4kv_cache *cache, const void *q
         return st;
     p.pool = static_cast<const uint8_t *>(cache->pool);
     apply_tensor_scale(p, sm_scale, cache);
+    if (const int ranks = num_workers == 0 ? cluster_ranks(p, false) : 0)
+        return from_cuda(launch_cluster_decode_nvfp4(p, ranks, to_cuda(stream)));
     cudaError_t e = launch_decode_selected_nvfp4(p, to_cuda(stream));
     if (e == cudaSuccess)
         e = launch_merge(p, to_cuda(stream));
@@ -1321,6 +1317,8 @@ nvfp4kv_status fp8bkv_selected_decode(const fp8bkv_cache *cache, const void *q, 
     if (st != NVFP4KV_OK || batch == 0)
         return st;
     p.pool = static_cast<const uint8_t *>(cache->pool);
+    if (const int ranks = num_workers == 0 ? cluster_ranks(p, true) : 0)
+        return from_cuda(launch_cluster_decode_fp8_block(p, ranks, to_cuda(stream)));
     cudaError_t e = launch_decode_selected_fp8_block(p, to_cuda(stream));
     if (e == cudaSuccess)
         e = launch_merge(p, to_cuda(stream));

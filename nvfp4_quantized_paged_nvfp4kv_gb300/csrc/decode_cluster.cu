@@ -1,0 +1,322 @@
+// Decode over few pages a query token, listed or all, in one launch: a cluster of
+// CTAs for each (query token, kv head).
+//
+// The worker split of decode_kernel balances any lengths, at the price of
+// partials in the workspace and a second kernel.  Where a query token has few
+// pages -- a page list, or a short sequence -- those fixed costs are most of the
+// time.  Here the 8 warps of each of the cluster's 1 to 8 CTAs take equal runs of
+// the pages (staged and multiplied as in decode_kernel), the warps' softmax
+// states meet in shared memory and the CTAs' in the cluster's:
+//   M = max_w m_w,  o = sum_w 2^(m_w - M) O_w / sum_w 2^(m_w - M) l_w.
+// No partial goes to memory.  Two CTAs to an SM, so that one's merge runs beside
+// the other's loads.
+#include "cluster.cuh"
+#include "decode_common.cuh"
+
+namespace nvfp4kv {
+namespace {
+
+constexpr int kClWarps = 8, kClThreads = 32 * kClWarps;
+constexpr int kRowFloats = kHeadDim + 4;         // (rows 2tig of four lanes in different banks)
+constexpr int kStateFloats = kMaxGroup * kRowFloats + 2 * kMaxGroup;
+
+template <class Fmt>
+constexpr int kClStages = Fmt::kRecord > 4000 ? 3 : 6;
+
+template <class Fmt>
+constexpr size_t kClSmem = 128 + static_cast<size_t>(kClWarps) * kClStages<Fmt> * (Fmt::kRecord + 8 + 4);
+
+template <class Fmt>
+constexpr bool kClFits = 2 * (kClSmem<Fmt> + 1024) <= 228 * 1024 &&
+                         kClStages<Fmt> *Fmt::kRecord >= kStateFloats * static_cast<int>(sizeof(float));
+static_assert(kClFits<Nvfp4Format> && kClFits<Fp8BlockFormat>, "two CTAs an SM; a warp's state in its ring");
+
+template <class Fmt, bool kListed>
+__global__ void __launch_bounds__(kClThreads, 2) cluster_decode_kernel(const __grid_constant__ DecodeParams p)
+{
+    extern __shared__ __align__(16) uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((128u - (smem_addr(smem_raw) & 127u)) & 127u);
+    constexpr int S = kClStages<Fmt>, R = Fmt::kRecord;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int gid = lane >> 2, tig = lane & 3;
+    uint8_t *ring = smem + warp * S * R;
+    const uint32_t wdata = smem_addr(ring);
+    const uint32_t wbar = smem_addr(smem + kClWarps * S * R) + warp * S * 8;
+    // tokens of the page in each stage that count
+    volatile int32_t *counted = reinterpret_cast<int32_t *>(smem + kClWarps * S * (R + 8)) + warp * S;
+
+    if (lane == 0) {
+        for (int s = 0; s < S; ++s)
+            mbar_init(wbar + 8 * s, 1);
+        fence_mbar_init();
+    }
+    pdl_launch_dependents();
+    // Lengths and block tables may be read ahead of the kernel before, as in
+    // decode_kernel; lists, queries and records may not.
+    const uint32_t rank = cluster_rank(), ranks = cluster_size();
+    const int seg = blockIdx.x / ranks, row = seg / p.hkv, h = seg - row * p.hkv;
+    const int b = row / p.sel_q_len;
+    if (rank == 0 && h == 0 && threadIdx.x == 0 && row == b * p.sel_q_len) {
+        const int L = __ldg(p.seq_lens + b);
+        if (L < 0 || L > p.max_pages * kPageSize)
+            report(p.dev_status, NVFP4KV_DEV_BAD_LEN);
+    }
+    const int L = selected_row_len(p, row);
+    const int pages = (L + kPageSize - 1) / kPageSize, n = kListed ? min(p.budget, pages) : pages;
+    const int w = rank * kClWarps + warp, workers = ranks * kClWarps;
+    const int lo = static_cast<int>(static_cast<long long>(n) * w / workers);
+    const int hi = static_cast<int>(static_cast<long long>(n) * (w + 1) / workers);
+    const int32_t *list = kListed ? p.sel_pages + (static_cast<size_t>(row) * p.hkv + h) * p.budget : nullptr;
+    const int32_t *table = p.block_table + static_cast<size_t>(b) * p.max_pages;
+
+    // Lane l looks up entry win + l of the current window of 32, and of the next.
+    uint32_t cur_rec = 0, nxt_rec = 0;
+    int cur_counted = 0, nxt_counted = 0, win = lo;
+    auto lookup = [&](int j) {
+        nxt_rec = 0;
+        nxt_counted = 0;
+        if (j >= hi)
+            return;
+        const int page = kListed ? __ldcg(list + j) : j;
+        if (page < 0 || page >= pages) {
+            report(p.dev_status, NVFP4KV_DEV_BAD_PAGE);              // (no token of it counts)
+            return;
+        }
+        int phys = __ldg(table + page);
+        if (static_cast<unsigned>(phys) >= static_cast<unsigned>(p.num_pages)) {
+            report(p.dev_status, NVFP4KV_DEV_BAD_PAGE);
+            phys = 0;
+        }
+        nxt_counted = min(L - page * kPageSize, kPageSize);
+        nxt_rec = static_cast<uint32_t>(phys) * static_cast<uint32_t>(p.hkv) + static_cast<uint32_t>(h);
+    };
+    auto issue = [&](int j, int st) {
+        int rel = j - win;
+        if (rel >= 32) {
+            win += 32;
+            rel -= 32;
+            cur_rec = nxt_rec;
+            cur_counted = nxt_counted;
+            lookup(win + 32 + lane);
+        }
+        const uint32_t z = __shfl_sync(kFullMask, cur_rec, rel);
+        if (lane == rel)
+            counted[st] = cur_counted;
+        if (lane == 0) {
+            const uint32_t bar = wbar + 8 * st;
+            mbar_arrive_expect_tx(bar, R);
+            bulk_g2s(wdata + st * R, p.pool + static_cast<size_t>(z) * R, R, bar);
+        }
+    };
+    if (kListed)
+        pdl_wait();
+    lookup(lo + lane);
+    cur_rec = nxt_rec;
+    cur_counted = nxt_counted;
+    lookup(lo + 32 + lane);
+    if (!kListed)
+        pdl_wait();
+    for (int x = lo; x < min(lo + S, hi); ++x)
+        issue(x, x - lo);
+
+    uint32_t qf[16];
+    float inv0 = 1.f, inv1 = 1.f, m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    float oacc[8][4];
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            oacc[j][e] = 0.f;
+    {
+        const bool has_row = gid < p.group;
+        const uint16_t *q = p.q + (static_cast<size_t>(row) * p.hq + h * p.group + (has_row ? gid : 0)) * kHeadDim;
+        if constexpr (Fmt::kPageScales)
+            load_rows_apart(q, has_row, p.qscale, tig, qf, inv0, inv1);
+        else
+            load_rows(q, has_row ? (p.hs.per_head ? p.qs[h] : p.qscale) : 0.f, tig, qf);
+    }
+    const LaneOffsets off = Fmt::offsets(gid, tig);
+
+    int st = 0;
+    uint32_t ph = 0;
+    for (int j = lo; j < hi;) {
+        const int np = j + 1 < hi ? 2 : 1;
+        int st1 = st + 1;
+        uint32_t ph1 = ph;
+        if (st1 == S) {
+            st1 = 0;
+            ph1 ^= 1u;
+        }
+        const bool arrived = np == 2 ? mbar_wait2_bounded(wbar + 8 * st, ph, wbar + 8 * st1, ph1, p.wait_limit)
+                                     : mbar_wait_bounded(wbar + 8 * st, ph, p.wait_limit);
+        if (!__all_sync(kFullMask, arrived)) {
+            // staged data never arrived: report, let the copies in flight land, and
+            // go to the cluster's barriers with nothing
+            if (lane == 0)
+                report(p.dev_status, NVFP4KV_DEV_TIMEOUT);
+            for (int k = 0; k < min(S, hi - j); ++k) {
+                const int s2 = st + k;
+                mbar_wait_bounded(wbar + 8 * (s2 < S ? s2 : s2 - S), s2 < S ? ph : ph ^ 1u, kWaitLimit);
+            }
+            break;
+        }
+        __syncwarp();
+        const int v0 = counted[st], v1 = np == 2 ? counted[st1] : v0;
+        if (np == 2)
+            attend_pages<Fmt, 2, Counted::kEach>(qf, inv0, inv1, m0, m1, l0, l1, oacc, wdata + st * R, wdata + st1 * R, v0,
+                                                 v1, 0, 0, 0, off, gid, tig);
+        else
+            attend_pages<Fmt, 1, Counted::kEach>(qf, inv0, inv1, m0, m1, l0, l1, oacc, wdata + st * R, wdata + st * R, v0,
+                                                 v0, 0, 0, 0, off, gid, tig);
+        __syncwarp();
+        if (j + S < hi)
+            issue(j + S, st);
+        if (np == 2 && j + 1 + S < hi)
+            issue(j + 1 + S, st1);
+        st += np;
+        if (st >= S) {
+            st -= S;
+            ph ^= 1u;
+        }
+        j += np;
+    }
+
+    // the warp's state into its ring, whose copies have all landed
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1) {
+        l0 += __shfl_xor_sync(kFullMask, l0, o);
+        l1 += __shfl_xor_sync(kFullMask, l1, o);
+    }
+    float *mine = reinterpret_cast<float *>(ring);
+#pragma unroll
+    for (int which = 0; which < 2; ++which) {
+        float *dst = mine + (2 * tig + which) * kRowFloats;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            dst[Fmt::channel(j, gid, 0)] = oacc[j][which];
+            dst[Fmt::channel(j, gid, 1)] = oacc[j][2 + which];
+        }
+    }
+    if (gid == 0) {
+        float *ml = mine + kMaxGroup * kRowFloats;
+        ml[2 * tig] = m0;
+        ml[2 * tig + 1] = m1;
+        ml[kMaxGroup + 2 * tig] = l0;
+        ml[kMaxGroup + 2 * tig + 1] = l1;
+    }
+    __syncthreads();
+    // warp r joins row r of the CTA's warps, four channels a lane
+    const int r = warp;
+    constexpr int kStep = S * R / static_cast<int>(sizeof(float));   // from one warp's state to the next
+    float *all = reinterpret_cast<float *>(smem);
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float M = -INFINITY, l = 0.f;
+    if (r < p.group) {
+#pragma unroll
+        for (int k = 0; k < kClWarps; ++k)
+            M = fmaxf(M, all[k * kStep + kMaxGroup * kRowFloats + r]);
+#pragma unroll
+        for (int k = 0; k < kClWarps; ++k) {
+            const float *from = all + k * kStep;
+            const float m = from[kMaxGroup * kRowFloats + r], e = m == -INFINITY ? 0.f : fast_exp2(m - M);
+            const float4 v = *reinterpret_cast<const float4 *>(from + r * kRowFloats + 4 * lane);
+            o.x += e * v.x;
+            o.y += e * v.y;
+            o.z += e * v.z;
+            o.w += e * v.w;
+            l += e * from[kMaxGroup * kRowFloats + kMaxGroup + r];
+        }
+    }
+    if (ranks > 1) {
+        // the CTAs' rows, in the place of warp 0's; CTA r mod ranks finishes row r
+        if (r < p.group) {
+            __syncwarp();
+            *reinterpret_cast<float4 *>(all + r * kRowFloats + 4 * lane) = o;
+            if (lane == 0) {
+                all[kMaxGroup * kRowFloats + r] = M;
+                all[kMaxGroup * kRowFloats + kMaxGroup + r] = l;
+            }
+        }
+        cluster_sync();
+        if (r < p.group && r % ranks == rank) {
+            const uint32_t base = smem_addr(smem);
+            const uint32_t at_m = base + 4 * (kMaxGroup * kRowFloats + r), at_o = base + 4 * (r * kRowFloats + 4 * lane);
+            for (uint32_t k = 0; k < ranks; ++k)
+                M = fmaxf(M, ld_cluster(in_cta(at_m, k)));
+            o = make_float4(0.f, 0.f, 0.f, 0.f);
+            l = 0.f;
+            for (uint32_t k = 0; k < ranks; ++k) {
+                const float m = ld_cluster(in_cta(at_m, k)), e = m == -INFINITY ? 0.f : fast_exp2(m - M);
+                const float4 v = ld_cluster4(in_cta(at_o, k));
+                o.x += e * v.x;
+                o.y += e * v.y;
+                o.z += e * v.z;
+                o.w += e * v.w;
+                l += e * ld_cluster(in_cta(at_m + 4 * kMaxGroup, k));
+            }
+        }
+    }
+    if (r < p.group && r % ranks == rank) {
+        const float osc = head_tensor_scale(p.hs, true, h, p.out_scale), by = l > 0.f ? osc / l : 0.f;
+        const size_t at = (static_cast<size_t>(row) * p.hq + h * p.group + r) * kHeadDim + 4 * lane;
+        if (p.out_bf16) {
+            const __nv_bfloat162 x = __floats2bfloat162_rn(o.x * by, o.y * by), y = __floats2bfloat162_rn(o.z * by, o.w * by);
+            *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p.out) + at) =
+                make_uint2(*reinterpret_cast<const uint32_t *>(&x), *reinterpret_cast<const uint32_t *>(&y));
+        } else {
+            *reinterpret_cast<float4 *>(static_cast<float *>(p.out) + at) =
+                make_float4(o.x * by, o.y * by, o.z * by, o.w * by);
+        }
+    }
+    if (ranks > 1)
+        cluster_sync();                          // (nobody leaves while its rows are read)
+}
+
+template <class Fmt, bool kListed>
+cudaError_t launch(const DecodeParams &p, int ranks, cudaStream_t s)
+{
+    auto kernel = cluster_decode_kernel<Fmt, kListed>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(kClSmem<Fmt>));
+    if (e != cudaSuccess)
+        return e;
+    return launch_cluster(kernel, dim3(static_cast<unsigned>(p.batch) * p.hkv * ranks), dim3(kClThreads), ranks,
+                          kClSmem<Fmt>, s, p);
+}
+
+} // namespace
+
+// CTAs a cluster: as many as fill two places an SM (or one place for each page and
+// warp), and whether that is faster than the worker split.  In us, measured with
+// 48 + 8 heads: a wave of clusters 3.6 and for each page of a CTA 0.115 with a
+// neighbour on the SM, 0.075 without (8 bits: 0.19 and 0.085); the workers 10 (8
+// bits: 16, their CTAs leave no registers for the next kernel's), 0.00042 (0.00053)
+// a page-head and 0.015 a (query token, kv head) to be joined.  80 of 256 pages: 14
+// and 18; 320 of 128 pages: 33 and 28.
+int cluster_decode_ranks(int64_t segments, int64_t pages, bool eight_bits)
+{
+    const int64_t sms = sm_count(), slots = 2 * sms;
+    if (segments > (int64_t{1} << 27))
+        return 0;
+    int64_t ranks = segments > 0 ? slots / segments : 1;
+    ranks = ranks < pages / kClWarps ? ranks : pages / kClWarps;
+    ranks = ranks < 1 ? 1 : (ranks > 8 ? 8 : ranks);
+    const int64_t ctas = segments * ranks, waves = (ctas + slots - 1) / slots;
+    const bool crowded = ctas > sms || ranks > 4;
+    const double page = eight_bits ? (crowded ? 0.19 : 0.085) : (crowded ? 0.115 : 0.075);
+    const double clusters = waves * (3.6 + page * ((pages + ranks - 1) / ranks));
+    const double workers = (eight_bits ? 16.0 : 10.0) + (eight_bits ? 0.00053 : 0.00042) * segments * pages + 0.015 * segments;
+    return clusters <= workers ? static_cast<int>(ranks) : 0;
+}
+
+cudaError_t launch_cluster_decode_nvfp4(const DecodeParams &p, int ranks, cudaStream_t s)
+{
+    return launch<Nvfp4Format, true>(p, ranks, s);
+}
+
+cudaError_t launch_cluster_decode_fp8_block(const DecodeParams &p, int ranks, cudaStream_t s)
+{
+    return p.sel_pages != nullptr ? launch<Fp8BlockFormat, true>(p, ranks, s) : launch<Fp8BlockFormat, false>(p, ranks, s);
+}
+
+} // namespace nvfp4kv

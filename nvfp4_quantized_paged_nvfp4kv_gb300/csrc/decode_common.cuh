@@ -392,6 +392,210 @@ __device__ __forceinline__ size_t out_row(const DecodeParams &p, int b, int hp, 
     return ((static_cast<size_t>(b) * p.q_len + t) * p.hq + hp * p.group + i) * kHeadDim;
 }
 
+// A lane's 32 channels of query row gid times qsc, in fp16.
+__device__ __forceinline__ void load_rows(const uint16_t *qsrc, float qsc, int tig, uint32_t (&qf)[16])
+{
+    const uint4 *qrow = reinterpret_cast<const uint4 *>(qsrc + 32 * tig);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint4 r = __ldg(qrow + i);
+        const uint32_t ww[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const float lo_f = __uint_as_float(ww[k] << 16) * qsc;
+            const float hi_f = __uint_as_float(ww[k] & 0xffff0000u) * qsc;
+            qf[4 * i + k] = pack_f16x2(lo_f, hi_f);
+        }
+    }
+}
+
+// The same for keys whose pages have scales.  A page's scale may be anything, and
+// with it the queries that go with it: each row times the power of two that puts
+// its largest element in [2^14, 2^15), which makes bf16 -> f16 exact but for
+// elements under 2^-28 of that; its inverse and qscale, which go to the fp32
+// scores, come in inv0 and inv1 for rows 2tig and 2tig + 1.
+__device__ __forceinline__ void load_rows_apart(const uint16_t *qsrc, bool has_row, float qscale, int tig,
+                                                uint32_t (&qf)[16], float &inv0, float &inv1)
+{
+    uint32_t w[16];
+    float top = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint4 r = has_row ? __ldg(reinterpret_cast<const uint4 *>(qsrc + 32 * tig) + i) : make_uint4(0, 0, 0, 0);
+        w[4 * i] = r.x;
+        w[4 * i + 1] = r.y;
+        w[4 * i + 2] = r.z;
+        w[4 * i + 3] = r.w;
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        top = fmaxf(top, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xffff0000u))));
+    top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 2));
+    // (the exponents of 2^up and 2^-up both stay within fp32's)
+    const int up = top > 0.f ? max(-112, min(126, 127 + 14 - static_cast<int>(__float_as_uint(top) >> 23))) : 0;
+    const float by = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+        qf[i] = pack_f16x2(__uint_as_float(w[i] << 16) * by, __uint_as_float(w[i] & 0xffff0000u) * by);
+    const float inv = qscale * __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
+    inv0 = __shfl_sync(kFullMask, inv, 8 * tig);
+    inv1 = __shfl_sync(kFullMask, inv, 8 * tig + 4);
+}
+
+// What of a step's pages counts: everything up to last_valid tokens of the last
+// one (kLast), its own number of tokens of each (kEach), or for each of a lane's
+// two rows the keys before its limit (kRows).
+enum class Counted { kLast, kEach, kRows };
+
+// One page-head (NP = 1), or two, at rec0 and rec1, for a warp's eight query
+// rows qf; lane (gid, tig) holds the softmax state and outputs of rows 2tig and
+// 2tig + 1.  first_valid, last_valid: tokens of the first of two and of the last
+// one that count; pos0: position of the first page's first token; inv0, inv1
+// (page scales): factors of the scores.
+template <class Fmt, int NP, Counted kCounted>
+__device__ __forceinline__ void attend_pages(const uint32_t (&qf)[16], float inv0, float inv1, float &m0, float &m1,
+                                             float &l0, float &l1, float (&oacc)[8][4], uint32_t rec0, uint32_t rec1,
+                                             int first_valid, int last_valid, int pos0, int limA, int limB,
+                                             const LaneOffsets &off, int gid, int tig)
+{
+    // S^T = K . Q^T
+    // (two accumulators per page-head halve the dependent MMA chain)
+    float sc[NP][4];
+#pragma unroll
+    for (int q = 0; q < NP; ++q) {
+        uint32_t fa[16], fb[16];
+        Fmt::load_k(q == 0 ? rec0 : rec1, off, fa, fb);
+        float sd[4] = {0.f, 0.f, 0.f, 0.f};
+        sc[q][0] = sc[q][1] = sc[q][2] = sc[q][3] = 0.f;
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+            mma_f16_16816((s & 1) ? sd : sc[q], fa[2 * s], fb[2 * s], fa[2 * s + 1], fb[2 * s + 1], qf[2 * s],
+                          qf[2 * s + 1]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            sc[q][e] += sd[e];
+        if constexpr (Fmt::kPageScales) {
+            const float ks = __uint_as_float(lds32((q == 0 ? rec0 : rec1) + kFp8Record));
+            const float f0 = ks * inv0, f1 = ks * inv1;
+            sc[q][0] *= f0;
+            sc[q][1] *= f1;
+            sc[q][2] *= f0;
+            sc[q][3] *= f1;
+        }
+    }
+    if constexpr (kCounted == Counted::kEach) {
+#pragma unroll
+        for (int q = 0; q < NP; ++q) {
+            const int valid = q == NP - 1 ? last_valid : first_valid;
+            if (valid < kPageSize) {
+                if (gid >= valid)
+                    sc[q][0] = sc[q][1] = -INFINITY;
+                if (gid + 8 >= valid)
+                    sc[q][2] = sc[q][3] = -INFINITY;
+            }
+        }
+    } else if constexpr (kCounted == Counted::kRows) {
+        // key pos0 + 16q + token against each column's visible count
+        if (pos0 + NP * kPageSize > min(limA, limB)) {
+#pragma unroll
+            for (int q = 0; q < NP; ++q) {
+                const int k0 = pos0 + q * kPageSize + gid, k1 = k0 + 8;
+                if (k0 >= limA)
+                    sc[q][0] = -INFINITY;
+                if (k0 >= limB)
+                    sc[q][1] = -INFINITY;
+                if (k1 >= limA)
+                    sc[q][2] = -INFINITY;
+                if (k1 >= limB)
+                    sc[q][3] = -INFINITY;
+            }
+        }
+    } else if (last_valid < kPageSize) {
+        if (gid >= last_valid)
+            sc[NP - 1][0] = sc[NP - 1][1] = -INFINITY;
+        if (gid + 8 >= last_valid)
+            sc[NP - 1][2] = sc[NP - 1][3] = -INFINITY;
+    }
+    // Online softmax, heads (2tig, 2tig+1).  The running maximum is only
+    // moved when some score exceeds it by more than kLazyRescale, so the
+    // common step needs no cross-lane reduction.
+    float mx0 = fmaxf(sc[0][0], sc[0][2]), mx1 = fmaxf(sc[0][1], sc[0][3]);
+#pragma unroll
+    for (int q = 1; q < NP; ++q) {
+        mx0 = fmaxf(mx0, fmaxf(sc[q][0], sc[q][2]));
+        mx1 = fmaxf(mx1, fmaxf(sc[q][1], sc[q][3]));
+    }
+    if (__any_sync(kFullMask, (mx0 > m0 + kLazyRescale) || (mx1 > m1 + kLazyRescale))) {
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1) {
+            mx0 = fmaxf(mx0, __shfl_xor_sync(kFullMask, mx0, o));
+            mx1 = fmaxf(mx1, __shfl_xor_sync(kFullMask, mx1, o));
+        }
+        const float n0 = fmaxf(m0, mx0), n1 = fmaxf(m1, mx1);
+        const float a0 = (m0 == -INFINITY) ? 0.f : fast_exp2(m0 - n0);
+        const float a1 = (m1 == -INFINITY) ? 0.f : fast_exp2(m1 - n1);
+        l0 *= a0;
+        l1 *= a1;
+#pragma unroll
+        for (int jj = 0; jj < 8; ++jj) {
+            oacc[jj][0] *= a0;
+            oacc[jj][1] *= a1;
+            oacc[jj][2] *= a0;
+            oacc[jj][3] *= a1;
+        }
+        m0 = n0;
+        m1 = n1;
+    }
+    uint32_t pb[NP][2];
+    float ls0 = 0.f, ls1 = 0.f;
+#pragma unroll
+    for (int q = 0; q < NP; ++q) {
+        float p0 = fast_exp2(sc[q][0] - m0), p1 = fast_exp2(sc[q][1] - m1);
+        float p2 = fast_exp2(sc[q][2] - m0), p3 = fast_exp2(sc[q][3] - m1);
+        if constexpr (kCounted != Counted::kLast) {
+            // a masked score against a maximum that is still -inf
+            p0 = sc[q][0] == -INFINITY ? 0.f : p0;
+            p1 = sc[q][1] == -INFINITY ? 0.f : p1;
+            p2 = sc[q][2] == -INFINITY ? 0.f : p2;
+            p3 = sc[q][3] == -INFINITY ? 0.f : p3;
+        }
+        ls0 += p0 + p2;
+        ls1 += p1 + p3;
+        pb[q][0] = movmatrix_trans(pack_f16x2(p0, p1));
+        pb[q][1] = movmatrix_trans(pack_f16x2(p2, p3));
+    }
+    l0 += ls0;
+    l1 += ls1;
+    // O^T += V^T . P^T (V arrives scaled)
+#pragma unroll
+    for (int q = 0; q < NP; ++q) {
+        uint32_t va[8][4];
+        const int valid = q == NP - 1 ? last_valid : (kCounted == Counted::kEach ? first_valid : kPageSize);
+        Fmt::load_v(q == 0 ? rec0 : rec1, off, tig, valid, va);
+        if constexpr (Fmt::kPageScales) {
+            // (a page of which nothing counts: its scale may be anything)
+            const float vs = valid > 0 ? __uint_as_float(lds32((q == 0 ? rec0 : rec1) + kFp8Record + 4)) : 0.f;
+#pragma unroll
+            for (int jj = 0; jj < 8; ++jj) {
+                float o[4];
+                mma_f16_16816_new(o, va[jj][0], va[jj][1], va[jj][2], va[jj][3], pb[q][0], pb[q][1]);
+#pragma unroll
+                for (int e = 0; e < 4; e += 2) {
+                    const uint64_t x = fma_f32x2(f32x2_pack(o[e], o[e + 1]), f32x2_pack(vs, vs),
+                                                 f32x2_pack(oacc[jj][e], oacc[jj][e + 1]));
+                    oacc[jj][e] = f32x2_lo(x);
+                    oacc[jj][e + 1] = f32x2_hi(x);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int jj = 0; jj < 8; ++jj)
+                mma_f16_16816(oacc[jj], va[jj][0], va[jj][1], va[jj][2], va[jj][3], pb[q][0], pb[q][1]);
+        }
+    }
+}
+
 // kMulti: several query tokens per sequence.  A segment is then one row group
 // of one kv head ("virtual heads" hkv * row_groups per sequence), numbered
 // with the row group innermost so that the row groups of a kv head read the
@@ -637,48 +841,9 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, kDecodeCtasPerSm) decode_ke
             limB = rB < p.rows ? L - p.q_len + rB / g + 1 : 0;
         }
         if constexpr (Fmt::kPageScales) {
-            // A page's scale may be anything, and with it the queries that go with
-            // it: each row times the power of two that puts its largest element in
-            // [2^14, 2^15), which makes bf16 -> f16 exact but for elements under
-            // 2^-28 of that; its inverse and sm_scale go to the fp32 scores.
-            uint32_t w[16];
-            float top = 0.f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint4 r = has_row ? __ldg(reinterpret_cast<const uint4 *>(qsrc + 32 * tig) + i) : make_uint4(0, 0, 0, 0);
-                w[4 * i] = r.x;
-                w[4 * i + 1] = r.y;
-                w[4 * i + 2] = r.z;
-                w[4 * i + 3] = r.w;
-            }
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                top = fmaxf(top, fmaxf(fabsf(__uint_as_float(w[i] << 16)), fabsf(__uint_as_float(w[i] & 0xffff0000u))));
-            top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 1));
-            top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 2));
-            // (the exponents of 2^up and 2^-up both stay within fp32's)
-            const int up = top > 0.f ? max(-112, min(126, 127 + 14 - static_cast<int>(__float_as_uint(top) >> 23))) : 0;
-            const float by = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                qf[i] = pack_f16x2(__uint_as_float(w[i] << 16) * by, __uint_as_float(w[i] & 0xffff0000u) * by);
-            const float inv = p.qscale * __uint_as_float(static_cast<uint32_t>(127 - up) << 23);
-            inv0 = __shfl_sync(kFullMask, inv, 8 * tig);
-            inv1 = __shfl_sync(kFullMask, inv, 8 * tig + 4);
+            load_rows_apart(qsrc, has_row, p.qscale, tig, qf, inv0, inv1);
         } else if (has_row) {
-            const float qsc = p.hs.per_head ? p.qs[kMulti ? hp : h] : p.qscale;
-            const uint4 *qrow = reinterpret_cast<const uint4 *>(qsrc + 32 * tig);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint4 r = __ldg(qrow + i);
-                const uint32_t ww[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float lo_f = __uint_as_float(ww[k] << 16) * qsc;
-                    const float hi_f = __uint_as_float(ww[k] & 0xffff0000u) * qsc;
-                    qf[4 * i + k] = pack_f16x2(lo_f, hi_f);
-                }
-            }
+            load_rows(qsrc, p.hs.per_head ? p.qs[kMulti ? hp : h] : p.qscale, tig, qf);
         } else {
 #pragma unroll
             for (int k = 0; k < 16; ++k)
@@ -766,141 +931,10 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, kDecodeCtasPerSm) decode_ke
     }
 
     // One step handles one page-head, or two of the same segment.
-    // Tokens that count: all of a first of two, last_valid of the last one; with
-    // page lists each has its own number.
+    constexpr Counted kCounted = kMulti ? Counted::kRows : (kSelected ? Counted::kEach : Counted::kLast);
     auto step = [&](auto npc, uint32_t rec0, uint32_t rec1, int first_valid, int last_valid, int pos0) {
-        constexpr int NP = decltype(npc)::value;
-        // S^T = K . Q^T
-        // (two accumulators per page-head halve the dependent MMA chain)
-        float sc[NP][4];
-#pragma unroll
-        for (int q = 0; q < NP; ++q) {
-            uint32_t fa[16], fb[16];
-            Fmt::load_k(q == 0 ? rec0 : rec1, off, fa, fb);
-            float sd[4] = {0.f, 0.f, 0.f, 0.f};
-            sc[q][0] = sc[q][1] = sc[q][2] = sc[q][3] = 0.f;
-#pragma unroll
-            for (int s = 0; s < 8; ++s)
-                mma_f16_16816((s & 1) ? sd : sc[q], fa[2 * s], fb[2 * s], fa[2 * s + 1], fb[2 * s + 1], qf[2 * s],
-                              qf[2 * s + 1]);
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                sc[q][e] += sd[e];
-            if constexpr (Fmt::kPageScales) {
-                const float ks = __uint_as_float(lds32((q == 0 ? rec0 : rec1) + kFp8Record));
-                const float f0 = ks * inv0, f1 = ks * inv1;
-                sc[q][0] *= f0;
-                sc[q][1] *= f1;
-                sc[q][2] *= f0;
-                sc[q][3] *= f1;
-            }
-        }
-        if constexpr (kSelected) {
-#pragma unroll
-            for (int q = 0; q < NP; ++q) {
-                const int valid = q == NP - 1 ? last_valid : first_valid;
-                if (valid < kPageSize) {
-                    if (gid >= valid)
-                        sc[q][0] = sc[q][1] = -INFINITY;
-                    if (gid + 8 >= valid)
-                        sc[q][2] = sc[q][3] = -INFINITY;
-                }
-            }
-        } else if constexpr (kMulti) {
-            // key pos0 + 16q + token against each column's visible count
-            if (pos0 + NP * kPageSize > min(limA, limB)) {
-#pragma unroll
-                for (int q = 0; q < NP; ++q) {
-                    const int k0 = pos0 + q * kPageSize + gid, k1 = k0 + 8;
-                    if (k0 >= limA)
-                        sc[q][0] = -INFINITY;
-                    if (k0 >= limB)
-                        sc[q][1] = -INFINITY;
-                    if (k1 >= limA)
-                        sc[q][2] = -INFINITY;
-                    if (k1 >= limB)
-                        sc[q][3] = -INFINITY;
-                }
-            }
-        } else if (last_valid < kPageSize) {
-            if (gid >= last_valid)
-                sc[NP - 1][0] = sc[NP - 1][1] = -INFINITY;
-            if (gid + 8 >= last_valid)
-                sc[NP - 1][2] = sc[NP - 1][3] = -INFINITY;
-        }
-        // Online softmax, heads (2tig, 2tig+1).  The running maximum is only
-        // moved when some score exceeds it by more than kLazyRescale, so the
-        // common step needs no cross-lane reduction.
-        float mx0 = fmaxf(sc[0][0], sc[0][2]), mx1 = fmaxf(sc[0][1], sc[0][3]);
-#pragma unroll
-        for (int q = 1; q < NP; ++q) {
-            mx0 = fmaxf(mx0, fmaxf(sc[q][0], sc[q][2]));
-            mx1 = fmaxf(mx1, fmaxf(sc[q][1], sc[q][3]));
-        }
-        if (__any_sync(kFullMask, (mx0 > m0 + kLazyRescale) || (mx1 > m1 + kLazyRescale))) {
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1) {
-                mx0 = fmaxf(mx0, __shfl_xor_sync(kFullMask, mx0, o));
-                mx1 = fmaxf(mx1, __shfl_xor_sync(kFullMask, mx1, o));
-            }
-            const float n0 = fmaxf(m0, mx0), n1 = fmaxf(m1, mx1);
-            const float a0 = (m0 == -INFINITY) ? 0.f : fast_exp2(m0 - n0);
-            const float a1 = (m1 == -INFINITY) ? 0.f : fast_exp2(m1 - n1);
-            l0 *= a0;
-            l1 *= a1;
-#pragma unroll
-            for (int jj = 0; jj < 8; ++jj) {
-                oacc[jj][0] *= a0;
-                oacc[jj][1] *= a1;
-                oacc[jj][2] *= a0;
-                oacc[jj][3] *= a1;
-            }
-            m0 = n0;
-            m1 = n1;
-        }
-        uint32_t pb[NP][2];
-        float ls0 = 0.f, ls1 = 0.f;
-#pragma unroll
-        for (int q = 0; q < NP; ++q) {
-            float p0 = fast_exp2(sc[q][0] - m0), p1 = fast_exp2(sc[q][1] - m1);
-            float p2 = fast_exp2(sc[q][2] - m0), p3 = fast_exp2(sc[q][3] - m1);
-            if constexpr (kMulti || kSelected) {
-                // a masked score against a maximum that is still -inf
-                p0 = sc[q][0] == -INFINITY ? 0.f : p0;
-                p1 = sc[q][1] == -INFINITY ? 0.f : p1;
-                p2 = sc[q][2] == -INFINITY ? 0.f : p2;
-                p3 = sc[q][3] == -INFINITY ? 0.f : p3;
-            }
-            ls0 += p0 + p2;
-            ls1 += p1 + p3;
-            pb[q][0] = movmatrix_trans(pack_f16x2(p0, p1));
-            pb[q][1] = movmatrix_trans(pack_f16x2(p2, p3));
-        }
-        l0 += ls0;
-        l1 += ls1;
-        // O^T += V^T . P^T (V arrives scaled)
-#pragma unroll
-        for (int q = 0; q < NP; ++q) {
-            uint32_t va[8][4];
-            const int valid = q == NP - 1 ? last_valid : (kSelected ? first_valid : kPageSize);
-            Fmt::load_v(q == 0 ? rec0 : rec1, off, tig, valid, va);
-            if constexpr (Fmt::kPageScales) {
-                // (a page of which nothing counts: its scale may be anything)
-                const float vs = valid > 0 ? __uint_as_float(lds32((q == 0 ? rec0 : rec1) + kFp8Record + 4)) : 0.f;
-#pragma unroll
-                for (int jj = 0; jj < 8; ++jj) {
-                    float o[4] = {0.f, 0.f, 0.f, 0.f};
-                    mma_f16_16816(o, va[jj][0], va[jj][1], va[jj][2], va[jj][3], pb[q][0], pb[q][1]);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        oacc[jj][e] = fmaf(o[e], vs, oacc[jj][e]);
-                }
-            } else {
-#pragma unroll
-                for (int jj = 0; jj < 8; ++jj)
-                    mma_f16_16816(oacc[jj], va[jj][0], va[jj][1], va[jj][2], va[jj][3], pb[q][0], pb[q][1]);
-            }
-        }
+        attend_pages<Fmt, decltype(npc)::value, kCounted>(qf, inv0, inv1, m0, m1, l0, l1, oacc, rec0, rec1, first_valid,
+                                                          last_valid, pos0, limA, limB, off, gid, tig);
     };
 
     int st = 0;            // ring stage of page-head j

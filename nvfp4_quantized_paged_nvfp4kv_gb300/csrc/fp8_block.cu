@@ -126,7 +126,7 @@ __device__ __forceinline__ int find_unit(const int32_t *q_indptr, int batch, lon
 // tokens' bytes interleaved) is one lane's.  All rows of the page are asked for
 // before the first is used; the page's old codes and scale come beside them.
 template <bool kBf16>
-__global__ void __launch_bounds__(256) block_append_kernel(const __grid_constant__ BlockAppendParams p)
+__global__ void __launch_bounds__(256, kBf16 ? 3 : 2) block_append_kernel(const __grid_constant__ BlockAppendParams p)
 {
     pdl_wait();                  // the records may still be read, the tables still be written
     pdl_launch_dependents();
@@ -165,7 +165,6 @@ __global__ void __launch_bounds__(256) block_append_kernel(const __grid_constant
     const long long row0 = c0 + page * kPageSize - pos0;                     // row of the page's token 0
 
     Eight<kBf16> x[4][2];
-    uint4 old[4];                // K: channels of tokens 2p, then 2p + 1; V: the chunk
 #pragma unroll
     for (int it = 0; it < 4; ++it) {
         const int t0 = 4 * it + 2 * half;
@@ -176,33 +175,14 @@ __global__ void __launch_bounds__(256) block_append_kernel(const __grid_constant
             else
                 x[it][w].zero();
         }
-        old[it] = make_uint4(0, 0, 0, 0);
     }
     int e_old = kLeastExp;
-    uint8_t *at[4][2];           // K: where the tokens' eight channels go; V: the chunk
-#pragma unroll
-    for (int it = 0; it < 4; ++it) {
-        const int pr = 2 * it + half;
-        if (is_v) {
-            const int f = (pr & 1) + 4 * ((pr >> 1) & 1);
-            at[it][0] = at[it][1] = rec + 2048 + pr * 256 + ((c + f) & 15) * 16;
-        } else {
-            at[it][0] = rec + pr * 256 + (c >> 1) * 16 + (c & 1) * 8;
-            at[it][1] = rec + pr * 256 + 128 + (((c >> 1) + 1) & 7) * 16 + (c & 1) * 8;
-        }
-        if (2 * pr < begin) {
-            if (is_v) {
-                old[it] = __ldcg(reinterpret_cast<const uint4 *>(at[it][0]));
-            } else {
-                const uint2 a = __ldcg(reinterpret_cast<const uint2 *>(at[it][0]));
-                const uint2 d = __ldcg(reinterpret_cast<const uint2 *>(at[it][1]));
-                old[it] = make_uint4(a.x, a.y, d.x, d.y);
-            }
-        }
-    }
-    if (begin > 0)
+    if (begin > 0) {
         e_old = max(kLeastExp, min(kMostExp, static_cast<int>((__float_as_uint(__ldcg(scale)) >> 23) & 0xffu) - 127));
-
+        // the codes that are there, into L2: they are wanted if the scale rises, V's
+        // of a shared pair in any case
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(rec + (is_v ? 2048 : 0) + 64 * lane));
+    }
     float amax = 0.f;
 #pragma unroll
     for (int it = 0; it < 4; ++it)
@@ -217,7 +197,7 @@ __global__ void __launch_bounds__(256) block_append_kernel(const __grid_constant
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
         amax = fmaxf(amax, __shfl_xor_sync(kFullMask, amax, o));
-    const int e = begin > 0 ? max(e_old, scale_exp(amax)) : scale_exp(amax);
+    const int e = max(e_old, scale_exp(amax));
     const float by = two_to(-e);
     const bool raised = begin > 0 && e > e_old;
     const int shift = e_old - e;                             // 2^shift: at most 1, from 2^-126 on as good as 0
@@ -228,7 +208,7 @@ __global__ void __launch_bounds__(256) block_append_kernel(const __grid_constant
 
 #pragma unroll
     for (int it = 0; it < 4; ++it) {
-        const int t0 = 4 * it + 2 * half;
+        const int pr = 2 * it + half, t0 = 2 * pr;
         if (t0 >= end || (t0 + 1 < begin && !raised))
             continue;                                        // nothing of the pair is written
         uint2 code[2];
@@ -237,25 +217,35 @@ __global__ void __launch_bounds__(256) block_append_kernel(const __grid_constant
             float f[8];
             x[it][w].get(f);
             code[w] = codes_of(f, by);
-            if (t0 + w < begin) {
-                const uint4 o = old[it];
-                // V: byte 2i + w of the chunk is token w's channel i
-                code[w] = !is_v ? (w ? make_uint2(o.z, o.w) : make_uint2(o.x, o.y))
-                                : make_uint2(__byte_perm(o.x, o.y, w ? 0x7531 : 0x6420),
-                                             __byte_perm(o.z, o.w, w ? 0x7531 : 0x6420));
-                if (raised)
-                    code[w] = recode(code[w], down);
-            }
         }
         if (is_v) {
-            *reinterpret_cast<uint4 *>(at[it][0]) =
-                make_uint4(__byte_perm(code[0].x, code[1].x, 0x5140), __byte_perm(code[0].x, code[1].x, 0x7362),
-                           __byte_perm(code[0].y, code[1].y, 0x5140), __byte_perm(code[0].y, code[1].y, 0x7362));
+            const int f = (pr & 1) + 4 * ((pr >> 1) & 1);
+            uint4 *at = reinterpret_cast<uint4 *>(rec + 2048 + pr * 256 + ((c + f) & 15) * 16);
+            if (t0 < begin) {
+                // byte 2i + w of the chunk is token w's channel i
+                const uint4 o = __ldcg(at);
+#pragma unroll
+                for (int w = 0; w < 2; ++w)
+                    if (t0 + w < begin) {
+                        code[w] = make_uint2(__byte_perm(o.x, o.y, w ? 0x7531 : 0x6420),
+                                             __byte_perm(o.z, o.w, w ? 0x7531 : 0x6420));
+                        if (raised)
+                            code[w] = recode(code[w], down);
+                    }
+            }
+            *at = make_uint4(__byte_perm(code[0].x, code[1].x, 0x5140), __byte_perm(code[0].x, code[1].x, 0x7362),
+                             __byte_perm(code[0].y, code[1].y, 0x5140), __byte_perm(code[0].y, code[1].y, 0x7362));
         } else {
 #pragma unroll
-            for (int w = 0; w < 2; ++w)
-                if (t0 + w < end && (t0 + w >= begin || raised))
-                    *reinterpret_cast<uint2 *>(at[it][w]) = code[w];
+            for (int w = 0; w < 2; ++w) {
+                uint2 *at = reinterpret_cast<uint2 *>(rec + (t0 + w) * 128 + (((c >> 1) + w) & 7) * 16 + (c & 1) * 8);
+                if (t0 + w >= begin) {
+                    if (t0 + w < end)
+                        *at = code[w];
+                } else if (raised) {
+                    *at = recode(__ldcg(at), down);
+                }
+            }
         }
     }
 }
@@ -302,57 +292,69 @@ __device__ __forceinline__ void put_eight(void *out, size_t at, uint2 c, float s
 
 constexpr int kReadThreads = 256;
 
-// One warp a page-head: its eight loads of 512 bytes go out together.  Bound by
-// its writes, 2 bytes a value in bf16 to one read.
+// One warp a page's K or V of one kv head: 16 lanes a row, eight channels a lane,
+// so that a half warp writes whole rows of one head.  Bound by its writes, 2 bytes a
+// value in bf16 to one read.
 template <int kType>
-__global__ void __launch_bounds__(kReadThreads) block_read_kernel(const __grid_constant__ BlockReadParams p)
+__global__ void __launch_bounds__(kReadThreads, 5) block_read_kernel(const __grid_constant__ BlockReadParams p)
 {
     extern __shared__ int32_t rsmem[];
     int32_t *scratch = rsmem, *prefix = rsmem + kPrefixScratch;
     pdl_wait();
     pdl_launch_dependents();
     build_prefix(p.lens, p.batch, 1, p.max_pages * kPageSize, prefix, scratch, blockIdx.x == 0 ? p.dev_status : nullptr);
-    const int lane = threadIdx.x & 31;
-    const long long units = static_cast<long long>(prefix[p.batch]) * p.hkv;
+    const int lane = threadIdx.x & 31, half = lane >> 4, c = lane & 15;
+    const unsigned both = 2u * p.hkv;
+    const long long units = static_cast<long long>(prefix[p.batch]) * both;
     const long long step = static_cast<long long>(gridDim.x) * (kReadThreads / 32);
     for (long long u = static_cast<long long>(blockIdx.x) * (kReadThreads / 32) + (threadIdx.x >> 5); u < units; u += step) {
-        const int pg = static_cast<int>(u / p.hkv), h = static_cast<int>(u - static_cast<long long>(pg) * p.hkv);
+        const int pg = units < (1LL << 32) ? static_cast<int>(static_cast<unsigned>(u) / both) : static_cast<int>(u / both);
+        const int hv = static_cast<int>(u - static_cast<long long>(pg) * both), h = hv >> 1;
+        const bool is_v = hv & 1;
         const int b = find_seq(prefix, p.batch, pg);
         const int page = pg - prefix[b];
         const int len = min(__ldg(p.lens + b), p.max_pages * kPageSize);
         int phys = __ldg(p.block_table + static_cast<size_t>(b) * p.max_pages + page);
         const long long row = static_cast<long long>(__ldg(p.kv_indptr + b)) + page * kPageSize;
         if (static_cast<unsigned>(phys) >= static_cast<unsigned>(p.num_pages)) {
-            if (h == 0 && lane == 0)
+            if (hv == 0 && lane == 0)
                 report(p.dev_status, NVFP4KV_DEV_BAD_PAGE);
             phys = 0;
         }
         const uint8_t *rec = p.pool + (static_cast<size_t>(phys) * p.hkv + h) * kFp8BlockRecord;
-        uint4 k[4], v[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            k[i] = __ldg(reinterpret_cast<const uint4 *>(rec) + 32 * i + lane);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            v[i] = __ldg(reinterpret_cast<const uint4 *>(rec + 2048) + 32 * i + lane);
-        const float2 s = __ldg(reinterpret_cast<const float2 *>(rec + kFp8Record));
+        const float s = __ldg(reinterpret_cast<const float *>(rec + kFp8Record) + is_v);
         const int valid = len - page * kPageSize;
+        void *out = is_v ? p.v_out : p.k_out;
+        // a row's place: channels 8c .. of token t at row t
+        const size_t at = (static_cast<size_t>(row) * p.hkv + h) * kHeadDim + 8 * c, next = static_cast<size_t>(p.hkv) * kHeadDim;
+        if (!is_v) {
+            uint2 x[8];                                          // tokens 2i + half
+            const uint2 *src = reinterpret_cast<const uint2 *>(rec) + 16 * half + 2 * (((c >> 1) + half) & 7) + (c & 1);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int t = 4 * i + (lane >> 3), ch = ((lane & 7) - (t & 1)) & 7;      // token, 16-channel chunk
-            if (t < valid) {
-                const size_t o = (static_cast<size_t>(row + t) * p.hkv + h) * kHeadDim + 16 * ch;
-                put_eight<kType>(p.k_out, o, make_uint2(k[i].x, k[i].y), s.x);
-                put_eight<kType>(p.k_out, o + 8, make_uint2(k[i].z, k[i].w), s.x);
+            for (int i = 0; i < 8; ++i)
+                x[i] = __ldg(src + 32 * i);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (2 * i + half < valid)
+                    put_eight<kType>(out, at + (2 * i + half) * next, x[i], s);
+        } else {
+            uint4 x[4];                                          // token pairs 2i + half
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int pr = 2 * i + half, f = (pr & 1) + 4 * ((pr >> 1) & 1);
+                x[i] = __ldg(reinterpret_cast<const uint4 *>(rec + 2048) + 16 * pr + ((c + f) & 15));
             }
-            const int pr = 2 * i + (lane >> 4), f = (pr & 1) + 4 * ((pr >> 1) & 1), c = ((lane & 15) - f) & 15;
 #pragma unroll
-            for (int w = 0; w < 2; ++w)
-                if (2 * pr + w < valid)
-                    put_eight<kType>(p.v_out, (static_cast<size_t>(row + 2 * pr + w) * p.hkv + h) * kHeadDim + 8 * c,
-                                     make_uint2(__byte_perm(v[i].x, v[i].y, w ? 0x7531 : 0x6420),
-                                                __byte_perm(v[i].z, v[i].w, w ? 0x7531 : 0x6420)),
-                                     s.y);
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    const int t = 2 * (2 * i + half) + w;
+                    if (t < valid)
+                        put_eight<kType>(out, at + t * next,
+                                         make_uint2(__byte_perm(x[i].x, x[i].y, w ? 0x7531 : 0x6420),
+                                                    __byte_perm(x[i].z, x[i].w, w ? 0x7531 : 0x6420)),
+                                         s);
+                }
         }
     }
 }
@@ -361,7 +363,7 @@ template <int kType>
 cudaError_t launch_read(const BlockReadParams &p, cudaStream_t s)
 {
     const size_t smem = (kPrefixScratch + static_cast<size_t>(p.batch) + 1) * sizeof(int32_t);
-    const long long warps = static_cast<long long>(p.batch) * p.max_pages * p.hkv;
+    const long long warps = static_cast<long long>(p.batch) * p.max_pages * p.hkv * 2;
     long long grid = static_cast<long long>(sm_count()) * 6;
     grid = min(grid, (warps + kReadThreads / 32 - 1) / (kReadThreads / 32));
     return launch_pdl(block_read_kernel<kType>, dim3(static_cast<unsigned>(grid)), dim3(kReadThreads), smem, s, p);

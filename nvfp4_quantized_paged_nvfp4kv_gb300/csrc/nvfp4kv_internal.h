@@ -205,7 +205,6 @@ struct SelectParams {
     const int32_t *block_table;
     const int32_t *seq_lens;
     int32_t *pages;              // [batch][q_len][hkv][budget]
-    float *scores;               // [batch][q_len][hkv][score_stride]
     int32_t *dev_status;
     int batch;
     int q_len;
@@ -217,7 +216,7 @@ struct SelectParams {
     int budget;
     int first;                   // pages always taken, at the beginning
     int last;                    // ... and at the end
-    int score_stride;            // max_pages rounded up to tiles
+    int chunk_tiles;             // (set by the launcher) tiles of 16 pages a CTA has at most
 };
 
 // Chunk attention over the paged NVFP4 cache.
@@ -348,12 +347,16 @@ cudaError_t launch_decode_fp8(const DecodeParams &p, cudaStream_t s);
 cudaError_t launch_decode_fp8_block(const DecodeParams &p, cudaStream_t s);         // (p.q_len > 1: several tokens)
 cudaError_t launch_decode_selected_nvfp4(const DecodeParams &p, cudaStream_t s);
 cudaError_t launch_decode_selected_fp8_block(const DecodeParams &p, cudaStream_t s);
+// CTAs of a cluster for each (query token, kv head) of at most so many pages; 0:
+// the worker split is the faster one.
+int cluster_decode_ranks(int64_t segments, int64_t pages, bool eight_bits);
+cudaError_t launch_cluster_decode_nvfp4(const DecodeParams &p, int ranks, cudaStream_t s);
+cudaError_t launch_cluster_decode_fp8_block(const DecodeParams &p, int ranks, cudaStream_t s);   // (listed or all pages)
 cudaError_t launch_merge(const DecodeParams &p, cudaStream_t s);
 cudaError_t launch_block_append(const BlockAppendParams &p, cudaStream_t s);
 cudaError_t launch_block_read(const BlockReadParams &p, cudaStream_t s);
 cudaError_t launch_page_bounds_nvfp4(const BoundsParams &p, cudaStream_t s);
 cudaError_t launch_page_bounds_fp8_block(const BoundsParams &p, cudaStream_t s);
-int score_row_stride(int max_pages);                                               // floats of a row of scores
 cudaError_t launch_select_pages(const SelectParams &p, cudaStream_t s);
 cudaError_t launch_dequant_prefix_fp8(const PrefixParams &p, cudaStream_t s);
 ExtendShape paged_extend_shape(int64_t q_rows, int64_t max_q_len, int64_t batch, int64_t hkv, int64_t group,

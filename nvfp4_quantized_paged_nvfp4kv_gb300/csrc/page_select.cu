@@ -12,9 +12,10 @@
 // I is a whole number of at most 128 * 127^2 < 2^24, exact in any order of sums,
 // and the product is one rounding: the selection is the same whatever the work
 // split.  Positive and negative parts of w make I a product of 256 terms,
-// (w+, w-) . (hi, lo), which runs on the tensor cores in 8-bit integers.
+// (w+, w-) . (hi, lo), which runs on the tensor cores.
 // A query takes the first pages and the last ones of its sequence and, of the
 // others, those of the largest scores, the lower page first where they tie.
+#include "cluster.cuh"
 #include "decode_common.cuh"
 
 namespace nvfp4kv {
@@ -38,94 +39,132 @@ __device__ __forceinline__ uint32_t hmax2(uint32_t a, uint32_t b)
     return r;
 }
 
-// Keys of a page-head by lane: kRegs f16x2 (channel pairs from first(lane) on) of
-// kTokens tokens.  The lanes that share channels differ in the bits kShare of the
-// lane; value(x) = x * scale is exact in fp32.
+// Keys of a page-head by lane: lane l holds channels 8c .. 8c + 7, c = l mod 16,
+// of the tokens 2i + floor(l / 16), i = 0 .. 7.  A value is x[i] * unit().
 struct Nvfp4Keys {
-    static constexpr int kRecord = kNvfp4Record, kRegs = 16, kTokens = 2, kTopBit = 16, kLowBit = 4;
-    uint4 d[2];
-    uint32_t s[2];
+    static constexpr int kRecord = kNvfp4Record;
+    uint32_t d[8], s[8];
 
     __device__ __forceinline__ void load(const uint8_t *rec, int lane)
     {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            d[i] = __ldg(reinterpret_cast<const uint4 *>(rec) + 32 * i + lane);
-            s[i] = __ldg(reinterpret_cast<const uint16_t *>(rec + 2048) + 32 * i + lane);
+        for (int i = 0; i < 8; ++i) {
+            d[i] = __ldg(reinterpret_cast<const uint32_t *>(rec) + 32 * i + lane);
+            s[i] = __ldg(rec + 2048 + 16 * i + 8 * (lane >> 4) + ((lane & 15) >> 1));
         }
     }
-    __device__ __forceinline__ float scale() const { return 1.f; }
-    __device__ static __forceinline__ int token(int i, int lane) { return 8 * i + (lane >> 2); }
-    __device__ static __forceinline__ int first(int lane) { return 32 * (lane & 3); }
-    __device__ __forceinline__ void get(int i, uint32_t (&x)[16]) const
+    // The scale byte's seven bits moved to f16's exponent and mantissa are the
+    // scale times 2^-8 without a conversion; times a code's value it is exact.
+    __device__ __forceinline__ float unit() const { return 256.f; }
+    __device__ __forceinline__ void get(int i, uint32_t (&x)[4]) const
     {
-        const uint32_t w[4] = {d[i].x, d[i].y, d[i].z, d[i].w};
-        const uint32_t sc = e4m3x2_to_f16x2(s[i]);
-        const uint32_t s0 = __byte_perm(sc, 0, 0x1010), s1 = __byte_perm(sc, 0, 0x3232);
+        const uint32_t sc = (s[i] & 0x7fu) * 0x00800080u;
+        e2m1x8_to_f16x2x4(d[i], x[0], x[1], x[2], x[3]);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-            e2m1x8_to_f16x2x4(w[k], x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
-#pragma unroll
-        for (int k = 0; k < 16; ++k)
-            x[k] = hmul2(x[k], k < 8 ? s0 : s1);
+            x[k] = hmul2(x[k], sc);
     }
 };
 
 struct Fp8BlockKeys {
-    static constexpr int kRecord = kFp8BlockRecord, kRegs = 8, kTokens = 4, kTopBit = 16, kLowBit = 8;
-    uint4 d[4];
+    static constexpr int kRecord = kFp8BlockRecord;
+    uint2 d[8];
     float s;
 
     __device__ __forceinline__ void load(const uint8_t *rec, int lane)
     {
-        const int place = ((lane & 7) + ((lane >> 3) & 1)) & 7;      // of chunk lane % 8 in rows of this parity
+        // (the chunk of 16 channels is one place further in odd rows)
+        const int place = 2 * ((((lane & 15) >> 1) + (lane >> 4)) & 7) + (lane & 1);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            d[i] = __ldg(reinterpret_cast<const uint4 *>(rec) + 32 * i + (lane & ~7) + place);
+        for (int i = 0; i < 8; ++i)
+            d[i] = __ldg(reinterpret_cast<const uint2 *>(rec) + 32 * i + (lane & 16) + place);
         s = __ldg(reinterpret_cast<const float *>(rec + kFp8Record));
     }
-    __device__ __forceinline__ float scale() const { return s; }
-    __device__ static __forceinline__ int token(int i, int lane) { return 4 * i + (lane >> 3); }
-    __device__ static __forceinline__ int first(int lane) { return 16 * (lane & 7); }
-    __device__ __forceinline__ void get(int i, uint32_t (&x)[8]) const
+    __device__ __forceinline__ float unit() const { return s; }
+    __device__ __forceinline__ void get(int i, uint32_t (&x)[4]) const
     {
-        const uint32_t w[4] = {d[i].x, d[i].y, d[i].z, d[i].w};
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            e4m3x4_to_f16x2x2(w[k], x[2 * k], x[2 * k + 1]);
+        e4m3x4_to_f16x2x2(d[i].x, x[0], x[1]);
+        e4m3x4_to_f16x2x2(d[i].y, x[2], x[3]);
     }
 };
 
-// Combine lo / hi over the lanes that share channels, halving what a lane keeps
-// with each exchange: in the end two registers, four channels.  Returns the
-// first of them (relative to the lane's).
-template <int kRegs, int kBit, int kLowBit>
-__device__ __forceinline__ int gather_bounds(uint32_t (&lo)[kRegs], uint32_t (&hi)[kRegs], int lane, uint32_t (&out)[4])
+// 1.5 * 2^23: a sum with it, rounded up or down, has the whole number in its low
+// byte, as two's complement.
+constexpr float kWhole = 12582912.f;
+
+// The bounds of one page-head by a warp.  All arithmetic in fp32 is on x, the
+// values over unit(), a power of two: fl32(x * fl32(127 / max |x|)) is what the
+// definition has for k = x * unit.
+template <class Keys>
+__device__ __forceinline__ void write_bounds(const Keys &keys, int valid, int8_t *dst, float *step, int lane)
 {
-    constexpr int kHalf = kRegs / 2;
-    const bool upper = lane & kBit;
-    uint32_t l2[kHalf], h2[kHalf];
+    uint32_t lo[4], hi[4];
 #pragma unroll
-    for (int k = 0; k < kHalf; ++k) {
-        const uint32_t lo_away = upper ? lo[k] : lo[k + kHalf], hi_away = upper ? hi[k] : hi[k + kHalf];
-        const uint32_t lo_keep = upper ? lo[k + kHalf] : lo[k], hi_keep = upper ? hi[k + kHalf] : hi[k];
-        l2[k] = hmin2(lo_keep, __shfl_xor_sync(kFullMask, lo_away, kBit));
-        h2[k] = hmax2(hi_keep, __shfl_xor_sync(kFullMask, hi_away, kBit));
+    for (int k = 0; k < 4; ++k) {
+        lo[k] = 0x7c007c00u;                                     // +inf, -inf
+        hi[k] = 0xfc00fc00u;
     }
-    const int at = upper ? 2 * kHalf : 0;
-    if constexpr (kBit == kLowBit) {
-        static_assert(kHalf == 2, "four channels a lane");
-        out[0] = l2[0];
-        out[1] = l2[1];
-        out[2] = h2[0];
-        out[3] = h2[1];
-        return at;
+    auto take = [&](int i) {
+        uint32_t x[4];
+        keys.get(i, x);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            lo[k] = hmin2(lo[k], x[k]);
+            hi[k] = hmax2(hi[k], x[k]);
+        }
+    };
+    if (valid >= kPageSize) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            take(i);
     } else {
-        return at + gather_bounds<kHalf, kBit / 2, kLowBit>(l2, h2, lane, out);
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (2 * i + (lane >> 4) < valid)
+                take(i);
     }
+    // even and odd tokens meet; each lane keeps four of its eight channels
+    const bool upper = lane & 16;
+    uint32_t l[2], h[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const uint32_t lo_away = upper ? lo[k] : lo[k + 2], hi_away = upper ? hi[k] : hi[k + 2];
+        l[k] = hmin2(upper ? lo[k + 2] : lo[k], __shfl_xor_sync(kFullMask, lo_away, 16));
+        h[k] = hmax2(upper ? hi[k + 2] : hi[k], __shfl_xor_sync(kFullMask, hi_away, 16));
+    }
+    uint32_t t2 = hmax2(hmax2(l[0] & 0x7fff7fffu, l[1] & 0x7fff7fffu), hmax2(h[0] & 0x7fff7fffu, h[1] & 0x7fff7fffu));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+        t2 = hmax2(t2, __shfl_xor_sync(kFullMask, t2, o));
+    const float2 tt = __half22float2(*reinterpret_cast<__half2 *>(&t2));
+    const float top = fmaxf(tt.x, tt.y);
+    // one division: 127 / top in the lower half warp, top / 127 in the upper one
+    const float quot = __fdiv_rn(upper ? top : 127.f, upper ? 127.f : top);
+    const float r = top > 0.f ? __shfl_sync(kFullMask, quot, 0) : 0.f;
+    uint32_t wl[4], wh[4];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const float2 a = __half22float2(*reinterpret_cast<__half2 *>(&l[k]));
+        const float2 d = __half22float2(*reinterpret_cast<__half2 *>(&h[k]));
+        wl[2 * k] = __float_as_uint(fmaxf(__fadd_rd(__fmul_rn(a.x, r), kWhole), kWhole - 127.f));
+        wl[2 * k + 1] = __float_as_uint(fmaxf(__fadd_rd(__fmul_rn(a.y, r), kWhole), kWhole - 127.f));
+        wh[2 * k] = __float_as_uint(fminf(__fadd_ru(__fmul_rn(d.x, r), kWhole), kWhole + 127.f));
+        wh[2 * k + 1] = __float_as_uint(fminf(__fadd_ru(__fmul_rn(d.y, r), kWhole), kWhole + 127.f));
+    }
+    auto bytes = [](const uint32_t (&w)[4]) {
+        return __byte_perm(__byte_perm(w[0], w[1], 0x0040), __byte_perm(w[2], w[3], 0x0040), 0x5410);
+    };
+    int8_t *at = dst + 8 * (lane & 15) + (upper ? 4 : 0);
+    *reinterpret_cast<uint32_t *>(at) = bytes(wl);
+    *reinterpret_cast<uint32_t *>(at + kHeadDim) = bytes(wh);
+    if (lane == 16)
+        *step = quot * keys.unit();
 }
 
-// One warp a (page, kv head).
+// One warp a page, or a part of its heads where there are fewer pages than warps;
+// the next head's keys are asked for before the last one's are worked on.  Bound
+// by its instructions more than by memory: some 250 a page-head, half of them
+// the expansion to f16 and the two comparisons a pair of values.
 template <class Keys>
 __global__ void __launch_bounds__(kBoundThreads) page_bounds_kernel(const __grid_constant__ BoundsParams p)
 {
@@ -148,73 +187,37 @@ __global__ void __launch_bounds__(kBoundThreads) page_bounds_kernel(const __grid
         },
         p.batch, prefix, scratch);
     const int lane = threadIdx.x & 31;
-    const long long units = static_cast<long long>(prefix[p.batch]) * p.hkv;
-    const long long step = static_cast<long long>(gridDim.x) * (kBoundThreads / 32);
-    for (long long u = static_cast<long long>(blockIdx.x) * (kBoundThreads / 32) + (threadIdx.x >> 5); u < units; u += step) {
-        const int pg = static_cast<int>(u / p.hkv), h = static_cast<int>(u - static_cast<long long>(pg) * p.hkv);
+    const int pages = prefix[p.batch], warps = gridDim.x * (kBoundThreads / 32);
+    if (pages == 0)
+        return;
+    const int parts = min(p.hkv, max(1, warps / pages));
+    const long long units = static_cast<long long>(pages) * parts;
+    for (long long u = blockIdx.x * (kBoundThreads / 32) + (threadIdx.x >> 5); u < units; u += warps) {
+        const int pg = parts == 1 ? static_cast<int>(u) : static_cast<int>(u / parts);
+        const int part = static_cast<int>(u - static_cast<long long>(pg) * parts);
         const int b = find_seq(prefix, p.batch, pg);
         const int len = clamp_len(__ldg(p.seq_lens + b), max_len);
         const int page = first_page(b, len) + pg - prefix[b];
         const int phys = __ldg(p.block_table + static_cast<size_t>(b) * p.max_pages + page);
         if (static_cast<unsigned>(phys) >= static_cast<unsigned>(p.num_pages)) {
-            if (h == 0 && lane == 0)
+            if (part == 0 && lane == 0)
                 report(p.dev_status, NVFP4KV_DEV_BAD_PAGE);
             continue;
         }
-        const size_t head = static_cast<size_t>(phys) * p.hkv + h;
-        Keys keys;
-        keys.load(p.pool + head * Keys::kRecord, lane);
-        uint32_t lo[Keys::kRegs], hi[Keys::kRegs];
-#pragma unroll
-        for (int k = 0; k < Keys::kRegs; ++k) {
-            lo[k] = 0x7c007c00u;                             // +inf, -inf
-            hi[k] = 0xfc00fc00u;
-        }
         const int valid = len - page * kPageSize;
-#pragma unroll
-        for (int i = 0; i < Keys::kTokens; ++i) {
-            if (Keys::token(i, lane) >= valid)
-                continue;
-            uint32_t x[Keys::kRegs];
-            keys.get(i, x);
-#pragma unroll
-            for (int k = 0; k < Keys::kRegs; ++k) {
-                lo[k] = hmin2(lo[k], x[k]);
-                hi[k] = hmax2(hi[k], x[k]);
-            }
+        const int h0 = static_cast<int>(static_cast<long long>(p.hkv) * part / parts);
+        const int h1 = static_cast<int>(static_cast<long long>(p.hkv) * (part + 1) / parts);
+        size_t head = static_cast<size_t>(phys) * p.hkv + h0;
+        const uint8_t *rec = p.pool + head * Keys::kRecord;
+        Keys keys, next;
+        keys.load(rec, lane);
+        for (int h = h0; h < h1; ++h, ++head) {
+            rec += Keys::kRecord;
+            if (h + 1 < h1)
+                next.load(rec, lane);
+            write_bounds(keys, valid, p.bounds + head * (2 * kHeadDim), p.steps + head, lane);
+            keys = next;
         }
-        uint32_t four[4];
-        const int c = Keys::first(lane) + gather_bounds<Keys::kRegs, Keys::kTopBit, Keys::kLowBit>(lo, hi, lane, four);
-        float l[4], g[4], top = 0.f;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const float2 a = __half22float2(*reinterpret_cast<__half2 *>(&four[k]));
-            const float2 d = __half22float2(*reinterpret_cast<__half2 *>(&four[2 + k]));
-            l[2 * k] = a.x * keys.scale();
-            l[2 * k + 1] = a.y * keys.scale();
-            g[2 * k] = d.x * keys.scale();
-            g[2 * k + 1] = d.y * keys.scale();
-        }
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            top = fmaxf(top, fmaxf(fabsf(l[k]), fabsf(g[k])));
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-            top = fmaxf(top, __shfl_xor_sync(kFullMask, top, o));
-        const float r = top > 0.f ? __fdiv_rn(127.f, top) : 0.f;
-        uint32_t wl = 0, wg = 0;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            const int a = static_cast<int>(fmaxf(floorf(__fmul_rn(l[k], r)), -127.f));
-            const int d = static_cast<int>(fminf(ceilf(__fmul_rn(g[k], r)), 127.f));
-            wl |= (static_cast<uint32_t>(a) & 0xffu) << (8 * k);
-            wg |= (static_cast<uint32_t>(d) & 0xffu) << (8 * k);
-        }
-        int8_t *dst = p.bounds + head * (2 * kHeadDim) + c;
-        *reinterpret_cast<uint32_t *>(dst) = wl;
-        *reinterpret_cast<uint32_t *>(dst + kHeadDim) = wg;
-        if (lane == 0)
-            p.steps[head] = __fdiv_rn(top, 127.f);
     }
 }
 
@@ -223,26 +226,18 @@ cudaError_t launch_bounds(const BoundsParams &p, cudaStream_t s)
 {
     const size_t smem = (kPrefixScratch + static_cast<size_t>(p.batch) + 1) * sizeof(int32_t);
     const long long warps = static_cast<long long>(p.batch) * p.max_pages * p.hkv;
-    long long grid = static_cast<long long>(sm_count()) * 6;
+    long long grid = static_cast<long long>(sm_count()) * 4;
     grid = min(grid, (warps + kBoundThreads / 32 - 1) / (kBoundThreads / 32));
     return launch_pdl(page_bounds_kernel<Keys>, dim3(static_cast<unsigned>(grid)), dim3(kBoundThreads), smem, s, p);
 }
 
 // ---- scores --------------------------------------------------------------------
 
-constexpr int kScoreThreads = 256, kScoreWarps = kScoreThreads / 32;
 constexpr int kTile = 16;                // pages of one matrix instruction
 
-// D(16x8 s32) += A(16x32 s8, row) * B(32x8 s8, col).
-__device__ __forceinline__ void mma_s8_16832(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                             uint32_t b1)
-{
-    asm volatile(
-        "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7},"
-        " {%8, %9}, {%0, %1, %2, %3};"
-        : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
+// Queries of a token and kv head as operands: a token's are kQueryWords uint4 --
+// [8][32 lanes] of f16 pairs, then what each of the eight heads' sums starts from.
+constexpr int kQueryWords = 8 * 32 + 2;
 
 // Pages that query token t of a sequence of length len sees.
 __device__ __forceinline__ int pages_seen(int len, int q_len, int t)
@@ -251,134 +246,163 @@ __device__ __forceinline__ int pages_seen(int len, int q_len, int t)
     return n > 0 ? (n + kPageSize - 1) / kPageSize : 0;
 }
 
-// The CTAs take equal runs of the (sequence, kv head)s' tiles of 16 pages; a
-// CTA's warps take the tiles of its run in turn.  A lane (gid, tig) holds bytes
-// 16 tig + 64 i .. + 15, i = 0 .. 3, of the bounds of pages gid and gid + 8: four
-// 16-byte loads a page, straight into the operand (its K order is free as long as
-// the queries', laid out in shared memory once a (sequence, kv head), is the
-// same).  A tile's bounds serve all query tokens.
-__global__ void __launch_bounds__(kScoreThreads) page_scores_kernel(const __grid_constant__ SelectParams p)
+// The queries of a token and kv head in whole steps, by a warp: lane (head gid,
+// channels 16 tig + 64 i .. + 15, i = 0, 1).
+__device__ __forceinline__ void load_queries(const SelectParams &p, int b, int t, int h, uint4 *frag, int lane)
 {
-    extern __shared__ __align__(16) uint8_t ssmem[];
-    uint4 *frag = reinterpret_cast<uint4 *>(ssmem);              // [q_len][4][32 lanes]
-    int32_t *scratch = reinterpret_cast<int32_t *>(frag + p.q_len * 128), *prefix = scratch + kPrefixScratch;
-    pdl_wait();
-    pdl_launch_dependents();
-    const int max_len = p.max_pages * kPageSize;
-    build_prefix_of(
-        [&](int b) {
-            const int len = __ldg(p.seq_lens + b);
-            if (blockIdx.x == 0 && (len < 0 || len > max_len))
-                report(p.dev_status, NVFP4KV_DEV_BAD_LEN);
-            const int pages = (clamp_len(len, max_len) + kPageSize - 1) / kPageSize;
-            // (where every page is taken anyway no score is asked for)
-            return pages > p.budget ? p.hkv * ((pages + kTile - 1) / kTile) : 0;
-        },
-        p.batch, prefix, scratch);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, gid = lane >> 2, tig = lane & 3;
-    const long long total = prefix[p.batch];
-    int at = static_cast<int>(total * blockIdx.x / gridDim.x);
-    const int end = static_cast<int>(total * (blockIdx.x + 1) / gridDim.x);
-    while (at < end) {
-        const int b = find_seq(prefix, p.batch, at);
-        const int tiles = (prefix[b + 1] - prefix[b]) / p.hkv;
-        const int h = (at - prefix[b]) / tiles, tile0 = at - prefix[b] - h * tiles;
-        const int stop = min(tiles, tile0 + end - at);           // of this (sequence, kv head)
-        const int len = clamp_len(__ldg(p.seq_lens + b), max_len);
-        const int pages = (len + kPageSize - 1) / kPageSize;
-        __syncthreads();                                         // the last queries are done with
-        // the queries, a warp a token: lane (head gid, channels 16 tig + 64 i ..)
-        for (int t = warp; t < p.q_len; t += kScoreWarps) {
-            // (columns past the group repeat its last head)
-            const uint16_t *q = p.q + ((static_cast<size_t>(b) * p.q_len + t) * p.hq + h * p.group + min(gid, p.group - 1)) *
-                                          kHeadDim;
-            float x[32], top = 0.f;
+    const int gid = lane >> 2, tig = lane & 3;
+    // (columns past the group repeat its last head)
+    const uint16_t *q = p.q + ((static_cast<size_t>(b) * p.q_len + t) * p.hq + h * p.group + min(gid, p.group - 1)) *
+                                  kHeadDim;
+    float x[32], top = 0.f;
 #pragma unroll
-            for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const uint4 v = __ldg(reinterpret_cast<const uint4 *>(q + 64 * i + 16 * tig) + k);
-                    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        for (int k = 0; k < 2; ++k) {
+            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(q + 64 * i + 16 * tig) + k);
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                    for (int m = 0; m < 4; ++m) {
-                        x[16 * i + 8 * k + 2 * m] = __uint_as_float(w[m] << 16);
-                        x[16 * i + 8 * k + 2 * m + 1] = __uint_as_float(w[m] & 0xffff0000u);
-                    }
-                }
-#pragma unroll
-            for (int k = 0; k < 32; ++k)
-                top = fmaxf(top, fabsf(x[k]));
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1)
-                top = fmaxf(top, __shfl_xor_sync(kFullMask, top, o));
-            const float r = top > 0.f ? __fdiv_rn(127.f, top) : 0.f;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                uint32_t pos[4], neg[4];
-#pragma unroll
-                for (int m = 0; m < 4; ++m) {
-                    pos[m] = neg[m] = 0;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const int w = static_cast<int>(fminf(fmaxf(rintf(__fmul_rn(x[16 * i + 4 * m + k], r)), -127.f), 127.f));
-                        pos[m] |= (static_cast<uint32_t>(max(w, 0)) & 0xffu) << (8 * k);
-                        neg[m] |= (static_cast<uint32_t>(min(w, 0)) & 0xffu) << (8 * k);
-                    }
-                }
-                // bytes 0 .. 127 of the bounds are the least keys
-                frag[(t * 4 + i) * 32 + lane] = make_uint4(neg[0], neg[1], neg[2], neg[3]);
-                frag[(t * 4 + 2 + i) * 32 + lane] = make_uint4(pos[0], pos[1], pos[2], pos[3]);
+            for (int m = 0; m < 4; ++m) {
+                x[16 * i + 8 * k + 2 * m] = __uint_as_float(w[m] << 16);
+                x[16 * i + 8 * k + 2 * m + 1] = __uint_as_float(w[m] & 0xffff0000u);
             }
         }
-        __syncthreads();
-        const int32_t *table = p.block_table + static_cast<size_t>(b) * p.max_pages;
-        for (int tile = tile0 + warp; tile < stop; tile += kScoreWarps) {
-            const int page = tile * kTile + (lane & 15);
-            int phys = page < pages ? __ldg(table + page) : 0;
-            if (static_cast<unsigned>(phys) >= static_cast<unsigned>(p.num_pages)) {
-                report(p.dev_status, NVFP4KV_DEV_BAD_PAGE);
-                phys = 0;
-            }
-            const size_t head = static_cast<size_t>(phys) * p.hkv + h;
-            const float step = __ldg(p.steps + head);
-            uint4 a[2][4];
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const int src = __shfl_sync(kFullMask, phys, gid + 8 * r);
-                const uint4 *d = reinterpret_cast<const uint4 *>(p.bounds + (static_cast<size_t>(src) * p.hkv + h) *
-                                                                                (2 * kHeadDim)) + tig;
+    for (int k = 0; k < 32; ++k)
+        top = fmaxf(top, fabsf(x[k]));
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    a[r][i] = __ldg(d + 4 * i);
-            }
-            for (int t = 0; t < p.q_len; ++t) {
-                int d0[4] = {0, 0, 0, 0}, d1[4] = {0, 0, 0, 0};
+    for (int o = 16; o > 0; o >>= 1)
+        top = fmaxf(top, __shfl_xor_sync(kFullMask, top, o));
+    const float r = top > 0.f ? __fdiv_rn(127.f, top) : 0.f;
+    int sum = 0;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint4 w = frag[(t * 4 + i) * 32 + lane];
-                    mma_s8_16832(d0, a[0][i].x, a[1][i].x, a[0][i].y, a[1][i].y, w.x, w.y);
-                    mma_s8_16832(d1, a[0][i].z, a[1][i].z, a[0][i].w, a[1][i].w, w.z, w.w);
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int m = 0; m < 2; ++m) {
+            uint32_t pos[4], neg[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                float w[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    w[e] = fminf(fmaxf(rintf(__fmul_rn(x[16 * i + 8 * m + 2 * k + e], r)), -127.f), 127.f);
+                    sum += static_cast<int>(w[e]);
                 }
-                int lo = max(d0[0] + d1[0], d0[1] + d1[1]), hi = max(d0[2] + d1[2], d0[3] + d1[3]);
-#pragma unroll
-                for (int o = 1; o < 4; o <<= 1) {
-                    lo = max(lo, __shfl_xor_sync(kFullMask, lo, o));
-                    hi = max(hi, __shfl_xor_sync(kFullMask, hi, o));
-                }
-                // row gid's sum is in lanes 4 gid ..; lane l < 16 stores page l's
-                const int s0 = __shfl_sync(kFullMask, lo, 4 * (lane & 7)), s1 = __shfl_sync(kFullMask, hi, 4 * (lane & 7));
-                if (lane < 16 && page < pages)
-                    p.scores[((static_cast<size_t>(b) * p.q_len + t) * p.hkv + h) * p.score_stride + page] =
-                        __fmul_rn(static_cast<float>(lane < 8 ? s0 : s1), step);
+                pos[k] = pack_f16x2(fmaxf(w[0], 0.f), fmaxf(w[1], 0.f));
+                neg[k] = pack_f16x2(fminf(w[0], 0.f), fminf(w[1], 0.f));
             }
+            // bytes 0 .. 127 of the bounds are the least keys
+            frag[(2 * i + m) * 32 + lane] = make_uint4(neg[0], neg[1], neg[2], neg[3]);
+            frag[(4 + 2 * i + m) * 32 + lane] = make_uint4(pos[0], pos[1], pos[2], pos[3]);
         }
-        at += stop - tile0;
+    sum += __shfl_xor_sync(kFullMask, sum, 1);
+    sum += __shfl_xor_sync(kFullMask, sum, 2);
+    if (tig == 0)
+        reinterpret_cast<float *>(frag + 8 * 32)[gid] = static_cast<float>(-128 * sum) * 0x1p-24f;
+}
+
+// A warp's ring of tiles in shared memory, copied 16 bytes a lane, so that what is in
+// flight takes no registers.  (Bulk copies of a page's 256 bytes each came in at 43
+// GB/s an SM: one in 11 cycles.)  Pages 2r and 2r + 1 of a tile lie 320 bytes apart
+// and the next pair 576 further, so that the eight lanes of a read, four a page, meet
+// different banks.
+constexpr int kStages = 2;
+constexpr uint32_t kStageBytes = 8 * 576;
+
+struct TileRing {
+    uint32_t data;                       // shared-memory address
+    float step[kStages];                 // of page lane mod 16 of each stage's tile
+
+    // Asks for the tile whose page ids lanes l and l + 16 hold for page l; with
+    // `there` false for nothing.  One call a turn, so that the turns can be counted.
+    __device__ __forceinline__ void ask(const SelectParams &p, int h, bool there, int phys, int stage, int lane)
+    {
+        if (there) {
+            __syncwarp();                // (the stage has been read)
+            const uint32_t dst = data + stage * kStageBytes + (lane >> 4) * 320 + (lane & 15) * 16;
+#pragma unroll
+            for (int k = 0; k < kTile / 2; ++k) {
+                const int id = __shfl_sync(kFullMask, phys, 2 * k + (lane >> 4));
+                const int8_t *src = p.bounds + (static_cast<size_t>(id) * p.hkv + h) * (2 * kHeadDim) + (lane & 15) * 16;
+                asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + k * 576), "l"(src) : "memory");
+            }
+            step[stage] = __ldg(p.steps + static_cast<size_t>(phys) * p.hkv + h);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
     }
+
+    // Waits for the oldest tile asked for.
+    __device__ __forceinline__ void wait() const
+    {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+        __syncwarp();
+    }
+
+    // The stage's tile into registers, after which the stage is free: a lane (gid,
+    // tig) takes bytes 16 tig + 64 i .. + 15, i = 0 .. 3, of pages gid and gid + 8
+    // (the operand's K order is free as long as the queries' is the same).
+    __device__ __forceinline__ void read(int stage, uint4 (&a)[2][4], int lane) const
+    {
+        const int gid = lane >> 2;
+        const uint32_t at = data + stage * kStageBytes + (gid >> 1) * 576 + (gid & 1) * 320 + 16 * (lane & 3);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            a[0][i] = lds128(at + 64 * i);
+            a[1][i] = lds128(at + 4 * 576 + 64 * i);
+        }
+    }
+};
+
+// The score of a tile's page lane mod 16; query(i): the queries' word i of the lane,
+// from: what the sums of heads 2tig and 2tig + 1 start from.  (8-bit integer matrix
+// instructions: three tokens and more a sequence take 1.4 times as long.)  A byte plus
+// 128, with a zero byte above it, is the f16 number (byte + 128) * 2^-24: two
+// permutations for four bytes.  The sums start from -128 sum w and are exact multiples
+// of 2^-24 below 1.  What no bounds of finite keys give (a step that is NaN or
+// infinite) is held to finite numbers.
+template <class Query>
+__device__ __forceinline__ float score_of(const uint4 (&tile)[2][4], Query query, float2 from, float step, int lane)
+{
+    float d[4][4] = {{from.x, from.y, from.x, from.y}, {0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint4 w0 = query(2 * i), w1 = query(2 * i + 1);
+        const uint32_t a[4] = {tile[0][i].x, tile[0][i].y, tile[0][i].z, tile[0][i].w};
+        const uint32_t b[4] = {tile[1][i].x, tile[1][i].y, tile[1][i].z, tile[1][i].w};
+        const uint32_t w[8] = {w0.x, w0.y, w0.z, w0.w, w1.x, w1.y, w1.z, w1.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t x = a[k] ^ 0x80808080u, y = b[k] ^ 0x80808080u;
+            mma_f16_16816(d[k], __byte_perm(x, 0, 0x4140), __byte_perm(y, 0, 0x4140), __byte_perm(x, 0, 0x4342),
+                          __byte_perm(y, 0, 0x4342), w[2 * k], w[2 * k + 1]);
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+        d[0][e] = (d[0][e] + d[1][e]) + (d[2][e] + d[3][e]);
+    float lo = fmaxf(d[0][0], d[0][1]), hi = fmaxf(d[0][2], d[0][3]);
+#pragma unroll
+    for (int o = 1; o < 4; o <<= 1) {
+        lo = fmaxf(lo, __shfl_xor_sync(kFullMask, lo, o));
+        hi = fmaxf(hi, __shfl_xor_sync(kFullMask, hi, o));
+    }
+    // page gid's is in lanes 4 gid ..
+    const float s0 = __shfl_sync(kFullMask, lo, 4 * (lane & 7)), s1 = __shfl_sync(kFullMask, hi, 4 * (lane & 7));
+    constexpr float kLargest = 3.40282347e+38f;
+    return fminf(fmaxf(__fmul_rn(((lane & 8) ? s1 : s0) * 0x1p24f, step), -kLargest), kLargest) + 0.f;   // (-0 is 0)
+}
+
+// A page id of a table, 0 for one that is not there.
+__device__ __forceinline__ int checked(const SelectParams &p, int phys)
+{
+    if (static_cast<unsigned>(phys) < static_cast<unsigned>(p.num_pages))
+        return phys;
+    report(p.dev_status, NVFP4KV_DEV_BAD_PAGE);
+    return 0;
 }
 
 // ---- selection -----------------------------------------------------------------
 
-constexpr int kPickThreads = 512, kPickWarps = kPickThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kTies = 1024;              // scores of the border's bin that are ranked side by side
 
@@ -395,6 +419,7 @@ __device__ __forceinline__ float float_at(uint32_t place)
 }
 
 // Exclusive sum over the CTA of one value a thread; the total in `total`.
+template <int kThreads>
 __device__ __forceinline__ int cta_sum_before(int v, int32_t *scratch, int &total)
 {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -411,187 +436,354 @@ __device__ __forceinline__ int cta_sum_before(int v, int32_t *scratch, int &tota
     __syncthreads();
     int before = 0;
     total = 0;
-    for (int i = 0; i < kPickWarps; ++i) {
+    for (int i = 0; i < kThreads / 32; ++i) {
         before += i < warp ? scratch[i] : 0;
         total += scratch[i];
     }
     return before + x - v;
 }
 
-// One CTA a (query token, kv head).  Counts of the scores in 2,048 equal parts of
-// [least, largest] say, from the top, in which part the last wanted one lies; what
-// lies above is taken, what lies in that part is ranked pair by pair.  (The part
-// of a score never falls as the score grows, whatever its subtraction and product
-// round.)  Where more than kTies scores share the part, it is cut into 2,048
-// again, by the order of floats, until they fit or are one number, of which the
-// lowest pages are taken.
-__global__ void __launch_bounds__(kPickThreads) page_pick_kernel(const __grid_constant__ SelectParams p)
+// What the CTAs of a cluster show one another while they select, and a CTA's scratch.
+struct alignas(16) PickShared {
+    int32_t scratch[32], count[kBins];
+    uint32_t tie_key[kTies];
+    int32_t tie_page[kTies];
+    int32_t found[4];                    // the border's part, scores above it, scores in it; ties that are kept
+    uint32_t least, most;                // of this CTA's scores, as places in the order of floats
+    uint32_t part_least, part_most;      // ... of those in the border's part
+    int32_t equal, listed;               // scores that are the one number left; entries of the list
+};
+
+// A query token and kv head's selection, by a cluster: this CTA has the scores of
+// pages p0 .. p0 + count - 1 in `score`.
+struct Selection {
+    const float *score;
+    uint32_t *taken;                     // a bit a page of this CTA, all clear
+    int p0, count;
+    int pages, first, last;              // of the sequence; pages that are taken in any case
+    uint32_t rank, ranks;
+};
+
+// The CTAs of the cluster meet.
+__device__ __forceinline__ void meet(uint32_t ranks)
 {
-    extern __shared__ uint32_t taken[];                          // a bit a page
-    __shared__ int32_t scratch[kPickWarps], count[kBins];
-    __shared__ uint32_t tie_key[kTies];
-    __shared__ int32_t tie_page[kTies];
-    __shared__ uint32_t edge[2];
-    __shared__ int32_t found[3];
+    if (ranks > 1)
+        cluster_sync();
+    else
+        __syncthreads();
+}
+
+// Finds the `want` best of the candidates, all pages but the first and last ones (there
+// are more of them), and lists them with those, ascending, at `out`.  Counts of the
+// scores in 2,048 equal parts of [least, largest] say, from the top, in which part the
+// last wanted one lies; what lies above is taken, what lies in that part is ranked pair
+// by pair.  (The part of a score, f below cut to a whole number, never falls as the
+// score grows, whatever its subtraction and product round.)  Where more than kTies
+// scores share the part, its places in the order of floats are cut into 2,048 parts,
+// again until they fit or are one number, of which the lowest pages are taken.  Every
+// CTA adds up all CTAs' counts and comes to the same border.
+template <int kThreads>
+__device__ __forceinline__ void pick_pages(const Selection &s, int want, int32_t *out, PickShared &sh)
+{
     const int tid = threadIdx.x, lane = tid & 31;
-    const long long unit = blockIdx.x;                           // (sequence, token, kv head)
-    const long long row = unit / p.hkv;
-    const int b = static_cast<int>(row / p.q_len), t = static_cast<int>(row - static_cast<long long>(b) * p.q_len);
-    pdl_wait();
-    pdl_launch_dependents();
-    const int pages = pages_seen(clamp_len(__ldg(p.seq_lens + b), p.max_pages * kPageSize), p.q_len, t);
-    int32_t *out = p.pages + unit * p.budget;
-    if (pages <= p.budget) {
-        for (int i = tid; i < p.budget; i += kPickThreads)
-            out[i] = i < pages ? i : -1;
-        return;
-    }
-    const float *score = p.scores + unit * p.score_stride;
-    const int lo = p.first, hi = pages - p.last;                 // the candidates
-    int want = p.budget - p.first - p.last;                      // fewer than there are
-    const int words = (pages + 31) / 32;
-    for (int i = tid; i < words; i += kPickThreads)
-        taken[i] = 0;
-    // fn(page, its score's place in the order of floats)
+    const int lo = max(s.first - s.p0, 0), hi = min(s.pages - s.last - s.p0, s.count);     // this CTA's candidates
+    const uint32_t base = smem_addr(&sh);
+    auto peer = [&](const void *field, uint32_t k) { return in_cta(base + static_cast<uint32_t>(
+        static_cast<const uint8_t *>(field) - reinterpret_cast<const uint8_t *>(&sh)), k); };
     auto for_scores = [&](auto fn) {
-        for (int i = lo + tid; i < hi; i += kPickThreads)
-            fn(i, order_of(__ldcg(score + i)));
+#pragma unroll 4
+        for (int i = lo + tid; i < hi; i += kThreads)
+            fn(i, s.score[i]);
     };
-    // edge: the least and the largest of those that in(place) holds for
-    auto find_edges = [&](auto in) {
-        uint32_t least = 0xffffffffu, most = 0;
-        __syncthreads();
+    // A place range of the cluster, from each CTA's.
+    auto range_of = [&](const uint32_t &least, const uint32_t &most, uint32_t &a, uint32_t &z) {
+        a = 0xffffffffu;
+        z = 0;
+        for (uint32_t k = 0; k < s.ranks; ++k) {
+            a = min(a, ld_cluster_u32(peer(&least, k)));
+            z = max(z, ld_cluster_u32(peer(&most, k)));
+        }
+    };
+    auto clear = [&]() {
+        for (int i = tid; i < kBins; i += kThreads)
+            sh.count[i] = 0;
         if (tid == 0) {
-            edge[0] = 0xffffffffu;
-            edge[1] = 0;
-        }
-        __syncthreads();
-        for_scores([&](int, uint32_t k) {
-            if (in(k)) {
-                least = min(least, k);
-                most = max(most, k);
-            }
-        });
-        least = __reduce_min_sync(kFullMask, least);
-        most = __reduce_max_sync(kFullMask, most);
-        if (lane == 0) {
-            atomicMin(edge, least);
-            atomicMax(edge + 1, most);
+            sh.found[3] = 0;
+            sh.part_least = 0xffffffffu;
+            sh.part_most = 0;
         }
         __syncthreads();
     };
-    find_edges([](uint32_t) { return true; });
-    uint32_t from = edge[0], to = edge[1];                       // the places that are still open, both ends among them
-    bool equal_parts = true;                                     // of numbers; later, of places
-    while (want > 0 && from < to) {
-        const float base = float_at(from), by = kBins / (float_at(to) - base);
-        const uint32_t span = to - from;
-        const int shift = span < kBins ? 0 : 21 - __clz(span);   // at most 2,048 parts of 2^shift places
-        auto part_of = [&](uint32_t k) {                         // -1 under the open ones, kBins above
-            if (k < from || k > to)
-                return k < from ? -1 : kBins;
-            return equal_parts ? static_cast<int>(fminf(fmaxf((float_at(k) - base) * by, 0.f), kBins - 1.f))
-                               : static_cast<int>((k - from) >> shift);
-        };
-        __syncthreads();
-        for (int i = tid; i < kBins; i += kPickThreads)
-            count[i] = 0;
-        if (tid == 0)
-            found[2] = 0;
-        __syncthreads();
-        for_scores([&](int, uint32_t k) {
-            const int part = part_of(k);
-            if (part >= 0 && part < kBins)
-                atomicAdd(&count[part], 1);
-        });
-        __syncthreads();
-        // the part where the count from the top reaches `want`
-        int mine[kBins / kPickThreads], sum = 0, total;
-        const int top = kBins - 1 - tid * (kBins / kPickThreads);
+    // The part where the count from the top reaches `want`, which loses what lies
+    // above; scores in the part.
+    int border = 0, inside = 0;
+    auto find_border = [&]() {
+        meet(s.ranks);
+        constexpr int kEach = kBins / kThreads;
+        int mine[kEach], sum = 0, total;
+        const int top = kBins - 1 - tid * kEach;
 #pragma unroll
-        for (int k = 0; k < kBins / kPickThreads; ++k) {
-            mine[k] = count[top - k];
+        for (int k = 0; k < kEach; ++k) {
+            mine[k] = 0;
+            for (uint32_t r = 0; r < s.ranks; ++r)
+                mine[k] += static_cast<int>(ld_cluster_u32(peer(&sh.count[top - k], r)));
             sum += mine[k];
         }
-        int before = cta_sum_before(sum, scratch, total);
+        int before = cta_sum_before<kThreads>(sum, sh.scratch, total);
 #pragma unroll
-        for (int k = 0; k < kBins / kPickThreads; ++k) {
+        for (int k = 0; k < kEach; ++k) {
             if (before < want && want <= before + mine[k]) {
-                found[0] = top - k;
-                found[1] = before;
+                sh.found[0] = top - k;
+                sh.found[1] = before;
+                sh.found[2] = mine[k];
             }
             before += mine[k];
         }
         __syncthreads();
-        const int border = found[0], inside = count[border];
-        want -= found[1];
-        const bool whole = inside == want, rank = !whole && inside <= kTies;
-        for_scores([&](int i, uint32_t k) {
-            const int part = part_of(k);
-            if (part < border || part == kBins)                  // (above the open ones: taken in an earlier turn)
-                return;
-            if (part > border || whole) {
-                atomicOr(&taken[i >> 5], 1u << (i & 31));
-            } else if (rank) {
-                const int n = atomicAdd(&found[2], 1);
-                tie_key[n] = k;
-                tie_page[n] = i;
-            }
-        });
-        __syncthreads();
-        if (rank)
-            for (int x = tid; x < inside; x += kPickThreads) {
-                const uint32_t k = tie_key[x];
-                const int page = tie_page[x];
-                int r = 0;
-                for (int y = 0; y < inside; ++y)
-                    r += tie_key[y] > k || (tie_key[y] == k && tie_page[y] < page);
-                if (r < want)
-                    atomicOr(&taken[page >> 5], 1u << (page & 31));
-            }
-        if (whole || rank) {
-            want = 0;
+        border = sh.found[0];
+        inside = sh.found[2];
+        want -= sh.found[1];
+    };
+    auto take = [&](int i) { atomicOr(&s.taken[i >> 5], 1u << (i & 31)); };
+    // A score in the border's part: taken with all of it, kept to be ranked, or only
+    // noted in the part's range.
+    auto at_border = [&](int i, float x) {
+        const uint32_t k = order_of(x);
+        if (inside == want) {
+            take(i);
+        } else if (inside <= kTies) {
+            const int n = atomicAdd(&sh.found[3], 1);
+            sh.tie_key[n] = k;
+            sh.tie_page[n] = s.p0 + i;
         } else {
-            find_edges([&](uint32_t k) { return part_of(k) == border; });
-            from = edge[0];
-            to = edge[1];
-            equal_parts = false;
+            atomicMin(&sh.part_least, k);
+            atomicMax(&sh.part_most, k);
         }
-    }
-    // (one number left) the lowest `want` of the pages that have it
-    for (int i0 = lo; i0 < hi && want > 0; i0 += kPickThreads) {
-        const int i = i0 + tid;
-        const bool is = i < hi && order_of(__ldcg(score + i)) == from;
-        int total;
-        const int before = cta_sum_before(is, scratch, total);
-        if (is && before < want)
-            atomicOr(&taken[i >> 5], 1u << (i & 31));
-        want -= total;
+    };
+    // What is left of the border's part; false when it is still to be cut.
+    auto finish = [&]() {
+        meet(s.ranks);
+        if (inside == want)
+            return true;
+        if (inside > kTies)
+            return false;
+        const int mine = sh.found[3];
+        for (int x = tid; x < mine; x += kThreads) {
+            const uint32_t k = sh.tie_key[x];
+            const int page = sh.tie_page[x];
+            int r = 0;
+            for (uint32_t c = 0; c < s.ranks; ++c) {
+                const int n = static_cast<int>(ld_cluster_u32(peer(&sh.found[3], c)));
+                const uint32_t keys = peer(sh.tie_key, c), pages = peer(sh.tie_page, c);
+                for (int y = 0; y < n; ++y) {
+                    const uint32_t other = ld_cluster_u32(keys + 4 * y);
+                    r += other > k || (other == k && static_cast<int>(ld_cluster_u32(pages + 4 * y)) < page);
+                }
+            }
+            if (r < want)
+                take(page - s.p0);
+        }
+        return true;
+    };
+
+    // the range of the scores
+    uint32_t from = 0xffffffffu, to = 0;                         // the places that are still open, both ends among them
+    for_scores([&](int, float x) {
+        from = min(from, order_of(x));
+        to = max(to, order_of(x));
+    });
+    if (tid == 0) {
+        sh.least = 0xffffffffu;
+        sh.most = 0;
     }
     __syncthreads();
-    // the list, ascending
-    int done = 0;
-    for (int w0 = 0; w0 < words; w0 += kPickThreads) {
-        const int w = w0 + tid;
-        uint32_t bits = 0;
-        if (w < words) {
-            bits = taken[w];
-            const int p0 = 32 * w;
-            // first pages, and last ones
-            bits |= p0 + 32 <= p.first ? 0xffffffffu : (p0 < p.first ? (1u << (p.first - p0)) - 1u : 0u);
-            const uint32_t below = hi >= p0 + 32 ? 0xffffffffu : (hi > p0 ? (1u << (hi - p0)) - 1u : 0u);
-            const uint32_t there = pages >= p0 + 32 ? 0xffffffffu : (1u << (pages - p0)) - 1u;
-            bits |= there & ~below;
+    from = __reduce_min_sync(kFullMask, from);
+    to = __reduce_max_sync(kFullMask, to);
+    if (lane == 0) {
+        atomicMin(&sh.least, from);
+        atomicMax(&sh.most, to);
+    }
+    clear();
+    meet(s.ranks);
+    range_of(sh.least, sh.most, from, to);
+    bool done = want <= 0;
+    if (!done && from < to) {
+        const float least = float_at(from), by = kBins / (float_at(to) - least);   // (0 where the difference passes fp32)
+        for_scores([&](int, float x) {
+            const int part = static_cast<int>(fminf((x - least) * by, kBins - 1.f));
+            atomicAdd(&sh.count[part & (kBins - 1)], 1);
+        });
+        find_border();
+        const float below = border > 0 ? static_cast<float>(border) : -INFINITY;
+        const float above = border < kBins - 1 ? static_cast<float>(border + 1) : NAN;
+        for_scores([&](int i, float x) {
+            const float f = (x - least) * by;
+            if (f >= above)
+                take(i);
+            else if (!(f < below))
+                at_border(i, x);
+        });
+        done = finish();
+        if (!done)
+            range_of(sh.part_least, sh.part_most, from, to);
+    }
+    while (!done && from < to) {
+        const uint32_t span = to - from;
+        const int shift = span < kBins ? 0 : 21 - __clz(span);   // at most 2,048 parts of 2^shift places
+        meet(s.ranks);                                           // (the counts and the range have been read)
+        clear();
+        for_scores([&](int, float x) {
+            const uint32_t k = order_of(x);
+            if (k >= from && k <= to)
+                atomicAdd(&sh.count[(k - from) >> shift], 1);
+        });
+        find_border();
+        const uint32_t b0 = from + (static_cast<uint32_t>(border) << shift);
+        const uint32_t b1 = min(to, b0 + ((1u << shift) - 1u));
+        for_scores([&](int i, float x) {
+            const uint32_t k = order_of(x);
+            if (k > b1 && k <= to)                               // (above the open ones: taken in an earlier turn)
+                take(i);
+            else if (k >= b0 && k <= b1)
+                at_border(i, x);
+        });
+        done = finish();
+        from = b0;
+        to = b1;
+    }
+    if (!done) {
+        // one number left: the lowest `want` of the pages that have it
+        int n = 0, total;
+        for (int i = lo + tid; i < hi; i += kThreads)
+            n += order_of(s.score[i]) == from;
+        __syncthreads();
+        cta_sum_before<kThreads>(n, sh.scratch, total);
+        if (tid == 0)
+            sh.equal = total;
+        meet(s.ranks);
+        for (uint32_t k = 0; k < s.rank; ++k)
+            want -= static_cast<int>(ld_cluster_u32(peer(&sh.equal, k)));
+        for (int i0 = lo; i0 < hi && want > 0; i0 += kThreads) {
+            const int i = i0 + tid;
+            const bool is = i < hi && order_of(s.score[i]) == from;
+            const int before = cta_sum_before<kThreads>(is, sh.scratch, total);
+            if (is && before < want)
+                take(i);
+            want -= total;
         }
-        int total;
-        int n = done + cta_sum_before(__popc(bits), scratch, total);
+    }
+    __syncthreads();
+    // the list, ascending: first how many entries each CTA has
+    auto word = [&](int w) {
+        uint32_t bits = s.taken[w];
+        const int page = s.p0 + 32 * w, held = s.count - 32 * w;
+        auto under = [](int n) { return n >= 32 ? 0xffffffffu : (n > 0 ? (1u << n) - 1u : 0u); };
+        bits |= under(s.first - page) | ~under(s.pages - s.last - page);
+        return bits & under(held);
+    };
+    const int words = (s.count + 31) / 32;
+    int n0 = 0, total;
+    for (int w = tid; w < words; w += kThreads)
+        n0 += __popc(word(w));
+    cta_sum_before<kThreads>(n0, sh.scratch, total);
+    if (tid == 0)
+        sh.listed = total;
+    meet(s.ranks);
+    n0 = 0;
+    for (uint32_t k = 0; k < s.rank; ++k)
+        n0 += static_cast<int>(ld_cluster_u32(peer(&sh.listed, k)));
+    for (int w0 = 0; w0 < words; w0 += kThreads) {
+        const int w = w0 + tid;
+        uint32_t bits = w < words ? word(w) : 0;
+        int n = n0 + cta_sum_before<kThreads>(__popc(bits), sh.scratch, total);
         while (bits) {
             const int k = __ffs(bits) - 1;
             bits &= bits - 1;
-            out[n++] = 32 * w + k;
+            out[n++] = s.p0 + 32 * w + k;
         }
-        done += total;
+        n0 += total;
     }
+    meet(s.ranks);                                               // (nobody leaves while it is read)
+}
+
+// A cluster a (query token, kv head): its CTAs share out the tiles, work their scores
+// out, which stay in shared memory, and select together.  Lengths and block tables may
+// be read ahead of the kernel before, as by the decode; bounds and queries may not.
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads, kThreads == 512 ? 1 : 2) page_select_kernel(const __grid_constant__ SelectParams p)
+{
+    extern __shared__ __align__(128) uint8_t ssmem[];
+    __shared__ PickShared sh;
+    constexpr int kWarps = kThreads / 32;
+    uint4 *frag = reinterpret_cast<uint4 *>(ssmem + kWarps * kStages * kStageBytes);      // [kQueryWords]
+    // page ids, and once a tile is worked on its scores
+    uint32_t *place = reinterpret_cast<uint32_t *>(frag + kQueryWords);
+    uint32_t *taken = place + p.chunk_tiles * kTile;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    pdl_launch_dependents();
+    const uint32_t rank = cluster_rank(), ranks = cluster_size();
+    const long long unit = blockIdx.x / ranks, row = unit / p.hkv;
+    const int h = static_cast<int>(unit - row * p.hkv);
+    const int b = static_cast<int>(row / p.q_len), t = static_cast<int>(row - static_cast<long long>(b) * p.q_len);
+    const int len = __ldg(p.seq_lens + b), max_len = p.max_pages * kPageSize;
+    if (h == 0 && t == 0 && rank == 0 && tid == 0 && (len < 0 || len > max_len))
+        report(p.dev_status, NVFP4KV_DEV_BAD_LEN);
+    const int pages = pages_seen(clamp_len(len, max_len), p.q_len, t);
+    int32_t *out = p.pages + unit * p.budget;
+    if (pages <= p.budget) {
+        pdl_wait();
+        for (int i = rank * kThreads + tid; i < p.budget; i += ranks * kThreads)
+            out[i] = i < pages ? i : -1;
+        return;
+    }
+    // this CTA's tiles (chunk_tiles at most) and pages
+    const int all = (pages + kTile - 1) / kTile;
+    const int begin = static_cast<int>(static_cast<long long>(all) * rank / ranks);
+    const int tiles = static_cast<int>(static_cast<long long>(all) * (rank + 1) / ranks) - begin;
+    const int p0 = begin * kTile, count = min(tiles * kTile, pages - p0);
+    for (int i = tid; i < (tiles * kTile + 31) / 32; i += kThreads)
+        taken[i] = 0;
+    const int32_t *table = p.block_table + static_cast<size_t>(b) * p.max_pages + p0;
+    for (int i = tid; i < tiles * kTile; i += kThreads)
+        place[i] = i < count ? checked(p, __ldg(table + i)) : 0;
+    __syncthreads();
+    pdl_wait();
+    TileRing ring{smem_addr(ssmem) + warp * kStages * kStageBytes, {}};
+#pragma unroll
+    for (int k = 0; k < kStages; ++k) {
+        const int tile = warp + k * kWarps;
+        ring.ask(p, h, tile < tiles, tile < tiles ? place[tile * kTile + (lane & 15)] : 0, k, lane);
+    }
+    if (warp == kWarps - 1)
+        load_queries(p, b, t, h, frag, lane);
+    __syncthreads();
+    // (read from shared memory for every tile, the queries would take as much of its
+    // bandwidth as the tiles)
+    uint4 w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        w[i] = frag[i * 32 + lane];
+    const float2 from = reinterpret_cast<const float2 *>(frag + 8 * 32)[lane & 3];
+    for (int tile = warp; tile < tiles;) {
+#pragma unroll
+        for (int k = 0; k < kStages; ++k) {
+            if (tile >= tiles)
+                break;
+            ring.wait();
+            uint4 a[2][4];
+            ring.read(k, a, lane);
+            const float step = ring.step[k];
+            const int next = tile + kStages * kWarps;
+            ring.ask(p, h, next < tiles, next < tiles ? place[next * kTile + (lane & 15)] : 0, k, lane);
+            const float score = score_of(a, [&](int i) { return w[i]; }, from, step, lane);
+            if (lane < 16)
+                place[tile * kTile + lane] = __float_as_uint(score);
+            tile += kWarps;
+        }
+    }
+    __syncthreads();
+    const Selection s{reinterpret_cast<const float *>(place), taken, p0, count, pages, p.first, p.last, rank, ranks};
+    pick_pages<kThreads>(s, p.budget - p.first - p.last, out, sh);
 }
 
 } // namespace
@@ -606,35 +798,48 @@ cudaError_t launch_page_bounds_fp8_block(const BoundsParams &p, cudaStream_t s)
     return launch_bounds<Fp8BlockKeys>(p, s);
 }
 
-int score_row_stride(int max_pages)
+template <int kThreads>
+static cudaError_t launch_select(const SelectParams &p, long long units, size_t smem, int ranks, cudaStream_t s)
 {
-    return (max_pages + kTile - 1) / kTile * kTile;
-}
-
-cudaError_t launch_select_pages(const SelectParams &p, cudaStream_t s)
-{
-    const size_t smem = static_cast<size_t>(p.q_len) * 4 * 32 * sizeof(uint4) +
-                        (kPrefixScratch + static_cast<size_t>(p.batch) + 1) * sizeof(int32_t);
-    if (smem > 48 * 1024) {
-        const cudaError_t e = cudaFuncSetAttribute(page_scores_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                   static_cast<int>(smem));
-        if (e != cudaSuccess)
-            return e;
-    }
-    const long long tiles = static_cast<long long>(p.batch) * p.hkv * ((p.max_pages + kTile - 1) / kTile);
-    long long grid = static_cast<long long>(sm_count()) * 3;
-    grid = max(1LL, min(grid, (tiles + kScoreWarps - 1) / kScoreWarps));
-    cudaError_t e = launch_pdl(page_scores_kernel, dim3(static_cast<unsigned>(grid)), dim3(kScoreThreads), smem, s, p);
+    auto kernel = page_select_kernel<kThreads>;
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess)
         return e;
-    const size_t bits = (static_cast<size_t>(p.max_pages) + 31) / 32 * 4;
-    if (bits > 16 * 1024) {
-        e = cudaFuncSetAttribute(page_pick_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bits));
-        if (e != cudaSuccess)
-            return e;
-    }
-    return launch_pdl(page_pick_kernel, dim3(static_cast<unsigned>(p.batch * p.q_len * p.hkv)), dim3(kPickThreads), bits, s,
-                      p);
+    return launch_cluster(kernel, dim3(static_cast<unsigned>(units * ranks)), dim3(kThreads), ranks, smem, s, p);
+}
+
+// CTAs of 512 threads, one an SM, or of 256, two an SM, and how many a cluster.  A
+// CTA takes a page in 3.6 ns, a meeting of the cluster costs a microsecond: more than
+// one CTA pays from some 2,048 pages on (8 heads of one sequence, 2,000 pages: 13.7 us
+// with one, 12.3 with two, 12.7 with four; 8,125 pages: 34.8, 23.2, 18.8).  Where the
+// SMs are taken by one CTA each, smaller ones share a long sequence better (80 x 10,240
+// pages: 57 us with one CTA of 512, 54 with three of 256; 96 x 2,000: 16.4 and 26.6),
+// and where there are more units than SMs, two at a time an SM run beside each other
+// (560 x 2,000 pages: 74 us with 512 threads, 62 with 256).
+cudaError_t launch_select_pages(const SelectParams &p, cudaStream_t s)
+{
+    const long long units = static_cast<long long>(p.batch) * p.q_len * p.hkv;
+    const int tiles = (p.max_pages + kTile - 1) / kTile;
+    const long long sms = max(1, sm_count()), fit = max(1LL, sms / units);
+    const bool lengthy = p.max_pages > 6144;
+    const int threads = units > sms || (fit == 1 && lengthy) ? 256 : 512;
+    long long ranks = threads == 512 ? min(fit, (p.max_pages + 1023LL) / 2048) : (lengthy ? 2 * sms / units : 1);
+    ranks = max(1LL, min(8LL, ranks));
+    SelectParams q = p;
+    auto bytes = [&]() {
+        q.chunk_tiles = (tiles + static_cast<int>(ranks) - 1) / static_cast<int>(ranks);
+        return threads / 32 * kStages * kStageBytes + kQueryWords * sizeof(uint4) +
+               static_cast<size_t>(q.chunk_tiles) * kTile * 4 + (static_cast<size_t>(q.chunk_tiles) * kTile + 31) / 32 * 4;
+    };
+    constexpr size_t kMost = 227 * 1024 - sizeof(PickShared) - 1024;
+    static_assert(512 / 32 * kStages * kStageBytes + kQueryWords * sizeof(uint4) +
+                          NVFP4KV_MAX_SELECT_PAGES / 8 / 8 * 33 + 1024 <= kMost, "the largest call fits eight CTAs");
+    while (bytes() > kMost && ranks < 8)
+        ++ranks;
+    const size_t smem = bytes();
+    return threads == 256 ? launch_select<256>(q, units, smem, static_cast<int>(ranks), s)
+                          : launch_select<512>(q, units, smem, static_cast<int>(ranks), s);
 }
 
 } // namespace nvfp4kv

@@ -134,8 +134,7 @@ def make_bounds(pages, hkv, seed, values=127, steps=None):
 def picks(b, q, bt, lens, budget, first, last, q_len, status=None):
     B, hkv = len(lens), b.num_kv_heads
     pages = torch.full((B, q_len, hkv, budget), 12345, dtype=torch.int32, device=DEV)
-    ws = nv.new_select_workspace(B, q_len, hkv, bt.shape[1], device=DEV).fill_(0xFF)
-    nv.nvfp4kv_select_pages(b, q, i32(bt), i32(lens), pages, ws, first_pages=first, last_pages=last, dev_status=status)
+    nv.nvfp4kv_select_pages(b, q, i32(bt), i32(lens), pages, first_pages=first, last_pages=last, dev_status=status)
     return pages.cpu().numpy()
 
 
@@ -345,13 +344,13 @@ def test_a_step_captured_and_replayed():
     q = torch.zeros((B, hq, 128), dtype=torch.bfloat16, device=DEV)
     out = torch.zeros((B, hq, 128), device=DEV)
     pages = torch.zeros((B, hkv, budget), dtype=torch.int32, device=DEV)
-    ws, sw = nv.new_workspace(device=DEV), nv.new_select_workspace(B, 1, hkv, maxp, device=DEV)
+    ws = nv.new_workspace(device=DEV)
 
     def step():
         nv.nvfp4kv_plan_step(ctx, new, table, pool_pages, free, num_free, num_free, seq, ptr, slots, dev_status=status)
         nv.nvfp4kv_quantize_append(cache, k, v, slots, status)
         nv.nvfp4kv_page_bounds(cache, b, table, seq, from_lens=ctx, dev_status=status)
-        nv.nvfp4kv_select_pages(b, q, table, seq, pages, sw, dev_status=status)
+        nv.nvfp4kv_select_pages(b, q, table, seq, pages, dev_status=status)
         nv.nvfp4kv_selected_decode(cache, q, table, seq, pages, out, ws, dev_status=status)
         ctx.copy_(seq)
 

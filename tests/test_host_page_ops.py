@@ -52,9 +52,9 @@ def page_bounds(name, b=None, table=A[6], pages=4, begin=A[5], lens=A[7], batch=
 
 
 def select_pages(b=None, q=A[3], batch=2, q_len=1, hq=8, table=A[6], pages=100, lens=A[7], budget=8, first=1, last=1,
-                 out=A[4], ws=A[8], ws_bytes=1 << 30):
+                 out=A[4]):
     return nv.load().nvfp4kv_select_pages(the_bounds() if b is None else b, q, batch, q_len, hq, table, pages, lens, budget,
-                                          first, last, out, ws, ws_bytes, None, None)
+                                          first, last, out, None, None)
 
 
 def selected(name, q=A[3], batch=2, q_len=1, hq=8, table=A[6], pages=100, lens=A[7], lists=A[9], budget=8, scale=0.1,
@@ -120,25 +120,12 @@ def test_page_bounds(name):
     (dict(q_len=0), INVALID), (dict(q_len=9), UNSUPPORTED), (dict(batch=5000, q_len=2), UNSUPPORTED), (dict(batch=-1), INVALID),
     (dict(hq=7), INVALID), (dict(hq=0), INVALID), (dict(hq=18), UNSUPPORTED), (dict(budget=0), INVALID),
     (dict(first=-1), INVALID), (dict(last=-1), INVALID), (dict(first=5, last=4), INVALID),
-    (dict(first=2 ** 31 - 1, last=2 ** 31 - 1), INVALID), (dict(pages=0), INVALID), (dict(pages=2 ** 20 + 1), UNSUPPORTED),
+    (dict(first=2 ** 31 - 1, last=2 ** 31 - 1), INVALID), (dict(pages=0), INVALID), (dict(pages=2 ** 16 + 1), UNSUPPORTED),
     (dict(q=None), INVALID), (dict(q=A[3] + 8), INVALID), (dict(table=None), INVALID), (dict(lens=A[7] + 2), INVALID),
-    (dict(out=None), INVALID), (dict(out=A[4] + 2), INVALID), (dict(ws=None), WORKSPACE), (dict(ws=A[8] + 4), WORKSPACE),
-    (dict(ws_bytes=100), WORKSPACE), (dict(out=A[8]), INVALID), (dict(out=A[6] + 16), INVALID), (dict(ws=A[1] + 256), INVALID),
-    (dict(batch=0, q=None, table=None, lens=None, out=None, ws=None), OK)])
+    (dict(out=None), INVALID), (dict(out=A[4] + 2), INVALID), (dict(out=A[6] + 16), INVALID), (dict(out=A[1] + 256), INVALID),
+    (dict(out=A[3]), INVALID), (dict(batch=0, q=None, table=None, lens=None, out=None), OK)])
 def test_select(kw, want):
     assert select_pages(**kw) == want
-
-
-def test_select_workspace_size():
-    size = nv.nvfp4kv_select_pages_workspace_size
-    assert size(2, 1, 2, 100) == 2 * 2 * 112 * 4         # rows of whole tiles of 16 pages
-    assert size(3, 4, 8, 4096) == 3 * 4 * 8 * 4096 * 4
-    for bad in ((-1, 1, 2, 100), (2, 0, 2, 100), (2, 9, 2, 100), (2, 1, 0, 100), (2, 1, 2, 0), (2, 1, 2, 2 ** 20 + 1),
-                (8192, 2, 1, 1)):
-        assert size(*bad) == 0
-    with pytest.raises(ValueError):
-        size(2 ** 32 + 2, 1, 2, 100)
-    assert select_pages(ws_bytes=2 * 2 * 112 * 4 - 1) == WORKSPACE
 
 
 @pytest.mark.parametrize("name", ["nvfp4kv_selected_decode", "fp8bkv_selected_decode"])
