@@ -292,12 +292,24 @@ class FP8Cache(NVFP4Cache):
         self._c = self._struct(pool.data_ptr(), self.num_pages, self.num_kv_heads, PAGE_SIZE, HEAD_DIM)
 
 
+def _whole(t, name, dtype) -> None:
+    """Check a tensor whose address a handle keeps: type, contiguous."""
+    if str(t.dtype) != "torch." + dtype:
+        raise TypeError(f"{name}: expected torch.{dtype}, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+
+
 class FP8BlockCache(FP8Cache):
     """An FP8-E4M3 pool with a scale for each page and kv head: uint8
     [num_pages][num_kv_heads][FP8_BLOCK_RECORD_BYTES] records."""
 
     record_bytes = FP8_BLOCK_RECORD_BYTES
     _struct = _Fp8BlockCache
+
+    def __init__(self, pool):
+        _whole(pool, "pool", "uint8")
+        super().__init__(pool)
 
 
 class PageBounds:
@@ -306,8 +318,13 @@ class PageBounds:
     [num_pages][num_kv_heads]."""
 
     def __init__(self, bounds, steps):
-        self.bounds, self.steps = bounds, steps
+        _whole(bounds, "bounds", "int8")
+        _whole(steps, "steps", "float32")
         self.num_pages, self.num_kv_heads = steps.shape
+        if bounds.shape != (self.num_pages, self.num_kv_heads, 2, HEAD_DIM) or bounds.device != steps.device:
+            raise ValueError(f"bounds: expected shape {(self.num_pages, self.num_kv_heads, 2, HEAD_DIM)} on "
+                             f"{steps.device}, got {tuple(bounds.shape)} on {bounds.device}")
+        self.bounds, self.steps = bounds, steps
         self._c = _Bounds(bounds.data_ptr(), steps.data_ptr(), self.num_pages, self.num_kv_heads)
         self.c = ctypes.byref(self._c)
 
@@ -689,12 +706,19 @@ def nvfp4kv_qk_norm_rope_append(cache: NVFP4Cache, q, k, v, positions, slot_mapp
     _check(st, "nvfp4kv_qk_norm_rope_append")
 
 
-def _pool(cache, kind):
-    """(cache, name, shape) of a cache argument's pool for _tensors."""
+def _kind(cache, kind, dev) -> None:
+    """Check a cache argument: of its kind (another one's records would be
+    misread), on device dev.  (Its pool was checked as it was made.)"""
     if type(cache).record_bytes != kind.record_bytes:
         raise TypeError(f"cache: expected {kind.__name__}, got {type(cache).__name__}")
-    return cache.pool, "cache", (cache.num_pages, cache.num_kv_heads, kind.record_bytes)
+    if cache.pool.get_device() != dev or dev < 0:
+        raise ValueError("cache: not on the current CUDA device")
+    if not cache.pool.is_contiguous():
+        raise ValueError("cache: must be contiguous")
 
+
+# The calls below check each tensor in one expression of the caller's (the host's
+# time is most of a short call's); what fails goes through _tensors, which says why.
 
 def fp8bkv_append(cache: FP8BlockCache, k_new, v_new, q_indptr, block_table, seq_lens, dev_status=None,
                   stream=None) -> None:
@@ -703,18 +727,27 @@ def fp8bkv_append(cache: FP8BlockCache, k_new, v_new, q_indptr, block_table, seq
     seq_lens[b] (int32 [B], they included) into the pages of block_table int32
     [B][pages]; a page's scale rises where they need it."""
     import torch
-    pool = _pool(cache, FP8BlockCache)
-    dev = _current_device()
+    dev, i32 = _current_device(), torch.int32
+    _kind(cache, FP8BlockCache, dev)
     B, pages = block_table.shape
-    T, code = k_new.shape[0], _dtype_code(k_new)
+    T, code, dtype = k_new.shape[0], _dtype_code(k_new), k_new.dtype
     rows = (T, cache.num_kv_heads, HEAD_DIM)
-    _tensors(dev, torch.uint8, pool)
-    _tensors(dev, k_new.dtype, (k_new, "k_new", rows), (v_new, "v_new", rows))
-    _tensors(dev, torch.int32, (q_indptr, "q_indptr", (B + 1,)), (block_table, "block_table", (B, pages)),
-             (seq_lens, "seq_lens", (B,)), (dev_status, "dev_status", (1,)))
-    st = load().fp8bkv_append(cache.c, _ptr(k_new), _ptr(v_new), code, T, _ptr(q_indptr), B, _ptr(block_table), pages,
-                              _ptr(seq_lens), _ptr(dev_status), _stream(stream, dev))
-    _check(st, "fp8bkv_append")
+    if not (k_new.shape == rows and k_new.get_device() == dev and k_new.is_contiguous() and
+            v_new.dtype is dtype and v_new.shape == rows and v_new.get_device() == dev and v_new.is_contiguous()):
+        _tensors(dev, dtype, (k_new, "k_new", rows), (v_new, "v_new", rows))
+    if not (q_indptr.dtype is i32 and q_indptr.shape == (B + 1,) and q_indptr.get_device() == dev and
+            q_indptr.is_contiguous() and
+            block_table.dtype is i32 and block_table.get_device() == dev and block_table.is_contiguous() and
+            seq_lens.dtype is i32 and seq_lens.shape == (B,) and seq_lens.get_device() == dev and
+            seq_lens.is_contiguous()):
+        _tensors(dev, i32, (q_indptr, "q_indptr", (B + 1,)), (block_table, "block_table", (B, pages)),
+                 (seq_lens, "seq_lens", (B,)))
+    if dev_status is not None:
+        _tensors(dev, i32, (dev_status, "dev_status", (1,)))
+    st = load().fp8bkv_append(cache.c, k_new.data_ptr(), v_new.data_ptr(), code, T, q_indptr.data_ptr(), B,
+                              block_table.data_ptr(), pages, seq_lens.data_ptr(), _ptr(dev_status), _stream(stream, dev))
+    if st:
+        _check(st, "fp8bkv_append")
 
 
 def fp8bkv_dequant(cache: FP8BlockCache, block_table, lens, kv_indptr, k_out, v_out, dev_status=None,
@@ -723,32 +756,54 @@ def fp8bkv_dequant(cache: FP8BlockCache, block_table, lens, kv_indptr, k_out, v_
     kv_indptr[b] .. of k_out and v_out [rows][Hkv][128]: fp32, bf16, or E4M3
     (uint8 or float8_e4m3fn: the workspace of the extend calls)."""
     import torch
-    pool = _pool(cache, FP8BlockCache)
-    dev = _current_device()
+    dev, i32, dtype = _current_device(), torch.int32, k_out.dtype
+    _kind(cache, FP8BlockCache, dev)
     B, pages = block_table.shape
-    code = _dtype_code(k_out) if k_out.dtype is torch.float32 else _chunk_dtype_code(k_out)
+    code = F32 if dtype is torch.float32 else _chunk_dtype_code(k_out)
     rows = (k_out.shape[0], cache.num_kv_heads, HEAD_DIM)
-    _tensors(dev, torch.uint8, pool)
-    _tensors(dev, k_out.dtype, (k_out, "k_out", rows), (v_out, "v_out", rows))
-    _tensors(dev, torch.int32, (block_table, "block_table", (B, pages)), (lens, "lens", (B,)),
-             (kv_indptr, "kv_indptr", (B,)), (dev_status, "dev_status", (1,)))
-    st = load().fp8bkv_dequant(cache.c, _ptr(block_table), pages, _ptr(lens), _ptr(kv_indptr), B, _ptr(k_out),
-                               _ptr(v_out), code, _ptr(dev_status), _stream(stream, dev))
-    _check(st, "fp8bkv_dequant")
+    if not (k_out.shape == rows and k_out.get_device() == dev and k_out.is_contiguous() and
+            v_out.dtype is dtype and v_out.shape == rows and v_out.get_device() == dev and v_out.is_contiguous()):
+        _tensors(dev, dtype, (k_out, "k_out", rows), (v_out, "v_out", rows))
+    if not (kv_indptr.dtype is i32 and kv_indptr.shape == (B,) and kv_indptr.get_device() == dev and
+            kv_indptr.is_contiguous() and
+            block_table.dtype is i32 and block_table.get_device() == dev and block_table.is_contiguous() and
+            lens.dtype is i32 and lens.shape == (B,) and lens.get_device() == dev and lens.is_contiguous()):
+        _tensors(dev, i32, (kv_indptr, "kv_indptr", (B,)), (block_table, "block_table", (B, pages)),
+                 (lens, "lens", (B,)))
+    if dev_status is not None:
+        _tensors(dev, i32, (dev_status, "dev_status", (1,)))
+    st = load().fp8bkv_dequant(cache.c, block_table.data_ptr(), pages, lens.data_ptr(), kv_indptr.data_ptr(), B,
+                               k_out.data_ptr(), v_out.data_ptr(), code, _ptr(dev_status), _stream(stream, dev))
+    if st:
+        _check(st, "fp8bkv_dequant")
 
 
-def _query_rows(dev, q, out, batch):
-    """Check q bf16 [B][Hq][128] or [B][q_len][Hq][128] and out of its shape;
-    returns (q_len, Hq)."""
+def _attention_tensors(dev, B, max_pages, q, block_table, seq_lens, out, workspace, dev_status):
+    """Check what the decode calls share: q bf16 [B][Hq][128] or
+    [B][q_len][Hq][128], out of its shape (None: there is none); returns (q_len,
+    Hq, bytes of workspace)."""
     import torch
-    if q.dim() not in (3, 4):
-        raise ValueError(f"q: expected [B][Hq][128] or [B][q_len][Hq][128], got shape {tuple(q.shape)}")
-    q_len, heads = (1, q.shape[1]) if q.dim() == 3 else (q.shape[1], q.shape[2])
-    shape = (batch, heads, HEAD_DIM) if q.dim() == 3 else (batch, q_len, heads, HEAD_DIM)
-    _tensors(dev, torch.bfloat16, (q, "q", shape))
-    if out is not None:
+    i32 = torch.int32
+    shape = q.shape
+    q_len, heads = (1, shape[1]) if len(shape) == 3 else ((shape[1], shape[2]) if len(shape) == 4 else (-1, 0))
+    if q_len < 0 or shape[0] != B or shape[-1] != HEAD_DIM:
+        raise ValueError(f"q: expected [{B}][Hq][{HEAD_DIM}] or [{B}][q_len][Hq][{HEAD_DIM}], got shape {tuple(shape)}")
+    if not (q.dtype is torch.bfloat16 and q.get_device() == dev and q.is_contiguous()):
+        _tensors(dev, torch.bfloat16, (q, "q", shape))
+    if out is not None and not (out.shape == shape and out.get_device() == dev and out.is_contiguous()):
         _tensors(dev, out.dtype, (out, "out", shape))
-    return q_len, heads
+    if not (block_table.dtype is i32 and block_table.get_device() == dev and block_table.is_contiguous() and
+            seq_lens.dtype is i32 and seq_lens.shape == (B,) and seq_lens.get_device() == dev and
+            seq_lens.is_contiguous()):
+        _tensors(dev, i32, (block_table, "block_table", (B, max_pages)), (seq_lens, "seq_lens", (B,)))
+    if dev_status is not None:
+        _tensors(dev, i32, (dev_status, "dev_status", (1,)))
+    if workspace is None:
+        return q_len, heads, 0
+    n = workspace.numel()
+    if not (workspace.dtype is torch.uint8 and workspace.get_device() == dev and workspace.is_contiguous()):
+        _tensors(dev, torch.uint8, (workspace, "workspace", (n,)))
+    return q_len, heads, n
 
 
 def fp8bkv_paged_decode(cache: FP8BlockCache, q, block_table, seq_lens, out, workspace, sm_scale=None, num_workers=0,
@@ -756,43 +811,38 @@ def fp8bkv_paged_decode(cache: FP8BlockCache, q, block_table, seq_lens, out, wor
     """Decode attention over the block-scaled FP8 cache.  q: bf16 [B][Hq][128], or
     [B][q_len][Hq][128] for the last q_len positions of each sequence, causal
     among themselves; out: bf16 or fp32 of q's shape; workspace: new_workspace."""
-    import torch
-    if sm_scale is None:
-        sm_scale = 1.0 / math.sqrt(HEAD_DIM)
-    pool = _pool(cache, FP8BlockCache)
     dev = _current_device()
+    _kind(cache, FP8BlockCache, dev)
     B, pages = block_table.shape
-    q_len, heads = _query_rows(dev, q, out, B)
-    _tensors(dev, torch.uint8, pool,
-             (workspace, "workspace", (0 if workspace is None else workspace.numel(),)))
-    _tensors(dev, torch.int32, (block_table, "block_table", (B, pages)), (seq_lens, "seq_lens", (B,)),
-             (dev_status, "dev_status", (1,)))
+    q_len, heads, n = _attention_tensors(dev, B, pages, q, block_table, seq_lens, out, workspace, dev_status)
     st = load().fp8bkv_paged_decode(
-        cache.c, _ptr(q), B, q_len, heads, _ptr(block_table), pages, _ptr(seq_lens), float(sm_scale), _ptr(out),
-        _dtype_code(out), _ptr(workspace), 0 if workspace is None else workspace.numel(),
+        cache.c, q.data_ptr(), B, q_len, heads, block_table.data_ptr(), pages, seq_lens.data_ptr(),
+        _SM_SCALE if sm_scale is None else float(sm_scale), out.data_ptr(), _dtype_code(out), _ptr(workspace), n,
         _int32(num_workers, "num_workers"), _ptr(dev_status), _stream(stream, dev))
-    _check(st, "fp8bkv_paged_decode")
+    if st:
+        _check(st, "fp8bkv_paged_decode")
 
 
-def _bounds_tensors(dev, bounds: PageBounds) -> None:
-    import torch
-    n, h = bounds.num_pages, bounds.num_kv_heads
-    _tensors(dev, torch.int8, (bounds.bounds, "bounds.bounds", (n, h, 2, HEAD_DIM)))
-    _tensors(dev, torch.float32, (bounds.steps, "bounds.steps", (n, h)))
+_SM_SCALE = 1.0 / math.sqrt(HEAD_DIM)
 
 
 def _page_bounds(name, kind, cache, bounds, block_table, seq_lens, from_lens, dev_status, stream):
     import torch
-    pool = _pool(cache, kind)
-    dev = _current_device()
+    dev, i32 = _current_device(), torch.int32
+    _kind(cache, kind, dev)
     B, pages = block_table.shape
-    _tensors(dev, torch.uint8, pool)
-    _bounds_tensors(dev, bounds)
-    _tensors(dev, torch.int32, (block_table, "block_table", (B, pages)), (seq_lens, "seq_lens", (B,)),
-             (from_lens, "from_lens", (B,)), (dev_status, "dev_status", (1,)))
-    st = getattr(load(), name)(cache.c, bounds.c, _ptr(block_table), pages, _ptr(from_lens), _ptr(seq_lens), B,
+    if bounds.steps.get_device() != dev:
+        raise ValueError("bounds: not on the current CUDA device")
+    if not (block_table.dtype is i32 and block_table.get_device() == dev and block_table.is_contiguous() and
+            seq_lens.dtype is i32 and seq_lens.shape == (B,) and seq_lens.get_device() == dev and
+            seq_lens.is_contiguous()):
+        _tensors(dev, i32, (block_table, "block_table", (B, pages)), (seq_lens, "seq_lens", (B,)))
+    if from_lens is not None or dev_status is not None:
+        _tensors(dev, i32, (from_lens, "from_lens", (B,)), (dev_status, "dev_status", (1,)))
+    st = getattr(load(), name)(cache.c, bounds.c, block_table.data_ptr(), pages, _ptr(from_lens), seq_lens.data_ptr(), B,
                                _ptr(dev_status), _stream(stream, dev))
-    _check(st, name)
+    if st:
+        _check(st, name)
 
 
 def nvfp4kv_page_bounds(cache: NVFP4Cache, bounds: PageBounds, block_table, seq_lens, from_lens=None, dev_status=None,
@@ -808,6 +858,19 @@ def fp8bkv_page_bounds(cache: FP8BlockCache, bounds: PageBounds, block_table, se
     _page_bounds("fp8bkv_page_bounds", FP8BlockCache, cache, bounds, block_table, seq_lens, from_lens, dev_status, stream)
 
 
+def _page_lists(dev, pages, B, q_len, heads, flat) -> int:
+    """Check lists of pages int32 [B][q_len][Hkv][budget] (flat: or
+    [B][Hkv][budget]); returns the budget."""
+    import torch
+    shape = pages.shape
+    budget = shape[-1]
+    if not (pages.dtype is torch.int32 and pages.get_device() == dev and pages.is_contiguous() and
+            (shape == (B, q_len, heads, budget) or (flat and shape == (B, heads, budget)))):
+        _tensors(dev, torch.int32, (pages, "pages", (B, heads, budget) if flat and len(shape) == 3
+                                    else (B, q_len, heads, budget)))
+    return budget
+
+
 def nvfp4kv_select_pages(bounds: PageBounds, q, block_table, seq_lens, pages, first_pages=1, last_pages=1,
                          dev_status=None, stream=None) -> None:
     """Select pages for each query token and kv head: the first first_pages and
@@ -815,46 +878,33 @@ def nvfp4kv_select_pages(bounds: PageBounds, q, block_table, seq_lens, pages, fi
     score of their bounds, into pages int32 [B][q_len][Hkv][budget] (ascending
     places in the sequence, -1 behind the last; [B][Hkv][budget] where q is
     [B][Hq][128])."""
-    import torch
     dev = _current_device()
     B, max_pages = block_table.shape
-    q_len, heads = _query_rows(dev, q, None, B)
-    _bounds_tensors(dev, bounds)
-    budget = pages.shape[-1]
-    shape = (B, q_len, bounds.num_kv_heads, budget)
-    _tensors(dev, torch.int32,
-             (pages, "pages", shape if pages.dim() == 4 or q.dim() == 4 else (B, bounds.num_kv_heads, budget)),
-             (block_table, "block_table", (B, max_pages)), (seq_lens, "seq_lens", (B,)),
-             (dev_status, "dev_status", (1,)))
+    if bounds.steps.get_device() != dev or dev < 0:
+        raise ValueError("bounds: not on the current CUDA device")
+    q_len, heads, _ = _attention_tensors(dev, B, max_pages, q, block_table, seq_lens, None, None, dev_status)
+    budget = _page_lists(dev, pages, B, q_len, bounds.num_kv_heads, q.dim() == 3)
     st = load().nvfp4kv_select_pages(
-        bounds.c, _ptr(q), B, q_len, heads, _ptr(block_table), max_pages, _ptr(seq_lens), budget,
-        _int32(first_pages, "first_pages"), _int32(last_pages, "last_pages"), _ptr(pages), _ptr(dev_status),
+        bounds.c, q.data_ptr(), B, q_len, heads, block_table.data_ptr(), max_pages, seq_lens.data_ptr(), budget,
+        _int32(first_pages, "first_pages"), _int32(last_pages, "last_pages"), pages.data_ptr(), _ptr(dev_status),
         _stream(stream, dev))
-    _check(st, "nvfp4kv_select_pages")
+    if st:
+        _check(st, "nvfp4kv_select_pages")
 
 
 def _selected_decode(name, kind, cache, q, block_table, seq_lens, pages, out, workspace, sm_scale, num_workers,
                      dev_status, stream):
-    import torch
-    if sm_scale is None:
-        sm_scale = 1.0 / math.sqrt(HEAD_DIM)
-    pool = _pool(cache, kind)
     dev = _current_device()
+    _kind(cache, kind, dev)
     B, max_pages = block_table.shape
-    q_len, heads = _query_rows(dev, q, out, B)
-    budget = pages.shape[-1]
-    shape = (B, q_len, cache.num_kv_heads, budget)
-    _tensors(dev, torch.uint8, pool,
-             (workspace, "workspace", (0 if workspace is None else workspace.numel(),)))
-    _tensors(dev, torch.int32,
-             (pages, "pages", shape if pages.dim() == 4 or q.dim() == 4 else (B, cache.num_kv_heads, budget)),
-             (block_table, "block_table", (B, max_pages)), (seq_lens, "seq_lens", (B,)),
-             (dev_status, "dev_status", (1,)))
+    q_len, heads, n = _attention_tensors(dev, B, max_pages, q, block_table, seq_lens, out, workspace, dev_status)
+    budget = _page_lists(dev, pages, B, q_len, cache.num_kv_heads, q.dim() == 3)
     st = getattr(load(), name)(
-        cache.c, _ptr(q), B, q_len, heads, _ptr(block_table), max_pages, _ptr(seq_lens), _ptr(pages), budget,
-        float(sm_scale), _ptr(out), _dtype_code(out), _ptr(workspace), 0 if workspace is None else workspace.numel(),
+        cache.c, q.data_ptr(), B, q_len, heads, block_table.data_ptr(), max_pages, seq_lens.data_ptr(), pages.data_ptr(),
+        budget, _SM_SCALE if sm_scale is None else float(sm_scale), out.data_ptr(), _dtype_code(out), _ptr(workspace), n,
         _int32(num_workers, "num_workers"), _ptr(dev_status), _stream(stream, dev))
-    _check(st, name)
+    if st:
+        _check(st, name)
 
 
 def nvfp4kv_selected_decode(cache: NVFP4Cache, q, block_table, seq_lens, pages, out, workspace, sm_scale=None,

@@ -435,7 +435,7 @@ nvfp4kv_status check_select_sizes(int32_t batch, int32_t q_len, int32_t hkv, int
 int cluster_ranks(const DecodeParams &p, bool eight_bits)
 {
     return cluster_decode_ranks(static_cast<int64_t>(p.batch) * p.hkv, p.budget < p.max_pages ? p.budget : p.max_pages,
-                                eight_bits);
+                                eight_bits, 1);
 }
 
 // Decode over listed pages: fills p (except the cache's pool and scales).
@@ -1181,7 +1181,7 @@ nvfp4kv_status fp8bkv_paged_decode(const fp8bkv_cache *cache, const void *q, int
     p.pool = static_cast<const uint8_t *>(cache->pool);
     // short sequences: each query token by a cluster of its own
     const int ranks =
-        num_workers == 0 ? cluster_decode_ranks(static_cast<int64_t>(batch) * q_len * p.hkv, max_pages_per_seq, true) : 0;
+        num_workers == 0 ? cluster_decode_ranks(static_cast<int64_t>(batch) * q_len * p.hkv, max_pages_per_seq, true, q_len) : 0;
     if (ranks > 0) {
         p.batch = batch * q_len;
         p.sel_q_len = q_len;

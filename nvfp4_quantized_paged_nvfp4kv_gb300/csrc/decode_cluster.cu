@@ -31,9 +31,20 @@ constexpr bool kClFits = 2 * (kClSmem<Fmt> + 1024) <= 228 * 1024 &&
                          kClStages<Fmt> *Fmt::kRecord >= kStateFloats * static_cast<int>(sizeof(float));
 static_assert(kClFits<Nvfp4Format> && kClFits<Fp8BlockFormat>, "two CTAs an SM; a warp's state in its ring");
 
-template <class Fmt, bool kListed>
-__global__ void __launch_bounds__(kClThreads, 2) cluster_decode_kernel(const __grid_constant__ DecodeParams p)
+__device__ __forceinline__ float query_scale(const ClusterParams &p, int)
 {
+    return p.qscale;
+}
+
+__device__ __forceinline__ float query_scale(const ClusterHeadParams &p, int h)
+{
+    return p.qs[h];
+}
+
+template <class Fmt, bool kListed, class Params>
+__global__ void __launch_bounds__(kClThreads, 2) cluster_decode_kernel(const __grid_constant__ Params p)
+{
+    constexpr bool kHeadScales = std::is_same_v<Params, ClusterHeadParams>;
     extern __shared__ __align__(16) uint8_t smem_raw[];
     uint8_t *smem = smem_raw + ((128u - (smem_addr(smem_raw) & 127u)) & 127u);
     constexpr int S = kClStages<Fmt>, R = Fmt::kRecord;
@@ -61,7 +72,8 @@ __global__ void __launch_bounds__(kClThreads, 2) cluster_decode_kernel(const __g
         if (L < 0 || L > p.max_pages * kPageSize)
             report(p.dev_status, NVFP4KV_DEV_BAD_LEN);
     }
-    const int L = selected_row_len(p, row);
+    const int sees = clamp_len(__ldg(p.seq_lens + b), p.max_pages * kPageSize) - p.sel_q_len + (row - b * p.sel_q_len) + 1;
+    const int L = max(sees, 0);
     const int pages = (L + kPageSize - 1) / kPageSize, n = kListed ? min(p.budget, pages) : pages;
     const int w = rank * kClWarps + warp, workers = ranks * kClWarps;
     const int lo = static_cast<int>(static_cast<long long>(n) * w / workers);
@@ -133,7 +145,7 @@ __global__ void __launch_bounds__(kClThreads, 2) cluster_decode_kernel(const __g
         if constexpr (Fmt::kPageScales)
             load_rows_apart(q, has_row, p.qscale, tig, qf, inv0, inv1);
         else
-            load_rows(q, has_row ? (p.hs.per_head ? p.qs[h] : p.qscale) : 0.f, tig, qf);
+            load_rows(q, has_row ? query_scale(p, h) : 0.f, tig, qf);
     }
     const LaneOffsets off = Fmt::offsets(gid, tig);
 
@@ -257,7 +269,10 @@ __global__ void __launch_bounds__(kClThreads, 2) cluster_decode_kernel(const __g
         }
     }
     if (r < p.group && r % ranks == rank) {
-        const float osc = head_tensor_scale(p.hs, true, h, p.out_scale), by = l > 0.f ? osc / l : 0.f;
+        float osc = p.out_scale;
+        if constexpr (kHeadScales)
+            osc = p.vs[h];
+        const float by = l > 0.f ? osc / l : 0.f;
         const size_t at = (static_cast<size_t>(row) * p.hq + h * p.group + r) * kHeadDim + 4 * lane;
         if (p.out_bf16) {
             const __nv_bfloat162 x = __floats2bfloat162_rn(o.x * by, o.y * by), y = __floats2bfloat162_rn(o.z * by, o.w * by);
@@ -272,16 +287,22 @@ __global__ void __launch_bounds__(kClThreads, 2) cluster_decode_kernel(const __g
         cluster_sync();                          // (nobody leaves while its rows are read)
 }
 
-template <class Fmt, bool kListed>
-cudaError_t launch(const DecodeParams &p, int ranks, cudaStream_t s)
+template <class Fmt, bool kListed, class Params>
+cudaError_t launch(const Params &c, const DecodeParams &p, int ranks, cudaStream_t s)
 {
-    auto kernel = cluster_decode_kernel<Fmt, kListed>;
-    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(kClSmem<Fmt>));
+    constexpr auto kernel = cluster_decode_kernel<Fmt, kListed, Params>;
+    const cudaError_t e = allow_shared<kernel>();
     if (e != cudaSuccess)
         return e;
     return launch_cluster(kernel, dim3(static_cast<unsigned>(p.batch) * p.hkv * ranks), dim3(kClThreads), ranks,
-                          kClSmem<Fmt>, s, p);
+                          kClSmem<Fmt>, s, c);
+}
+
+ClusterParams cluster_params(const DecodeParams &p)
+{
+    return {p.pool,      p.q,         p.out,    p.block_table, p.seq_lens, p.sel_pages, p.dev_status, p.hq,         p.hkv,
+            p.group,     p.max_pages, p.num_pages, p.budget,   p.sel_q_len, p.out_bf16, p.qscale,     p.out_scale,
+            p.wait_limit};
 }
 
 } // namespace
@@ -289,11 +310,12 @@ cudaError_t launch(const DecodeParams &p, int ranks, cudaStream_t s)
 // CTAs a cluster: as many as fill two places an SM (or one place for each page and
 // warp), and whether that is faster than the worker split.  In us, measured with
 // 48 + 8 heads: a wave of clusters 3.6 and for each page of a CTA 0.115 with a
-// neighbour on the SM, 0.075 without (8 bits: 0.19 and 0.085); the workers 10 (8
-// bits: 16, their CTAs leave no registers for the next kernel's), 0.00042 (0.00053)
-// a page-head and 0.015 a (query token, kv head) to be joined.  80 of 256 pages: 14
-// and 18; 320 of 128 pages: 33 and 28.
-int cluster_decode_ranks(int64_t segments, int64_t pages, bool eight_bits)
+// neighbour on the SM, 0.075 without (8 bits: 0.19, or 0.09 where query tokens share
+// their pages, and 0.085); the workers 10 (8 bits: 16, their CTAs leave no registers
+// for the next kernel's), 0.00042 (0.00053) a page-head and 0.015 a (query token, kv
+// head) to be joined.  80 of 256 pages: 14 and 18; 320 of 128 pages: 33 and 28; four
+// tokens of 12 sequences at 8K in 8 bits: 98 and 107.
+int cluster_decode_ranks(int64_t segments, int64_t pages, bool eight_bits, int shared)
 {
     const int64_t sms = sm_count(), slots = 2 * sms;
     if (segments > (int64_t{1} << 27))
@@ -303,7 +325,8 @@ int cluster_decode_ranks(int64_t segments, int64_t pages, bool eight_bits)
     ranks = ranks < 1 ? 1 : (ranks > 8 ? 8 : ranks);
     const int64_t ctas = segments * ranks, waves = (ctas + slots - 1) / slots;
     const bool crowded = ctas > sms || ranks > 4;
-    const double page = eight_bits ? (crowded ? 0.19 : 0.085) : (crowded ? 0.115 : 0.075);
+    const double busy = eight_bits ? (shared > 1 ? 0.09 : 0.19) : 0.115;
+    const double page = crowded ? busy : (eight_bits ? 0.085 : 0.075);
     const double clusters = waves * (3.6 + page * ((pages + ranks - 1) / ranks));
     const double workers = (eight_bits ? 16.0 : 10.0) + (eight_bits ? 0.00053 : 0.00042) * segments * pages + 0.015 * segments;
     return clusters <= workers ? static_cast<int>(ranks) : 0;
@@ -311,12 +334,20 @@ int cluster_decode_ranks(int64_t segments, int64_t pages, bool eight_bits)
 
 cudaError_t launch_cluster_decode_nvfp4(const DecodeParams &p, int ranks, cudaStream_t s)
 {
-    return launch<Nvfp4Format, true>(p, ranks, s);
+    if (!p.hs.per_head)
+        return launch<Nvfp4Format, true>(cluster_params(p), p, ranks, s);
+    ClusterHeadParams c{cluster_params(p), {}, {}};
+    for (int h = 0; h < p.hkv; ++h) {
+        c.qs[h] = p.qs[h];
+        c.vs[h] = p.hs.v[h];
+    }
+    return launch<Nvfp4Format, true>(c, p, ranks, s);
 }
 
 cudaError_t launch_cluster_decode_fp8_block(const DecodeParams &p, int ranks, cudaStream_t s)
 {
-    return p.sel_pages != nullptr ? launch<Fp8BlockFormat, true>(p, ranks, s) : launch<Fp8BlockFormat, false>(p, ranks, s);
+    return p.sel_pages != nullptr ? launch<Fp8BlockFormat, true>(cluster_params(p), p, ranks, s)
+                                  : launch<Fp8BlockFormat, false>(cluster_params(p), p, ranks, s);
 }
 
 } // namespace nvfp4kv

@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "nvfp4kv.h"
 
 namespace nvfp4kv {
@@ -35,6 +37,34 @@ struct HeadScales {
     int per_head;
     float k[kMaxScaledHeads];
     float v[kMaxScaledHeads];
+};
+
+// What a decode over few pages needs (launched by clusters, without partials); the
+// per-head scales, two thirds of the full parameters, only where there are any.
+struct ClusterParams {
+    const uint8_t *pool;
+    const uint16_t *q;
+    void *out;
+    const int32_t *block_table;
+    const int32_t *seq_lens;
+    const int32_t *sel_pages;    // null: all pages
+    int32_t *dev_status;
+    int hq;
+    int hkv;
+    int group;
+    int max_pages;
+    int num_pages;
+    int budget;
+    int sel_q_len;
+    int out_bf16;
+    float qscale;
+    float out_scale;
+    uint32_t wait_limit;
+};
+
+struct ClusterHeadParams : ClusterParams {
+    float qs[kMaxScaledHeads];   // query scale and output scale of each kv head
+    float vs[kMaxScaledHeads];
 };
 
 // Split-KV decode over either cache format.
@@ -335,6 +365,23 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<Args &&>(args)...);
 }
 
+// Allows a kernel the most dynamic shared memory that it can have beside
+// kStatic bytes of its own, once a device (the runtime call costs a launch a third
+// of a microsecond).
+template <auto kKernel, int kStatic = 0>
+cudaError_t allow_shared()
+{
+    static std::atomic<bool> done[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess || (dev >= 0 && dev < 64 && done[dev].load(std::memory_order_acquire)))
+        return e;
+    e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024 - kStatic);
+    if (e == cudaSuccess && dev >= 0 && dev < 64)
+        done[dev].store(true, std::memory_order_release);
+    return e;
+}
+
 int sm_count();                  // current device, cached
 int default_num_workers();       // sm_count * kDecodeCtasPerSm * kDecodeWarps
 size_t decode_workspace_bytes(int num_workers);
@@ -348,8 +395,8 @@ cudaError_t launch_decode_fp8_block(const DecodeParams &p, cudaStream_t s);     
 cudaError_t launch_decode_selected_nvfp4(const DecodeParams &p, cudaStream_t s);
 cudaError_t launch_decode_selected_fp8_block(const DecodeParams &p, cudaStream_t s);
 // CTAs of a cluster for each (query token, kv head) of at most so many pages; 0:
-// the worker split is the faster one.
-int cluster_decode_ranks(int64_t segments, int64_t pages, bool eight_bits);
+// the worker split is the faster one.  `shared`: query tokens that see the same pages.
+int cluster_decode_ranks(int64_t segments, int64_t pages, bool eight_bits, int shared);
 cudaError_t launch_cluster_decode_nvfp4(const DecodeParams &p, int ranks, cudaStream_t s);
 cudaError_t launch_cluster_decode_fp8_block(const DecodeParams &p, int ranks, cudaStream_t s);   // (listed or all pages)
 cudaError_t launch_merge(const DecodeParams &p, cudaStream_t s);

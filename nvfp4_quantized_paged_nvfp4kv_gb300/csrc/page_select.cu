@@ -133,23 +133,25 @@ __device__ __forceinline__ void write_bounds(const Keys &keys, int valid, int8_t
         h[k] = hmax2(upper ? hi[k + 2] : hi[k], __shfl_xor_sync(kFullMask, hi_away, 16));
     }
     uint32_t t2 = hmax2(hmax2(l[0] & 0x7fff7fffu, l[1] & 0x7fff7fffu), hmax2(h[0] & 0x7fff7fffu, h[1] & 0x7fff7fffu));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1)
-        t2 = hmax2(t2, __shfl_xor_sync(kFullMask, t2, o));
-    const float2 tt = __half22float2(*reinterpret_cast<__half2 *>(&t2));
-    const float top = fmaxf(tt.x, tt.y);
+    // (f16 numbers that are not negative are in the order of their bits)
+    t2 = __reduce_max_sync(kFullMask, max(t2 & 0xffffu, t2 >> 16));
+    const float top = __half2float(__ushort_as_half(static_cast<unsigned short>(t2)));
     // one division: 127 / top in the lower half warp, top / 127 in the upper one
     const float quot = __fdiv_rn(upper ? top : 127.f, upper ? 127.f : top);
     const float r = top > 0.f ? __shfl_sync(kFullMask, quot, 0) : 0.f;
     uint32_t wl[4], wh[4];
+    const uint64_t r2 = f32x2_pack(r, r), whole2 = f32x2_pack(kWhole, kWhole);
 #pragma unroll
     for (int k = 0; k < 2; ++k) {
         const float2 a = __half22float2(*reinterpret_cast<__half2 *>(&l[k]));
         const float2 d = __half22float2(*reinterpret_cast<__half2 *>(&h[k]));
-        wl[2 * k] = __float_as_uint(fmaxf(__fadd_rd(__fmul_rn(a.x, r), kWhole), kWhole - 127.f));
-        wl[2 * k + 1] = __float_as_uint(fmaxf(__fadd_rd(__fmul_rn(a.y, r), kWhole), kWhole - 127.f));
-        wh[2 * k] = __float_as_uint(fminf(__fadd_ru(__fmul_rn(d.x, r), kWhole), kWhole + 127.f));
-        wh[2 * k + 1] = __float_as_uint(fminf(__fadd_ru(__fmul_rn(d.y, r), kWhole), kWhole + 127.f));
+        uint64_t lo2, hi2;
+        asm("add.rm.f32x2 %0, %1, %2;" : "=l"(lo2) : "l"(mul_f32x2(f32x2_pack(a.x, a.y), r2)), "l"(whole2));
+        asm("add.rp.f32x2 %0, %1, %2;" : "=l"(hi2) : "l"(mul_f32x2(f32x2_pack(d.x, d.y), r2)), "l"(whole2));
+        wl[2 * k] = __float_as_uint(fmaxf(f32x2_lo(lo2), kWhole - 127.f));
+        wl[2 * k + 1] = __float_as_uint(fmaxf(f32x2_hi(lo2), kWhole - 127.f));
+        wh[2 * k] = __float_as_uint(fminf(f32x2_lo(hi2), kWhole + 127.f));
+        wh[2 * k + 1] = __float_as_uint(fminf(f32x2_hi(hi2), kWhole + 127.f));
     }
     auto bytes = [](const uint32_t (&w)[4]) {
         return __byte_perm(__byte_perm(w[0], w[1], 0x0040), __byte_perm(w[2], w[3], 0x0040), 0x5410);
@@ -801,9 +803,8 @@ cudaError_t launch_page_bounds_fp8_block(const BoundsParams &p, cudaStream_t s)
 template <int kThreads>
 static cudaError_t launch_select(const SelectParams &p, long long units, size_t smem, int ranks, cudaStream_t s)
 {
-    auto kernel = page_select_kernel<kThreads>;
-    const cudaError_t e =
-        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    constexpr auto kernel = page_select_kernel<kThreads>;
+    const cudaError_t e = allow_shared<kernel, (sizeof(PickShared) + 127) / 128 * 128>();
     if (e != cudaSuccess)
         return e;
     return launch_cluster(kernel, dim3(static_cast<unsigned>(units * ranks)), dim3(kThreads), ranks, smem, s, p);

@@ -20,16 +20,20 @@ def i32(x):
 class Cache:
     """Random pages of either cache and their keys and values in 64 bits."""
 
-    def __init__(self, kind, pages, hkv, seed, global_scale=1.0):
+    def __init__(self, kind, pages, hkv, seed, global_scale=1.0, head_scales=None):
         rng = np.random.default_rng(seed)
-        self.kind, self.hkv, self.pages, self.G = kind, hkv, pages, global_scale
+        self.kind, self.hkv, self.pages, self.G = kind, hkv, pages, np.ones((2, hkv))
         drift = rng.standard_normal((pages, hkv, 1, 128)) * rng.uniform(0, 2, (pages, hkv, 1, 1))
         k, v = rng.standard_normal((2, pages, hkv, 16, 128))
         k = k + drift
         if kind == "nvfp4":
-            self.c = nv.NVFP4Cache.allocate(pages, hkv, device=DEV, global_scale=global_scale)
-            rows = lambda x: torch.tensor(x.transpose(0, 2, 1, 3).reshape(-1, hkv, 128), dtype=torch.float32, device=DEV)
-            nv.nvfp4kv_quantize_append(self.c, rows(k * global_scale), rows(v * global_scale),
+            self.c = nv.NVFP4Cache.allocate(pages, hkv, device=DEV, global_scale=global_scale, head_scales=head_scales)
+            rows = lambda x, g: torch.tensor(x.transpose(0, 2, 1, 3).reshape(-1, hkv, 128) * g[:, None],
+                                             dtype=torch.float32, device=DEV)
+            self.G = np.float32(global_scale) * np.ones((2, hkv), np.float32)
+            if head_scales is not None:
+                self.G = self.G * np.float32(head_scales)
+            nv.nvfp4kv_quantize_append(self.c, rows(k, self.G[0]), rows(v, self.G[1]),
                                        torch.arange(pages * 16, dtype=torch.int32, device=DEV))
             self.k, self.v = nvfp4_values(self.c.pool.cpu().numpy())
         else:
@@ -261,7 +265,7 @@ def assert_decode(cache, q, bt, lens, pages, got, q_len, out_eps=0.0):
                     if 0 <= p < P:
                         k.append(cache.k[bt[s, p], h, :m - 16 * p])
                         v.append(cache.v[bt[s, p], h, :m - 16 * p])
-                k, v = (np.concatenate(x) * cache.G if x else np.zeros((0, 128)) for x in (k, v))
+                k, v = (np.concatenate(x) * float(cache.G[i, h]) if x else np.zeros((0, 128)) for i, x in enumerate((k, v)))
                 want, bound = attend(qn[s, t, h], k, v, 1 / math.sqrt(128), out_eps,
                                      2.0 ** -11 if cache.kind == "nvfp4" else 0.0)
                 check(got[s, t, h], want, bound, f"sequence {s}, token {t}, kv head {h}")
@@ -299,6 +303,23 @@ def test_selected_decode(kind, q_len, hkv, g, workers):
     assert int(status.item()) == nv.DEV_BAD_PAGE
     assert_decode(cache, q, bt, lens, pages, out, q_len, 2.0 ** -8 if workers == 5 else 0.0)
     assert not out[7].any()
+
+
+@pytest.mark.parametrize("workers", [3, 0])
+def test_selected_decode_with_a_scale_a_head(workers):
+    """Factors of K and V of each head, beside the tensor scale."""
+    rng = np.random.default_rng(5)
+    cache = Cache("nvfp4", 30, 3, 2, 0.5, [[0.25, 3.0, 17.0], [8.0, 0.5, 1.5]])
+    lens, budget = [100, 17, 400], 6
+    bt = np.stack([rng.permutation(30)[:25] for _ in lens]).astype(np.int32)
+    pages = np.full((3, 1, 3, budget), -1, np.int32)
+    for s, n in enumerate(lens):
+        for h in range(3):
+            k = min(-(-n // 16), budget)
+            pages[s, 0, h, :k] = rng.permutation(-(-n // 16))[:k]
+    q = queries(3, 1, 12, 8)
+    out = run_decode(cache, q, bt, lens, pages, workers)
+    assert_decode(cache, q, bt, lens, pages, out, 1)
 
 
 @pytest.mark.parametrize("kind", ["nvfp4", "fp8b"])
@@ -386,4 +407,4 @@ class Host:
 
     def __init__(self, cache, hkv):
         self.k, self.v = nvfp4_values(cache.pool.cpu().numpy())
-        self.hkv, self.pages, self.kind, self.G = hkv, cache.num_pages, "nvfp4", 1.0
+        self.hkv, self.pages, self.kind, self.G = hkv, cache.num_pages, "nvfp4", np.ones((2, hkv))
