@@ -58,7 +58,7 @@ struct Nvfp4Keys {
     __device__ __forceinline__ float unit() const { return 256.f; }
     __device__ __forceinline__ void get(int i, uint32_t (&x)[4]) const
     {
-        const uint32_t sc = (s[i] & 0x7fu) * 0x00800080u;
+        const uint32_t sc = s[i] * 0x00800080u;
         e2m1x8_to_f16x2x4(d[i], x[0], x[1], x[2], x[3]);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
