@@ -407,6 +407,7 @@ __device__ __forceinline__ int checked(const SelectParams &p, int phys)
 
 constexpr int kBins = 2048;
 constexpr int kTies = 1024;              // scores of the border's bin that are ranked side by side
+static_assert(2 * kTies <= kBins, "all CTAs' ties in the place of a CTA's counts");
 
 // A float's place in the order of floats, as an unsigned number.
 __device__ __forceinline__ uint32_t order_of(float x)
@@ -497,14 +498,21 @@ __device__ __forceinline__ void pick_pages(const Selection &s, int want, int32_t
         for (int i = lo + tid; i < hi; i += kThreads)
             fn(i, s.score[i]);
     };
+    // What lane k reads of CTA k, `none` in the lanes past the last one: one trip to
+    // the other CTAs for all of them.
+    auto of_each = [&](const void *field, uint32_t none) {
+        return static_cast<uint32_t>(lane) < s.ranks ? ld_cluster_u32(peer(field, lane)) : none;
+    };
     // A place range of the cluster, from each CTA's.
     auto range_of = [&](const uint32_t &least, const uint32_t &most, uint32_t &a, uint32_t &z) {
-        a = 0xffffffffu;
-        z = 0;
-        for (uint32_t k = 0; k < s.ranks; ++k) {
-            a = min(a, ld_cluster_u32(peer(&least, k)));
-            z = max(z, ld_cluster_u32(peer(&most, k)));
-        }
+        const uint32_t x = of_each(&least, 0xffffffffu), y = of_each(&most, 0);
+        a = __reduce_min_sync(kFullMask, x);
+        z = __reduce_max_sync(kFullMask, y);
+    };
+    // The sum of what the CTAs before this one have.
+    auto before_me = [&](const int32_t &field) {
+        const uint32_t x = of_each(&field, 0);
+        return static_cast<int>(__reduce_add_sync(kFullMask, static_cast<uint32_t>(lane) < s.rank ? x : 0u));
     };
     auto clear = [&]() {
         for (int i = tid; i < kBins; i += kThreads)
@@ -525,12 +533,26 @@ __device__ __forceinline__ void pick_pages(const Selection &s, int want, int32_t
         int mine[kEach], sum = 0, total;
         const int top = kBins - 1 - tid * kEach;
 #pragma unroll
-        for (int k = 0; k < kEach; ++k) {
-            mine[k] = 0;
-            for (uint32_t r = 0; r < s.ranks; ++r)
-                mine[k] += static_cast<int>(ld_cluster_u32(peer(&sh.count[top - k], r)));
-            sum += mine[k];
+        for (int k = 0; k < kEach; ++k)
+            mine[k] = s.ranks > 1 ? 0 : sh.count[top - k];
+        for (uint32_t r0 = 0; s.ranks > 1 && r0 < s.ranks; r0 += 4) {
+            uint32_t n[4][kEach];                                // (asked for together)
+#pragma unroll
+            for (uint32_t r = 0; r < 4; ++r) {
+                const uint32_t at = peer(&sh.count[top], min(r0 + r, s.ranks - 1));
+#pragma unroll
+                for (int k = 0; k < kEach; ++k)
+                    n[r][k] = r0 + r < s.ranks ? ld_cluster_u32(at - 4 * k) : 0u;
+            }
+#pragma unroll
+            for (uint32_t r = 0; r < 4; ++r)
+#pragma unroll
+                for (int k = 0; k < kEach; ++k)
+                    mine[k] += static_cast<int>(n[r][k]);
         }
+#pragma unroll
+        for (int k = 0; k < kEach; ++k)
+            sum += mine[k];
         int before = cta_sum_before<kThreads>(sum, sh.scratch, total);
 #pragma unroll
         for (int k = 0; k < kEach; ++k) {
@@ -569,21 +591,48 @@ __device__ __forceinline__ void pick_pages(const Selection &s, int want, int32_t
             return true;
         if (inside > kTies)
             return false;
-        const int mine = sh.found[3];
-        for (int x = tid; x < mine; x += kThreads) {
-            const uint32_t k = sh.tie_key[x];
-            const int page = sh.tie_page[x];
-            int r = 0;
-            for (uint32_t c = 0; c < s.ranks; ++c) {
-                const int n = static_cast<int>(ld_cluster_u32(peer(&sh.found[3], c)));
-                const uint32_t keys = peer(sh.tie_key, c), pages = peer(sh.tie_page, c);
-                for (int y = 0; y < n; ++y) {
-                    const uint32_t other = ld_cluster_u32(keys + 4 * y);
-                    r += other > k || (other == k && static_cast<int>(ld_cluster_u32(pages + 4 * y)) < page);
+        const uint32_t *keys = sh.tie_key;
+        const int32_t *at = sh.tie_page;
+        if (s.ranks > 1) {
+            // all CTAs' ties, in the place of the counts, which have been read
+            uint32_t *to = reinterpret_cast<uint32_t *>(sh.count);
+            uint32_t end = of_each(&sh.found[3], 0);             // where CTA `lane`'s end among them all
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) {
+                const uint32_t x = __shfl_up_sync(kFullMask, end, o);
+                end += lane >= o ? x : 0u;
+            }
+            for (int x0 = 0; x0 < inside; x0 += kThreads) {
+                const int x = x0 + tid;
+                uint32_t c = 0, begin = 0;
+#pragma unroll
+                for (int k = 0; k < 7; ++k) {
+                    const uint32_t e = __shfl_sync(kFullMask, end, k);
+                    if (static_cast<uint32_t>(x) >= e) {
+                        c = k + 1;
+                        begin = e;
+                    }
+                }
+                if (x < inside && c < s.ranks) {
+                    to[x] = ld_cluster_u32(peer(sh.tie_key, c) + 4 * (x - begin));
+                    to[kTies + x] = ld_cluster_u32(peer(sh.tie_page, c) + 4 * (x - begin));
                 }
             }
+            keys = to;
+            at = reinterpret_cast<const int32_t *>(to + kTies);
+            __syncthreads();
+        }
+        for (int x = tid; x < inside; x += kThreads) {
+            const uint32_t k = keys[x];
+            const int page = at[x], i = page - s.p0;
+            if (i < 0 || i >= s.count)
+                continue;                                        // (another CTA's)
+            int r = 0;
+#pragma unroll 4
+            for (int y = 0; y < inside; ++y)
+                r += keys[y] > k || (keys[y] == k && at[y] < page);
             if (r < want)
-                take(page - s.p0);
+                take(i);
         }
         return true;
     };
@@ -663,8 +712,7 @@ __device__ __forceinline__ void pick_pages(const Selection &s, int want, int32_t
         if (tid == 0)
             sh.equal = total;
         meet(s.ranks);
-        for (uint32_t k = 0; k < s.rank; ++k)
-            want -= static_cast<int>(ld_cluster_u32(peer(&sh.equal, k)));
+        want -= before_me(sh.equal);
         for (int i0 = lo; i0 < hi && want > 0; i0 += kThreads) {
             const int i = i0 + tid;
             const bool is = i < hi && order_of(s.score[i]) == from;
@@ -691,9 +739,7 @@ __device__ __forceinline__ void pick_pages(const Selection &s, int want, int32_t
     if (tid == 0)
         sh.listed = total;
     meet(s.ranks);
-    n0 = 0;
-    for (uint32_t k = 0; k < s.rank; ++k)
-        n0 += static_cast<int>(ld_cluster_u32(peer(&sh.listed, k)));
+    n0 = before_me(sh.listed);
     for (int w0 = 0; w0 < words; w0 += kThreads) {
         const int w = w0 + tid;
         uint32_t bits = w < words ? word(w) : 0;
@@ -811,22 +857,21 @@ static cudaError_t launch_select(const SelectParams &p, long long units, size_t 
 }
 
 // CTAs of 512 threads, one an SM, or of 256, two an SM, and how many a cluster.  A
-// CTA takes a page in 3.6 ns, a meeting of the cluster costs a microsecond: more than
-// one CTA pays from some 2,048 pages on (8 heads of one sequence, 2,000 pages: 13.7 us
-// with one, 12.3 with two, 12.7 with four; 8,125 pages: 34.8, 23.2, 18.8).  Where the
-// SMs are taken by one CTA each, smaller ones share a long sequence better (80 x 10,240
-// pages: 57 us with one CTA of 512, 54 with three of 256; 96 x 2,000: 16.4 and 26.6),
-// and where there are more units than SMs, two at a time an SM run beside each other
-// (560 x 2,000 pages: 74 us with 512 threads, 62 with 256).
+// meeting of the cluster costs a microsecond: more than one CTA pays from some 2,048
+// pages on (8 heads of one sequence, 2,000 pages: 13.4 us with one, 12.6 with two, 13.4
+// with four; 8,125 pages: 34.5, 23.4, 19.4), as long as every CTA has an SM of its own
+// (96 units of 2,000 pages: 16.2 and 28.4).  Where there are more units than SMs, two at
+// a time on an SM work beside each other (560 units of 2,000 pages: 73 us with 512
+// threads, 62 with 256; 320 of 4,000: 84.2 and 83.5), but of long sequences a wave that
+// is not full costs more than that gains (160 units of 8,125 pages: 102 and 120; 560:
+// 232 and 270).
 cudaError_t launch_select_pages(const SelectParams &p, cudaStream_t s)
 {
     const long long units = static_cast<long long>(p.batch) * p.q_len * p.hkv;
     const int tiles = (p.max_pages + kTile - 1) / kTile;
     const long long sms = max(1, sm_count()), fit = max(1LL, sms / units);
-    const bool lengthy = p.max_pages > 6144;
-    const int threads = units > sms || (fit == 1 && lengthy) ? 256 : 512;
-    long long ranks = threads == 512 ? min(fit, (p.max_pages + 1023LL) / 2048) : (lengthy ? 2 * sms / units : 1);
-    ranks = max(1LL, min(8LL, ranks));
+    const int threads = units > sms && p.max_pages <= 6144 ? 256 : 512;
+    long long ranks = max(1LL, min(8LL, min(fit, (p.max_pages + 1023LL) / 2048)));
     SelectParams q = p;
     auto bytes = [&]() {
         q.chunk_tiles = (tiles + static_cast<int>(ranks) - 1) / static_cast<int>(ranks);
