@@ -308,8 +308,13 @@ ClusterParams cluster_params(const DecodeParams &p)
 } // namespace
 
 // CTAs a cluster: as many as fill two places an SM (or one place for each page and
-// warp), and whether that is faster than the worker split.  In us, measured with
-// 48 + 8 heads: a wave of clusters 3.6 and for each page of a CTA 0.115 with a
+// warp), and whether that is faster than the worker split.  Clusters of more than two
+// leave some places free: their CTAs start in one part of the GPU, and where the kernel
+// before leaves its SMs one by one, the last clusters wait for a part with room (a
+// selection and the decode of 96 rows of 128 pages in 8 bits: 38.6 us with three CTAs a
+// cluster in 288 of 304 places, 31.9 with two; 48 rows: 31.3 with six in 288, 24.5 with
+// four in 192; 64 rows: 28.3 with three in 192, 27.9 with four in 256).  In us, measured
+// with 48 + 8 heads: a wave of clusters 3.6 and for each page of a CTA 0.115 with a
 // neighbour on the SM, 0.075 without (8 bits: 0.19, or 0.09 where query tokens share
 // their pages, and 0.085); the workers 10 (8 bits: 16, their CTAs leave no registers
 // for the next kernel's), 0.00042 (0.00053) a page-head and 0.015 a (query token, kv
@@ -321,8 +326,11 @@ int cluster_decode_ranks(int64_t segments, int64_t pages, bool eight_bits, int s
     if (segments > (int64_t{1} << 27))
         return 0;
     int64_t ranks = segments > 0 ? slots / segments : 1;
+    ranks = ranks < 8 ? ranks : 8;
+    while ((ranks > 4 && segments * ranks > slots * 3 / 4) || (ranks > 2 && segments * ranks > slots * 6 / 7))
+        --ranks;
     ranks = ranks < pages / kClWarps ? ranks : pages / kClWarps;
-    ranks = ranks < 1 ? 1 : (ranks > 8 ? 8 : ranks);
+    ranks = ranks < 1 ? 1 : ranks;
     const int64_t ctas = segments * ranks, waves = (ctas + slots - 1) / slots;
     const bool crowded = ctas > sms || ranks > 4;
     const double busy = eight_bits ? (shared > 1 ? 0.09 : 0.19) : 0.115;
