@@ -463,6 +463,7 @@ struct Selection {
     const float *score;
     uint32_t *taken;                     // a bit a page of this CTA, all clear
     int p0, count;
+    int lo, hi;                          // the candidates among them, as score[lo .. hi - 1]
     int pages, first, last;              // of the sequence; pages that are taken in any case
     uint32_t rank, ranks;
 };
@@ -480,22 +481,22 @@ __device__ __forceinline__ void meet(uint32_t ranks)
 // are more of them), and lists them with those, ascending, at `out`.  Counts of the
 // scores in 2,048 equal parts of [least, largest] say, from the top, in which part the
 // last wanted one lies; what lies above is taken, what lies in that part is ranked pair
-// by pair.  (The part of a score, f below cut to a whole number, never falls as the
+// by pair.  `from` and `to` are the ends of the thread's scores in the order of floats,
+// then of what is still open.  (The part of a score, f below cut to a whole number, never falls as the
 // score grows, whatever its subtraction and product round.)  Where more than kTies
 // scores share the part, its places in the order of floats are cut into 2,048 parts,
 // again until they fit or are one number, of which the lowest pages are taken.  Every
 // CTA adds up all CTAs' counts and comes to the same border.
 template <int kThreads>
-__device__ __forceinline__ void pick_pages(const Selection &s, int want, int32_t *out, PickShared &sh)
+__device__ __forceinline__ void pick_pages(const Selection &s, uint32_t from, uint32_t to, int want, int32_t *out, PickShared &sh)
 {
     const int tid = threadIdx.x, lane = tid & 31;
-    const int lo = max(s.first - s.p0, 0), hi = min(s.pages - s.last - s.p0, s.count);     // this CTA's candidates
     const uint32_t base = smem_addr(&sh);
     auto peer = [&](const void *field, uint32_t k) { return in_cta(base + static_cast<uint32_t>(
         static_cast<const uint8_t *>(field) - reinterpret_cast<const uint8_t *>(&sh)), k); };
     auto for_scores = [&](auto fn) {
 #pragma unroll 4
-        for (int i = lo + tid; i < hi; i += kThreads)
+        for (int i = s.lo + tid; i < s.hi; i += kThreads)
             fn(i, s.score[i]);
     };
     // What lane k reads of CTA k, `none` in the lanes past the last one: one trip to
@@ -637,17 +638,6 @@ __device__ __forceinline__ void pick_pages(const Selection &s, int want, int32_t
         return true;
     };
 
-    // the range of the scores
-    uint32_t from = 0xffffffffu, to = 0;                         // the places that are still open, both ends among them
-    for_scores([&](int, float x) {
-        from = min(from, order_of(x));
-        to = max(to, order_of(x));
-    });
-    if (tid == 0) {
-        sh.least = 0xffffffffu;
-        sh.most = 0;
-    }
-    __syncthreads();
     from = __reduce_min_sync(kFullMask, from);
     to = __reduce_max_sync(kFullMask, to);
     if (lane == 0) {
@@ -705,7 +695,7 @@ __device__ __forceinline__ void pick_pages(const Selection &s, int want, int32_t
     if (!done) {
         // one number left: the lowest `want` of the pages that have it
         int n = 0, total;
-        for (int i = lo + tid; i < hi; i += kThreads)
+        for (int i = s.lo + tid; i < s.hi; i += kThreads)
             n += order_of(s.score[i]) == from;
         __syncthreads();
         cta_sum_before<kThreads>(n, sh.scratch, total);
@@ -713,9 +703,9 @@ __device__ __forceinline__ void pick_pages(const Selection &s, int want, int32_t
             sh.equal = total;
         meet(s.ranks);
         want -= before_me(sh.equal);
-        for (int i0 = lo; i0 < hi && want > 0; i0 += kThreads) {
+        for (int i0 = s.lo; i0 < s.hi && want > 0; i0 += kThreads) {
             const int i = i0 + tid;
-            const bool is = i < hi && order_of(s.score[i]) == from;
+            const bool is = i < s.hi && order_of(s.score[i]) == from;
             const int before = cta_sum_before<kThreads>(is, sh.scratch, total);
             if (is && before < want)
                 take(i);
@@ -740,16 +730,20 @@ __device__ __forceinline__ void pick_pages(const Selection &s, int want, int32_t
         sh.listed = total;
     meet(s.ranks);
     n0 = before_me(sh.listed);
-    for (int w0 = 0; w0 < words; w0 += kThreads) {
-        const int w = w0 + tid;
-        uint32_t bits = w < words ? word(w) : 0;
-        int n = n0 + cta_sum_before<kThreads>(__popc(bits), sh.scratch, total);
-        while (bits) {
-            const int k = __ffs(bits) - 1;
-            bits &= bits - 1;
-            out[n++] = s.p0 + 32 * w + k;
+    constexpr int kWarps = kThreads / 32;
+    for (int w0 = 0; w0 < words;) {
+        const int each = min((words - w0 + kWarps - 1) / kWarps, 32);        // words of a warp
+        const int w = w0 + (tid >> 5) * each + lane;
+        const uint32_t bits = lane < each && w < words ? word(w) : 0;
+        const int n = n0 + cta_sum_before<kThreads>(__popc(bits), sh.scratch, total);
+        for (int k = 0; k < each; ++k) {                         // a lane a page
+            const uint32_t x = __shfl_sync(kFullMask, bits, k);
+            const int at = __shfl_sync(kFullMask, n, k);
+            if (x >> lane & 1)
+                out[at + __popc(x & ((1u << lane) - 1u))] = s.p0 + 32 * (w - lane + k) + lane;
         }
         n0 += total;
+        w0 += kWarps * each;
     }
     meet(s.ranks);                                               // (nobody leaves while it is read)
 }
@@ -791,9 +785,21 @@ __global__ void __launch_bounds__(kThreads, kThreads == 512 ? 1 : 2) page_select
     const int p0 = begin * kTile, count = min(tiles * kTile, pages - p0);
     for (int i = tid; i < (tiles * kTile + 31) / 32; i += kThreads)
         taken[i] = 0;
+    if (tid == 0) {
+        sh.least = 0xffffffffu;
+        sh.most = 0;
+    }
     const int32_t *table = p.block_table + static_cast<size_t>(b) * p.max_pages + p0;
-    for (int i = tid; i < tiles * kTile; i += kThreads)
-        place[i] = i < count ? checked(p, __ldg(table + i)) : 0;
+    for (int i0 = tid; i0 < tiles * kTile; i0 += 8 * kThreads) {
+        int phys[8];                                             // (asked for together)
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            phys[k] = i0 + k * kThreads < count ? __ldg(table + i0 + k * kThreads) : 0;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            if (i0 + k * kThreads < tiles * kTile)
+                place[i0 + k * kThreads] = checked(p, phys[k]);
+    }
     __syncthreads();
     pdl_wait();
     TileRing ring{smem_addr(ssmem) + warp * kStages * kStageBytes, {}};
@@ -812,6 +818,8 @@ __global__ void __launch_bounds__(kThreads, kThreads == 512 ? 1 : 2) page_select
     for (int i = 0; i < 8; ++i)
         w[i] = frag[i * 32 + lane];
     const float2 from = reinterpret_cast<const float2 *>(frag + 8 * 32)[lane & 3];
+    const int lo = max(p.first - p0, 0), hi = min(pages - p.last - p0, count);
+    uint32_t least = 0xffffffffu, most = 0;
     for (int tile = warp; tile < tiles;) {
 #pragma unroll
         for (int k = 0; k < kStages; ++k) {
@@ -824,14 +832,19 @@ __global__ void __launch_bounds__(kThreads, kThreads == 512 ? 1 : 2) page_select
             const int next = tile + kStages * kWarps;
             ring.ask(p, h, next < tiles, next < tiles ? place[next * kTile + (lane & 15)] : 0, k, lane);
             const float score = score_of(a, [&](int i) { return w[i]; }, from, step, lane);
+            const int i = tile * kTile + (lane & 15);
             if (lane < 16)
-                place[tile * kTile + lane] = __float_as_uint(score);
+                place[i] = __float_as_uint(score);
+            if (i >= lo && i < hi) {
+                least = min(least, order_of(score));
+                most = max(most, order_of(score));
+            }
             tile += kWarps;
         }
     }
     __syncthreads();
-    const Selection s{reinterpret_cast<const float *>(place), taken, p0, count, pages, p.first, p.last, rank, ranks};
-    pick_pages<kThreads>(s, p.budget - p.first - p.last, out, sh);
+    const Selection s{reinterpret_cast<const float *>(place), taken, p0, count, lo, hi, pages, p.first, p.last, rank, ranks};
+    pick_pages<kThreads>(s, least, most, p.budget - p.first - p.last, out, sh);
 }
 
 } // namespace
