@@ -1,5 +1,5 @@
-// Thread-block clusters: rank and size, the barrier, and reads of another CTA's
-// shared memory, as inline PTX from the PTX ISA.
+// Thread-block clusters: rank and size, the barrier, and access to another
+// CTA's shared memory, as inline PTX from the PTX ISA.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -7,9 +7,20 @@
 
 namespace nvfp4kv {
 
+__device__ __forceinline__ void cluster_arrive()
+{
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+
+__device__ __forceinline__ void cluster_wait()
+{
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
 __device__ __forceinline__ void cluster_sync()
 {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+    cluster_arrive();
+    cluster_wait();
 }
 
 __device__ __forceinline__ uint32_t cluster_rank()
@@ -34,21 +45,10 @@ __device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank)
     return r;
 }
 
-__device__ __forceinline__ float4 ld_cluster4(uint32_t addr)
+__device__ __forceinline__ void st_cluster4(uint32_t addr, float4 v)
 {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(addr)
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
                  : "memory");
-    return v;
-}
-
-__device__ __forceinline__ float ld_cluster(uint32_t addr)
-{
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
-    return v;
 }
 
 __device__ __forceinline__ uint32_t ld_cluster_u32(uint32_t addr)

@@ -21,10 +21,14 @@ constexpr int kRowFloats = kHeadDim + 4;         // (rows 2tig of four lanes in 
 constexpr int kStateFloats = kMaxGroup * kRowFloats + 2 * kMaxGroup;
 
 template <class Fmt>
-constexpr int kClStages = Fmt::kRecord > 4000 ? 3 : 6;
+constexpr int kClStages = Fmt::kRecord > 4000 ? 3 : 5;
+
+// Rows that a CTA is sent to be joined, at most: r ranks * ceil(8 / r) of them.
+constexpr int kSentRows = 14;
 
 template <class Fmt>
-constexpr size_t kClSmem = 128 + static_cast<size_t>(kClWarps) * kClStages<Fmt> * (Fmt::kRecord + 8 + 4);
+constexpr size_t kClSmem = 128 + static_cast<size_t>(kClWarps) * kClStages<Fmt> * (Fmt::kRecord + 8 + 4) +
+                           kSentRows * kRowFloats * sizeof(float);
 
 template <class Fmt>
 constexpr bool kClFits = 2 * (kClSmem<Fmt> + 1024) <= 228 * 1024 &&
@@ -55,6 +59,8 @@ __global__ void __launch_bounds__(kClThreads, 2) cluster_decode_kernel(const __g
     const uint32_t wbar = smem_addr(smem + kClWarps * S * R) + warp * S * 8;
     // tokens of the page in each stage that count
     volatile int32_t *counted = reinterpret_cast<int32_t *>(smem + kClWarps * S * (R + 8)) + warp * S;
+    // the cluster's rows that this CTA finishes, as their CTAs send them: 128 channels, M, l
+    float *sent = reinterpret_cast<float *>(smem + kClWarps * S * (R + 12));
 
     if (lane == 0) {
         for (int s = 0; s < S; ++s)
@@ -65,6 +71,8 @@ __global__ void __launch_bounds__(kClThreads, 2) cluster_decode_kernel(const __g
     // Lengths and block tables may be read ahead of the kernel before, as in
     // decode_kernel; lists, queries and records may not.
     const uint32_t rank = cluster_rank(), ranks = cluster_size();
+    if (ranks > 1)
+        cluster_arrive();                        // (this CTA runs: it can be written to)
     const int seg = blockIdx.x / ranks, row = seg / p.hkv, h = seg - row * p.hkv;
     const int b = row / p.sel_q_len;
     if (rank == 0 && h == 0 && threadIdx.x == 0 && row == b * p.sel_q_len) {
@@ -240,31 +248,32 @@ __global__ void __launch_bounds__(kClThreads, 2) cluster_decode_kernel(const __g
         }
     }
     if (ranks > 1) {
-        // the CTAs' rows, in the place of warp 0's; CTA r mod ranks finishes row r
+        // CTA r mod ranks finishes row r; sent rather than fetched, so that there is one
+        // trip and nobody has to stay for the others
+        const uint32_t each = (kMaxGroup + ranks - 1) / ranks;
+        cluster_wait();
         if (r < p.group) {
-            __syncwarp();
-            *reinterpret_cast<float4 *>(all + r * kRowFloats + 4 * lane) = o;
-            if (lane == 0) {
-                all[kMaxGroup * kRowFloats + r] = M;
-                all[kMaxGroup * kRowFloats + kMaxGroup + r] = l;
-            }
+            const uint32_t at = in_cta(smem_addr(sent + (rank * each + r / ranks) * kRowFloats), r % ranks);
+            st_cluster4(at + 16 * lane, o);
+            if (lane == 0)
+                st_cluster4(at + 4 * kHeadDim, make_float4(M, l, 0.f, 0.f));
         }
         cluster_sync();
         if (r < p.group && r % ranks == rank) {
-            const uint32_t base = smem_addr(smem);
-            const uint32_t at_m = base + 4 * (kMaxGroup * kRowFloats + r), at_o = base + 4 * (r * kRowFloats + 4 * lane);
+            const float *from = sent + r / ranks * kRowFloats;
             for (uint32_t k = 0; k < ranks; ++k)
-                M = fmaxf(M, ld_cluster(in_cta(at_m, k)));
+                M = fmaxf(M, from[k * each * kRowFloats + kHeadDim]);
             o = make_float4(0.f, 0.f, 0.f, 0.f);
             l = 0.f;
             for (uint32_t k = 0; k < ranks; ++k) {
-                const float m = ld_cluster(in_cta(at_m, k)), e = m == -INFINITY ? 0.f : fast_exp2(m - M);
-                const float4 v = ld_cluster4(in_cta(at_o, k));
+                const float *row_k = from + k * each * kRowFloats;
+                const float m = row_k[kHeadDim], e = m == -INFINITY ? 0.f : fast_exp2(m - M);
+                const float4 v = *reinterpret_cast<const float4 *>(row_k + 4 * lane);
                 o.x += e * v.x;
                 o.y += e * v.y;
                 o.z += e * v.z;
                 o.w += e * v.w;
-                l += e * ld_cluster(in_cta(at_m + 4 * kMaxGroup, k));
+                l += e * row_k[kHeadDim + 1];
             }
         }
     }
@@ -283,8 +292,6 @@ __global__ void __launch_bounds__(kClThreads, 2) cluster_decode_kernel(const __g
                 make_float4(o.x * by, o.y * by, o.z * by, o.w * by);
         }
     }
-    if (ranks > 1)
-        cluster_sync();                          // (nobody leaves while its rows are read)
 }
 
 template <class Fmt, bool kListed, class Params>
