@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace nvfp4kv {
 
 __device__ __forceinline__ void cluster_arrive()
@@ -78,6 +80,37 @@ cudaError_t launch_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 block, int 
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kernel, static_cast<Args &&>(args)...);
+}
+
+// Clusters of `ranks` CTAs (at most 8) that the current device runs at a time, by the
+// runtime's occupancy query, once a device and size (it costs microseconds): a cluster
+// has to fit into one part of the GPU, so they are fewer than the SMs would hold.
+template <auto kKernel, int kThreads>
+int clusters_at_once(int ranks, size_t smem)
+{
+    static std::atomic<int> known[64][9];
+    int dev = 0, n = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64)
+        return 0;
+    n = known[dev][ranks].load(std::memory_order_relaxed);
+    if (n > 0)
+        return n - 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ranks);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = ranks;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, kKernel, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    known[dev][ranks].store(n + 1, std::memory_order_relaxed);
+    return n;
 }
 
 } // namespace nvfp4kv

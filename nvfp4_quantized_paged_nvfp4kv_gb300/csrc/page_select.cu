@@ -859,46 +859,63 @@ cudaError_t launch_page_bounds_fp8_block(const BoundsParams &p, cudaStream_t s)
     return launch_bounds<Fp8BlockKeys>(p, s);
 }
 
+// Dynamic shared memory that a launch may take, beside PickShared.
+constexpr size_t kMostShared = 227 * 1024 - sizeof(PickShared) - 1024;
+
+template <int kThreads>
+static cudaError_t allow_select()
+{
+    return allow_shared<page_select_kernel<kThreads>, (sizeof(PickShared) + 127) / 128 * 128>();
+}
+
 template <int kThreads>
 static cudaError_t launch_select(const SelectParams &p, long long units, size_t smem, int ranks, cudaStream_t s)
 {
-    constexpr auto kernel = page_select_kernel<kThreads>;
-    const cudaError_t e = allow_shared<kernel, (sizeof(PickShared) + 127) / 128 * 128>();
+    const cudaError_t e = allow_select<kThreads>();
     if (e != cudaSuccess)
         return e;
-    return launch_cluster(kernel, dim3(static_cast<unsigned>(units * ranks)), dim3(kThreads), ranks, smem, s, p);
+    return launch_cluster(page_select_kernel<kThreads>, dim3(static_cast<unsigned>(units * ranks)), dim3(kThreads), ranks,
+                          smem, s, p);
 }
 
 // CTAs of 512 threads, one an SM, or of 256, two an SM, and how many a cluster.  A
-// meeting of the cluster costs a microsecond: more than one CTA pays from some 2,048
-// pages on (8 heads of one sequence, 2,000 pages: 13.4 us with one, 12.6 with two, 13.4
-// with four; 8,125 pages: 34.5, 23.4, 19.4), as long as every CTA has an SM of its own
-// (96 units of 2,000 pages: 16.2 and 28.4).  Where there are more units than SMs, two at
-// a time on an SM work beside each other (560 units of 2,000 pages: 73 us with 512
-// threads, 62 with 256; 320 of 4,000: 84.2 and 83.5), but of long sequences a wave that
-// is not full costs more than that gains (160 units of 8,125 pages: 102 and 120; 560:
-// 232 and 270).
+// meeting of the cluster costs a microsecond, which r CTAs repay from some 512 r^2
+// pages on (8 heads of one sequence: 2,048 pages 13.5 us with one, 12.5 with two, 13.5
+// with four; 4,096 pages 16.4 with two, 15.2 with three, 15.8 with four; 8,192 pages
+// 24.0, 20.2, 19.7), as long as all clusters run at a time (48 units of 8,192 pages: 28
+// us by clusters of two, 47 by 48 of three, whose last ones wait; 96 of 2,000: 16 and
+// 28).  Where there are more units than SMs, two CTAs at a time on an SM work beside
+// each other (560 units of 2,000 pages: 73 us with 512 threads, 62 with 256; 320 of
+// 4,000: 84.2 and 83.5), but of long sequences a wave that is not full costs more than
+// that gains (160 units of 8,125 pages: 102 and 120; 560: 232 and 270).
 cudaError_t launch_select_pages(const SelectParams &p, cudaStream_t s)
 {
     const long long units = static_cast<long long>(p.batch) * p.q_len * p.hkv;
     const int tiles = (p.max_pages + kTile - 1) / kTile;
-    const long long sms = max(1, sm_count()), fit = max(1LL, sms / units);
-    const int threads = units > sms && p.max_pages <= 6144 ? 256 : 512;
-    long long ranks = max(1LL, min(8LL, min(fit, (p.max_pages + 1023LL) / 2048)));
+    const int threads = units > sm_count() && p.max_pages <= 6144 ? 256 : 512;
+    int ranks = 1;
+    if (units * 2 <= sm_count()) {
+        while (ranks < 8 && (2 * ranks + 1) * (2 * ranks + 1) * 128 <= p.max_pages)
+            ++ranks;                                             // (the next whole number to sqrt(pages / 512))
+        const cudaError_t e = allow_select<512>();
+        if (e != cudaSuccess)
+            return e;
+        while (ranks > 1 && units > clusters_at_once<page_select_kernel<512>, 512>(ranks, kMostShared))
+            --ranks;
+    }
     SelectParams q = p;
     auto bytes = [&]() {
-        q.chunk_tiles = (tiles + static_cast<int>(ranks) - 1) / static_cast<int>(ranks);
+        q.chunk_tiles = (tiles + ranks - 1) / ranks;
         return threads / 32 * kStages * kStageBytes + kQueryWords * sizeof(uint4) +
                static_cast<size_t>(q.chunk_tiles) * kTile * 4 + (static_cast<size_t>(q.chunk_tiles) * kTile + 31) / 32 * 4;
     };
-    constexpr size_t kMost = 227 * 1024 - sizeof(PickShared) - 1024;
     static_assert(512 / 32 * kStages * kStageBytes + kQueryWords * sizeof(uint4) +
-                          NVFP4KV_MAX_SELECT_PAGES / 8 / 8 * 33 + 1024 <= kMost, "the largest call fits eight CTAs");
-    while (bytes() > kMost && ranks < 8)
+                          NVFP4KV_MAX_SELECT_PAGES / 8 / 8 * 33 + 1024 <= kMostShared, "the largest call fits eight CTAs");
+    while (bytes() > kMostShared && ranks < 8)
         ++ranks;
     const size_t smem = bytes();
-    return threads == 256 ? launch_select<256>(q, units, smem, static_cast<int>(ranks), s)
-                          : launch_select<512>(q, units, smem, static_cast<int>(ranks), s);
+    return threads == 256 ? launch_select<256>(q, units, smem, ranks, s)
+                          : launch_select<512>(q, units, smem, ranks, s);
 }
 
 } // namespace nvfp4kv
