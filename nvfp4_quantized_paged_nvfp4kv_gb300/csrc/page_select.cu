@@ -163,12 +163,14 @@ __device__ __forceinline__ void write_bounds(const Keys &keys, int valid, int8_t
         *step = quot * keys.unit();
 }
 
-// One warp a page, or a part of its heads where there are fewer pages than warps;
-// the next head's keys are asked for before the last one's are worked on.  Bound
-// by its instructions more than by memory: some 250 a page-head, half of them
-// the expansion to f16 and the two comparisons a pair of values.
+// One warp a page, or a part of its heads where there are fewer pages than warps.
+// Bound by its instructions more than by memory, half of them the expansion to f16 and
+// the two comparisons a pair of values: 15 prompts of 32K at 8 heads take 77 us for 304
+// MB.  So many warps rather than loads ahead of their use: with the next head's keys in
+// registers, 32 warps an SM instead of 48, 81 us.  More CTAs than run at a time, for the
+// last pages' sake (8 an SM, 6 of which run; with 4, which are not placed evenly, 117).
 template <class Keys>
-__global__ void __launch_bounds__(kBoundThreads) page_bounds_kernel(const __grid_constant__ BoundsParams p)
+__global__ void __launch_bounds__(kBoundThreads, 6) page_bounds_kernel(const __grid_constant__ BoundsParams p)
 {
     extern __shared__ int32_t bsmem[];
     int32_t *scratch = bsmem, *prefix = bsmem + kPrefixScratch;
@@ -211,14 +213,10 @@ __global__ void __launch_bounds__(kBoundThreads) page_bounds_kernel(const __grid
         const int h1 = static_cast<int>(static_cast<long long>(p.hkv) * (part + 1) / parts);
         size_t head = static_cast<size_t>(phys) * p.hkv + h0;
         const uint8_t *rec = p.pool + head * Keys::kRecord;
-        Keys keys, next;
-        keys.load(rec, lane);
-        for (int h = h0; h < h1; ++h, ++head) {
-            rec += Keys::kRecord;
-            if (h + 1 < h1)
-                next.load(rec, lane);
+        for (int h = h0; h < h1; ++h, ++head, rec += Keys::kRecord) {
+            Keys keys;
+            keys.load(rec, lane);
             write_bounds(keys, valid, p.bounds + head * (2 * kHeadDim), p.steps + head, lane);
-            keys = next;
         }
     }
 }
@@ -228,7 +226,7 @@ cudaError_t launch_bounds(const BoundsParams &p, cudaStream_t s)
 {
     const size_t smem = (kPrefixScratch + static_cast<size_t>(p.batch) + 1) * sizeof(int32_t);
     const long long warps = static_cast<long long>(p.batch) * p.max_pages * p.hkv;
-    long long grid = static_cast<long long>(sm_count()) * 4;
+    long long grid = static_cast<long long>(sm_count()) * 8;
     grid = min(grid, (warps + kBoundThreads / 32 - 1) / (kBoundThreads / 32));
     return launch_pdl(page_bounds_kernel<Keys>, dim3(static_cast<unsigned>(grid)), dim3(kBoundThreads), smem, s, p);
 }
