@@ -6,7 +6,8 @@
 // pages -- a page list, or a short sequence -- those fixed costs are most of the
 // time.  Here the 8 warps of each of the cluster's 1 to 8 CTAs take equal runs of
 // the pages (staged and multiplied as in decode_kernel), the warps' softmax
-// states meet in shared memory and the CTAs' in the cluster's:
+// states meet in shared memory and the CTAs' in the cluster's (a row's states are sent
+// to the CTA that finishes it):
 //   M = max_w m_w,  o = sum_w 2^(m_w - M) O_w / sum_w 2^(m_w - M) l_w.
 // No partial goes to memory.  Two CTAs to an SM, so that one's merge runs beside
 // the other's loads.
@@ -323,10 +324,11 @@ ClusterParams cluster_params(const DecodeParams &p)
 // four in 192; 64 rows: 28.3 with three in 192, 27.9 with four in 256).  In us, measured
 // with 48 + 8 heads: a wave of clusters 3.6 and for each page of a CTA 0.115 with a
 // neighbour on the SM, 0.075 without (8 bits: 0.19, or 0.09 where query tokens share
-// their pages, and 0.085); the workers 10 (8 bits: 16, their CTAs leave no registers
-// for the next kernel's), 0.00042 (0.00053) a page-head and 0.015 a (query token, kv
-// head) to be joined.  80 of 256 pages: 14 and 18; 320 of 128 pages: 33 and 28; four
-// tokens of 12 sequences at 8K in 8 bits: 98 and 107.
+// their pages, and 0.085); the workers 8.5 (8 bits: 16, their CTAs leave no registers
+// for the next kernel's), 0.00036 (0.00053) a page-head and 0.012 (0.015) a (query
+// token, kv head) to be joined.  80 of 256 pages: 12 and 18; 320 of 128 pages: 32 and
+// 28, in 8 bits 42 and 46; 312 of 256: 55 and 42; four tokens of 12 sequences at 8K in 8
+// bits: 97 and 107.
 int cluster_decode_ranks(int64_t segments, int64_t pages, bool eight_bits, int shared)
 {
     const int64_t sms = sm_count(), slots = 2 * sms;
@@ -338,12 +340,13 @@ int cluster_decode_ranks(int64_t segments, int64_t pages, bool eight_bits, int s
         --ranks;
     ranks = ranks < pages / kClWarps ? ranks : pages / kClWarps;
     ranks = ranks < 1 ? 1 : ranks;
-    const int64_t ctas = segments * ranks, waves = (ctas + slots - 1) / slots;
-    const bool crowded = ctas > sms || ranks > 4;
-    const double busy = eight_bits ? (shared > 1 ? 0.09 : 0.19) : 0.115;
-    const double page = crowded ? busy : (eight_bits ? 0.085 : 0.075);
-    const double clusters = waves * (3.6 + page * ((pages + ranks - 1) / ranks));
-    const double workers = (eight_bits ? 16.0 : 10.0) + (eight_bits ? 0.00053 : 0.00042) * segments * pages + 0.015 * segments;
+    const double busy = eight_bits ? (shared > 1 ? 0.09 : 0.19) : 0.115, idle = eight_bits ? 0.085 : 0.075;
+    const int64_t full = segments * ranks / slots, rest = segments * ranks % slots;
+    const double each = static_cast<double>((pages + ranks - 1) / ranks);
+    const double last = rest == 0 ? 0.0 : 3.6 + (rest > sms || ranks > 4 ? busy : idle) * each;
+    const double clusters = full * (3.6 + busy * each) + last;
+    const double workers = eight_bits ? 16.0 + 0.00053 * segments * pages + 0.015 * segments
+                                      : 8.5 + 0.00036 * segments * pages + 0.012 * segments;
     return clusters <= workers ? static_cast<int>(ranks) : 0;
 }
 
