@@ -665,7 +665,8 @@ nvfp4kv_status fp8bkv_dequant(const fp8bkv_cache *cache, const int32_t *block_ta
 /* Decode attention over the block-scaled cache (a library utility with no
  * counterpart on the pages): q_len query tokens per sequence (1 ..
  * NVFP4KV_MAX_QUERY_TOKENS), causal among themselves, as in
- * nvfp4kv_paged_decode_multi.  Arguments, checks and results as there.
+ * nvfp4kv_paged_decode_multi.  Arguments, checks and results as there; seq_lens
+ * and block_table are read ahead of the wait for the kernel before, too.
  * Arithmetic: codes are exact in fp16, q too (bf16 significands under a power of
  * two a row; elements under 2^-28 of the row's largest lose bits); sm_scale and
  * a page's scales are applied in fp32, where scores, softmax and outputs are held;
@@ -735,7 +736,9 @@ nvfp4kv_status fp8bkv_page_bounds(const fp8bkv_cache *cache, const nvfp4kv_bound
  * max_pages_per_seq * 16] is clamped and sets NVFP4KV_DEV_BAD_LEN; the score of a
  * page id outside [0, num_pages) is that of page 0 and sets
  * NVFP4KV_DEV_BAD_PAGE.  Non-finite queries give an unspecified selection (of
- * pages there are).  pages overlaps nothing else (NVFP4KV_ERR_INVALID_ARG). */
+ * pages there are).  pages overlaps nothing else (NVFP4KV_ERR_INVALID_ARG).
+ * seq_lens and block_table are read ahead of the wait for the kernel before, as
+ * in nvfp4kv_paged_decode. */
 #define NVFP4KV_MAX_SELECT_PAGES 65536
 nvfp4kv_status nvfp4kv_select_pages(const nvfp4kv_bounds *bounds, const void *q, int32_t batch, int32_t q_len,
                                     int32_t num_q_heads, const int32_t *block_table, int32_t max_pages_per_seq,
@@ -751,7 +754,8 @@ nvfp4kv_status nvfp4kv_select_pages(const nvfp4kv_bounds *bounds, const void *q,
  *   q    bf16 [batch][q_len][num_q_heads][128], out the same in out_dtype
  *   workspace, num_workers  as for nvfp4kv_paged_decode
  * batch * q_len at most NVFP4KV_MAX_BATCH; other arguments, checks and arithmetic
- * as for nvfp4kv_paged_decode. */
+ * as for nvfp4kv_paged_decode, whose reading of seq_lens and block_table ahead of
+ * the wait for the kernel before this call shares (pages is read behind it). */
 nvfp4kv_status nvfp4kv_selected_decode(const nvfp4kv_cache *cache, const void *q, int32_t batch, int32_t q_len,
                                        int32_t num_q_heads, const int32_t *block_table, int32_t max_pages_per_seq,
                                        const int32_t *seq_lens, const int32_t *pages, int32_t budget, float sm_scale,

@@ -1,4 +1,6 @@
-// Decode over listed pages, of either cache: instantiations and launchers.
+// Decode over listed pages, of either cache: instantiations and launchers of the worker
+// split, which many rows of long lists take (312 rows of 256 pages in 4 bits: 42 us, by
+// clusters 55) and every call that names its workers; decode_cluster.cu has the rest.
 #include "decode_common.cuh"
 
 namespace nvfp4kv {
