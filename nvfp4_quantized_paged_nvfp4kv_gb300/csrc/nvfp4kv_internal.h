@@ -247,6 +247,7 @@ struct SelectParams {
     int first;                   // pages always taken, at the beginning
     int last;                    // ... and at the end
     int chunk_tiles;             // (set by the launcher) tiles of 16 pages a CTA has at most
+    long long unit0;             // (set by the launcher) its first (query token, kv head)
 };
 
 // Chunk attention over the paged NVFP4 cache.

@@ -215,6 +215,18 @@ def test_select_a_million_tokens():
     assert_picks(b, queries(2, 2, 4, 1), bt, [65536 * 16, 65535 * 16 + 1], 700, 4, 4, 2)
 
 
+@pytest.mark.parametrize("rows,q_len,hkv,pages", [(156, 1, 1, 6200), (53, 3, 1, 6145), (310, 1, 1, 2050), (41, 1, 8, 2048),
+                                                  (50, 1, 1, 8192), (21, 1, 2, 20000)])
+def test_select_more_or_fewer_units_than_run_at_a_time(rows, q_len, hkv, pages):
+    """Long tables, so that units past the last full wave and units in clusters come up."""
+    rng = np.random.default_rng(rows)
+    lens = rng.integers(pages * 8, pages * 16 + 1, rows)
+    lens[0], lens[1], lens[-2], lens[-1] = pages * 16, 0, 37, pages * 16 - 15
+    b = make_bounds(400, hkv, 11)
+    bt = rng.integers(0, 400, (rows, pages)).astype(np.int32)
+    assert_picks(b, queries(rows, q_len, hkv, 6), bt, lens.tolist(), 40, 2, 3, q_len)
+
+
 def test_select_same_result_whatever_else_is_in_the_call():
     """A sequence's lists do not depend on its neighbours or on the replay."""
     rng = np.random.default_rng(4)
