@@ -431,11 +431,11 @@ nvfp4kv_status check_select_sizes(int32_t batch, int32_t q_len, int32_t hkv, int
     return NVFP4KV_OK;
 }
 
-// CTAs a cluster for a decode over listed pages (0: the worker split).
-int cluster_ranks(const DecodeParams &p, bool eight_bits)
+// How clusters take a decode over listed pages (none of it: the worker split).
+ClusterPlan cluster_plan(const DecodeParams &p, bool eight_bits)
 {
-    return cluster_decode_ranks(static_cast<int64_t>(p.batch) * p.hkv, p.budget < p.max_pages ? p.budget : p.max_pages,
-                                eight_bits, 1);
+    return plan_cluster_decode(static_cast<int64_t>(p.batch) * p.hkv, p.budget < p.max_pages ? p.budget : p.max_pages,
+                               eight_bits, true, p.sel_q_len);
 }
 
 // Decode over listed pages: fills p (except the cache's pool and scales).
@@ -1180,12 +1180,13 @@ nvfp4kv_status fp8bkv_paged_decode(const fp8bkv_cache *cache, const void *q, int
         return st;
     p.pool = static_cast<const uint8_t *>(cache->pool);
     // short sequences: each query token by a cluster of its own
-    const int ranks =
-        num_workers == 0 ? cluster_decode_ranks(static_cast<int64_t>(batch) * q_len * p.hkv, max_pages_per_seq, true, q_len) : 0;
-    if (ranks > 0) {
+    const ClusterPlan plan =
+        num_workers == 0 ? plan_cluster_decode(static_cast<int64_t>(batch) * q_len * p.hkv, max_pages_per_seq, true, false, q_len)
+                         : ClusterPlan{};
+    if (plan.first > 0) {
         p.batch = batch * q_len;
         p.sel_q_len = q_len;
-        return from_cuda(launch_cluster_decode_fp8_block(p, ranks, to_cuda(stream)));
+        return from_cuda(launch_cluster_decode_fp8_block(p, plan, to_cuda(stream)));
     }
     p.q_len = q_len;
     p.rows = p.group * q_len;
@@ -1292,8 +1293,9 @@ nvfp4kv_status nvfp4kv_selected_decode(const nvfp4kv_cache *cache, const void *q
         return st;
     p.pool = static_cast<const uint8_t *>(cache->pool);
     apply_tensor_scale(p, sm_scale, cache);
-    if (const int ranks = num_workers == 0 ? cluster_ranks(p, false) : 0)
-        return from_cuda(launch_cluster_decode_nvfp4(p, ranks, to_cuda(stream)));
+    const ClusterPlan plan = num_workers == 0 ? cluster_plan(p, false) : ClusterPlan{};
+    if (plan.first > 0)
+        return from_cuda(launch_cluster_decode_nvfp4(p, plan, to_cuda(stream)));
     cudaError_t e = launch_decode_selected_nvfp4(p, to_cuda(stream));
     if (e == cudaSuccess)
         e = launch_merge(p, to_cuda(stream));
@@ -1317,8 +1319,9 @@ nvfp4kv_status fp8bkv_selected_decode(const fp8bkv_cache *cache, const void *q, 
     if (st != NVFP4KV_OK || batch == 0)
         return st;
     p.pool = static_cast<const uint8_t *>(cache->pool);
-    if (const int ranks = num_workers == 0 ? cluster_ranks(p, true) : 0)
-        return from_cuda(launch_cluster_decode_fp8_block(p, ranks, to_cuda(stream)));
+    const ClusterPlan plan = num_workers == 0 ? cluster_plan(p, true) : ClusterPlan{};
+    if (plan.first > 0)
+        return from_cuda(launch_cluster_decode_fp8_block(p, plan, to_cuda(stream)));
     cudaError_t e = launch_decode_selected_fp8_block(p, to_cuda(stream));
     if (e == cudaSuccess)
         e = launch_merge(p, to_cuda(stream));

@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(kClThreads, 2) cluster_decode_kernel(const __g
     const uint32_t rank = cluster_rank(), ranks = cluster_size();
     if (ranks > 1)
         cluster_arrive();                        // (this CTA runs: it can be written to)
-    const int seg = blockIdx.x / ranks, row = seg / p.hkv, h = seg - row * p.hkv;
+    const int seg = p.seg0 + blockIdx.x / ranks, row = seg / p.hkv, h = seg - row * p.hkv;
     const int b = row / p.sel_q_len;
     if (rank == 0 && h == 0 && threadIdx.x == 0 && row == b * p.sel_q_len) {
         const int L = __ldg(p.seq_lens + b);
@@ -296,22 +296,50 @@ __global__ void __launch_bounds__(kClThreads, 2) cluster_decode_kernel(const __g
 }
 
 template <class Fmt, bool kListed, class Params>
-cudaError_t launch(const Params &c, const DecodeParams &p, int ranks, cudaStream_t s)
+cudaError_t launch(Params &c, const DecodeParams &p, const ClusterPlan &plan, cudaStream_t s)
 {
     constexpr auto kernel = cluster_decode_kernel<Fmt, kListed, Params>;
-    const cudaError_t e = allow_shared<kernel>();
-    if (e != cudaSuccess)
-        return e;
-    return launch_cluster(kernel, dim3(static_cast<unsigned>(p.batch) * p.hkv * ranks), dim3(kClThreads), ranks,
-                          kClSmem<Fmt>, s, c);
+    cudaError_t e = allow_shared<kernel>();
+    const int segments = p.batch * p.hkv;
+    auto part = [&](int n, int ranks) {
+        if (e == cudaSuccess && n > 0)
+            e = launch_cluster(kernel, dim3(static_cast<unsigned>(n) * ranks), dim3(kClThreads), ranks, kClSmem<Fmt>, s, c);
+        c.seg0 += n;
+    };
+    part(plan.first, plan.ranks);
+    part(segments - plan.first, plan.rest_ranks);
+    return e;
 }
 
 ClusterParams cluster_params(const DecodeParams &p)
 {
     return {p.pool,      p.q,         p.out,    p.block_table, p.seq_lens, p.sel_pages, p.dev_status, p.hq,         p.hkv,
             p.group,     p.max_pages, p.num_pages, p.budget,   p.sel_q_len, p.out_bf16, p.qscale,     p.out_scale,
-            p.wait_limit};
+            p.wait_limit, 0};
 }
+
+// What plan_cluster_decode reckons with.
+struct ClusterCost {
+    int64_t pages, sms, slots;
+    double busy, idle;           // us a page of a CTA, with a neighbour on the SM and without
+
+    // CTAs a cluster
+    int64_t ranks(int64_t segments) const
+    {
+        int64_t r = slots / segments;
+        r = r < 8 ? r : 8;
+        while ((r > 4 && segments * r > slots * 3 / 4) || (r > 2 && segments * r > slots * 6 / 7))
+            --r;
+        r = r < pages / kClWarps ? r : pages / kClWarps;
+        return r < 1 ? 1 : r;
+    }
+    double wave(int64_t r, bool crowded) const { return 3.6 + (crowded ? busy : idle) * ((pages + r - 1) / r); }
+    double all(int64_t segments, int64_t r) const
+    {
+        const int64_t full = segments * r / slots, rest = segments * r % slots;
+        return full * wave(r, true) + (rest == 0 ? 0.0 : wave(r, rest > sms || r > 4));
+    }
+};
 
 } // namespace
 
@@ -321,51 +349,61 @@ ClusterParams cluster_params(const DecodeParams &p)
 // before leaves its SMs one by one, the last clusters wait for a part with room (a
 // selection and the decode of 96 rows of 128 pages in 8 bits: 38.6 us with three CTAs a
 // cluster in 288 of 304 places, 31.9 with two; 48 rows: 31.3 with six in 288, 24.5 with
-// four in 192; 64 rows: 28.3 with three in 192, 27.9 with four in 256).  In us, measured
-// with 48 + 8 heads: a wave of clusters 3.6 and for each page of a CTA 0.115 with a
-// neighbour on the SM, 0.075 without (8 bits: 0.19, or 0.09 where query tokens share
-// their pages, and 0.085); the workers 8.5 (8 bits: 16, their CTAs leave no registers
-// for the next kernel's), 0.00036 (0.00053) a page-head and 0.012 (0.015) a (query
-// token, kv head) to be joined.  80 of 256 pages: 12 and 18; 320 of 128 pages: 32 and
-// 28, in 8 bits 42 and 46; 312 of 256: 55 and 42; four tokens of 12 sequences at 8K in 8
-// bits: 97 and 107.
-int cluster_decode_ranks(int64_t segments, int64_t pages, bool eight_bits, int shared)
+// four in 192; 64 rows: 28.3 with three in 192, 27.9 with four in 256).  Full waves of one
+// or two CTAs a list may leave a rest that goes faster by a launch of its own, as larger
+// clusters (320 lists of 128 pages in 8 bits: 42 us by one launch, 37 by two).  Not so
+// where all pages are read, whose numbers differ: the second launch cannot fill in
+// behind the short ones of the first (four tokens of 12 sequences in 8 bits, all of 8K
+// tokens, 97 and 85 us; of 100 to 8K, 62 and 80).
+// In us, measured with 48 + 8 heads: a wave of clusters 3.6 and for each page of a CTA
+// 0.115 with a neighbour on the SM, 0.075 without (8 bits: 0.19, or 0.09 where query
+// tokens share their pages, and 0.085), a second launch 4; the workers 8.5 (8 bits: 16,
+// their CTAs leave no registers for the next kernel's), 0.00036 (0.00053) a page-head and
+// 0.012 (0.015) a (query token, kv head) to be joined.
+ClusterPlan plan_cluster_decode(int64_t segments, int64_t pages, bool eight_bits, bool listed, int q_len)
 {
-    const int64_t sms = sm_count(), slots = 2 * sms;
-    if (segments > (int64_t{1} << 27))
-        return 0;
-    int64_t ranks = segments > 0 ? slots / segments : 1;
-    ranks = ranks < 8 ? ranks : 8;
-    while ((ranks > 4 && segments * ranks > slots * 3 / 4) || (ranks > 2 && segments * ranks > slots * 6 / 7))
-        --ranks;
-    ranks = ranks < pages / kClWarps ? ranks : pages / kClWarps;
-    ranks = ranks < 1 ? 1 : ranks;
-    const double busy = eight_bits ? (shared > 1 ? 0.09 : 0.19) : 0.115, idle = eight_bits ? 0.085 : 0.075;
-    const int64_t full = segments * ranks / slots, rest = segments * ranks % slots;
-    const double each = static_cast<double>((pages + ranks - 1) / ranks);
-    const double last = rest == 0 ? 0.0 : 3.6 + (rest > sms || ranks > 4 ? busy : idle) * each;
-    const double clusters = full * (3.6 + busy * each) + last;
+    if (segments < 1 || segments > (int64_t{1} << 27))
+        return {};
+    const int64_t sms = sm_count();
+    const ClusterCost cost{pages, sms, 2 * sms, eight_bits ? (!listed && q_len > 1 ? 0.09 : 0.19) : 0.115, eight_bits ? 0.085 : 0.075};
+    int64_t ranks = cost.ranks(segments), first = segments, rest_ranks = 1;
+    double best = cost.all(segments, ranks);
+    for (int64_t r = 1; listed && r <= 2 && (r == 1 || pages >= 2 * kClWarps); ++r) {
+        const int64_t n = segments * r / cost.slots * (cost.slots / r), rest = segments - n;
+        if (n <= 0 || rest <= 0 || cost.ranks(rest) == r)
+            continue;
+        const double both = cost.all(n, r) + cost.all(rest, cost.ranks(rest)) + 4.0;
+        if (both < best) {
+            best = both;
+            ranks = r;
+            first = n;
+            rest_ranks = cost.ranks(rest);
+        }
+    }
     const double workers = eight_bits ? 16.0 + 0.00053 * segments * pages + 0.015 * segments
                                       : 8.5 + 0.00036 * segments * pages + 0.012 * segments;
-    return clusters <= workers ? static_cast<int>(ranks) : 0;
+    if (best > workers)
+        return {};
+    return {static_cast<int>(first), static_cast<int>(ranks), static_cast<int>(rest_ranks)};
 }
 
-cudaError_t launch_cluster_decode_nvfp4(const DecodeParams &p, int ranks, cudaStream_t s)
+cudaError_t launch_cluster_decode_nvfp4(const DecodeParams &p, const ClusterPlan &plan, cudaStream_t s)
 {
+    ClusterParams all = cluster_params(p);
     if (!p.hs.per_head)
-        return launch<Nvfp4Format, true>(cluster_params(p), p, ranks, s);
-    ClusterHeadParams c{cluster_params(p), {}, {}};
+        return launch<Nvfp4Format, true>(all, p, plan, s);
+    ClusterHeadParams c{all, {}, {}};
     for (int h = 0; h < p.hkv; ++h) {
         c.qs[h] = p.qs[h];
         c.vs[h] = p.hs.v[h];
     }
-    return launch<Nvfp4Format, true>(c, p, ranks, s);
+    return launch<Nvfp4Format, true>(c, p, plan, s);
 }
 
-cudaError_t launch_cluster_decode_fp8_block(const DecodeParams &p, int ranks, cudaStream_t s)
+cudaError_t launch_cluster_decode_fp8_block(const DecodeParams &p, const ClusterPlan &plan, cudaStream_t s)
 {
-    return p.sel_pages != nullptr ? launch<Fp8BlockFormat, true>(cluster_params(p), p, ranks, s)
-                                  : launch<Fp8BlockFormat, false>(cluster_params(p), p, ranks, s);
+    ClusterParams c = cluster_params(p);
+    return p.sel_pages != nullptr ? launch<Fp8BlockFormat, true>(c, p, plan, s) : launch<Fp8BlockFormat, false>(c, p, plan, s);
 }
 
 } // namespace nvfp4kv

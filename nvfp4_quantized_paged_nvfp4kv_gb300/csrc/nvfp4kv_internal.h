@@ -60,6 +60,7 @@ struct ClusterParams {
     float qscale;
     float out_scale;
     uint32_t wait_limit;
+    int seg0;                    // the launch's first (query token, kv head)
 };
 
 struct ClusterHeadParams : ClusterParams {
@@ -395,11 +396,15 @@ cudaError_t launch_decode_fp8(const DecodeParams &p, cudaStream_t s);
 cudaError_t launch_decode_fp8_block(const DecodeParams &p, cudaStream_t s);         // (p.q_len > 1: several tokens)
 cudaError_t launch_decode_selected_nvfp4(const DecodeParams &p, cudaStream_t s);
 cudaError_t launch_decode_selected_fp8_block(const DecodeParams &p, cudaStream_t s);
-// CTAs of a cluster for each (query token, kv head) of at most so many pages; 0:
-// the worker split is the faster one.  `shared`: query tokens that see the same pages.
-int cluster_decode_ranks(int64_t segments, int64_t pages, bool eight_bits, int shared);
-cudaError_t launch_cluster_decode_nvfp4(const DecodeParams &p, int ranks, cudaStream_t s);
-cudaError_t launch_cluster_decode_fp8_block(const DecodeParams &p, int ranks, cudaStream_t s);   // (listed or all pages)
+// How clusters take a decode of so many (query token, kv head)s of at most so many pages.
+struct ClusterPlan {
+    int first = 0;               // (query token, kv head)s of the first launch; 0: the worker split
+    int ranks = 1, rest_ranks = 1;
+};
+ClusterPlan plan_cluster_decode(int64_t segments, int64_t pages, bool eight_bits, bool listed, int q_len);
+cudaError_t launch_cluster_decode_nvfp4(const DecodeParams &p, const ClusterPlan &plan, cudaStream_t s);
+cudaError_t launch_cluster_decode_fp8_block(const DecodeParams &p, const ClusterPlan &plan,
+                                            cudaStream_t s);        // (listed or all pages)
 cudaError_t launch_merge(const DecodeParams &p, cudaStream_t s);
 cudaError_t launch_block_append(const BlockAppendParams &p, cudaStream_t s);
 cudaError_t launch_block_read(const BlockReadParams &p, cudaStream_t s);
