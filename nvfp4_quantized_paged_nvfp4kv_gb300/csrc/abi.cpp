@@ -191,6 +191,7 @@ nvfp4kv_status check_decode(int32_t hkv, int32_t num_pages, const void *q, int32
     p.q_len = 1;
     p.rows = group;
     p.row_groups = 1;
+    p.lanes = 1;
     p.wait_limit = wait_limit();
     return NVFP4KV_OK;
 }
@@ -434,8 +435,9 @@ nvfp4kv_status check_select_sizes(int32_t batch, int32_t q_len, int32_t hkv, int
 // How clusters take a decode over listed pages (none of it: the worker split).
 ClusterPlan cluster_plan(const DecodeParams &p, bool eight_bits)
 {
-    return plan_cluster_decode(static_cast<int64_t>(p.batch) * p.hkv, p.budget < p.max_pages ? p.budget : p.max_pages,
-                               eight_bits, true, p.sel_q_len);
+    const int64_t segments = static_cast<int64_t>(p.batch) * p.hkv;
+    return plan_cluster_decode(segments, segments, p.budget < p.max_pages ? p.budget : p.max_pages, eight_bits, true,
+                               p.sel_q_len);
 }
 
 // Decode over listed pages: fills p (except the cache's pool and scales).
@@ -1179,20 +1181,23 @@ nvfp4kv_status fp8bkv_paged_decode(const fp8bkv_cache *cache, const void *q, int
     if (st != NVFP4KV_OK || batch == 0)
         return st;
     p.pool = static_cast<const uint8_t *>(cache->pool);
+    const int rows = p.group * q_len, row_groups = (rows + kMaxGroup - 1) / kMaxGroup;
+    const int64_t heads = static_cast<int64_t>(batch) * p.hkv;
     // short sequences: each query token by a cluster of its own
-    const ClusterPlan plan =
-        num_workers == 0 ? plan_cluster_decode(static_cast<int64_t>(batch) * q_len * p.hkv, max_pages_per_seq, true, false, q_len)
-                         : ClusterPlan{};
+    const ClusterPlan plan = num_workers == 0 ? plan_cluster_decode(heads * q_len, heads * row_groups, max_pages_per_seq,
+                                                                    true, false, q_len)
+                                              : ClusterPlan{};
     if (plan.first > 0) {
         p.batch = batch * q_len;
         p.sel_q_len = q_len;
         return from_cuda(launch_cluster_decode_fp8_block(p, plan, to_cuda(stream)));
     }
     p.q_len = q_len;
-    p.rows = p.group * q_len;
-    p.row_groups = (p.rows + kMaxGroup - 1) / kMaxGroup;
+    p.rows = rows;
+    p.row_groups = row_groups;
     if (static_cast<int64_t>(batch) * cache->num_kv_heads * p.row_groups * max_pages_per_seq > (int64_t{1} << 31) - 1)
         return NVFP4KV_ERR_UNSUPPORTED;
+    p.lanes = p.row_groups > 1 && p.num_workers >= p.row_groups ? p.row_groups : 1;
     cudaError_t e = launch_decode_fp8_block(p, to_cuda(stream));
     if (e == cudaSuccess)
         e = launch_merge(p, to_cuda(stream));

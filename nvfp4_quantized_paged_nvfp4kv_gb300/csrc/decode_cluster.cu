@@ -355,17 +355,22 @@ struct ClusterCost {
 // where all pages are read, whose numbers differ: the second launch cannot fill in
 // behind the short ones of the first (four tokens of 12 sequences in 8 bits, all of 8K
 // tokens, 97 and 85 us; of 100 to 8K, 62 and 80).
-// In us, measured with 48 + 8 heads: a wave of clusters 3.6 and for each page of a CTA
-// 0.115 with a neighbour on the SM, 0.075 without (8 bits: 0.19, or 0.09 where query
-// tokens share their pages, and 0.085), a second launch 4; the workers 8.5 (8 bits: 16,
-// their CTAs leave no registers for the next kernel's), 0.00036 (0.00053) a page-head and
-// 0.012 (0.015) a (query token, kv head) to be joined.
-ClusterPlan plan_cluster_decode(int64_t segments, int64_t pages, bool eight_bits, bool listed, int q_len)
+// In us, measured: a wave of clusters 3.6 and for each page of a CTA 0.115 with a
+// neighbour on the SM, 0.075 without (8 bits: 0.19, or 0.105 where query tokens share
+// their pages, and 0.085), a second launch 4; the workers 8.5 (8 bits: 16, or 18 for
+// several tokens; their CTAs leave no registers for the next kernel's), 0.00036 (one
+// token in 8 bits 0.00053) a page-head and 0.012 (0.015) a segment to be joined, of
+// which `worker_segments` are row groups of up to eight query rows.  80 of 256 pages in 4
+// bits: 11 and 18 us; 312 of 256: 55 and 42.  Four tokens in 8 bits: 20 sequences of 2K
+// and three tokens 36 and 46, 12 of 8K 98 and 93, six of 128K to 160K 1,059 and 477.
+ClusterPlan plan_cluster_decode(int64_t segments, int64_t worker_segments, int64_t pages, bool eight_bits, bool listed,
+                                int q_len)
 {
     if (segments < 1 || segments > (int64_t{1} << 27))
         return {};
     const int64_t sms = sm_count();
-    const ClusterCost cost{pages, sms, 2 * sms, eight_bits ? (!listed && q_len > 1 ? 0.09 : 0.19) : 0.115, eight_bits ? 0.085 : 0.075};
+    const bool shared = !listed && q_len > 1;
+    const ClusterCost cost{pages, sms, 2 * sms, eight_bits ? (shared ? 0.105 : 0.19) : 0.115, eight_bits ? 0.085 : 0.075};
     int64_t ranks = cost.ranks(segments), first = segments, rest_ranks = 1;
     double best = cost.all(segments, ranks);
     for (int64_t r = 1; listed && r <= 2 && (r == 1 || pages >= 2 * kClWarps); ++r) {
@@ -380,8 +385,10 @@ ClusterPlan plan_cluster_decode(int64_t segments, int64_t pages, bool eight_bits
             rest_ranks = cost.ranks(rest);
         }
     }
-    const double workers = eight_bits ? 16.0 + 0.00053 * segments * pages + 0.015 * segments
-                                      : 8.5 + 0.00036 * segments * pages + 0.012 * segments;
+    const double heads = static_cast<double>(worker_segments) * pages, joins = static_cast<double>(worker_segments);
+    const double workers = !eight_bits ? 8.5 + 0.00036 * heads + 0.012 * joins
+                           : shared    ? 18.0 + 0.00036 * heads + 0.012 * joins
+                                       : 16.0 + 0.00053 * heads + 0.015 * joins;
     if (best > workers)
         return {};
     return {static_cast<int>(first), static_cast<int>(ranks), static_cast<int>(rest_ranks)};

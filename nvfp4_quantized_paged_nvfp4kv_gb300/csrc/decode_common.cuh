@@ -600,6 +600,12 @@ __device__ __forceinline__ void attend_pages(const uint32_t (&qf)[16], float inv
 // of one kv head ("virtual heads" hkv * row_groups per sequence), numbered
 // with the row group innermost so that the row groups of a kv head read the
 // same pages close together in time.
+// With a scale a page (kLanes) the row groups of a kv head are taken side by side
+// instead, where there are workers enough: worker w is worker floor(w / lanes) of the
+// one-row-group split and takes row group w mod lanes, so that neighbours read the same
+// pages at the same time whatever the lengths.  (In the other numbering a page comes up
+// again some segments' worth of workers later, in another part of their time, which L2
+// only bridges for caches it holds.)
 // kSelected: attention over listed pages.  A "sequence" is one query token, a
 // segment's pages are the entries of its list; they come from the kernel
 // before, so nothing of them is read ahead of the wait.
@@ -638,7 +644,9 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, kDecodeCtasPerSm) decode_ke
     // cache records, q, the new K/V, the output and the workspace are touched
     // only after the wait.
     const int max_len = p.max_pages * kPageSize;
-    const int nseg = kMulti ? p.hkv * p.row_groups : p.hkv;   // segments per sequence
+    constexpr bool kLanes = kMulti && Fmt::kPageScales;
+    const int lanes = kLanes ? p.lanes : 1;
+    const int nseg = kMulti ? p.hkv * p.row_groups / lanes : p.hkv;   // segments per sequence
     if constexpr (kSelected) {
         build_prefix_of(
             [&](int row) {
@@ -663,9 +671,10 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, kDecodeCtasPerSm) decode_ke
 
     const int w = blockIdx.x * kDecodeWarps + warp;
     const long long T = prefix[p.batch];
-    const long long NW = effective_workers(p.num_workers, T);
-    const int lo = w < NW ? static_cast<int>((T * w) / NW) : 0;
-    const int hi = w < NW ? static_cast<int>((T * (w + 1)) / NW) : 0;
+    const long long NW = effective_workers(kLanes ? p.num_workers / lanes : p.num_workers, T);
+    const int ws = kLanes ? w / lanes : w, lane_rg = kLanes ? w - ws * lanes : 0;
+    const int lo = ws < NW ? static_cast<int>((T * ws) / NW) : 0;
+    const int hi = ws < NW ? static_cast<int>((T * (ws + 1)) / NW) : 0;
 
     // The worker: this warp's page-heads [lo, hi).
     auto run_worker = [&]() {
@@ -714,7 +723,7 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, kDecodeCtasPerSm) decode_ke
             hh = r / n;
             const int pg = r - hh * n;
             if constexpr (kMulti)
-                hh /= p.row_groups;                  // the kv head of the row group
+                hh = (kLanes ? hh * lanes : hh) / p.row_groups;      // the kv head of the row group
             phys = __ldg(p.block_table + static_cast<size_t>(b) * p.max_pages + pg);
         }
     };
@@ -830,8 +839,9 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, kDecodeCtasPerSm) decode_ke
         bool has_row = gid < g;
         const uint16_t *qsrc = p.q + (static_cast<size_t>(b) * p.hq + h * g + gid) * kHeadDim;
         if constexpr (kMulti) {
-            hp = h / p.row_groups;
-            rg = h - hp * p.row_groups;
+            const int v = kLanes ? h * lanes + lane_rg : h;
+            hp = v / p.row_groups;
+            rg = v - hp * p.row_groups;
             const int r = rg * kMaxGroup + gid;
             has_row = r < p.rows;
             qsrc = p.q + out_row(p, b, hp, has_row ? r : 0);

@@ -23,16 +23,18 @@ __device__ __forceinline__ void merge_segment_row(const DecodeParams &p, int32_t
     __shared__ int seg[3];                       // first contributor, count (-1: empty sequence), its slot
     int32_t *scratch = msmem;
     int32_t *prefix = msmem + kPrefixScratch;
-    const int nseg = p.hkv * p.row_groups;       // segments per sequence (row groups of kv heads)
+    const int nvirt = p.hkv * p.row_groups;      // row groups of a sequence's kv heads
+    const int nseg = nvirt / p.lanes;            // segments per sequence
     if (p.sel_pages != nullptr)
         build_prefix_of([&](int row) { return nseg * selected_row_pages(p, row); }, p.batch, prefix, scratch);
     else
         build_prefix(p.seq_lens, p.batch, nseg, p.max_pages * kPageSize, prefix, scratch, nullptr);
 
-    const int b = blockIdx.x / nseg;
-    const int h = blockIdx.x - b * nseg;
+    const int b = blockIdx.x / nvirt;
+    const int v = blockIdx.x - b * nvirt;
+    const int h = v / p.lanes, lane_rg = v - h * p.lanes;
     const int i = blockIdx.y;                    // row of the segment's row group
-    const int hp = h / p.row_groups, row = (h - hp * p.row_groups) * kMaxGroup + i;
+    const int hp = v / p.row_groups, row = (v - hp * p.row_groups) * kMaxGroup + i;
     if (row >= p.rows)
         return;
     const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
@@ -41,14 +43,14 @@ __device__ __forceinline__ void merge_segment_row(const DecodeParams &p, int32_t
         int wf = 0, nc = -1, slot = 0;
         if (n > 0) {
             const long long T = prefix[p.batch];
-            const long long NW = effective_workers(p.num_workers, T);
+            const long long NW = effective_workers(p.num_workers / p.lanes, T);
             const int seg_begin = prefix[b] + h * n;
             wf = owner_of(seg_begin, T, NW);
             nc = owner_of(static_cast<long long>(seg_begin) + n - 1, T, NW) - wf + 1;
             // wf reached this segment from an earlier one unless it starts at
             // seg_begin; every later contributor starts inside the segment, so
             // this is its first partial (slot 2w)
-            slot = partial_slot(wf, seg_begin, T, NW);
+            slot = partial_slot(wf, seg_begin, T, NW) + 2 * (wf * (p.lanes - 1) + lane_rg);
         }
         seg[0] = wf;
         seg[1] = nc;
@@ -75,7 +77,7 @@ __device__ __forceinline__ void merge_segment_row(const DecodeParams &p, int32_t
                 lk[u] = 0.f;
                 v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (k < nc) {
-                    const int slot = k == 0 ? slot_wf : 2 * (wf + k);
+                    const int slot = k == 0 ? slot_wf : 2 * ((wf + k) * p.lanes + lane_rg);
                     const float *sl = p.partials + static_cast<size_t>(slot) * kPartialFloats;
                     mk[u] = __ldcg(sl + kMaxGroup * kHeadDim + i);
                     lk[u] = __ldcg(sl + kMaxGroup * kHeadDim + kMaxGroup + i);

@@ -100,6 +100,7 @@ struct DecodeParams {
     int q_len;
     int rows;
     int row_groups;
+    int lanes;                   // row groups that neighbouring workers take side by side: row_groups, or 1
     // per-head tensor scales (NVFP4): append divisors and V output scales,
     // and the query scale sm_scale * log2(e) * G_k,h of each kv head
     HeadScales hs;
@@ -401,7 +402,8 @@ struct ClusterPlan {
     int first = 0;               // (query token, kv head)s of the first launch; 0: the worker split
     int ranks = 1, rest_ranks = 1;
 };
-ClusterPlan plan_cluster_decode(int64_t segments, int64_t pages, bool eight_bits, bool listed, int q_len);
+ClusterPlan plan_cluster_decode(int64_t segments, int64_t worker_segments, int64_t pages, bool eight_bits, bool listed,
+                                int q_len);
 cudaError_t launch_cluster_decode_nvfp4(const DecodeParams &p, const ClusterPlan &plan, cudaStream_t s);
 cudaError_t launch_cluster_decode_fp8_block(const DecodeParams &p, const ClusterPlan &plan,
                                             cudaStream_t s);        // (listed or all pages)

@@ -250,6 +250,17 @@ def test_decode_pages_of_different_scales(exps, q_size, sm_scale, q_len):
     attention(cache, ref, bt, lens, 8, 2, q_len, rng, sm_scale=sm_scale, q_size=q_size)
 
 
+@pytest.mark.parametrize("q_len,g", [(2, 8), (3, 5), (4, 3), (5, 8), (8, 6), (8, 1)])
+@pytest.mark.parametrize("workers", [2, 8, 61, 2432])
+def test_decode_row_groups_side_by_side(q_len, g, workers):
+    """Fewer workers than row groups, numbers that row groups do not divide, more than
+    there is work for; lengths that put borders of the split inside segments."""
+    rng = np.random.default_rng(q_len + workers)
+    lens = [0, 3, 777, 1, 2001, 64]
+    cache, ref, bt = filled(rng, lens, 2)
+    attention(cache, ref, bt, lens, 2 * g, 2, q_len, rng, workers=workers)
+
+
 def test_decode_long_sequence():
     rng = np.random.default_rng(3)
     lens = [40007, 9000]
