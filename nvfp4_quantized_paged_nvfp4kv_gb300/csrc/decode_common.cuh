@@ -1038,7 +1038,9 @@ __global__ void __launch_bounds__(kDecodeWarps * 32, kDecodeCtasPerSm) decode_ke
 // step's decode CTA need not wait for them to leave; 128 threads while four
 // groups do (seven CTAs to an SM once the decode CTA has left); wider CTAs for
 // the few long segments of a small batch at a long context.
-template <int kThreads>
+enum class Split { kSequences, kSelected, kLanes };
+
+template <int kThreads, Split kSplit>
 __global__ void __launch_bounds__(kThreads, kThreads == 64 ? 16 : 1) merge_kernel(const __grid_constant__ DecodeParams p);
 
 } // namespace nvfp4kv

@@ -13,7 +13,10 @@ namespace nvfp4kv {
 // its own running maximum (one pass over the partials), and the groups are
 // combined in shared memory at the end.  The segment's contributor range is
 // worked out once per CTA, before the wait for the decode kernel.
-template <int kThreads>
+// The numberings of the work split: sequences; query tokens with page lists; row groups
+// side by side.  (Told apart at compile time: in one kernel the two divisions and the
+// other lengths cost the sequences' merge a microsecond of four.)
+template <int kThreads, Split kSplit>
 __device__ __forceinline__ void merge_segment_row(const DecodeParams &p, int32_t *msmem)
 {
     constexpr int kGroups = kThreads / 32;
@@ -23,18 +26,19 @@ __device__ __forceinline__ void merge_segment_row(const DecodeParams &p, int32_t
     __shared__ int seg[3];                       // first contributor, count (-1: empty sequence), its slot
     int32_t *scratch = msmem;
     int32_t *prefix = msmem + kPrefixScratch;
+    constexpr bool kLanes = kSplit == Split::kLanes;
     const int nvirt = p.hkv * p.row_groups;      // row groups of a sequence's kv heads
-    const int nseg = nvirt / p.lanes;            // segments per sequence
-    if (p.sel_pages != nullptr)
+    const int nseg = kLanes ? nvirt / p.lanes : nvirt;           // segments per sequence
+    if constexpr (kSplit == Split::kSelected)
         build_prefix_of([&](int row) { return nseg * selected_row_pages(p, row); }, p.batch, prefix, scratch);
     else
         build_prefix(p.seq_lens, p.batch, nseg, p.max_pages * kPageSize, prefix, scratch, nullptr);
 
     const int b = blockIdx.x / nvirt;
-    const int v = blockIdx.x - b * nvirt;
-    const int h = v / p.lanes, lane_rg = v - h * p.lanes;
+    const int virt = blockIdx.x - b * nvirt;
+    const int h = kLanes ? virt / p.lanes : virt;
     const int i = blockIdx.y;                    // row of the segment's row group
-    const int hp = v / p.row_groups, row = (v - hp * p.row_groups) * kMaxGroup + i;
+    const int hp = virt / p.row_groups, row = (virt - hp * p.row_groups) * kMaxGroup + i;
     if (row >= p.rows)
         return;
     const int lane = threadIdx.x & 31, grp = threadIdx.x >> 5;
@@ -43,14 +47,16 @@ __device__ __forceinline__ void merge_segment_row(const DecodeParams &p, int32_t
         int wf = 0, nc = -1, slot = 0;
         if (n > 0) {
             const long long T = prefix[p.batch];
-            const long long NW = effective_workers(p.num_workers / p.lanes, T);
+            const long long NW = effective_workers(kLanes ? p.num_workers / p.lanes : p.num_workers, T);
             const int seg_begin = prefix[b] + h * n;
             wf = owner_of(seg_begin, T, NW);
             nc = owner_of(static_cast<long long>(seg_begin) + n - 1, T, NW) - wf + 1;
             // wf reached this segment from an earlier one unless it starts at
             // seg_begin; every later contributor starts inside the segment, so
             // this is its first partial (slot 2w)
-            slot = partial_slot(wf, seg_begin, T, NW) + 2 * (wf * (p.lanes - 1) + lane_rg);
+            slot = partial_slot(wf, seg_begin, T, NW);
+            if constexpr (kLanes)
+                slot += 2 * (wf * (p.lanes - 1) + virt - h * p.lanes);
         }
         seg[0] = wf;
         seg[1] = nc;
@@ -77,7 +83,7 @@ __device__ __forceinline__ void merge_segment_row(const DecodeParams &p, int32_t
                 lk[u] = 0.f;
                 v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
                 if (k < nc) {
-                    const int slot = k == 0 ? slot_wf : 2 * ((wf + k) * p.lanes + lane_rg);
+                    const int slot = k == 0 ? slot_wf : 2 * (kLanes ? (wf + k) * p.lanes + virt - h * p.lanes : wf + k);
                     const float *sl = p.partials + static_cast<size_t>(slot) * kPartialFloats;
                     mk[u] = __ldcg(sl + kMaxGroup * kHeadDim + i);
                     lk[u] = __ldcg(sl + kMaxGroup * kHeadDim + kMaxGroup + i);
@@ -141,12 +147,12 @@ __device__ __forceinline__ void merge_segment_row(const DecodeParams &p, int32_t
     }
 }
 
-template <int kThreads>
+template <int kThreads, Split kSplit>
 __global__ void __launch_bounds__(kThreads, kThreads == 64 ? 16 : 1) merge_kernel(const __grid_constant__ DecodeParams p)
 {
     extern __shared__ int32_t msmem[];
     pdl_launch_dependents();                     // the next kernel may start its prologue
-    merge_segment_row<kThreads>(p, msmem);
+    merge_segment_row<kThreads, kSplit>(p, msmem);
     // The next kernel in the stream waits for this grid only, and the decode's
     // own outputs (segments one worker covered) must be complete by then: one
     // thread of the grid always waits for the decode grid, so this grid cannot
@@ -155,17 +161,17 @@ __global__ void __launch_bounds__(kThreads, kThreads == 64 ? 16 : 1) merge_kerne
         pdl_wait();
 }
 
-template <int kThreads>
+template <int kThreads, Split kSplit>
 static cudaError_t launch_merge_width(const DecodeParams &p, cudaStream_t s)
 {
     const size_t smem = (kPrefixScratch + static_cast<size_t>(p.batch) + 1) * sizeof(int32_t);
     if (smem > 40 * 1024) {
-        cudaError_t e = cudaFuncSetAttribute(merge_kernel<kThreads>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        cudaError_t e = cudaFuncSetAttribute(merge_kernel<kThreads, kSplit>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                              static_cast<int>(smem));
         if (e != cudaSuccess)
             return e;
     }
-    return launch_pdl(merge_kernel<kThreads>,
+    return launch_pdl(merge_kernel<kThreads, kSplit>,
                       dim3(p.batch * p.hkv * p.row_groups, p.rows < kMaxGroup ? p.rows : kMaxGroup),
                       dim3(kThreads), smem, s, p);
 }
@@ -174,19 +180,27 @@ static cudaError_t launch_merge_width(const DecodeParams &p, cudaStream_t s)
 // segment's page-heads are its sequence's pages; lengths are on the device,
 // so equal lengths are assumed).  Each group of 32 threads loads eight
 // contributors per round; the width gives about one round.
-cudaError_t launch_merge(const DecodeParams &p, cudaStream_t s)
+template <Split kSplit>
+static cudaError_t launch_merge_of(const DecodeParams &p, cudaStream_t s)
 {
     const long long segments = static_cast<long long>(p.batch) * p.hkv * p.row_groups;
     const long long per_segment = segments > 0 ? (p.num_workers + segments - 1) / segments : 1;
     if (per_segment > 8 * 16)
-        return launch_merge_width<1024>(p, s);
+        return launch_merge_width<1024, kSplit>(p, s);
     if (per_segment > 8 * 8)
-        return launch_merge_width<512>(p, s);
+        return launch_merge_width<512, kSplit>(p, s);
     if (per_segment > 8 * 4)
-        return launch_merge_width<256>(p, s);
+        return launch_merge_width<256, kSplit>(p, s);
     if (per_segment > 8 * 2)
-        return launch_merge_width<128>(p, s);
-    return launch_merge_width<64>(p, s);
+        return launch_merge_width<128, kSplit>(p, s);
+    return launch_merge_width<64, kSplit>(p, s);
+}
+
+cudaError_t launch_merge(const DecodeParams &p, cudaStream_t s)
+{
+    if (p.sel_pages != nullptr)
+        return launch_merge_of<Split::kSelected>(p, s);
+    return p.lanes > 1 ? launch_merge_of<Split::kLanes>(p, s) : launch_merge_of<Split::kSequences>(p, s);
 }
 
 int sm_count()
