@@ -218,13 +218,22 @@ def _ptr(t) -> int | None:
     return None if t is None else t.data_ptr()
 
 
+_raw_stream = None        # torch's query of a device's current stream, once looked up (False: it has none)
+_device = None            # ... of the current device
+
+
 def _stream(stream, dev=None) -> int | None:
-    import torch
+    global _raw_stream
     if stream is None:
         # the handle alone, without the Stream object around it (3 us a call)
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-        if raw is not None:
-            return raw(torch.cuda.current_device() if dev is None else dev)
+        if _raw_stream is None:
+            import torch
+            _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", False)
+        if _raw_stream and dev is not None:
+            return _raw_stream(dev)
+        import torch
+        if _raw_stream:
+            return _raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -350,10 +359,12 @@ class Rope:
 
 def _current_device() -> int:
     """The current CUDA device; -1, which the checks refuse, where there is none."""
-    import torch
+    global _device
     try:
-        get = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
-        return get()
+        if _device is None:
+            import torch
+            _device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+        return _device()
     except (AssertionError, RuntimeError):
         return -1
 
@@ -742,7 +753,8 @@ def fp8bkv_append(cache: FP8BlockCache, k_new, v_new, q_indptr, block_table, seq
             seq_lens.is_contiguous()):
         _tensors(dev, i32, (q_indptr, "q_indptr", (B + 1,)), (block_table, "block_table", (B, pages)),
                  (seq_lens, "seq_lens", (B,)))
-    if dev_status is not None:
+    if not (dev_status is None or (dev_status.dtype is i32 and dev_status.shape == (1,) and
+                                   dev_status.get_device() == dev)):
         _tensors(dev, i32, (dev_status, "dev_status", (1,)))
     st = load().fp8bkv_append(cache.c, k_new.data_ptr(), v_new.data_ptr(), code, T, q_indptr.data_ptr(), B,
                               block_table.data_ptr(), pages, seq_lens.data_ptr(), _ptr(dev_status), _stream(stream, dev))
@@ -770,7 +782,8 @@ def fp8bkv_dequant(cache: FP8BlockCache, block_table, lens, kv_indptr, k_out, v_
             lens.dtype is i32 and lens.shape == (B,) and lens.get_device() == dev and lens.is_contiguous()):
         _tensors(dev, i32, (kv_indptr, "kv_indptr", (B,)), (block_table, "block_table", (B, pages)),
                  (lens, "lens", (B,)))
-    if dev_status is not None:
+    if not (dev_status is None or (dev_status.dtype is i32 and dev_status.shape == (1,) and
+                                   dev_status.get_device() == dev)):
         _tensors(dev, i32, (dev_status, "dev_status", (1,)))
     st = load().fp8bkv_dequant(cache.c, block_table.data_ptr(), pages, lens.data_ptr(), kv_indptr.data_ptr(), B,
                                k_out.data_ptr(), v_out.data_ptr(), code, _ptr(dev_status), _stream(stream, dev))
@@ -796,7 +809,8 @@ def _attention_tensors(dev, B, max_pages, q, block_table, seq_lens, out, workspa
             seq_lens.dtype is i32 and seq_lens.shape == (B,) and seq_lens.get_device() == dev and
             seq_lens.is_contiguous()):
         _tensors(dev, i32, (block_table, "block_table", (B, max_pages)), (seq_lens, "seq_lens", (B,)))
-    if dev_status is not None:
+    if not (dev_status is None or (dev_status.dtype is i32 and dev_status.shape == (1,) and
+                                   dev_status.get_device() == dev)):
         _tensors(dev, i32, (dev_status, "dev_status", (1,)))
     if workspace is None:
         return q_len, heads, 0
@@ -837,7 +851,10 @@ def _page_bounds(name, kind, cache, bounds, block_table, seq_lens, from_lens, de
             seq_lens.dtype is i32 and seq_lens.shape == (B,) and seq_lens.get_device() == dev and
             seq_lens.is_contiguous()):
         _tensors(dev, i32, (block_table, "block_table", (B, pages)), (seq_lens, "seq_lens", (B,)))
-    if from_lens is not None or dev_status is not None:
+    if not ((from_lens is None or (from_lens.dtype is i32 and from_lens.shape == (B,) and
+                                   from_lens.get_device() == dev and from_lens.is_contiguous())) and
+            (dev_status is None or (dev_status.dtype is i32 and dev_status.shape == (1,) and
+                                    dev_status.get_device() == dev))):
         _tensors(dev, i32, (from_lens, "from_lens", (B,)), (dev_status, "dev_status", (1,)))
     st = getattr(load(), name)(cache.c, bounds.c, block_table.data_ptr(), pages, _ptr(from_lens), seq_lens.data_ptr(), B,
                                _ptr(dev_status), _stream(stream, dev))
