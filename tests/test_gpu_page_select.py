@@ -317,6 +317,28 @@ def test_selected_decode(kind, q_len, hkv, g, workers):
     assert not out[7].any()
 
 
+@pytest.mark.parametrize("kind", ["nvfp4", "fp8b"])
+@pytest.mark.parametrize("rows,q_len,hkv,budget", [(320, 1, 1, 128), (38, 3, 3, 100), (311, 1, 1, 40), (97, 1, 1, 130), (75, 2, 5, 17)])
+def test_selected_decode_of_more_or_fewer_lists_than_run_at_a_time(kind, rows, q_len, hkv, budget):
+    """Numbers of lists around the places of the GPU, with some rows that have few pages or none."""
+    rng = np.random.default_rng(rows)
+    cache = Cache(kind, 40, hkv, 3)
+    lens = rng.integers(budget * 16, 200 * 16 + 1, rows)
+    lens[0], lens[7], lens[-1], lens[-3] = 0, 5, 16 * budget - 9, 1
+    bt = rng.integers(0, 40, (rows, 200)).astype(np.int32)
+    pages = np.full((rows, q_len, hkv, budget), -1, np.int32)
+    for s, n in enumerate(lens):
+        for t in range(q_len):
+            P = -(-max(0, int(n) - q_len + t + 1) // 16)
+            for h in range(hkv):
+                pages[s, t, h, :min(P, budget)] = rng.permutation(P)[:budget]
+    q = queries(rows, q_len, 2 * hkv, 9)
+    status = i32([0])
+    out = run_decode(cache, q, bt, lens, pages, 0, torch.float32, status)
+    assert int(status.item()) == 0
+    assert_decode(cache, q, bt, lens.tolist(), pages, out, q_len)
+
+
 @pytest.mark.parametrize("workers", [3, 0])
 def test_selected_decode_with_a_scale_a_head(workers):
     """Factors of K and V of each head, beside the tensor scale."""
