@@ -362,7 +362,7 @@ struct ClusterCost {
 // token in 8 bits 0.00053) a page-head and 0.012 (0.015) a segment to be joined, of
 // which `worker_segments` are row groups of up to eight query rows.  80 of 256 pages in 4
 // bits: 11 and 18 us; 312 of 256: 55 and 42.  Four tokens in 8 bits: 20 sequences of 2K
-// and three tokens 36 and 46, 12 of 8K 98 and 93, six of 128K to 160K 1,059 and 477.
+// and three tokens 36 and 44, 12 of 8K 98 and 90, six of 128K to 160K 1,059 and 467.
 ClusterPlan plan_cluster_decode(int64_t segments, int64_t worker_segments, int64_t pages, bool eight_bits, bool listed,
                                 int q_len)
 {
