@@ -238,13 +238,25 @@ def _stream(stream, dev=None) -> int | None:
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
-def _dtype_code(t) -> int:
+_int_t = _bf16_t = _byte_t = None      # torch's types, once a call has looked the device up (torch is imported late)
+_codes = {}
+
+
+def _types() -> None:
+    global _int_t, _bf16_t, _byte_t
     import torch
-    if t.dtype == torch.float32:
-        return F32
-    if t.dtype == torch.bfloat16:
-        return BF16
-    raise TypeError(f"unsupported dtype {t.dtype}")
+    _int_t, _bf16_t, _byte_t = torch.int32, torch.bfloat16, torch.uint8
+    _codes.update({torch.float32: F32, torch.bfloat16: BF16})
+
+
+def _dtype_code(t) -> int:
+    code = _codes.get(t.dtype)
+    if code is None:
+        _types()
+        code = _codes.get(t.dtype)
+        if code is None:
+            raise TypeError(f"unsupported dtype {t.dtype}")
+    return code
 
 
 # --- caches -----------------------------------------------------------------
@@ -363,6 +375,7 @@ def _current_device() -> int:
     try:
         if _device is None:
             import torch
+            _types()
             _device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
         return _device()
     except (AssertionError, RuntimeError):
@@ -737,8 +750,8 @@ def fp8bkv_append(cache: FP8BlockCache, k_new, v_new, q_indptr, block_table, seq
     q_indptr[b] .. q_indptr[b+1] - 1 (int32 [B+1]), as the last tokens of its
     seq_lens[b] (int32 [B], they included) into the pages of block_table int32
     [B][pages]; a page's scale rises where they need it."""
-    import torch
-    dev, i32 = _current_device(), torch.int32
+    dev = _current_device()
+    i32 = _int_t
     _kind(cache, FP8BlockCache, dev)
     B, pages = block_table.shape
     T, code, dtype = k_new.shape[0], _dtype_code(k_new), k_new.dtype
@@ -767,11 +780,13 @@ def fp8bkv_dequant(cache: FP8BlockCache, block_table, lens, kv_indptr, k_out, v_
     """Read the first lens[b] cached rows of each sequence back into rows
     kv_indptr[b] .. of k_out and v_out [rows][Hkv][128]: fp32, bf16, or E4M3
     (uint8 or float8_e4m3fn: the workspace of the extend calls)."""
-    import torch
-    dev, i32, dtype = _current_device(), torch.int32, k_out.dtype
+    dev = _current_device()
+    i32, dtype = _int_t, k_out.dtype
     _kind(cache, FP8BlockCache, dev)
     B, pages = block_table.shape
-    code = F32 if dtype is torch.float32 else _chunk_dtype_code(k_out)
+    code = _codes.get(dtype)
+    if code is None:
+        code = _chunk_dtype_code(k_out)
     rows = (k_out.shape[0], cache.num_kv_heads, HEAD_DIM)
     if not (k_out.shape == rows and k_out.get_device() == dev and k_out.is_contiguous() and
             v_out.dtype is dtype and v_out.shape == rows and v_out.get_device() == dev and v_out.is_contiguous()):
@@ -795,14 +810,13 @@ def _attention_tensors(dev, B, max_pages, q, block_table, seq_lens, out, workspa
     """Check what the decode calls share: q bf16 [B][Hq][128] or
     [B][q_len][Hq][128], out of its shape (None: there is none); returns (q_len,
     Hq, bytes of workspace)."""
-    import torch
-    i32 = torch.int32
+    i32 = _int_t
     shape = q.shape
     q_len, heads = (1, shape[1]) if len(shape) == 3 else ((shape[1], shape[2]) if len(shape) == 4 else (-1, 0))
     if q_len < 0 or shape[0] != B or shape[-1] != HEAD_DIM:
         raise ValueError(f"q: expected [{B}][Hq][{HEAD_DIM}] or [{B}][q_len][Hq][{HEAD_DIM}], got shape {tuple(shape)}")
-    if not (q.dtype is torch.bfloat16 and q.get_device() == dev and q.is_contiguous()):
-        _tensors(dev, torch.bfloat16, (q, "q", shape))
+    if not (q.dtype is _bf16_t and q.get_device() == dev and q.is_contiguous()):
+        _tensors(dev, _bf16_t, (q, "q", shape))
     if out is not None and not (out.shape == shape and out.get_device() == dev and out.is_contiguous()):
         _tensors(dev, out.dtype, (out, "out", shape))
     if not (block_table.dtype is i32 and block_table.get_device() == dev and block_table.is_contiguous() and
@@ -815,8 +829,8 @@ def _attention_tensors(dev, B, max_pages, q, block_table, seq_lens, out, workspa
     if workspace is None:
         return q_len, heads, 0
     n = workspace.numel()
-    if not (workspace.dtype is torch.uint8 and workspace.get_device() == dev and workspace.is_contiguous()):
-        _tensors(dev, torch.uint8, (workspace, "workspace", (n,)))
+    if not (workspace.dtype is _byte_t and workspace.get_device() == dev and workspace.is_contiguous()):
+        _tensors(dev, _byte_t, (workspace, "workspace", (n,)))
     return q_len, heads, n
 
 
@@ -841,8 +855,8 @@ _SM_SCALE = 1.0 / math.sqrt(HEAD_DIM)
 
 
 def _page_bounds(name, kind, cache, bounds, block_table, seq_lens, from_lens, dev_status, stream):
-    import torch
-    dev, i32 = _current_device(), torch.int32
+    dev = _current_device()
+    i32 = _int_t
     _kind(cache, kind, dev)
     B, pages = block_table.shape
     if bounds.steps.get_device() != dev:
@@ -878,12 +892,11 @@ def fp8bkv_page_bounds(cache: FP8BlockCache, bounds: PageBounds, block_table, se
 def _page_lists(dev, pages, B, q_len, heads, flat) -> int:
     """Check lists of pages int32 [B][q_len][Hkv][budget] (flat: or
     [B][Hkv][budget]); returns the budget."""
-    import torch
     shape = pages.shape
     budget = shape[-1]
-    if not (pages.dtype is torch.int32 and pages.get_device() == dev and pages.is_contiguous() and
+    if not (pages.dtype is _int_t and pages.get_device() == dev and pages.is_contiguous() and
             (shape == (B, q_len, heads, budget) or (flat and shape == (B, heads, budget)))):
-        _tensors(dev, torch.int32, (pages, "pages", (B, heads, budget) if flat and len(shape) == 3
+        _tensors(dev, _int_t, (pages, "pages", (B, heads, budget) if flat and len(shape) == 3
                                     else (B, q_len, heads, budget)))
     return budget
 
