@@ -455,6 +455,19 @@ struct alignas(16) PickShared {
     int32_t equal, listed;               // scores that are the one number left; entries of the list
 };
 
+// Ready for the first counts (the CTA meets before they begin).
+template <int kThreads>
+__device__ __forceinline__ void clear_counts(PickShared &sh)
+{
+    for (int i = threadIdx.x; i < kBins; i += kThreads)
+        sh.count[i] = 0;
+    if (threadIdx.x == 0) {
+        sh.found[3] = 0;
+        sh.part_least = 0xffffffffu;
+        sh.part_most = 0;
+    }
+}
+
 // A query token and kv head's selection, by a cluster: this CTA has the scores of
 // pages p0 .. p0 + count - 1 in `score`.
 struct Selection {
@@ -504,24 +517,21 @@ __device__ __forceinline__ void pick_pages(const Selection &s, uint32_t from, ui
     };
     // A place range of the cluster, from each CTA's.
     auto range_of = [&](const uint32_t &least, const uint32_t &most, uint32_t &a, uint32_t &z) {
+        if (s.ranks == 1) {
+            a = least;
+            z = most;
+            return;
+        }
         const uint32_t x = of_each(&least, 0xffffffffu), y = of_each(&most, 0);
         a = __reduce_min_sync(kFullMask, x);
         z = __reduce_max_sync(kFullMask, y);
     };
     // The sum of what the CTAs before this one have.
     auto before_me = [&](const int32_t &field) {
+        if (s.ranks == 1)
+            return 0;
         const uint32_t x = of_each(&field, 0);
         return static_cast<int>(__reduce_add_sync(kFullMask, static_cast<uint32_t>(lane) < s.rank ? x : 0u));
-    };
-    auto clear = [&]() {
-        for (int i = tid; i < kBins; i += kThreads)
-            sh.count[i] = 0;
-        if (tid == 0) {
-            sh.found[3] = 0;
-            sh.part_least = 0xffffffffu;
-            sh.part_most = 0;
-        }
-        __syncthreads();
     };
     // The part where the count from the top reaches `want`, which loses what lies
     // above; scores in the part.
@@ -642,7 +652,6 @@ __device__ __forceinline__ void pick_pages(const Selection &s, uint32_t from, ui
         atomicMin(&sh.least, from);
         atomicMax(&sh.most, to);
     }
-    clear();
     meet(s.ranks);
     range_of(sh.least, sh.most, from, to);
     bool done = want <= 0;
@@ -670,7 +679,8 @@ __device__ __forceinline__ void pick_pages(const Selection &s, uint32_t from, ui
         const uint32_t span = to - from;
         const int shift = span < kBins ? 0 : 21 - __clz(span);   // at most 2,048 parts of 2^shift places
         meet(s.ranks);                                           // (the counts and the range have been read)
-        clear();
+        clear_counts<kThreads>(sh);
+        __syncthreads();
         for_scores([&](int, float x) {
             const uint32_t k = order_of(x);
             if (k >= from && k <= to)
@@ -721,13 +731,15 @@ __device__ __forceinline__ void pick_pages(const Selection &s, uint32_t from, ui
     };
     const int words = (s.count + 31) / 32;
     int n0 = 0, total;
-    for (int w = tid; w < words; w += kThreads)
-        n0 += __popc(word(w));
-    cta_sum_before<kThreads>(n0, sh.scratch, total);
-    if (tid == 0)
-        sh.listed = total;
-    meet(s.ranks);
-    n0 = before_me(sh.listed);
+    if (s.ranks > 1) {
+        for (int w = tid; w < words; w += kThreads)
+            n0 += __popc(word(w));
+        cta_sum_before<kThreads>(n0, sh.scratch, total);
+        if (tid == 0)
+            sh.listed = total;
+        meet(s.ranks);
+        n0 = before_me(sh.listed);
+    }
     constexpr int kWarps = kThreads / 32;
     for (int w0 = 0; w0 < words;) {
         const int each = min((words - w0 + kWarps - 1) / kWarps, 32);        // words of a warp
@@ -743,7 +755,8 @@ __device__ __forceinline__ void pick_pages(const Selection &s, uint32_t from, ui
         n0 += total;
         w0 += kWarps * each;
     }
-    meet(s.ranks);                                               // (nobody leaves while it is read)
+    if (s.ranks > 1)
+        meet(s.ranks);                                           // (nobody leaves while it is read)
 }
 
 // A cluster a (query token, kv head): its CTAs share out the tiles, work their scores
@@ -783,6 +796,7 @@ __global__ void __launch_bounds__(kThreads, kThreads == 512 ? 1 : 2) page_select
     const int p0 = begin * kTile, count = min(tiles * kTile, pages - p0);
     for (int i = tid; i < (tiles * kTile + 31) / 32; i += kThreads)
         taken[i] = 0;
+    clear_counts<kThreads>(sh);
     if (tid == 0) {
         sh.least = 0xffffffffu;
         sh.most = 0;
