@@ -894,11 +894,11 @@ constexpr int kLongPages = 6144;
 
 // CTAs of 512 threads, one an SM, or of 256, two an SM, and how many a cluster.  A
 // meeting of the cluster costs a microsecond, which r CTAs repay from some 512 r^2
-// pages on (8 heads of one sequence: 2,048 pages 13.5 us with one, 12.5 with two, 13.5
-// with four; 4,096 pages 16.4 with two, 15.2 with three, 15.8 with four; 8,192 pages
-// 24.0, 20.2, 19.7), as long as all clusters run at a time (48 units of 8,192 pages: 28
-// us by clusters of two, 47 by 48 of three, whose last ones wait; 96 of 2,000: 16 and
-// 28).  Where there are more units than SMs, two CTAs at a time on an SM work beside
+// pages on (8 heads of one sequence: 2,048 pages 12.6 us with one, 12.1 with two, 12.9
+// with four; 4,096 pages 16.0 with two, 14.8 with three, 15.2 with four; 8,192 pages
+// 23.7, 20.0, 19.3), as long as all clusters run at a time (48 units of 8,192 pages: 28
+// us by clusters of two, 45 by 48 of three, whose last ones wait; 96 of 2,000: 15 and
+// 27).  Where there are more units than SMs, two CTAs at a time on an SM work beside
 // each other (560 units of 2,000 pages: 73 us with 512 threads, 62 with 256; 320 of
 // 4,000: 84.2 and 83.5), but of long sequences a wave that is not full costs more than
 // that gains (160 units of 8,125 pages: 102 and 120; 560: 232 and 270).
@@ -933,8 +933,8 @@ static cudaError_t launch_units(const SelectParams &p, long long unit0, long lon
 }
 
 // The units past the last full wave go by a launch of their own where they are few
-// enough for clusters: 160 units of 8,125 pages in 80 us instead of 97, 192 in 84 instead
-// of 99, 320 of 4,000 in 76 instead of 87, of 2,048 in 47.5 instead of 49.3.
+// enough for clusters: 160 units of 8,125 pages in 78 us instead of 96, 192 in 82 instead
+// of 97, 320 of 4,000 in 76 instead of 87, of 2,048 in 47.5 instead of 49.3.
 cudaError_t launch_select_pages(const SelectParams &p, cudaStream_t s)
 {
     const long long units = static_cast<long long>(p.batch) * p.q_len * p.hkv, sms = max(1, sm_count());
