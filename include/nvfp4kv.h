@@ -724,6 +724,7 @@ nvfp4kv_status fp8bkv_page_bounds(const fp8bkv_cache *cache, const nvfp4kv_bound
  *   score(page) = fl32(step * max_h sum_c max(w_hc * hi_c, w_hc * lo_c)),
  * the most that a key within the bounds can reach with one of the heads; the
  * sum is a whole number below 2^24, so the score depends on no order of sums.
+ * A score past fp32's range counts as its largest finite number of that sign.
  * Selected are the first `first_pages` and the last `last_pages` of the P and the
  * others of the largest scores, the lower page where two are equal, `budget` in
  * all, or all P where they are no more than that.

@@ -494,7 +494,7 @@ __device__ __forceinline__ void meet(uint32_t ranks)
 // last wanted one lies; what lies above is taken, what lies in that part is ranked pair
 // by pair.  `from` and `to` are the ends of the thread's scores in the order of floats,
 // then of what is still open.  (The part of a score, f below cut to a whole number, never falls as the
-// score grows, whatever its subtraction and product round.)  Where more than kTies
+// score grows, whatever its difference and product round.)  Where more than kTies
 // scores share the part, its places in the order of floats are cut into 2,048 parts,
 // again until they fit or are one number, of which the lowest pages are taken.  Every
 // CTA adds up all CTAs' counts and comes to the same border.
@@ -656,16 +656,22 @@ __device__ __forceinline__ void pick_pages(const Selection &s, uint32_t from, ui
     range_of(sh.least, sh.most, from, to);
     bool done = want <= 0;
     if (!done && from < to) {
-        const float least = float_at(from), by = kBins / (float_at(to) - least);   // (0 where the difference passes fp32)
+        // Halves, whose difference is finite whatever the scores, in the same arithmetic for
+        // both passes: a score that is counted in one part and found in another would be
+        // missed, or be one more than the ties that there is room for.  (Scores so close
+        // that `by` is infinite all come to the last part: 0 times it is NaN, which the
+        // clamp turns into it and no comparison with a border holds for.)
+        const float half = 0.5f * float_at(from), by = kBins / __fmaf_rn(0.5f, float_at(to), -half);
+        auto place_of = [&](float x) { return __fmul_rn(__fmaf_rn(0.5f, x, -half), by); };
         for_scores([&](int, float x) {
-            const int part = static_cast<int>(fminf((x - least) * by, kBins - 1.f));
+            const int part = static_cast<int>(fminf(place_of(x), kBins - 1.f));
             atomicAdd(&sh.count[part & (kBins - 1)], 1);
         });
         find_border();
         const float below = border > 0 ? static_cast<float>(border) : -INFINITY;
         const float above = border < kBins - 1 ? static_cast<float>(border + 1) : NAN;
         for_scores([&](int i, float x) {
-            const float f = (x - least) * by;
+            const float f = place_of(x);
             if (f >= above)
                 take(i);
             else if (!(f < below))

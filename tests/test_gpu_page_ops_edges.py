@@ -1,0 +1,91 @@
+"""The block-scaled cache, page bounds, selection and decode over selected pages at
+the edges of what the header allows."""
+import numpy as np
+import pytest
+import torch
+
+import nvfp4_quantized_paged_nvfp4kv_gb300 as nv
+from gpu_util import DEV
+from test_gpu_page_select import i32, make_bounds, picks, queries
+
+pytestmark = pytest.mark.gpu
+
+LARGEST = np.finfo(np.float32).max
+
+
+def held_select(q, ints, steps, n, budget, first, last):
+    """page_ops_ref.select with scores past fp32's range held to its largest numbers."""
+    P = -(-n // 16)
+    top = np.abs(q).max()
+    w = np.rint(q * (np.float32(127) / top)).astype(np.int64)
+    i = ints[:P].astype(np.int64)
+    best = np.maximum(w[:, None] * i[None, :, 0], w[:, None] * i[None, :, 1]).sum(-1).max(0)
+    with np.errstate(over="ignore"):
+        score = np.clip(best.astype(np.float32) * steps[:P], -LARGEST, LARGEST).astype(np.float64)
+    score[:first], score[P - last:] = np.inf, np.inf
+    return sorted(np.lexsort((np.arange(P), -score))[:budget].tolist())
+
+
+def both_signs(pages, seed):
+    """Bounds half of whose pages have only negative products with queries that are not negative."""
+    b, g = make_bounds(pages, 2, seed), torch.Generator(device=DEV).manual_seed(seed)
+    low = torch.randint(-120, -20, (pages, 2, 128), generator=g, device=DEV, dtype=torch.int32).to(torch.int8)
+    away = torch.rand((pages, 2), generator=g, device=DEV) < 0.5
+    b.bounds[:, :, 0] = torch.where(away[..., None], low, b.bounds[:, :, 0])
+    b.bounds[:, :, 1] = torch.where(away[..., None], low, b.bounds[:, :, 1])
+    return b, queries(1, 1, 8, seed).abs()
+
+
+@pytest.mark.parametrize("steps", [1e31, 1e32, 3e32, 1e33, 1e38, "far", "mixed"])
+@pytest.mark.parametrize("pages", [900, 9000])
+def test_scores_whose_difference_passes_fp32(steps, pages):
+    """Scores of both signs so large that their range, or they themselves, pass fp32,
+    with the border among the highest, the lowest and between."""
+    b, q = both_signs(pages, pages)
+    g = torch.Generator(device=DEV).manual_seed(5)
+    if steps == "far":                                   # two pages span the range, the others are usual
+        b.steps[17], b.steps[pages - 5] = 3e38, 3e38
+        b.bounds[17, :, :], b.bounds[pages - 5, :, :] = 100, -100
+    elif steps == "mixed":
+        b.steps[:] = 10.0 ** (76 * torch.rand(b.steps.shape, generator=g, device=DEV) - 38)
+    else:
+        b.steps[:] = steps * (0.5 + torch.rand(b.steps.shape, generator=g, device=DEV))
+    bt = np.random.default_rng(1).permutation(pages).astype(np.int32)[None]
+    n = pages * 16 - 3
+    ints, s = b.bounds.cpu().numpy()[bt[0]], b.steps.cpu().numpy()[bt[0]]
+    qn = q.float().cpu().numpy().reshape(2, -1, 128)
+    for budget, first, last in ((1, 0, 0), (50, 1, 2), (pages // 2 - 7, 0, 0), (pages // 2 + 9, 3, 0), (pages - 1, 0, 0)):
+        got = picks(b, q, bt, [n], budget, first, last, 1)
+        for h in range(2):
+            assert got[0, 0, h].tolist() == held_select(qn[h], ints[:, h], s[:, h], n, budget, first, last), (budget, h)
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+def test_steps_that_are_not_finite(bad):
+    """No bounds of finite keys have them; the lists are of pages that are there, each once."""
+    pages = 5000
+    b, q = both_signs(pages, 3)
+    b.steps[torch.rand(b.steps.shape, generator=torch.Generator(device=DEV).manual_seed(2), device=DEV) < 0.7] = bad
+    bt = np.arange(pages, dtype=np.int32)[None]
+    for budget in (1, 40, 2600, pages - 1):
+        got = picks(b, q, bt, [pages * 16], budget, min(budget, 2), 0, 1)
+        for h in range(2):
+            x = got[0, 0, h]
+            assert (np.diff(x) > 0).all() and x[0] == 0 and x[-1] < pages
+
+
+@pytest.mark.parametrize("size", [1e-45, 1e-44, 1e-40, 1e-37])
+def test_scores_so_small_that_their_difference_is_subnormal(size):
+    pages = 3000
+    b, q = make_bounds(pages, 1, 4), queries(1, 1, 4, 1)
+    b.bounds[:] = 0
+    b.bounds[:, :, :, 0] = torch.arange(pages, device=DEV)[:, None, None].remainder(3).sub(1).to(torch.int8)
+    q[:] = 0
+    q[..., 0] = 2.0
+    b.steps[:] = size
+    ints, s = b.bounds.cpu().numpy(), b.steps.cpu().numpy()
+    bt = np.arange(pages, dtype=np.int32)[None]
+    for budget in (1, 900, 1000, 1001, 2500):
+        got = picks(b, q, bt, [pages * 16], budget, 0, 0, 1)
+        assert got[0, 0, 0].tolist() == held_select(q.float().cpu().numpy().reshape(-1, 128), ints[:, 0], s[:, 0], pages * 16,
+                                                    budget, 0, 0)
