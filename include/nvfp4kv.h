@@ -644,8 +644,10 @@ nvfp4kv_status fp8kv_append_paged_decode(const fp8kv_cache *cache, const void *k
  * A sequence whose range is outside [0, num_tokens], or whose length is less
  * than C or more than max_pages_per_seq * 16, is not written and sets
  * NVFP4KV_DEV_BAD_LEN; a page id outside [0, num_pages) is skipped and sets
- * NVFP4KV_DEV_BAD_PAGE.  q_indptr must not fall from one sequence to the next.
- * batch at most NVFP4KV_MAX_BATCH.  Non-finite inputs give unspecified codes. */
+ * NVFP4KV_DEV_BAD_PAGE.  q_indptr must not fall from one sequence to the next
+ * (the rows behind one that does may be left out).  A call of no rows
+ * (num_tokens 0) reads and sets nothing.  batch at most NVFP4KV_MAX_BATCH.
+ * Non-finite inputs give unspecified codes. */
 nvfp4kv_status fp8bkv_append(const fp8bkv_cache *cache, const void *k_new, const void *v_new, nvfp4kv_dtype in_dtype,
                              int32_t num_tokens, const int32_t *q_indptr, int32_t batch, const int32_t *block_table,
                              int32_t max_pages_per_seq, const int32_t *seq_lens, int32_t *dev_status,

@@ -101,6 +101,12 @@ __device__ __forceinline__ uint2 recode(uint2 c, float by)
     return codes_of(x, by);
 }
 
+// Whether rows c0 .. c1 - 1 can be the last ones of a sequence of len tokens.
+__device__ __forceinline__ bool good_range(const BlockAppendParams &p, int c0, int c1, int len)
+{
+    return c0 >= 0 && c1 >= c0 && c1 <= p.num_tokens && len >= c1 - c0 && len <= p.max_pages * kPageSize;
+}
+
 // Last sequence whose first unit is at or before u, by the whole warp (32
 // probes a round); -1 where there is none.  Sequence b's units begin at
 // floor(q_indptr[b] / 16) + 2b: its pages are at most floor(C / 16) + 2.
@@ -138,16 +144,20 @@ __global__ void __launch_bounds__(256, kBf16 ? 3 : 2) block_append_kernel(const 
     const long long u = id / (2 * p.hkv);
     const int hv = static_cast<int>(id - u * 2 * p.hkv), h = hv >> 1;
     const bool is_v = hv & 1;
+    // The ranges are reported on by the first warps, a lane a sequence (there are at
+    // least 4 warps a sequence): one that points outside the rows may own no unit here.
+    if (id * 32 < p.batch) {
+        const int mine = static_cast<int>(id) * 32 + lane;
+        if (mine < p.batch && !good_range(p, __ldg(p.q_indptr + mine), __ldg(p.q_indptr + mine + 1), __ldg(p.seq_lens + mine)))
+            report(p.dev_status, NVFP4KV_DEV_BAD_LEN);
+    }
     const int b = find_unit(p.q_indptr, p.batch, u, lane);
     if (b < 0)
         return;
     const int c0 = __ldg(p.q_indptr + b), c1 = __ldg(p.q_indptr + b + 1), len = __ldg(p.seq_lens + b);
     const long long i = u - ((static_cast<long long>(c0) >> 4) + 2 * b);     // page of the sequence's new ones
-    if (c0 < 0 || c1 < c0 || c1 > p.num_tokens || len < c1 - c0 || len > p.max_pages * kPageSize) {
-        if (i == 0 && hv == 0 && lane == 0)
-            report(p.dev_status, NVFP4KV_DEV_BAD_LEN);
+    if (!good_range(p, c0, c1, len))
         return;
-    }
     const int pos0 = len - (c1 - c0);
     const long long page = pos0 / kPageSize + i;
     const int begin = static_cast<int>(max(static_cast<long long>(pos0), page * kPageSize) - page * kPageSize);

@@ -89,3 +89,43 @@ def test_scores_so_small_that_their_difference_is_subnormal(size):
         got = picks(b, q, bt, [pages * 16], budget, 0, 0, 1)
         assert got[0, 0, 0].tolist() == held_select(q.float().cpu().numpy().reshape(-1, 128), ints[:, 0], s[:, 0], pages * 16,
                                                     budget, 0, 0)
+
+
+@pytest.mark.parametrize("batch", [1, 40, 300])
+@pytest.mark.parametrize("hkv", [1, 8])
+def test_append_says_which_ranges_it_refuses(batch, hkv):
+    """A range outside the rows, or a length that does not go with it, sets the status
+    wherever in the call it stands, and nothing of that sequence is written."""
+    pages = batch + 1
+    bt = i32(np.arange(batch)[:, None])
+    x = torch.ones((2 * batch, hkv, 128), device=DEV)
+    good = 2 * np.arange(batch + 1)
+    for at in sorted({0, batch // 2, batch - 1}):
+        for what, value in (("first", -5), ("first", -2 ** 31), ("last", 2 * batch + 1), ("last", 2 ** 31 - 1), ("length", 1),
+                            ("length", 17), ("length", -3), ("length", 2 ** 31 - 1), ("both", 2 ** 31 - 1)):
+            ptr, lens = good.copy(), np.full(batch, 9)
+            if what == "length":
+                lens[at] = value
+            elif what == "first":                        # (those before it fall, or are below 0 too)
+                ptr[:at + 1] = value
+            elif what == "last":
+                ptr[at + 1:] = value
+            else:
+                ptr[at:] = value
+            cache = nv.FP8BlockCache(torch.full((pages, hkv, nv.FP8_BLOCK_RECORD_BYTES), 7, dtype=torch.uint8, device=DEV))
+            status = i32([0])
+            nv.fp8bkv_append(cache, x, x, i32(ptr), bt, i32(lens), dev_status=status)
+            assert int(status.item()) == nv.DEV_BAD_LEN, (at, what, value)
+            written = (cache.pool != 7).flatten(1).any(1).cpu().numpy()
+            fine = [0 <= ptr[b] < ptr[b + 1] <= 2 * batch and ptr[b + 1] - ptr[b] <= lens[b] <= 16 for b in range(batch)]
+            assert written.tolist() == fine + [False], (at, what, value)
+
+
+def test_append_of_ranges_outside_the_rows_alone():
+    x = torch.ones((101, 2, 128), device=DEV)
+    for ptr in ([-5, 3], [0, 102], [50, 40], [2 ** 31 - 1, 2 ** 31 - 1], [-2 ** 31, 5], [101, 102], [102, 102], [-1, -1]):
+        cache = nv.FP8BlockCache(torch.full((4, 2, nv.FP8_BLOCK_RECORD_BYTES), 7, dtype=torch.uint8, device=DEV))
+        status = i32([0])
+        nv.fp8bkv_append(cache, x, x, i32(ptr), i32([[0, 1, 2]]), i32([20]), dev_status=status)
+        assert int(status.item()) == nv.DEV_BAD_LEN, ptr
+        assert (cache.pool == 7).all(), ptr
