@@ -12,8 +12,7 @@ template <bool kMulti>
 static cudaError_t launch_decode(const DecodeParams &p, cudaStream_t s)
 {
     const size_t smem = decode_smem_bytes<Fp8BlockFormat>(p.batch);
-    cudaError_t e = cudaFuncSetAttribute(decode_kernel<Fp8BlockFormat, kMulti>,
-                                         cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    const cudaError_t e = allow_shared<decode_kernel<Fp8BlockFormat, kMulti>>();
     if (e != cudaSuccess)
         return e;
     const int grid = (p.num_workers + kDecodeWarps - 1) / kDecodeWarps;

@@ -7,8 +7,7 @@ template <class Fmt, bool kMulti>
 static cudaError_t launch_decode(const DecodeParams &p, cudaStream_t s)
 {
     const size_t smem = decode_smem_bytes<Fmt>(p.batch);
-    cudaError_t e = cudaFuncSetAttribute(decode_kernel<Fmt, kMulti>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(smem));
+    const cudaError_t e = allow_shared<decode_kernel<Fmt, kMulti>>();
     if (e != cudaSuccess)
         return e;
     const int grid = (p.num_workers + kDecodeWarps - 1) / kDecodeWarps;

@@ -9,8 +9,7 @@ template <class Fmt>
 static cudaError_t launch_decode(const DecodeParams &p, cudaStream_t s)
 {
     const size_t smem = decode_smem_bytes<Fmt, true>(p.batch);
-    cudaError_t e = cudaFuncSetAttribute(decode_kernel<Fmt, false, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(smem));
+    const cudaError_t e = allow_shared<decode_kernel<Fmt, false, true>>();
     if (e != cudaSuccess)
         return e;
     const int grid = (p.num_workers + kDecodeWarps - 1) / kDecodeWarps;

@@ -369,8 +369,9 @@ cudaError_t launch_pdl(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t s
 }
 
 // Allows a kernel the most dynamic shared memory that it can have beside
-// kStatic bytes of its own, once a device (the runtime call costs a launch a third
-// of a microsecond).
+// kStatic bytes of its own, once a device: what is allowed is one for all threads, so a
+// call's own need, set at each launch, might be taken back by another's before it starts
+// (and the runtime call costs a launch a third of a microsecond).
 template <auto kKernel, int kStatic = 0>
 cudaError_t allow_shared()
 {

@@ -268,8 +268,9 @@ cudaError_t launch_tables(K kernel, K count, StepTablesParams p, long long items
     p.count_here = grid == 1 || p.num_free_in != p.num_free_out;
     if (smem > 48 * 1024)
         for (K k : {kernel, count}) {
+            // (what the largest batch takes, for other threads' launches too)
             const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                       static_cast<int>(smem));
+                                                       2 * (kMaxBatch + 1) * static_cast<int>(sizeof(int32_t)));
             if (e != cudaSuccess)
                 return e;
         }

@@ -1,5 +1,7 @@
 """The block-scaled cache, page bounds, selection and decode over selected pages at
 the edges of what the header allows."""
+import threading
+
 import numpy as np
 import pytest
 import torch
@@ -129,3 +131,61 @@ def test_append_of_ranges_outside_the_rows_alone():
         nv.fp8bkv_append(cache, x, x, i32(ptr), i32([[0, 1, 2]]), i32([20]), dev_status=status)
         assert int(status.item()) == nv.DEV_BAD_LEN, ptr
         assert (cache.pool == 7).all(), ptr
+
+
+def decodes_of(kind, batch, q_len):
+    """A decode by named workers of `batch` sequences of a page each: a function that makes the call."""
+    four = kind.startswith("nvfp4")
+    cache = {"nvfp4": nv.NVFP4Cache, "nvfp4_selected": nv.NVFP4Cache, "fp8": nv.FP8Cache}.get(kind, nv.FP8BlockCache).allocate(
+        1, 1, device=DEV)
+    cache.pool.zero_()
+    shape = (batch, 2, 128) if q_len == 1 else (batch, q_len, 2, 128)
+    q, out, ws = torch.zeros(shape, dtype=torch.bfloat16, device=DEV), torch.ones(shape, device=DEV), nv.new_workspace(64, device=DEV)
+    table, lens, lists = i32(np.zeros((batch, 1))), i32(np.full(batch, q_len)), i32(np.zeros((batch, q_len, 1, 1)))
+    s = torch.cuda.Stream()
+    call = {"nvfp4": nv.nvfp4kv_paged_decode if q_len == 1 else nv.nvfp4kv_paged_decode_multi, "fp8": nv.fp8kv_paged_decode,
+            "fp8b": nv.fp8bkv_paged_decode, "nvfp4_selected": nv.nvfp4kv_selected_decode,
+            "fp8b_selected": nv.fp8bkv_selected_decode}[kind]
+    args = (cache, q, table, lens, lists, out, ws) if kind.endswith("selected") else (cache, q, table, lens, out, ws)
+    return out, lambda: call(*args, num_workers=64, stream=s)
+
+
+@pytest.mark.parametrize("kind,q_len", [("fp8b", 1), ("fp8b", 2), ("nvfp4_selected", 1), ("fp8b_selected", 1), ("nvfp4", 1),
+                                        ("nvfp4", 2), ("fp8", 1)])
+def test_decodes_of_different_batches_from_two_threads(kind, q_len):
+    """What a launch is allowed on a device is one for all threads: a call of few
+    sequences leaves a call of many what it needs."""
+    calls = [decodes_of(kind, batch, q_len) for batch in (1, 8192 // q_len)]
+    from_threads([call for _, call in calls])
+    assert all(not out.any() for out, _ in calls)
+
+
+def from_threads(calls, times=1500):
+    """Each of the calls from two threads at once, that often; none may fail."""
+    torch.cuda.synchronize()
+    failed = []
+
+    def loop(call):
+        try:
+            for _ in range(times):
+                call()
+        except Exception as e:
+            failed.append(e)
+
+    threads = [threading.Thread(target=loop, args=(call,)) for call in calls for _ in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed, failed
+
+
+def test_step_tables_of_different_batches_from_two_threads():
+    def call_of(batch):
+        zeros, s = i32(np.zeros(batch)), torch.cuda.Stream()
+        table, free, num, after = i32(np.full((batch, 1), -1)), i32([0]), i32([1]), i32([0])
+        seq, ptr, slots = i32(np.zeros(batch)), i32(np.zeros(batch + 1)), i32([5])
+        return lambda: nv.nvfp4kv_plan_step(zeros, zeros, table, 1, free, num, after, seq, ptr, slots, stream=s)
+
+    from_threads([call_of(6200), call_of(8192)])
