@@ -877,13 +877,15 @@ cudaError_t launch_page_bounds_fp8_block(const BoundsParams &p, cudaStream_t s)
     return launch_bounds<Fp8BlockKeys>(p, s);
 }
 
+// PickShared in a CTA's shared memory, in front of the dynamic part's 128-byte places.
+constexpr int kPickStatic = (sizeof(PickShared) + 127) / 128 * 128;
 // Dynamic shared memory that a launch may take, beside PickShared.
 constexpr size_t kMostShared = 227 * 1024 - sizeof(PickShared) - 1024;
 
 template <int kThreads>
 static cudaError_t allow_select()
 {
-    return allow_shared<page_select_kernel<kThreads>, (sizeof(PickShared) + 127) / 128 * 128>();
+    return allow_shared<page_select_kernel<kThreads>, kPickStatic>();
 }
 
 template <int kThreads>
@@ -896,7 +898,19 @@ static cudaError_t launch_select(const SelectParams &p, long long units, size_t 
                           smem, s, p);
 }
 
-constexpr int kLongPages = 6144;
+// Dynamic shared memory of a CTA with so many tiles.
+static size_t select_bytes(int threads, int tiles)
+{
+    const size_t pages = static_cast<size_t>(tiles) * kTile;
+    return threads / 32 * kStages * kStageBytes + kQueryWords * sizeof(uint4) + pages * 4 + (pages + 31) / 32 * 4;
+}
+
+// Whether two CTAs of 256 threads with all pages of a unit fit on an SM (1 KB of each is
+// the system's): up to 5,136 pages.
+static bool two_on_an_sm(int max_pages)
+{
+    return 2 * (select_bytes(256, (max_pages + kTile - 1) / kTile) + kPickStatic + 1024) <= 228 * 1024;
+}
 
 // CTAs of 512 threads, one an SM, or of 256, two an SM, and how many a cluster.  A
 // meeting of the cluster costs a microsecond, which r CTAs repay from some 512 r^2
@@ -906,12 +920,13 @@ constexpr int kLongPages = 6144;
 // us by clusters of two, 45 by 48 of three, whose last ones wait; 96 of 2,000: 15 and
 // 27).  Where there are more units than SMs, two CTAs at a time on an SM work beside
 // each other (560 units of 2,000 pages: 73 us with 512 threads, 62 with 256; 320 of
-// 4,000: 84.2 and 83.5), but of long sequences a wave that is not full costs more than
-// that gains (160 units of 8,125 pages: 102 and 120; 560: 232 and 270).
+// 4,000: 84.2 and 83.5), as long as two fit: one alone has half the warps and loads in
+// flight (160 units of 5,152 pages over the bounds of 24,000: 43 us with 512 threads, 59
+// with 256; 560 of 8,125 over 84,000: 167 and 237).
 static cudaError_t launch_units(const SelectParams &p, long long unit0, long long units, cudaStream_t s)
 {
     const int tiles = (p.max_pages + kTile - 1) / kTile;
-    const int threads = units > sm_count() && p.max_pages <= kLongPages ? 256 : 512;
+    const int threads = units > sm_count() && two_on_an_sm(p.max_pages) ? 256 : 512;
     int ranks = 1;
     if (units * 2 <= sm_count()) {
         while (ranks < 8 && (2 * ranks + 1) * (2 * ranks + 1) * 128 <= p.max_pages)
@@ -926,8 +941,7 @@ static cudaError_t launch_units(const SelectParams &p, long long unit0, long lon
     q.unit0 = unit0;
     auto bytes = [&]() {
         q.chunk_tiles = (tiles + ranks - 1) / ranks;
-        return threads / 32 * kStages * kStageBytes + kQueryWords * sizeof(uint4) +
-               static_cast<size_t>(q.chunk_tiles) * kTile * 4 + (static_cast<size_t>(q.chunk_tiles) * kTile + 31) / 32 * 4;
+        return select_bytes(threads, q.chunk_tiles);
     };
     static_assert(512 / 32 * kStages * kStageBytes + kQueryWords * sizeof(uint4) +
                           NVFP4KV_MAX_SELECT_PAGES / 8 / 8 * 33 + 1024 <= kMostShared, "the largest call fits eight CTAs");
@@ -944,7 +958,7 @@ static cudaError_t launch_units(const SelectParams &p, long long unit0, long lon
 cudaError_t launch_select_pages(const SelectParams &p, cudaStream_t s)
 {
     const long long units = static_cast<long long>(p.batch) * p.q_len * p.hkv, sms = max(1, sm_count());
-    const long long wave = units > sms && p.max_pages <= kLongPages ? 2 * sms : sms;
+    const long long wave = units > sms && two_on_an_sm(p.max_pages) ? 2 * sms : sms;
     const long long full = p.max_pages >= 2048 ? units / wave * wave : 0;
     const long long rest = units - full;
     if (full == 0 || rest * 2 > sms || rest == 0)

@@ -8,7 +8,7 @@ import torch
 
 import nvfp4_quantized_paged_nvfp4kv_gb300 as nv
 from gpu_util import DEV
-from test_gpu_page_select import i32, make_bounds, picks, queries
+from test_gpu_page_select import assert_picks, i32, make_bounds, picks, queries
 
 pytestmark = pytest.mark.gpu
 
@@ -189,3 +189,13 @@ def test_step_tables_of_different_batches_from_two_threads():
         return lambda: nv.nvfp4kv_plan_step(zeros, zeros, table, 1, free, num, after, seq, ptr, slots, stream=s)
 
     from_threads([call_of(6200), call_of(8192)])
+
+
+@pytest.mark.parametrize("rows,q_len,hkv,pages", [(160, 1, 1, 5120), (306, 1, 1, 5136), (160, 1, 1, 5137), (39, 2, 4, 5200),
+                                                  (310, 1, 1, 5153), (153, 1, 1, 6144)])
+def test_select_around_the_pages_of_which_two_units_share_an_sm(rows, q_len, hkv, pages):
+    rng = np.random.default_rng(pages)
+    lens = rng.integers(pages * 12, pages * 16 + 1, rows)
+    lens[0], lens[1], lens[-2], lens[-1] = pages * 16, 0, 37, pages * 16 - 15
+    bt = rng.integers(0, 300, (rows, pages)).astype(np.int32)
+    assert_picks(make_bounds(300, hkv, 13), queries(rows, q_len, 2 * hkv, 6), bt, lens.tolist(), 40, 2, 3, q_len)
