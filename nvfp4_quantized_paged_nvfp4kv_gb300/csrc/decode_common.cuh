@@ -398,7 +398,7 @@ __device__ __forceinline__ void load_rows(const uint16_t *qsrc, float qsc, int t
     const uint4 *qrow = reinterpret_cast<const uint4 *>(qsrc + 32 * tig);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint4 r = __ldg(qrow + i);
+        const uint4 r = qrow[i];
         const uint32_t ww[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
@@ -421,7 +421,7 @@ __device__ __forceinline__ void load_rows_apart(const uint16_t *qsrc, bool has_r
     float top = 0.f;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const uint4 r = has_row ? __ldg(reinterpret_cast<const uint4 *>(qsrc + 32 * tig) + i) : make_uint4(0, 0, 0, 0);
+        const uint4 r = has_row ? reinterpret_cast<const uint4 *>(qsrc + 32 * tig)[i] : make_uint4(0, 0, 0, 0);
         w[4 * i] = r.x;
         w[4 * i + 1] = r.y;
         w[4 * i + 2] = r.z;

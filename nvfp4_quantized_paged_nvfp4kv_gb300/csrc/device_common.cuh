@@ -323,6 +323,10 @@ __device__ __forceinline__ void fence_async_shared()
 
 // Programmatic dependent launch: wait for the preceding kernel in the stream
 // (no-op when the launch did not allow overlap) / let the next one start.
+// (What that kernel writes -- queries, rows, records, bounds, lists -- is read behind the
+// wait by plain loads, __ldcg or asynchronous copies, not by __ldg: the read-only path is
+// for data that nobody writes while the kernel runs, and this one may be resident
+// already.  Lengths and tables, see decode_kernel, are over before.)
 __device__ __forceinline__ void pdl_wait()
 {
     asm volatile("griddepcontrol.wait;" ::: "memory");

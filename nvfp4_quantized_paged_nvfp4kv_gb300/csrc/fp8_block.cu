@@ -41,7 +41,7 @@ struct Eight {
                                : reinterpret_cast<const uint4 *>(static_cast<const float *>(src) + elem);
 #pragma unroll
         for (int i = 0; i < (kBf16 ? 1 : 2); ++i)
-            v[i] = __ldg(p + i);
+            v[i] = p[i];
     }
 
     __device__ __forceinline__ void zero()
@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(kReadThreads, 5) block_read_kernel(const __gri
             phys = 0;
         }
         const uint8_t *rec = p.pool + (static_cast<size_t>(phys) * p.hkv + h) * kFp8BlockRecord;
-        const float s = __ldg(reinterpret_cast<const float *>(rec + kFp8Record) + is_v);
+        const float s = reinterpret_cast<const float *>(rec + kFp8Record)[is_v];
         const int valid = len - page * kPageSize;
         void *out = is_v ? p.v_out : p.k_out;
         // a row's place: channels 8c .. of token t at row t
@@ -345,7 +345,7 @@ __global__ void __launch_bounds__(kReadThreads, 5) block_read_kernel(const __gri
             const uint2 *src = reinterpret_cast<const uint2 *>(rec) + 16 * half + 2 * (((c >> 1) + half) & 7) + (c & 1);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
-                x[i] = __ldg(src + 32 * i);
+                x[i] = src[32 * i];
 #pragma unroll
             for (int i = 0; i < 8; ++i)
                 if (2 * i + half < valid)
@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(kReadThreads, 5) block_read_kernel(const __gri
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const int pr = 2 * i + half, f = (pr & 1) + 4 * ((pr >> 1) & 1);
-                x[i] = __ldg(reinterpret_cast<const uint4 *>(rec + 2048) + 16 * pr + ((c + f) & 15));
+                x[i] = reinterpret_cast<const uint4 *>(rec + 2048)[16 * pr + ((c + f) & 15)];
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i)

@@ -49,8 +49,8 @@ struct Nvfp4Keys {
     {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            d[i] = __ldg(reinterpret_cast<const uint32_t *>(rec) + 32 * i + lane);
-            s[i] = __ldg(rec + 2048 + 16 * i + 8 * (lane >> 4) + ((lane & 15) >> 1));
+            d[i] = reinterpret_cast<const uint32_t *>(rec)[32 * i + lane];
+            s[i] = rec[2048 + 16 * i + 8 * (lane >> 4) + ((lane & 15) >> 1)];
         }
     }
     // The scale byte's seven bits moved to f16's exponent and mantissa are the
@@ -77,8 +77,8 @@ struct Fp8BlockKeys {
         const int place = 2 * ((((lane & 15) >> 1) + (lane >> 4)) & 7) + (lane & 1);
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            d[i] = __ldg(reinterpret_cast<const uint2 *>(rec) + 32 * i + (lane & 16) + place);
-        s = __ldg(reinterpret_cast<const float *>(rec + kFp8Record));
+            d[i] = reinterpret_cast<const uint2 *>(rec)[32 * i + (lane & 16) + place];
+        s = *reinterpret_cast<const float *>(rec + kFp8Record);
     }
     __device__ __forceinline__ float unit() const { return s; }
     __device__ __forceinline__ void get(int i, uint32_t (&x)[4]) const
@@ -259,7 +259,7 @@ __device__ __forceinline__ void load_queries(const SelectParams &p, int b, int t
     for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            const uint4 v = __ldg(reinterpret_cast<const uint4 *>(q + 64 * i + 16 * tig) + k);
+            const uint4 v = reinterpret_cast<const uint4 *>(q + 64 * i + 16 * tig)[k];
             const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
@@ -326,7 +326,7 @@ struct TileRing {
                 const int8_t *src = p.bounds + (static_cast<size_t>(id) * p.hkv + h) * (2 * kHeadDim) + (lane & 15) * 16;
                 asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + k * 576), "l"(src) : "memory");
             }
-            step[stage] = __ldg(p.steps + static_cast<size_t>(phys) * p.hkv + h);
+            step[stage] = p.steps[static_cast<size_t>(phys) * p.hkv + h];
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     }

@@ -1107,7 +1107,7 @@ __global__ void __launch_bounds__(Shape<kKeySplit>::kThreads, 1)
                 const int at = __shfl_sync(kFullMask, rel, of);
                 w[i] = make_uint4(0, 0, 0, 0);
                 if ((live >> of) & 1u)
-                    w[i] = __ldg(from + static_cast<int64_t>(at) * (kHeadDim / 8));
+                    w[i] = from[static_cast<int64_t>(at) * (kHeadDim / 8)];
             }
             const float ks = p.hs.per_head ? p.hs.k[u.h] : p.gscale;
             const float to_log2 = 256.f * ks * fabsf(p.qscale);

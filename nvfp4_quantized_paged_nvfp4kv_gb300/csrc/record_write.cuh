@@ -20,7 +20,7 @@ __device__ __forceinline__ void load_raw(const void *src, size_t elem_off, RawBl
                            : reinterpret_cast<const uint4 *>(static_cast<const float *>(src) + elem_off);
 #pragma unroll
     for (int i = 0; i < (kBf16 ? 2 : 4); ++i)
-        r.v[i] = __ldg(p + i);
+        r.v[i] = p[i];
 }
 
 template <bool kBf16>

@@ -199,3 +199,64 @@ def test_select_around_the_pages_of_which_two_units_share_an_sm(rows, q_len, hkv
     lens[0], lens[1], lens[-2], lens[-1] = pages * 16, 0, 37, pages * 16 - 15
     bt = rng.integers(0, 300, (rows, pages)).astype(np.int32)
     assert_picks(make_bounds(300, hkv, 13), queries(rows, q_len, 2 * hkv, 6), bt, lens.tolist(), 40, 2, 3, q_len)
+
+
+def test_what_a_kernel_writes_is_what_the_next_one_reads():
+    """Each call's kernel may be resident before the kernel in front of it has written;
+    chains of calls over the same buffers, without a pause between them, equal the
+    same calls made one by one."""
+    rng = np.random.default_rng(17)
+    C, hkv, hq, pages, budget, turns = 32, 2, 8, 64, 6, 30
+    T, n = 2 * C, np.array([277, 91])
+    bt = rng.permutation(pages)[:40].reshape(2, 20).astype(np.int32)
+    at = (n[:, None] - C + np.arange(C)).ravel()
+    rows = np.repeat([0, 1], C)
+    slots, positions, table, lens, ptr = i32(bt[rows, at // 16] * 16 + at % 16), i32(at), i32(bt), i32(n), i32([0, C, T])
+    random = lambda heads: [torch.tensor(rng.standard_normal((T, heads, 128)), dtype=torch.float32).to(torch.bfloat16).to(DEV)
+                            for _ in range(3)]
+    q, k, v = random(hq), random(hkv), random(hkv)
+    weight, start = torch.ones(128, device=DEV), i32([0, 300])
+
+    def run(pause):
+        eight, four = nv.FP8BlockCache.allocate(pages, hkv, device=DEV), nv.NVFP4Cache.allocate(pages, hkv, device=DEV)
+        b8, b4 = (nv.PageBounds.allocate(pages, hkv, device=DEV) for _ in range(2))
+        q1, k1 = (torch.zeros((T, heads, 128), dtype=torch.bfloat16, device=DEV) for heads in (hq, hkv))
+        ws, ews, status = nv.new_workspace(device=DEV), nv.new_extend_workspace(T, C, 2, hq, hkv, 20, device=DEV), i32([0])
+        lists = torch.zeros((turns, 2, 2, hkv, budget), dtype=torch.int32, device=DEV)
+        out, chunk = torch.zeros((turns, 3, 2, hq, 128), device=DEV), torch.zeros((turns, T, hq, 128), device=DEV)
+        back = torch.zeros((turns, 2, 400, hkv, 128), device=DEV)
+        torch.cuda.synchronize()
+
+        def then(call, *a, **kw):
+            call(*a, dev_status=status, **kw)
+            if pause:
+                torch.cuda.synchronize()
+
+        def norm(j):
+            then(nv.nvfp4kv_qk_norm_rope, q[j % 3], k[j % 3], positions, q1, k1, q_weight=weight, k_weight=weight)
+
+        for j in range(turns):
+            norm(j)
+            then(nv.fp8bkv_append, eight, k1, v[j % 3], ptr, table, lens)
+            then(nv.fp8bkv_page_bounds, eight, b8, table, lens)
+            then(nv.nvfp4kv_select_pages, b8, q1[:2], table, lens, lists[j, 0])
+            norm(j + 1)
+            then(nv.fp8bkv_selected_decode, eight, q1[:2], table, lens, lists[j, 0], out[j, 0], ws)
+            norm(j + 2)
+            then(nv.nvfp4kv_quantize_append, four, k1, v[j % 3], slots)
+            then(nv.nvfp4kv_page_bounds, four, b4, table, lens)
+            norm(j)
+            then(nv.nvfp4kv_select_pages, b4, q1[2:4], table, lens, lists[j, 1])
+            then(nv.nvfp4kv_selected_decode, four, q1[2:4], table, lens, lists[j, 1], out[j, 1], ws)
+            norm(j + 1)
+            then(nv.fp8bkv_paged_decode, eight, q1[4:6], table, lens, out[j, 2], ws)
+            norm(j + 2)
+            then(nv.nvfp4kv_paged_extend, four, q1, ptr, table, lens, chunk[j], ews, max_q_len=C)
+            then(nv.fp8bkv_append, eight, k1, v[j % 3], ptr, table, lens)
+            then(nv.fp8bkv_dequant, eight, table, lens, start, back[j, 0], back[j, 1])
+        torch.cuda.synchronize()
+        assert int(status.item()) == 0
+        return lists, out, chunk, back, eight.pool, four.pool, b8.bounds, b4.bounds
+
+    for one, chained in zip(run(True), run(False)):
+        assert torch.equal(one, chained)
