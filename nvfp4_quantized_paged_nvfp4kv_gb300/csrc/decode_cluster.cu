@@ -366,9 +366,10 @@ struct ClusterCost {
 ClusterPlan plan_cluster_decode(int64_t segments, int64_t worker_segments, int64_t pages, bool eight_bits, bool listed,
                                 int q_len)
 {
-    if (segments < 1 || segments > (int64_t{1} << 27))
-        return {};
     const int64_t sms = sm_count();
+    // (no device: the worker split's launch says so)
+    if (segments < 1 || segments > (int64_t{1} << 27) || sms < 1)
+        return {};
     const bool shared = !listed && q_len > 1;
     const ClusterCost cost{pages, sms, 2 * sms, eight_bits ? (shared ? 0.105 : 0.19) : 0.115, eight_bits ? 0.085 : 0.075};
     int64_t ranks = cost.ranks(segments), first = segments, rest_ranks = 1;
