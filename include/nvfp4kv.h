@@ -659,7 +659,9 @@ nvfp4kv_status fp8bkv_append(const fp8bkv_cache *cache, const void *k_new, const
  * rounds and saturates: the FP8 workspace that the extend calls take), v_out the
  * same; each [rows][num_kv_heads][128], 16-byte aligned, sized by the caller.
  * Lengths and page ids are checked as in nvfp4kv_paged_decode.  batch at most
- * NVFP4KV_MAX_BATCH. */
+ * NVFP4KV_MAX_BATCH.  k_out and v_out overlap neither one another nor anything
+ * that is read; an output whose first row does is refused
+ * (NVFP4KV_ERR_INVALID_ARG), the rows behind it are the device's to know. */
 nvfp4kv_status fp8bkv_dequant(const fp8bkv_cache *cache, const int32_t *block_table, int32_t max_pages_per_seq,
                               const int32_t *lens, const int32_t *kv_indptr, int32_t batch, void *k_out, void *v_out,
                               nvfp4kv_dtype out_dtype, int32_t *dev_status, nvfp4kv_stream_t stream);
@@ -668,7 +670,8 @@ nvfp4kv_status fp8bkv_dequant(const fp8bkv_cache *cache, const int32_t *block_ta
  * counterpart on the pages): q_len query tokens per sequence (1 ..
  * NVFP4KV_MAX_QUERY_TOKENS), causal among themselves, as in
  * nvfp4kv_paged_decode_multi.  Arguments, checks and results as there; seq_lens
- * and block_table are read ahead of the wait for the kernel before, too.
+ * and block_table are read ahead of the wait for the kernel before, too.  out and
+ * the workspace overlap nothing else (NVFP4KV_ERR_INVALID_ARG).
  * Arithmetic: codes are exact in fp16, q too (bf16 significands under a power of
  * two a row; elements under 2^-28 of the row's largest lose bits); sm_scale and
  * a page's scales are applied in fp32, where scores, softmax and outputs are held;
@@ -758,7 +761,8 @@ nvfp4kv_status nvfp4kv_select_pages(const nvfp4kv_bounds *bounds, const void *q,
  *   workspace, num_workers  as for nvfp4kv_paged_decode
  * batch * q_len at most NVFP4KV_MAX_BATCH; other arguments, checks and arithmetic
  * as for nvfp4kv_paged_decode, whose reading of seq_lens and block_table ahead of
- * the wait for the kernel before this call shares (pages is read behind it). */
+ * the wait for the kernel before this call shares (pages is read behind it).  out
+ * and the workspace overlap nothing else (NVFP4KV_ERR_INVALID_ARG). */
 nvfp4kv_status nvfp4kv_selected_decode(const nvfp4kv_cache *cache, const void *q, int32_t batch, int32_t q_len,
                                        int32_t num_q_heads, const int32_t *block_table, int32_t max_pages_per_seq,
                                        const int32_t *seq_lens, const int32_t *pages, int32_t budget, float sm_scale,

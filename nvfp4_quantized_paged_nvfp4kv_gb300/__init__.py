@@ -331,6 +331,7 @@ class FP8BlockCache(FP8Cache):
     def __init__(self, pool):
         _whole(pool, "pool", "uint8")
         super().__init__(pool)
+        self._span = (pool.data_ptr(), pool.data_ptr() + pool.nbytes)
 
 
 class PageBounds:
@@ -775,6 +776,9 @@ def fp8bkv_append(cache: FP8BlockCache, k_new, v_new, q_indptr, block_table, seq
         _check(st, "fp8bkv_append")
 
 
+_HEAD_BYTES = {F32: 4 * HEAD_DIM, BF16: 2 * HEAD_DIM, E4M3: HEAD_DIM}
+
+
 def fp8bkv_dequant(cache: FP8BlockCache, block_table, lens, kv_indptr, k_out, v_out, dev_status=None,
                    stream=None) -> None:
     """Read the first lens[b] cached rows of each sequence back into rows
@@ -800,8 +804,13 @@ def fp8bkv_dequant(cache: FP8BlockCache, block_table, lens, kv_indptr, k_out, v_
     if not (dev_status is None or (dev_status.dtype is i32 and dev_status.shape == (1,) and
                                    dev_status.get_device() == dev)):
         _tensors(dev, i32, (dev_status, "dev_status", (1,)))
+    # (the call sees one row of the outputs, whose number only the device knows)
+    k_at, v_at, size = k_out.data_ptr(), v_out.data_ptr(), rows[0] * rows[1] * _HEAD_BYTES[code]
+    begin, end = cache._span
+    if -size < k_at - v_at < size or begin - size < k_at < end or begin - size < v_at < end:
+        raise ValueError("k_out, v_out: overlap one another or the cache")
     st = load().fp8bkv_dequant(cache.c, block_table.data_ptr(), pages, lens.data_ptr(), kv_indptr.data_ptr(), B,
-                               k_out.data_ptr(), v_out.data_ptr(), code, _ptr(dev_status), _stream(stream, dev))
+                               k_at, v_at, code, _ptr(dev_status), _stream(stream, dev))
     if st:
         _check(st, "fp8bkv_dequant")
 

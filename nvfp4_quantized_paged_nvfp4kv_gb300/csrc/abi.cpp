@@ -1148,6 +1148,18 @@ nvfp4kv_status fp8bkv_dequant(const fp8bkv_cache *cache, const int32_t *block_ta
         return st;
     if (kv_indptr == nullptr || k_out == nullptr || v_out == nullptr || !aligned16(k_out) || !aligned16(v_out))
         return NVFP4KV_ERR_INVALID_ARG;
+    // (how many rows the outputs have, only the device knows: one each is looked at)
+    const size_t n = 4 * static_cast<size_t>(batch);
+    const size_t row = static_cast<size_t>(cache->num_kv_heads) * kHeadDim *
+                       (out_dtype == NVFP4KV_F32 ? 4 : (out_dtype == NVFP4KV_BF16 ? 2 : 1));
+    const Span spans[] = {{cache->pool, static_cast<size_t>(cache->num_pages) * cache->num_kv_heads * kFp8BlockRecord, false},
+                          {block_table, n * static_cast<size_t>(max_pages_per_seq), false},
+                          {lens, n, false},
+                          {kv_indptr, n, false},
+                          {k_out, row, true},
+                          {v_out, row, true}};
+    if (written_overlap(spans))
+        return NVFP4KV_ERR_INVALID_ARG;
     BlockReadParams p{};
     p.pool = static_cast<const uint8_t *>(cache->pool);
     p.block_table = block_table;
@@ -1180,6 +1192,15 @@ nvfp4kv_status fp8bkv_paged_decode(const fp8bkv_cache *cache, const void *q, int
                       seq_lens, sm_scale, out, out_dtype, workspace, workspace_bytes, num_workers, dev_status, p);
     if (st != NVFP4KV_OK || batch == 0)
         return st;
+    const size_t elems = static_cast<size_t>(batch) * q_len * num_q_heads * kHeadDim;
+    const Span spans[] = {{q, 2 * elems, false},
+                          {block_table, 4 * static_cast<size_t>(batch) * max_pages_per_seq, false},
+                          {seq_lens, 4 * static_cast<size_t>(batch), false},
+                          {cache->pool, static_cast<size_t>(cache->num_pages) * cache->num_kv_heads * kFp8BlockRecord, false},
+                          {out, elems * (out_dtype == NVFP4KV_F32 ? 4 : 2), true},
+                          {workspace, decode_workspace_bytes(p.num_workers), true}};
+    if (written_overlap(spans))
+        return NVFP4KV_ERR_INVALID_ARG;
     p.pool = static_cast<const uint8_t *>(cache->pool);
     const int rows = p.group * q_len, row_groups = (rows + kMaxGroup - 1) / kMaxGroup;
     const int64_t heads = static_cast<int64_t>(batch) * p.hkv;

@@ -260,3 +260,23 @@ def test_what_a_kernel_writes_is_what_the_next_one_reads():
 
     for one, chained in zip(run(True), run(False)):
         assert torch.equal(one, chained)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16, torch.uint8])
+def test_dequant_refuses_outputs_that_share_memory(dtype):
+    """... with one another or with the cache, in whatever row; side by side they may lie."""
+    hkv, rows = 2, 40
+    cache = nv.FP8BlockCache.allocate(4, hkv, device=DEV)
+    table, lens, start = i32([[0, 1, 2]]), i32([rows]), i32([0])
+    both = torch.zeros((2 * rows, hkv, 128), dtype=dtype, device=DEV)
+    nv.fp8bkv_dequant(cache, table, lens, start, both[:rows], both[rows:])
+    inside = cache.pool.flatten()[:8192].view(dtype)
+    inside = inside[:inside.numel() // (hkv * 128) * hkv * 128].view(-1, hkv, 128)
+    apart = torch.zeros((len(inside), hkv, 128), dtype=dtype, device=DEV)
+    before = cache.pool.clone()
+    for k, v in ((both[:rows], both[rows - 1:-1]), (both[rows - 1:-1], both[:rows]), (both[:rows], both[:rows]),
+                 (inside, apart), (apart, inside)):
+        with pytest.raises(ValueError):
+            nv.fp8bkv_dequant(cache, table, lens, start, k, v)
+    torch.cuda.synchronize()
+    assert torch.equal(cache.pool, before)
