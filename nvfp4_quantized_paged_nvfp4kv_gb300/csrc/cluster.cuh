@@ -9,13 +9,17 @@
 
 namespace nvfp4kv {
 
+// The barrier's aligned forms are executed by whole warps: a warp whose lanes went
+// different ways before (a lane's store, a loop left at different turns) meets first.
 __device__ __forceinline__ void cluster_arrive()
 {
+    __syncwarp();
     asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
 }
 
 __device__ __forceinline__ void cluster_wait()
 {
+    __syncwarp();
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
