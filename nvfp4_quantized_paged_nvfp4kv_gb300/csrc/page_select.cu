@@ -273,6 +273,13 @@ __device__ __forceinline__ void load_queries(const SelectParams &p, int b, int t
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1)
         top = fmaxf(top, __shfl_xor_sync(kFullMask, top, o));
+    if (top < 0x1p-100f) {
+        // (127 / top might pass fp32: the same weights of queries 2^100 times as large)
+        top *= 0x1p100f;
+#pragma unroll
+        for (int k = 0; k < 32; ++k)
+            x[k] *= 0x1p100f;
+    }
     const float r = top > 0.f ? __fdiv_rn(127.f, top) : 0.f;
     int sum = 0;
 #pragma unroll

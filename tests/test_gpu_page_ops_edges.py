@@ -280,3 +280,17 @@ def test_dequant_refuses_outputs_that_share_memory(dtype):
             nv.fp8bkv_dequant(cache, table, lens, start, k, v)
     torch.cuda.synchronize()
     assert torch.equal(cache.pool, before)
+
+
+@pytest.mark.parametrize("exponent", [-133, -130, -120, -101, -100, -99, -60, 60, 119])
+def test_select_by_queries_of_any_size(exponent):
+    """Whole numbers times a power of two: weights, and so the lists, are the whole numbers'."""
+    g = torch.Generator(device=DEV).manual_seed(3)
+    whole = torch.randint(-127, 128, (2, 1, 8, 128), generator=g, device=DEV).float()
+    q = (whole.double() * 2.0 ** exponent).to(torch.bfloat16)
+    assert torch.equal(q.double(), whole.double() * 2.0 ** exponent)
+    b = make_bounds(700, 2, 8)
+    bt = np.random.default_rng(2).integers(0, 700, (2, 600)).astype(np.int32)
+    got = picks(b, q, bt, [600 * 16, 431 * 16 + 7], 37, 1, 2, 1)
+    assert np.array_equal(got, picks(b, whole.to(torch.bfloat16), bt, [600 * 16, 431 * 16 + 7], 37, 1, 2, 1))
+    assert_picks(b, whole.to(torch.bfloat16), bt, [600 * 16, 431 * 16 + 7], 37, 1, 2, 1)
