@@ -656,8 +656,13 @@ nvfp4kv_status fp8bkv_append(const fp8bkv_cache *cache, const void *k_new, const
 /* Read cached rows back (a library utility): for j < lens[b]
  *   k_out[kv_indptr[b] + j][h][c] = code * scale, rounded to out_dtype
  * (fp32 and bf16 hold it exactly, but for values past their range; NVFP4KV_E4M3
- * rounds and saturates: the FP8 workspace that the extend calls take), v_out the
- * same; each [rows][num_kv_heads][128], 16-byte aligned, sized by the caller.
+ * rounds and saturates: the FP8 workspace that the extend calls take, which has
+ * no scales), v_out the same; each [rows][num_kv_heads][128], 16-byte aligned,
+ * sized by the caller.  Cached values past 448, or so small that E4M3 at scale 1.0
+ * has no bits for them, are not what that workspace holds: a prompt chunk that the
+ * extend calls attend over it sees others there than the decodes, which apply the
+ * scales.  Cached values of 0 or of magnitude 2^-6 .. 448 come
+ * through as they are.
  * Lengths and page ids are checked as in nvfp4kv_paged_decode.  batch at most
  * NVFP4KV_MAX_BATCH.  k_out and v_out overlap neither one another nor anything
  * that is read; an output whose first row does is refused
@@ -675,7 +680,9 @@ nvfp4kv_status fp8bkv_dequant(const fp8bkv_cache *cache, const int32_t *block_ta
  * Arithmetic: codes are exact in fp16, q too (bf16 significands under a power of
  * two a row; elements under 2^-28 of the row's largest lose bits); sm_scale and
  * a page's scales are applied in fp32, where scores, softmax and outputs are held;
- * softmax weights are rounded to fp16 for the value product. */
+ * softmax weights are rounded to fp16 for the value product, before the scale of
+ * a page's values: a weight below 2^-25 of the row's largest counts as none, also
+ * where its page's values are so much larger than the others'. */
 nvfp4kv_status fp8bkv_paged_decode(const fp8bkv_cache *cache, const void *q, int32_t batch, int32_t q_len,
                                    int32_t num_q_heads, const int32_t *block_table, int32_t max_pages_per_seq,
                                    const int32_t *seq_lens, float sm_scale, void *out, nvfp4kv_dtype out_dtype,

@@ -782,8 +782,9 @@ _HEAD_BYTES = {F32: 4 * HEAD_DIM, BF16: 2 * HEAD_DIM, E4M3: HEAD_DIM}
 def fp8bkv_dequant(cache: FP8BlockCache, block_table, lens, kv_indptr, k_out, v_out, dev_status=None,
                    stream=None) -> None:
     """Read the first lens[b] cached rows of each sequence back into rows
-    kv_indptr[b] .. of k_out and v_out [rows][Hkv][128]: fp32, bf16, or E4M3
-    (uint8 or float8_e4m3fn: the workspace of the extend calls)."""
+    kv_indptr[b] .. of k_out and v_out [rows][Hkv][128]: fp32, bf16, or E4M3 at
+    scale 1.0 (uint8 or float8_e4m3fn: the workspace of the extend calls, where
+    values past 448 saturate and small ones lose bits)."""
     dev = _current_device()
     i32, dtype = _int_t, k_out.dtype
     _kind(cache, FP8BlockCache, dev)

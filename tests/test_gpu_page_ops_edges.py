@@ -294,3 +294,23 @@ def test_select_by_queries_of_any_size(exponent):
     got = picks(b, q, bt, [600 * 16, 431 * 16 + 7], 37, 1, 2, 1)
     assert np.array_equal(got, picks(b, whole.to(torch.bfloat16), bt, [600 * 16, 431 * 16 + 7], 37, 1, 2, 1))
     assert_picks(b, whole.to(torch.bfloat16), bt, [600 * 16, 431 * 16 + 7], 37, 1, 2, 1)
+
+
+def test_dequant_to_e4m3_keeps_what_scale_one_holds():
+    """Magnitudes of 2^-6 .. 448 come through as they are, larger ones as 448."""
+    rng = np.random.default_rng(4)
+    x = rng.standard_normal((160, 2, 128)) * 2.0 ** rng.integers(-12, 14, (160, 2, 1))
+    cache = nv.FP8BlockCache.allocate(10, 2, device=DEV)
+    x = torch.tensor(x, dtype=torch.float32, device=DEV)
+    table, lens = i32(rng.permutation(10)[None]), i32([160])
+    nv.fp8bkv_append(cache, x, x, i32([0, 160]), table, lens)
+    full, code = [torch.zeros((160, 2, 128), device=DEV) for _ in range(2)], [
+        torch.zeros((160, 2, 128), dtype=torch.float8_e4m3fn, device=DEV) for _ in range(2)]
+    nv.fp8bkv_dequant(cache, table, lens, i32([0]), *full)
+    nv.fp8bkv_dequant(cache, table, lens, i32([0]), *code)
+    for a, b in zip(full, code):
+        b = b.float()
+        held = ((a.abs() >= 2.0 ** -6) & (a.abs() <= 448)) | (a == 0)
+        assert held.any() and torch.equal(a[held], b[held])
+        past = a.abs() > 448
+        assert past.any() and torch.equal(b[past], torch.copysign(torch.full_like(a[past], 448), a[past]))
