@@ -8,7 +8,8 @@ import torch
 
 import nvfp4_quantized_paged_nvfp4kv_gb300 as nv
 from gpu_util import DEV
-from test_gpu_page_select import assert_picks, i32, make_bounds, picks, queries
+from page_ops_ref import attend, check, nvfp4_values
+from test_gpu_page_select import Cache, assert_picks, i32, make_bounds, picks, queries
 
 pytestmark = pytest.mark.gpu
 
@@ -314,3 +315,97 @@ def test_dequant_to_e4m3_keeps_what_scale_one_holds():
         assert held.any() and torch.equal(a[held], b[held])
         past = a.abs() > 448
         assert past.any() and torch.equal(b[past], torch.copysign(torch.full_like(a[past], 448), a[past]))
+
+
+@pytest.mark.parametrize("kind", ["nvfp4", "fp8b"])
+@pytest.mark.parametrize("sm_scale", [-0.11, 0.0])
+@pytest.mark.parametrize("workers", [0, 3])
+def test_decodes_with_a_scale_that_is_not_positive(kind, sm_scale, workers):
+    """Both decodes of both caches; with 0 every key counts the same."""
+    cache, hkv, g, budget = Cache(kind, 40, 2, 6), 2, 3, 5
+    rng = np.random.default_rng(1)
+    lens = [0, 1, 90, 300]
+    bt = np.stack([rng.permutation(40)[:20] for _ in lens]).astype(np.int32)
+    pages = np.full((4, 1, hkv, budget), -1, np.int32)
+    for s, n in enumerate(lens):
+        for h in range(hkv):
+            P = -(-n // 16)
+            pages[s, 0, h, :min(P, budget)] = rng.permutation(P)[:budget]
+    q, ws, status = queries(4, 1, hkv * g, 2), nv.new_workspace(workers, device=DEV), i32([0])
+    listed, dense = (torch.full(q.shape, float("nan"), device=DEV) for _ in range(2))
+    cache.decode(q, i32(bt), i32(lens), i32(pages), listed, ws, sm_scale=sm_scale, num_workers=workers, dev_status=status)
+    whole = nv.nvfp4kv_paged_decode if kind == "nvfp4" else nv.fp8bkv_paged_decode
+    whole(cache.c, q, i32(bt), i32(lens), dense, ws, sm_scale=sm_scale, num_workers=workers, dev_status=status)
+    assert int(status.item()) == 0
+    # (the definition with the scale's sign, or its zero, on the queries)
+    qn = q.double().cpu().numpy().reshape(4, hkv, g, 128) * np.sign(sm_scale)
+    for out, of in ((listed, lambda s, h: pages[s, 0, h]), (dense, lambda s, h: np.arange(-(-lens[s] // 16)))):
+        got = out.double().cpu().numpy().reshape(qn.shape)
+        for s, n in enumerate(lens):
+            for h in range(hkv):
+                kv = [np.concatenate([x[bt[s, p], h, :n - 16 * p] for p in of(s, h) if p >= 0] or [np.zeros((0, 128))])
+                      for x in (cache.k, cache.v)]
+                want, bound = attend(qn[s, h], *kv, abs(sm_scale) or 1.0, 0.0, 2.0 ** -11 if kind == "nvfp4" else 0.0)
+                check(got[s, h], want, bound, f"sequence {s}, kv head {h}")
+
+
+def test_select_many_units_of_the_most_pages():
+    """More units than SMs, each in several CTAs, and a rest: as each by itself."""
+    rows, pages, budget = 155, 65536, 90
+    rng = np.random.default_rng(8)
+    b, q = make_bounds(700, 1, 21), queries(rows, 1, 4, 12)
+    bt = rng.integers(0, 700, (rows, pages)).astype(np.int32)
+    lens = rng.integers(pages * 8, pages * 16 + 1, rows)
+    lens[0], lens[3], lens[-1] = pages * 16, 5, pages * 16 - 15
+    together = picks(b, q, bt, lens, budget, 2, 3, 1)
+    for i in range(rows):
+        alone = picks(b, q[i:i + 1].contiguous(), bt[i:i + 1], lens[i:i + 1], budget, 2, 3, 1)
+        assert np.array_equal(alone[0], together[i]), i
+    assert_picks(b, q[-1:].contiguous(), bt[-1:], lens[-1:].tolist(), budget, 2, 3, 1)
+
+
+@pytest.mark.parametrize("kind,exponent", [("nvfp4", 12), ("fp8b", 12), ("fp8b", 20), ("fp8b", 40), ("fp8b", 100)])
+@pytest.mark.parametrize("workers", [0, 2])
+def test_scores_far_apart_leave_the_largest(kind, exponent, workers):
+    """Keys and queries that are whole numbers, scores that differ by 2^12 and more: the
+    mean of the values whose keys reach the largest one.  (The 4-bit cache's decode
+    holds q * sm_scale in fp16.)"""
+    rng = np.random.default_rng(exponent)
+    cache = Cache(kind, 30, 1, 2)
+    lens, g = [400, 47], 4
+    k = rng.integers(-1, 2, (480, 1, 128)).astype(np.float32)
+    v = rng.integers(-4, 5, (480, 1, 128)).astype(np.float32)
+    bt = rng.permutation(30)[None].repeat(2, 0).astype(np.int32)
+    k[:, :, ::16], v[:, :, ::16] = 6, 4                  # (so that four bits hold the keys exactly)
+    rows = [torch.tensor(x, device=DEV) for x in (k, v)]
+    if kind == "nvfp4":
+        nv.nvfp4kv_quantize_append(cache.c, *rows, i32(bt[0][np.arange(480) // 16] * 16 + np.arange(480) % 16))
+    else:
+        cache.c.pool.zero_()
+        nv.fp8bkv_append(cache.c, *rows, i32([0, 480]), i32(bt[:1]), i32([480]))
+    held = Held(cache, bt[0], kind)
+    q = torch.tensor(rng.integers(-1, 2, (2, g, 128)), dtype=torch.float32, device=DEV).to(torch.bfloat16)
+    ws, lists = nv.new_workspace(workers, device=DEV), i32(np.arange(25)[None, None].repeat(2, 0))
+    for out, call in ((torch.zeros(q.shape, device=DEV), nv.nvfp4kv_paged_decode if kind == "nvfp4" else nv.fp8bkv_paged_decode),
+                      (torch.zeros(q.shape, device=DEV), cache.decode)):
+        if call == cache.decode:
+            call(q, i32(bt), i32(lens), lists, out, ws, sm_scale=2.0 ** exponent, num_workers=workers)
+        else:
+            call(cache.c, q, i32(bt), i32(lens), out, ws, sm_scale=2.0 ** exponent, num_workers=workers)
+        for s, n in enumerate(lens):
+            score = q[s].double().cpu().numpy() @ held.k[:n].T
+            top = score == score.max(1, keepdims=True)
+            want = top @ held.v[:n] / top.sum(1, keepdims=True)
+            assert np.abs(out[s].cpu().numpy() - want).max() <= 2.0 ** -20 * 6, (s, call)
+
+
+class Held:
+    """Keys and values [tokens][128] as a cache holds them, read back."""
+
+    def __init__(self, cache, table, kind):
+        if kind == "nvfp4":
+            self.k, self.v = (x[table, 0].reshape(-1, 128) for x in nvfp4_values(cache.c.pool.cpu().numpy()))
+        else:
+            k, v = (torch.zeros((480, 1, 128), device=DEV) for _ in range(2))
+            nv.fp8bkv_dequant(cache.c, i32(table[None]), i32([480]), i32([0]), k, v)
+            self.k, self.v = (x[:, 0].double().cpu().numpy() for x in (k, v))
