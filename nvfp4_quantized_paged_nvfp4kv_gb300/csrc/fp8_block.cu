@@ -131,7 +131,7 @@ __device__ __forceinline__ int find_unit(const int32_t *q_indptr, int batch, lon
 // load of bf16, whole rows a half warp, and a V record's 16-byte chunk (the two
 // tokens' bytes interleaved) is one lane's.  All rows of the page are asked for
 // before the first is used; the page's old codes and scale come beside them.
-// Three prompts, 12,288 rows of 8 heads in bf16: 16.4 us for 75 MB, two thirds of the
+// Three prompts, 12,288 rows of 8 heads in bf16: 16.6 us for 75 MB, two thirds of the
 // copy rate, bound by the latency of its one round of loads (24 warps an SM; K and V in
 // one warp, with twice the registers, 20.6 us; more warps of fewer rows: no faster).
 template <bool kBf16>
