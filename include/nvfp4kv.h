@@ -732,7 +732,8 @@ nvfp4kv_status fp8bkv_page_bounds(const fp8bkv_cache *cache, const nvfp4kv_bound
  * q_len 1 .. NVFP4KV_MAX_QUERY_TOKENS, the sequence's last positions) sees the
  * first n = seq_lens[b] - q_len + t + 1 tokens, so P = ceil(n / 16) pages (none
  * where n <= 0).  With the group's queries in whole steps, w = rint(fl32(q *
- * fl32(127 / max |q|))), the maximum over the group's heads and channels:
+ * fl32(127 / max |q|))), the maximum over the group's heads and channels (where it
+ * is below 2^-100, of queries 2^100 times as large, for the quotient's sake):
  *   score(page) = fl32(step * max_h sum_c max(w_hc * hi_c, w_hc * lo_c)),
  * the most that a key within the bounds can reach with one of the heads; the
  * sum is a whole number below 2^24, so the score depends on no order of sums.
